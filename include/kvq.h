@@ -58,6 +58,8 @@ enum {
 enum { KVQ_FMT_LOOPVQ = 0, KVQ_FMT_KIVI = 1 };
 enum { KVQ_OUT_BF16 = 0, KVQ_OUT_FP32 = 1 };
 enum { KVQ_PER_CHANNEL = 0, KVQ_PER_TOKEN = 1 };
+/* types of arrays that may be stored in several */
+enum { KVQ_DT_BF16 = 0, KVQ_DT_FP32 = 1, KVQ_DT_FP16 = 2 };
 
 typedef void* kvq_stream; /* cudaStream_t */
 
@@ -313,6 +315,100 @@ kvq_status kvq_kivi_prefill(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache
 kvq_status kvq_kivi_append(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
                            const uint16_t* k_new, const uint16_t* v_new, int n_seq,
                            kvq_stream stream);
+
+/* Commit of drafted tokens (speculative decoding): for every request b < n_seq the tokens
+ * path[b][0 .. n_accept[b] - 1] of its drafts are appended in that order. The cache is left as
+ * n_accept[b] calls of kvq_kivi_append with those tokens would leave it, bit for bit (key
+ * flushes, value evictions and lengths included); one launch serves every request.
+ * k_draft, v_draft: fp16 [n_seq][N][n_heads][D]; path: device int32 [n_seq][N], each entry an
+ * index in [0, N) (an index may come twice); n_accept: device int32 [n_seq]. A request with
+ * n_accept = 0 is left as it is. So is one that cannot be committed whole, and kvq_device_error()
+ * then reports KVQ_ERR_INVALID_ARG (n_accept outside [0, N], an index outside [0, N)) or
+ * KVQ_ERR_CAPACITY (n_accept > residual, an invalid state, or a key flush past max_tokens).
+ * Commits and appends to one cache must not run at the same time.
+ * Errors: KVQ_ERR_INVALID_ARG (residual not a positive multiple of group, n_seq or N < 0),
+ * KVQ_ERR_CAPACITY (n_seq > max_batch). */
+kvq_status kvq_kivi_commit(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
+                           const uint16_t* k_draft, const uint16_t* v_draft, const int32_t* path,
+                           const int32_t* n_accept, int n_seq, int N, kvq_stream stream);
+
+/* Reading a cache back: row j < n_tok of request b0 + i receives token t = tok_begin[i] + j
+ * (tok_begin: device int32 [B], or NULL for 0): s (q - z) in fp32 where it is quantized, else its
+ * fp16 row, rounded once to out_dtype (KVQ_DT_*; fp16 overflows to infinity past 65504). Rows
+ * whose t lies outside [0, n_tok of the request) are left as they are.
+ * k_out, v_out: element (i, h, j, ch) at x[i*x_stride_b + h*x_stride_h + j*D + ch], as
+ * kvq_kivi_prefill reads them; one of the two may be NULL (not read back).
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_CAPACITY (b0 + B > max_batch), KVQ_ERR_UNSUPPORTED (a
+ * call of more than 2^31 blocks). */
+kvq_status kvq_kivi_read(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
+                         const int32_t* tok_begin, int b0, int B, int n_tok, void* k_out,
+                         void* v_out, int out_dtype, int64_t x_stride_b, int64_t x_stride_h,
+                         kvq_stream stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* Rows of queries, keys and values on their way to a cache                            */
+/* ---------------------------------------------------------------------------------- */
+
+/* One array of rows: element (b, j, h, ch) at p[b*stride_b + j*stride_t + h*stride_h + ch],
+ * channels contiguous, strides non-negative multiples of 8 elements. */
+typedef struct {
+  void* p;
+  int64_t stride_b, stride_t, stride_h;
+  int heads;
+  int dtype; /* KVQ_DT_* */
+} kvq_rows;
+
+/* Norm of queries and keys for each head and the position rotation, in one pass: for every row
+ * x of D channels, y = x / sqrt(mean(x^2) + eps) * w (w: w_q or w_k, [D], of x's type), then, if
+ * rope_cos and rope_sin are given ([max_ctx][D/2], kvq_rope_table), the rotate-half pairs
+ * (i, i + D/2) turn by the angle of the token's position pos[b][j]. Value rows are converted to
+ * their output's type only. fp32 arithmetic, one rounding to the output's type (fp16 overflows
+ * to infinity past 65504). With fp16 keys and values it feeds kvq_kivi_prefill, kvq_kivi_append
+ * and kvq_kivi_tree_attn (rotated keys); without rotation and in bf16, kvq_prefill_vq and
+ * kvq_append_page.
+ * q, k, v: inputs of one type; each may be NULL (then its output is NULL too), not all three.
+ * pos: device int32 [B][N]. May be NULL without rotation. A token with a negative position is
+ * padding: its rows are neither read nor written. One with rotation and a position >= max_ctx is
+ * left as it is and raises KVQ_ERR_CAPACITY through kvq_device_error().
+ * An output may be its own input (same pointer, strides and type); other overlaps are not allowed.
+ * Errors: KVQ_ERR_INVALID_ARG (pointers, strides, types, head counts; eps outside [1e-30, 1]),
+ * KVQ_ERR_UNSUPPORTED (D other than 128, more than 2^31 blocks). */
+kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_rows* k,
+                            const kvq_rows* v, const void* w_q, const void* w_k, float eps,
+                            const float* rope_cos, const float* rope_sin, int max_ctx,
+                            const int32_t* pos, const kvq_rows* q_out, const kvq_rows* k_out,
+                            const kvq_rows* v_out, kvq_stream stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* Attention of drafted tokens over a KIVI cache                                       */
+/* ---------------------------------------------------------------------------------- */
+
+/* Request b < B has N <= 64 drafted tokens beside its cache, the nodes of a tree (a chain is a
+ * tree too). Drafted token i attends every cached token and the drafted tokens j whose bit j is
+ * set in mask[b][i] (its ancestors and itself), one softmax over both, scale 1/sqrt(D).
+ * q: bf16 [B][N][n_q_heads][D], already rotated; k_draft, v_draft: fp16 [B][N][n_heads][D], keys
+ * rotated; mask: device uint64 [B][N]; n_draft: device int32 [B], the drafted tokens of each
+ * request (NULL: N for every one; values outside [0, N] count as the nearest). Tokens
+ * i >= n_draft[b] are padding: their rows of out stay as they are, and no row attends them
+ * whatever its mask says. Keys and values a row does not attend cannot change it, infinities and
+ * NaN among them; a row that attends nothing (no cached token, empty mask) is 0.
+ * The cache is read, not changed; kvq_kivi_commit appends the accepted tokens afterwards.
+ * out: [B][N][n_q_heads][D], KVQ_OUT_BF16 or KVQ_OUT_FP32.
+ * Arithmetic: softmax statistics and all sums in fp32; q (scaled by a power of two for each row),
+ * the dequantized keys and values and the softmax weights enter the tensor cores as fp16, one
+ * rounding each (relative 2^-11); a dequantized value beyond 65504 overflows.
+ * ws: device workspace of at least kvq_kivi_tree_workspace_size() bytes, needing no
+ * initialisation. Two calls that run at the same time need two workspaces.
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_CAPACITY (B > max_batch), KVQ_ERR_WORKSPACE,
+ * KVQ_ERR_UNSUPPORTED (N > 64, or more than 2^31 blocks). */
+kvq_status kvq_kivi_tree_attn(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
+                              const uint16_t* q, const uint16_t* k_draft,
+                              const uint16_t* v_draft, const uint64_t* mask,
+                              const int32_t* n_draft, int B, int N, void* out, int out_dtype,
+                              void* ws, size_t ws_bytes, kvq_stream stream);
+
+/* Workspace bytes kvq_kivi_tree_attn needs for these arguments on the current device. */
+size_t kvq_kivi_tree_workspace_size(const kvq_kivi_cfg* cfg, int B, int N);
 
 /* ---------------------------------------------------------------------------------- */
 /* Decode attention (both formats)                                                     */

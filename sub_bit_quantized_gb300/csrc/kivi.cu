@@ -548,6 +548,78 @@ __global__ void __launch_bounds__(128) kivi_append_kernel(const KiviAppendArgs a
   }
 }
 
+// Commit: the accepted drafted tokens of every request, appended in the order of its path as
+// that many appends one after the other would. One 128-thread block per (request, KV head). A
+// path of m <= R tokens flushes the key residual at most once: the new keys first fill it to R
+// rows, those are quantized, and the rest start a fresh residual. The m values that leave the
+// window are older than the new ones (m <= R), so they are quantized first and the new rows then
+// take their places in the ring.
+// Bound: latency. The call is one launch whose blocks each run through loads, (a flush: 32 KB of
+// keys quantized by four warps) and stores that depend on one another.
+template <int KB, int VB>
+__global__ void __launch_bounds__(128) kivi_commit_kernel(const KiviCommitArgs a) {
+  constexpr int kKRow = kD * KB / 8, kVRow = kD * VB / 8;
+  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_warps = blockDim.x >> 5;
+  const int R = a.residual, H = a.H;
+  const int n = a.n_tok[b], nqk = a.n_quant_k[b], nqv = a.n_quant_v[b], m = a.n_accept[b];
+  if (m == 0) return;  // every block of the request
+  const bool valid = nqk >= 0 && nqk % kGroup == 0 && nqv >= 0 && nqv <= nqk && nqk <= n && n - nqk <= R &&
+                     n - nqv <= R && nqk <= a.max_tokens;
+  const int* path = a.path + (size_t)b * a.N;
+  bool known = m > 0 && m <= a.N;
+  for (int i = 0; known && i < m; ++i) known = path[i] >= 0 && path[i] < a.N;
+  const int held = n - nqk;  // keys in the residual
+  const bool flush = valid && known && m <= R && held + m > R;
+  if (!valid || !known || m > R || (flush && nqk + R > a.max_tokens)) {
+    // every block of the request leaves it as it is
+    if (h == 0 && tid == 0) set_error(a.err, known ? KVQ_ERR_CAPACITY : KVQ_ERR_INVALID_ARG);
+    return;
+  }
+  const size_t bh = (size_t)b * H + h;
+  auto draft = [&](const uint16_t* x, int i) { return x + (((size_t)b * a.N + path[i]) * H + h) * kD; };
+  auto copy_keys = [&](int i0, int i1, int row0) {  // accepted keys i0 .. i1 - 1 to residual rows row0 ..
+    for (int x = tid; x < (i1 - i0) * (kD / 8); x += blockDim.x) {
+      const int i = x / (kD / 8), c8 = (x % (kD / 8)) * 8;
+      *reinterpret_cast<uint4*>(a.k_resid + (bh * R + row0 + i) * kD + c8) =
+          __ldg(reinterpret_cast<const uint4*>(draft(a.k_draft, i0 + i) + c8));
+    }
+  };
+  const int fill = flush ? R - held : m;  // keys that go behind the residual's
+  copy_keys(0, fill, held);
+  const int evict = max(0, n + m - R - nqv);
+  for (int i = warp; i < evict; i += n_warps) {
+    const int t = nqv + i;
+    const uint2 raw = *reinterpret_cast<const uint2*>(a.v_resid + (bh * R + t % R) * kD + 4 * lane);
+    const size_t tok = bh * a.max_tokens + t;
+    quant_value_row<VB>(raw, a.v_codes + tok * kVRow, a.v_scale + tok * (kD / kGroup), a.v_zero + tok * (kD / kGroup),
+                        lane);
+  }
+  __syncthreads();  // the residual is full, the evicted values are read
+  for (int x = tid; x < m * (kD / 8); x += blockDim.x) {
+    const int i = x / (kD / 8), c8 = (x % (kD / 8)) * 8;
+    *reinterpret_cast<uint4*>(a.v_resid + (bh * R + (n + i) % R) * kD + c8) =
+        __ldg(reinterpret_cast<const uint4*>(draft(a.v_draft, i) + c8));
+  }
+  if (flush) {
+    for (int gi = warp; gi < R / kGroup; gi += n_warps) {
+      const size_t sz = (bh * (a.max_tokens / kGroup) + nqk / kGroup + gi) * kD;
+      quant_key_group<KB, false>(a.k_resid + (bh * R + (size_t)gi * kGroup) * kD, kD,
+                                 a.k_codes + (bh * a.max_tokens + nqk + (size_t)gi * kGroup) * kKRow, a.k_scale + sz,
+                                 a.k_zero + sz, lane);
+    }
+    __syncthreads();  // the flushed rows are read
+    copy_keys(fill, m, 0);
+  }
+  __syncthreads();
+  if (tid == 0 && atomicAdd(&a.sync[b], 1) == H - 1) {  // every block of the request has read the lengths
+    a.n_tok[b] = n + m;
+    if (flush) a.n_quant_k[b] = nqk + R;
+    a.n_quant_v[b] = nqv + evict;
+    a.sync[b] = 0;
+  }
+}
+
 // ---------------------------------------------------------------- attention
 // Blocks (split, head subgroup) x request x KV head; splits 0 .. n_split-1 take equal token
 // ranges of the quantized keys, the last split the fp16 key residual. A subgroup is RH query
@@ -1415,6 +1487,16 @@ cudaError_t launch_kivi_append(const KiviAppendArgs& a, cudaStream_t s) {
   else if (a.k_bits == 2) kivi_append_kernel<2, 4><<<grid, 128, 0, s>>>(a);
   else if (a.v_bits == 2) kivi_append_kernel<4, 2><<<grid, 128, 0, s>>>(a);
   else kivi_append_kernel<4, 4><<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kivi_commit(const KiviCommitArgs& a, cudaStream_t s) {
+  if (a.n_seq <= 0) return cudaSuccess;
+  const dim3 grid(a.n_seq, a.H);
+  if (a.k_bits == 2 && a.v_bits == 2) kivi_commit_kernel<2, 2><<<grid, 128, 0, s>>>(a);
+  else if (a.k_bits == 2) kivi_commit_kernel<2, 4><<<grid, 128, 0, s>>>(a);
+  else if (a.v_bits == 2) kivi_commit_kernel<4, 2><<<grid, 128, 0, s>>>(a);
+  else kivi_commit_kernel<4, 4><<<grid, 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -33,6 +33,8 @@ kvq_status cuda_status(cudaError_t e, const char* what) {
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool known_dtype(int d) { return d == KVQ_DT_BF16 || d == KVQ_DT_FP32 || d == KVQ_DT_FP16; }
+
 #define CHECK_PTR(p)                                                                          \
   do {                                                                                        \
     if (!aligned16(p)) return fail(KVQ_ERR_INVALID_ARG, "%s: pointer " #p " is null or not " \
@@ -479,6 +481,155 @@ KVQ_API kvq_status kvq_kivi_append(const kvq_kivi_cfg* c, const kvq_kivi_cache* 
   a.n_seq = n_seq; a.H = c->n_heads; a.k_bits = c->k_bits; a.v_bits = c->v_bits; a.residual = c->residual;
   a.max_tokens = c->max_tokens;
   return cuda_status(kvq::launch_kivi_append(a, (cudaStream_t)stream), __func__);
+}
+
+KVQ_API kvq_status kvq_kivi_commit(const kvq_kivi_cfg* c, const kvq_kivi_cache* k, const uint16_t* k_draft,
+                                   const uint16_t* v_draft, const int32_t* path, const int32_t* n_accept, int n_seq,
+                                   int N, kvq_stream stream) {
+  kvq_status st = check_kivi_cfg(c, __func__);
+  if (st != KVQ_OK) return st;
+  if ((st = check_kivi_cache(k, __func__)) != KVQ_OK) return st;
+  CHECK_PTR(k_draft);
+  CHECK_PTR(v_draft);
+  CHECK_PTR(path);
+  CHECK_PTR(n_accept);
+  if (c->residual <= 0) return fail(KVQ_ERR_INVALID_ARG, "%s: the streaming cache needs residual > 0", __func__);
+  if (n_seq < 0 || N < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: n_seq or N < 0", __func__);
+  if (n_seq > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: n_seq > max_batch", __func__);
+  if (n_seq == 0 || N == 0) return KVQ_OK;
+  kvq::KiviCommitArgs a{};
+  a.k_draft = k_draft; a.v_draft = v_draft; a.path = path; a.n_accept = n_accept;
+  a.k_codes = k->k_codes; a.k_scale = k->k_scale; a.k_zero = k->k_zero;
+  a.v_codes = k->v_codes; a.v_scale = k->v_scale; a.v_zero = k->v_zero;
+  a.k_resid = k->k_resid; a.v_resid = k->v_resid;
+  a.n_tok = k->n_tok; a.n_quant_k = k->n_quant_k; a.n_quant_v = k->n_quant_v; a.sync = k->sync;
+  a.err = device_error_ptr();
+  a.n_seq = n_seq; a.N = N; a.H = c->n_heads; a.k_bits = c->k_bits; a.v_bits = c->v_bits;
+  a.residual = c->residual; a.max_tokens = c->max_tokens;
+  return cuda_status(kvq::launch_kivi_commit(a, (cudaStream_t)stream), __func__);
+}
+
+KVQ_API kvq_status kvq_kivi_read(const kvq_kivi_cfg* c, const kvq_kivi_cache* k, const int32_t* tok_begin, int b0,
+                                 int B, int n_tok, void* k_out, void* v_out, int out_dtype, int64_t st_b,
+                                 int64_t st_h, kvq_stream stream) {
+  kvq_status st = check_kivi_cfg(c, __func__);
+  if (st != KVQ_OK) return st;
+  if ((st = check_kivi_cache(k, __func__)) != KVQ_OK) return st;
+  if ((st = check_x_strides(__func__, 0, st_b, st_h)) != KVQ_OK) return st;
+  if (tok_begin) CHECK_PTR(tok_begin);
+  if (!k_out && !v_out) return fail(KVQ_ERR_INVALID_ARG, "%s: neither k_out nor v_out is given", __func__);
+  if (k_out) CHECK_PTR(k_out);
+  if (v_out) CHECK_PTR(v_out);
+  if (!known_dtype(out_dtype)) return fail(KVQ_ERR_INVALID_ARG, "%s: out_dtype must be a KVQ_DT_ value", __func__);
+  if (b0 < 0 || B < 0 || n_tok < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: negative size", __func__);
+  if ((long long)b0 + B > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: b0 + B > max_batch", __func__);
+  if (B == 0 || n_tok == 0) return KVQ_OK;
+  if ((double)B * c->n_heads * (n_tok / 32 + 1) >= 2147483648.0)
+    return fail(KVQ_ERR_UNSUPPORTED, "%s: too many rows for one call", __func__);
+  kvq::KiviReadArgs a{};
+  a.k_codes = k->k_codes; a.k_scale = k->k_scale; a.k_zero = k->k_zero;
+  a.v_codes = k->v_codes; a.v_scale = k->v_scale; a.v_zero = k->v_zero;
+  a.k_resid = k->k_resid; a.v_resid = k->v_resid;
+  a.n_tok = k->n_tok; a.n_quant_k = k->n_quant_k; a.n_quant_v = k->n_quant_v;
+  a.tok_begin = tok_begin; a.k_out = k_out; a.v_out = v_out; a.sb = st_b; a.sh = st_h;
+  a.b0 = b0; a.B = B; a.H = c->n_heads; a.k_bits = c->k_bits; a.v_bits = c->v_bits; a.residual = c->residual;
+  a.max_tokens = c->max_tokens; a.n_tok_out = n_tok;
+  return cuda_status(kvq::launch_kivi_read(a, out_dtype, (cudaStream_t)stream), __func__);
+}
+
+// one kind of rows of kvq_qk_norm_rope: input and output of the same heads
+static kvq_status check_rows(const char* fn, const char* kind, const kvq_rows* in, const kvq_rows* out, int in_dt,
+                             kvq::QkRows* r) {
+  *r = kvq::QkRows{};
+  if (!in != !out) return fail(KVQ_ERR_INVALID_ARG, "%s: %s rows need both an input and an output", fn, kind);
+  if (!in) return KVQ_OK;
+  if (!aligned16(in->p) || !aligned16(out->p))
+    return fail(KVQ_ERR_INVALID_ARG, "%s: a pointer of the %s rows is null or not 16-byte aligned", fn, kind);
+  kvq_status st = check_x_strides(fn, in->stride_t, in->stride_b, in->stride_h);
+  if (st != KVQ_OK) return st;
+  if ((st = check_x_strides(fn, out->stride_t, out->stride_b, out->stride_h)) != KVQ_OK) return st;
+  if (in->heads <= 0 || in->heads > 65535 || in->heads != out->heads)
+    return fail(KVQ_ERR_INVALID_ARG, "%s: %s rows with %d heads in and %d out", fn, kind, in->heads, out->heads);
+  if (in->dtype != in_dt || !known_dtype(in_dt) || !known_dtype(out->dtype))
+    return fail(KVQ_ERR_INVALID_ARG, "%s: types of the %s rows (inputs share one KVQ_DT_ type)", fn, kind);
+  r->in = in->p; r->out = out->p;
+  r->sb = in->stride_b; r->st = in->stride_t; r->sh = in->stride_h;
+  r->ob = out->stride_b; r->ot = out->stride_t; r->oh = out->stride_h;
+  r->heads = in->heads; r->out_dt = out->dtype;
+  return KVQ_OK;
+}
+
+KVQ_API kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_rows* k, const kvq_rows* v,
+                                    const void* w_q, const void* w_k, float eps, const float* rope_cos,
+                                    const float* rope_sin, int max_ctx, const int32_t* pos, const kvq_rows* q_out,
+                                    const kvq_rows* k_out, const kvq_rows* v_out, kvq_stream stream) {
+  if (D != kvq::kD) return fail(KVQ_ERR_UNSUPPORTED, "%s: D=%d (this build supports 128)", __func__, D);
+  if (B < 0 || N < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: B or N < 0", __func__);
+  if (!q && !k && !v) return fail(KVQ_ERR_INVALID_ARG, "%s: no rows given", __func__);
+  if (!(eps >= 1e-30f && eps <= 1.f)) return fail(KVQ_ERR_INVALID_ARG, "%s: eps outside [1e-30, 1]", __func__);
+  kvq::QkRowsArgs a{};
+  const int dt = q ? q->dtype : k ? k->dtype : v->dtype;
+  kvq_status st;
+  if ((st = check_rows(__func__, "query", q, q_out, dt, &a.q)) != KVQ_OK) return st;
+  if ((st = check_rows(__func__, "key", k, k_out, dt, &a.k)) != KVQ_OK) return st;
+  if ((st = check_rows(__func__, "value", v, v_out, dt, &a.v)) != KVQ_OK) return st;
+  if (q) CHECK_PTR(w_q);
+  if (k) CHECK_PTR(w_k);
+  if (!rope_cos != !rope_sin) return fail(KVQ_ERR_INVALID_ARG, "%s: rope_cos and rope_sin go together", __func__);
+  if (rope_cos) {
+    CHECK_PTR(rope_cos);
+    CHECK_PTR(rope_sin);
+    if (max_ctx <= 0) return fail(KVQ_ERR_INVALID_ARG, "%s: max_ctx <= 0", __func__);
+    if (!pos) return fail(KVQ_ERR_INVALID_ARG, "%s: rotation needs positions", __func__);
+  }
+  if (pos) CHECK_PTR(pos);
+  if (B == 0 || N == 0) return KVQ_OK;
+  const int rows = a.q.heads + a.k.heads + a.v.heads;
+  if ((double)B * N * ((rows + 3) / 4) >= 2147483648.0)
+    return fail(KVQ_ERR_UNSUPPORTED, "%s: too many rows for one call", __func__);
+  a.wq = w_q; a.wk = w_k; a.cos = rope_cos; a.sin = rope_sin; a.pos = pos; a.err = device_error_ptr();
+  a.eps = eps; a.B = B; a.N = N; a.max_ctx = max_ctx;
+  return cuda_status(kvq::launch_qk_rows(a, dt, (cudaStream_t)stream), __func__);
+}
+
+KVQ_API size_t kvq_kivi_tree_workspace_size(const kvq_kivi_cfg* c, int B, int N) {
+  if (check_kivi_cfg(c, __func__) != KVQ_OK || B <= 0 || N <= 0 || N > 64) return 0;
+  return align256(kvq::kivi_tree_ws_bytes(B, N, c->n_heads, c->n_q_heads, c->k_bits, c->v_bits));
+}
+
+KVQ_API kvq_status kvq_kivi_tree_attn(const kvq_kivi_cfg* c, const kvq_kivi_cache* k, const uint16_t* q,
+                                      const uint16_t* k_draft, const uint16_t* v_draft, const uint64_t* mask,
+                                      const int32_t* n_draft, int B, int N, void* out, int out_dtype, void* ws,
+                                      size_t ws_bytes, kvq_stream stream) {
+  kvq_status st = check_kivi_cfg(c, __func__);
+  if (st != KVQ_OK) return st;
+  if ((st = check_kivi_cache(k, __func__)) != KVQ_OK) return st;
+  CHECK_PTR(q);
+  CHECK_PTR(k_draft);
+  CHECK_PTR(v_draft);
+  CHECK_PTR(mask);
+  if (n_draft) CHECK_PTR(n_draft);
+  CHECK_PTR(out);
+  if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_FP32)
+    return fail(KVQ_ERR_INVALID_ARG, "%s: out_dtype must be KVQ_OUT_BF16 or KVQ_OUT_FP32", __func__);
+  if (B < 1 || N < 1) return fail(KVQ_ERR_INVALID_ARG, "%s: B or N < 1", __func__);
+  if (B > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: B > max_batch", __func__);
+  if (N > 64) return fail(KVQ_ERR_UNSUPPORTED, "%s: N=%d (a tree has at most 64 drafted tokens)", __func__, N);
+  if ((double)B * c->n_heads * ((double)N * (c->n_q_heads / c->n_heads) + 64) >= 2147483648.0)
+    return fail(KVQ_ERR_UNSUPPORTED, "%s: too many query rows for one call", __func__);
+  const size_t need = kvq_kivi_tree_workspace_size(c, B, N);
+  if (!ws || ws_bytes < need || !aligned16(ws))
+    return fail(KVQ_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu)", __func__, need, ws_bytes);
+  kvq::KiviTreeArgs a{};
+  a.k_codes = k->k_codes; a.k_scale = k->k_scale; a.k_zero = k->k_zero;
+  a.v_codes = k->v_codes; a.v_scale = k->v_scale; a.v_zero = k->v_zero;
+  a.k_resid = k->k_resid; a.v_resid = k->v_resid;
+  a.n_tok = k->n_tok; a.n_quant_k = k->n_quant_k; a.n_quant_v = k->n_quant_v;
+  a.q = q; a.k_draft = k_draft; a.v_draft = v_draft; a.mask = mask; a.n_draft = n_draft;
+  a.out = out; a.out_fp32 = (out_dtype == KVQ_OUT_FP32); a.part = static_cast<float*>(ws); a.err = device_error_ptr();
+  a.B = B; a.N = N; a.H = c->n_heads; a.Hq = c->n_q_heads; a.k_bits = c->k_bits; a.v_bits = c->v_bits;
+  a.max_tokens = c->max_tokens; a.residual = c->residual;
+  return cuda_status(kvq::launch_kivi_tree(a, (cudaStream_t)stream), __func__);
 }
 
 KVQ_API size_t kvq_decode_workspace_size(int format, const void* cfg, int B, int n_splits) {

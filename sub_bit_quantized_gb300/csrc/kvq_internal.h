@@ -168,6 +168,30 @@ struct KiviAppendArgs {
 };
 cudaError_t launch_kivi_append(const KiviAppendArgs& a, cudaStream_t s);
 
+struct KiviCommitArgs {
+  const uint16_t* k_draft; const uint16_t* v_draft;  // fp16 [n_seq][N][H][D]
+  const int32_t* path; const int32_t* n_accept;      // [n_seq][N], [n_seq]
+  uint8_t* k_codes; uint16_t* k_scale; uint16_t* k_zero;
+  uint8_t* v_codes; uint16_t* v_scale; uint16_t* v_zero;
+  uint16_t* k_resid; uint16_t* v_resid;
+  int32_t* n_tok; int32_t* n_quant_k; int32_t* n_quant_v; int32_t* sync;
+  int* err;
+  int n_seq, N, H, k_bits, v_bits, residual, max_tokens;
+};
+cudaError_t launch_kivi_commit(const KiviCommitArgs& a, cudaStream_t s);
+
+struct KiviReadArgs {
+  const uint8_t* k_codes; const uint16_t* k_scale; const uint16_t* k_zero;
+  const uint8_t* v_codes; const uint16_t* v_scale; const uint16_t* v_zero;
+  const uint16_t* k_resid; const uint16_t* v_resid;
+  const int32_t* n_tok; const int32_t* n_quant_k; const int32_t* n_quant_v;
+  const int32_t* tok_begin;        // [B], request b0 + i begins at tok_begin[i]; null: 0
+  void* k_out; void* v_out;        // element (i, h, j, ch) at i*sb + h*sh + j*D + ch; one may be null
+  int64_t sb, sh;
+  int b0, B, H, k_bits, v_bits, residual, max_tokens, n_tok_out;
+};
+cudaError_t launch_kivi_read(const KiviReadArgs& a, int out_dt, cudaStream_t s);
+
 struct KiviAttnArgs {
   const uint8_t* k_codes; const uint16_t* k_scale; const uint16_t* k_zero;
   const uint8_t* v_codes; const uint16_t* v_scale; const uint16_t* v_zero;
@@ -185,5 +209,41 @@ size_t kivi_attn_smem_bytes(int k_bits, int v_bits, int heads_per_block, int res
 int kivi_attn_blocks_per_sm(int k_bits, int v_bits, int heads_per_block);  // resident attention blocks per SM
 int kivi_attn_max_tok_per_split(int residual);
 cudaError_t launch_kivi_attn(const KiviAttnArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- tree attention
+struct KiviTreeArgs {
+  const uint8_t* k_codes; const uint16_t* k_scale; const uint16_t* k_zero;
+  const uint8_t* v_codes; const uint16_t* v_scale; const uint16_t* v_zero;
+  const uint16_t* k_resid; const uint16_t* v_resid;
+  const int32_t* n_tok; const int32_t* n_quant_k; const int32_t* n_quant_v;
+  const uint16_t* q;               // bf16 [B][N][Hq][D]
+  const uint16_t* k_draft; const uint16_t* v_draft;  // fp16 [B][N][H][D]
+  const uint64_t* mask;            // [B][N]
+  const int32_t* n_draft;          // [B], null: N
+  void* out; int out_fp32;         // [B][N][Hq][D]
+  float* part;                     // partial softmaxes of segments shared by blocks
+  int* err;
+  int B, N, H, Hq, k_bits, v_bits, max_tokens, residual;
+};
+// bytes of partials a launch of this shape may write
+size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits);
+cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- norm and rotation of rows
+struct QkRows {                    // rows of one kind: heads == 0 when absent
+  const void* in; void* out;
+  int64_t sb, st, sh, ob, ot, oh;  // element strides of (request, token, head), input and output
+  int heads, out_dt;
+};
+struct QkRowsArgs {
+  QkRows q, k, v;
+  const void* wq; const void* wk;  // [D], of the input's type
+  const float* cos; const float* sin;  // [max_ctx][D/2] or null
+  const int32_t* pos;              // [B][N] or null
+  int* err;
+  float eps;
+  int B, N, max_ctx;
+};
+cudaError_t launch_qk_rows(const QkRowsArgs& a, int in_dt, cudaStream_t s);
 
 }  // namespace kvq

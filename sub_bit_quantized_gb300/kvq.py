@@ -24,6 +24,7 @@ STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARG", 2: "KVQ_ERR_CAPACITY", 3: "KVQ_
 FMT_LOOPVQ, FMT_KIVI = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 PER_CHANNEL, PER_TOKEN = 0, 1
+DT_BF16, DT_FP32, DT_FP16 = 0, 1, 2
 PAGE = 8
 
 
@@ -64,8 +65,14 @@ class KiviCacheC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in KIVI_CACHE_FIELDS]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("heads", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _SIGS = {
@@ -84,6 +91,11 @@ _SIGS = {
     "kvq_quantize_kivi": (_I, [_P, _I, _P, _I64, _I64, _I, _I, _P, _P, _P, _I, _P]),
     "kvq_kivi_prefill": (_I, [_P, _P, _P, _P, _I64, _I64, _I, _I, _I, _P]),
     "kvq_kivi_append": (_I, [_P, _P, _P, _P, _I, _P]),
+    "kvq_kivi_commit": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "kvq_kivi_read": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I64, _I64, _P]),
+    "kvq_qk_norm_rope": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _F, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "kvq_kivi_tree_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _SZ, _P]),
+    "kvq_kivi_tree_workspace_size": (_SZ, [_P, _I, _I]),
     "kvq_decode_attn": (_I, [_I, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _SZ, _P]),
     "kvq_decode_attn_noalloc": (_I, [_I, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P]),
     "kvq_decode_workspace_size": (_SZ, [_I, _P, _I, _I]),
@@ -152,6 +164,43 @@ def _bits(t: torch.Tensor, dtypes) -> torch.Tensor:
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("expected a contiguous CUDA tensor")
     return t
+
+
+_DT = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32, torch.float16: DT_FP16}
+
+
+def _operand(name: str, t: torch.Tensor, dtypes, shape, contiguous: bool = True) -> torch.Tensor:
+    """``t`` if it has one of the types, the shape (None: any size) and lies on the current device."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected one of {dtypes}, got {t.dtype}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device, got one on {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t
+
+
+def _step(t: torch.Tensor, dim: int) -> int:
+    """The stride of a dimension, 0 where it has one entry (any number may stand there)."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+class _Call:
+    """Pre-marshalled arguments of a repeated library call. It holds its tensors, and runs on ``stream``
+    or else on the stream that is current when it is called."""
+
+    def __init__(self, name: str, stream, device, keep):
+        self._name, self._f = name, getattr(lib(), name)
+        self._stream, self._device, self._keep = stream, device, keep
+
+    def __call__(self):
+        s = self._stream
+        s = torch.cuda.current_stream(self._device).cuda_stream if s is None else _stream(s)
+        st = self._f(*self._args, s)
+        if st != KVQ_OK:
+            _check(st, self._name)
 
 
 # ------------------------------------------------------------------------------------------
@@ -393,6 +442,156 @@ def kvq_kivi_append(cfg: KiviConfig, cache: KiviCache, k_new, v_new, stream=None
     kc = cache.c_struct()
     _check(lib().kvq_kivi_append(ctypes.byref(c), ctypes.byref(kc), _ptr(k_new), _ptr(v_new), k_new.shape[0],
                                  _stream(stream)), "kvq_kivi_append")
+
+
+class KiviCommitCall(_Call):
+    """kvq_kivi_commit: k_draft, v_draft fp16 [n_seq][N][H][D], path int32 [n_seq][N], n_accept int32 [n_seq]."""
+
+    def __init__(self, cfg: KiviConfig, cache: KiviCache, k_draft, v_draft, path, n_accept, stream=None):
+        n_seq, N = path.shape
+        for name, x in (("k_draft", k_draft), ("v_draft", v_draft)):
+            _operand(name, x, (torch.float16,), (n_seq, N, cfg.n_heads, cfg.D))
+        _operand("path", path, (torch.int32,), (n_seq, N))
+        _operand("n_accept", n_accept, (torch.int32,), (n_seq,))
+        c, kc = cfg.to_c(), cache.c_struct()
+        super().__init__("kvq_kivi_commit", stream, path.device, (c, kc, cache, k_draft, v_draft, path, n_accept))
+        self._args = (ctypes.byref(c), ctypes.byref(kc), _ptr(k_draft), _ptr(v_draft), _ptr(path), _ptr(n_accept),
+                      n_seq, N)
+
+
+def kvq_kivi_commit(cfg: KiviConfig, cache: KiviCache, k_draft, v_draft, path, n_accept, stream=None):
+    """Append request b's drafted tokens path[b, :n_accept[b]] to the cache, in that order."""
+    KiviCommitCall(cfg, cache, k_draft, v_draft, path, n_accept, stream)()
+
+
+class KiviReadCall(_Call):
+    """kvq_kivi_read into k_out and v_out (bf16, fp16 or fp32 [B][H][n_tok][D], rows of D contiguous channels
+    packed along the tokens, one of them may be None); tok_begin int32 [B] or None."""
+
+    def __init__(self, cfg: KiviConfig, cache: KiviCache, k_out, v_out, tok_begin=None, b0: int = 0, stream=None):
+        x = k_out if k_out is not None else v_out
+        if x is None:
+            raise ValueError("neither k_out nor v_out is given")
+        B, _, n, _ = x.shape
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
+                _operand(name, t, tuple(_DT), (B, cfg.n_heads, n, cfg.D), contiguous=False)
+                if t.stride(3) != 1 or (n > 1 and t.stride(2) != cfg.D):
+                    raise ValueError(f"{name}: expected rows of D contiguous channels, packed along the tokens")
+                if t.dtype != x.dtype or (_step(t, 0), _step(t, 1)) != (_step(x, 0), _step(x, 1)):
+                    raise ValueError("k_out and v_out need one type and layout")
+        if tok_begin is not None:
+            _operand("tok_begin", tok_begin, (torch.int32,), (B,))
+        c, kc = cfg.to_c(), cache.c_struct()
+        super().__init__("kvq_kivi_read", stream, x.device, (c, kc, cache, k_out, v_out, tok_begin))
+        self._args = (ctypes.byref(c), ctypes.byref(kc), _ptr(tok_begin), b0, B, n, _ptr(k_out), _ptr(v_out),
+                      _DT[x.dtype], _step(x, 0), _step(x, 1))
+
+
+def kvq_kivi_read(cfg: KiviConfig, cache: KiviCache, k_out, v_out, tok_begin=None, b0: int = 0, stream=None):
+    """Read the cached tokens tok_begin[i] + j of requests b0 + i back into rows j of k_out and v_out."""
+    KiviReadCall(cfg, cache, k_out, v_out, tok_begin, b0, stream)()
+
+
+# ------------------------------------------------------------------------------------------
+# Rows of queries, keys and values
+# ------------------------------------------------------------------------------------------
+
+def _rows(t: torch.Tensor | None):
+    if t is None:
+        return None
+    return Rows(t.data_ptr(), _step(t, 0), _step(t, 1), _step(t, 2), t.shape[2], _DT[t.dtype])
+
+
+class QkNormRopeCall(_Call):
+    """kvq_qk_norm_rope over tensors [B][N][heads][D] of any strides with contiguous channels (views of a fused
+    projection among them). q, k, v share a type; each may be None together with its output. w_q, w_k: [D] of that
+    type. rope_cos, rope_sin: fp32 [max_ctx][D/2] or None; pos: int32 [B][N], None only without rotation."""
+
+    def __init__(self, q, k, v, w_q, w_k, eps, rope_cos, rope_sin, pos, q_out, k_out, v_out, stream=None):
+        x = next((t for t in (q, k, v) if t is not None), None)
+        if x is None:
+            raise ValueError("none of q, k and v is given")
+        if x.dtype not in _DT:
+            raise TypeError(f"expected one of {tuple(_DT)}, got {x.dtype}")
+        B, N, _, D = x.shape
+        for name, i, o in (("q", q, q_out), ("k", k, k_out), ("v", v, v_out)):
+            if (i is None) != (o is None):
+                raise ValueError(f"{name} needs both an input and an output")
+            if i is not None:
+                _operand(name, i, (x.dtype,), (B, N, None, D), contiguous=False)
+                _operand(name + "_out", o, tuple(_DT), (B, N, i.shape[2], D), contiguous=False)
+                if i.stride(3) != 1 or o.stride(3) != 1:
+                    raise ValueError(f"{name}: the channels of a row need to be contiguous")
+        for name, i, w in (("w_q", q, w_q), ("w_k", k, w_k)):
+            if i is not None:
+                if w is None:
+                    raise ValueError(f"{name} is missing")
+                _operand(name, w, (x.dtype,), (D,))
+        if (rope_cos is None) != (rope_sin is None):
+            raise ValueError("rope_cos and rope_sin go together")
+        if rope_cos is not None:
+            _operand("rope_cos", rope_cos, (torch.float32,), (None, D // 2))
+            _operand("rope_sin", rope_sin, (torch.float32,), tuple(rope_cos.shape))
+        if pos is not None:
+            _operand("pos", pos, (torch.int32,), (B, N))
+        rows = [_rows(t) for t in (q, k, v, q_out, k_out, v_out)]
+        super().__init__("kvq_qk_norm_rope", stream, x.device,
+                         (rows, q, k, v, w_q, w_k, rope_cos, rope_sin, pos, q_out, k_out, v_out))
+        ref = [None if r is None else ctypes.byref(r) for r in rows]
+        self._args = (D, B, N, *ref[:3], _ptr(w_q) if q is not None else None, _ptr(w_k) if k is not None else None,
+                      float(eps), _ptr(rope_cos), _ptr(rope_sin), 0 if rope_cos is None else rope_cos.shape[0],
+                      _ptr(pos), *ref[3:])
+
+
+def kvq_qk_norm_rope(q, k, v, w_q, w_k, eps, rope_cos, rope_sin, pos, q_out, k_out, v_out, stream=None):
+    """Norm of queries and keys for each head and the position rotation in one pass; values are converted."""
+    QkNormRopeCall(q, k, v, w_q, w_k, eps, rope_cos, rope_sin, pos, q_out, k_out, v_out, stream)()
+
+
+# ------------------------------------------------------------------------------------------
+# Attention of drafted tokens
+# ------------------------------------------------------------------------------------------
+
+def kvq_kivi_tree_workspace_size(cfg: KiviConfig, B: int, N: int) -> int:
+    c = cfg.to_c()
+    return lib().kvq_kivi_tree_workspace_size(ctypes.byref(c), B, N)
+
+
+def make_tree_workspace(cfg: KiviConfig, B: int, N: int, device="cuda") -> torch.Tensor:
+    """A workspace for kvq_kivi_tree_attn (needs no initialisation; one for each call that runs at a time)."""
+    return torch.empty(max(16, kvq_kivi_tree_workspace_size(cfg, B, N)), dtype=torch.uint8, device=device)
+
+
+class TreeAttnCall(_Call):
+    """kvq_kivi_tree_attn: q bf16 [B][N][Hq][D], k_draft and v_draft fp16 [B][N][H][D], mask int64 (or uint64)
+    [B][N] (bit j: drafted token j is seen), out bf16 or fp32 [B][N][Hq][D], n_draft int32 [B] or None (all N)."""
+
+    def __init__(self, cfg: KiviConfig, cache: KiviCache, q, k_draft, v_draft, mask, out, n_draft=None, ws=None,
+                 stream=None):
+        B, N = mask.shape
+        _operand("q", q, (torch.bfloat16,), (B, N, cfg.q_heads, cfg.D))
+        _operand("out", out, (torch.bfloat16, torch.float32), tuple(q.shape))
+        for name, x in (("k_draft", k_draft), ("v_draft", v_draft)):
+            _operand(name, x, (torch.float16,), (B, N, cfg.n_heads, cfg.D))
+        _operand("mask", mask, (torch.int64, torch.uint64), (B, N))
+        if n_draft is not None:
+            _operand("n_draft", n_draft, (torch.int32,), (B,))
+        if ws is None:
+            ws = make_tree_workspace(cfg, B, N, q.device)
+        c, kc = cfg.to_c(), cache.c_struct()
+        super().__init__("kvq_kivi_tree_attn", stream, q.device,
+                         (c, kc, cache, q, k_draft, v_draft, mask, out, n_draft, ws))
+        self._args = (ctypes.byref(c), ctypes.byref(kc), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
+                      _ptr(n_draft), B, N, _ptr(out), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16,
+                      _ptr(ws), ws.numel() * ws.element_size())
+
+
+def kvq_kivi_tree_attn(cfg: KiviConfig, cache: KiviCache, q, k_draft, v_draft, mask, out, n_draft=None, ws=None,
+                       stream=None):
+    """Attention of a tree of drafted tokens over the cache and one another. Without a workspace one is allocated
+    for this call (through PyTorch)."""
+    TreeAttnCall(cfg, cache, q, k_draft, v_draft, mask, out, n_draft, ws, stream)()
 
 
 # ------------------------------------------------------------------------------------------
