@@ -105,17 +105,18 @@ __global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a
   for (int i = 0; i < 8; ++i) ss = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], ss));
   ss = sum8(0xFFFFFFFFu, ss);
   float r = rsqrtf(fmaf(ss, 1.f / kD, a.eps));
-  if (!(ss < 1e37f)) {
-    // squares of large bf16 or fp32 values pass the fp32 range: the mean of (x 2^-64)^2 instead
-    // (eps is far below its rounding). All eight lanes of a row come here, the warp's others may not.
-    constexpr float kDown = 5.42101086242752217e-20f;  // 2^-64
+  if (!is_v && !(ss < 1e37f)) {
+    // squares of large bf16 or fp32 values pass the fp32 range: the row times 2^-72 instead (eps is far
+    // below the mean's rounding). All eight lanes of a row come here, the warp's others may not.
+    constexpr float kDown = 2.117582368135750837e-22f;  // 2^-72
     float s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float x = lo[i] * kDown, y = hi[i] * kDown;
-      s2 = fmaf(x, x, fmaf(y, y, s2));
+      lo[i] *= kDown;
+      hi[i] *= kDown;
+      s2 = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], s2));
     }
-    r = rsqrtf(sum8(0xFFu << (lane & 24), s2) * (1.f / kD)) * kDown;
+    r = rsqrtf(sum8(0xFFu << (lane & 24), s2) * (1.f / kD));
   }
   if (!there) return;
   if (!is_v) {
