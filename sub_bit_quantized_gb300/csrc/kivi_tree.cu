@@ -15,7 +15,7 @@
 // 2^kSlack (a block-wide vote), the sums l stay per thread until the segment ends.
 #include <cuda_fp16.h>
 
-#include <algorithm>
+#include <cfloat>
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
@@ -32,26 +32,35 @@ constexpr float kSlack = 7.f;   // log2 by which a score may pass its row's runn
 constexpr float kRaise = 8.f;   // weights are exp2(x - m + kRaise) <= 2^15, held as fp16: one below 2^-32 of the
                                 // maximum's is lost instead of one below 2^-24
 
-// V^T is staged in 8 channel x 8 token core matrices; those of consecutive token octets are 144
-// bytes apart so that eight threads with eight octets store to different banks
-constexpr int kVOct = 144;
-constexpr int kVRowGrp = (kTile / 8) * kVOct;
+// V^T is staged in 8 channel x 8 token core matrices: the 16 of a row group (8 channels) are contiguous, row
+// groups 2064 bytes apart, so that eight threads with eight row groups store to different banks
+constexpr int kVRowGrp = (kTile / 8) * 128 + 16;
 
-template <int ROWS>
+template <int KB, int VB, int ROWS>
 struct TreeLayout {
+  static constexpr int kKRow = kD * KB / 8, kVRow = kD * VB / 8;   // code bytes per token
   static constexpr int kOffQ = 0;                                  // fp16 [ROWS x 128], K-major
   static constexpr int kOffK = kOffQ + ROWS * kD * 2;              // fp16 [128 tokens x 128], K-major; then P
   static constexpr int kOffV = kOffK + kTile * kD * 2;             // fp16 [128 channels x 128 tokens], K-major
-  static constexpr int kOffMask = kOffV + (kD / 8) * kVRowGrp;     // uint64 [ROWS]
+  // a tile as it is stored: key codes, scales and zeros [4 groups][128], value codes, scales and zeros [128][4]
+  static constexpr int kOffKc = (kOffV + (kD / 8) * kVRowGrp + 127) / 128 * 128;
+  static constexpr int kOffKs = kOffKc + kTile * kKRow;
+  static constexpr int kOffKz = kOffKs + (kTile / kGroupT) * kD * 2;
+  static constexpr int kOffVc = kOffKz + (kTile / kGroupT) * kD * 2;
+  static constexpr int kOffVs = kOffVc + kTile * kVRow;
+  static constexpr int kOffVz = kOffVs + kTile * (kD / kGroupT) * 2;
+  static constexpr int kOffMask = kOffVz + kTile * (kD / kGroupT) * 2;  // uint64 [ROWS]
   static constexpr int kOffC = kOffMask + ROWS * 8;                // float [ROWS]: log2 units per score unit
-  static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: running maximum (log2)
-  static constexpr int kOffF = kOffM + ROWS * 4;                   // float [ROWS]: rescale factor
+  static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: running maximum (log2) - kRaise
+  static constexpr int kOffT = kOffM + ROWS * 4;                   // float [ROWS]: running maximum + kSlack
+  static constexpr int kOffF = kOffT + ROWS * 4;                   // float [ROWS]: rescale factor
   static constexpr int kOffRed = kOffF + ROWS * 4;                 // float [4][ROWS]: per lane quadrant
   static constexpr int kOffBar = kOffRed + 4 * ROWS * 4;           // mbarriers, TMEM address, flags
   static constexpr int kSmem = kOffBar + 64;
   static constexpr uint32_t kCols = 2 * ROWS < 32 ? 32 : 2 * ROWS;  // TMEM: S^T, O^T
+  static constexpr uint32_t kKBytes = kOffVc - kOffKc, kVBytes = kOffMask - kOffVc;
   static_assert(ROWS * 256 <= kTile * kD * 2, "P fits in the key tile");
-  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kSmem <= 232448 / 2 - 1024, "two blocks per SM");
 };
 
 // shared-memory matrix descriptor, no swizzle. K-major: lbo steps 8 elements along K, sbo 8 rows;
@@ -199,18 +208,63 @@ __device__ __forceinline__ uint4 value8(const Token& k, int t, int c, int* nonfi
   return make_uint4(0u, 0u, 0u, 0u);
 }
 
+// Channel order of the staged keys and queries. The contraction runs over all 128 channels, so any order serves
+// that both share; this one is the order in which a code word's halves unpack: pairs (c, c + 8) of 16 channels
+// (2 bits), (c, c + 4) of 8 (4 bits). lo, hi: channels 16 w .. + 7, 16 w + 8 .. + 15, natural order; out: the two
+// 16-byte chunks of the block.
+template <int KB>
+__device__ __forceinline__ void pair_order(const uint4 lo, const uint4 hi, uint4& out0, uint4& out1) {
+  if constexpr (KB == 2) {
+    out0 = make_uint4(__byte_perm(lo.x, hi.x, 0x5410), __byte_perm(lo.x, hi.x, 0x7632), __byte_perm(lo.y, hi.y, 0x5410),
+                      __byte_perm(lo.y, hi.y, 0x7632));
+    out1 = make_uint4(__byte_perm(lo.z, hi.z, 0x5410), __byte_perm(lo.z, hi.z, 0x7632), __byte_perm(lo.w, hi.w, 0x5410),
+                      __byte_perm(lo.w, hi.w, 0x7632));
+  } else {
+    out0 = make_uint4(__byte_perm(lo.x, lo.z, 0x5410), __byte_perm(lo.x, lo.z, 0x7632), __byte_perm(lo.y, lo.w, 0x5410),
+                      __byte_perm(lo.y, lo.w, 0x7632));
+    out1 = make_uint4(__byte_perm(hi.x, hi.z, 0x5410), __byte_perm(hi.x, hi.z, 0x7632), __byte_perm(hi.y, hi.w, 0x5410),
+                      __byte_perm(hi.y, hi.w, 0x7632));
+  }
+}
+// Token order of the staged values and weights: in odd octets neighbours change places, so that the two octets a
+// warp reads at a time come from different banks.
+__device__ __forceinline__ int token_place(int t) { return t ^ ((t >> 3) & 1); }
+
+__device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t as_u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+// Code j of both halves of w as fp16 (exact): masked in place under the exponent of 2^10, where it stands for
+// 1024 + c 2^(b j), and scaled back by one FMA. Codes above the ten mantissa bits come from w shifted right.
+template <int BITS>
+__device__ __forceinline__ __half2 code_h2(uint32_t w, int j) {
+  constexpr int kIn = (BITS == 2) ? 5 : 2;  // codes that fit in place
+  const int jj = j < kIn ? j : j - kIn;
+  const uint32_t m = ((j < kIn ? w : w >> (BITS * kIn)) & ((((1u << BITS) - 1u) << (BITS * jj)) * 0x10001u)) | 0x64006400u;
+  const float p = 1.f / (float)(1 << (BITS * jj));
+  return __hfma2(as_h2(m), __float2half2_rn(p), __float2half2_rn(-1024.f * p));
+}
+// s c - s z, one rounding of s z and one of the result
+__device__ __forceinline__ uint32_t dequant_h2(__half2 c, __half2 s, __half2 nsz) { return as_u(__hfma2(c, s, nsz)); }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <int KB, int VB, int ROWS>
 __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTreeArgs a, const float scale_log2) {
-  using L = TreeLayout<ROWS>;
+  using L = TreeLayout<KB, VB, ROWS>;
   extern __shared__ __align__(128) unsigned char sm[];
   uint64_t* mask = reinterpret_cast<uint64_t*>(sm + L::kOffMask);
   float* rowc = reinterpret_cast<float*>(sm + L::kOffC);
   float* rowm = reinterpret_cast<float*>(sm + L::kOffM);
+  float* rowt = reinterpret_cast<float*>(sm + L::kOffT);
   float* rowf = reinterpret_cast<float*>(sm + L::kOffF);
   float* red = reinterpret_cast<float*>(sm + L::kOffRed);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // scores done
   uint64_t* bar_o = bar_s + 1;                                      // value product done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_o + 1);
+  uint64_t* bar_k = bar_s + 2;                                      // the tile's stored keys landed
+  uint64_t* bar_v = bar_s + 3;                                      // its stored values
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 4);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* nonfinite = reinterpret_cast<int*>(tmem_slot + 2);
   long long* scan = reinterpret_cast<long long*>(sm);  // before the first tile: one per thread
@@ -250,12 +304,36 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // the stored keys (values) of a tile whose tokens are all quantized: into the stage by bulk copies
+  auto copy_keys = [&](int cb, int ch, int t0) {
+    const size_t bh = (size_t)cb * a.H + ch, g = (bh * (a.max_tokens / kGroupT) + t0 / kGroupT) * kD;
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(bar_k, L::kKBytes);
+    bulk_g2s(sm + L::kOffKc, a.k_codes + (bh * a.max_tokens + t0) * L::kKRow, kTile * L::kKRow, bar_k);
+    bulk_g2s(sm + L::kOffKs, a.k_scale + g, L::kOffKz - L::kOffKs, bar_k);
+    bulk_g2s(sm + L::kOffKz, a.k_zero + g, L::kOffVc - L::kOffKz, bar_k);
+  };
+  auto copy_values = [&](int cb, int ch, int t0) {
+    const size_t tok = ((size_t)cb * a.H + ch) * a.max_tokens + t0;
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(bar_v, L::kVBytes);
+    bulk_g2s(sm + L::kOffVc, a.v_codes + tok * L::kVRow, kTile * L::kVRow, bar_v);
+    bulk_g2s(sm + L::kOffVs, a.v_scale + tok * (kD / kGroupT), L::kOffVz - L::kOffVs, bar_v);
+    bulk_g2s(sm + L::kOffVz, a.v_zero + tok * (kD / kGroupT), L::kOffMask - L::kOffVz, bar_v);
+  };
+  auto stored = [](const TreeLens& l, int tl) { return (tl + 1) * kTile <= l.nqv; };  // nqv <= nqk
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_o, 1);
+    mbar_init(bar_k, 1);
+    mbar_init(bar_v, 1);
     *failed = 0;
     *nonfinite = 0;
     fence_mbar_init();
+    if (stored(len, tile)) {
+      copy_keys(b, seg / n_rt, tile * kTile);
+      copy_values(b, seg / n_rt, tile * kTile);
+    }
   }
   tmem_before();
   __syncthreads();
@@ -265,58 +343,137 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
   constexpr int kHR = ROWS / 2;                            // rows a thread works on
   const int r0 = half * kHR;
-  uint32_t phase = 0;   // of both barriers: one completion each per tile
+  uint32_t phase = 0;    // of bar_s and bar_o: one completion each per tile
+  uint32_t landed = 0;   // tiles that came through the stage: their parity is that of bar_k and bar_v
   float l[kHR];
   bool first = true;    // of the segment's tiles in this block
   int tile_first = 0;   // that tile
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait_bounded(bar, parity)) {
+      *failed = 1;
+      set_error(a.err, KVQ_ERR_TIMEOUT);
+    }
+  };
 
   for (long long p = p0; p < p1; ++p) {
     const int h = seg / n_rt, rt = seg % n_rt;
     const Token tk = {&a, len, (size_t)b * a.H + h, b, h};
     const int row0 = rt * ROWS;
+    const int t0 = tile * kTile;
+    const bool from_stage = stored(len, tile);
+    // ---- the position after this one ----
+    const bool last = tile + 1 == len.tiles;
+    int nb = b, nseg = seg, ntile = tile + 1;
+    TreeLens nlen = len;
+    if (last) {
+      ntile = 0;
+      if (++nseg == seg_per_b) {
+        nseg = 0;
+        if (p + 1 < p1) {
+          do nlen = tree_lens(a, ++nb);
+          while (nlen.tiles == 0);  // a position is left, so such a request exists
+        }
+      }
+    }
+    const bool copy_next = p + 1 < p1 && stored(nlen, ntile);
     if (first) {
       // ---- the segment's query rows: fp16, each divided by a power of two that puts its largest
       //      magnitude in [2^14, 2^15); the masks and the running state ----
 #pragma unroll
       for (int i = 0; i < kHR; ++i) l[i] = 0.f;
-      for (int i = tid; i < ROWS * 16; i += kTreeThreads) {  // 16 lanes per row
-        const int r = i >> 4, c = i & 15, row = row0 + r, di = row / rep;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows_all && di < len.nd)
-          u = __ldg(reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 8 * c));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int i = tid; i < ROWS * 8; i += kTreeThreads) {  // 8 lanes per row, 16 channels each
+        const int r = i >> 3, c = i & 7, row = row0 + r, di = row / rep;
+        uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (row < rows_all && di < len.nd) {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 16 * c);
+          u[0] = __ldg(src);
+          u[1] = __ldg(src + 1);
+        }
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
         float mx = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
 #pragma unroll
-        for (int off = 8; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+        for (int off = 4; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
         const int ex = (int)(__float_as_uint(mx) >> 23);  // biased exponent; 0: zero or subnormal, 255: not finite
         // times 2^(14 - (ex - 127)) in two factors, since the power may pass the fp32 range
         const int sh = (ex == 0 || ex == 255) ? 0 : 141 - ex;
         const float f1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
-        uint32_t o[4];
+        uint32_t o[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = pack_h2(bf16_lo(w[e]) * f1 * f2, bf16_hi(w[e]) * f1 * f2);
-        *reinterpret_cast<uint4*>(sm + L::kOffQ + (r >> 3) * 2048 + c * 128 + (r & 7) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int e = 0; e < 8; ++e) o[e] = pack_h2(bf16_lo(w[e]) * f1 * f2, bf16_hi(w[e]) * f1 * f2);
+        uint4 x0, x1;
+        pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
+        unsigned char* dst = sm + L::kOffQ + (r >> 3) * 2048 + c * 256 + (r & 7) * 16;
+        *reinterpret_cast<uint4*>(dst) = x0;
+        *reinterpret_cast<uint4*>(dst + 128) = x1;
         if (c == 0) {
           rowc[r] = scale_log2 / f1 / f2;
-          rowm[r] = -INFINITY;
+          rowm[r] = rowt[r] = -FLT_MAX;
           mask[r] = (row < rows_all && di < len.nd) ? a.mask[(size_t)b * a.N + di] : 0ull;
         }
       }
       if (tid == 0) *nonfinite = 0;
       tile_first = tile;
     }
-    const int t0 = tile * kTile;
-    // ---- keys of the tile: thread (token, 16-byte chunk), eight tokens x four chunks a warp step ----
-#pragma unroll 2
-    for (int i = warp; i < 64; i += kTreeWarps) {
-      const int t = 8 * (i >> 2) + (lane & 7), c = 4 * (i & 3) + (lane >> 3);
-      *reinterpret_cast<uint4*>(sm + L::kOffK + (t >> 3) * 2048 + c * 128 + (t & 7) * 16) = key8<KB>(tk, t0 + t, c);
+    // ---- keys of the tile. A lane takes token lane % 8 of an octet and a code word (2 bits: 16 channels, 4
+    //      bits: 8); a warp one key group and half of the words, so a lane unpacks four tokens per scale ----
+    if (from_stage) {
+      wait(bar_k, landed & 1);
+      const int g = warp & 3, tok = 32 * g + (lane & 7);
+      constexpr int kBlocks = (KB == 2) ? 1 : 2;   // of four words
+#pragma unroll
+      for (int blk = 0; blk < kBlocks; ++blk) {
+        const int w = (warp >> 2) * 4 * kBlocks + 4 * blk + (lane >> 3);
+        constexpr int kPairs = (KB == 2) ? 8 : 4;  // channel pairs of a word
+        __half2 s[kPairs], nsz[kPairs];
+        const uint4* sp = reinterpret_cast<const uint4*>(sm + L::kOffKs + (g * kD + 2 * kPairs * w) * 2);
+        const uint4* zp = reinterpret_cast<const uint4*>(sm + L::kOffKz + (g * kD + 2 * kPairs * w) * 2);
+        {
+          uint4 s0, s1 = make_uint4(0u, 0u, 0u, 0u), z0, z1 = s1;
+          if constexpr (KB == 2) {
+            pair_order<2>(sp[0], sp[1], s0, s1);
+            pair_order<2>(zp[0], zp[1], z0, z1);
+          } else {
+            uint4 none;
+            pair_order<4>(sp[0], sp[0], s0, none);
+            pair_order<4>(zp[0], zp[0], z0, none);
+          }
+          const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+          const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            s[j] = as_h2(sw[j]);
+            nsz[j] = __hneg2(__hmul2(s[j], as_h2(zw[j])));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = tok + 8 * i;
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(sm + L::kOffKc + t * L::kKRow + 4 * w);
+          uint32_t o[kPairs];
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) o[j] = dequant_h2(code_h2<KB>(u, j), s[j], nsz[j]);
+          unsigned char* dst = sm + L::kOffK + (t >> 3) * 2048 + w * (kPairs * 32) + (t & 7) * 16;
+          *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+          if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int i = warp; i < 32; i += kTreeWarps) {
+        const int t = 8 * (i >> 1) + (lane & 7), c = 4 * (i & 1) + (lane >> 3);  // 16 channels c
+        uint4 x0, x1;
+        pair_order<KB>(key8<KB>(tk, t0 + t, 2 * c), key8<KB>(tk, t0 + t, 2 * c + 1), x0, x1);
+        unsigned char* dst = sm + L::kOffK + (t >> 3) * 2048 + c * 256 + (t & 7) * 16;
+        *reinterpret_cast<uint4*>(dst) = x0;
+        *reinterpret_cast<uint4*>(dst + 128) = x1;
+      }
     }
     fence_proxy_async_smem();
     tmem_before();
-    __syncthreads();
+    if (__syncthreads_or(*failed)) break;
     if (tid == 0) {
       tmem_after();
 #pragma unroll
@@ -324,50 +481,112 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         umma_f16(tmem, tree_desc(smem_u32(sm + L::kOffK) + k * 256, 128, 2048),
                  tree_desc(smem_u32(sm + L::kOffQ) + k * 256, 128, 2048), tree_idesc(ROWS, false), k > 0);
       tree_commit(bar_s);
+      if (copy_next) copy_keys(nb, nseg / n_rt, ntile * kTile);  // every thread has read this tile's
     }
-    // ---- values of the tile, transposed: thread (token octet, eight channels) ----
+    // ---- values of the tile, transposed. A thread takes a token octet and eight channels ----
     {
-      const int oct = lane & 15, c = 2 * warp + (lane >> 4);
-      uint32_t x[8][4];
+      const int c = lane & 15, oct = 2 * warp + (lane >> 4), flip = oct & 1;
+      unsigned char* dst = sm + L::kOffV + c * kVRowGrp + oct * 128;
+      if (from_stage) {
+        wait(bar_v, landed & 1);
+        uint32_t w[8];  // place i of the octet: token i ^ flip
+        __half2 s[4], nsz[4];
+        const unsigned char* cw = sm + L::kOffVc + 8 * oct * L::kVRow + ((VB == 2) ? (c >> 1) : c) * 4;
+        const uint16_t* sp = reinterpret_cast<const uint16_t*>(sm + L::kOffVs) + 8 * oct * 4 + (c >> 2);
+        const uint16_t* zp = reinterpret_cast<const uint16_t*>(sm + L::kOffVz) + 8 * oct * 4 + (c >> 2);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 u = value8<VB>(tk, t0 + 8 * oct + i, c, nonfinite);
-        x[i][0] = u.x;
-        x[i][1] = u.y;
-        x[i][2] = u.z;
-        x[i][3] = u.w;
-      }
+        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(cw + (i ^ flip) * L::kVRow);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t o[4];
+        for (int i = 0; i < 4; ++i) {
+          const int ta = ((2 * i) ^ flip) * 4, tb = ((2 * i + 1) ^ flip) * 4;
+          s[i] = as_h2(sp[ta] | ((uint32_t)sp[tb] << 16));
+          nsz[i] = __hneg2(__hmul2(s[i], as_h2(zp[ta] | ((uint32_t)zp[tb] << 16))));
+        }
+        if constexpr (VB == 2) {
+          const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
+          uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = __byte_perm(x[2 * i][e >> 1], x[2 * i + 1][e >> 1], (e & 1) ? 0x7632 : 0x5410);
-        *reinterpret_cast<uint4*>(sm + L::kOffV + c * kVRowGrp + oct * kVOct + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int i = 0; i < 4; ++i) x[i] = __byte_perm(w[2 * i], w[2 * i + 1], sel);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<2>(x[i], e), s[i], nsz[i]);
+            *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        } else {
+#pragma unroll
+          for (int hw = 0; hw < 2; ++hw) {
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __byte_perm(w[2 * i], w[2 * i + 1], hw ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t o[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<4>(x[i], e), s[i], nsz[i]);
+              *reinterpret_cast<uint4*>(dst + (4 * hw + e) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        ++landed;
+      } else {
+        uint32_t x[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 u = value8<VB>(tk, t0 + 8 * oct + (i ^ flip), c, nonfinite);
+          x[i][0] = u.x;
+          x[i][1] = u.y;
+          x[i][2] = u.z;
+          x[i][3] = u.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = __byte_perm(x[2 * i][e >> 1], x[2 * i + 1][e >> 1], (e & 1) ? 0x7632 : 0x5410);
+          *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
     }
-    if (!mbar_wait_bounded(bar_s, phase)) {
-      *failed = 1;
-      set_error(a.err, KVQ_ERR_TIMEOUT);
-    }
+    wait(bar_s, phase);
     tmem_after();
-    // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1 ----
-    const int t = t0 + 32 * quad + lane;
-    const bool cached = t < len.n;
-    const int dj = t - len.n;  // drafted token
-    uint32_t xr[kHR];
-#pragma unroll
-    for (int i = 0; i < kHR; i += 8) tmem_ld8(t_lane + r0 + i, xr + i);
-    tmem_wait_ld();
+    // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1. x = s c is rounded before the
+    //      maximum is taken from it, so that the largest score's weight is exact however large it is ----
+    const int tt = 32 * quad + lane, t = t0 + tt;
     float x[kHR];
+    {
+      uint32_t xr[kHR];
+#pragma unroll
+      for (int i = 0; i < kHR; i += 8) tmem_ld8(t_lane + r0 + i, xr + i);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kHR; i += 4) {
+        const float4 c4 = *reinterpret_cast<const float4*>(rowc + r0 + i);
+        x[i] = __fmul_rn(__uint_as_float(xr[i]), c4.x);
+        x[i + 1] = __fmul_rn(__uint_as_float(xr[i + 1]), c4.y);
+        x[i + 2] = __fmul_rn(__uint_as_float(xr[i + 2]), c4.z);
+        x[i + 3] = __fmul_rn(__uint_as_float(xr[i + 3]), c4.w);
+      }
+    }
+    if (t0 + kTile > len.n) {  // drafted tokens in the tile, or none at all behind the last one
+      const int dj = t - len.n;
+      if (dj >= 0) {
+#pragma unroll
+        for (int i = 0; i < kHR; ++i)
+          if (dj >= len.nd || !((mask[r0 + i] >> dj) & 1ull)) x[i] = -INFINITY;
+      }
+    }
     bool over = false;
 #pragma unroll
-    for (int i = 0; i < kHR; ++i) {
-      const bool seen = cached || (dj < len.nd && ((mask[r0 + i] >> dj) & 1ull));
-      x[i] = seen ? __uint_as_float(xr[i]) * rowc[r0 + i] : -INFINITY;
-      over = over || (x[i] > rowm[r0 + i] + kSlack);
+    for (int i = 0; i < kHR; i += 4) {
+      const float4 t4 = *reinterpret_cast<const float4*>(rowt + r0 + i);
+      over = over || x[i] > t4.x || x[i + 1] > t4.y || x[i + 2] > t4.z || x[i + 3] > t4.w;
     }
     tmem_before();
-    if (__syncthreads_or(over)) {
+    const bool raise = __syncthreads_or(over);
+    if (tid == 0 && copy_next) copy_values(nb, nseg / n_rt, ntile * kTile);  // every thread has read this tile's
+    if (raise) {
       // ---- raise the running maxima of the rows with a score past them ----
 #pragma unroll
       for (int i = 0; i < kHR; ++i) {
@@ -378,11 +597,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       }
       __syncthreads();
       for (int r = tid; r < ROWS; r += kTreeThreads) {
-        const float mo = rowm[r];
         const float mt = fmaxf(fmaxf(red[r], red[ROWS + r]), fmaxf(red[2 * ROWS + r], red[3 * ROWS + r]));
-        const bool up = mt > mo + kSlack;
-        rowm[r] = up ? mt : mo;
-        rowf[r] = !up ? 1.f : (mo == -INFINITY) ? 0.f : exp2f(mo - mt);
+        const bool up = mt > rowt[r];
+        rowf[r] = up ? exp2_approx(rowm[r] - (mt - kRaise)) : 1.f;
+        if (up) {
+          rowm[r] = mt - kRaise;
+          rowt[r] = mt + kSlack;
+        }
       }
       __syncthreads();
 #pragma unroll
@@ -406,17 +627,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     for (int i = 0; i < kHR; i += 8) {  // P^T over the key tile, which the score product has read
       uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float pe[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const float xe = x[i + e + f];  // NaN stays NaN
-          pe[f] = (xe == -INFINITY) ? 0.f : exp2f(xe - rowm[r0 + i + e + f] + kRaise);
-          l[i + e + f] += pe[f];
-        }
-        o[e / 2] = pack_h2(pe[0], pe[1]);
+      for (int e = 0; e < 8; e += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(rowm + r0 + i + e);
+        const float p0e = exp2_approx(x[i + e] - m4.x), p1e = exp2_approx(x[i + e + 1] - m4.y);
+        const float p2e = exp2_approx(x[i + e + 2] - m4.z), p3e = exp2_approx(x[i + e + 3] - m4.w);
+        l[i + e] += p0e;
+        l[i + e + 1] += p1e;
+        l[i + e + 2] += p2e;
+        l[i + e + 3] += p3e;
+        o[e / 2] = pack_h2(p0e, p1e);
+        o[e / 2 + 1] = pack_h2(p2e, p3e);
       }
-      *reinterpret_cast<uint4*>(sm + L::kOffK + ((r0 + i) >> 3) * 2048 + (32 * quad + lane) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(sm + L::kOffK + ((r0 + i) >> 3) * 2048 + token_place(tt) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     fence_proxy_async_smem();
     tmem_before();
@@ -425,20 +647,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       tmem_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        umma_f16(tmem + ROWS, tree_desc(smem_u32(sm + L::kOffV) + k * 2 * kVOct, kVOct, kVRowGrp),
+        umma_f16(tmem + ROWS, tree_desc(smem_u32(sm + L::kOffV) + k * 256, 128, kVRowGrp),
                  tree_desc(smem_u32(sm + L::kOffK) + k * 256, 128, 2048), tree_idesc(ROWS, true), !first || k > 0);
       tree_commit(bar_o);
     }
-    if (!mbar_wait_bounded(bar_o, phase)) {
-      *failed = 1;
-      set_error(a.err, KVQ_ERR_TIMEOUT);
-    }
+    wait(bar_o, phase);
     tmem_after();
     phase ^= 1;
     first = false;
 
     // ---- the segment ends here (or the share does): hand its sums on ----
-    const bool last = tile + 1 == len.tiles;
     if (last || p + 1 == p1) {
       // l: over the tokens (lanes and quadrants)
 #pragma unroll
@@ -491,19 +709,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       __syncthreads();  // the row state is read before the next segment resets it
       first = true;
     }
-    if (__syncthreads_or(*failed)) break;
-    if (last) {
-      tile = 0;
-      if (++seg == seg_per_b) {
-        seg = 0;
-        if (p + 1 < p1) {
-          do len = tree_lens(a, ++b);
-          while (len.tiles == 0);  // a position is left, so such a request exists
-        }
-      }
-    } else {
-      ++tile;
-    }
+    b = nb;
+    seg = nseg;
+    tile = ntile;
+    len = nlen;
+  }
+  // a wait that ran out leaves the loop at the next barrier: let this block's copies land first
+  if (tid == 0 && *failed) {
+    mbar_wait_bounded(bar_k, landed & 1);
+    mbar_wait_bounded(bar_v, landed & 1);
   }
   tmem_before();
   __syncthreads();
@@ -547,7 +761,7 @@ __global__ void __launch_bounds__(kMergeThreads) kivi_tree_merge_kernel(const Ki
   auto slot = [&](int k) {  // a segment that began in an earlier block is in a block's first slot
     return a.part + ((size_t)k * 2 + (share_begin(P, k, G) > s0 ? 0 : 1)) * slot_floats<ROWS>();
   };
-  float M = -INFINITY;
+  float M = -FLT_MAX;
   for (int k = k0; k <= k1; ++k)
     if (share_begin(P, k, G) < share_begin(P, k + 1, G)) M = fmaxf(M, slot(k)[(size_t)ROWS * kD + r]);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -557,7 +771,7 @@ __global__ void __launch_bounds__(kMergeThreads) kivi_tree_merge_kernel(const Ki
     const float* s = slot(k);
     const float lk = s[(size_t)ROWS * kD + ROWS + r];
     if (lk == 0.f) continue;  // the row saw nothing there
-    const float w = (M == -INFINITY) ? 1.f : exp2f(s[(size_t)ROWS * kD + r] - M);
+    const float w = exp2f(s[(size_t)ROWS * kD + r] - M);
     const float4 v = *reinterpret_cast<const float4*>(s + (size_t)r * kD + 4 * lane);
     lt = fmaf(w, lk, lt);
     o.x = fmaf(w, v.x, o.x);
@@ -590,7 +804,7 @@ int tree_blocks() {
 
 template <int KB, int VB, int ROWS>
 cudaError_t launch_tree(const KiviTreeArgs& a, cudaStream_t st) {
-  using L = TreeLayout<ROWS>;
+  using L = TreeLayout<KB, VB, ROWS>;
   cudaError_t e = cudaFuncSetAttribute(kivi_tree_kernel<KB, VB, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   const int G = tree_blocks();
