@@ -549,26 +549,77 @@ __global__ void __launch_bounds__(128) kivi_append_kernel(const KiviAppendArgs a
 }
 
 // Commit: the accepted drafted tokens of every request, appended in the order of its path as
-// that many appends one after the other would. One 128-thread block per (request, KV head). A
-// path of m <= R tokens flushes the key residual at most once: the new keys first fill it to R
-// rows, those are quantized, and the rest start a fresh residual. The m values that leave the
-// window are older than the new ones (m <= R), so they are quantized first and the new rows then
-// take their places in the ring.
-// Bound: latency. The call is one launch whose blocks each run through loads, (a flush: 32 KB of
-// keys quantized by four warps) and stores that depend on one another.
+// that many appends one after the other would. One 256-thread block per (request, KV head). A
+// path of m <= R tokens flushes the key residual at most once: its R rows are the residual's
+// and the first new keys, which go straight into the quantizer; the rest start a fresh
+// residual. The values that leave the window are older than the new ones (m <= R), so they are
+// read and quantized before the new rows take their places in the ring.
+// Bound: latency. A block is a chain of loads (lengths and path, rows), quantization and stores;
+// a flush takes one warp for each 32-row group, its rows copied to shared memory all at once.
+constexpr int kCommitThreads = 128;
+constexpr int kCommitWarps = kCommitThreads / 32;
+
+// quant_key_tile with the tile's rows (lane l: channels 4l .. 4l + 3) in shared memory: few registers, so that many
+// blocks fit an SM
+template <int BITS>
+__device__ __forceinline__ void quant_key_shared(const uint16_t* tile, uint8_t* codes, uint16_t* scale, uint16_t* zero,
+                                                 int lane) {
+  constexpr int kRow = kD * BITS / 8;
+  const uint16_t* mine = tile + 4 * lane;
+  auto row = [&](int j) { return *reinterpret_cast<const uint2*>(mine + j * kD); };
+  const uint2 r0 = row(0);
+  __half2 mn0 = u2h2(r0.x), mn1 = u2h2(r0.y), mx0 = mn0, mx1 = mn1;
+#pragma unroll 8
+  for (int j = 1; j < kGroup; ++j) {
+    const uint2 r = row(j);
+    mn0 = __hmin2(mn0, u2h2(r.x));
+    mn1 = __hmin2(mn1, u2h2(r.y));
+    mx0 = __hmax2(mx0, u2h2(r.x));
+    mx1 = __hmax2(mx1, u2h2(r.y));
+  }
+  const float2 a0 = __half22float2(mn0), a1 = __half22float2(mn1), b0 = __half22float2(mx0), b1 = __half22float2(mx1);
+  const float mn[4] = {a0.x, a0.y, a1.x, a1.y}, mx[4] = {b0.x, b0.y, b1.x, b1.y};
+  GroupF f[4];
+  uint32_t sb[4], zb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const GroupQ g = group_params<BITS>(mn[i], mx[i]);
+    f[i] = group_fast(g, mn[i], mx[i]);
+    sb[i] = g.s_bits;
+    zb[i] = g.z_bits;
+  }
+  *reinterpret_cast<uint2*>(scale + 4 * lane) = make_uint2(sb[0] | (sb[1] << 16), sb[2] | (sb[3] << 16));
+  *reinterpret_cast<uint2*>(zero + 4 * lane) = make_uint2(zb[0] | (zb[1] << 16), zb[2] | (zb[3] << 16));
+  const Quad q = {make_float2(f[0].rs, f[1].rs), make_float2(f[2].rs, f[3].rs), make_float2(f[0].z, f[1].z),
+                  make_float2(f[2].z, f[3].z),   make_float2(f[0].th, f[1].th), make_float2(f[2].th, f[3].th)};
+#pragma unroll 4
+  for (int j = 0; j < kGroup; ++j) {
+    const uint2 r = row(j);
+    bool bad;
+    uint32_t c = row_codes_fast<BITS, true>(r, q, bad);
+    if (bad) c = row_codes_exact<BITS>(r, f);  // rare: a value near a rounding boundary
+    store_packed4<BITS>(codes + (size_t)j * kRow, lane, c);
+  }
+}
+
 template <int KB, int VB>
-__global__ void __launch_bounds__(128) kivi_commit_kernel(const KiviCommitArgs a) {
+__global__ void __launch_bounds__(kCommitThreads) kivi_commit_kernel(const KiviCommitArgs a) {
   constexpr int kKRow = kD * KB / 8, kVRow = kD * VB / 8;
+  __shared__ __align__(16) uint16_t tiles[kCommitWarps][kGroup * kD];  // of keys, one per warp
   const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n_warps = blockDim.x >> 5;
   const int R = a.residual, H = a.H;
+  const int* path = a.path + (size_t)b * a.N;
+  const int first_path = lane < a.N ? path[lane] : 0;  // issued with the lengths
   const int n = a.n_tok[b], nqk = a.n_quant_k[b], nqv = a.n_quant_v[b], m = a.n_accept[b];
   if (m == 0) return;  // every block of the request
   const bool valid = nqk >= 0 && nqk % kGroup == 0 && nqv >= 0 && nqv <= nqk && nqk <= n && n - nqk <= R &&
                      n - nqv <= R && nqk <= a.max_tokens;
-  const int* path = a.path + (size_t)b * a.N;
   bool known = m > 0 && m <= a.N;
-  for (int i = 0; known && i < m; ++i) known = path[i] >= 0 && path[i] < a.N;
+  if (known) {  // every warp looks at the whole path
+    bool bad = lane < m && (first_path < 0 || first_path >= a.N);
+    for (int i = lane + 32; i < m; i += 32) bad = bad || path[i] < 0 || path[i] >= a.N;
+    known = !__any_sync(0xFFFFFFFFu, bad);
+  }
   const int held = n - nqk;  // keys in the residual
   const bool flush = valid && known && m <= R && held + m > R;
   if (!valid || !known || m > R || (flush && nqk + R > a.max_tokens)) {
@@ -579,39 +630,51 @@ __global__ void __launch_bounds__(128) kivi_commit_kernel(const KiviCommitArgs a
   const size_t bh = (size_t)b * H + h;
   auto draft = [&](const uint16_t* x, int i) { return x + (((size_t)b * a.N + path[i]) * H + h) * kD; };
   auto copy_keys = [&](int i0, int i1, int row0) {  // accepted keys i0 .. i1 - 1 to residual rows row0 ..
-    for (int x = tid; x < (i1 - i0) * (kD / 8); x += blockDim.x) {
+    for (int x = tid; x < (i1 - i0) * (kD / 8); x += kCommitThreads) {
       const int i = x / (kD / 8), c8 = (x % (kD / 8)) * 8;
       *reinterpret_cast<uint4*>(a.k_resid + (bh * R + row0 + i) * kD + c8) =
           __ldg(reinterpret_cast<const uint4*>(draft(a.k_draft, i0 + i) + c8));
     }
   };
-  const int fill = flush ? R - held : m;  // keys that go behind the residual's
-  copy_keys(0, fill, held);
+  if (!flush) copy_keys(0, m, held);
   const int evict = max(0, n + m - R - nqv);
-  for (int i = warp; i < evict; i += n_warps) {
+  // evicted values from the last warp down, flushed groups from the first up
+  for (int i = kCommitWarps - 1 - warp; i < evict; i += kCommitWarps) {
     const int t = nqv + i;
     const uint2 raw = *reinterpret_cast<const uint2*>(a.v_resid + (bh * R + t % R) * kD + 4 * lane);
     const size_t tok = bh * a.max_tokens + t;
     quant_value_row<VB>(raw, a.v_codes + tok * kVRow, a.v_scale + tok * (kD / kGroup), a.v_zero + tok * (kD / kGroup),
                         lane);
   }
-  __syncthreads();  // the residual is full, the evicted values are read
-  for (int x = tid; x < m * (kD / 8); x += blockDim.x) {
+  if (flush) {
+    uint16_t* tile = tiles[warp];
+    for (int gi = warp; gi < R / kGroup; gi += kCommitWarps) {
+      __syncwarp();  // the tile before is used up
+#pragma unroll 4
+      for (int j = lane >> 4; j < kGroup; j += 2) {  // 16 lanes per row
+        const int row = gi * kGroup + j;
+        const uint16_t* src = row < held ? a.k_resid + (bh * R + row) * kD : draft(a.k_draft, row - held);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(tile + j * kD + 8 * (lane & 15))),
+                     "l"(src + 8 * (lane & 15))
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      const size_t sz = (bh * (a.max_tokens / kGroup) + nqk / kGroup + gi) * kD;
+      quant_key_shared<KB>(tile, a.k_codes + (bh * a.max_tokens + nqk + (size_t)gi * kGroup) * kKRow, a.k_scale + sz,
+                           a.k_zero + sz, lane);
+    }
+  }
+  __syncthreads();  // the evicted values and the flushed rows are read
+  for (int x = tid; x < m * (kD / 8); x += kCommitThreads) {
     const int i = x / (kD / 8), c8 = (x % (kD / 8)) * 8;
     *reinterpret_cast<uint4*>(a.v_resid + (bh * R + (n + i) % R) * kD + c8) =
         __ldg(reinterpret_cast<const uint4*>(draft(a.v_draft, i) + c8));
   }
-  if (flush) {
-    for (int gi = warp; gi < R / kGroup; gi += n_warps) {
-      const size_t sz = (bh * (a.max_tokens / kGroup) + nqk / kGroup + gi) * kD;
-      quant_key_group<KB, false>(a.k_resid + (bh * R + (size_t)gi * kGroup) * kD, kD,
-                                 a.k_codes + (bh * a.max_tokens + nqk + (size_t)gi * kGroup) * kKRow, a.k_scale + sz,
-                                 a.k_zero + sz, lane);
-    }
-    __syncthreads();  // the flushed rows are read
-    copy_keys(fill, m, 0);
+  if (flush) {  // the rows that filled the residual stay in it as appends leave them, the rest go to its start
+    copy_keys(0, R - held, held);
+    copy_keys(R - held, m, 0);  // below row `held`: m <= R
   }
-  __syncthreads();
   if (tid == 0 && atomicAdd(&a.sync[b], 1) == H - 1) {  // every block of the request has read the lengths
     a.n_tok[b] = n + m;
     if (flush) a.n_quant_k[b] = nqk + R;
@@ -1493,10 +1556,10 @@ cudaError_t launch_kivi_append(const KiviAppendArgs& a, cudaStream_t s) {
 cudaError_t launch_kivi_commit(const KiviCommitArgs& a, cudaStream_t s) {
   if (a.n_seq <= 0) return cudaSuccess;
   const dim3 grid(a.n_seq, a.H);
-  if (a.k_bits == 2 && a.v_bits == 2) kivi_commit_kernel<2, 2><<<grid, 128, 0, s>>>(a);
-  else if (a.k_bits == 2) kivi_commit_kernel<2, 4><<<grid, 128, 0, s>>>(a);
-  else if (a.v_bits == 2) kivi_commit_kernel<4, 2><<<grid, 128, 0, s>>>(a);
-  else kivi_commit_kernel<4, 4><<<grid, 128, 0, s>>>(a);
+  if (a.k_bits == 2 && a.v_bits == 2) kivi_commit_kernel<2, 2><<<grid, kCommitThreads, 0, s>>>(a);
+  else if (a.k_bits == 2) kivi_commit_kernel<2, 4><<<grid, kCommitThreads, 0, s>>>(a);
+  else if (a.v_bits == 2) kivi_commit_kernel<4, 2><<<grid, kCommitThreads, 0, s>>>(a);
+  else kivi_commit_kernel<4, 4><<<grid, kCommitThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

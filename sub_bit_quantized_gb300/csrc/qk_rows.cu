@@ -9,7 +9,7 @@
 // Bound: HBM (each row is read once and written once; about 6 operations a channel). Eight
 // lanes share a row, lane l holding channels 8l .. 8l+7 and their partners 64 + 8l .., so both
 // halves of every pair are in one lane, the loads and stores are 16 bytes and the mean takes
-// three shuffles; a warp works on four rows of one token at a time.
+// three shuffles; a warp works on four rows of one token at a time, several such quads in turn.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -73,90 +73,148 @@ __device__ __forceinline__ float sum8(unsigned mask, float x) {
   return x;
 }
 
+// eight consecutive channels as stored
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a) {
+struct Raw8 {
+  uint4 u[DT == KVQ_DT_FP32 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const void* base, int64_t elem) {
+  Raw8<DT> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + elem * (DT == KVQ_DT_FP32 ? 4 : 2));
+  r.u[0] = p[0];
+  if constexpr (DT == KVQ_DT_FP32) r.u[1] = p[1];
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == KVQ_DT_FP32) {
+      const uint4 u = r.u[i >> 1];
+      v[2 * i] = __uint_as_float((i & 1) ? u.z : u.x);
+      v[2 * i + 1] = __uint_as_float((i & 1) ? u.w : u.y);
+    } else {
+      const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+      const float2 f = (DT == KVQ_DT_BF16) ? bf2(w[i]) : hf2(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// A warp takes kPer row quads of one token (the first quads of the query, key and value rows, in that order, are
+// part 0), all their loads in flight before the first is used; the token's cos and sin serve them all.
+template <int DT, int kPer>
+__global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a, const unsigned parts) {
   const int lane = threadIdx.x & 31, l8 = lane & 7;
-  const int rows = a.q.heads + a.k.heads + a.v.heads, quads = (rows + 3) / 4;
-  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  if (unit >= (int64_t)a.B * a.N * quads) return;  // warp-uniform
-  const int64_t token = unit / quads;
-  const int b = (int)(token / a.N), j = (int)(token - (int64_t)b * a.N);
-  int h = (int)(unit - token * quads) * 4 + (lane >> 3);
+  const int rows = a.q.heads + a.k.heads + a.v.heads;
+  const unsigned unit = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const unsigned token = unit / parts, part = unit - token * parts;
+  if (token >= (unsigned)a.B * (unsigned)a.N) return;  // warp-uniform
+  const int b = (int)(token / (unsigned)a.N), j = (int)(token - (unsigned)b * (unsigned)a.N);
   const int pos = a.pos ? a.pos[token] : 0;
   if (pos < 0) return;  // padding: neither read nor written
   if (a.cos && pos >= a.max_ctx) {
     if (lane == 0) set_error(a.err, KVQ_ERR_CAPACITY);
     return;
   }
-  const bool there = h < rows;
-  const bool is_q = h < a.q.heads, is_v = h >= a.q.heads + a.k.heads;
-  if (!is_q) h -= a.q.heads;
-  if (is_v) h -= a.k.heads;
-  const QkRows& t = is_q ? a.q : is_v ? a.v : a.k;
-  const void* w = is_q ? a.wq : a.wk;
-  float lo[8] = {}, hi[8] = {};
-  if (there) {
+  Raw8<DT> rl[kPer], rh[kPer];
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    int h = ((int)part * kPer + p) * 4 + (lane >> 3);
+    if (h >= rows) {
+      rl[p] = rh[p] = {};
+      continue;
+    }
+    const QkRows& t = h < a.q.heads ? a.q : h < a.q.heads + a.k.heads ? a.k : a.v;
+    if (h >= a.q.heads) h -= h < a.q.heads + a.k.heads ? a.q.heads : a.q.heads + a.k.heads;
     const int64_t e = (int64_t)b * t.sb + (int64_t)j * t.st + (int64_t)h * t.sh + 8 * l8;
-    load8<DT>(t.in, e, lo);
-    load8<DT>(t.in, e + 64, hi);
+    rl[p] = load_raw8<DT>(t.in, e);
+    rh[p] = load_raw8<DT>(t.in, e + 64);
   }
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], ss));
-  ss = sum8(0xFFFFFFFFu, ss);
-  float r = rsqrtf(fmaf(ss, 1.f / kD, a.eps));
-  if (!is_v && !(ss < 1e37f)) {
-    // squares of large bf16 or fp32 values pass the fp32 range: the row times 2^-72 instead (eps is far
-    // below the mean's rounding). All eight lanes of a row come here, the warp's others may not.
-    constexpr float kDown = 2.117582368135750837e-22f;  // 2^-72
-    float s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] *= kDown;
-      hi[i] *= kDown;
-      s2 = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], s2));
-    }
-    r = rsqrtf(sum8(0xFFu << (lane & 24), s2) * (1.f / kD));
+  float c[8] = {}, s[8] = {};
+  if (a.cos) {
+    load8<KVQ_DT_FP32>(a.cos, (int64_t)pos * (kD / 2) + 8 * l8, c);
+    load8<KVQ_DT_FP32>(a.sin, (int64_t)pos * (kD / 2) + 8 * l8, s);
   }
-  if (!there) return;
-  if (!is_v) {
-    float wl[8], wh[8];
-    load8<DT>(w, 8 * l8, wl);
-    load8<DT>(w, 64 + 8 * l8, wh);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = lo[i] * r * wl[i];
-      hi[i] = hi[i] * r * wh[i];
-    }
-    if (a.cos) {
-      float c[8], s[8];
-      load8<KVQ_DT_FP32>(a.cos, (int64_t)pos * (kD / 2) + 8 * l8, c);
-      load8<KVQ_DT_FP32>(a.sin, (int64_t)pos * (kD / 2) + 8 * l8, s);
+  for (int p = 0; p < kPer; ++p) {
+    int h = ((int)part * kPer + p) * 4 + (lane >> 3);
+    const bool there = h < rows;
+    const bool is_q = h < a.q.heads, is_v = h >= a.q.heads + a.k.heads;
+    if (!is_q) h -= is_v ? a.q.heads + a.k.heads : a.q.heads;
+    const QkRows& t = is_q ? a.q : is_v ? a.v : a.k;
+    float lo[8], hi[8];
+    widen8<DT>(rl[p], lo);
+    widen8<DT>(rh[p], hi);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], ss));
+    ss = sum8(0xFFFFFFFFu, ss);
+    float r = rsqrtf(fmaf(ss, 1.f / kD, a.eps));
+    if (!is_v && !(ss < 1e37f)) {
+      // squares of large bf16 or fp32 values pass the fp32 range: the row times 2^-72 instead (eps is far
+      // below the mean's rounding). All eight lanes of a row come here, the warp's others may not.
+      constexpr float kDown = 2.117582368135750837e-22f;  // 2^-72
+      float s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float x = lo[i], y = hi[i];
-        lo[i] = x * c[i] - y * s[i];
-        hi[i] = y * c[i] + x * s[i];
+        lo[i] *= kDown;
+        hi[i] *= kDown;
+        s2 = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], s2));
+      }
+      r = rsqrtf(sum8(0xFFu << (lane & 24), s2) * (1.f / kD));
+    }
+    if (!there) continue;
+    if (!is_v) {
+      const void* w = is_q ? a.wq : a.wk;
+      float wl[8], wh[8];
+      load8<DT>(w, 8 * l8, wl);
+      load8<DT>(w, 64 + 8 * l8, wh);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo[i] = lo[i] * r * wl[i];
+        hi[i] = hi[i] * r * wh[i];
+      }
+      if (a.cos) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = lo[i], y = hi[i];
+          lo[i] = x * c[i] - y * s[i];
+          hi[i] = y * c[i] + x * s[i];
+        }
       }
     }
+    const int64_t o = (int64_t)b * t.ob + (int64_t)j * t.ot + (int64_t)h * t.oh + 8 * l8;
+    store8(t.out, o, t.out_dt, lo);
+    store8(t.out, o + 64, t.out_dt, hi);
   }
-  const int64_t o = (int64_t)b * t.ob + (int64_t)j * t.ot + (int64_t)h * t.oh + 8 * l8;
-  store8(t.out, o, t.out_dt, lo);
-  store8(t.out, o + 64, t.out_dt, hi);
+}
+
+template <int DT, int kPer>
+cudaError_t launch_rows(const QkRowsArgs& a, int quads, cudaStream_t s) {
+  const unsigned parts = (unsigned)((quads + kPer - 1) / kPer);
+  const int64_t units = (int64_t)a.B * a.N * parts;
+  // below 2^31 (checked by the host)
+  qk_rows_kernel<DT, kPer><<<(unsigned)((units + kRowThreads / 32 - 1) / (kRowThreads / 32)), kRowThreads, 0, s>>>(a, parts);
+  return cudaGetLastError();
+}
+template <int DT>
+cudaError_t launch_rows_of(const QkRowsArgs& a, cudaStream_t s) {
+  const int quads = (a.q.heads + a.k.heads + a.v.heads + 3) / 4;
+  // two quads a warp once that still leaves every SM two rounds of warps, so that few tokens use every SM
+  if ((int64_t)a.B * a.N * quads >= 2 * 2 * 64 * 152) return launch_rows<DT, 2>(a, quads, s);
+  return launch_rows<DT, 1>(a, quads, s);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_rows(const QkRowsArgs& a, int in_dt, cudaStream_t s) {
-  const int rows = a.q.heads + a.k.heads + a.v.heads;
-  const int64_t units = (int64_t)a.B * a.N * ((rows + 3) / 4);
-  const int64_t blocks = (units + kRowThreads / 32 - 1) / (kRowThreads / 32);
-  if (blocks == 0) return cudaSuccess;
-  const unsigned g = (unsigned)blocks;  // below 2^31 (checked by the host)
-  if (in_dt == KVQ_DT_FP32) qk_rows_kernel<KVQ_DT_FP32><<<g, kRowThreads, 0, s>>>(a);
-  else if (in_dt == KVQ_DT_FP16) qk_rows_kernel<KVQ_DT_FP16><<<g, kRowThreads, 0, s>>>(a);
-  else qk_rows_kernel<KVQ_DT_BF16><<<g, kRowThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if ((int64_t)a.B * a.N == 0) return cudaSuccess;
+  if (in_dt == KVQ_DT_FP32) return launch_rows_of<KVQ_DT_FP32>(a, s);
+  if (in_dt == KVQ_DT_FP16) return launch_rows_of<KVQ_DT_FP16>(a, s);
+  return launch_rows_of<KVQ_DT_BF16>(a, s);
 }
 
 }  // namespace kvq

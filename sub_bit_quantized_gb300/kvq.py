@@ -193,12 +193,12 @@ class _Call:
 
     def __init__(self, name: str, stream, device, keep):
         self._name, self._f = name, getattr(lib(), name)
-        self._stream, self._device, self._keep = stream, device, keep
+        self._stream = None if stream is None else _stream(stream)
+        self._device, self._keep = device.index, (stream, keep)
 
     def __call__(self):
         s = self._stream
-        s = torch.cuda.current_stream(self._device).cuda_stream if s is None else _stream(s)
-        st = self._f(*self._args, s)
+        st = self._f(*self._args, torch._C._cuda_getCurrentRawStream(self._device) if s is None else s)
         if st != KVQ_OK:
             _check(st, self._name)
 
