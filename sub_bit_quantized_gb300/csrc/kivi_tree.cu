@@ -6,13 +6,20 @@
 //   o_i = sum_t p_it v_t / sum_t p_it,  p_it = exp(q_i k_t / sqrt(D) - m_i).
 // The rows of a KV head are the N drafted tokens times its n_q_heads / n_heads query heads.
 //
-// Tokens (cached, then drafted) form tiles of 128. For a tile and up to kRows query rows:
-//   S^T [128 tokens x rows] = K [128 x 128] . q^T      tcgen05, K dequantized to fp16
-//   P^T = exp2(S^T c - m)                               a thread owns a token and half the rows
-//   O^T [128 channels x rows] += V^T [128 x 128] . P^T  tcgen05, V dequantized to fp16
-// so the 128 lanes of every product are full however few rows there are, and no shuffle is
-// needed inside the tile: the running maximum m of a row moves only when a score passes it by
-// 2^kSlack (a block-wide vote), the sums l stay per thread until the segment ends.
+// Tokens (cached, then drafted) form tiles of 128, and a persistent grid takes equal contiguous
+// shares of all tiles (segment by segment, a segment being a request, KV head and row tile).
+// Keys and values are dequantized to fp16 operands, one rounding each; the sums, the running
+// maxima and the normalisers are fp32. The running maximum of a row moves only when a score
+// passes it by 2^kSlack. Segments that blocks share leave partial softmaxes in the workspace,
+// which a second small kernel joins in block order.
+//
+// Two kernels by the number of rows R of a KV head (tree_rows):
+//  * R <= 32: warp-wide products. A warp takes a 32-token key group, unpacks the codes straight
+//    into the B fragments of m16n8k16 products and keeps scores and sums in registers; nothing
+//    goes through shared memory but the stored tile, and warps meet only at the segment's end.
+//  * more rows: tcgen05 on tiles of 64 rows. S^T [128 tokens x rows] = K . q^T and
+//    O^T [128 channels x rows] += V^T . P^T keep all 128 lanes of every product busy; the unpacked
+//    operands go through shared memory once for 64 rows.
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -24,13 +31,775 @@
 namespace kvq {
 namespace {
 
-constexpr int kTreeThreads = 256;
-constexpr int kTreeWarps = kTreeThreads / 32;
-constexpr int kTile = 128;    // tokens per tile (MMA M of the scores, K of the value product)
+constexpr int kTile = 128;    // tokens per tile
 constexpr int kGroupT = 32;   // tokens per key group, channels per value group
 constexpr float kSlack = 7.f;   // log2 by which a score may pass its row's running maximum
 constexpr float kRaise = 8.f;   // weights are exp2(x - m + kRaise) <= 2^15, held as fp16: one below 2^-32 of the
                                 // maximum's is lost instead of one below 2^-24
+
+// A tile as it is stored: key codes, scales and zeros [4 groups][128], value codes, scales and zeros [128][4]
+template <int KB, int VB>
+struct StageLayout {
+  static constexpr int kKRow = kD * KB / 8, kVRow = kD * VB / 8;   // code bytes per token
+  static constexpr int kKs = kTile * kKRow, kKz = kKs + (kTile / kGroupT) * kD * 2;
+  static constexpr int kVc = kKz + (kTile / kGroupT) * kD * 2;
+  static constexpr int kVs = kVc + kTile * kVRow, kVz = kVs + kTile * (kD / kGroupT) * 2;
+  static constexpr int kBytes = kVz + kTile * (kD / kGroupT) * 2;
+};
+
+__device__ __forceinline__ float th2f(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The work of a call, the same for every block: segment (b, h, row tile) has T_b tiles (its cached
+// and drafted tokens), all segments in the order b, h, row tile form one list of P tile positions,
+// and block k of G takes positions [k P / G, (k + 1) P / G).
+struct TreeLens {
+  int nqk, nqv, n, nd;  // quantized keys, quantized values, cached tokens, drafted tokens
+  int tiles;
+};
+__device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
+  TreeLens L;
+  L.nqk = min(max(a.n_quant_k[b], 0), a.max_tokens) / kGroupT * kGroupT;
+  L.nqv = (a.residual > 0) ? min(max(a.n_quant_v[b], 0), L.nqk) : L.nqk;
+  L.n = L.nqk + max(0, min(a.n_tok[b] - L.nqk, a.residual));
+  L.nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
+  L.tiles = L.nd > 0 ? (L.n + L.nd + kTile - 1) / kTile : 0;
+  return L;
+}
+__device__ __forceinline__ int share_begin(int P, int k, int G) { return (int)((long long)P * k / G); }
+
+// A role's place in the block's share
+struct Walk {
+  int b, seg, tile;  // seg = h * row tiles + row tile
+  TreeLens len;
+  __device__ __forceinline__ bool last() const { return tile + 1 == len.tiles; }
+  // to the next position; `more`: there is one in the share
+  __device__ __forceinline__ void next(const KiviTreeArgs& a, int seg_per_b, bool more) {
+    if (++tile < len.tiles || !more) return;
+    tile = 0;
+    if (++seg < seg_per_b) return;
+    seg = 0;
+    do len = tree_lens(a, ++b);
+    while (len.tiles == 0);  // a position is left, so such a request exists
+  }
+};
+
+// partial softmax of a segment: rows of o[128], then m, l per row
+template <int ROWS>
+__host__ __device__ constexpr size_t slot_floats() { return (size_t)ROWS * (kD + 2); }
+// What block k did with the segments it shares, for the merge. first: 0 its first segment begins there, 1 it goes
+// on past the block, 2 it ends there, 3 the block had no work. open: the segment that begins in the block and goes
+// on (b * segments per request + seg), or -1; nd: that request's drafted tokens.
+struct TreeShared {
+  int first, open, nd, pad;
+};
+
+// The place in all positions where the block's share begins; scan: one int per thread, shared memory (two barriers).
+// Returns the share's [p0, p1).
+__device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b, int* scan, Walk& w) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int chunk = (a.B + threads - 1) / threads, chunks = (a.B + chunk - 1) / chunk;  // threads with requests
+  int mine = 0;
+  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += tree_lens(a, b).tiles;
+  scan[tid] = mine;
+  __syncthreads();
+  int P = 0, before = 0;
+  for (int i = 0; i < chunks; ++i) P += scan[i];
+  P *= seg_per_b;
+  const int p0 = share_begin(P, blockIdx.x, gridDim.x), p1 = share_begin(P, blockIdx.x + 1, gridDim.x);
+  w.b = w.seg = w.tile = 0;
+  if (p0 < p1) {
+    int c0 = 0;
+    while (p0 >= (before + scan[c0]) * seg_per_b) before += scan[c0++];  // ends: p0 < P
+    w.b = c0 * chunk;
+    w.len = tree_lens(a, w.b);
+    while (p0 >= (before + w.len.tiles) * seg_per_b) {  // ends inside chunk c0
+      before += w.len.tiles;
+      w.len = tree_lens(a, ++w.b);
+    }
+    const int off = p0 - before * seg_per_b;
+    w.seg = off / w.len.tiles;
+    w.tile = off - w.seg * w.len.tiles;
+  }
+  __syncthreads();  // scan is read
+  return make_int2(p0, p1);
+}
+
+// channels 8c .. 8c+7 of a token behind the quantized ones: residual, drafted, or nothing (zero)
+__device__ __forceinline__ uint4 fp16_key8(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int c) {
+  const uint16_t* p = nullptr;
+  if (t < L.n) p = a.k_resid + (((size_t)b * a.H + h) * a.residual + (t - L.nqk)) * kD;
+  else if (t < L.n + L.nd) p = a.k_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
+  return p ? __ldg(reinterpret_cast<const uint4*>(p + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ uint4 fp16_value8(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int c) {
+  const uint16_t* p = nullptr;
+  if (t < L.n) p = a.v_resid + (((size_t)b * a.H + h) * a.residual + t % a.residual) * kD;
+  else if (t < L.n + L.nd) p = a.v_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
+  return p ? __ldg(reinterpret_cast<const uint4*>(p + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+}
+// true where a half of w is infinite or NaN; those become 0
+__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
+  bool any = false;
+  if ((w & 0x7C00u) == 0x7C00u) { w &= 0xFFFF0000u; any = true; }
+  if ((w & 0x7C000000u) == 0x7C000000u) { w &= 0xFFFFu; any = true; }
+  return any;
+}
+
+// Channel order of the staged keys and queries. The contraction runs over all 128 channels, so any order serves
+// that both share; this one is the order in which a code word's halves unpack: pairs (c, c + 8) of 16 channels
+// (2 bits), (c, c + 4) of 8 (4 bits). lo, hi: channels 16 w .. + 7, 16 w + 8 .. + 15, natural order; out: the two
+// 16-byte chunks of the block.
+template <int KB>
+__device__ __forceinline__ void pair_order(const uint4 lo, const uint4 hi, uint4& out0, uint4& out1) {
+  if constexpr (KB == 2) {
+    out0 = make_uint4(__byte_perm(lo.x, hi.x, 0x5410), __byte_perm(lo.x, hi.x, 0x7632), __byte_perm(lo.y, hi.y, 0x5410),
+                      __byte_perm(lo.y, hi.y, 0x7632));
+    out1 = make_uint4(__byte_perm(lo.z, hi.z, 0x5410), __byte_perm(lo.z, hi.z, 0x7632), __byte_perm(lo.w, hi.w, 0x5410),
+                      __byte_perm(lo.w, hi.w, 0x7632));
+  } else {
+    out0 = make_uint4(__byte_perm(lo.x, lo.z, 0x5410), __byte_perm(lo.x, lo.z, 0x7632), __byte_perm(lo.y, lo.w, 0x5410),
+                      __byte_perm(lo.y, lo.w, 0x7632));
+    out1 = make_uint4(__byte_perm(hi.x, hi.z, 0x5410), __byte_perm(hi.x, hi.z, 0x7632), __byte_perm(hi.y, hi.w, 0x5410),
+                      __byte_perm(hi.y, hi.w, 0x7632));
+  }
+}
+// Token order of the staged values and weights: in odd octets neighbours change places, so that the two octets a
+// warp reads at a time come from different banks.
+__device__ __forceinline__ int token_place(int t) { return t ^ ((t >> 3) & 1); }
+
+__device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t as_u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+// Code j of both halves of w as fp16 (exact): masked in place under the exponent of 2^10, where it stands for
+// 1024 + c 2^(b j), and scaled back by one FMA. Codes above the ten mantissa bits come from w shifted right.
+template <int BITS>
+__device__ __forceinline__ __half2 code_h2(uint32_t w, int j) {
+  constexpr int kIn = (BITS == 2) ? 5 : 2;  // codes that fit in place
+  const int jj = j < kIn ? j : j - kIn;
+  const uint32_t m = ((j < kIn ? w : w >> (BITS * kIn)) & ((((1u << BITS) - 1u) << (BITS * jj)) * 0x10001u)) | 0x64006400u;
+  const float p = 1.f / (float)(1 << (BITS * jj));
+  return __hfma2(as_h2(m), __float2half2_rn(p), __float2half2_rn(-1024.f * p));
+}
+// s c - s z, one rounding of s z and one of the result
+__device__ __forceinline__ uint32_t dequant_h2(__half2 c, __half2 s, __half2 nsz) { return as_u(__hfma2(c, s, nsz)); }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The stored part of a tile into a stage: its quantized keys on kfull, its quantized values on vfull (one thread).
+// With nothing to copy the barrier completes at once.
+template <int KB, int VB>
+__device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
+                                          unsigned char* stage, uint64_t* full) {
+  using S = StageLayout<KB, VB>;
+  const int nk = min(kTile, len.nqk - t0);
+  if (nk <= 0) {
+    mbar_arrive(full);
+    return;
+  }
+  const size_t g = (bh * (a.max_tokens / kGroupT) + t0 / kGroupT) * kD;
+  const uint32_t gb = nk / kGroupT * kD * 2;
+  mbar_arrive_expect_tx(full, nk * S::kKRow + 2 * gb);
+  bulk_g2s(stage, a.k_codes + (bh * a.max_tokens + t0) * S::kKRow, nk * S::kKRow, full);
+  bulk_g2s(stage + S::kKs, a.k_scale + g, gb, full);
+  bulk_g2s(stage + S::kKz, a.k_zero + g, gb, full);
+}
+template <int KB, int VB>
+__device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
+                                            unsigned char* stage, uint64_t* full) {
+  using S = StageLayout<KB, VB>;
+  const int nv = (min(kTile, len.nqv - t0) + 1) & ~1;  // whole 16-byte pieces
+  if (nv <= 0) {
+    mbar_arrive(full);
+    return;
+  }
+  const size_t tok = bh * a.max_tokens + t0;
+  mbar_arrive_expect_tx(full, nv * (S::kVRow + 16));
+  bulk_g2s(stage + S::kVc, a.v_codes + tok * S::kVRow, nv * S::kVRow, full);
+  bulk_g2s(stage + S::kVs, a.v_scale + tok * (kD / kGroupT), nv * 8, full);
+  bulk_g2s(stage + S::kVz, a.v_zero + tok * (kD / kGroupT), nv * 8, full);
+}
+
+// A query row as fp16 times a power of two that puts its largest magnitude in [2^14, 2^15): eight lanes, 16 channels
+// each (w: bf16 pairs; o: fp16 pairs). Returns what a score has to be multiplied with (scale: log2 units).
+__device__ __forceinline__ float query_fp16(const uint32_t (&w)[8], uint32_t (&o)[8], float scale) {
+  float mx = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+  const int ex = (int)(__float_as_uint(mx) >> 23);  // biased exponent; 0: zero or subnormal, 255: not finite
+  // times 2^(14 - (ex - 127)) in two factors, since the power may pass the fp32 range
+  const int sh = (ex == 0 || ex == 255) ? 0 : 141 - ex;
+  const float f1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = pack_h2(bf16_lo(w[e]) * f1 * f2, bf16_hi(w[e]) * f1 * f2);
+  return scale / f1 / f2;
+}
+// 16 channels 16c .. of query row `row` of (b, KV head h), zero for padding
+__device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int row, int c,
+                                           uint32_t (&w)[8]) {
+  const int rep = a.Hq / a.H, di = row / rep;
+  const bool real = row < a.N * rep && di < len.nd;
+  uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (real) {
+    const uint4* src = reinterpret_cast<const uint4*>(
+        a.q + (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 16 * c);
+    u[0] = __ldg(src);
+    u[1] = __ldg(src + 1);
+  }
+  w[0] = u[0].x; w[1] = u[0].y; w[2] = u[0].z; w[3] = u[0].w;
+  w[4] = u[1].x; w[5] = u[1].y; w[6] = u[1].z; w[7] = u[1].w;
+  return real;
+}
+
+// eight codes of a word as fp16 values s (c - z), natural order
+template <int BITS>
+__device__ __forceinline__ uint4 scalar_dequant8(uint32_t w, float s, float z) {
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    o[e] = pack_h2(s * ((float)((w >> (BITS * 2 * e)) & ((1 << BITS) - 1)) - z),
+                   s * ((float)((w >> (BITS * (2 * e + 1))) & ((1 << BITS) - 1)) - z));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ======================================================================================
+// Up to 32 rows: warp-wide products
+// ======================================================================================
+//
+// Fragment orders. The contraction over channels and the one over tokens may run in any order that both operands
+// share, and output columns may be any channels; they are chosen so that a code word's halves are a fragment's
+// register without moving single codes.
+//  * Scores: lane (n = lane / 4, q = lane % 4) holds token column n and channels 32 q .. + 31, i.e. its own code
+//    words; k-step kk takes two channel pairs of them ((c, c + 8) at 2 bits, (c, c + 4) at 4 bits).
+//  * Columns n of score tile i are tokens 8 i + (n ^ (n >> 2 & 1)): the four tokens a lane quartet reads for the
+//    value product then lie in different banks.
+//  * Values: lane column n holds channels 16 n .. + 15, its own code word(s); column tile t takes channel 16 n + t,
+//    so a lane ends with 32 consecutive channels of its rows.
+// Bound: instruction issue. A group of 32 tokens costs a warp about 300 instructions for the keys (3 per code pair),
+// 90 for the softmax of 16 rows and 280 for the values.
+constexpr int kMmaThreads = 128;
+constexpr int kMmaWarps = kMmaThreads / 32;
+
+template <int KB, int VB, int MT>  // MT: row tiles of 16
+struct MmaLayout {
+  using S = StageLayout<KB, VB>;
+  static constexpr int kStages = (KB + VB == 4) ? 3 : 2;
+  static constexpr int kOffQ = kStages * S::kBytes;                 // uint4 [8 k-steps][MT][32 lanes]: A fragments
+  static constexpr int kOffO = kOffQ + 8 * MT * 32 * 16;            // float [2][MT 16][128]: sums on their way to a warp
+  static constexpr int kOffMl = kOffO + 2 * MT * 16 * kD * 4;       // float [4 warps][MT 16][2]: m, l
+  static constexpr int kOffMask = kOffMl + kMmaWarps * MT * 16 * 8; // uint64 [MT 16]
+  static constexpr int kOffC = kOffMask + MT * 16 * 8;              // float [MT 16]: log2 units per score unit
+  static constexpr int kOffBar = kOffC + MT * 16 * 4;               // mbarriers, flags
+  static constexpr int kSmem = kOffBar + 128;
+  static constexpr int kBlocks = (MT == 1) ? 3 : 2;                 // per SM
+  static_assert(kSmem <= 232448 / kBlocks - 1024, "blocks per SM");
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+template <int KB, int VB, int MT>
+__global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
+    kivi_tree_mma_kernel(const KiviTreeArgs a, const float scale_log2) {
+  using L = MmaLayout<KB, VB, MT>;
+  using S = StageLayout<KB, VB>;
+  constexpr int kRows = 16 * MT, kSt = L::kStages;
+  extern __shared__ __align__(128) unsigned char sm[];
+  uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ);
+  float* osum = reinterpret_cast<float*>(sm + L::kOffO);
+  float2* ml = reinterpret_cast<float2*>(sm + L::kOffMl);
+  uint64_t* mask = reinterpret_cast<uint64_t*>(sm + L::kOffMask);
+  float* rowc = reinterpret_cast<float*>(sm + L::kOffC);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [kSt] the stage's copies landed
+  uint64_t* empty = full + 4;                                      // [kSt] four warps are done with it
+  volatile int* failed = reinterpret_cast<volatile int*>(full + 8);
+  int* nonfinite = reinterpret_cast<int*>(full + 8) + 1;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = lane & 3, n8 = lane >> 2;
+  const int rep = a.Hq / a.H, rows_all = a.N * rep, seg_per_b = a.H;  // one row tile
+  TreeShared* shared = reinterpret_cast<TreeShared*>(a.part);
+  float* slots = reinterpret_cast<float*>(shared + gridDim.x);
+
+  Walk w;
+  const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), w);
+  const int n = share.y - share.x;
+  TreeShared sh = {n > 0 ? 0 : 3, -1, 0, 0};
+  if (n == 0) {
+    if (tid == 0) shared[blockIdx.x] = sh;
+    return;
+  }
+  Walk ahead = w;      // thread 0: the next tile to copy
+  int copied = 0;      // tiles whose copies were issued
+  auto produce = [&]() {
+    unsigned char* stage = sm + (copied % kSt) * S::kBytes;
+    const size_t bh = (size_t)ahead.b * a.H + ahead.seg;
+    uint64_t* f = &full[copied % kSt];  // two arrivals: keys, values
+    fence_proxy_async_smem();
+    copy_keys<KB, VB>(a, ahead.len, bh, ahead.tile * kTile, stage, f);
+    copy_values<KB, VB>(a, ahead.len, bh, ahead.tile * kTile, stage, f);
+    ++copied;
+    ahead.next(a, seg_per_b, copied < n);
+  };
+  // A wait that runs out is recorded; later waits return at once, so the block runs through and leaves.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (*failed) return;
+    if (!mbar_wait_bounded(bar, parity)) {
+      *failed = 1;
+      set_error(a.err, KVQ_ERR_TIMEOUT);
+    }
+  };
+  if (tid == 0) {
+    for (int i = 0; i < kSt; ++i) {
+      mbar_init(&full[i], 2);
+      mbar_init(&empty[i], kMmaWarps);
+    }
+    *failed = 0;
+    *nonfinite = 0;
+    fence_mbar_init();
+    for (int i = 0; i < min(kSt, n); ++i) produce();
+  }
+
+  int i = 0;  // tiles done
+  while (i < n) {
+    // ================= one segment's part: its queries =================
+    const int h = w.seg;
+#pragma unroll 1
+    for (int x = tid; x < kRows * 8; x += kMmaThreads) {  // 8 lanes per row, 16 channels each
+      const int r = x >> 3, c = x & 7;
+      uint32_t u[8], o[8];
+      const bool real = load_query(a, w.len, w.b, h, r, c, u);
+      const float back = query_fp16(u, o, scale_log2);
+      uint4 x0, x1;
+      pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
+      const uint32_t pr[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};  // pairs in fragment order
+      // lane (row % 8, c / 2), k-steps 4 (c % 2) .. + 3, registers (row >= 8) and 2 + (row >= 8)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int kk = 4 * (c & 1) + (e >> 1);
+        reinterpret_cast<uint32_t*>(qf + (kk * MT + (r >> 4)) * 32 + (r & 7) * 4 + (c >> 1))[((r >> 3) & 1) + 2 * (e & 1)] = pr[e];
+      }
+      if (c == 0) {
+        rowc[r] = back;
+        mask[r] = real ? a.mask[(size_t)w.b * a.N + r / rep] : 0ull;
+      }
+    }
+    __syncthreads();  // queries staged (and, the first time, the barriers)
+    float m[MT][2], top[MT][2], l[MT][2], cs[MT][2];  // of rows 16 mt + n8, + 8: maximum - kRaise, + kSlack, sum, scale
+    float o[MT][16][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[mt][e] = top[mt][e] = -FLT_MAX;
+        l[mt][e] = 0.f;
+        cs[mt][e] = rowc[16 * mt + n8 + 8 * e];
+      }
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.f;
+    }
+    const int i_first = i, tile_first = w.tile;
+    const int i_end = min(n, i + w.len.tiles - w.tile);
+    for (; i < i_end; ++i) {
+      const int st = i % kSt;
+      const unsigned char* stage = sm + st * S::kBytes;
+      const int tw = (tile_first + i - i_first) * kTile + 32 * warp;  // the warp's first token
+      wait(&full[st], (i / kSt) & 1);
+      if (tw < w.len.n + w.len.nd) {
+        // ---- scores: 4 tiles of 8 tokens ----
+        float s[MT][4][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][t][e] = 0.f;
+        const int tcol = n8 ^ ((n8 >> 2) & 1);  // the lane's token of each score tile
+        if (tw < w.len.nqk) {
+          uint32_t u[4][KB];  // code words of the lane's 32 channels, four tokens
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const unsigned char* p = stage + (32 * warp + 8 * t + tcol) * S::kKRow + q4 * (4 * KB);
+            if constexpr (KB == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(p);
+              u[t][0] = v.x;
+              u[t][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4*>(p);
+              u[t][0] = v.x;
+              u[t][1] = v.y;
+              u[t][2] = v.z;
+              u[t][3] = v.w;
+            }
+          }
+#pragma unroll
+          for (int hw = 0; hw < 2; ++hw) {  // 16 channels, 4 k-steps
+            uint32_t sc[8], nz[8];
+            {
+              const uint4* sp = reinterpret_cast<const uint4*>(stage + S::kKs + (warp * kD + 32 * q4 + 16 * hw) * 2);
+              const uint4* zp = reinterpret_cast<const uint4*>(stage + S::kKz + (warp * kD + 32 * q4 + 16 * hw) * 2);
+              uint4 s0, s1, z0, z1;
+              pair_order<KB>(sp[0], sp[1], s0, s1);
+              pair_order<KB>(zp[0], zp[1], z0, z1);
+              const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+              const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                sc[j] = sw[j];
+                nz[j] = as_u(__hmul2(__hneg2(as_h2(sw[j])), as_h2(zw[j])));
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 af[MT];
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) af[mt] = qf[((4 * hw + k) * MT + mt) * 32 + lane];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                // pairs 2 k, 2 k + 1 of the 16 channels
+                const uint32_t cw = (KB == 2) ? u[t][hw] : u[t][2 * hw + (k >> 1)];
+                const int j = (KB == 2) ? 2 * k : 2 * (k & 1);
+                const uint32_t b0 = dequant_h2(code_h2<KB>(cw, j), as_h2(sc[2 * k]), as_h2(nz[2 * k]));
+                const uint32_t b1 = dequant_h2(code_h2<KB>(cw, j + 1), as_h2(sc[2 * k + 1]), as_h2(nz[2 * k + 1]));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma_f16(s[mt][t], af[mt], b0, b1);
+              }
+            }
+          }
+        } else {  // fp16 rows: residual, drafted, or none
+#pragma unroll 1
+          for (int hw = 0; hw < 2; ++hw) {
+            uint4 x[4][2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                x[t][e] = fp16_key8(a, w.len, w.b, h, tw + 8 * t + tcol, 4 * q4 + 2 * hw + e);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              uint4 x0, x1;
+              pair_order<KB>(x[t][0], x[t][1], x0, x1);
+              const uint32_t pr[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  mma_f16(s[mt][t], qf[((4 * hw + k) * MT + mt) * 32 + lane], pr[2 * k], pr[2 * k + 1]);
+            }
+          }
+        }
+        // ---- softmax. x = s c is rounded before the maximum is taken from it, so that the largest score's
+        //      weight is exact however large it is. Element e of tile t: row + 8 (e / 2), column 2 q4 + e % 2 ----
+        const bool plain = tw + 32 <= w.len.n;
+        bool over = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x = __fmul_rn(s[mt][t][e], cs[mt][e >> 1]);
+              if (!plain) {
+                const int col = 2 * q4 + (e & 1), dj = tw + 8 * t + (col ^ ((col >> 2) & 1)) - w.len.n;
+                if (dj >= 0 && (dj >= w.len.nd || !((mask[16 * mt + n8 + 8 * (e >> 1)] >> dj) & 1ull))) x = -INFINITY;
+              }
+              s[mt][t][e] = x;
+              over = over || x > top[mt][e >> 1];
+            }
+        if (__any_sync(0xFFFFFFFFu, over)) {
+          // raise the maxima of the rows with a score past them
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int t = 0; t < 4; ++t) mx = fmaxf(mx, fmaxf(s[mt][t][2 * e], s[mt][t][2 * e + 1]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+              if (mx > top[mt][e]) {
+                const float f = exp2_approx(m[mt][e] - (mx - kRaise));
+                m[mt][e] = mx - kRaise;
+                top[mt][e] = mx + kSlack;
+                l[mt][e] *= f;
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                  o[mt][t][2 * e] *= f;
+                  o[mt][t][2 * e + 1] *= f;
+                }
+              }
+            }
+        }
+        uint4 pf[MT][2];  // weights: A fragments of the two 16-token steps
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t pr[4][2];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float p0 = exp2_approx(s[mt][t][2 * e] - m[mt][e]), p1 = exp2_approx(s[mt][t][2 * e + 1] - m[mt][e]);
+              l[mt][e] += p0 + p1;
+              pr[t][e] = pack_h2(p0, p1);
+            }
+          pf[mt][0] = make_uint4(pr[0][0], pr[0][1], pr[1][0], pr[1][1]);
+          pf[mt][1] = make_uint4(pr[2][0], pr[2][1], pr[3][0], pr[3][1]);
+        }
+        // ---- values: step k takes token columns 2 q4, 2 q4 + 1 of score tiles 2 k, 2 k + 1 ----
+        const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);
+        if (tw + 32 <= w.len.nqv) {
+          const uint16_t* sp = reinterpret_cast<const uint16_t*>(stage + S::kVs) + 32 * warp * 4 + (n8 >> 1);
+          const uint16_t* zp = reinterpret_cast<const uint16_t*>(stage + S::kVz) + 32 * warp * 4 + (n8 >> 1);
+          const unsigned char* cw = stage + S::kVc + 32 * warp * S::kVRow + n8 * (2 * VB);
+          uint32_t sv[4], nz[4];
+          uint32_t wa[4][VB / 2], wb[4][VB / 2];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int ta = 8 * t + ca, tb = 8 * t + cb;
+            if constexpr (VB == 2) {
+              wa[t][0] = *reinterpret_cast<const uint32_t*>(cw + ta * S::kVRow);
+              wb[t][0] = *reinterpret_cast<const uint32_t*>(cw + tb * S::kVRow);
+            } else {
+              const uint2 va = *reinterpret_cast<const uint2*>(cw + ta * S::kVRow), vb = *reinterpret_cast<const uint2*>(cw + tb * S::kVRow);
+              wa[t][0] = va.x;
+              wa[t][1] = va.y;
+              wb[t][0] = vb.x;
+              wb[t][1] = vb.y;
+            }
+            sv[t] = sp[ta * 4] | ((uint32_t)sp[tb * 4] << 16);
+            nz[t] = as_u(__hmul2(__hneg2(as_h2(sv[t])), as_h2(zp[ta * 4] | ((uint32_t)zp[tb * 4] << 16))));
+          }
+          constexpr int kCodes = 16 / VB;  // channels of a half word
+#pragma unroll
+          for (int hw = 0; hw < VB; ++hw) {  // half words of the lane's 16 channels
+            uint32_t x[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) x[t] = __byte_perm(wa[t][hw >> 1], wb[t][hw >> 1], (hw & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int c = 0; c < kCodes; ++c)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t b0 = dequant_h2(code_h2<VB>(x[2 * k], c), as_h2(sv[2 * k]), as_h2(nz[2 * k]));
+                const uint32_t b1 = dequant_h2(code_h2<VB>(x[2 * k + 1], c), as_h2(sv[2 * k + 1]), as_h2(nz[2 * k + 1]));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][hw * kCodes + c], pf[mt][k], b0, b1);
+              }
+          }
+        } else {  // fp16 rows, and the group in which the quantized values end
+#pragma unroll 1
+          for (int hw = 0; hw < 2; ++hw) {  // channels 16 n8 + 8 hw .. + 7
+            uint32_t x[8][4];  // tokens (t, a), (t, b)
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int tt = 8 * (y >> 1) + ((y & 1) ? cb : ca);
+              uint4 v;
+              if (tw + tt < w.len.nqv) {
+                const uint32_t cwd = *reinterpret_cast<const uint32_t*>(stage + S::kVc + (32 * warp + tt) * S::kVRow + n8 * (2 * VB) + (VB == 4 ? 4 * hw : 0)) >> (VB == 2 ? 16 * hw : 0);
+                const int at = (32 * warp + tt) * 4 + (n8 >> 1);
+                v = scalar_dequant8<VB>(cwd, th2f(reinterpret_cast<const uint16_t*>(stage + S::kVs)[at]),
+                                        th2f(reinterpret_cast<const uint16_t*>(stage + S::kVz)[at]));
+              } else {
+                v = fp16_value8(a, w.len, w.b, h, tw + tt, 2 * n8 + hw);
+              }
+              x[y][0] = v.x;
+              x[y][1] = v.y;
+              x[y][2] = v.z;
+              x[y][3] = v.w;
+              if (tw + tt >= w.len.n) {
+                // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
+                // every row's weight, 0 for the others: one that is not finite is taken as 0 and added at the
+                // end to the rows that see it.
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) any |= drop_nonfinite(x[y][e]);
+                if (any) *nonfinite = 1;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int sel = (c & 1) ? 0x7632 : 0x5410;
+                const uint32_t b0 = __byte_perm(x[4 * k][c >> 1], x[4 * k + 1][c >> 1], sel);
+                const uint32_t b1 = __byte_perm(x[4 * k + 2][c >> 1], x[4 * k + 3][c >> 1], sel);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  if (hw == 0) mma_f16(o[mt][c], pf[mt][k], b0, b1);
+                  else mma_f16(o[mt][8 + c], pf[mt][k], b0, b1);
+                }
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      // the stage of the tile before takes the next copies once all warps are done with it
+      if (tid == 0 && i > 0 && copied < n && copied < i + kSt) {
+        wait(&empty[(i - 1) % kSt], ((i - 1) / kSt) & 1);
+        if (!*failed) produce();
+      }
+    }
+
+    // ================= the segment ends here (or the share does): hand its sums on =================
+    const int t_end = tile_first + i - i_first;  // tiles of the segment that are done
+    const bool last = t_end == w.len.tiles, earlier = tile_first > 0 && i_first == 0;
+    const bool whole = last && !earlier;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[mt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][e], 1);
+        l[mt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][e], 2);
+        if (q4 == 0) ml[warp * kRows + 16 * mt + n8 + 8 * e] = make_float2(m[mt][e], l[mt][e]);
+      }
+    __syncthreads();
+    // every warp's sums against the block's maximum; warps 2, 3 hand theirs to 0, 1, then 1 to 0
+    float ms[MT][2], lt[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * mt + n8 + 8 * e;
+        float2 v[kMmaWarps];
+#pragma unroll
+        for (int k = 0; k < kMmaWarps; ++k) v[k] = ml[k * kRows + r];
+        ms[mt][e] = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+        lt[mt][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMmaWarps; ++k)
+          if (v[k].y != 0.f) lt[mt][e] += v[k].y * exp2_approx(v[k].x - ms[mt][e]);  // 0: the row saw nothing there
+        const float f = l[mt][e] == 0.f ? 0.f : exp2_approx(m[mt][e] - ms[mt][e]);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          o[mt][t][2 * e] = f == 0.f ? 0.f : o[mt][t][2 * e] * f;
+          o[mt][t][2 * e + 1] = f == 0.f ? 0.f : o[mt][t][2 * e + 1] * f;
+        }
+      }
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+      // [sender][mt][t][e][lane]
+      if (warp >= half && warp < 2 * half) {
+        float* dst = osum + (warp - half) * kRows * kD + lane;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[((mt * 16 + t) * 4 + e) * 32] = o[mt][t][e];
+      }
+      __syncthreads();
+      if (warp < half) {
+        const float* src = osum + warp * kRows * kD + lane;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][t][e] += src[((mt * 16 + t) * 4 + e) * 32];
+      }
+      __syncthreads();
+    }
+    if (warp == 0) {  // rows 16 mt + n8 + 8 e, channels 32 q4 + 16 f + t
+      if (earlier) sh.first = last ? 2 : 1;
+      else if (!last) {
+        sh.open = w.b * seg_per_b + w.seg;
+        sh.nd = w.len.nd;
+      }
+      float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<kRows>();
+      const bool fix = *nonfinite != 0;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * mt + n8 + 8 * e, di = r / rep;
+          if (r >= rows_all || di >= w.len.nd) continue;  // padding
+          if (fix) {  // of the drafted tokens in this block's tiles
+            const int j1 = min(w.len.nd, t_end * kTile - w.len.n);
+            for (int j = max(0, tile_first * kTile - w.len.n); j < j1; ++j) {
+              if (!((mask[r] >> j) & 1ull)) continue;
+              const uint16_t* v = a.v_draft + (((size_t)w.b * a.N + j) * a.H + h) * kD + 32 * q4;
+#pragma unroll
+              for (int t = 0; t < 16; ++t) {
+                if ((v[t] & 0x7C00u) == 0x7C00u) o[mt][t][2 * e] += th2f(v[t]);
+                if ((v[16 + t] & 0x7C00u) == 0x7C00u) o[mt][t][2 * e + 1] += th2f(v[16 + t]);
+              }
+            }
+          }
+          const float ls = lt[mt][e];
+          const bool some = ls > 0.f || ls != ls;
+          if (whole) {
+            const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r % rep) * kD + 32 * q4;
+            if (a.out_fp32) {
+              float* p = reinterpret_cast<float*>(a.out) + at;
+#pragma unroll
+              for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int t = 0; t < 16; t += 4)
+                  *reinterpret_cast<float4*>(p + 16 * f + t) =
+                      some ? make_float4(o[mt][t][2 * e + f] / ls, o[mt][t + 1][2 * e + f] / ls, o[mt][t + 2][2 * e + f] / ls, o[mt][t + 3][2 * e + f] / ls)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+              uint16_t* p = reinterpret_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+              for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int t = 0; t < 16; t += 8) {
+                  uint32_t u[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    u[k] = some ? f32_to_bf16(o[mt][t + 2 * k][2 * e + f] / ls) | ((uint32_t)f32_to_bf16(o[mt][t + 2 * k + 1][2 * e + f] / ls) << 16) : 0u;
+                  *reinterpret_cast<uint4*>(p + 16 * f + t) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+          } else {
+            float* p = slot + (size_t)r * kD + 32 * q4;
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+              for (int t = 0; t < 16; t += 4)
+                *reinterpret_cast<float4*>(p + 16 * f + t) = make_float4(o[mt][t][2 * e + f], o[mt][t + 1][2 * e + f], o[mt][t + 2][2 * e + f], o[mt][t + 3][2 * e + f]);
+            if (q4 == 0) {
+              slot[(size_t)kRows * kD + r] = ms[mt][e];
+              slot[(size_t)kRows * kD + kRows + r] = ls;
+            }
+          }
+        }
+      __syncwarp();
+      if (lane == 0) *nonfinite = 0;
+    }
+    w.tile = t_end - 1;
+    w.next(a, seg_per_b, i < n);
+    __syncthreads();  // the queries and row state are read before the next segment's
+  }
+  if (tid == 0) {
+    shared[blockIdx.x] = sh;
+    if (*failed)  // copies in flight land before the block leaves
+      for (int k = max(0, copied - kSt); k < copied; ++k) mbar_wait_bounded(&full[k % kSt], (k / kSt) & 1, 10000000ull);
+  }
+}
+
+// ======================================================================================
+// More rows: tcgen05 on tiles of 64 rows
+// ======================================================================================
+//
+//   S^T [128 tokens x rows] = K [128 x 128] . q^T      K dequantized to fp16 in shared memory
+//   P^T = exp2(S^T c - m)                               a thread owns a token and half the rows
+//   O^T [128 channels x rows] += V^T [128 x 128] . P^T  V^T dequantized to fp16 in shared memory
+// The sums l stay per thread until the segment ends; whether a running maximum has to move is a block-wide vote.
+constexpr int kTreeThreads = 256;
 
 // V^T is staged in 8 channel x 8 token core matrices: the 16 of a row group (8 channels) are contiguous, row
 // groups 2064 bytes apart, so that eight threads with eight row groups store to different banks
@@ -38,18 +807,11 @@ constexpr int kVRowGrp = (kTile / 8) * 128 + 16;
 
 template <int KB, int VB, int ROWS>
 struct TreeLayout {
-  static constexpr int kKRow = kD * KB / 8, kVRow = kD * VB / 8;   // code bytes per token
   static constexpr int kOffQ = 0;                                  // fp16 [ROWS x 128], K-major
   static constexpr int kOffK = kOffQ + ROWS * kD * 2;              // fp16 [128 tokens x 128], K-major; then P
   static constexpr int kOffV = kOffK + kTile * kD * 2;             // fp16 [128 channels x 128 tokens], K-major
-  // a tile as it is stored: key codes, scales and zeros [4 groups][128], value codes, scales and zeros [128][4]
-  static constexpr int kOffKc = (kOffV + (kD / 8) * kVRowGrp + 127) / 128 * 128;
-  static constexpr int kOffKs = kOffKc + kTile * kKRow;
-  static constexpr int kOffKz = kOffKs + (kTile / kGroupT) * kD * 2;
-  static constexpr int kOffVc = kOffKz + (kTile / kGroupT) * kD * 2;
-  static constexpr int kOffVs = kOffVc + kTile * kVRow;
-  static constexpr int kOffVz = kOffVs + kTile * (kD / kGroupT) * 2;
-  static constexpr int kOffMask = kOffVz + kTile * (kD / kGroupT) * 2;  // uint64 [ROWS]
+  static constexpr int kOffStage = (kOffV + (kD / 8) * kVRowGrp + 127) / 128 * 128;
+  static constexpr int kOffMask = kOffStage + StageLayout<KB, VB>::kBytes;  // uint64 [ROWS]
   static constexpr int kOffC = kOffMask + ROWS * 8;                // float [ROWS]: log2 units per score unit
   static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: running maximum (log2) - kRaise
   static constexpr int kOffT = kOffM + ROWS * 4;                   // float [ROWS]: running maximum + kSlack
@@ -58,7 +820,6 @@ struct TreeLayout {
   static constexpr int kOffBar = kOffRed + 4 * ROWS * 4;           // mbarriers, TMEM address, flags
   static constexpr int kSmem = kOffBar + 64;
   static constexpr uint32_t kCols = 2 * ROWS < 32 ? 32 : 2 * ROWS;  // TMEM: S^T, O^T
-  static constexpr uint32_t kKBytes = kOffVc - kOffKc, kVBytes = kOffMask - kOffVc;
   static_assert(ROWS * 256 <= kTile * kD * 2, "P fits in the key tile");
   static_assert(kSmem <= 232448 / 2 - 1024, "two blocks per SM");
 };
@@ -109,150 +870,166 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                : "memory");
 }
 
-__device__ __forceinline__ float th2f(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The work of a call, the same for every block: segment (b, h, row tile) has T_b tiles (its cached
-// and drafted tokens), all segments in the order b, h, row tile form one list of P tile positions,
-// and block k of G takes positions [k P / G, (k + 1) P / G).
-struct TreeLens {
-  int nqk, nqv, n, nd;  // quantized keys, quantized values, cached tokens, drafted tokens
-  int tiles;
-};
-__device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
-  TreeLens L;
-  L.nqk = min(max(a.n_quant_k[b], 0), a.max_tokens) / kGroupT * kGroupT;
-  L.nqv = (a.residual > 0) ? min(max(a.n_quant_v[b], 0), L.nqk) : L.nqk;
-  L.n = L.nqk + max(0, min(a.n_tok[b] - L.nqk, a.residual));
-  L.nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
-  L.tiles = L.nd > 0 ? (int)(((long long)L.n + L.nd + kTile - 1) / kTile) : 0;
-  return L;
-}
-__device__ __forceinline__ long long share_begin(long long P, int k, int G) { return P * k / G; }
-// the block whose share holds position p
-__device__ __forceinline__ int share_of(long long P, long long p, int G) { return (int)(((p + 1) * G - 1) / P); }
-
-// partial softmax of a segment: rows of o[128], then m, l per row
-template <int ROWS>
-__host__ __device__ constexpr size_t slot_floats() { return (size_t)ROWS * (kD + 2); }
-
-struct Token {
-  const KiviTreeArgs* a;
-  TreeLens L;
-  size_t bh;  // b * H + h
-  int b, h;
-};
-
-// channels 8c .. 8c+7 of token t's key / value as fp16 (zero past the last drafted token)
+// ---- keys of a tile. A lane takes token lane % 8 of an octet and a code word (2 bits: 16 channels, 4 bits: 8);
+//      a warp one key group and half of the words, so a lane unpacks four tokens per scale. Groups behind the
+//      quantized keys are fp16 rows. ----
 template <int KB>
-__device__ __forceinline__ uint4 key8(const Token& k, int t, int c) {
-  const KiviTreeArgs& a = *k.a;
-  if (t < k.L.nqk) {
-    const uint8_t* row = a.k_codes + (k.bh * a.max_tokens + t) * (kD * KB / 8);
-    const uint32_t w = (KB == 2) ? __ldg(reinterpret_cast<const uint16_t*>(row) + c) : __ldg(reinterpret_cast<const uint32_t*>(row) + c);
-    const size_t g = (k.bh * (a.max_tokens / kGroupT) + t / kGroupT) * kD + 8 * c;
-    const uint4 s = __ldg(reinterpret_cast<const uint4*>(a.k_scale + g)), z = __ldg(reinterpret_cast<const uint4*>(a.k_zero + g));
-    const uint32_t sw[4] = {s.x, s.y, s.z, s.w}, zw[4] = {z.x, z.y, z.z, z.w};
-    uint32_t o[4];
+__device__ __forceinline__ void unpack_keys(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
+                                            const unsigned char* codes, const unsigned char* scale,
+                                            const unsigned char* zero, unsigned char* dst0, int warp, int lane) {
+  constexpr int kRow = kD * KB / 8;
+  const int g = warp & 3, tok = 32 * g + (lane & 7);
+  if (t0 + 32 * g < len.nqk) {
+    constexpr int kBlocks = (KB == 2) ? 1 : 2;   // of four words
+    constexpr int kPairs = (KB == 2) ? 8 : 4;    // channel pairs of a word
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float c0 = (float)((w >> (KB * 2 * i)) & ((1 << KB) - 1)), c1 = (float)((w >> (KB * (2 * i + 1))) & ((1 << KB) - 1));
-      o[i] = pack_h2(th2f(sw[i] & 0xFFFFu) * (c0 - th2f(zw[i] & 0xFFFFu)), th2f(sw[i] >> 16) * (c1 - th2f(zw[i] >> 16)));
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  if (t < k.L.n)
-    return __ldg(reinterpret_cast<const uint4*>(a.k_resid + (k.bh * a.residual + (t - k.L.nqk)) * kD + 8 * c));
-  if (t < k.L.n + k.L.nd)
-    return __ldg(reinterpret_cast<const uint4*>(a.k_draft + (((size_t)k.b * a.N + (t - k.L.n)) * a.H + k.h) * kD + 8 * c));
-  return make_uint4(0u, 0u, 0u, 0u);
-}
-__device__ __forceinline__ bool half2_finite(uint32_t w) { return (w & 0x7C00u) != 0x7C00u && (w & 0x7C000000u) != 0x7C000000u; }
-template <int VB>
-__device__ __forceinline__ uint4 value8(const Token& k, int t, int c, int* nonfinite) {
-  const KiviTreeArgs& a = *k.a;
-  if (t < k.L.nqv) {
-    const size_t tok = k.bh * a.max_tokens + t;
-    const uint8_t* row = a.v_codes + tok * (kD * VB / 8);
-    const uint32_t w = (VB == 2) ? __ldg(reinterpret_cast<const uint16_t*>(row) + c) : __ldg(reinterpret_cast<const uint32_t*>(row) + c);
-    const float s = th2f(__ldg(a.v_scale + tok * (kD / kGroupT) + c / 4)), z = th2f(__ldg(a.v_zero + tok * (kD / kGroupT) + c / 4));
-    uint32_t o[4];
+    for (int blk = 0; blk < kBlocks; ++blk) {
+      const int w = (warp >> 2) * 4 * kBlocks + 4 * blk + (lane >> 3);
+      __half2 s[kPairs], nsz[kPairs];
+      const uint4* sp = reinterpret_cast<const uint4*>(scale + (g * kD + 2 * kPairs * w) * 2);
+      const uint4* zp = reinterpret_cast<const uint4*>(zero + (g * kD + 2 * kPairs * w) * 2);
+      {
+        uint4 s0, s1, z0, z1;
+        pair_order<KB>(sp[0], sp[KB == 2 ? 1 : 0], s0, s1);
+        pair_order<KB>(zp[0], zp[KB == 2 ? 1 : 0], z0, z1);
+        const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float c0 = (float)((w >> (VB * 2 * i)) & ((1 << VB) - 1)), c1 = (float)((w >> (VB * (2 * i + 1))) & ((1 << VB) - 1));
-      o[i] = pack_h2(s * (c0 - z), s * (c1 - z));
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  if (t < k.L.n) return __ldg(reinterpret_cast<const uint4*>(a.v_resid + (k.bh * a.residual + t % a.residual) * kD + 8 * c));
-  if (t < k.L.n + k.L.nd) {
-    // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
-    // every row's weight, 0 for the others: one that is not finite is staged as 0 and added at the
-    // end to the rows that see it.
-    uint4 u = __ldg(reinterpret_cast<const uint4*>(a.v_draft + (((size_t)k.b * a.N + (t - k.L.n)) * a.H + k.h) * kD + 8 * c));
-    if (!(half2_finite(u.x) && half2_finite(u.y) && half2_finite(u.z) && half2_finite(u.w))) {
-      *nonfinite = 1;
-      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int j = 0; j < kPairs; ++j) {
+          s[j] = as_h2(sw[j]);
+          nsz[j] = __hneg2(__hmul2(s[j], as_h2(zw[j])));
+        }
+      }
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint32_t*>(codes + (tok + 8 * i) * kRow + 4 * w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if ((w[i] & 0x7C00u) == 0x7C00u) w[i] &= 0xFFFF0000u;
-        if ((w[i] & 0x7C000000u) == 0x7C000000u) w[i] &= 0xFFFFu;
+        const int t = tok + 8 * i;
+        uint32_t o[kPairs];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) o[j] = dequant_h2(code_h2<KB>(u[i], j), s[j], nsz[j]);
+        unsigned char* dst = dst0 + (t >> 3) * 2048 + w * (kPairs * 32) + (t & 7) * 16;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      u = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return u;
-  }
-  return make_uint4(0u, 0u, 0u, 0u);
-}
-
-// Channel order of the staged keys and queries. The contraction runs over all 128 channels, so any order serves
-// that both share; this one is the order in which a code word's halves unpack: pairs (c, c + 8) of 16 channels
-// (2 bits), (c, c + 4) of 8 (4 bits). lo, hi: channels 16 w .. + 7, 16 w + 8 .. + 15, natural order; out: the two
-// 16-byte chunks of the block.
-template <int KB>
-__device__ __forceinline__ void pair_order(const uint4 lo, const uint4 hi, uint4& out0, uint4& out1) {
-  if constexpr (KB == 2) {
-    out0 = make_uint4(__byte_perm(lo.x, hi.x, 0x5410), __byte_perm(lo.x, hi.x, 0x7632), __byte_perm(lo.y, hi.y, 0x5410),
-                      __byte_perm(lo.y, hi.y, 0x7632));
-    out1 = make_uint4(__byte_perm(lo.z, hi.z, 0x5410), __byte_perm(lo.z, hi.z, 0x7632), __byte_perm(lo.w, hi.w, 0x5410),
-                      __byte_perm(lo.w, hi.w, 0x7632));
   } else {
-    out0 = make_uint4(__byte_perm(lo.x, lo.z, 0x5410), __byte_perm(lo.x, lo.z, 0x7632), __byte_perm(lo.y, lo.w, 0x5410),
-                      __byte_perm(lo.y, lo.w, 0x7632));
-    out1 = make_uint4(__byte_perm(hi.x, hi.z, 0x5410), __byte_perm(hi.x, hi.z, 0x7632), __byte_perm(hi.y, hi.w, 0x5410),
-                      __byte_perm(hi.y, hi.w, 0x7632));
+    const int c = (warp >> 2) * 4 + (lane >> 3);  // 16 channels c
+    uint4 x[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i][0] = fp16_key8(a, len, b, h, t0 + tok + 8 * i, 2 * c);
+      x[i][1] = fp16_key8(a, len, b, h, t0 + tok + 8 * i, 2 * c + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = tok + 8 * i;
+      uint4 x0, x1;
+      pair_order<KB>(x[i][0], x[i][1], x0, x1);
+      unsigned char* dst = dst0 + (t >> 3) * 2048 + c * 256 + (t & 7) * 16;
+      *reinterpret_cast<uint4*>(dst) = x0;
+      *reinterpret_cast<uint4*>(dst + 128) = x1;
+    }
   }
 }
-// Token order of the staged values and weights: in odd octets neighbours change places, so that the two octets a
-// warp reads at a time come from different banks.
-__device__ __forceinline__ int token_place(int t) { return t ^ ((t >> 3) & 1); }
 
-__device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
-__device__ __forceinline__ uint32_t as_u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-// Code j of both halves of w as fp16 (exact): masked in place under the exponent of 2^10, where it stands for
-// 1024 + c 2^(b j), and scaled back by one FMA. Codes above the ten mantissa bits come from w shifted right.
-template <int BITS>
-__device__ __forceinline__ __half2 code_h2(uint32_t w, int j) {
-  constexpr int kIn = (BITS == 2) ? 5 : 2;  // codes that fit in place
-  const int jj = j < kIn ? j : j - kIn;
-  const uint32_t m = ((j < kIn ? w : w >> (BITS * kIn)) & ((((1u << BITS) - 1u) << (BITS * jj)) * 0x10001u)) | 0x64006400u;
-  const float p = 1.f / (float)(1 << (BITS * jj));
-  return __hfma2(as_h2(m), __float2half2_rn(p), __float2half2_rn(-1024.f * p));
-}
-// s c - s z, one rounding of s z and one of the result
-__device__ __forceinline__ uint32_t dequant_h2(__half2 c, __half2 s, __half2 nsz) { return as_u(__hfma2(c, s, nsz)); }
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// ---- values of a tile, transposed. A thread takes a token octet and eight channels; octets with tokens behind
+//      the quantized values mix stored tokens and fp16 rows ----
+template <int VB>
+__device__ __forceinline__ void unpack_values(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
+                                              const unsigned char* codes, const unsigned char* scale,
+                                              const unsigned char* zero, unsigned char* dst0, int* nonfinite, int warp,
+                                              int lane) {
+  constexpr int kRow = kD * VB / 8;
+  const int c = lane & 15, oct = 2 * warp + (lane >> 4), flip = oct & 1;
+  unsigned char* dst = dst0 + c * kVRowGrp + oct * 128;
+  const unsigned char* cw = codes + 8 * oct * kRow + ((VB == 2) ? (c >> 1) : c) * 4;
+  const uint16_t* sp = reinterpret_cast<const uint16_t*>(scale) + 8 * oct * 4 + (c >> 2);
+  const uint16_t* zp = reinterpret_cast<const uint16_t*>(zero) + 8 * oct * 4 + (c >> 2);
+  if (t0 + 8 * oct + 8 <= len.nqv) {
+    uint32_t w[8];  // place i of the octet: token i ^ flip
+    __half2 s[4], nsz[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(cw + (i ^ flip) * kRow);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ta = ((2 * i) ^ flip) * 4, tb = ((2 * i + 1) ^ flip) * 4;
+      s[i] = as_h2(sp[ta] | ((uint32_t)sp[tb] << 16));
+      nsz[i] = __hneg2(__hmul2(s[i], as_h2(zp[ta] | ((uint32_t)zp[tb] << 16))));
+    }
+    if constexpr (VB == 2) {
+      const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __byte_perm(w[2 * i], w[2 * i + 1], sel);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<2>(x[i], e), s[i], nsz[i]);
+        *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    } else {
+#pragma unroll
+      for (int hw = 0; hw < 2; ++hw) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __byte_perm(w[2 * i], w[2 * i + 1], hw ? 0x7632 : 0x5410);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<4>(x[i], e), s[i], nsz[i]);
+          *reinterpret_cast<uint4*>(dst + (4 * hw + e) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+  } else {
+    uint32_t x[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = t0 + 8 * oct + (i ^ flip);
+      const uint4 u = t >= len.nqv ? fp16_value8(a, len, b, h, t, c) : make_uint4(0u, 0u, 0u, 0u);
+      x[i][0] = u.x;
+      x[i][1] = u.y;
+      x[i][2] = u.z;
+      x[i][3] = u.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = t0 + 8 * oct + (i ^ flip);
+      if (t < len.nqv) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(cw + (i ^ flip) * kRow) >> ((VB == 2) ? 16 * (c & 1) : 0);
+        const uint4 u = scalar_dequant8<VB>(w, th2f(sp[(i ^ flip) * 4]), th2f(zp[(i ^ flip) * 4]));
+        x[i][0] = u.x;
+        x[i][1] = u.y;
+        x[i][2] = u.z;
+        x[i][3] = u.w;
+      } else if (t >= len.n) {
+        // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
+        // every row's weight, 0 for the others: one that is not finite is staged as 0 and added at the
+        // end to the rows that see it.
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= drop_nonfinite(x[i][e]);
+        if (any) *nonfinite = 1;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __byte_perm(x[2 * i][e >> 1], x[2 * i + 1][e >> 1], (e & 1) ? 0x7632 : 0x5410);
+      *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 template <int KB, int VB, int ROWS>
 __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTreeArgs a, const float scale_log2) {
   using L = TreeLayout<KB, VB, ROWS>;
+  using S = StageLayout<KB, VB>;
   extern __shared__ __align__(128) unsigned char sm[];
   uint64_t* mask = reinterpret_cast<uint64_t*>(sm + L::kOffMask);
   float* rowc = reinterpret_cast<float*>(sm + L::kOffC);
@@ -267,36 +1044,22 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 4);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* nonfinite = reinterpret_cast<int*>(tmem_slot + 2);
-  long long* scan = reinterpret_cast<long long*>(sm);  // before the first tile: one per thread
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rep = a.Hq / a.H, rows_all = a.N * rep;
   const int n_rt = (rows_all + ROWS - 1) / ROWS;  // row tiles of a KV head
   const int seg_per_b = a.H * n_rt;
 
-  // ---- the block's share: tiles of all requests, and the request its first position lies in ----
-  const int chunk = (a.B + kTreeThreads - 1) / kTreeThreads;
-  const int chunks = (a.B + chunk - 1) / chunk;  // threads with requests
-  long long mine = 0;
-  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += tree_lens(a, b).tiles;
-  scan[tid] = mine;
-  __syncthreads();
-  long long P = 0, before = 0;
-  for (int i = 0; i < chunks; ++i) P += scan[i];
-  P *= seg_per_b;
-  const long long p0 = share_begin(P, blockIdx.x, gridDim.x), p1 = share_begin(P, blockIdx.x + 1, gridDim.x);
-  if (p0 >= p1) return;  // uniform
-  int c0 = 0;
-  while (p0 >= (before + scan[c0]) * seg_per_b) before += scan[c0++];  // ends: p0 < P
-  int b = c0 * chunk;
-  TreeLens len = tree_lens(a, b);
-  while (p0 >= (before + len.tiles) * seg_per_b) {  // ends inside chunk c0
-    before += len.tiles;
-    len = tree_lens(a, ++b);
+  TreeShared* shared = reinterpret_cast<TreeShared*>(a.part);
+  float* slots = reinterpret_cast<float*>(shared + gridDim.x);
+  Walk w;
+  const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), w);
+  const int p0 = share.x, p1 = share.y;
+  TreeShared sh = {p0 < p1 ? 0 : 3, -1, 0, 0};
+  if (p0 >= p1) {
+    if (tid == 0) shared[blockIdx.x] = sh;
+    return;
   }
-  int seg = (int)((p0 - before * seg_per_b) / len.tiles);  // h * n_rt + row tile
-  int tile = (int)((p0 - before * seg_per_b) % len.tiles);
-  __syncthreads();
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -304,24 +1067,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // the stored keys (values) of a tile whose tokens are all quantized: into the stage by bulk copies
-  auto copy_keys = [&](int cb, int ch, int t0) {
-    const size_t bh = (size_t)cb * a.H + ch, g = (bh * (a.max_tokens / kGroupT) + t0 / kGroupT) * kD;
+  unsigned char* stage = sm + L::kOffStage;
+  auto keys_of = [&](const Walk& x) {
     fence_proxy_async_smem();
-    mbar_arrive_expect_tx(bar_k, L::kKBytes);
-    bulk_g2s(sm + L::kOffKc, a.k_codes + (bh * a.max_tokens + t0) * L::kKRow, kTile * L::kKRow, bar_k);
-    bulk_g2s(sm + L::kOffKs, a.k_scale + g, L::kOffKz - L::kOffKs, bar_k);
-    bulk_g2s(sm + L::kOffKz, a.k_zero + g, L::kOffVc - L::kOffKz, bar_k);
+    copy_keys<KB, VB>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, bar_k);
   };
-  auto copy_values = [&](int cb, int ch, int t0) {
-    const size_t tok = ((size_t)cb * a.H + ch) * a.max_tokens + t0;
+  auto values_of = [&](const Walk& x) {
     fence_proxy_async_smem();
-    mbar_arrive_expect_tx(bar_v, L::kVBytes);
-    bulk_g2s(sm + L::kOffVc, a.v_codes + tok * L::kVRow, kTile * L::kVRow, bar_v);
-    bulk_g2s(sm + L::kOffVs, a.v_scale + tok * (kD / kGroupT), L::kOffVz - L::kOffVs, bar_v);
-    bulk_g2s(sm + L::kOffVz, a.v_zero + tok * (kD / kGroupT), L::kOffMask - L::kOffVz, bar_v);
+    copy_values<KB, VB>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, bar_v);
   };
-  auto stored = [](const TreeLens& l, int tl) { return (tl + 1) * kTile <= l.nqv; };  // nqv <= nqk
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_o, 1);
@@ -330,10 +1084,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     *failed = 0;
     *nonfinite = 0;
     fence_mbar_init();
-    if (stored(len, tile)) {
-      copy_keys(b, seg / n_rt, tile * kTile);
-      copy_values(b, seg / n_rt, tile * kTile);
-    }
+    keys_of(w);
+    values_of(w);
   }
   tmem_before();
   __syncthreads();
@@ -343,8 +1095,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
   constexpr int kHR = ROWS / 2;                            // rows a thread works on
   const int r0 = half * kHR;
-  uint32_t phase = 0;    // of bar_s and bar_o: one completion each per tile
-  uint32_t landed = 0;   // tiles that came through the stage: their parity is that of bar_k and bar_v
+  uint32_t phase = 0;    // of the barriers: one completion each per tile
   float l[kHR];
   bool first = true;    // of the segment's tiles in this block
   int tile_first = 0;   // that tile
@@ -355,122 +1106,38 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     }
   };
 
-  for (long long p = p0; p < p1; ++p) {
-    const int h = seg / n_rt, rt = seg % n_rt;
-    const Token tk = {&a, len, (size_t)b * a.H + h, b, h};
-    const int row0 = rt * ROWS;
-    const int t0 = tile * kTile;
-    const bool from_stage = stored(len, tile);
-    // ---- the position after this one ----
-    const bool last = tile + 1 == len.tiles;
-    int nb = b, nseg = seg, ntile = tile + 1;
-    TreeLens nlen = len;
-    if (last) {
-      ntile = 0;
-      if (++nseg == seg_per_b) {
-        nseg = 0;
-        if (p + 1 < p1) {
-          do nlen = tree_lens(a, ++nb);
-          while (nlen.tiles == 0);  // a position is left, so such a request exists
-        }
-      }
-    }
-    const bool copy_next = p + 1 < p1 && stored(nlen, ntile);
+  for (int p = p0; p < p1; ++p) {
+    const int b = w.b, h = w.seg / n_rt, row0 = (w.seg - h * n_rt) * ROWS, tile = w.tile, t0 = tile * kTile;
+    const TreeLens& len = w.len;
+    const bool last = w.last(), more = p + 1 < p1;
+    Walk nw = w;
+    nw.next(a, seg_per_b, more);
     if (first) {
-      // ---- the segment's query rows: fp16, each divided by a power of two that puts its largest
-      //      magnitude in [2^14, 2^15); the masks and the running state ----
+      // ---- the segment's query rows, masks and running state (8 lanes a row) ----
 #pragma unroll
       for (int i = 0; i < kHR; ++i) l[i] = 0.f;
-      for (int i = tid; i < ROWS * 8; i += kTreeThreads) {  // 8 lanes per row, 16 channels each
-        const int r = i >> 3, c = i & 7, row = row0 + r, di = row / rep;
-        uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (row < rows_all && di < len.nd) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 16 * c);
-          u[0] = __ldg(src);
-          u[1] = __ldg(src + 1);
-        }
-        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-        float mx = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-#pragma unroll
-        for (int off = 4; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-        const int ex = (int)(__float_as_uint(mx) >> 23);  // biased exponent; 0: zero or subnormal, 255: not finite
-        // times 2^(14 - (ex - 127)) in two factors, since the power may pass the fp32 range
-        const int sh = (ex == 0 || ex == 255) ? 0 : 141 - ex;
-        const float f1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = pack_h2(bf16_lo(w[e]) * f1 * f2, bf16_hi(w[e]) * f1 * f2);
+#pragma unroll 1
+      for (int i = tid; i < ROWS * 8; i += kTreeThreads) {
+        const int r = i >> 3, c = i & 7;
+        uint32_t u[8], o[8];
+        const bool real = load_query(a, len, b, h, row0 + r, c, u);
+        const float back = query_fp16(u, o, scale_log2);
         uint4 x0, x1;
         pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
         unsigned char* dst = sm + L::kOffQ + (r >> 3) * 2048 + c * 256 + (r & 7) * 16;
         *reinterpret_cast<uint4*>(dst) = x0;
         *reinterpret_cast<uint4*>(dst + 128) = x1;
         if (c == 0) {
-          rowc[r] = scale_log2 / f1 / f2;
+          rowc[r] = back;
           rowm[r] = rowt[r] = -FLT_MAX;
-          mask[r] = (row < rows_all && di < len.nd) ? a.mask[(size_t)b * a.N + di] : 0ull;
+          mask[r] = real ? a.mask[(size_t)b * a.N + (row0 + r) / rep] : 0ull;
         }
       }
       if (tid == 0) *nonfinite = 0;
       tile_first = tile;
     }
-    // ---- keys of the tile. A lane takes token lane % 8 of an octet and a code word (2 bits: 16 channels, 4
-    //      bits: 8); a warp one key group and half of the words, so a lane unpacks four tokens per scale ----
-    if (from_stage) {
-      wait(bar_k, landed & 1);
-      const int g = warp & 3, tok = 32 * g + (lane & 7);
-      constexpr int kBlocks = (KB == 2) ? 1 : 2;   // of four words
-#pragma unroll
-      for (int blk = 0; blk < kBlocks; ++blk) {
-        const int w = (warp >> 2) * 4 * kBlocks + 4 * blk + (lane >> 3);
-        constexpr int kPairs = (KB == 2) ? 8 : 4;  // channel pairs of a word
-        __half2 s[kPairs], nsz[kPairs];
-        const uint4* sp = reinterpret_cast<const uint4*>(sm + L::kOffKs + (g * kD + 2 * kPairs * w) * 2);
-        const uint4* zp = reinterpret_cast<const uint4*>(sm + L::kOffKz + (g * kD + 2 * kPairs * w) * 2);
-        {
-          uint4 s0, s1 = make_uint4(0u, 0u, 0u, 0u), z0, z1 = s1;
-          if constexpr (KB == 2) {
-            pair_order<2>(sp[0], sp[1], s0, s1);
-            pair_order<2>(zp[0], zp[1], z0, z1);
-          } else {
-            uint4 none;
-            pair_order<4>(sp[0], sp[0], s0, none);
-            pair_order<4>(zp[0], zp[0], z0, none);
-          }
-          const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-          const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) {
-            s[j] = as_h2(sw[j]);
-            nsz[j] = __hneg2(__hmul2(s[j], as_h2(zw[j])));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = tok + 8 * i;
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(sm + L::kOffKc + t * L::kKRow + 4 * w);
-          uint32_t o[kPairs];
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) o[j] = dequant_h2(code_h2<KB>(u, j), s[j], nsz[j]);
-          unsigned char* dst = sm + L::kOffK + (t >> 3) * 2048 + w * (kPairs * 32) + (t & 7) * 16;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-          if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-      }
-    } else {
-#pragma unroll 1
-      for (int i = warp; i < 32; i += kTreeWarps) {
-        const int t = 8 * (i >> 1) + (lane & 7), c = 4 * (i & 1) + (lane >> 3);  // 16 channels c
-        uint4 x0, x1;
-        pair_order<KB>(key8<KB>(tk, t0 + t, 2 * c), key8<KB>(tk, t0 + t, 2 * c + 1), x0, x1);
-        unsigned char* dst = sm + L::kOffK + (t >> 3) * 2048 + c * 256 + (t & 7) * 16;
-        *reinterpret_cast<uint4*>(dst) = x0;
-        *reinterpret_cast<uint4*>(dst + 128) = x1;
-      }
-    }
+    wait(bar_k, phase);
+    unpack_keys<KB>(a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane);
     fence_proxy_async_smem();
     tmem_before();
     if (__syncthreads_or(*failed)) break;
@@ -481,74 +1148,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         umma_f16(tmem, tree_desc(smem_u32(sm + L::kOffK) + k * 256, 128, 2048),
                  tree_desc(smem_u32(sm + L::kOffQ) + k * 256, 128, 2048), tree_idesc(ROWS, false), k > 0);
       tree_commit(bar_s);
-      if (copy_next) copy_keys(nb, nseg / n_rt, ntile * kTile);  // every thread has read this tile's
+      if (more) keys_of(nw);  // every thread has read this tile's
     }
-    // ---- values of the tile, transposed. A thread takes a token octet and eight channels ----
-    {
-      const int c = lane & 15, oct = 2 * warp + (lane >> 4), flip = oct & 1;
-      unsigned char* dst = sm + L::kOffV + c * kVRowGrp + oct * 128;
-      if (from_stage) {
-        wait(bar_v, landed & 1);
-        uint32_t w[8];  // place i of the octet: token i ^ flip
-        __half2 s[4], nsz[4];
-        const unsigned char* cw = sm + L::kOffVc + 8 * oct * L::kVRow + ((VB == 2) ? (c >> 1) : c) * 4;
-        const uint16_t* sp = reinterpret_cast<const uint16_t*>(sm + L::kOffVs) + 8 * oct * 4 + (c >> 2);
-        const uint16_t* zp = reinterpret_cast<const uint16_t*>(sm + L::kOffVz) + 8 * oct * 4 + (c >> 2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(cw + (i ^ flip) * L::kVRow);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ta = ((2 * i) ^ flip) * 4, tb = ((2 * i + 1) ^ flip) * 4;
-          s[i] = as_h2(sp[ta] | ((uint32_t)sp[tb] << 16));
-          nsz[i] = __hneg2(__hmul2(s[i], as_h2(zp[ta] | ((uint32_t)zp[tb] << 16))));
-        }
-        if constexpr (VB == 2) {
-          const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
-          uint32_t x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = __byte_perm(w[2 * i], w[2 * i + 1], sel);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<2>(x[i], e), s[i], nsz[i]);
-            *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        } else {
-#pragma unroll
-          for (int hw = 0; hw < 2; ++hw) {
-            uint32_t x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = __byte_perm(w[2 * i], w[2 * i + 1], hw ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t o[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<4>(x[i], e), s[i], nsz[i]);
-              *reinterpret_cast<uint4*>(dst + (4 * hw + e) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          }
-        }
-        ++landed;
-      } else {
-        uint32_t x[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 u = value8<VB>(tk, t0 + 8 * oct + (i ^ flip), c, nonfinite);
-          x[i][0] = u.x;
-          x[i][1] = u.y;
-          x[i][2] = u.z;
-          x[i][3] = u.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = __byte_perm(x[2 * i][e >> 1], x[2 * i + 1][e >> 1], (e & 1) ? 0x7632 : 0x5410);
-          *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-    }
+    wait(bar_v, phase);
+    unpack_values<VB>(a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, nonfinite, warp, lane);
     wait(bar_s, phase);
     tmem_after();
     // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1. x = s c is rounded before the
@@ -585,7 +1188,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     }
     tmem_before();
     const bool raise = __syncthreads_or(over);
-    if (tid == 0 && copy_next) copy_values(nb, nseg / n_rt, ntile * kTile);  // every thread has read this tile's
+    if (tid == 0 && more) values_of(nw);  // every thread has read this tile's
     if (raise) {
       // ---- raise the running maxima of the rows with a score past them ----
 #pragma unroll
@@ -669,7 +1272,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       __syncthreads();
       const bool earlier = p - tile < p0;  // the segment began in an earlier block
       const bool whole = last && !earlier;
-      float* slot = a.part + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<ROWS>();
+      if (earlier) sh.first = last ? 2 : 1;
+      else if (!last) {
+        sh.open = b * seg_per_b + w.seg;
+        sh.nd = len.nd;
+      }
+      float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<ROWS>();
       const int ch = 32 * quad + lane;
       const bool fix = *nonfinite != 0;
 #pragma unroll 1
@@ -709,15 +1317,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       __syncthreads();  // the row state is read before the next segment resets it
       first = true;
     }
-    b = nb;
-    seg = nseg;
-    tile = ntile;
-    len = nlen;
+    w = nw;
   }
-  // a wait that ran out leaves the loop at the next barrier: let this block's copies land first
-  if (tid == 0 && *failed) {
-    mbar_wait_bounded(bar_k, landed & 1);
-    mbar_wait_bounded(bar_v, landed & 1);
+  if (tid == 0) {
+    shared[blockIdx.x] = sh;
+    if (*failed) {  // a wait that ran out leaves the loop at the next barrier: let this block's copies land first
+      mbar_wait_bounded(bar_k, phase, 10000000ull);
+      mbar_wait_bounded(bar_v, phase, 10000000ull);
+    }
   }
   tmem_before();
   __syncthreads();
@@ -727,57 +1334,67 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   }
 }
 
-// Joins the partials of the segments that several blocks shared, in block order: a warp takes a
-// row, a lane four channels.
+// Joins the partials of a segment that several blocks shared, in block order. Block (k, rows): the segment that
+// block k of the attention began and left open; a warp takes a row, a lane four channels.
 constexpr int kMergeThreads = 128;
 template <int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) kivi_tree_merge_kernel(const KiviTreeArgs a, const int G) {
-  __shared__ long long part[2][kMergeThreads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead of the attention's end
+  const int lane = threadIdx.x & 31, k = blockIdx.x, r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const TreeShared* shared = reinterpret_cast<const TreeShared*>(a.part);
+  const float* slots = reinterpret_cast<const float*>(shared + G);
+  const int seg_all = shared[k].open;
+  if (seg_all < 0) return;
   const int rep = a.Hq / a.H, rows_all = a.N * rep, n_rt = (rows_all + ROWS - 1) / ROWS, seg_per_b = a.H * n_rt;
-  const int per_seg = ROWS / (kMergeThreads / 32);
-  const int sg = blockIdx.x / per_seg;
-  const int b = sg / seg_per_b, seg = sg % seg_per_b, h = seg / n_rt, rt = seg % n_rt;
-  const int r = (int)(blockIdx.x % per_seg) * (kMergeThreads / 32) + warp, row = rt * ROWS + r, di = row / rep;
-  long long all = 0, pre = 0;
-  for (int i = tid; i < a.B; i += kMergeThreads) {
-    const int t = tree_lens(a, i).tiles;
-    all += t;
-    if (i < b) pre += t;
-  }
-  part[0][tid] = all;
-  part[1][tid] = pre;
-  __syncthreads();
-  all = pre = 0;
-  for (int i = 0; i < min(a.B, kMergeThreads); ++i) {
-    all += part[0][i];
-    pre += part[1][i];
-  }
-  const TreeLens len = tree_lens(a, b);
-  if (len.tiles == 0 || row >= rows_all || di >= len.nd) return;
-  const long long P = all * seg_per_b, s0 = pre * seg_per_b + (long long)seg * len.tiles, s1 = s0 + len.tiles;
-  const int k0 = share_of(P, s0, G), k1 = share_of(P, s1 - 1, G);
-  if (k0 == k1) return;  // one block wrote the output
-  auto slot = [&](int k) {  // a segment that began in an earlier block is in a block's first slot
-    return a.part + ((size_t)k * 2 + (share_begin(P, k, G) > s0 ? 0 : 1)) * slot_floats<ROWS>();
+  const int b = seg_all / seg_per_b, seg = seg_all % seg_per_b, h = seg / n_rt;
+  const int row = (seg - h * n_rt) * ROWS + r, di = row / rep;
+  if (row >= rows_all || di >= shared[k].nd) return;
+  const size_t mo = (size_t)ROWS * kD + r, lo = mo + ROWS;
+  const float* own = slots + ((size_t)k * 2 + 1) * slot_floats<ROWS>();
+  // the blocks behind k that hold a part, 32 at a time: slot 0 of those, up to the one it ends in
+  auto part_of = [&](int kk, bool& ends) {
+    const int f = kk < G ? shared[kk].first : 2;
+    ends = f == 2;
+    return kk < G && (f == 1 || f == 2) ? slots + (size_t)kk * 2 * slot_floats<ROWS>() : nullptr;
   };
-  float M = -FLT_MAX;
-  for (int k = k0; k <= k1; ++k)
-    if (share_begin(P, k, G) < share_begin(P, k + 1, G)) M = fmaxf(M, slot(k)[(size_t)ROWS * kD + r]);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float lt = 0.f;
-  for (int k = k0; k <= k1; ++k) {
-    if (share_begin(P, k, G) == share_begin(P, k + 1, G)) continue;  // an empty share
-    const float* s = slot(k);
-    const float lk = s[(size_t)ROWS * kD + ROWS + r];
-    if (lk == 0.f) continue;  // the row saw nothing there
-    const float w = exp2f(s[(size_t)ROWS * kD + r] - M);
-    const float4 v = *reinterpret_cast<const float4*>(s + (size_t)r * kD + 4 * lane);
-    lt = fmaf(w, lk, lt);
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  float M = own[mo];
+  for (int base = k + 1;; base += 32) {
+    bool ends;
+    const float* s = part_of(base + lane, ends);
+    const uint32_t end = __ballot_sync(0xFFFFFFFFu, ends);
+    float m = (s && lane <= (end ? __ffs(end) - 1 : 31)) ? s[mo] : -FLT_MAX;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+    M = fmaxf(M, m);
+    if (end) break;
+  }
+  float lt = own[lo];
+  const float wo = lt == 0.f ? 0.f : exp2_approx(own[mo] - M);  // 0: the row saw nothing there
+  lt *= wo;
+  float4 o = *reinterpret_cast<const float4*>(own + (size_t)r * kD + 4 * lane);
+  o = wo == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
+  for (int base = k + 1;; base += 32) {
+    bool ends;
+    const float* s = part_of(base + lane, ends);
+    const uint32_t end = __ballot_sync(0xFFFFFFFFu, ends);
+    const int cnt = end ? __ffs(end) : 32;
+    float lk = (s && lane < cnt) ? s[lo] : 0.f;
+    const float wk = lk == 0.f ? 0.f : exp2_approx(s[mo] - M);
+    lk = wk == 0.f ? 0.f : lk * wk;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) lk += __shfl_xor_sync(0xFFFFFFFFu, lk, off);
+    lt += lk;
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      const float wj = __shfl_sync(0xFFFFFFFFu, wk, j);
+      if (wj == 0.f) continue;
+      const float4 v = *reinterpret_cast<const float4*>(slots + (size_t)(base + j) * 2 * slot_floats<ROWS>() + (size_t)r * kD + 4 * lane);
+      o.x = fmaf(wj, v.x, o.x);
+      o.y = fmaf(wj, v.y, o.y);
+      o.z = fmaf(wj, v.z, o.z);
+      o.w = fmaf(wj, v.w, o.w);
+    }
+    if (end) break;
   }
   const bool none = !(lt > 0.f || lt != lt);
   const size_t at = (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 4 * lane;
@@ -787,46 +1404,64 @@ __global__ void __launch_bounds__(kMergeThreads) kivi_tree_merge_kernel(const Ki
   if (a.out_fp32) {
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(val[0], val[1], val[2], val[3]);
   } else {
-    uint2 w;
-    w.x = f32_to_bf16(val[0]) | ((uint32_t)f32_to_bf16(val[1]) << 16);
-    w.y = f32_to_bf16(val[2]) | ((uint32_t)f32_to_bf16(val[3]) << 16);
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) = w;
+    uint2 u;
+    u.x = f32_to_bf16(val[0]) | ((uint32_t)f32_to_bf16(val[1]) << 16);
+    u.y = f32_to_bf16(val[2]) | ((uint32_t)f32_to_bf16(val[3]) << 16);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) = u;
   }
 }
 
-// rows of a tile: the smallest that holds a KV head's, 64 at most
+// Rows of a tile, which also choose the kernel: up to 32 rows the warp-wide products (16 or 32 rows), else tcgen05 on
+// tiles of 64.
 int tree_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-int tree_blocks() {
+int sm_count_tree() {
+  static int cached[64] = {};
   int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return 2 * sms;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms;
+  if (cached[dev] == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) cached[dev] = sms;
+  return cached[dev] ? cached[dev] : sms;
 }
+int tree_blocks(int r) { return sm_count_tree() * (r == 16 ? 3 : 2); }  // resident blocks
 
-template <int KB, int VB, int ROWS>
-cudaError_t launch_tree(const KiviTreeArgs& a, cudaStream_t st) {
-  using L = TreeLayout<KB, VB, ROWS>;
-  cudaError_t e = cudaFuncSetAttribute(kivi_tree_kernel<KB, VB, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+template <int ROWS>
+cudaError_t launch_merge(const KiviTreeArgs& a, int G, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(G, ROWS / (kMergeThreads / 32));
+  cfg.blockDim = kMergeThreads;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kivi_tree_merge_kernel<ROWS>, a, G);
+}
+template <int ROWS, typename K>
+cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int G = tree_blocks();
-  kivi_tree_kernel<KB, VB, ROWS><<<G, kTreeThreads, L::kSmem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
+  const int G = tree_blocks(ROWS);
+  kernel<<<G, threads, smem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long segs = (long long)a.B * a.H * ((a.N * (a.Hq / a.H) + ROWS - 1) / ROWS);
-  kivi_tree_merge_kernel<ROWS><<<(unsigned)(segs * (ROWS / (kMergeThreads / 32))), kMergeThreads, 0, st>>>(a, G);
-  return cudaGetLastError();
+  return launch_merge<ROWS>(a, G, st);
 }
 template <int KB, int VB>
 cudaError_t launch_tree_rows(const KiviTreeArgs& a, cudaStream_t st) {
   const int r = tree_rows(a.N * (a.Hq / a.H));
-  if (r == 16) return launch_tree<KB, VB, 16>(a, st);
-  if (r == 32) return launch_tree<KB, VB, 32>(a, st);
-  return launch_tree<KB, VB, 64>(a, st);
+  if (r == 16) return launch_with<16>(kivi_tree_mma_kernel<KB, VB, 1>, kMmaThreads, MmaLayout<KB, VB, 1>::kSmem, a, st);
+  if (r == 32) return launch_with<32>(kivi_tree_mma_kernel<KB, VB, 2>, kMmaThreads, MmaLayout<KB, VB, 2>::kSmem, a, st);
+  return launch_with<64>(kivi_tree_kernel<KB, VB, 64>, kTreeThreads, TreeLayout<KB, VB, 64>::kSmem, a, st);
 }
 
 }  // namespace
 
 size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits) {
   const int r = tree_rows(N * (Hq / H));
-  return (size_t)tree_blocks() * 2 * r * (kD + 2) * sizeof(float);
+  return (size_t)tree_blocks(r) * (sizeof(TreeShared) + 2 * r * (kD + 2) * sizeof(float));
+}
+long long kivi_tree_positions(int B, int N, int H, int Hq, int max_tokens, int residual) {
+  const int rows = N * (Hq / H), r = tree_rows(rows);
+  return (long long)B * H * ((rows + r - 1) / r) * (((long long)max_tokens + residual + N + kTile - 1) / kTile);
 }
 
 cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t st) {

@@ -615,8 +615,8 @@ KVQ_API kvq_status kvq_kivi_tree_attn(const kvq_kivi_cfg* c, const kvq_kivi_cach
   if (B < 1 || N < 1) return fail(KVQ_ERR_INVALID_ARG, "%s: B or N < 1", __func__);
   if (B > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: B > max_batch", __func__);
   if (N > 64) return fail(KVQ_ERR_UNSUPPORTED, "%s: N=%d (a tree has at most 64 drafted tokens)", __func__, N);
-  if ((double)B * c->n_heads * ((double)N * (c->n_q_heads / c->n_heads) + 64) >= 2147483648.0)
-    return fail(KVQ_ERR_UNSUPPORTED, "%s: too many query rows for one call", __func__);
+  if (kvq::kivi_tree_positions(B, N, c->n_heads, c->n_q_heads, c->max_tokens, c->residual) >= (1ll << 31))
+    return fail(KVQ_ERR_UNSUPPORTED, "%s: too many tokens and query rows for one call", __func__);
   const size_t need = kvq_kivi_tree_workspace_size(c, B, N);
   if (!ws || ws_bytes < need || !aligned16(ws))
     return fail(KVQ_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu)", __func__, need, ws_bytes);

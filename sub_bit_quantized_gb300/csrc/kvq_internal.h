@@ -221,12 +221,14 @@ struct KiviTreeArgs {
   const uint64_t* mask;            // [B][N]
   const int32_t* n_draft;          // [B], null: N
   void* out; int out_fp32;         // [B][N][Hq][D]
-  float* part;                     // partial softmaxes of segments shared by blocks
+  float* part;                     // workspace: what blocks share, partial softmaxes of those segments
   int* err;
   int B, N, H, Hq, k_bits, v_bits, max_tokens, residual;
 };
 // bytes of partials a launch of this shape may write
 size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits);
+// tile positions of a launch whose requests are full (below 2^31: checked by the host)
+long long kivi_tree_positions(int B, int N, int H, int Hq, int max_tokens, int residual);
 cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- norm and rotation of rows
