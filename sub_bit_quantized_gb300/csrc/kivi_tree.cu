@@ -273,49 +273,61 @@ __device__ __forceinline__ uint4 scalar_dequant8(uint32_t w, float s, float z) {
 // Up to 32 rows: warp-wide products
 // ======================================================================================
 //
-// Fragment orders. The contraction over channels and the one over tokens may run in any order that both operands
-// share, and output columns may be any channels; they are chosen so that a code word's halves are a fragment's
-// register without moving single codes.
-//  * Scores: lane (n = lane / 4, q = lane % 4) holds token column n and channels 32 q .. + 31, i.e. its own code
-//    words; k-step kk takes two channel pairs of them ((c, c + 8) at 2 bits, (c, c + 4) at 4 bits).
-//  * Columns n of score tile i are tokens 8 i + (n ^ (n >> 2 & 1)): the four tokens a lane quartet reads for the
-//    value product then lie in different banks.
-//  * Values: lane column n holds channels 16 n .. + 15, its own code word(s); column tile t takes channel 16 n + t,
-//    so a lane ends with 32 consecutive channels of its rows.
-// Bound: instruction issue. A group of 32 tokens costs a warp about 300 instructions for the keys (3 per code pair),
-// 90 for the softmax of 16 rows and 280 for the values.
+// Tokens (scores) and channels (values) are the 16 rows of an m16n8k16 product, the query rows its 8 columns:
+//   S^T [16 tokens x 8 rows] = K . q^T,  O^T [16 channels x 8 rows] += V^T . P^T,
+// so a row tile is 8 query rows (NT of them) and the unpacked codes are the A fragments. Fragment orders: the
+// contraction over channels and the one over tokens may run in any order that both operands share, and output rows
+// may be any channels; they are chosen so that a code word's halves are a fragment's register without moving single
+// codes. Lane (n = lane / 4, q = lane % 4):
+//  * Scores: the lane holds token rows n and n + 8 of a token tile and channels 32 q .. + 31 of those, i.e. its own
+//    code words; k-step kk takes two channel pairs of them ((c, c + 8) at 2 bits, (c, c + 4) at 4 bits).
+//  * Place n of eight is token n ^ (n >> 2 & 1): the four tokens a lane quartet reads for the value product then
+//    lie in different banks.
+//  * Values: the lane holds channels 16 n .. + 15, its own code word(s): rows n and n + 8 of channel tile t are
+//    channels 16 n + 2 t and + 1.
+//  * P^T turns from accumulator into B fragment by the 8 x 8 transposition of packed halves.
+// Bound: instruction issue. A group of 32 tokens costs a warp about 290 instructions for the keys (3 per code pair),
+// 50 for the softmax of 8 rows and 270 for the values, and 32 products per 8 rows.
 constexpr int kMmaThreads = 128;
 constexpr int kMmaWarps = kMmaThreads / 32;
 
-template <int KB, int VB, int MT>  // MT: row tiles of 16
+template <int KB, int VB, int NT>  // NT: row tiles of 8
 struct MmaLayout {
   using S = StageLayout<KB, VB>;
-  static constexpr int kStages = (KB + VB == 4) ? 3 : 2;
-  static constexpr int kOffQ = kStages * S::kBytes;                 // uint4 [8 k-steps][MT][32 lanes]: A fragments
-  static constexpr int kOffO = kOffQ + 8 * MT * 32 * 16;            // float [2][MT 16][128]: sums on their way to a warp
-  static constexpr int kOffMl = kOffO + 2 * MT * 16 * kD * 4;       // float [4 warps][MT 16][2]: m, l
-  static constexpr int kOffMask = kOffMl + kMmaWarps * MT * 16 * 8; // uint64 [MT 16]
-  static constexpr int kOffC = kOffMask + MT * 16 * 8;              // float [MT 16]: log2 units per score unit
-  static constexpr int kOffBar = kOffC + MT * 16 * 4;               // mbarriers, flags
+  static constexpr int kRows = 8 * NT;
+  // resident blocks the registers (32 NT sums a thread) and the shared memory leave room for
+  static constexpr int kBlocks = (NT == 1) ? ((KB + VB == 4) ? 5 : 4) : (NT == 2) ? 3 : 2;
+  static constexpr int kStages = 2;
+  static constexpr int kOffQ = kStages * S::kBytes;                 // uint4 [4][NT][32 lanes]: B fragments of two k-steps
+  static constexpr int kOffO = kOffQ + 4 * NT * 32 * 16;            // float [2][kRows][128]: sums on their way to a warp
+  static constexpr int kOffMl = kOffO + 2 * kRows * kD * 4;         // float2 [4 warps][kRows]: m, l
+  static constexpr int kOffMask = kOffMl + kMmaWarps * kRows * 8;   // uint64 [kRows]
+  static constexpr int kOffC = kOffMask + kRows * 8;                // float [kRows]: log2 units per score unit
+  static constexpr int kOffBar = kOffC + kRows * 4;                 // mbarriers, flags
   static constexpr int kSmem = kOffBar + 128;
-  static constexpr int kBlocks = (MT == 1) ? 3 : 2;                 // per SM
   static_assert(kSmem <= 232448 / kBlocks - 1024, "blocks per SM");
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-template <int KB, int VB, int MT>
-__global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
+template <int KB, int VB, int NT>
+__global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     kivi_tree_mma_kernel(const KiviTreeArgs a, const float scale_log2) {
-  using L = MmaLayout<KB, VB, MT>;
+  using L = MmaLayout<KB, VB, NT>;
   using S = StageLayout<KB, VB>;
-  constexpr int kRows = 16 * MT, kSt = L::kStages;
+  constexpr int kRows = L::kRows, kSt = L::kStages;
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ);
   float* osum = reinterpret_cast<float*>(sm + L::kOffO);
@@ -370,6 +382,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
     fence_mbar_init();
     for (int i = 0; i < min(kSt, n); ++i) produce();
   }
+  const int tok8 = n8 ^ ((n8 >> 2) & 1);                                       // the token at place n of eight
+  const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);  // at places 2 q, 2 q + 1
 
   int i = 0;  // tiles done
   while (i < n) {
@@ -383,33 +397,30 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
       const float back = query_fp16(u, o, scale_log2);
       uint4 x0, x1;
       pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
-      const uint32_t pr[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};  // pairs in fragment order
-      // lane (row % 8, c / 2), k-steps 4 (c % 2) .. + 3, registers (row >= 8) and 2 + (row >= 8)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int kk = 4 * (c & 1) + (e >> 1);
-        reinterpret_cast<uint32_t*>(qf + (kk * MT + (r >> 4)) * 32 + (r & 7) * 4 + (c >> 1))[((r >> 3) & 1) + 2 * (e & 1)] = pr[e];
-      }
+      // lane (row % 8, c / 2); k-steps 4 (c % 2) .. + 3: (pair 0, pair 1) each, two steps a uint4
+      uint4* dst = qf + (2 * (c & 1) * NT + (r >> 3)) * 32 + (r & 7) * 4 + (c >> 1);
+      dst[0] = x0;
+      dst[NT * 32] = x1;
       if (c == 0) {
         rowc[r] = back;
         mask[r] = real ? a.mask[(size_t)w.b * a.N + r / rep] : 0ull;
       }
     }
     __syncthreads();  // queries staged (and, the first time, the barriers)
-    float m[MT][2], top[MT][2], l[MT][2], cs[MT][2];  // of rows 16 mt + n8, + 8: maximum - kRaise, + kSlack, sum, scale
-    float o[MT][16][4];
+    float m[NT][2], top[NT][2], l[NT][2], cs[NT][2];  // of rows 8 nt + 2 q, + 1: maximum - kRaise, + kSlack, sum, scale
+    float o[NT][8][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[mt][e] = top[mt][e] = -FLT_MAX;
-        l[mt][e] = 0.f;
-        cs[mt][e] = rowc[16 * mt + n8 + 8 * e];
+        m[nt][e] = top[nt][e] = -FLT_MAX;
+        l[nt][e] = 0.f;
+        cs[nt][e] = rowc[8 * nt + 2 * q4 + e];
       }
 #pragma unroll
-      for (int t = 0; t < 16; ++t)
+      for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.f;
     }
     const int i_first = i, tile_first = w.tile;
     const int i_end = min(n, i + w.len.tiles - w.tile);
@@ -419,20 +430,19 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
       const int tw = (tile_first + i - i_first) * kTile + 32 * warp;  // the warp's first token
       wait(&full[st], (i / kSt) & 1);
       if (tw < w.len.n + w.len.nd) {
-        // ---- scores: 4 tiles of 8 tokens ----
-        float s[MT][4][4];
+        // ---- scores: 2 tiles of 16 tokens ----
+        float s[NT][2][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][t][e] = 0.f;
-        const int tcol = n8 ^ ((n8 >> 2) & 1);  // the lane's token of each score tile
+            for (int e = 0; e < 4; ++e) s[nt][t][e] = 0.f;
         if (tw < w.len.nqk) {
-          uint32_t u[4][KB];  // code words of the lane's 32 channels, four tokens
+          uint32_t u[4][KB];  // code words of the lane's 32 channels, four tokens (octets of the group)
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const unsigned char* p = stage + (32 * warp + 8 * t + tcol) * S::kKRow + q4 * (4 * KB);
+            const unsigned char* p = stage + (32 * warp + 8 * t + tok8) * S::kKRow + q4 * (4 * KB);
             if constexpr (KB == 2) {
               const uint2 v = *reinterpret_cast<const uint2*>(p);
               u[t][0] = v.x;
@@ -463,19 +473,27 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
               }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 af[MT];
+            for (int k2 = 0; k2 < 2; ++k2) {
+              uint4 bq[NT];
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) af[mt] = qf[((4 * hw + k) * MT + mt) * 32 + lane];
+              for (int nt = 0; nt < NT; ++nt) bq[nt] = qf[((2 * hw + k2) * NT + nt) * 32 + lane];
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                // pairs 2 k, 2 k + 1 of the 16 channels
-                const uint32_t cw = (KB == 2) ? u[t][hw] : u[t][2 * hw + (k >> 1)];
-                const int j = (KB == 2) ? 2 * k : 2 * (k & 1);
-                const uint32_t b0 = dequant_h2(code_h2<KB>(cw, j), as_h2(sc[2 * k]), as_h2(nz[2 * k]));
-                const uint32_t b1 = dequant_h2(code_h2<KB>(cw, j + 1), as_h2(sc[2 * k + 1]), as_h2(nz[2 * k + 1]));
+              for (int kk = 0; kk < 2; ++kk) {
+                const int k = 2 * k2 + kk;  // pairs 2 k, 2 k + 1 of the 16 channels
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma_f16(s[mt][t], af[mt], b0, b1);
+                for (int t = 0; t < 2; ++t) {
+                  uint32_t af[4];
+#pragma unroll
+                  for (int oc = 0; oc < 2; ++oc) {
+                    const uint32_t cw = (KB == 2) ? u[2 * t + oc][hw] : u[2 * t + oc][2 * hw + (k >> 1)];
+                    const int j = (KB == 2) ? 2 * k : 2 * (k & 1);
+                    af[oc] = dequant_h2(code_h2<KB>(cw, j), as_h2(sc[2 * k]), as_h2(nz[2 * k]));
+                    af[2 + oc] = dequant_h2(code_h2<KB>(cw, j + 1), as_h2(sc[2 * k + 1]), as_h2(nz[2 * k + 1]));
+                  }
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(s[nt][t], af[0], af[1], af[2], af[3], kk ? bq[nt].z : bq[nt].x, kk ? bq[nt].w : bq[nt].y);
+                }
               }
             }
           }
@@ -487,79 +505,81 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
             for (int t = 0; t < 4; ++t)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                x[t][e] = fp16_key8(a, w.len, w.b, h, tw + 8 * t + tcol, 4 * q4 + 2 * hw + e);
+                x[t][e] = fp16_key8(a, w.len, w.b, h, tw + 8 * t + tok8, 4 * q4 + 2 * hw + e);
+            uint32_t pr[4][8];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               uint4 x0, x1;
               pair_order<KB>(x[t][0], x[t][1], x0, x1);
-              const uint32_t pr[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                  mma_f16(s[mt][t], qf[((4 * hw + k) * MT + mt) * 32 + lane], pr[2 * k], pr[2 * k + 1]);
+              pr[t][0] = x0.x; pr[t][1] = x0.y; pr[t][2] = x0.z; pr[t][3] = x0.w;
+              pr[t][4] = x1.x; pr[t][5] = x1.y; pr[t][6] = x1.z; pr[t][7] = x1.w;
             }
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint4 bq = qf[((2 * hw + k2) * NT + nt) * 32 + lane];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  mma_f16(s[nt][t], pr[2 * t][4 * k2], pr[2 * t + 1][4 * k2], pr[2 * t][4 * k2 + 1], pr[2 * t + 1][4 * k2 + 1], bq.x, bq.y);
+                  mma_f16(s[nt][t], pr[2 * t][4 * k2 + 2], pr[2 * t + 1][4 * k2 + 2], pr[2 * t][4 * k2 + 3], pr[2 * t + 1][4 * k2 + 3], bq.z, bq.w);
+                }
+              }
           }
         }
         // ---- softmax. x = s c is rounded before the maximum is taken from it, so that the largest score's
-        //      weight is exact however large it is. Element e of tile t: row + 8 (e / 2), column 2 q4 + e % 2 ----
+        //      weight is exact however large it is. Element e of tile t: octet 2 t + e / 2, row 2 q + e % 2 ----
         const bool plain = tw + 32 <= w.len.n;
         bool over = false;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x = __fmul_rn(s[mt][t][e], cs[mt][e >> 1]);
+              float x = __fmul_rn(s[nt][t][e], cs[nt][e & 1]);
               if (!plain) {
-                const int col = 2 * q4 + (e & 1), dj = tw + 8 * t + (col ^ ((col >> 2) & 1)) - w.len.n;
-                if (dj >= 0 && (dj >= w.len.nd || !((mask[16 * mt + n8 + 8 * (e >> 1)] >> dj) & 1ull))) x = -INFINITY;
+                const int dj = tw + 8 * (2 * t + (e >> 1)) + tok8 - w.len.n;
+                if (dj >= 0 && (dj >= w.len.nd || !((mask[8 * nt + 2 * q4 + (e & 1)] >> dj) & 1ull))) x = -INFINITY;
               }
-              s[mt][t][e] = x;
-              over = over || x > top[mt][e >> 1];
+              s[nt][t][e] = x;
+              over = over || x > top[nt][e & 1];
             }
         if (__any_sync(0xFFFFFFFFu, over)) {
           // raise the maxima of the rows with a score past them
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = -INFINITY;
+              float mx = fmaxf(fmaxf(s[nt][0][e], s[nt][0][2 + e]), fmaxf(s[nt][1][e], s[nt][1][2 + e]));
 #pragma unroll
-              for (int t = 0; t < 4; ++t) mx = fmaxf(mx, fmaxf(s[mt][t][2 * e], s[mt][t][2 * e + 1]));
-              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-              if (mx > top[mt][e]) {
-                const float f = exp2_approx(m[mt][e] - (mx - kRaise));
-                m[mt][e] = mx - kRaise;
-                top[mt][e] = mx + kSlack;
-                l[mt][e] *= f;
+              for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+              if (mx > top[nt][e]) {
+                const float f = exp2_approx(m[nt][e] - (mx - kRaise));
+                m[nt][e] = mx - kRaise;
+                top[nt][e] = mx + kSlack;
+                l[nt][e] *= f;
 #pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                  o[mt][t][2 * e] *= f;
-                  o[mt][t][2 * e + 1] *= f;
+                for (int t = 0; t < 8; ++t) {
+                  o[nt][t][e] *= f;
+                  o[nt][t][2 + e] *= f;
                 }
               }
             }
         }
-        uint4 pf[MT][2];  // weights: A fragments of the two 16-token steps
+        uint32_t pf[NT][4];  // weights: B fragments of the two 16-token steps
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t pr[4][2];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p0 = exp2_approx(s[mt][t][2 * e] - m[mt][e]), p1 = exp2_approx(s[mt][t][2 * e + 1] - m[mt][e]);
-              l[mt][e] += p0 + p1;
-              pr[t][e] = pack_h2(p0, p1);
+            for (int oc = 0; oc < 2; ++oc) {
+              const float p0 = exp2_approx(s[nt][t][2 * oc] - m[nt][0]), p1 = exp2_approx(s[nt][t][2 * oc + 1] - m[nt][1]);
+              l[nt][0] += p0;
+              l[nt][1] += p1;
+              pf[nt][2 * t + oc] = transpose8(pack_h2(p0, p1));
             }
-          pf[mt][0] = make_uint4(pr[0][0], pr[0][1], pr[1][0], pr[1][1]);
-          pf[mt][1] = make_uint4(pr[2][0], pr[2][1], pr[3][0], pr[3][1]);
-        }
-        // ---- values: step k takes token columns 2 q4, 2 q4 + 1 of score tiles 2 k, 2 k + 1 ----
-        const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);
+        // ---- values: token pairs at places 2 q, 2 q + 1 of the four octets ----
         if (tw + 32 <= w.len.nqv) {
           const uint16_t* sp = reinterpret_cast<const uint16_t*>(stage + S::kVs) + 32 * warp * 4 + (n8 >> 1);
           const uint16_t* zp = reinterpret_cast<const uint16_t*>(stage + S::kVz) + 32 * warp * 4 + (n8 >> 1);
@@ -589,19 +609,24 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
 #pragma unroll
             for (int t = 0; t < 4; ++t) x[t] = __byte_perm(wa[t][hw >> 1], wb[t][hw >> 1], (hw & 1) ? 0x7632 : 0x5410);
 #pragma unroll
-            for (int c = 0; c < kCodes; ++c)
+            for (int c = 0; c < kCodes; c += 2)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t b0 = dequant_h2(code_h2<VB>(x[2 * k], c), as_h2(sv[2 * k]), as_h2(nz[2 * k]));
-                const uint32_t b1 = dequant_h2(code_h2<VB>(x[2 * k + 1], c), as_h2(sv[2 * k + 1]), as_h2(nz[2 * k + 1]));
+                uint32_t af[4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][hw * kCodes + c], pf[mt][k], b0, b1);
+                for (int oc = 0; oc < 2; ++oc)
+#pragma unroll
+                  for (int f = 0; f < 2; ++f)
+                    af[2 * oc + f] = dequant_h2(code_h2<VB>(x[2 * k + oc], c + f), as_h2(sv[2 * k + oc]), as_h2(nz[2 * k + oc]));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(o[nt][(hw * kCodes + c) / 2], af[0], af[1], af[2], af[3], pf[nt][2 * k], pf[nt][2 * k + 1]);
               }
           }
         } else {  // fp16 rows, and the group in which the quantized values end
 #pragma unroll 1
           for (int hw = 0; hw < 2; ++hw) {  // channels 16 n8 + 8 hw .. + 7
-            uint32_t x[8][4];  // tokens (t, a), (t, b)
+            uint32_t x[8][4];  // octet y / 2, place 2 q + y % 2
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const int tt = 8 * (y >> 1) + ((y & 1) ? cb : ca);
@@ -618,27 +643,34 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
               x[y][1] = v.y;
               x[y][2] = v.z;
               x[y][3] = v.w;
-              if (tw + tt >= w.len.n) {
-                // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
-                // every row's weight, 0 for the others: one that is not finite is taken as 0 and added at the
-                // end to the rows that see it.
-                bool any = false;
+            }
+            if (!plain) {
+              // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
+              // every row's weight, 0 for the others: one that is not finite is taken as 0 and added at the
+              // end to the rows that see it.
 #pragma unroll
-                for (int e = 0; e < 4; ++e) any |= drop_nonfinite(x[y][e]);
-                if (any) *nonfinite = 1;
-              }
+              for (int y = 0; y < 8; ++y)
+                if (tw + 8 * (y >> 1) + ((y & 1) ? cb : ca) >= w.len.n) {
+                  bool any = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) any |= drop_nonfinite(x[y][e]);
+                  if (any) *nonfinite = 1;
+                }
             }
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
+            for (int c = 0; c < 4; ++c)  // channels 2 c, 2 c + 1 of the eight
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const int sel = (c & 1) ? 0x7632 : 0x5410;
-                const uint32_t b0 = __byte_perm(x[4 * k][c >> 1], x[4 * k + 1][c >> 1], sel);
-                const uint32_t b1 = __byte_perm(x[4 * k + 2][c >> 1], x[4 * k + 3][c >> 1], sel);
+                uint32_t af[4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  if (hw == 0) mma_f16(o[mt][c], pf[mt][k], b0, b1);
-                  else mma_f16(o[mt][8 + c], pf[mt][k], b0, b1);
+                for (int oc = 0; oc < 2; ++oc)
+#pragma unroll
+                  for (int f = 0; f < 2; ++f)
+                    af[2 * oc + f] = __byte_perm(x[4 * k + 2 * oc][c], x[4 * k + 2 * oc + 1][c], f ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (hw == 0) mma_f16(o[nt][c], af[0], af[1], af[2], af[3], pf[nt][2 * k], pf[nt][2 * k + 1]);
+                  else mma_f16(o[nt][4 + c], af[0], af[1], af[2], af[3], pf[nt][2 * k], pf[nt][2 * k + 1]);
                 }
               }
           }
@@ -658,61 +690,60 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
     const bool last = t_end == w.len.tiles, earlier = tile_first > 0 && i_first == 0;
     const bool whole = last && !earlier;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[mt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][e], 1);
-        l[mt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][e], 2);
-        if (q4 == 0) ml[warp * kRows + 16 * mt + n8 + 8 * e] = make_float2(m[mt][e], l[mt][e]);
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], off);
+        if (n8 == 0) ml[warp * kRows + 8 * nt + 2 * q4 + e] = make_float2(m[nt][e], l[nt][e]);
       }
     __syncthreads();
     // every warp's sums against the block's maximum; warps 2, 3 hand theirs to 0, 1, then 1 to 0
-    float ms[MT][2], lt[MT][2];
+    float ms[NT][2], lt[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 16 * mt + n8 + 8 * e;
+        const int r = 8 * nt + 2 * q4 + e;
         float2 v[kMmaWarps];
 #pragma unroll
         for (int k = 0; k < kMmaWarps; ++k) v[k] = ml[k * kRows + r];
-        ms[mt][e] = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-        lt[mt][e] = 0.f;
+        ms[nt][e] = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+        lt[nt][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < kMmaWarps; ++k)
-          if (v[k].y != 0.f) lt[mt][e] += v[k].y * exp2_approx(v[k].x - ms[mt][e]);  // 0: the row saw nothing there
-        const float f = l[mt][e] == 0.f ? 0.f : exp2_approx(m[mt][e] - ms[mt][e]);
+          if (v[k].y != 0.f) lt[nt][e] += v[k].y * exp2_approx(v[k].x - ms[nt][e]);  // 0: the row saw nothing there
+        const float f = l[nt][e] == 0.f ? 0.f : exp2_approx(m[nt][e] - ms[nt][e]);
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          o[mt][t][2 * e] = f == 0.f ? 0.f : o[mt][t][2 * e] * f;
-          o[mt][t][2 * e + 1] = f == 0.f ? 0.f : o[mt][t][2 * e + 1] * f;
+        for (int t = 0; t < 8; ++t) {
+          o[nt][t][e] = f == 0.f ? 0.f : o[nt][t][e] * f;
+          o[nt][t][2 + e] = f == 0.f ? 0.f : o[nt][t][2 + e] * f;
         }
       }
 #pragma unroll
     for (int half = 2; half >= 1; half >>= 1) {
-      // [sender][mt][t][e][lane]
       if (warp >= half && warp < 2 * half) {
         float* dst = osum + (warp - half) * kRows * kD + lane;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int t = 0; t < 16; ++t)
+          for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[((mt * 16 + t) * 4 + e) * 32] = o[mt][t][e];
+            for (int e = 0; e < 4; ++e) dst[((nt * 8 + t) * 4 + e) * 32] = o[nt][t][e];
       }
       __syncthreads();
       if (warp < half) {
         const float* src = osum + warp * kRows * kD + lane;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int t = 0; t < 16; ++t)
+          for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][t][e] += src[((mt * 16 + t) * 4 + e) * 32];
+            for (int e = 0; e < 4; ++e) o[nt][t][e] += src[((nt * 8 + t) * 4 + e) * 32];
       }
       __syncthreads();
     }
-    if (warp == 0) {  // rows 16 mt + n8 + 8 e, channels 32 q4 + 16 f + t
+    if (warp == 0) {  // rows 8 nt + 2 q + e, channels 16 n + 0 .. 15: o[nt][c / 2][e + 2 (c % 2)]
       if (earlier) sh.first = last ? 2 : 1;
       else if (!last) {
         sh.open = w.b * seg_per_b + w.seg;
@@ -721,58 +752,51 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, MT>::kBlocks)
       float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<kRows>();
       const bool fix = *nonfinite != 0;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 16 * mt + n8 + 8 * e, di = r / rep;
+          const int r = 8 * nt + 2 * q4 + e, di = r / rep;
           if (r >= rows_all || di >= w.len.nd) continue;  // padding
+          float v[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] = o[nt][c >> 1][e + 2 * (c & 1)];
           if (fix) {  // of the drafted tokens in this block's tiles
             const int j1 = min(w.len.nd, t_end * kTile - w.len.n);
+#pragma unroll 1
             for (int j = max(0, tile_first * kTile - w.len.n); j < j1; ++j) {
               if (!((mask[r] >> j) & 1ull)) continue;
-              const uint16_t* v = a.v_draft + (((size_t)w.b * a.N + j) * a.H + h) * kD + 32 * q4;
+              const uint16_t* d = a.v_draft + (((size_t)w.b * a.N + j) * a.H + h) * kD + 16 * n8;
 #pragma unroll
-              for (int t = 0; t < 16; ++t) {
-                if ((v[t] & 0x7C00u) == 0x7C00u) o[mt][t][2 * e] += th2f(v[t]);
-                if ((v[16 + t] & 0x7C00u) == 0x7C00u) o[mt][t][2 * e + 1] += th2f(v[16 + t]);
-              }
+              for (int c = 0; c < 16; ++c)
+                if ((d[c] & 0x7C00u) == 0x7C00u) v[c] += th2f(d[c]);
             }
           }
-          const float ls = lt[mt][e];
-          const bool some = ls > 0.f || ls != ls;
+          const float ls = lt[nt][e];
           if (whole) {
-            const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r % rep) * kD + 32 * q4;
+            const bool some = ls > 0.f || ls != ls;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = some ? v[c] / ls : 0.f;
+            const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r % rep) * kD + 16 * n8;
             if (a.out_fp32) {
-              float* p = reinterpret_cast<float*>(a.out) + at;
+              float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
 #pragma unroll
-              for (int f = 0; f < 2; ++f)
-#pragma unroll
-                for (int t = 0; t < 16; t += 4)
-                  *reinterpret_cast<float4*>(p + 16 * f + t) =
-                      some ? make_float4(o[mt][t][2 * e + f] / ls, o[mt][t + 1][2 * e + f] / ls, o[mt][t + 2][2 * e + f] / ls, o[mt][t + 3][2 * e + f] / ls)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int c = 0; c < 4; ++c) p[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
             } else {
-              uint16_t* p = reinterpret_cast<uint16_t*>(a.out) + at;
+              uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
 #pragma unroll
-              for (int f = 0; f < 2; ++f)
+              for (int c = 0; c < 2; ++c) {
+                uint32_t u[4];
 #pragma unroll
-                for (int t = 0; t < 16; t += 8) {
-                  uint32_t u[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    u[k] = some ? f32_to_bf16(o[mt][t + 2 * k][2 * e + f] / ls) | ((uint32_t)f32_to_bf16(o[mt][t + 2 * k + 1][2 * e + f] / ls) << 16) : 0u;
-                  *reinterpret_cast<uint4*>(p + 16 * f + t) = make_uint4(u[0], u[1], u[2], u[3]);
-                }
+                for (int k = 0; k < 4; ++k) u[k] = f32_to_bf16(v[8 * c + 2 * k]) | ((uint32_t)f32_to_bf16(v[8 * c + 2 * k + 1]) << 16);
+                p[c] = make_uint4(u[0], u[1], u[2], u[3]);
+              }
             }
           } else {
-            float* p = slot + (size_t)r * kD + 32 * q4;
+            float4* p = reinterpret_cast<float4*>(slot + (size_t)r * kD + 16 * n8);
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-              for (int t = 0; t < 16; t += 4)
-                *reinterpret_cast<float4*>(p + 16 * f + t) = make_float4(o[mt][t][2 * e + f], o[mt][t + 1][2 * e + f], o[mt][t + 2][2 * e + f], o[mt][t + 3][2 * e + f]);
-            if (q4 == 0) {
-              slot[(size_t)kRows * kD + r] = ms[mt][e];
+            for (int c = 0; c < 4; ++c) p[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            if (n8 == 0) {
+              slot[(size_t)kRows * kD + r] = ms[nt][e];
               slot[(size_t)kRows * kD + kRows + r] = ls;
             }
           }
@@ -1411,9 +1435,9 @@ __global__ void __launch_bounds__(kMergeThreads) kivi_tree_merge_kernel(const Ki
   }
 }
 
-// Rows of a tile, which also choose the kernel: up to 32 rows the warp-wide products (16 or 32 rows), else tcgen05 on
-// tiles of 64.
-int tree_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows of a tile, which also choose the kernel: up to 32 rows the warp-wide products (8, 16 or 32 rows), else tcgen05
+// on tiles of 64.
+int tree_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 int sm_count_tree() {
   static int cached[64] = {};
   int dev = 0, sms = 148;
@@ -1421,7 +1445,11 @@ int sm_count_tree() {
   if (cached[dev] == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) cached[dev] = sms;
   return cached[dev] ? cached[dev] : sms;
 }
-int tree_blocks(int r) { return sm_count_tree() * (r == 16 ? 3 : 2); }  // resident blocks
+// resident blocks
+int tree_blocks(int r, int bits) {
+  return sm_count_tree() * (r == 8 ? (bits == 4 ? MmaLayout<2, 2, 1>::kBlocks : MmaLayout<4, 4, 1>::kBlocks)
+                                   : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
+}
 
 template <int ROWS>
 cudaError_t launch_merge(const KiviTreeArgs& a, int G, cudaStream_t st) {
@@ -1440,7 +1468,7 @@ template <int ROWS, typename K>
 cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int G = tree_blocks(ROWS);
+  const int G = tree_blocks(ROWS, a.k_bits + a.v_bits);
   kernel<<<G, threads, smem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_merge<ROWS>(a, G, st);
@@ -1448,8 +1476,9 @@ cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& a, 
 template <int KB, int VB>
 cudaError_t launch_tree_rows(const KiviTreeArgs& a, cudaStream_t st) {
   const int r = tree_rows(a.N * (a.Hq / a.H));
-  if (r == 16) return launch_with<16>(kivi_tree_mma_kernel<KB, VB, 1>, kMmaThreads, MmaLayout<KB, VB, 1>::kSmem, a, st);
-  if (r == 32) return launch_with<32>(kivi_tree_mma_kernel<KB, VB, 2>, kMmaThreads, MmaLayout<KB, VB, 2>::kSmem, a, st);
+  if (r == 8) return launch_with<8>(kivi_tree_mma_kernel<KB, VB, 1>, kMmaThreads, MmaLayout<KB, VB, 1>::kSmem, a, st);
+  if (r == 16) return launch_with<16>(kivi_tree_mma_kernel<KB, VB, 2>, kMmaThreads, MmaLayout<KB, VB, 2>::kSmem, a, st);
+  if (r == 32) return launch_with<32>(kivi_tree_mma_kernel<KB, VB, 4>, kMmaThreads, MmaLayout<KB, VB, 4>::kSmem, a, st);
   return launch_with<64>(kivi_tree_kernel<KB, VB, 64>, kTreeThreads, TreeLayout<KB, VB, 64>::kSmem, a, st);
 }
 
@@ -1457,7 +1486,7 @@ cudaError_t launch_tree_rows(const KiviTreeArgs& a, cudaStream_t st) {
 
 size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits) {
   const int r = tree_rows(N * (Hq / H));
-  return (size_t)tree_blocks(r) * (sizeof(TreeShared) + 2 * r * (kD + 2) * sizeof(float));
+  return (size_t)tree_blocks(r, k_bits + v_bits) * (sizeof(TreeShared) + 2 * r * (kD + 2) * sizeof(float));
 }
 long long kivi_tree_positions(int B, int N, int H, int Hq, int max_tokens, int residual) {
   const int rows = N * (Hq / H), r = tree_rows(rows);
