@@ -173,15 +173,32 @@ __device__ __forceinline__ int token_place(int t) { return t ^ ((t >> 3) & 1); }
 
 __device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 __device__ __forceinline__ uint32_t as_u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+// Constants of the unpacking, held in registers, since an instruction has room for one immediate: the exponent of
+// 2^10 in both halves (mask and insert are then one instruction), and the powers of two that bring codes unpacked in
+// place back to their value.
+struct CodeScale {
+  uint32_t magic;
+  uint32_t p[4];  // 2^-2, 2^-4, 2^-6, 2^-8 as packed halves
+  __device__ __forceinline__ CodeScale() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+    asm volatile("mov.b32 %0, 0x34003400;" : "=r"(p[0]));
+    asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(p[1]));
+    asm volatile("mov.b32 %0, 0x24002400;" : "=r"(p[2]));
+    asm volatile("mov.b32 %0, 0x1C001C00;" : "=r"(p[3]));
+  }
+};
 // Code j of both halves of w as fp16 (exact): masked in place under the exponent of 2^10, where it stands for
 // 1024 + c 2^(b j), and scaled back by one FMA. Codes above the ten mantissa bits come from w shifted right.
 template <int BITS>
-__device__ __forceinline__ __half2 code_h2(uint32_t w, int j) {
+__device__ __forceinline__ __half2 code_h2(const CodeScale& cs, uint32_t w, int j) {
   constexpr int kIn = (BITS == 2) ? 5 : 2;  // codes that fit in place
-  const int jj = j < kIn ? j : j - kIn;
-  const uint32_t m = ((j < kIn ? w : w >> (BITS * kIn)) & ((((1u << BITS) - 1u) << (BITS * jj)) * 0x10001u)) | 0x64006400u;
-  const float p = 1.f / (float)(1 << (BITS * jj));
-  return __hfma2(as_h2(m), __float2half2_rn(p), __float2half2_rn(-1024.f * p));
+  const int jj = j < kIn ? j : j - kIn, k = BITS * jj / 2;
+  uint32_t m;  // (w & mask) | magic
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+      : "=r"(m)
+      : "r"(j < kIn ? w : w >> (BITS * kIn)), "r"((((1u << BITS) - 1u) << (BITS * jj)) * 0x10001u), "r"(cs.magic));
+  if (k == 0) return __hadd2(as_h2(m), __float2half2_rn(-1024.f));
+  return __hfma2(as_h2(m), as_h2(cs.p[k - 1]), __float2half2_rn(-1024.f / (float)(1 << (2 * k))));
 }
 // s c - s z, one rounding of s z and one of the result
 __device__ __forceinline__ uint32_t dequant_h2(__half2 c, __half2 s, __half2 nsz) { return as_u(__hfma2(c, s, nsz)); }
@@ -296,7 +313,7 @@ struct MmaLayout {
   using S = StageLayout<KB, VB>;
   static constexpr int kRows = 8 * NT;
   // resident blocks the registers (32 NT sums a thread) and the shared memory leave room for
-  static constexpr int kBlocks = (NT == 1) ? ((KB + VB == 4) ? 5 : 4) : (NT == 2) ? 3 : 2;
+  static constexpr int kBlocks = (NT == 1) ? 4 : (NT == 2) ? 3 : 2;
   static constexpr int kStages = 2;
   static constexpr int kOffQ = kStages * S::kBytes;                 // uint4 [4][NT][32 lanes]: B fragments of two k-steps
   static constexpr int kOffO = kOffQ + 4 * NT * 32 * 16;            // float [2][kRows][128]: sums on their way to a warp
@@ -304,7 +321,8 @@ struct MmaLayout {
   static constexpr int kOffMask = kOffMl + kMmaWarps * kRows * 8;   // uint64 [kRows]
   static constexpr int kOffC = kOffMask + kRows * 8;                // float [kRows]: log2 units per score unit
   static constexpr int kOffBar = kOffC + kRows * 4;                 // mbarriers, flags
-  static constexpr int kSmem = kOffBar + 128;
+  static constexpr int kOffAhead = kOffBar + 128;                   // the copying thread's place
+  static constexpr int kSmem = kOffAhead + 64;
   static_assert(kSmem <= 232448 / kBlocks - 1024, "blocks per SM");
 };
 
@@ -315,6 +333,17 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -352,8 +381,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     if (tid == 0) shared[blockIdx.x] = sh;
     return;
   }
-  Walk ahead = w;      // thread 0: the next tile to copy
-  int copied = 0;      // tiles whose copies were issued
+  Walk& ahead = *reinterpret_cast<Walk*>(sm + L::kOffAhead);  // thread 0: the next tile to copy (kept out of registers)
+  int copied = 0;                                              // tiles whose copies were issued
   auto produce = [&]() {
     unsigned char* stage = sm + (copied % kSt) * S::kBytes;
     const size_t bh = (size_t)ahead.b * a.H + ahead.seg;
@@ -372,6 +401,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       set_error(a.err, KVQ_ERR_TIMEOUT);
     }
   };
+  auto refill_due = [&](int i) { return tid == 0 && i > 0 && copied < n && copied < i + kSt; };
   if (tid == 0) {
     for (int i = 0; i < kSt; ++i) {
       mbar_init(&full[i], 2);
@@ -379,9 +409,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     }
     *failed = 0;
     *nonfinite = 0;
+    ahead = w;
     fence_mbar_init();
     for (int i = 0; i < min(kSt, n); ++i) produce();
   }
+  const CodeScale cs0;
   const int tok8 = n8 ^ ((n8 >> 2) & 1);                                       // the token at place n of eight
   const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);  // at places 2 q, 2 q + 1
 
@@ -428,6 +460,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       const int st = i % kSt;
       const unsigned char* stage = sm + st * S::kBytes;
       const int tw = (tile_first + i - i_first) * kTile + 32 * warp;  // the warp's first token
+      // the stage of the tile before takes the next copies as soon as all warps are done with it
+      if (refill_due(i) && mbar_test(&empty[(i - 1) % kSt], ((i - 1) / kSt) & 1)) produce();
       wait(&full[st], (i / kSt) & 1);
       if (tw < w.len.n + w.len.nd) {
         // ---- scores: 2 tiles of 16 tokens ----
@@ -487,8 +521,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
                   for (int oc = 0; oc < 2; ++oc) {
                     const uint32_t cw = (KB == 2) ? u[2 * t + oc][hw] : u[2 * t + oc][2 * hw + (k >> 1)];
                     const int j = (KB == 2) ? 2 * k : 2 * (k & 1);
-                    af[oc] = dequant_h2(code_h2<KB>(cw, j), as_h2(sc[2 * k]), as_h2(nz[2 * k]));
-                    af[2 + oc] = dequant_h2(code_h2<KB>(cw, j + 1), as_h2(sc[2 * k + 1]), as_h2(nz[2 * k + 1]));
+                    af[oc] = dequant_h2(code_h2<KB>(cs0, cw, j), as_h2(sc[2 * k]), as_h2(nz[2 * k]));
+                    af[2 + oc] = dequant_h2(code_h2<KB>(cs0, cw, j + 1), as_h2(sc[2 * k + 1]), as_h2(nz[2 * k + 1]));
                   }
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt)
@@ -527,6 +561,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               }
           }
         }
+        if (refill_due(i) && mbar_test(&empty[(i - 1) % kSt], ((i - 1) / kSt) & 1)) produce();
         // ---- softmax. x = s c is rounded before the maximum is taken from it, so that the largest score's
         //      weight is exact however large it is. Element e of tile t: octet 2 t + e / 2, row 2 q + e % 2 ----
         const bool plain = tw + 32 <= w.len.n;
@@ -617,7 +652,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
                 for (int oc = 0; oc < 2; ++oc)
 #pragma unroll
                   for (int f = 0; f < 2; ++f)
-                    af[2 * oc + f] = dequant_h2(code_h2<VB>(x[2 * k + oc], c + f), as_h2(sv[2 * k + oc]), as_h2(nz[2 * k + oc]));
+                    af[2 * oc + f] = dequant_h2(code_h2<VB>(cs0, x[2 * k + oc], c + f), as_h2(sv[2 * k + oc]), as_h2(nz[2 * k + oc]));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma_f16(o[nt][(hw * kCodes + c) / 2], af[0], af[1], af[2], af[3], pf[nt][2 * k], pf[nt][2 * k + 1]);
@@ -678,8 +713,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
-      // the stage of the tile before takes the next copies once all warps are done with it
-      if (tid == 0 && i > 0 && copied < n && copied < i + kSt) {
+      if (refill_due(i)) {  // at the latest now
         wait(&empty[(i - 1) % kSt], ((i - 1) / kSt) & 1);
         if (!*failed) produce();
       }
@@ -898,7 +932,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
 //      a warp one key group and half of the words, so a lane unpacks four tokens per scale. Groups behind the
 //      quantized keys are fp16 rows. ----
 template <int KB>
-__device__ __forceinline__ void unpack_keys(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
+__device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
                                             const unsigned char* codes, const unsigned char* scale,
                                             const unsigned char* zero, unsigned char* dst0, int warp, int lane) {
   constexpr int kRow = kD * KB / 8;
@@ -932,7 +966,7 @@ __device__ __forceinline__ void unpack_keys(const KiviTreeArgs& a, const TreeLen
         const int t = tok + 8 * i;
         uint32_t o[kPairs];
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) o[j] = dequant_h2(code_h2<KB>(u[i], j), s[j], nsz[j]);
+        for (int j = 0; j < kPairs; ++j) o[j] = dequant_h2(code_h2<KB>(cs0, u[i], j), s[j], nsz[j]);
         unsigned char* dst = dst0 + (t >> 3) * 2048 + w * (kPairs * 32) + (t & 7) * 16;
         *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
         if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -961,7 +995,7 @@ __device__ __forceinline__ void unpack_keys(const KiviTreeArgs& a, const TreeLen
 // ---- values of a tile, transposed. A thread takes a token octet and eight channels; octets with tokens behind
 //      the quantized values mix stored tokens and fp16 rows ----
 template <int VB>
-__device__ __forceinline__ void unpack_values(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
+__device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
                                               const unsigned char* codes, const unsigned char* scale,
                                               const unsigned char* zero, unsigned char* dst0, int* nonfinite, int warp,
                                               int lane) {
@@ -991,7 +1025,7 @@ __device__ __forceinline__ void unpack_values(const KiviTreeArgs& a, const TreeL
       for (int e = 0; e < 8; ++e) {
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<2>(x[i], e), s[i], nsz[i]);
+        for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<2>(cs0, x[i], e), s[i], nsz[i]);
         *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     } else {
@@ -1004,7 +1038,7 @@ __device__ __forceinline__ void unpack_values(const KiviTreeArgs& a, const TreeL
         for (int e = 0; e < 4; ++e) {
           uint32_t o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<4>(x[i], e), s[i], nsz[i]);
+          for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<4>(cs0, x[i], e), s[i], nsz[i]);
           *reinterpret_cast<uint4*>(dst + (4 * hw + e) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
@@ -1120,6 +1154,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   constexpr int kHR = ROWS / 2;                            // rows a thread works on
   const int r0 = half * kHR;
   uint32_t phase = 0;    // of the barriers: one completion each per tile
+  const CodeScale cs0;
   float l[kHR];
   bool first = true;    // of the segment's tiles in this block
   int tile_first = 0;   // that tile
@@ -1161,7 +1196,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       tile_first = tile;
     }
     wait(bar_k, phase);
-    unpack_keys<KB>(a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane);
+    unpack_keys<KB>(cs0, a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane);
     fence_proxy_async_smem();
     tmem_before();
     if (__syncthreads_or(*failed)) break;
@@ -1175,7 +1210,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       if (more) keys_of(nw);  // every thread has read this tile's
     }
     wait(bar_v, phase);
-    unpack_values<VB>(a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, nonfinite, warp, lane);
+    unpack_values<VB>(cs0, a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, nonfinite, warp, lane);
     wait(bar_s, phase);
     tmem_after();
     // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1. x = s c is rounded before the
@@ -1446,9 +1481,8 @@ int sm_count_tree() {
   return cached[dev] ? cached[dev] : sms;
 }
 // resident blocks
-int tree_blocks(int r, int bits) {
-  return sm_count_tree() * (r == 8 ? (bits == 4 ? MmaLayout<2, 2, 1>::kBlocks : MmaLayout<4, 4, 1>::kBlocks)
-                                   : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
+int tree_blocks(int r) {
+  return sm_count_tree() * (r == 8 ? MmaLayout<2, 2, 1>::kBlocks : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
 }
 
 template <int ROWS>
@@ -1468,7 +1502,7 @@ template <int ROWS, typename K>
 cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int G = tree_blocks(ROWS, a.k_bits + a.v_bits);
+  const int G = tree_blocks(ROWS);
   kernel<<<G, threads, smem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_merge<ROWS>(a, G, st);
@@ -1478,7 +1512,7 @@ cudaError_t launch_tree_rows(const KiviTreeArgs& a, cudaStream_t st) {
   const int r = tree_rows(a.N * (a.Hq / a.H));
   if (r == 8) return launch_with<8>(kivi_tree_mma_kernel<KB, VB, 1>, kMmaThreads, MmaLayout<KB, VB, 1>::kSmem, a, st);
   if (r == 16) return launch_with<16>(kivi_tree_mma_kernel<KB, VB, 2>, kMmaThreads, MmaLayout<KB, VB, 2>::kSmem, a, st);
-  if (r == 32) return launch_with<32>(kivi_tree_mma_kernel<KB, VB, 4>, kMmaThreads, MmaLayout<KB, VB, 4>::kSmem, a, st);
+  if (r == 32) return launch_with<32>(kivi_tree_kernel<KB, VB, 32>, kTreeThreads, TreeLayout<KB, VB, 32>::kSmem, a, st);
   return launch_with<64>(kivi_tree_kernel<KB, VB, 64>, kTreeThreads, TreeLayout<KB, VB, 64>::kSmem, a, st);
 }
 
@@ -1486,7 +1520,7 @@ cudaError_t launch_tree_rows(const KiviTreeArgs& a, cudaStream_t st) {
 
 size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits) {
   const int r = tree_rows(N * (Hq / H));
-  return (size_t)tree_blocks(r, k_bits + v_bits) * (sizeof(TreeShared) + 2 * r * (kD + 2) * sizeof(float));
+  return (size_t)tree_blocks(r) * (sizeof(TreeShared) + 2 * r * (kD + 2) * sizeof(float));
 }
 long long kivi_tree_positions(int B, int N, int H, int Hq, int max_tokens, int residual) {
   const int rows = N * (Hq / H), r = tree_rows(rows);
