@@ -37,14 +37,15 @@ constexpr float kSlack = 7.f;   // log2 by which a score may pass its row's runn
 constexpr float kRaise = 8.f;   // weights are exp2(x - m + kRaise) <= 2^15, held as fp16: one below 2^-32 of the
                                 // maximum's is lost instead of one below 2^-24
 
-// A tile as it is stored: key codes, scales and zeros [4 groups][128], value codes, scales and zeros [128][4]
-template <int KB, int VB>
+// TOK stored tokens (a key group or a tile): key codes, scales and zeros [groups][128], value codes, scales and
+// zeros [tokens][4]
+template <int KB, int VB, int TOK>
 struct StageLayout {
   static constexpr int kKRow = kD * KB / 8, kVRow = kD * VB / 8;   // code bytes per token
-  static constexpr int kKs = kTile * kKRow, kKz = kKs + (kTile / kGroupT) * kD * 2;
-  static constexpr int kVc = kKz + (kTile / kGroupT) * kD * 2;
-  static constexpr int kVs = kVc + kTile * kVRow, kVz = kVs + kTile * (kD / kGroupT) * 2;
-  static constexpr int kBytes = kVz + kTile * (kD / kGroupT) * 2;
+  static constexpr int kKs = TOK * kKRow, kKz = kKs + (TOK / kGroupT) * kD * 2;
+  static constexpr int kVc = kKz + (TOK / kGroupT) * kD * 2;
+  static constexpr int kVs = kVc + TOK * kVRow, kVz = kVs + TOK * (kD / kGroupT) * 2;
+  static constexpr int kBytes = kVz + TOK * (kD / kGroupT) * 2;
 };
 
 __device__ __forceinline__ float th2f(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
@@ -128,17 +129,26 @@ __device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b,
   return make_int2(p0, p1);
 }
 
-// channels 8c .. 8c+7 of a token behind the quantized ones: residual, drafted, or nothing (zero)
-__device__ __forceinline__ uint4 fp16_key8(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int c) {
-  const uint16_t* p = nullptr;
-  if (t < L.n) p = a.k_resid + (((size_t)b * a.H + h) * a.residual + (t - L.nqk)) * kD;
-  else if (t < L.n + L.nd) p = a.k_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
-  return p ? __ldg(reinterpret_cast<const uint4*>(p + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+// The row of a token behind the quantized ones (token t, value: of the ring): residual, drafted, or none
+__device__ __forceinline__ const uint16_t* fp16_key(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t) {
+  if (t < L.n) return a.k_resid + (((size_t)b * a.H + h) * a.residual + (t - L.nqk)) * kD;
+  if (t < L.n + L.nd) return a.k_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
+  return nullptr;
 }
-__device__ __forceinline__ uint4 fp16_value8(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int c) {
-  const uint16_t* p = nullptr;
-  if (t < L.n) p = a.v_resid + (((size_t)b * a.H + h) * a.residual + t % a.residual) * kD;
-  else if (t < L.n + L.nd) p = a.v_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
+// place: t % residual for a token that is cached
+__device__ __forceinline__ const uint16_t* fp16_value(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int place) {
+  if (t < L.n) return a.v_resid + (((size_t)b * a.H + h) * a.residual + place) * kD;
+  if (t < L.n + L.nd) return a.v_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
+  return nullptr;
+}
+// place of token t0 + i (i < 32) when t0's is p: the ring holds at least 32 rows, or none (no token is there then)
+__device__ __forceinline__ int ring_place(int p, int i, int R) {
+  p += i;
+  if (p >= R) p -= R;
+  return p;
+}
+// channels 8c .. 8c+7 of a row, zero without one
+__device__ __forceinline__ uint4 row8(const uint16_t* p, int c) {
   return p ? __ldg(reinterpret_cast<const uint4*>(p + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
 }
 // true where a half of w is infinite or NaN; those become 0
@@ -208,38 +218,59 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// The stored part of a tile into a stage: its quantized keys on kfull, its quantized values on vfull (one thread).
-// With nothing to copy the barrier completes at once.
-template <int KB, int VB>
-__device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
-                                          unsigned char* stage, uint64_t* full) {
-  using S = StageLayout<KB, VB>;
-  const int nk = min(kTile, len.nqk - t0);
-  if (nk <= 0) {
-    mbar_arrive(full);
-    return;
-  }
-  const size_t g = (bh * (a.max_tokens / kGroupT) + t0 / kGroupT) * kD;
-  const uint32_t gb = nk / kGroupT * kD * 2;
-  mbar_arrive_expect_tx(full, nk * S::kKRow + 2 * gb);
-  bulk_g2s(stage, a.k_codes + (bh * a.max_tokens + t0) * S::kKRow, nk * S::kKRow, full);
-  bulk_g2s(stage + S::kKs, a.k_scale + g, gb, full);
-  bulk_g2s(stage + S::kKz, a.k_zero + g, gb, full);
+__device__ __forceinline__ void cp_async16(unsigned char* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-template <int KB, int VB>
-__device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
-                                            unsigned char* stage, uint64_t* full) {
-  using S = StageLayout<KB, VB>;
-  const int nv = (min(kTile, len.nqv - t0) + 1) & ~1;  // whole 16-byte pieces
-  if (nv <= 0) {
-    mbar_arrive(full);
-    return;
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// The stored part of TOK tokens from t0 (a multiple of 32) into a stage, one 16-byte piece a thread at a time (thread i
+// of THREADS): the keys of whole groups below n_quant_k, the values of groups that have one below n_quant_v.
+template <int KB, int VB, int TOK, int THREADS>
+__device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
+                                          unsigned char* stage, int i) {
+  using S = StageLayout<KB, VB, TOK>;
+  const int nk = len.nqk - t0;  // of the TOK, a multiple of 32
+  const unsigned char* src = a.k_codes + (bh * a.max_tokens + t0) * S::kKRow;
+#pragma unroll
+  for (int x = i; x < TOK * S::kKRow / 16; x += THREADS)
+    if (x * 16 < nk * S::kKRow) cp_async16(stage + x * 16, src + x * 16);
+  const size_t g = (bh * (a.max_tokens / kGroupT) + t0 / kGroupT) * kD;
+  constexpr int kHalf = TOK / kGroupT * (kD / 8);  // pieces of scales, then of zeros
+#pragma unroll
+  for (int x = i; x < 2 * kHalf; x += THREADS) {
+    const int y = x < kHalf ? x : x - kHalf;
+    if (y / (kD / 8) * kGroupT < nk) cp_async16(stage + S::kKs + x * 16, (x < kHalf ? a.k_scale : a.k_zero) + g + y * 8);
   }
+}
+template <int KB, int VB, int TOK, int THREADS>
+__device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
+                                            unsigned char* stage, int i) {
+  using S = StageLayout<KB, VB, TOK>;
+  const int nv = (len.nqv - t0 + kGroupT - 1) / kGroupT * kGroupT;  // the rows behind n_quant_v are there, but not used
   const size_t tok = bh * a.max_tokens + t0;
-  mbar_arrive_expect_tx(full, nv * (S::kVRow + 16));
-  bulk_g2s(stage + S::kVc, a.v_codes + tok * S::kVRow, nv * S::kVRow, full);
-  bulk_g2s(stage + S::kVs, a.v_scale + tok * (kD / kGroupT), nv * 8, full);
-  bulk_g2s(stage + S::kVz, a.v_zero + tok * (kD / kGroupT), nv * 8, full);
+  const unsigned char* src = a.v_codes + tok * S::kVRow;
+#pragma unroll
+  for (int x = i; x < TOK * S::kVRow / 16; x += THREADS)
+    if (x * 16 < nv * S::kVRow) cp_async16(stage + S::kVc + x * 16, src + x * 16);
+  constexpr int kHalf = TOK / 2;  // two tokens a piece
+#pragma unroll
+  for (int x = i; x < 2 * kHalf; x += THREADS) {
+    const int y = x < kHalf ? x : x - kHalf;
+    if (2 * y < nv) cp_async16(stage + S::kVs + x * 16, (x < kHalf ? a.v_scale : a.v_zero) + (tok + 2 * y) * (kD / kGroupT));
+  }
+}
+
+// The fp16 rows of the tile's cached tokens into L2 (the warps read them with plain loads): the key residual's are
+// contiguous, the value ring's wrap around at most once.
+__device__ __forceinline__ void prefetch_fp16(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0) {
+  const int t1 = min(t0 + kTile, len.n), tk = max(t0, len.nqk), tv = max(t0, len.nqv), R = a.residual;
+  if (tk < t1) bulk_prefetch_l2(a.k_resid + (bh * R + (tk - len.nqk)) * kD, (t1 - tk) * kD * 2);
+  if (tv < t1) {
+    const int r = tv % R, first = min(t1 - tv, R - r);
+    bulk_prefetch_l2(a.v_resid + (bh * R + r) * kD, first * kD * 2);
+    if (first < t1 - tv) bulk_prefetch_l2(a.v_resid + bh * R * kD, (t1 - tv - first) * kD * 2);
+  }
 }
 
 // A query row as fp16 times a power of two that puts its largest magnitude in [2^14, 2^15): eight lanes, 16 channels
@@ -310,19 +341,20 @@ constexpr int kMmaWarps = kMmaThreads / 32;
 
 template <int KB, int VB, int NT>  // NT: row tiles of 8
 struct MmaLayout {
-  using S = StageLayout<KB, VB>;
+  using S = StageLayout<KB, VB, kGroupT>;
   static constexpr int kRows = 8 * NT;
   // resident blocks the registers (32 NT sums a thread) and the shared memory leave room for
   static constexpr int kBlocks = (NT == 1) ? 4 : (NT == 2) ? 3 : 2;
-  static constexpr int kStages = 2;
-  static constexpr int kOffQ = kStages * S::kBytes;                 // uint4 [4][NT][32 lanes]: B fragments of two k-steps
+  static constexpr int kStages = (KB + VB == 4) ? 3 : 2;            // of a warp's ring, one key group each
+  static constexpr int kOffQ = kMmaWarps * kStages * S::kBytes;     // uint4 [4][NT][32 lanes]: B fragments of two k-steps
   static constexpr int kOffO = kOffQ + 4 * NT * 32 * 16;            // float [2][kRows][128]: sums on their way to a warp
   static constexpr int kOffMl = kOffO + 2 * kRows * kD * 4;         // float2 [4 warps][kRows]: m, l
   static constexpr int kOffMask = kOffMl + kMmaWarps * kRows * 8;   // uint64 [kRows]
   static constexpr int kOffC = kOffMask + kRows * 8;                // float [kRows]: log2 units per score unit
-  static constexpr int kOffBar = kOffC + kRows * 4;                 // mbarriers, flags
-  static constexpr int kOffAhead = kOffBar + 128;                   // the copying thread's place
-  static constexpr int kSmem = kOffAhead + 64;
+  static constexpr int kOffAhead = kOffC + kRows * 4;               // Walk [4 warps]: the warp's next copy
+  static constexpr int kOffFlag = kOffAhead + kMmaWarps * 48;
+  static constexpr int kSmem = kOffFlag + 16;
+  static_assert(sizeof(Walk) <= 48, "a warp's place");
   static_assert(kSmem <= 232448 / kBlocks - 1024, "blocks per SM");
 };
 
@@ -334,17 +366,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -355,7 +376,7 @@ template <int KB, int VB, int NT>
 __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     kivi_tree_mma_kernel(const KiviTreeArgs a, const float scale_log2) {
   using L = MmaLayout<KB, VB, NT>;
-  using S = StageLayout<KB, VB>;
+  using S = StageLayout<KB, VB, kGroupT>;
   constexpr int kRows = L::kRows, kSt = L::kStages;
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ);
@@ -363,10 +384,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   float2* ml = reinterpret_cast<float2*>(sm + L::kOffMl);
   uint64_t* mask = reinterpret_cast<uint64_t*>(sm + L::kOffMask);
   float* rowc = reinterpret_cast<float*>(sm + L::kOffC);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [kSt] the stage's copies landed
-  uint64_t* empty = full + 4;                                      // [kSt] four warps are done with it
-  volatile int* failed = reinterpret_cast<volatile int*>(full + 8);
-  int* nonfinite = reinterpret_cast<int*>(full + 8) + 1;
+  int* nonfinite = reinterpret_cast<int*>(sm + L::kOffFlag);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = lane & 3, n8 = lane >> 2;
   const int rep = a.Hq / a.H, rows_all = a.N * rep, seg_per_b = a.H;  // one row tile
@@ -381,38 +399,31 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     if (tid == 0) shared[blockIdx.x] = sh;
     return;
   }
-  Walk& ahead = *reinterpret_cast<Walk*>(sm + L::kOffAhead);  // thread 0: the next tile to copy (kept out of registers)
-  int copied = 0;                                              // tiles whose copies were issued
-  auto produce = [&]() {
-    unsigned char* stage = sm + (copied % kSt) * S::kBytes;
-    const size_t bh = (size_t)ahead.b * a.H + ahead.seg;
-    uint64_t* f = &full[copied % kSt];  // two arrivals: keys, values
-    fence_proxy_async_smem();
-    copy_keys<KB, VB>(a, ahead.len, bh, ahead.tile * kTile, stage, f);
-    copy_values<KB, VB>(a, ahead.len, bh, ahead.tile * kTile, stage, f);
-    ++copied;
-    ahead.next(a, seg_per_b, copied < n);
-  };
-  // A wait that runs out is recorded; later waits return at once, so the block runs through and leaves.
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (*failed) return;
-    if (!mbar_wait_bounded(bar, parity)) {
-      *failed = 1;
-      set_error(a.err, KVQ_ERR_TIMEOUT);
+  // The warp's ring: its key group of tile i is in stage i % kSt, copied kSt - 1 tiles ahead by its own lanes.
+  unsigned char* ring = sm + warp * kSt * S::kBytes;
+  Walk& ahead = *reinterpret_cast<Walk*>(sm + L::kOffAhead + warp * 48);  // kept out of registers
+  int copied = 0;
+  auto copy_next = [&]() {  // one commit group per tile, also when there is nothing to copy
+    if (copied < n) {
+      const Walk x = ahead;
+      const size_t bh = (size_t)x.b * a.H + x.seg;
+      const int t = x.tile * kTile + 32 * warp;
+      unsigned char* stage = ring + copied % kSt * S::kBytes;
+      copy_keys<KB, VB, kGroupT, 32>(a, x.len, bh, t, stage, lane);
+      copy_values<KB, VB, kGroupT, 32>(a, x.len, bh, t, stage, lane);
+      if (tid == 0) prefetch_fp16(a, x.len, bh, x.tile * kTile);
+      ++copied;
+      __syncwarp();
+      if (lane == 0) ahead.next(a, seg_per_b, copied < n);
+      __syncwarp();
     }
+    cp_commit();
   };
-  auto refill_due = [&](int i) { return tid == 0 && i > 0 && copied < n && copied < i + kSt; };
-  if (tid == 0) {
-    for (int i = 0; i < kSt; ++i) {
-      mbar_init(&full[i], 2);
-      mbar_init(&empty[i], kMmaWarps);
-    }
-    *failed = 0;
-    *nonfinite = 0;
-    ahead = w;
-    fence_mbar_init();
-    for (int i = 0; i < min(kSt, n); ++i) produce();
-  }
+  if (tid == 0) *nonfinite = 0;
+  if (lane == 0) ahead = w;
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < kSt - 1; ++i) copy_next();
   const CodeScale cs0;
   const int tok8 = n8 ^ ((n8 >> 2) & 1);                                       // the token at place n of eight
   const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);  // at places 2 q, 2 q + 1
@@ -438,7 +449,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
         mask[r] = real ? a.mask[(size_t)w.b * a.N + r / rep] : 0ull;
       }
     }
-    __syncthreads();  // queries staged (and, the first time, the barriers)
+    __syncthreads();  // queries staged
     float m[NT][2], top[NT][2], l[NT][2], cs[NT][2];  // of rows 8 nt + 2 q, + 1: maximum - kRaise, + kSlack, sum, scale
     float o[NT][8][4];
 #pragma unroll
@@ -457,12 +468,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     const int i_first = i, tile_first = w.tile;
     const int i_end = min(n, i + w.len.tiles - w.tile);
     for (; i < i_end; ++i) {
-      const int st = i % kSt;
-      const unsigned char* stage = sm + st * S::kBytes;
+      const unsigned char* stage = ring + i % kSt * S::kBytes;
       const int tw = (tile_first + i - i_first) * kTile + 32 * warp;  // the warp's first token
-      // the stage of the tile before takes the next copies as soon as all warps are done with it
-      if (refill_due(i) && mbar_test(&empty[(i - 1) % kSt], ((i - 1) / kSt) & 1)) produce();
-      wait(&full[st], (i / kSt) & 1);
+      copy_next();  // into the stage of tile i - 1, which every lane has read
+      cp_wait<kSt - 1>();
+      __syncwarp();  // every lane's copies of tile i
       if (tw < w.len.n + w.len.nd) {
         // ---- scores: 2 tiles of 16 tokens ----
         float s[NT][2][4];
@@ -472,11 +482,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[nt][t][e] = 0.f;
-        if (tw < w.len.nqk) {
+        if (__builtin_expect(tw < w.len.nqk, 1)) {
           uint32_t u[4][KB];  // code words of the lane's 32 channels, four tokens (octets of the group)
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const unsigned char* p = stage + (32 * warp + 8 * t + tok8) * S::kKRow + q4 * (4 * KB);
+            const unsigned char* p = stage + (8 * t + tok8) * S::kKRow + q4 * (4 * KB);
             if constexpr (KB == 2) {
               const uint2 v = *reinterpret_cast<const uint2*>(p);
               u[t][0] = v.x;
@@ -493,8 +503,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           for (int hw = 0; hw < 2; ++hw) {  // 16 channels, 4 k-steps
             uint32_t sc[8], nz[8];
             {
-              const uint4* sp = reinterpret_cast<const uint4*>(stage + S::kKs + (warp * kD + 32 * q4 + 16 * hw) * 2);
-              const uint4* zp = reinterpret_cast<const uint4*>(stage + S::kKz + (warp * kD + 32 * q4 + 16 * hw) * 2);
+              const uint4* sp = reinterpret_cast<const uint4*>(stage + S::kKs + (32 * q4 + 16 * hw) * 2);
+              const uint4* zp = reinterpret_cast<const uint4*>(stage + S::kKz + (32 * q4 + 16 * hw) * 2);
               uint4 s0, s1, z0, z1;
               pair_order<KB>(sp[0], sp[1], s0, s1);
               pair_order<KB>(zp[0], zp[1], z0, z1);
@@ -532,14 +542,16 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
             }
           }
         } else {  // fp16 rows: residual, drafted, or none
+          const uint16_t* row[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) row[t] = fp16_key(a, w.len, w.b, h, tw + 8 * t + tok8);
 #pragma unroll 1
           for (int hw = 0; hw < 2; ++hw) {
             uint4 x[4][2];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                x[t][e] = fp16_key8(a, w.len, w.b, h, tw + 8 * t + tok8, 4 * q4 + 2 * hw + e);
+              for (int e = 0; e < 2; ++e) x[t][e] = row8(row[t], 4 * q4 + 2 * hw + e);
             uint32_t pr[4][8];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -561,7 +573,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               }
           }
         }
-        if (refill_due(i) && mbar_test(&empty[(i - 1) % kSt], ((i - 1) / kSt) & 1)) produce();
         // ---- softmax. x = s c is rounded before the maximum is taken from it, so that the largest score's
         //      weight is exact however large it is. Element e of tile t: octet 2 t + e / 2, row 2 q + e % 2 ----
         const bool plain = tw + 32 <= w.len.n;
@@ -572,15 +583,22 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x = __fmul_rn(s[nt][t][e], cs[nt][e & 1]);
-              if (!plain) {
-                const int dj = tw + 8 * (2 * t + (e >> 1)) + tok8 - w.len.n;
-                if (dj >= 0 && (dj >= w.len.nd || !((mask[8 * nt + 2 * q4 + (e & 1)] >> dj) & 1ull))) x = -INFINITY;
-              }
-              s[nt][t][e] = x;
-              over = over || x > top[nt][e & 1];
+              s[nt][t][e] = __fmul_rn(s[nt][t][e], cs[nt][e & 1]);
+              over = over || s[nt][t][e] > top[nt][e & 1];
             }
-        if (__any_sync(0xFFFFFFFFu, over)) {
+        if (!plain) {  // drafted tokens among the 32
+          over = true;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int dj = tw + 8 * (2 * t + (e >> 1)) + tok8 - w.len.n;
+                if (dj >= 0 && (dj >= w.len.nd || !((mask[8 * nt + 2 * q4 + (e & 1)] >> dj) & 1ull))) s[nt][t][e] = -INFINITY;
+              }
+        }
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, over), 0)) {
           // raise the maxima of the rows with a score past them
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -615,10 +633,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               pf[nt][2 * t + oc] = transpose8(pack_h2(p0, p1));
             }
         // ---- values: token pairs at places 2 q, 2 q + 1 of the four octets ----
-        if (tw + 32 <= w.len.nqv) {
-          const uint16_t* sp = reinterpret_cast<const uint16_t*>(stage + S::kVs) + 32 * warp * 4 + (n8 >> 1);
-          const uint16_t* zp = reinterpret_cast<const uint16_t*>(stage + S::kVz) + 32 * warp * 4 + (n8 >> 1);
-          const unsigned char* cw = stage + S::kVc + 32 * warp * S::kVRow + n8 * (2 * VB);
+        if (__builtin_expect(tw + 32 <= w.len.nqv, 1)) {
+          const uint16_t* sp = reinterpret_cast<const uint16_t*>(stage + S::kVs) + (n8 >> 1);
+          const uint16_t* zp = reinterpret_cast<const uint16_t*>(stage + S::kVz) + (n8 >> 1);
+          const unsigned char* cw = stage + S::kVc + n8 * (2 * VB);
           uint32_t sv[4], nz[4];
           uint32_t wa[4][VB / 2], wb[4][VB / 2];
 #pragma unroll
@@ -659,25 +677,36 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               }
           }
         } else {  // fp16 rows, and the group in which the quantized values end
+          const int place = a.residual > 0 ? tw % a.residual : 0;
 #pragma unroll 1
           for (int hw = 0; hw < 2; ++hw) {  // channels 16 n8 + 8 hw .. + 7
             uint32_t x[8][4];  // octet y / 2, place 2 q + y % 2
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const int tt = 8 * (y >> 1) + ((y & 1) ? cb : ca);
-              uint4 v;
-              if (tw + tt < w.len.nqv) {
-                const uint32_t cwd = *reinterpret_cast<const uint32_t*>(stage + S::kVc + (32 * warp + tt) * S::kVRow + n8 * (2 * VB) + (VB == 4 ? 4 * hw : 0)) >> (VB == 2 ? 16 * hw : 0);
-                const int at = (32 * warp + tt) * 4 + (n8 >> 1);
-                v = scalar_dequant8<VB>(cwd, th2f(reinterpret_cast<const uint16_t*>(stage + S::kVs)[at]),
-                                        th2f(reinterpret_cast<const uint16_t*>(stage + S::kVz)[at]));
-              } else {
-                v = fp16_value8(a, w.len, w.b, h, tw + tt, 2 * n8 + hw);
-              }
+              const uint4 v = tw + tt < w.len.nqv
+                                  ? make_uint4(0u, 0u, 0u, 0u)
+                                  : row8(fp16_value(a, w.len, w.b, h, tw + tt, ring_place(place, tt, a.residual)), 2 * n8 + hw);
               x[y][0] = v.x;
               x[y][1] = v.y;
               x[y][2] = v.z;
               x[y][3] = v.w;
+            }
+            if (tw < w.len.nqv) {
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const int tt = 8 * (y >> 1) + ((y & 1) ? cb : ca);
+                if (tw + tt < w.len.nqv) {
+                  const uint32_t cwd = *reinterpret_cast<const uint32_t*>(stage + S::kVc + tt * S::kVRow + n8 * (2 * VB) + (VB == 4 ? 4 * hw : 0)) >> (VB == 2 ? 16 * hw : 0);
+                  const int at = tt * 4 + (n8 >> 1);
+                  const uint4 v = scalar_dequant8<VB>(cwd, th2f(reinterpret_cast<const uint16_t*>(stage + S::kVs)[at]),
+                                                      th2f(reinterpret_cast<const uint16_t*>(stage + S::kVz)[at]));
+                  x[y][0] = v.x;
+                  x[y][1] = v.y;
+                  x[y][2] = v.z;
+                  x[y][3] = v.w;
+                }
+              }
             }
             if (!plain) {
               // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
@@ -711,12 +740,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-      if (refill_due(i)) {  // at the latest now
-        wait(&empty[(i - 1) % kSt], ((i - 1) / kSt) & 1);
-        if (!*failed) produce();
-      }
+      __syncwarp();  // the stage is read
     }
 
     // ================= the segment ends here (or the share does): hand its sums on =================
@@ -842,11 +866,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     w.next(a, seg_per_b, i < n);
     __syncthreads();  // the queries and row state are read before the next segment's
   }
-  if (tid == 0) {
-    shared[blockIdx.x] = sh;
-    if (*failed)  // copies in flight land before the block leaves
-      for (int k = max(0, copied - kSt); k < copied; ++k) mbar_wait_bounded(&full[k % kSt], (k / kSt) & 1, 10000000ull);
-  }
+  if (tid == 0) shared[blockIdx.x] = sh;
 }
 
 // ======================================================================================
@@ -869,7 +889,7 @@ struct TreeLayout {
   static constexpr int kOffK = kOffQ + ROWS * kD * 2;              // fp16 [128 tokens x 128], K-major; then P
   static constexpr int kOffV = kOffK + kTile * kD * 2;             // fp16 [128 channels x 128 tokens], K-major
   static constexpr int kOffStage = (kOffV + (kD / 8) * kVRowGrp + 127) / 128 * 128;
-  static constexpr int kOffMask = kOffStage + StageLayout<KB, VB>::kBytes;  // uint64 [ROWS]
+  static constexpr int kOffMask = kOffStage + StageLayout<KB, VB, kTile>::kBytes;  // uint64 [ROWS]
   static constexpr int kOffC = kOffMask + ROWS * 8;                // float [ROWS]: log2 units per score unit
   static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: running maximum (log2) - kRaise
   static constexpr int kOffT = kOffM + ROWS * 4;                   // float [ROWS]: running maximum + kSlack
@@ -977,8 +997,9 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
     uint4 x[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i][0] = fp16_key8(a, len, b, h, t0 + tok + 8 * i, 2 * c);
-      x[i][1] = fp16_key8(a, len, b, h, t0 + tok + 8 * i, 2 * c + 1);
+      const uint16_t* row = fp16_key(a, len, b, h, t0 + tok + 8 * i);
+      x[i][0] = row8(row, 2 * c);
+      x[i][1] = row8(row, 2 * c + 1);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1045,10 +1066,11 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
     }
   } else {
     uint32_t x[8][4];
+    const int place = a.residual > 0 ? (t0 + 8 * oct) % a.residual : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = t0 + 8 * oct + (i ^ flip);
-      const uint4 u = t >= len.nqv ? fp16_value8(a, len, b, h, t, c) : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 u = t >= len.nqv ? row8(fp16_value(a, len, b, h, t, ring_place(place, i ^ flip, a.residual)), c) : make_uint4(0u, 0u, 0u, 0u);
       x[i][0] = u.x;
       x[i][1] = u.y;
       x[i][2] = u.z;
@@ -1087,7 +1109,7 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
 template <int KB, int VB, int ROWS>
 __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTreeArgs a, const float scale_log2) {
   using L = TreeLayout<KB, VB, ROWS>;
-  using S = StageLayout<KB, VB>;
+  using S = StageLayout<KB, VB, kTile>;
   extern __shared__ __align__(128) unsigned char sm[];
   uint64_t* mask = reinterpret_cast<uint64_t*>(sm + L::kOffMask);
   float* rowc = reinterpret_cast<float*>(sm + L::kOffC);
@@ -1097,9 +1119,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   float* red = reinterpret_cast<float*>(sm + L::kOffRed);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // scores done
   uint64_t* bar_o = bar_s + 1;                                      // value product done
-  uint64_t* bar_k = bar_s + 2;                                      // the tile's stored keys landed
-  uint64_t* bar_v = bar_s + 3;                                      // its stored values
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 2);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* nonfinite = reinterpret_cast<int*>(tmem_slot + 2);
 
@@ -1126,25 +1146,27 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   unsigned char* stage = sm + L::kOffStage;
+  // one commit group each
   auto keys_of = [&](const Walk& x) {
-    fence_proxy_async_smem();
-    copy_keys<KB, VB>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, bar_k);
+    copy_keys<KB, VB, kTile, kTreeThreads>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, tid);
+    cp_commit();
   };
   auto values_of = [&](const Walk& x) {
-    fence_proxy_async_smem();
-    copy_values<KB, VB>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, bar_v);
+    const size_t bh = (size_t)x.b * a.H + x.seg / n_rt;
+    copy_values<KB, VB, kTile, kTreeThreads>(a, x.len, bh, x.tile * kTile, stage, tid);
+    cp_commit();
+    if (tid == 0) prefetch_fp16(a, x.len, bh, x.tile * kTile);
   };
+  keys_of(w);
+  values_of(w);
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_o, 1);
-    mbar_init(bar_k, 1);
-    mbar_init(bar_v, 1);
     *failed = 0;
     *nonfinite = 0;
     fence_mbar_init();
-    keys_of(w);
-    values_of(w);
   }
+  cp_wait<1>();  // the first tile's keys; the barrier below shows them to every thread
   tmem_before();
   __syncthreads();
   tmem_after();
@@ -1195,8 +1217,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       if (tid == 0) *nonfinite = 0;
       tile_first = tile;
     }
-    wait(bar_k, phase);
     unpack_keys<KB>(cs0, a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane);
+    cp_wait<0>();  // the tile's values
     fence_proxy_async_smem();
     tmem_before();
     if (__syncthreads_or(*failed)) break;
@@ -1207,9 +1229,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         umma_f16(tmem, tree_desc(smem_u32(sm + L::kOffK) + k * 256, 128, 2048),
                  tree_desc(smem_u32(sm + L::kOffQ) + k * 256, 128, 2048), tree_idesc(ROWS, false), k > 0);
       tree_commit(bar_s);
-      if (more) keys_of(nw);  // every thread has read this tile's
     }
-    wait(bar_v, phase);
+    if (more) keys_of(nw);  // every thread has read this tile's
     unpack_values<VB>(cs0, a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, nonfinite, warp, lane);
     wait(bar_s, phase);
     tmem_after();
@@ -1247,7 +1268,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     }
     tmem_before();
     const bool raise = __syncthreads_or(over);
-    if (tid == 0 && more) values_of(nw);  // every thread has read this tile's
+    if (more) values_of(nw);  // every thread has read this tile's
     if (raise) {
       // ---- raise the running maxima of the rows with a score past them ----
 #pragma unroll
@@ -1302,6 +1323,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       }
       *reinterpret_cast<uint4*>(sm + L::kOffK + ((r0 + i) >> 3) * 2048 + token_place(tt) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+    cp_wait<1>();  // the next tile's keys
     fence_proxy_async_smem();
     tmem_before();
     __syncthreads();
@@ -1378,13 +1400,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     }
     w = nw;
   }
-  if (tid == 0) {
-    shared[blockIdx.x] = sh;
-    if (*failed) {  // a wait that ran out leaves the loop at the next barrier: let this block's copies land first
-      mbar_wait_bounded(bar_k, phase, 10000000ull);
-      mbar_wait_bounded(bar_v, phase, 10000000ull);
-    }
-  }
+  cp_wait<0>();
+  if (tid == 0) shared[blockIdx.x] = sh;
   tmem_before();
   __syncthreads();
   if (warp == 0) {
