@@ -261,10 +261,11 @@ __device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLen
   }
 }
 
-// The fp16 rows of the tile's cached tokens into L2 (the warps read them with plain loads): the key residual's are
+// The fp16 rows of cached tokens t0 .. t1 - 1 into L2 (the warps read them with plain loads): the key residual's are
 // contiguous, the value ring's wrap around at most once.
-__device__ __forceinline__ void prefetch_fp16(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0) {
-  const int t1 = min(t0 + kTile, len.n), tk = max(t0, len.nqk), tv = max(t0, len.nqv), R = a.residual;
+__device__ __forceinline__ void prefetch_fp16(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0, int t1) {
+  t1 = min(t1, len.n);
+  const int tk = max(t0, len.nqk), tv = max(t0, len.nqv), R = a.residual;
   if (tk < t1) bulk_prefetch_l2(a.k_resid + (bh * R + (tk - len.nqk)) * kD, (t1 - tk) * kD * 2);
   if (tv < t1) {
     const int r = tv % R, first = min(t1 - tv, R - r);
@@ -273,8 +274,9 @@ __device__ __forceinline__ void prefetch_fp16(const KiviTreeArgs& a, const TreeL
   }
 }
 
-// A query row as fp16 times a power of two that puts its largest magnitude in [2^14, 2^15): eight lanes, 16 channels
-// each (w: bf16 pairs; o: fp16 pairs). Returns what a score has to be multiplied with (scale: log2 units).
+// A query row as fp16 times a power of two that puts its largest magnitude in [2^TOP, 2^(TOP + 1)): eight lanes, 16
+// channels each (w: bf16 pairs; o: fp16 pairs). Returns what a score has to be multiplied with (scale: log2 units).
+template <int TOP>
 __device__ __forceinline__ float query_fp16(const uint32_t (&w)[8], uint32_t (&o)[8], float scale) {
   float mx = 0.f;
 #pragma unroll
@@ -282,8 +284,8 @@ __device__ __forceinline__ float query_fp16(const uint32_t (&w)[8], uint32_t (&o
 #pragma unroll
   for (int off = 4; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
   const int ex = (int)(__float_as_uint(mx) >> 23);  // biased exponent; 0: zero or subnormal, 255: not finite
-  // times 2^(14 - (ex - 127)) in two factors, since the power may pass the fp32 range
-  const int sh = (ex == 0 || ex == 255) ? 0 : 141 - ex;
+  // times 2^(TOP - (ex - 127)) in two factors, since the power may pass the fp32 range
+  const int sh = (ex == 0 || ex == 255) ? 0 : TOP + 127 - ex;
   const float f1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = pack_h2(bf16_lo(w[e]) * f1 * f2, bf16_hi(w[e]) * f1 * f2);
@@ -334,10 +336,29 @@ __device__ __forceinline__ uint4 scalar_dequant8(uint32_t w, float s, float z) {
 //  * Values: the lane holds channels 16 n .. + 15, its own code word(s): rows n and n + 8 of channel tile t are
 //    channels 16 n + 2 t and + 1.
 //  * P^T turns from accumulator into B fragment by the 8 x 8 transposition of packed halves.
-// Bound: instruction issue. A group of 32 tokens costs a warp about 290 instructions for the keys (3 per code pair),
-// 50 for the softmax of 8 rows and 270 for the values, and 32 products per 8 rows.
+//  * Keys are not dequantized: sum_c q_c s_c (code_c - z_c) = sum_c (q_c s_c) code_c - sum_c (q_c s_c) z_c. A masked
+//    half of a code word is the fp16 subnormal code 2^(k - 24), exact; the scales of the group go into the queries
+//    (q' = fp16(q s 2^-k), one rounding, in both sums), and the second sum is a product with the zero-points as A.
+// Bound: instruction issue. A group of 32 tokens costs a warp about 170 instructions for the keys (1 per code pair),
+// 50 for the softmax of 8 rows and 270 for the values (3 per code pair), and 40 products per 8 rows.
 constexpr int kMmaThreads = 128;
 constexpr int kMmaWarps = kMmaThreads / 32;
+
+// Bit position of pair j (of the 8 of 16 channels) inside the half it is masked in: 2-bit codes 0 .. 2, 3 .. 5 and 6, 7
+// come from the word shifted by 0, 6 and 12, 4-bit codes 0, 1 and 2, 3 from shifts by 0 and 8.
+template <int KB>
+__host__ __device__ constexpr int pair_pos(int j) { return KB == 2 ? 2 * (j % 3) : 4 * (j % 2); }
+template <int KB>
+__device__ __forceinline__ uint32_t pair_codes(const uint32_t* w, int j) {  // w: the words of 16 channels
+  const uint32_t u = KB == 2 ? w[0] >> (6 * (j / 3)) : w[j >> 2] >> (8 * ((j & 3) >> 1));
+  return u & ((((1u << KB) - 1u) << pair_pos<KB>(j)) * 0x10001u);
+}
+// x 2^(SIGN pos) for pair j
+template <int KB, int SIGN>
+__device__ __forceinline__ uint32_t pos_scale(uint32_t x, int j) {
+  const int k = pair_pos<KB>(j);
+  return k == 0 ? x : as_u(__hmul2(as_h2(x), __float2half2_rn(SIGN > 0 ? (float)(1 << k) : 1.f / (float)(1 << k))));
+}
 
 template <int KB, int VB, int NT>  // NT: row tiles of 8
 struct MmaLayout {
@@ -402,33 +423,64 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   // The warp's ring: its key group of tile i is in stage i % kSt, copied kSt - 1 tiles ahead by its own lanes.
   unsigned char* ring = sm + warp * kSt * S::kBytes;
   Walk& ahead = *reinterpret_cast<Walk*>(sm + L::kOffAhead + warp * 48);  // kept out of registers
-  int copied = 0;
+  // the next copy: its first token among all tokens of the cache, its quantized keys and values (from there on), the
+  // tiles left in its segment and in the share, its stage
+  size_t c_tok = 0;
+  int c_nk = 0, c_nv = 0, c_left = 0, c_all = n, c_st = 0;
+  auto aim = [&]() {
+    c_tok = ((size_t)ahead.b * a.H + ahead.seg) * a.max_tokens + ahead.tile * kTile + 32 * warp;
+    c_nk = ahead.len.nqk - ahead.tile * kTile - 32 * warp;
+    c_nv = ahead.len.nqv - ahead.tile * kTile - 32 * warp;
+    c_left = ahead.len.tiles - ahead.tile;
+  };
   auto copy_next = [&]() {  // one commit group per tile, also when there is nothing to copy
-    if (copied < n) {
-      const Walk x = ahead;
-      const size_t bh = (size_t)x.b * a.H + x.seg;
-      const int t = x.tile * kTile + 32 * warp;
-      unsigned char* stage = ring + copied % kSt * S::kBytes;
-      copy_keys<KB, VB, kGroupT, 32>(a, x.len, bh, t, stage, lane);
-      copy_values<KB, VB, kGroupT, 32>(a, x.len, bh, t, stage, lane);
-      if (tid == 0) prefetch_fp16(a, x.len, bh, x.tile * kTile);
-      ++copied;
-      __syncwarp();
-      if (lane == 0) ahead.next(a, seg_per_b, copied < n);
-      __syncwarp();
+    if (c_all > 0) {
+      unsigned char* st = ring + c_st * S::kBytes + lane * 16;
+      const int half = lane & 15;
+      if (c_nk > 0) {  // a whole group or nothing
+        const unsigned char* src = a.k_codes + c_tok * S::kKRow + lane * 16;
+#pragma unroll
+        for (int x = 0; x < S::kKRow / 16; ++x) cp_async16(st + x * 512, src + x * 512);
+        cp_async16(st + S::kKs, (lane < 16 ? a.k_scale : a.k_zero) + c_tok / kGroupT * kD + half * 8);
+      }
+      if (c_nv > 0) {  // the rows behind n_quant_v are there, but not used
+        const unsigned char* src = a.v_codes + c_tok * S::kVRow + lane * 16;
+#pragma unroll
+        for (int x = 0; x < S::kVRow / 16; ++x) cp_async16(st + S::kVc + x * 512, src + x * 512);
+        cp_async16(st + S::kVs, (lane < 16 ? a.v_scale : a.v_zero) + c_tok * (kD / kGroupT) + half * 8);
+      }
+      c_st = c_st + 1 == kSt ? 0 : c_st + 1;
+      c_tok += kTile;
+      c_nk -= kTile;
+      c_nv -= kTile;
+      --c_all;
+      if (--c_left == 0) {  // on to the next segment
+        __syncwarp();
+        if (lane == 0) {
+          ahead.tile = ahead.len.tiles - 1;
+          ahead.next(a, seg_per_b, c_all > 0);
+          if (warp == 0 && c_all > 0) prefetch_fp16(a, ahead.len, (size_t)ahead.b * a.H + ahead.seg, 0, ahead.len.n);
+        }
+        __syncwarp();
+        aim();
+      }
     }
     cp_commit();
   };
-  if (tid == 0) *nonfinite = 0;
+  if (tid == 0) {
+    *nonfinite = 0;
+    prefetch_fp16(a, w.len, (size_t)w.b * a.H + w.seg, w.tile * kTile, w.len.n);
+  }
   if (lane == 0) ahead = w;
   __syncwarp();
+  aim();
 #pragma unroll 1
   for (int i = 0; i < kSt - 1; ++i) copy_next();
   const CodeScale cs0;
   const int tok8 = n8 ^ ((n8 >> 2) & 1);                                       // the token at place n of eight
   const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);  // at places 2 q, 2 q + 1
 
-  int i = 0;  // tiles done
+  int i = 0, st = 0;  // tiles done, the next one's stage
   while (i < n) {
     // ================= one segment's part: its queries =================
     const int h = w.seg;
@@ -437,9 +489,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       const int r = x >> 3, c = x & 7;
       uint32_t u[8], o[8];
       const bool real = load_query(a, w.len, w.b, h, r, c, u);
-      const float back = query_fp16(u, o, scale_log2);
+      const float back = query_fp16<-1>(u, o, scale_log2);
       uint4 x0, x1;
       pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
+      x0 = make_uint4(pos_scale<KB, -1>(x0.x, 0), pos_scale<KB, -1>(x0.y, 1), pos_scale<KB, -1>(x0.z, 2), pos_scale<KB, -1>(x0.w, 3));
+      x1 = make_uint4(pos_scale<KB, -1>(x1.x, 4), pos_scale<KB, -1>(x1.y, 5), pos_scale<KB, -1>(x1.z, 6), pos_scale<KB, -1>(x1.w, 7));
       // lane (row % 8, c / 2); k-steps 4 (c % 2) .. + 3: (pair 0, pair 1) each, two steps a uint4
       uint4* dst = qf + (2 * (c & 1) * NT + (r >> 3)) * 32 + (r & 7) * 4 + (c >> 1);
       dst[0] = x0;
@@ -468,7 +522,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     const int i_first = i, tile_first = w.tile;
     const int i_end = min(n, i + w.len.tiles - w.tile);
     for (; i < i_end; ++i) {
-      const unsigned char* stage = ring + i % kSt * S::kBytes;
+      const unsigned char* stage = ring + st * S::kBytes;
+      st = st + 1 == kSt ? 0 : st + 1;
       const int tw = (tile_first + i - i_first) * kTile + 32 * warp;  // the warp's first token
       copy_next();  // into the stage of tile i - 1, which every lane has read
       cp_wait<kSt - 1>();
@@ -499,48 +554,58 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               u[t][3] = v.w;
             }
           }
+          {  // the group's scales and zero-points in pair order, in place: a lane takes 16 channels of one of them
+            uint4* blk = reinterpret_cast<uint4*>(const_cast<unsigned char*>(stage) + S::kKs) + 2 * (lane & 15);
+            uint4 x0, x1;
+            pair_order<KB>(blk[0], blk[1], x0, x1);
+            __syncwarp();
+            if (lane < 16) {
+              blk[0] = x0;
+              blk[1] = x1;
+            }
+            __syncwarp();
+          }
+          float zs[NT][4];  // sum q' z
 #pragma unroll
-          for (int hw = 0; hw < 2; ++hw) {  // 16 channels, 4 k-steps
-            uint32_t sc[8], nz[8];
-            {
-              const uint4* sp = reinterpret_cast<const uint4*>(stage + S::kKs + (32 * q4 + 16 * hw) * 2);
-              const uint4* zp = reinterpret_cast<const uint4*>(stage + S::kKz + (32 * q4 + 16 * hw) * 2);
-              uint4 s0, s1, z0, z1;
-              pair_order<KB>(sp[0], sp[1], s0, s1);
-              pair_order<KB>(zp[0], zp[1], z0, z1);
-              const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-              const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                sc[j] = sw[j];
-                nz[j] = as_u(__hmul2(__hneg2(as_h2(sw[j])), as_h2(zw[j])));
-              }
+            for (int e = 0; e < 4; ++e) zs[nt][e] = 0.f;
+#pragma unroll
+          for (int k2 = 0; k2 < 4; ++k2) {  // two k-steps: pairs j0 .. j0 + 3 of 16 channels
+            const int j0 = 4 * (k2 & 1), hw = k2 >> 1;
+            const uint4 sc = *reinterpret_cast<const uint4*>(stage + S::kKs + (32 * q4 + 8 * k2) * 2);
+            const uint4 zp = *reinterpret_cast<const uint4*>(stage + S::kKz + (32 * q4 + 8 * k2) * 2);
+            uint4 bq[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint4 x = qf[(k2 * NT + nt) * 32 + lane];
+              bq[nt] = make_uint4(as_u(__hmul2(as_h2(x.x), as_h2(sc.x))), as_u(__hmul2(as_h2(x.y), as_h2(sc.y))),
+                                  as_u(__hmul2(as_h2(x.z), as_h2(sc.z))), as_u(__hmul2(as_h2(x.w), as_h2(sc.w))));
+              mma_f16(zs[nt], zp.x, zp.x, zp.y, zp.y, pos_scale<KB, 1>(bq[nt].x, j0), pos_scale<KB, 1>(bq[nt].y, j0 + 1));
+              mma_f16(zs[nt], zp.z, zp.z, zp.w, zp.w, pos_scale<KB, 1>(bq[nt].z, j0 + 2), pos_scale<KB, 1>(bq[nt].w, j0 + 3));
             }
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-              uint4 bq[NT];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) bq[nt] = qf[((2 * hw + k2) * NT + nt) * 32 + lane];
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t* ua = u[2 * t] + hw * (KB / 2);
+              const uint32_t* ub = u[2 * t + 1] + hw * (KB / 2);
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk) {
-                const int k = 2 * k2 + kk;  // pairs 2 k, 2 k + 1 of the 16 channels
+                const uint32_t a0 = pair_codes<KB>(ua, j0 + 2 * kk), a1 = pair_codes<KB>(ub, j0 + 2 * kk);
+                const uint32_t a2 = pair_codes<KB>(ua, j0 + 2 * kk + 1), a3 = pair_codes<KB>(ub, j0 + 2 * kk + 1);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                  uint32_t af[4];
-#pragma unroll
-                  for (int oc = 0; oc < 2; ++oc) {
-                    const uint32_t cw = (KB == 2) ? u[2 * t + oc][hw] : u[2 * t + oc][2 * hw + (k >> 1)];
-                    const int j = (KB == 2) ? 2 * k : 2 * (k & 1);
-                    af[oc] = dequant_h2(code_h2<KB>(cs0, cw, j), as_h2(sc[2 * k]), as_h2(nz[2 * k]));
-                    af[2 + oc] = dequant_h2(code_h2<KB>(cs0, cw, j + 1), as_h2(sc[2 * k + 1]), as_h2(nz[2 * k + 1]));
-                  }
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(s[nt][t], af[0], af[1], af[2], af[3], kk ? bq[nt].z : bq[nt].x, kk ? bq[nt].w : bq[nt].y);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(s[nt][t], a0, a1, a2, a3, kk ? bq[nt].z : bq[nt].x, kk ? bq[nt].w : bq[nt].y);
               }
             }
           }
+          // codes are 2^-24 of themselves in the products
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                s[nt][t][e] = fmaf(s[nt][t][e], cs[nt][e & 1] * 16777216.f, -zs[nt][e & 1] * cs[nt][e & 1]);
         } else {  // fp16 rows: residual, drafted, or none
           const uint16_t* row[4];
 #pragma unroll
@@ -552,29 +617,31 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
             for (int t = 0; t < 4; ++t)
 #pragma unroll
               for (int e = 0; e < 2; ++e) x[t][e] = row8(row[t], 4 * q4 + 2 * hw + e);
-            uint32_t pr[4][8];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              uint4 x0, x1;
-              pair_order<KB>(x[t][0], x[t][1], x0, x1);
-              pr[t][0] = x0.x; pr[t][1] = x0.y; pr[t][2] = x0.z; pr[t][3] = x0.w;
-              pr[t][4] = x1.x; pr[t][5] = x1.y; pr[t][6] = x1.z; pr[t][7] = x1.w;
-            }
+            for (int t = 0; t < 2; ++t) {
+              uint4 pa[2], pb[2];  // pairs of octets 2 t, 2 t + 1
+              pair_order<KB>(x[2 * t][0], x[2 * t][1], pa[0], pa[1]);
+              pair_order<KB>(x[2 * t + 1][0], x[2 * t + 1][1], pb[0], pb[1]);
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2)
+              for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint4 bq = qf[((2 * hw + k2) * NT + nt) * 32 + lane];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                  mma_f16(s[nt][t], pr[2 * t][4 * k2], pr[2 * t + 1][4 * k2], pr[2 * t][4 * k2 + 1], pr[2 * t + 1][4 * k2 + 1], bq.x, bq.y);
-                  mma_f16(s[nt][t], pr[2 * t][4 * k2 + 2], pr[2 * t + 1][4 * k2 + 2], pr[2 * t][4 * k2 + 3], pr[2 * t + 1][4 * k2 + 3], bq.z, bq.w);
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint4 bq = qf[((2 * hw + k2) * NT + nt) * 32 + lane];
+                  mma_f16(s[nt][t], pa[k2].x, pb[k2].x, pa[k2].y, pb[k2].y, pos_scale<KB, 1>(bq.x, 4 * k2), pos_scale<KB, 1>(bq.y, 4 * k2 + 1));
+                  mma_f16(s[nt][t], pa[k2].z, pb[k2].z, pa[k2].w, pb[k2].w, pos_scale<KB, 1>(bq.z, 4 * k2 + 2), pos_scale<KB, 1>(bq.w, 4 * k2 + 3));
                 }
-              }
+            }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[nt][t][e] *= cs[nt][e & 1];
         }
-        // ---- softmax. x = s c is rounded before the maximum is taken from it, so that the largest score's
-        //      weight is exact however large it is. Element e of tile t: octet 2 t + e / 2, row 2 q + e % 2 ----
+        // ---- softmax of the scores in log2 units; they are rounded before the maximum is taken from them, so that
+        //      the largest one's weight is exact however large it is. Element e of tile t: octet 2 t + e / 2, row
+        //      2 q + e % 2 ----
         const bool plain = tw + 32 <= w.len.n;
         bool over = false;
 #pragma unroll
@@ -582,10 +649,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[nt][t][e] = __fmul_rn(s[nt][t][e], cs[nt][e & 1]);
-              over = over || s[nt][t][e] > top[nt][e & 1];
-            }
+            for (int e = 0; e < 4; ++e) over = over || s[nt][t][e] > top[nt][e & 1];
         if (!plain) {  // drafted tokens among the 32
           over = true;
 #pragma unroll
@@ -1155,7 +1219,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     const size_t bh = (size_t)x.b * a.H + x.seg / n_rt;
     copy_values<KB, VB, kTile, kTreeThreads>(a, x.len, bh, x.tile * kTile, stage, tid);
     cp_commit();
-    if (tid == 0) prefetch_fp16(a, x.len, bh, x.tile * kTile);
+    if (tid == 0) prefetch_fp16(a, x.len, bh, x.tile * kTile, (x.tile + 1) * kTile);
   };
   keys_of(w);
   values_of(w);
@@ -1202,7 +1266,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         const int r = i >> 3, c = i & 7;
         uint32_t u[8], o[8];
         const bool real = load_query(a, len, b, h, row0 + r, c, u);
-        const float back = query_fp16(u, o, scale_log2);
+        const float back = query_fp16<14>(u, o, scale_log2);
         uint4 x0, x1;
         pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
         unsigned char* dst = sm + L::kOffQ + (r >> 3) * 2048 + c * 256 + (r & 7) * 16;
