@@ -372,8 +372,8 @@ struct MmaLayout {
   static constexpr int kOffMl = kOffO + 2 * kRows * kD * 4;         // float2 [4 warps][kRows]: m, l
   static constexpr int kOffMask = kOffMl + kMmaWarps * kRows * 8;   // uint64 [kRows]
   static constexpr int kOffC = kOffMask + kRows * 8;                // float [kRows]: log2 units per score unit
-  static constexpr int kOffAhead = kOffC + kRows * 4;               // Walk [4 warps]: the warp's next copy
-  static constexpr int kOffFlag = kOffAhead + kMmaWarps * 48;
+  static constexpr int kOffAhead = kOffC + kRows * 4;               // Walk [4 warps]: the warp's next copy; Walk: the block's
+  static constexpr int kOffFlag = kOffAhead + (kMmaWarps + 1) * 48;
   static constexpr int kSmem = kOffFlag + 16;
   static_assert(sizeof(Walk) <= 48, "a warp's place");
   static_assert(kSmem <= 232448 / kBlocks - 1024, "blocks per SM");
@@ -412,9 +412,15 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   TreeShared* shared = reinterpret_cast<TreeShared*>(a.part);
   float* slots = reinterpret_cast<float*>(shared + gridDim.x);
 
-  Walk w;
-  const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), w);
-  const int n = share.y - share.x;
+  Walk& w = *reinterpret_cast<Walk*>(sm + L::kOffAhead + kMmaWarps * 48);  // the block's place, kept out of registers
+  int n;
+  {
+    Walk x;
+    const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), x);
+    n = share.y - share.x;
+    if (tid == 0) w = x;
+    __syncthreads();
+  }
   TreeShared sh = {n > 0 ? 0 : 3, -1, 0, 0};
   if (n == 0) {
     if (tid == 0) shared[blockIdx.x] = sh;
@@ -424,18 +430,18 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   unsigned char* ring = sm + warp * kSt * S::kBytes;
   Walk& ahead = *reinterpret_cast<Walk*>(sm + L::kOffAhead + warp * 48);  // kept out of registers
   // the next copy: its first token among all tokens of the cache, its quantized keys and values (from there on), the
-  // tiles left in its segment and in the share, its stage
+  // tiles left in its segment and in the share
   size_t c_tok = 0;
-  int c_nk = 0, c_nv = 0, c_left = 0, c_all = n, c_st = 0;
+  int c_nk = 0, c_nv = 0, c_left = 0, c_all = n;
   auto aim = [&]() {
     c_tok = ((size_t)ahead.b * a.H + ahead.seg) * a.max_tokens + ahead.tile * kTile + 32 * warp;
     c_nk = ahead.len.nqk - ahead.tile * kTile - 32 * warp;
     c_nv = ahead.len.nqv - ahead.tile * kTile - 32 * warp;
     c_left = ahead.len.tiles - ahead.tile;
   };
-  auto copy_next = [&]() {  // one commit group per tile, also when there is nothing to copy
+  auto copy_next = [&](int stage) {  // one commit group per tile, also when there is nothing to copy
     if (c_all > 0) {
-      unsigned char* st = ring + c_st * S::kBytes + lane * 16;
+      unsigned char* st = ring + stage * S::kBytes + lane * 16;
       const int half = lane & 15;
       if (c_nk > 0) {  // a whole group or nothing
         const unsigned char* src = a.k_codes + c_tok * S::kKRow + lane * 16;
@@ -449,7 +455,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
         for (int x = 0; x < S::kVRow / 16; ++x) cp_async16(st + S::kVc + x * 512, src + x * 512);
         cp_async16(st + S::kVs, (lane < 16 ? a.v_scale : a.v_zero) + c_tok * (kD / kGroupT) + half * 8);
       }
-      c_st = c_st + 1 == kSt ? 0 : c_st + 1;
       c_tok += kTile;
       c_nk -= kTile;
       c_nv -= kTile;
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   __syncwarp();
   aim();
 #pragma unroll 1
-  for (int i = 0; i < kSt - 1; ++i) copy_next();
+  for (int i = 1; i < kSt; ++i) copy_next(i - 1);
   const CodeScale cs0;
   const int tok8 = n8 ^ ((n8 >> 2) & 1);                                       // the token at place n of eight
   const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);  // at places 2 q, 2 q + 1
@@ -504,13 +509,13 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       }
     }
     __syncthreads();  // queries staged
-    float m[NT][2], top[NT][2], l[NT][2], cs[NT][2];  // of rows 8 nt + 2 q, + 1: maximum - kRaise, + kSlack, sum, scale
+    float m[NT][2], l[NT][2], cs[NT][2];  // of rows 8 nt + 2 q, + 1: maximum - kRaise, sum, scale
     float o[NT][8][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[nt][e] = top[nt][e] = -FLT_MAX;
+        m[nt][e] = -FLT_MAX;
         l[nt][e] = 0.f;
         cs[nt][e] = rowc[8 * nt + 2 * q4 + e];
       }
@@ -519,16 +524,17 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.f;
     }
-    const int i_first = i, tile_first = w.tile;
-    const int i_end = min(n, i + w.len.tiles - w.tile);
-    for (; i < i_end; ++i) {
+    const int i_first = i, i_end = min(n, i + w.len.tiles - w.tile);
+    // the warp's tokens of a tile: tw, .. + 31; how far it is from there to the ends of the quantized keys and values
+    // and of the cached tokens
+    int tw = w.tile * kTile + 32 * warp, to_k = w.len.nqk - tw, to_v = w.len.nqv - tw, to_n = w.len.n - tw;
+    for (; i < i_end; ++i, tw += kTile, to_k -= kTile, to_v -= kTile, to_n -= kTile) {
       const unsigned char* stage = ring + st * S::kBytes;
+      copy_next(st == 0 ? kSt - 1 : st - 1);  // into the stage of tile i - 1, which every lane has read
       st = st + 1 == kSt ? 0 : st + 1;
-      const int tw = (tile_first + i - i_first) * kTile + 32 * warp;  // the warp's first token
-      copy_next();  // into the stage of tile i - 1, which every lane has read
       cp_wait<kSt - 1>();
       __syncwarp();  // every lane's copies of tile i
-      if (tw < w.len.n + w.len.nd) {
+      if (to_n > 0 || to_n + w.len.nd > 0) {
         // ---- scores: 2 tiles of 16 tokens ----
         float s[NT][2][4];
 #pragma unroll
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[nt][t][e] = 0.f;
-        if (__builtin_expect(tw < w.len.nqk, 1)) {
+        if (__builtin_expect(to_k > 0, 1)) {
           uint32_t u[4][KB];  // code words of the lane's 32 channels, four tokens (octets of the group)
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
@@ -642,14 +648,14 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
         // ---- softmax of the scores in log2 units; they are rounded before the maximum is taken from them, so that
         //      the largest one's weight is exact however large it is. Element e of tile t: octet 2 t + e / 2, row
         //      2 q + e % 2 ----
-        const bool plain = tw + 32 <= w.len.n;
+        const bool plain = to_n >= 32;
         bool over = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) over = over || s[nt][t][e] > top[nt][e & 1];
+            for (int e = 0; e < 4; ++e) over = over || s[nt][t][e] - m[nt][e & 1] > kRaise + kSlack;
         if (!plain) {  // drafted tokens among the 32
           over = true;
 #pragma unroll
@@ -658,7 +664,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int dj = tw + 8 * (2 * t + (e >> 1)) + tok8 - w.len.n;
+                const int dj = 8 * (2 * t + (e >> 1)) + tok8 - to_n;
                 if (dj >= 0 && (dj >= w.len.nd || !((mask[8 * nt + 2 * q4 + (e & 1)] >> dj) & 1ull))) s[nt][t][e] = -INFINITY;
               }
         }
@@ -671,10 +677,9 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               float mx = fmaxf(fmaxf(s[nt][0][e], s[nt][0][2 + e]), fmaxf(s[nt][1][e], s[nt][1][2 + e]));
 #pragma unroll
               for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-              if (mx > top[nt][e]) {
+              if (mx - m[nt][e] > kRaise + kSlack) {
                 const float f = exp2_approx(m[nt][e] - (mx - kRaise));
                 m[nt][e] = mx - kRaise;
-                top[nt][e] = mx + kSlack;
                 l[nt][e] *= f;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               pf[nt][2 * t + oc] = transpose8(pack_h2(p0, p1));
             }
         // ---- values: token pairs at places 2 q, 2 q + 1 of the four octets ----
-        if (__builtin_expect(tw + 32 <= w.len.nqv, 1)) {
+        if (__builtin_expect(to_v >= 32, 1)) {
           const uint16_t* sp = reinterpret_cast<const uint16_t*>(stage + S::kVs) + (n8 >> 1);
           const uint16_t* zp = reinterpret_cast<const uint16_t*>(stage + S::kVz) + (n8 >> 1);
           const unsigned char* cw = stage + S::kVc + n8 * (2 * VB);
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const int tt = 8 * (y >> 1) + ((y & 1) ? cb : ca);
-              const uint4 v = tw + tt < w.len.nqv
+              const uint4 v = tt < to_v
                                   ? make_uint4(0u, 0u, 0u, 0u)
                                   : row8(fp16_value(a, w.len, w.b, h, tw + tt, ring_place(place, tt, a.residual)), 2 * n8 + hw);
               x[y][0] = v.x;
@@ -756,11 +761,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               x[y][2] = v.z;
               x[y][3] = v.w;
             }
-            if (tw < w.len.nqv) {
+            if (to_v > 0) {
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
                 const int tt = 8 * (y >> 1) + ((y & 1) ? cb : ca);
-                if (tw + tt < w.len.nqv) {
+                if (tt < to_v) {
                   const uint32_t cwd = *reinterpret_cast<const uint32_t*>(stage + S::kVc + tt * S::kVRow + n8 * (2 * VB) + (VB == 4 ? 4 * hw : 0)) >> (VB == 2 ? 16 * hw : 0);
                   const int at = tt * 4 + (n8 >> 1);
                   const uint4 v = scalar_dequant8<VB>(cwd, th2f(reinterpret_cast<const uint16_t*>(stage + S::kVs)[at]),
@@ -778,7 +783,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               // end to the rows that see it.
 #pragma unroll
               for (int y = 0; y < 8; ++y)
-                if (tw + 8 * (y >> 1) + ((y & 1) ? cb : ca) >= w.len.n) {
+                if (8 * (y >> 1) + ((y & 1) ? cb : ca) >= to_n) {
                   bool any = false;
 #pragma unroll
                   for (int e = 0; e < 4; ++e) any |= drop_nonfinite(x[y][e]);
@@ -808,7 +813,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     }
 
     // ================= the segment ends here (or the share does): hand its sums on =================
-    const int t_end = tile_first + i - i_first;  // tiles of the segment that are done
+    const int tile_first = w.tile, t_end = tile_first + i - i_first;  // tiles of the segment that are done
     const bool last = t_end == w.len.tiles, earlier = tile_first > 0 && i_first == 0;
     const bool whole = last && !earlier;
 #pragma unroll
@@ -926,9 +931,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       __syncwarp();
       if (lane == 0) *nonfinite = 0;
     }
-    w.tile = t_end - 1;
-    w.next(a, seg_per_b, i < n);
-    __syncthreads();  // the queries and row state are read before the next segment's
+    __syncthreads();  // the queries, the row state and the place are read before the next segment's
+    if (tid == 0) {
+      w.tile = t_end - 1;
+      w.next(a, seg_per_b, i < n);
+    }
+    __syncthreads();
   }
   if (tid == 0) shared[blockIdx.x] = sh;
 }
