@@ -33,9 +33,11 @@ namespace {
 
 constexpr int kTile = 128;    // tokens per tile
 constexpr int kGroupT = 32;   // tokens per key group, channels per value group
-constexpr float kSlack = 7.f;   // log2 by which a score may pass its row's running maximum
-constexpr float kRaise = 8.f;   // weights are exp2(x - m + kRaise) <= 2^15, held as fp16: one below 2^-32 of the
-                                // maximum's is lost instead of one below 2^-24
+// A row's weights are exp2(x - m + kRaise), m its running maximum, which moves when a score passes it by kSlack (log2):
+// weights stay below 2^15 and are held as fp16, where one below 2^-30 of the maximum's is lost (2^-25 without kRaise).
+// Raising costs a pass over the sums; at a slack of 7 the peaked scores of outlier channels raise some row of a tile
+// of 64 in most of a segment's first tiles.
+constexpr float kSlack = 10.f, kRaise = 5.f;
 
 // TOK stored tokens (a key group or a tile): key codes, scales and zeros [groups][128], value codes, scales and
 // zeros [tokens][4]
@@ -366,7 +368,7 @@ struct MmaLayout {
   static constexpr int kRows = 8 * NT;
   // resident blocks the registers (32 NT sums a thread) and the shared memory leave room for
   static constexpr int kBlocks = (NT == 1) ? 4 : (NT == 2) ? 3 : 2;
-  static constexpr int kStages = (KB + VB == 4) ? 3 : 2;            // of a warp's ring, one key group each
+  static constexpr int kStages = 2;            // of a warp's ring, one key group each
   static constexpr int kOffQ = kMmaWarps * kStages * S::kBytes;     // uint4 [4][NT][32 lanes]: B fragments of two k-steps
   static constexpr int kOffO = kOffQ + 4 * NT * 32 * 16;            // float [2][kRows][128]: sums on their way to a warp
   static constexpr int kOffMl = kOffO + 2 * kRows * kD * 4;         // float2 [4 warps][kRows]: m, l
@@ -1571,7 +1573,7 @@ int sm_count_tree() {
 }
 // resident blocks
 int tree_blocks(int r) {
-  return sm_count_tree() * (r == 8 ? MmaLayout<2, 2, 1>::kBlocks : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
+  return sm_count_tree() * (r == 8 ? 4 : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
 }
 
 template <int ROWS>
