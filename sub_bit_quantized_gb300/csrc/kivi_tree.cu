@@ -965,11 +965,11 @@ struct TreeLayout {
   static constexpr int kOffStage = (kOffV + (kD / 8) * kVRowGrp + 127) / 128 * 128;
   static constexpr int kOffMask = kOffStage + StageLayout<KB, VB, kTile>::kBytes;  // uint64 [ROWS]
   static constexpr int kOffC = kOffMask + ROWS * 8;                // float [ROWS]: log2 units per score unit
-  static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: running maximum (log2) - kRaise
-  static constexpr int kOffT = kOffM + ROWS * 4;                   // float [ROWS]: running maximum + kSlack
-  static constexpr int kOffF = kOffT + ROWS * 4;                   // float [ROWS]: rescale factor
+  static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: kRaise - running maximum (log2)
+  static constexpr int kOffF = kOffM + ROWS * 4;                   // float [ROWS]: rescale factor
   static constexpr int kOffRed = kOffF + ROWS * 4;                 // float [4][ROWS]: per lane quadrant
-  static constexpr int kOffBar = kOffRed + 4 * ROWS * 4;           // mbarriers, TMEM address, flags
+  static constexpr int kOffWalk = kOffRed + 4 * ROWS * 4;          // Walk [2]: this position's and the next one's
+  static constexpr int kOffBar = kOffWalk + 96;                    // mbarriers, TMEM address, flags
   static constexpr int kSmem = kOffBar + 64;
   static constexpr uint32_t kCols = 2 * ROWS < 32 ? 32 : 2 * ROWS;  // TMEM: S^T, O^T
   static_assert(ROWS * 256 <= kTile * kD * 2, "P fits in the key tile");
@@ -1188,7 +1188,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   uint64_t* mask = reinterpret_cast<uint64_t*>(sm + L::kOffMask);
   float* rowc = reinterpret_cast<float*>(sm + L::kOffC);
   float* rowm = reinterpret_cast<float*>(sm + L::kOffM);
-  float* rowt = reinterpret_cast<float*>(sm + L::kOffT);
   float* rowf = reinterpret_cast<float*>(sm + L::kOffF);
   float* red = reinterpret_cast<float*>(sm + L::kOffRed);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // scores done
@@ -1204,9 +1203,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 
   TreeShared* shared = reinterpret_cast<TreeShared*>(a.part);
   float* slots = reinterpret_cast<float*>(shared + gridDim.x);
-  Walk w;
-  const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), w);
-  const int p0 = share.x, p1 = share.y;
+  Walk* place = reinterpret_cast<Walk*>(sm + L::kOffWalk);  // of position p in place[p & 1] (kept out of registers)
+  int p0, p1;
+  {
+    Walk x;
+    const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), x);
+    p0 = share.x;
+    p1 = share.y;
+    if (tid == 0) place[p0 & 1] = x;
+    __syncthreads();
+  }
   TreeShared sh = {p0 < p1 ? 0 : 3, -1, 0, 0};
   if (p0 >= p1) {
     if (tid == 0) shared[blockIdx.x] = sh;
@@ -1231,8 +1237,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     cp_commit();
     if (tid == 0) prefetch_fp16(a, x.len, bh, x.tile * kTile, (x.tile + 1) * kTile);
   };
-  keys_of(w);
-  values_of(w);
+  keys_of(place[p0 & 1]);
+  values_of(place[p0 & 1]);
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_o, 1);
@@ -1251,7 +1257,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   const int r0 = half * kHR;
   uint32_t phase = 0;    // of the barriers: one completion each per tile
   const CodeScale cs0;
-  float l[kHR];
+  float2 l[kHR / 2];
   bool first = true;    // of the segment's tiles in this block
   int tile_first = 0;   // that tile
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -1262,15 +1268,20 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   };
 
   for (int p = p0; p < p1; ++p) {
-    const int b = w.b, h = w.seg / n_rt, row0 = (w.seg - h * n_rt) * ROWS, tile = w.tile, t0 = tile * kTile;
+    const Walk& w = place[p & 1];
+    const Walk& nw = place[(p + 1) & 1];
     const TreeLens& len = w.len;
+    const int b = w.b, h = w.seg / n_rt, row0 = (w.seg - h * n_rt) * ROWS, tile = w.tile, t0 = tile * kTile;
     const bool last = w.last(), more = p + 1 < p1;
-    Walk nw = w;
-    nw.next(a, seg_per_b, more);
+    if (tid == 32 && more) {  // shown to the others by the next barrier
+      Walk x = w;
+      x.next(a, seg_per_b, true);
+      place[(p + 1) & 1] = x;
+    }
     if (first) {
       // ---- the segment's query rows, masks and running state (8 lanes a row) ----
 #pragma unroll
-      for (int i = 0; i < kHR; ++i) l[i] = 0.f;
+      for (int i = 0; i < kHR / 2; ++i) l[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int i = tid; i < ROWS * 8; i += kTreeThreads) {
         const int r = i >> 3, c = i & 7;
@@ -1284,7 +1295,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         *reinterpret_cast<uint4*>(dst + 128) = x1;
         if (c == 0) {
           rowc[r] = back;
-          rowm[r] = rowt[r] = -FLT_MAX;
+          rowm[r] = FLT_MAX;
           mask[r] = real ? a.mask[(size_t)b * a.N + (row0 + r) / rep] : 0ull;
         }
       }
@@ -1308,10 +1319,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     unpack_values<VB>(cs0, a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, nonfinite, warp, lane);
     wait(bar_s, phase);
     tmem_after();
-    // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1. x = s c is rounded before the
-    //      maximum is taken from it, so that the largest score's weight is exact however large it is ----
-    const int tt = 32 * quad + lane, t = t0 + tt;
-    float x[kHR];
+    // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1, two rows an operation. x = s c is rounded
+    //      before the maximum is taken from it, so that the largest score's weight is exact however large it is ----
+    const int tt = 32 * quad + lane;
+    float2 x[kHR / 2];
     {
       uint32_t xr[kHR];
 #pragma unroll
@@ -1320,34 +1331,36 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 #pragma unroll
       for (int i = 0; i < kHR; i += 4) {
         const float4 c4 = *reinterpret_cast<const float4*>(rowc + r0 + i);
-        x[i] = __fmul_rn(__uint_as_float(xr[i]), c4.x);
-        x[i + 1] = __fmul_rn(__uint_as_float(xr[i + 1]), c4.y);
-        x[i + 2] = __fmul_rn(__uint_as_float(xr[i + 2]), c4.z);
-        x[i + 3] = __fmul_rn(__uint_as_float(xr[i + 3]), c4.w);
+        x[i / 2] = __fmul2_rn(make_float2(__uint_as_float(xr[i]), __uint_as_float(xr[i + 1])), make_float2(c4.x, c4.y));
+        x[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(xr[i + 2]), __uint_as_float(xr[i + 3])), make_float2(c4.z, c4.w));
       }
     }
     if (t0 + kTile > len.n) {  // drafted tokens in the tile, or none at all behind the last one
-      const int dj = t - len.n;
+      const int dj = t0 + tt - len.n;
       if (dj >= 0) {
 #pragma unroll
-        for (int i = 0; i < kHR; ++i)
-          if (dj >= len.nd || !((mask[r0 + i] >> dj) & 1ull)) x[i] = -INFINITY;
+        for (int i = 0; i < kHR / 2; ++i) {
+          if (dj >= len.nd || !((mask[r0 + 2 * i] >> dj) & 1ull)) x[i].x = -INFINITY;
+          if (dj >= len.nd || !((mask[r0 + 2 * i + 1] >> dj) & 1ull)) x[i].y = -INFINITY;
+        }
       }
     }
-    bool over = false;
+    float most = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kHR; i += 4) {
-      const float4 t4 = *reinterpret_cast<const float4*>(rowt + r0 + i);
-      over = over || x[i] > t4.x || x[i + 1] > t4.y || x[i + 2] > t4.z || x[i + 3] > t4.w;
+      const float4 m4 = *reinterpret_cast<const float4*>(rowm + r0 + i);
+      const float2 d0 = __fadd2_rn(x[i / 2], make_float2(m4.x, m4.y)), d1 = __fadd2_rn(x[i / 2 + 1], make_float2(m4.z, m4.w));
+      most = fmaxf(most, fmaxf(d0.x, d0.y));
+      most = fmaxf(most, fmaxf(d1.x, d1.y));
     }
     tmem_before();
-    const bool raise = __syncthreads_or(over);
+    const bool raise = __syncthreads_or(most > kSlack + kRaise);
     if (more) values_of(nw);  // every thread has read this tile's
     if (raise) {
       // ---- raise the running maxima of the rows with a score past them ----
 #pragma unroll
       for (int i = 0; i < kHR; ++i) {
-        float mx = x[i];
+        float mx = (i & 1) ? x[i >> 1].y : x[i >> 1].x;
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
         if (lane == 0) red[quad * ROWS + r0 + i] = mx;
@@ -1355,16 +1368,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       __syncthreads();
       for (int r = tid; r < ROWS; r += kTreeThreads) {
         const float mt = fmaxf(fmaxf(red[r], red[ROWS + r]), fmaxf(red[2 * ROWS + r], red[3 * ROWS + r]));
-        const bool up = mt > rowt[r];
-        rowf[r] = up ? exp2_approx(rowm[r] - (mt - kRaise)) : 1.f;
-        if (up) {
-          rowm[r] = mt - kRaise;
-          rowt[r] = mt + kSlack;
-        }
+        const bool up = mt + rowm[r] > kSlack + kRaise;
+        rowf[r] = up ? exp2_approx((kRaise - mt) - rowm[r]) : 1.f;
+        if (up) rowm[r] = kRaise - mt;
       }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kHR; ++i) l[i] *= rowf[r0 + i];
+      for (int i = 0; i < kHR / 2; ++i) l[i] = __fmul2_rn(l[i], *reinterpret_cast<const float2*>(rowf + r0 + 2 * i));
       if (!first) {  // O^T: the value product of the tile before is done (waited for below)
         tmem_after();
 #pragma unroll
@@ -1386,14 +1396,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
         const float4 m4 = *reinterpret_cast<const float4*>(rowm + r0 + i + e);
-        const float p0e = exp2_approx(x[i + e] - m4.x), p1e = exp2_approx(x[i + e + 1] - m4.y);
-        const float p2e = exp2_approx(x[i + e + 2] - m4.z), p3e = exp2_approx(x[i + e + 3] - m4.w);
-        l[i + e] += p0e;
-        l[i + e + 1] += p1e;
-        l[i + e + 2] += p2e;
-        l[i + e + 3] += p3e;
-        o[e / 2] = pack_h2(p0e, p1e);
-        o[e / 2 + 1] = pack_h2(p2e, p3e);
+        const int y = (i + e) / 2;
+        float2 d0 = __fadd2_rn(x[y], make_float2(m4.x, m4.y)), d1 = __fadd2_rn(x[y + 1], make_float2(m4.z, m4.w));
+        d0 = make_float2(exp2_approx(d0.x), exp2_approx(d0.y));
+        d1 = make_float2(exp2_approx(d1.x), exp2_approx(d1.y));
+        l[y] = __fadd2_rn(l[y], d0);
+        l[y + 1] = __fadd2_rn(l[y + 1], d1);
+        o[e / 2] = pack_h2(d0.x, d0.y);
+        o[e / 2 + 1] = pack_h2(d1.x, d1.y);
       }
       *reinterpret_cast<uint4*>(sm + L::kOffK + ((r0 + i) >> 3) * 2048 + token_place(tt) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -1419,7 +1429,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       // l: over the tokens (lanes and quadrants)
 #pragma unroll
       for (int i = 0; i < kHR; ++i) {
-        float s = l[i];
+        float s = (i & 1) ? l[i >> 1].y : l[i >> 1].x;
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
         if (lane == 0) red[quad * ROWS + r0 + i] = s;
@@ -1462,7 +1472,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
           } else {
             slot[(size_t)r * kD + ch] = o;
             if (ch == 0) {
-              slot[(size_t)ROWS * kD + r] = rowm[r];
+              slot[(size_t)ROWS * kD + r] = -rowm[r];
               slot[(size_t)ROWS * kD + ROWS + r] = lt;
             }
           }
@@ -1472,7 +1482,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       __syncthreads();  // the row state is read before the next segment resets it
       first = true;
     }
-    w = nw;
   }
   cp_wait<0>();
   if (tid == 0) shared[blockIdx.x] = sh;
