@@ -226,41 +226,40 @@ __device__ __forceinline__ void cp_async16(unsigned char* dst, const void* src) 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-// The stored part of TOK tokens from t0 (a multiple of 32) into a stage, one 16-byte piece a thread at a time (thread i
-// of THREADS): the keys of whole groups below n_quant_k, the values of groups that have one below n_quant_v.
-template <int KB, int VB, int TOK, int THREADS>
-__device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
-                                          unsigned char* stage, int i) {
-  using S = StageLayout<KB, VB, TOK>;
-  const int nk = len.nqk - t0;  // of the TOK, a multiple of 32
-  const unsigned char* src = a.k_codes + (bh * a.max_tokens + t0) * S::kKRow;
-#pragma unroll
-  for (int x = i; x < TOK * S::kKRow / 16; x += THREADS)
-    if (x * 16 < nk * S::kKRow) cp_async16(stage + x * 16, src + x * 16);
+// The stored part of a tile into a stage by bulk copies of one thread: the keys of whole groups below n_quant_k, the
+// values below n_quant_v. With nothing to copy the barrier completes at once.
+template <int KB, int VB>
+__device__ __forceinline__ void bulk_keys(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
+                                          unsigned char* stage, uint64_t* full) {
+  using S = StageLayout<KB, VB, kTile>;
+  const int nk = min(kTile, len.nqk - t0);
+  if (nk <= 0) {
+    mbar_arrive(full);
+    return;
+  }
   const size_t g = (bh * (a.max_tokens / kGroupT) + t0 / kGroupT) * kD;
-  constexpr int kHalf = TOK / kGroupT * (kD / 8);  // pieces of scales, then of zeros
-#pragma unroll
-  for (int x = i; x < 2 * kHalf; x += THREADS) {
-    const int y = x < kHalf ? x : x - kHalf;
-    if (y / (kD / 8) * kGroupT < nk) cp_async16(stage + S::kKs + x * 16, (x < kHalf ? a.k_scale : a.k_zero) + g + y * 8);
-  }
+  const uint32_t gb = nk / kGroupT * kD * 2;
+  fence_proxy_async_smem();
+  mbar_arrive_expect_tx(full, nk * S::kKRow + 2 * gb);
+  bulk_g2s(stage, a.k_codes + (bh * a.max_tokens + t0) * S::kKRow, nk * S::kKRow, full);
+  bulk_g2s(stage + S::kKs, a.k_scale + g, gb, full);
+  bulk_g2s(stage + S::kKz, a.k_zero + g, gb, full);
 }
-template <int KB, int VB, int TOK, int THREADS>
-__device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
-                                            unsigned char* stage, int i) {
-  using S = StageLayout<KB, VB, TOK>;
-  const int nv = (len.nqv - t0 + kGroupT - 1) / kGroupT * kGroupT;  // the rows behind n_quant_v are there, but not used
-  const size_t tok = bh * a.max_tokens + t0;
-  const unsigned char* src = a.v_codes + tok * S::kVRow;
-#pragma unroll
-  for (int x = i; x < TOK * S::kVRow / 16; x += THREADS)
-    if (x * 16 < nv * S::kVRow) cp_async16(stage + S::kVc + x * 16, src + x * 16);
-  constexpr int kHalf = TOK / 2;  // two tokens a piece
-#pragma unroll
-  for (int x = i; x < 2 * kHalf; x += THREADS) {
-    const int y = x < kHalf ? x : x - kHalf;
-    if (2 * y < nv) cp_async16(stage + S::kVs + x * 16, (x < kHalf ? a.v_scale : a.v_zero) + (tok + 2 * y) * (kD / kGroupT));
+template <int KB, int VB>
+__device__ __forceinline__ void bulk_values(const KiviTreeArgs& a, const TreeLens& len, size_t bh, int t0,
+                                            unsigned char* stage, uint64_t* full) {
+  using S = StageLayout<KB, VB, kTile>;
+  const int nv = (min(kTile, len.nqv - t0) + 1) & ~1;  // whole 16-byte pieces
+  if (nv <= 0) {
+    mbar_arrive(full);
+    return;
   }
+  const size_t tok = bh * a.max_tokens + t0;
+  fence_proxy_async_smem();
+  mbar_arrive_expect_tx(full, nv * (S::kVRow + 16));
+  bulk_g2s(stage + S::kVc, a.v_codes + tok * S::kVRow, nv * S::kVRow, full);
+  bulk_g2s(stage + S::kVs, a.v_scale + tok * (kD / kGroupT), nv * 8, full);
+  bulk_g2s(stage + S::kVz, a.v_zero + tok * (kD / kGroupT), nv * 8, full);
 }
 
 // The fp16 rows of cached tokens t0 .. t1 - 1 into L2 (the warps read them with plain loads): the key residual's are
@@ -1022,6 +1021,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                : "memory");
 }
 
+// Reduces N (a power of two, up to 32) values over a warp's lanes: v[0] of lane i < N is value i's.
+template <int N, typename F>
+__device__ __forceinline__ void lanes_reduce(float (&v)[N], int lane, F f) {
+#pragma unroll
+  for (int off = 16; off >= N; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = f(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], off));
+#pragma unroll
+  for (int w = N / 2; w >= 1; w >>= 1) {
+    const bool up = (lane & w) != 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
+      v[i] = f(keep, __shfl_xor_sync(0xFFFFFFFFu, send, w));
+    }
+  }
+}
+
 // ---- keys of a tile. A lane takes token lane % 8 of an octet and a code word (2 bits: 16 channels, 4 bits: 8);
 //      a warp one key group and half of the words, so a lane unpacks four tokens per scale. Groups behind the
 //      quantized keys are fp16 rows. ----
@@ -1192,7 +1209,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   float* red = reinterpret_cast<float*>(sm + L::kOffRed);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // scores done
   uint64_t* bar_o = bar_s + 1;                                      // value product done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 2);
+  uint64_t* bar_k = bar_s + 2;                                      // the tile's stored keys landed
+  uint64_t* bar_v = bar_s + 3;                                      // its stored values
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 4);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* nonfinite = reinterpret_cast<int*>(tmem_slot + 2);
 
@@ -1226,27 +1245,26 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   unsigned char* stage = sm + L::kOffStage;
-  // one commit group each
+  // by one thread each, of warps that issue no products
   auto keys_of = [&](const Walk& x) {
-    copy_keys<KB, VB, kTile, kTreeThreads>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, tid);
-    cp_commit();
+    bulk_keys<KB, VB>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, bar_k);
   };
   auto values_of = [&](const Walk& x) {
     const size_t bh = (size_t)x.b * a.H + x.seg / n_rt;
-    copy_values<KB, VB, kTile, kTreeThreads>(a, x.len, bh, x.tile * kTile, stage, tid);
-    cp_commit();
-    if (tid == 0) prefetch_fp16(a, x.len, bh, x.tile * kTile, (x.tile + 1) * kTile);
+    bulk_values<KB, VB>(a, x.len, bh, x.tile * kTile, stage, bar_v);
+    prefetch_fp16(a, x.len, bh, x.tile * kTile, (x.tile + 1) * kTile);
   };
-  keys_of(place[p0 & 1]);
-  values_of(place[p0 & 1]);
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_o, 1);
+    mbar_init(bar_k, 1);
+    mbar_init(bar_v, 1);
     *failed = 0;
     *nonfinite = 0;
     fence_mbar_init();
+    keys_of(place[p0 & 1]);
+    values_of(place[p0 & 1]);
   }
-  cp_wait<1>();  // the first tile's keys; the barrier below shows them to every thread
   tmem_before();
   __syncthreads();
   tmem_after();
@@ -1256,6 +1274,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   constexpr int kHR = ROWS / 2;                            // rows a thread works on
   const int r0 = half * kHR;
   uint32_t phase = 0;    // of the barriers: one completion each per tile
+  // the operands' descriptors; a k-step further on is 256 bytes (16 units) further on in each
+  const uint64_t desc_k = tree_desc(smem_u32(sm + L::kOffK), 128, 2048), desc_q = tree_desc(smem_u32(sm + L::kOffQ), 128, 2048);
+  const uint64_t desc_v = tree_desc(smem_u32(sm + L::kOffV), 128, kVRowGrp), desc_p = desc_k;  // P lies where K was
   const CodeScale cs0;
   float2 l[kHR / 2];
   bool first = true;    // of the segment's tiles in this block
@@ -1302,20 +1323,19 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       if (tid == 0) *nonfinite = 0;
       tile_first = tile;
     }
+    wait(bar_k, phase);
     unpack_keys<KB>(cs0, a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane);
-    cp_wait<0>();  // the tile's values
     fence_proxy_async_smem();
     tmem_before();
     if (__syncthreads_or(*failed)) break;
     if (tid == 0) {
       tmem_after();
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_f16(tmem, tree_desc(smem_u32(sm + L::kOffK) + k * 256, 128, 2048),
-                 tree_desc(smem_u32(sm + L::kOffQ) + k * 256, 128, 2048), tree_idesc(ROWS, false), k > 0);
+      for (int k = 0; k < 8; ++k) umma_f16(tmem, desc_k + 16 * k, desc_q + 16 * k, tree_idesc(ROWS, false), k > 0);
       tree_commit(bar_s);
     }
-    if (more) keys_of(nw);  // every thread has read this tile's
+    if (tid == 96 && more) keys_of(nw);  // every thread has read this tile's
+    wait(bar_v, phase);
     unpack_values<VB>(cs0, a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, nonfinite, warp, lane);
     wait(bar_s, phase);
     tmem_after();
@@ -1355,15 +1375,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     }
     tmem_before();
     const bool raise = __syncthreads_or(most > kSlack + kRaise);
-    if (more) values_of(nw);  // every thread has read this tile's
+    if (tid == 224 && more) values_of(nw);  // every thread has read this tile's
     if (raise) {
       // ---- raise the running maxima of the rows with a score past them ----
+      {
+        float v[kHR];
 #pragma unroll
-      for (int i = 0; i < kHR; ++i) {
-        float mx = (i & 1) ? x[i >> 1].y : x[i >> 1].x;
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-        if (lane == 0) red[quad * ROWS + r0 + i] = mx;
+        for (int i = 0; i < kHR; ++i) v[i] = (i & 1) ? x[i >> 1].y : x[i >> 1].x;
+        lanes_reduce<kHR>(v, lane, [](float p, float q) { return fmaxf(p, q); });
+        if (lane < kHR) red[quad * ROWS + r0 + lane] = v[0];
       }
       __syncthreads();
       for (int r = tid; r < ROWS; r += kTreeThreads) {
@@ -1407,16 +1427,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       }
       *reinterpret_cast<uint4*>(sm + L::kOffK + ((r0 + i) >> 3) * 2048 + token_place(tt) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    cp_wait<1>();  // the next tile's keys
     fence_proxy_async_smem();
     tmem_before();
     __syncthreads();
     if (tid == 0) {
       tmem_after();
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_f16(tmem + ROWS, tree_desc(smem_u32(sm + L::kOffV) + k * 256, 128, kVRowGrp),
-                 tree_desc(smem_u32(sm + L::kOffK) + k * 256, 128, 2048), tree_idesc(ROWS, true), !first || k > 0);
+      for (int k = 0; k < 8; ++k) umma_f16(tmem + ROWS, desc_v + 16 * k, desc_p + 16 * k, tree_idesc(ROWS, true), !first || k > 0);
       tree_commit(bar_o);
     }
     wait(bar_o, phase);
@@ -1426,13 +1443,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 
     // ---- the segment ends here (or the share does): hand its sums on ----
     if (last || p + 1 == p1) {
-      // l: over the tokens (lanes and quadrants)
+      {  // l: over the tokens (lanes and quadrants)
+        float v[kHR];
 #pragma unroll
-      for (int i = 0; i < kHR; ++i) {
-        float s = (i & 1) ? l[i >> 1].y : l[i >> 1].x;
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-        if (lane == 0) red[quad * ROWS + r0 + i] = s;
+        for (int i = 0; i < kHR; ++i) v[i] = (i & 1) ? l[i >> 1].y : l[i >> 1].x;
+        lanes_reduce<kHR>(v, lane, [](float p, float q) { return p + q; });
+        if (lane < kHR) red[quad * ROWS + r0 + lane] = v[0];
       }
       __syncthreads();
       const bool earlier = p - tile < p0;  // the segment began in an earlier block
@@ -1443,8 +1459,23 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         sh.nd = len.nd;
       }
       float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<ROWS>();
+      // each row's sum, place in the output (-1: padding) and factor, once for all channels
+      int* at_row = reinterpret_cast<int*>(red + ROWS);
+      for (int r = tid; r < ROWS; r += kTreeThreads) {
+        const int row = row0 + r, di = row / rep;
+        const float lt = red[r] + red[ROWS + r] + red[2 * ROWS + r] + red[3 * ROWS + r];
+        const bool real = row < rows_all && di < len.nd;
+        if (real && !whole) {
+          slot[(size_t)ROWS * kD + r] = -rowm[r];
+          slot[(size_t)ROWS * kD + ROWS + r] = lt;
+        }
+        at_row[r] = real ? di * a.Hq + h * rep + row - di * rep : -1;
+        red[r] = !whole ? 1.f : (lt > 0.f || lt != lt) ? 1.f / lt : 0.f;
+      }
+      __syncthreads();
       const int ch = 32 * quad + lane;
       const bool fix = *nonfinite != 0;
+      const size_t out0 = (size_t)b * a.N * a.Hq * kD + ch;
 #pragma unroll 1
       for (int i = 0; i < kHR; i += 8) {
         uint32_t u[8];
@@ -1453,9 +1484,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float o = __uint_as_float(u[e]);
-          const int r = r0 + i + e, row = row0 + r, di = row / rep;
-          if (row >= rows_all || di >= len.nd) continue;  // padding
-          const float lt = red[r] + red[ROWS + r] + red[2 * ROWS + r] + red[3 * ROWS + r];
+          const int r = r0 + i + e, at = at_row[r];
+          if (at < 0) continue;
           if (fix) {  // of the drafted tokens in this block's tiles
             const int j1 = min(len.nd, (tile + 1) * kTile - len.n);
             for (int j = max(0, tile_first * kTile - len.n); j < j1; ++j) {
@@ -1464,18 +1494,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
               if ((v & 0x7C00u) == 0x7C00u) o += th2f(v);
             }
           }
-          if (whole) {
-            const size_t at = (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + ch;
-            const float val = lt > 0.f || lt != lt ? o / lt : 0.f;
-            if (a.out_fp32) reinterpret_cast<float*>(a.out)[at] = val;
-            else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(val);
-          } else {
-            slot[(size_t)r * kD + ch] = o;
-            if (ch == 0) {
-              slot[(size_t)ROWS * kD + r] = -rowm[r];
-              slot[(size_t)ROWS * kD + ROWS + r] = lt;
-            }
-          }
+          const float f = red[r];
+          o = f == 0.f ? 0.f : o * f;
+          if (!whole) slot[(size_t)r * kD + ch] = o;
+          else if (a.out_fp32) reinterpret_cast<float*>(a.out)[out0 + (size_t)at * kD] = o;
+          else reinterpret_cast<uint16_t*>(a.out)[out0 + (size_t)at * kD] = f32_to_bf16(o);
         }
       }
       tmem_before();
@@ -1483,8 +1506,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       first = true;
     }
   }
-  cp_wait<0>();
-  if (tid == 0) shared[blockIdx.x] = sh;
+  if (tid == 0) {
+    shared[blockIdx.x] = sh;
+    if (*failed) {  // a wait that ran out leaves the loop at the next barrier: let this block's copies land first
+      mbar_wait_bounded(bar_k, phase, 10000000ull);
+      mbar_wait_bounded(bar_v, phase, 10000000ull);
+    }
+  }
   tmem_before();
   __syncthreads();
   if (warp == 0) {
