@@ -1041,19 +1041,22 @@ __device__ __forceinline__ void lanes_reduce(float (&v)[N], int lane, F f) {
 
 // ---- keys of a tile. A lane takes token lane % 8 of an octet and a code word (2 bits: 16 channels, 4 bits: 8);
 //      a warp one key group and half of the words, so a lane unpacks four tokens per scale. Groups behind the
-//      quantized keys are fp16 rows. ----
-template <int KB>
+//      quantized keys are fp16 rows.
+//      free() waits until the tile may be written: the codes are unpacked into registers before. ----
+template <int KB, typename F>
 __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
                                             const unsigned char* codes, const unsigned char* scale,
-                                            const unsigned char* zero, unsigned char* dst0, int warp, int lane) {
+                                            const unsigned char* zero, unsigned char* dst0, int warp, int lane, F free) {
   constexpr int kRow = kD * KB / 8;
   const int g = warp & 3, tok = 32 * g + (lane & 7);
   if (t0 + 32 * g < len.nqk) {
     constexpr int kBlocks = (KB == 2) ? 1 : 2;   // of four words
     constexpr int kPairs = (KB == 2) ? 8 : 4;    // channel pairs of a word
+    const int w0 = (warp >> 2) * 4 * kBlocks + (lane >> 3);
+    uint32_t o[kBlocks][4][kPairs];
 #pragma unroll
     for (int blk = 0; blk < kBlocks; ++blk) {
-      const int w = (warp >> 2) * 4 * kBlocks + 4 * blk + (lane >> 3);
+      const int w = w0 + 4 * blk;
       __half2 s[kPairs], nsz[kPairs];
       const uint4* sp = reinterpret_cast<const uint4*>(scale + (g * kD + 2 * kPairs * w) * 2);
       const uint4* zp = reinterpret_cast<const uint4*>(zero + (g * kD + 2 * kPairs * w) * 2);
@@ -1073,16 +1076,21 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint32_t*>(codes + (tok + 8 * i) * kRow + 4 * w);
 #pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) o[blk][i][j] = dequant_h2(code_h2<KB>(cs0, u[i], j), s[j], nsz[j]);
+    }
+    free();
+#pragma unroll
+    for (int blk = 0; blk < kBlocks; ++blk)
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = tok + 8 * i;
-        uint32_t o[kPairs];
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) o[j] = dequant_h2(code_h2<KB>(cs0, u[i], j), s[j], nsz[j]);
-        unsigned char* dst = dst0 + (t >> 3) * 2048 + w * (kPairs * 32) + (t & 7) * 16;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-        if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+        const uint32_t(&x)[kPairs] = o[blk][i];
+        unsigned char* dst = dst0 + (t >> 3) * 2048 + (w0 + 4 * blk) * (kPairs * 32) + (t & 7) * 16;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+        if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + 128) = make_uint4(x[4], x[5], x[6], x[7]);
       }
-    }
   } else {
     const int c = (warp >> 2) * 4 + (lane >> 3);  // 16 channels c
     uint4 x[4][2];
@@ -1092,6 +1100,7 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
       x[i][0] = row8(row, 2 * c);
       x[i][1] = row8(row, 2 * c + 1);
     }
+    free();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = tok + 8 * i;
@@ -1324,7 +1333,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       tile_first = tile;
     }
     wait(bar_k, phase);
-    unpack_keys<KB>(cs0, a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane);
+    unpack_keys<KB>(cs0, a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane, [&]() {
+      if (p > p0) wait(bar_o, phase ^ 1);  // the value product before has read its weights
+      tmem_after();
+    });
     fence_proxy_async_smem();
     tmem_before();
     if (__syncthreads_or(*failed)) break;
@@ -1436,9 +1448,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       for (int k = 0; k < 8; ++k) umma_f16(tmem + ROWS, desc_v + 16 * k, desc_p + 16 * k, tree_idesc(ROWS, true), !first || k > 0);
       tree_commit(bar_o);
     }
-    wait(bar_o, phase);
-    tmem_after();
-    phase ^= 1;
     first = false;
 
     // ---- the segment ends here (or the share does): hand its sums on ----
@@ -1450,6 +1459,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         lanes_reduce<kHR>(v, lane, [](float p, float q) { return p + q; });
         if (lane < kHR) red[quad * ROWS + r0 + lane] = v[0];
       }
+      wait(bar_o, phase);
+      tmem_after();
       __syncthreads();
       const bool earlier = p - tile < p0;  // the segment began in an earlier block
       const bool whole = last && !earlier;
@@ -1505,6 +1516,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       __syncthreads();  // the row state is read before the next segment resets it
       first = true;
     }
+    phase ^= 1;
   }
   if (tid == 0) {
     shared[blockIdx.x] = sh;
