@@ -72,7 +72,11 @@ __device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
   L.tiles = L.nd > 0 ? (L.n + L.nd + kTile - 1) / kTile : 0;
   return L;
 }
-__device__ __forceinline__ int share_begin(int P, int k, int G) { return (int)((long long)P * k / G); }
+// k P / G without leaving 32 bits (k <= G, G far below 2^15)
+__device__ __forceinline__ int share_begin(int P, int k, int G) {
+  const int q = P / G;
+  return k * q + k * (P - q * G) / G;
+}
 
 // A role's place in the block's share
 struct Walk {
@@ -100,34 +104,43 @@ struct TreeShared {
   int first, open, nd, pad;
 };
 
-// The place in all positions where the block's share begins; scan: one int per thread, shared memory (two barriers).
-// Returns the share's [p0, p1).
-__device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b, int* scan, Walk& w) {
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const int chunk = (a.B + threads - 1) / threads, chunks = (a.B + chunk - 1) / chunk;  // threads with requests
-  int mine = 0;
-  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += tree_lens(a, b).tiles;
-  scan[tid] = mine;
-  __syncthreads();
-  int P = 0, before = 0;
-  for (int i = 0; i < chunks; ++i) P += scan[i];
-  P *= seg_per_b;
-  const int p0 = share_begin(P, blockIdx.x, gridDim.x), p1 = share_begin(P, blockIdx.x + 1, gridDim.x);
-  w.b = w.seg = w.tile = 0;
-  if (p0 < p1) {
-    int c0 = 0;
-    while (p0 >= (before + scan[c0]) * seg_per_b) before += scan[c0++];  // ends: p0 < P
-    w.b = c0 * chunk;
-    w.len = tree_lens(a, w.b);
-    while (p0 >= (before + w.len.tiles) * seg_per_b) {  // ends inside chunk c0
-      before += w.len.tiles;
-      w.len = tree_lens(a, ++w.b);
-    }
-    const int off = p0 - before * seg_per_b;
-    w.seg = off / w.len.tiles;
-    w.tile = off - w.seg * w.len.tiles;
+// The place in all positions where the block's share begins, and the share [p0, p1): each warp on its own, its lanes
+// take equal runs of requests.
+__device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b, int lane, Walk& w) {
+  const int run = (a.B + 31) / 32, b0 = lane * run, b1 = min(a.B, b0 + run);
+  TreeLens L = {};
+  int upto = 0;  // tiles of this lane's requests, then of all up to it
+  for (int b = b1 - 1; b >= b0; --b) {  // L: of the first one
+    L = tree_lens(a, b);
+    upto += L.tiles;
   }
-  __syncthreads();  // scan is read
+  const int mine = upto;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+    if (lane >= off) upto += v;
+  }
+  const int P = __shfl_sync(0xFFFFFFFFu, upto, 31) * seg_per_b;
+  const int p0 = share_begin(P, blockIdx.x, gridDim.x), p1 = share_begin(P, blockIdx.x + 1, gridDim.x);
+  w = {};
+  if (p0 < p1) {  // the first lane with p0 below its end
+    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, p0 < upto * seg_per_b)) - 1;
+    if (lane == src) {
+      int before = upto - mine;
+      w.b = b0;
+      while (p0 >= (before + L.tiles) * seg_per_b) {  // ends inside the run
+        before += L.tiles;
+        L = tree_lens(a, ++w.b);
+      }
+      const int off = p0 - before * seg_per_b;
+      w.len = L;
+      w.seg = off / L.tiles;
+      w.tile = off - w.seg * L.tiles;
+    }
+    int* f = reinterpret_cast<int*>(&w);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Walk) / 4); ++i) f[i] = __shfl_sync(0xFFFFFFFFu, f[i], src);
+  }
   return make_int2(p0, p1);
 }
 
@@ -414,14 +427,16 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   float* slots = reinterpret_cast<float*>(shared + gridDim.x);
 
   Walk& w = *reinterpret_cast<Walk*>(sm + L::kOffAhead + kMmaWarps * 48);  // the block's place, kept out of registers
+  Walk& ahead = *reinterpret_cast<Walk*>(sm + L::kOffAhead + warp * 48);    // the warp's copies'
   int n;
   {
     Walk x;
-    const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), x);
+    const int2 share = find_share(a, seg_per_b, lane, x);
     n = share.y - share.x;
     if (tid == 0) w = x;
-    __syncthreads();
+    if (lane == 0) ahead = x;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's blocks take places that become free
   TreeShared sh = {n > 0 ? 0 : 3, -1, 0, 0};
   if (n == 0) {
     if (tid == 0) shared[blockIdx.x] = sh;
@@ -429,7 +444,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   }
   // The warp's ring: its key group of tile i is in stage i % kSt, copied kSt - 1 tiles ahead by its own lanes.
   unsigned char* ring = sm + warp * kSt * S::kBytes;
-  Walk& ahead = *reinterpret_cast<Walk*>(sm + L::kOffAhead + warp * 48);  // kept out of registers
   // the next copy: its first token among all tokens of the cache, its quantized keys and values (from there on), the
   // tiles left in its segment and in the share
   size_t c_tok = 0;
@@ -477,11 +491,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     *nonfinite = 0;
     prefetch_fp16(a, w.len, (size_t)w.b * a.H + w.seg, w.tile * kTile, w.len.n);
   }
-  if (lane == 0) ahead = w;
   __syncwarp();
   aim();
 #pragma unroll 1
   for (int i = 1; i < kSt; ++i) copy_next(i - 1);
+  __syncthreads();  // w is there
   const CodeScale cs0;
   const int tok8 = n8 ^ ((n8 >> 2) & 1);                                       // the token at place n of eight
   const int ca = (2 * q4) ^ ((2 * q4 >> 2) & 1), cb = (2 * q4 + 1) ^ ((2 * q4 + 1) >> 2 & 1);  // at places 2 q, 2 q + 1
@@ -956,6 +970,10 @@ constexpr int kTreeThreads = 256;
 // groups 2064 bytes apart, so that eight threads with eight row groups store to different banks
 constexpr int kVRowGrp = (kTile / 8) * 128 + 16;
 
+struct Place : Walk {
+  int h, row0;  // KV head, first row
+};
+
 template <int KB, int VB, int ROWS>
 struct TreeLayout {
   static constexpr int kOffQ = 0;                                  // fp16 [ROWS x 128], K-major
@@ -967,7 +985,7 @@ struct TreeLayout {
   static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: kRaise - running maximum (log2)
   static constexpr int kOffF = kOffM + ROWS * 4;                   // float [ROWS]: rescale factor
   static constexpr int kOffRed = kOffF + ROWS * 4;                 // float [4][ROWS]: per lane quadrant
-  static constexpr int kOffWalk = kOffRed + 4 * ROWS * 4;          // Walk [2]: this position's and the next one's
+  static constexpr int kOffWalk = kOffRed + 4 * ROWS * 4;          // Place [2]: this position's and the next one's
   static constexpr int kOffBar = kOffWalk + 96;                    // mbarriers, TMEM address, flags
   static constexpr int kSmem = kOffBar + 64;
   static constexpr uint32_t kCols = 2 * ROWS < 32 ? 32 : 2 * ROWS;  // TMEM: S^T, O^T
@@ -1231,16 +1249,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 
   TreeShared* shared = reinterpret_cast<TreeShared*>(a.part);
   float* slots = reinterpret_cast<float*>(shared + gridDim.x);
-  Walk* place = reinterpret_cast<Walk*>(sm + L::kOffWalk);  // of position p in place[p & 1] (kept out of registers)
+  Place* place = reinterpret_cast<Place*>(sm + L::kOffWalk);  // of position p in place[p & 1] (kept out of registers)
   int p0, p1;
   {
     Walk x;
-    const int2 share = find_share(a, seg_per_b, reinterpret_cast<int*>(sm), x);
+    const int2 share = find_share(a, seg_per_b, lane, x);
     p0 = share.x;
     p1 = share.y;
-    if (tid == 0) place[p0 & 1] = x;
-    __syncthreads();
+    if (tid == 0) place[p0 & 1] = {x, x.seg / n_rt, x.seg % n_rt * ROWS};
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's blocks take places that become free
   TreeShared sh = {p0 < p1 ? 0 : 3, -1, 0, 0};
   if (p0 >= p1) {
     if (tid == 0) shared[blockIdx.x] = sh;
@@ -1255,11 +1273,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   }
   unsigned char* stage = sm + L::kOffStage;
   // by one thread each, of warps that issue no products
-  auto keys_of = [&](const Walk& x) {
-    bulk_keys<KB, VB>(a, x.len, (size_t)x.b * a.H + x.seg / n_rt, x.tile * kTile, stage, bar_k);
+  auto keys_of = [&](const Place& x) {
+    bulk_keys<KB, VB>(a, x.len, (size_t)x.b * a.H + x.h, x.tile * kTile, stage, bar_k);
   };
-  auto values_of = [&](const Walk& x) {
-    const size_t bh = (size_t)x.b * a.H + x.seg / n_rt;
+  auto values_of = [&](const Place& x) {
+    const size_t bh = (size_t)x.b * a.H + x.h;
     bulk_values<KB, VB>(a, x.len, bh, x.tile * kTile, stage, bar_v);
     prefetch_fp16(a, x.len, bh, x.tile * kTile, (x.tile + 1) * kTile);
   };
@@ -1271,12 +1289,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     *failed = 0;
     *nonfinite = 0;
     fence_mbar_init();
-    keys_of(place[p0 & 1]);
-    values_of(place[p0 & 1]);
   }
   tmem_before();
   __syncthreads();
   tmem_after();
+  if (tid == 96) keys_of(place[p0 & 1]);
+  if (tid == 224) values_of(place[p0 & 1]);
   const uint32_t tmem = *tmem_slot;
   const int quad = warp & 3, half = warp >> 2;            // TMEM lane quadrant, half of the rows
   const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
@@ -1298,26 +1316,34 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   };
 
   for (int p = p0; p < p1; ++p) {
-    const Walk& w = place[p & 1];
-    const Walk& nw = place[(p + 1) & 1];
+    const Place& w = place[p & 1];
+    const Place& nw = place[(p + 1) & 1];
     const TreeLens& len = w.len;
-    const int b = w.b, h = w.seg / n_rt, row0 = (w.seg - h * n_rt) * ROWS, tile = w.tile, t0 = tile * kTile;
+    const int b = w.b, h = w.h, row0 = w.row0, tile = w.tile, t0 = tile * kTile;
     const bool last = w.last(), more = p + 1 < p1;
     if (tid == 32 && more) {  // shown to the others by the next barrier
       Walk x = w;
       x.next(a, seg_per_b, true);
-      place[(p + 1) & 1] = x;
+      place[(p + 1) & 1] = {x, x.seg / n_rt, x.seg % n_rt * ROWS};
     }
     if (first) {
       // ---- the segment's query rows, masks and running state (8 lanes a row) ----
 #pragma unroll
       for (int i = 0; i < kHR / 2; ++i) l[i] = make_float2(0.f, 0.f);
-#pragma unroll 1
-      for (int i = tid; i < ROWS * 8; i += kTreeThreads) {
-        const int r = i >> 3, c = i & 7;
-        uint32_t u[8], o[8];
-        const bool real = load_query(a, len, b, h, row0 + r, c, u);
-        const float back = query_fp16<14>(u, o, scale_log2);
+      constexpr int kPart = ROWS * 8 / kTreeThreads;
+      uint32_t u[kPart][8];
+      uint64_t sees[kPart];
+#pragma unroll
+      for (int x = 0; x < kPart; ++x) {
+        const int r = (tid + x * kTreeThreads) >> 3;
+        const bool real = load_query(a, len, b, h, row0 + r, tid & 7, u[x]);
+        sees[x] = real ? a.mask[(size_t)b * a.N + (row0 + r) / rep] : 0ull;
+      }
+#pragma unroll
+      for (int x = 0; x < kPart; ++x) {
+        const int r = (tid + x * kTreeThreads) >> 3, c = tid & 7;
+        uint32_t o[8];
+        const float back = query_fp16<14>(u[x], o, scale_log2);
         uint4 x0, x1;
         pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
         unsigned char* dst = sm + L::kOffQ + (r >> 3) * 2048 + c * 256 + (r & 7) * 16;
@@ -1326,7 +1352,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         if (c == 0) {
           rowc[r] = back;
           rowm[r] = FLT_MAX;
-          mask[r] = real ? a.mask[(size_t)b * a.N + (row0 + r) / rep] : 0ull;
+          mask[r] = sees[x];
         }
       }
       if (tid == 0) *nonfinite = 0;
@@ -1459,8 +1485,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         lanes_reduce<kHR>(v, lane, [](float p, float q) { return p + q; });
         if (lane < kHR) red[quad * ROWS + r0 + lane] = v[0];
       }
-      wait(bar_o, phase);
-      tmem_after();
       __syncthreads();
       const bool earlier = p - tile < p0;  // the segment began in an earlier block
       const bool whole = last && !earlier;
@@ -1483,6 +1507,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         at_row[r] = real ? di * a.Hq + h * rep + row - di * rep : -1;
         red[r] = !whole ? 1.f : (lt > 0.f || lt != lt) ? 1.f / lt : 0.f;
       }
+      wait(bar_o, phase);
+      tmem_after();
       __syncthreads();
       const int ch = 32 * quad + lane;
       const bool fix = *nonfinite != 0;
@@ -1537,12 +1563,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 // block k of the attention began and left open; a warp takes a row, a lane four channels.
 constexpr int kMergeThreads = 128;
 template <int ROWS>
-__global__ void __launch_bounds__(kMergeThreads) kivi_tree_merge_kernel(const KiviTreeArgs a, const int G) {
+__global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_merge_kernel(const KiviTreeArgs a, const int G) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead of the attention's end
   const int lane = threadIdx.x & 31, k = blockIdx.x, r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
   const TreeShared* shared = reinterpret_cast<const TreeShared*>(a.part);
   const float* slots = reinterpret_cast<const float*>(shared + G);
   const int seg_all = shared[k].open;
+  int f = k + 1 + lane < G ? shared[k + 1 + lane].first : 2;
   if (seg_all < 0) return;
   const int rep = a.Hq / a.H, rows_all = a.N * rep, n_rt = (rows_all + ROWS - 1) / ROWS, seg_per_b = a.H * n_rt;
   const int b = seg_all / seg_per_b, seg = seg_all % seg_per_b, h = seg / n_rt;
@@ -1550,50 +1577,59 @@ __global__ void __launch_bounds__(kMergeThreads) kivi_tree_merge_kernel(const Ki
   if (row >= rows_all || di >= shared[k].nd) return;
   const size_t mo = (size_t)ROWS * kD + r, lo = mo + ROWS;
   const float* own = slots + ((size_t)k * 2 + 1) * slot_floats<ROWS>();
-  // the blocks behind k that hold a part, 32 at a time: slot 0 of those, up to the one it ends in
-  auto part_of = [&](int kk, bool& ends) {
-    const int f = kk < G ? shared[kk].first : 2;
-    ends = f == 2;
-    return kk < G && (f == 1 || f == 2) ? slots + (size_t)kk * 2 * slot_floats<ROWS>() : nullptr;
-  };
-  float M = own[mo];
-  for (int base = k + 1;; base += 32) {
-    bool ends;
-    const float* s = part_of(base + lane, ends);
-    const uint32_t end = __ballot_sync(0xFFFFFFFFu, ends);
-    float m = (s && lane <= (end ? __ffs(end) - 1 : 31)) ? s[mo] : -FLT_MAX;
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-    M = fmaxf(M, m);
-    if (end) break;
-  }
-  float lt = own[lo];
-  const float wo = lt == 0.f ? 0.f : exp2_approx(own[mo] - M);  // 0: the row saw nothing there
-  lt *= wo;
+  float M = own[mo], lt = own[lo];
   float4 o = *reinterpret_cast<const float4*>(own + (size_t)r * kD + 4 * lane);
-  o = wo == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
+  if (lt == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // the row saw nothing there
+  // the blocks behind k that hold a part, 32 at a time: slot 0 of those, up to the one it ends in
+  constexpr int kBatch = ROWS <= 16 ? 8 : 4;  // parts whose sums are on their way at once
   for (int base = k + 1;; base += 32) {
-    bool ends;
-    const float* s = part_of(base + lane, ends);
-    const uint32_t end = __ballot_sync(0xFFFFFFFFu, ends);
-    const int cnt = end ? __ffs(end) : 32;
-    float lk = (s && lane < cnt) ? s[lo] : 0.f;
-    const float wk = lk == 0.f ? 0.f : exp2_approx(s[mo] - M);
-    lk = wk == 0.f ? 0.f : lk * wk;
+    const uint32_t end = __ballot_sync(0xFFFFFFFFu, f == 2);
+    const uint32_t upto = end ? (end & -end) * 2 - 1 : 0xFFFFFFFFu;
+    uint32_t parts = __ballot_sync(0xFFFFFFFFu, f == 1 || f == 2) & upto;
+    const float* s = slots + (size_t)(base + lane) * 2 * slot_floats<ROWS>();
+    const bool has = (parts >> lane) & 1u;
+    float m = has ? s[mo] : -FLT_MAX, l = has ? s[lo] : 0.f;
+    float4 v[kBatch];
+    int at[kBatch];
+    auto load = [&]() {
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) lk += __shfl_xor_sync(0xFFFFFFFFu, lk, off);
-    lt += lk;
-#pragma unroll 4
-    for (int j = 0; j < cnt; ++j) {
-      const float wj = __shfl_sync(0xFFFFFFFFu, wk, j);
-      if (wj == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(slots + (size_t)(base + j) * 2 * slot_floats<ROWS>() + (size_t)r * kD + 4 * lane);
-      o.x = fmaf(wj, v.x, o.x);
-      o.y = fmaf(wj, v.y, o.y);
-      o.z = fmaf(wj, v.z, o.z);
-      o.w = fmaf(wj, v.w, o.w);
+      for (int e = 0; e < kBatch; ++e) {
+        at[e] = parts ? __ffs(parts) - 1 : -1;
+        parts &= parts - 1;
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at[e] >= 0)
+          v[e] = *reinterpret_cast<const float4*>(slots + (size_t)(base + at[e]) * 2 * slot_floats<ROWS>() + (size_t)r * kD + 4 * lane);
+      }
+    };
+    load();
+    float top = l == 0.f ? -FLT_MAX : m;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    top = fmaxf(M, top);
+    // a part that saw nothing stays out; one with a score that is not a number says so in the result
+    auto weight = [&](float l, float m) { return l == 0.f ? 0.f : l != l ? 1.f : exp2_approx(m - top); };
+    const float w0 = weight(lt, M), w = weight(l, m);
+    M = top;
+    l = w == 0.f ? 0.f : l * w;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+    lt = (w0 == 0.f ? 0.f : lt * w0) + l;
+    o = w0 == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
+    for (;;) {
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const float we = __shfl_sync(0xFFFFFFFFu, w, at[e] & 31);
+        if (at[e] < 0 || we == 0.f) continue;
+        o.x = fmaf(we, v[e].x, o.x);
+        o.y = fmaf(we, v[e].y, o.y);
+        o.z = fmaf(we, v[e].z, o.z);
+        o.w = fmaf(we, v[e].w, o.w);
+      }
+      if (!parts) break;
+      load();
     }
     if (end) break;
+    f = base + 32 + lane < G ? shared[base + 32 + lane].first : 2;
   }
   const bool none = !(lt > 0.f || lt != lt);
   const size_t at = (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 4 * lane;
