@@ -436,7 +436,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     if (tid == 0) w = x;
     if (lane == 0) ahead = x;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's blocks take places that become free
   TreeShared sh = {n > 0 ? 0 : 3, -1, 0, 0};
   if (n == 0) {
     if (tid == 0) shared[blockIdx.x] = sh;
