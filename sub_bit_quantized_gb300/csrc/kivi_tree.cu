@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// n / d: the high product is at most one too small, n (1 + 1 / d) / 2^32 < 1
+__device__ __forceinline__ int div_by(int n, const IntDiv& v) {
+  int q = (int)__umulhi((uint32_t)n, v.inv);
+  if (n - q * v.d >= v.d) ++q;
+  return q;
+}
+
 // The work of a call, the same for every block: segment (b, h, row tile) has T_b tiles (its cached
 // and drafted tokens), all segments in the order b, h, row tile form one list of P tile positions,
 // and block k of G takes positions [k P / G, (k + 1) P / G).
@@ -65,17 +72,17 @@ struct TreeLens {
 };
 __device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
   TreeLens L;
-  L.nqk = min(max(a.n_quant_k[b], 0), a.max_tokens) / kGroupT * kGroupT;
+  L.nqk = min(max(a.n_quant_k[b], 0), a.max_tokens) & -kGroupT;
   L.nqv = (a.residual > 0) ? min(max(a.n_quant_v[b], 0), L.nqk) : L.nqk;
   L.n = L.nqk + max(0, min(a.n_tok[b] - L.nqk, a.residual));
   L.nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
-  L.tiles = L.nd > 0 ? (L.n + L.nd + kTile - 1) / kTile : 0;
+  L.tiles = L.nd > 0 ? (int)((uint32_t)(L.n + L.nd + kTile - 1) / kTile) : 0;
   return L;
 }
 // k P / G without leaving 32 bits (k <= G, G far below 2^15)
-__device__ __forceinline__ int share_begin(int P, int k, int G) {
-  const int q = P / G;
-  return k * q + k * (P - q * G) / G;
+__device__ __forceinline__ int share_begin(int P, int k, const IntDiv& G) {
+  const int q = div_by(P, G);
+  return k * q + div_by(k * (P - q * G.d), G);
 }
 
 // A role's place in the block's share
@@ -110,6 +117,7 @@ __device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b,
   const int run = (a.B + 31) / 32, b0 = lane * run, b1 = min(a.B, b0 + run);
   TreeLens L = {};
   int upto = 0;  // tiles of this lane's requests, then of all up to it
+#pragma unroll 1
   for (int b = b1 - 1; b >= b0; --b) {  // L: of the first one
     L = tree_lens(a, b);
     upto += L.tiles;
@@ -121,7 +129,7 @@ __device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b,
     if (lane >= off) upto += v;
   }
   const int P = __shfl_sync(0xFFFFFFFFu, upto, 31) * seg_per_b;
-  const int p0 = share_begin(P, blockIdx.x, gridDim.x), p1 = share_begin(P, blockIdx.x + 1, gridDim.x);
+  const int p0 = share_begin(P, blockIdx.x, a.blocks), p1 = share_begin(P, blockIdx.x + 1, a.blocks);
   w = {};
   if (p0 < p1) {  // the first lane with p0 below its end
     const int src = __ffs(__ballot_sync(0xFFFFFFFFu, p0 < upto * seg_per_b)) - 1;
@@ -302,18 +310,21 @@ __device__ __forceinline__ float query_fp16(const uint32_t (&w)[8], uint32_t (&o
   const int sh = (ex == 0 || ex == 255) ? 0 : TOP + 127 - ex;
   const float f1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = pack_h2(bf16_lo(w[e]) * f1 * f2, bf16_hi(w[e]) * f1 * f2);
+  for (int e = 0; e < 8; ++e) {
+    const float2 y = __fmul2_rn(__fmul2_rn(make_float2(bf16_lo(w[e]), bf16_hi(w[e])), make_float2(f1, f1)), make_float2(f2, f2));
+    o[e] = pack_h2(y.x, y.y);
+  }
   return scale / f1 / f2;
 }
 // 16 channels 16c .. of query row `row` of (b, KV head h), zero for padding
 __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int row, int c,
                                            uint32_t (&w)[8]) {
-  const int rep = a.Hq / a.H, di = row / rep;
-  const bool real = row < a.N * rep && di < len.nd;
+  const int di = div_by(row, a.rep);
+  const bool real = row < a.N * a.rep.d && di < len.nd;
   uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
   if (real) {
     const uint4* src = reinterpret_cast<const uint4*>(
-        a.q + (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 16 * c);
+        a.q + (((size_t)b * a.N + di) * a.Hq + (size_t)h * a.rep.d + row - di * a.rep.d) * kD + 16 * c);
     u[0] = __ldg(src);
     u[1] = __ldg(src + 1);
   }
@@ -422,7 +433,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   int* nonfinite = reinterpret_cast<int*>(sm + L::kOffFlag);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = lane & 3, n8 = lane >> 2;
-  const int rep = a.Hq / a.H, rows_all = a.N * rep, seg_per_b = a.H;  // one row tile
+  const int rep = a.rep.d, rows_all = a.N * rep, seg_per_b = a.H;  // one row tile
   TreeShared* shared = reinterpret_cast<TreeShared*>(a.part);
   float* slots = reinterpret_cast<float*>(shared + gridDim.x);
 
@@ -519,7 +530,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       dst[NT * 32] = x1;
       if (c == 0) {
         rowc[r] = back;
-        mask[r] = real ? a.mask[(size_t)w.b * a.N + r / rep] : 0ull;
+        mask[r] = real ? a.mask[(size_t)w.b * a.N + div_by(r, a.rep)] : 0ull;
       }
     }
     __syncthreads();  // queries staged
@@ -760,7 +771,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               }
           }
         } else {  // fp16 rows, and the group in which the quantized values end
-          const int place = a.residual > 0 ? tw % a.residual : 0;
+          const int place = a.residual > 0 ? tw - div_by(tw, a.ring) * a.residual : 0;
 #pragma unroll 1
           for (int hw = 0; hw < 2; ++hw) {  // channels 16 n8 + 8 hw .. + 7
             uint32_t x[8][4];  // octet y / 2, place 2 q + y % 2
@@ -896,7 +907,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 8 * nt + 2 * q4 + e, di = r / rep;
+          const int r = 8 * nt + 2 * q4 + e, di = div_by(r, a.rep);
           if (r >= rows_all || di >= w.len.nd) continue;  // padding
           float v[16];
 #pragma unroll
@@ -917,7 +928,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
             const bool some = ls > 0.f || ls != ls;
 #pragma unroll
             for (int c = 0; c < 16; ++c) v[c] = some ? v[c] / ls : 0.f;
-            const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r % rep) * kD + 16 * n8;
+            const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r - di * rep) * kD + 16 * n8;
             if (a.out_fp32) {
               float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
 #pragma unroll
@@ -1030,6 +1041,21 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
                : "r"(taddr)
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+  tmem_wait_ld();
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
@@ -1038,6 +1064,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                : "memory");
 }
 
+// the largest of the lanes' values that are numbers
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+  return r;
+}
 // Reduces N (a power of two, up to 32) values over a warp's lanes: v[0] of lane i < N is value i's.
 template <int N, typename F>
 __device__ __forceinline__ void lanes_reduce(float (&v)[N], int lane, F f) {
@@ -1143,7 +1175,7 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
   const unsigned char* cw = codes + 8 * oct * kRow + ((VB == 2) ? (c >> 1) : c) * 4;
   const uint16_t* sp = reinterpret_cast<const uint16_t*>(scale) + 8 * oct * 4 + (c >> 2);
   const uint16_t* zp = reinterpret_cast<const uint16_t*>(zero) + 8 * oct * 4 + (c >> 2);
-  if (t0 + 8 * oct + 8 <= len.nqv) {
+  if (t0 + 8 * oct < len.nqv) {
     uint32_t w[8];  // place i of the octet: token i ^ flip
     __half2 s[4], nsz[4];
 #pragma unroll
@@ -1181,44 +1213,41 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
         }
       }
     }
-  } else {
-    uint32_t x[8][4];
-    const int place = a.residual > 0 ? (t0 + 8 * oct) % a.residual : 0;
+  }
+  if (t0 + 8 * oct + 8 > len.nqv) {
+    // tokens behind the quantized values, over what was unpacked for them from the end of the stage
+    const int t8 = t0 + 8 * oct, place = a.residual > 0 ? t8 - div_by(t8, a.ring) * a.residual : 0;
+#pragma unroll 1
+    for (int i = 0; i < 8; i += 4) {
+      uint4 u[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = t0 + 8 * oct + (i ^ flip);
-      const uint4 u = t >= len.nqv ? row8(fp16_value(a, len, b, h, t, ring_place(place, i ^ flip, a.residual)), c) : make_uint4(0u, 0u, 0u, 0u);
-      x[i][0] = u.x;
-      x[i][1] = u.y;
-      x[i][2] = u.z;
-      x[i][3] = u.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = t0 + 8 * oct + (i ^ flip);
-      if (t < len.nqv) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(cw + (i ^ flip) * kRow) >> ((VB == 2) ? 16 * (c & 1) : 0);
-        const uint4 u = scalar_dequant8<VB>(w, th2f(sp[(i ^ flip) * 4]), th2f(zp[(i ^ flip) * 4]));
-        x[i][0] = u.x;
-        x[i][1] = u.y;
-        x[i][2] = u.z;
-        x[i][3] = u.w;
-      } else if (t >= len.n) {
-        // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
-        // every row's weight, 0 for the others: one that is not finite is staged as 0 and added at the
-        // end to the rows that see it.
-        bool any = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) any |= drop_nonfinite(x[i][e]);
-        if (any) *nonfinite = 1;
+      for (int e = 0; e < 4; ++e) {
+        u[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (t8 + i + e >= len.nqv) u[e] = row8(fp16_value(a, len, b, h, t8 + i + e, ring_place(place, i + e, a.residual)), c);
       }
-    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t o[4];
+      for (int e = 0; e < 4; ++e) {
+        const int t = t8 + i + e;
+        if (t < len.nqv) continue;
+        uint32_t x[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+        // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by every row's
+        // weight, 0 for the others: one that is not finite is staged as 0 and added at the end to the rows that see it.
+        if (t >= len.n) {
+          const __half2 nil = __float2half2_rn(0.f);
+          const __half2 z = __hfma2(as_h2(x[0]), nil, __hfma2(as_h2(x[1]), nil, __hfma2(as_h2(x[2]), nil, __hmul2(as_h2(x[3]), nil))));
+          if (!__hbeq2(z, nil)) {  // 0 times a number that is not finite is not 0
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __byte_perm(x[2 * i][e >> 1], x[2 * i + 1][e >> 1], (e & 1) ? 0x7632 : 0x5410);
-      *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int y = 0; y < 4; ++y) drop_nonfinite(x[y]);
+            *nonfinite = 1;
+          }
+        }
+        unsigned char* at = dst + ((i + e) ^ flip) * 2;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          *reinterpret_cast<uint16_t*>(at + 32 * y) = (uint16_t)x[y];
+          *reinterpret_cast<uint16_t*>(at + 32 * y + 16) = (uint16_t)(x[y] >> 16);
+        }
+      }
     }
   }
 }
@@ -1242,20 +1271,23 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   int* nonfinite = reinterpret_cast<int*>(tmem_slot + 2);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rep = a.Hq / a.H, rows_all = a.N * rep;
-  const int n_rt = (rows_all + ROWS - 1) / ROWS;  // row tiles of a KV head
-  const int seg_per_b = a.H * n_rt;
+  const int rep = a.rep.d, rows_all = a.N * rep;
+  const int seg_per_b = a.segs.d;
 
   TreeShared* shared = reinterpret_cast<TreeShared*>(a.part);
   float* slots = reinterpret_cast<float*>(shared + gridDim.x);
   Place* place = reinterpret_cast<Place*>(sm + L::kOffWalk);  // of position p in place[p & 1] (kept out of registers)
+  auto place_of = [&](const Walk& x) {
+    const int h = div_by(x.seg, a.row_tiles);
+    return Place{x, h, (x.seg - h * a.row_tiles.d) * ROWS};
+  };
   int p0, p1;
   {
     Walk x;
     const int2 share = find_share(a, seg_per_b, lane, x);
     p0 = share.x;
     p1 = share.y;
-    if (tid == 0) place[p0 & 1] = {x, x.seg / n_rt, x.seg % n_rt * ROWS};
+    if (tid == 0) place[p0 & 1] = place_of(x);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's blocks take places that become free
   TreeShared sh = {p0 < p1 ? 0 : 3, -1, 0, 0};
@@ -1323,26 +1355,19 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     if (tid == 32 && more) {  // shown to the others by the next barrier
       Walk x = w;
       x.next(a, seg_per_b, true);
-      place[(p + 1) & 1] = {x, x.seg / n_rt, x.seg % n_rt * ROWS};
+      place[(p + 1) & 1] = place_of(x);
     }
     if (first) {
       // ---- the segment's query rows, masks and running state (8 lanes a row) ----
 #pragma unroll
       for (int i = 0; i < kHR / 2; ++i) l[i] = make_float2(0.f, 0.f);
-      constexpr int kPart = ROWS * 8 / kTreeThreads;
-      uint32_t u[kPart][8];
-      uint64_t sees[kPart];
-#pragma unroll
-      for (int x = 0; x < kPart; ++x) {
-        const int r = (tid + x * kTreeThreads) >> 3;
-        const bool real = load_query(a, len, b, h, row0 + r, tid & 7, u[x]);
-        sees[x] = real ? a.mask[(size_t)b * a.N + (row0 + r) / rep] : 0ull;
-      }
-#pragma unroll
-      for (int x = 0; x < kPart; ++x) {
-        const int r = (tid + x * kTreeThreads) >> 3, c = tid & 7;
-        uint32_t o[8];
-        const float back = query_fp16<14>(u[x], o, scale_log2);
+#pragma unroll 1  // run once per segment: fewer instructions to fetch
+      for (int i = tid; i < ROWS * 8; i += kTreeThreads) {
+        const int r = i >> 3, c = i & 7;
+        uint32_t u[8], o[8];
+        const bool real = load_query(a, len, b, h, row0 + r, c, u);
+        const uint64_t sees = real ? a.mask[(size_t)b * a.N + div_by(row0 + r, a.rep)] : 0ull;
+        const float back = query_fp16<14>(u, o, scale_log2);
         uint4 x0, x1;
         pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
         unsigned char* dst = sm + L::kOffQ + (r >> 3) * 2048 + c * 256 + (r & 7) * 16;
@@ -1351,7 +1376,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         if (c == 0) {
           rowc[r] = back;
           rowm[r] = FLT_MAX;
-          mask[r] = sees[x];
+          mask[r] = sees;
         }
       }
       if (tid == 0) *nonfinite = 0;
@@ -1394,12 +1419,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     }
     if (t0 + kTile > len.n) {  // drafted tokens in the tile, or none at all behind the last one
       const int dj = t0 + tt - len.n;
-      if (dj >= 0) {
+      uint32_t sees = dj < 0 ? 0xFFFFFFFFu : 0u;  // rows that see this thread's token
+      if (dj >= 0 && dj < len.nd) {
+#pragma unroll 4
+        for (int i = 0; i < kHR; ++i) sees |= (uint32_t)((mask[r0 + i] >> dj) & 1ull) << i;
+      }
 #pragma unroll
-        for (int i = 0; i < kHR / 2; ++i) {
-          if (dj >= len.nd || !((mask[r0 + 2 * i] >> dj) & 1ull)) x[i].x = -INFINITY;
-          if (dj >= len.nd || !((mask[r0 + 2 * i + 1] >> dj) & 1ull)) x[i].y = -INFINITY;
-        }
+      for (int i = 0; i < kHR / 2; ++i) {
+        if (!((sees >> (2 * i)) & 1u)) x[i].x = -INFINITY;
+        if (!((sees >> (2 * i + 1)) & 1u)) x[i].y = -INFINITY;
       }
     }
     float most = -INFINITY;
@@ -1416,11 +1444,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     if (raise) {
       // ---- raise the running maxima of the rows with a score past them ----
       {
-        float v[kHR];
+        float mine = 0.f;
 #pragma unroll
-        for (int i = 0; i < kHR; ++i) v[i] = (i & 1) ? x[i >> 1].y : x[i >> 1].x;
-        lanes_reduce<kHR>(v, lane, [](float p, float q) { return fmaxf(p, q); });
-        if (lane < kHR) red[quad * ROWS + r0 + lane] = v[0];
+        for (int i = 0; i < kHR; ++i) {
+          const float v = warp_max((i & 1) ? x[i >> 1].y : x[i >> 1].x);
+          if (lane == i) mine = v;
+        }
+        if (lane < kHR) red[quad * ROWS + r0 + lane] = mine;
       }
       __syncthreads();
       for (int r = tid; r < ROWS; r += kTreeThreads) {
@@ -1493,48 +1523,58 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         sh.nd = len.nd;
       }
       float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<ROWS>();
-      // each row's sum, place in the output (-1: padding) and factor, once for all channels
-      int* at_row = reinterpret_cast<int*>(red + ROWS);
-      for (int r = tid; r < ROWS; r += kTreeThreads) {
-        const int row = row0 + r, di = row / rep;
+      // each row's place in the output or the slot (-1: padding) and factor, once for all channels
+      int* at_row = reinterpret_cast<int*>(rowc);
+      if (tid < ROWS) {
+        const int r = tid, row = row0 + r, di = div_by(row, a.rep);
         const float lt = red[r] + red[ROWS + r] + red[2 * ROWS + r] + red[3 * ROWS + r];
         const bool real = row < rows_all && di < len.nd;
         if (real && !whole) {
           slot[(size_t)ROWS * kD + r] = -rowm[r];
           slot[(size_t)ROWS * kD + ROWS + r] = lt;
         }
-        at_row[r] = real ? di * a.Hq + h * rep + row - di * rep : -1;
-        red[r] = !whole ? 1.f : (lt > 0.f || lt != lt) ? 1.f / lt : 0.f;
+        at_row[r] = !real ? -1 : whole ? di * a.Hq + h * rep + row - di * rep : r;
+        rowf[r] = !whole ? 1.f : (lt > 0.f || lt != lt) ? 1.f / lt : 0.f;
       }
       wait(bar_o, phase);
       tmem_after();
       __syncthreads();
       const int ch = 32 * quad + lane;
-      const bool fix = *nonfinite != 0;
-      const size_t out0 = (size_t)b * a.N * a.Hq * kD + ch;
+      if (*nonfinite != 0) {  // of the drafted tokens in this block's tiles
+        const int j0 = max(0, tile_first * kTile - len.n), j1 = min(len.nd, (tile + 1) * kTile - len.n);
 #pragma unroll 1
-      for (int i = 0; i < kHR; i += 8) {
-        uint32_t u[8];
-        tmem_ld8(t_lane + ROWS + r0 + i, u);
+        for (int r = r0; r < r0 + kHR; ++r) {
+          if (at_row[r] < 0) continue;
+          float o = tmem_ld1(t_lane + ROWS + r);
+#pragma unroll 1
+          for (int j = j0; j < j1; ++j) {
+            if (!((mask[r] >> j) & 1ull)) continue;
+            const uint16_t v = a.v_draft[(((size_t)b * a.N + j) * a.H + h) * kD + ch];
+            if ((v & 0x7C00u) == 0x7C00u) o += th2f(v);
+          }
+          tmem_st1(t_lane + ROWS + r, o);
+        }
+        tmem_wait_st();
+      }
+      const bool f32 = !whole || a.out_fp32;
+      const size_t out0 = (size_t)b * a.N * a.Hq * kD + ch;
+      float* to32 = whole ? reinterpret_cast<float*>(a.out) + out0 : slot + ch;
+      uint16_t* to16 = reinterpret_cast<uint16_t*>(a.out) + out0;
+#pragma unroll 1
+      for (int i = r0; i < r0 + kHR; i += 4) {
+        uint32_t u[4];
+        tmem_ld4(t_lane + ROWS + i, u);
+        const float4 f4 = *reinterpret_cast<const float4*>(rowf + i);
+        const int4 at4 = *reinterpret_cast<const int4*>(at_row + i);
+        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+        const int at[4] = {at4.x, at4.y, at4.z, at4.w};
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float o = __uint_as_float(u[e]);
-          const int r = r0 + i + e, at = at_row[r];
-          if (at < 0) continue;
-          if (fix) {  // of the drafted tokens in this block's tiles
-            const int j1 = min(len.nd, (tile + 1) * kTile - len.n);
-            for (int j = max(0, tile_first * kTile - len.n); j < j1; ++j) {
-              if (!((mask[r] >> j) & 1ull)) continue;
-              const uint16_t v = a.v_draft[(((size_t)b * a.N + j) * a.H + h) * kD + ch];
-              if ((v & 0x7C00u) == 0x7C00u) o += th2f(v);
-            }
-          }
-          const float f = red[r];
-          o = f == 0.f ? 0.f : o * f;
-          if (!whole) slot[(size_t)r * kD + ch] = o;
-          else if (a.out_fp32) reinterpret_cast<float*>(a.out)[out0 + (size_t)at * kD] = o;
-          else reinterpret_cast<uint16_t*>(a.out)[out0 + (size_t)at * kD] = f32_to_bf16(o);
+        for (int e = 0; e < 4; ++e) {
+          const float o = f[e] == 0.f ? 0.f : __uint_as_float(u[e]) * f[e];
+          if (at[e] < 0) continue;
+          if (f32) to32[(size_t)at[e] * kD] = o;
+          else to16[(size_t)at[e] * kD] = f32_to_bf16(o);
         }
       }
       tmem_before();
@@ -1570,9 +1610,9 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
   const int seg_all = shared[k].open;
   int f = k + 1 + lane < G ? shared[k + 1 + lane].first : 2;
   if (seg_all < 0) return;
-  const int rep = a.Hq / a.H, rows_all = a.N * rep, n_rt = (rows_all + ROWS - 1) / ROWS, seg_per_b = a.H * n_rt;
-  const int b = seg_all / seg_per_b, seg = seg_all % seg_per_b, h = seg / n_rt;
-  const int row = (seg - h * n_rt) * ROWS + r, di = row / rep;
+  const int rep = a.rep.d, rows_all = a.N * rep;
+  const int b = div_by(seg_all, a.segs), seg = seg_all - b * a.segs.d, h = div_by(seg, a.row_tiles);
+  const int row = (seg - h * a.row_tiles.d) * ROWS + r, di = div_by(row, a.rep);
   if (row >= rows_all || di >= shared[k].nd) return;
   const size_t mo = (size_t)ROWS * kD + r, lo = mo + ROWS;
   const float* own = slots + ((size_t)k * 2 + 1) * slot_floats<ROWS>();
@@ -1631,7 +1671,7 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
     f = base + 32 + lane < G ? shared[base + 32 + lane].first : 2;
   }
   const bool none = !(lt > 0.f || lt != lt);
-  const size_t at = (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row % rep) * kD + 4 * lane;
+  const size_t at = (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row - di * rep) * kD + 4 * lane;
   float val[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) val[e] = none ? 0.f : val[e] / lt;
@@ -1660,6 +1700,8 @@ int tree_blocks(int r) {
   return sm_count_tree() * (r == 8 ? 4 : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
 }
 
+IntDiv int_div(int d) { return {d, d > 0 ? 0xFFFFFFFFu / (uint32_t)d : 0u}; }
+
 template <int ROWS>
 cudaError_t launch_merge(const KiviTreeArgs& a, int G, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
@@ -1674,10 +1716,16 @@ cudaError_t launch_merge(const KiviTreeArgs& a, int G, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kivi_tree_merge_kernel<ROWS>, a, G);
 }
 template <int ROWS, typename K>
-cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& a, cudaStream_t st) {
+cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& args, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int G = tree_blocks(ROWS);
+  const int G = tree_blocks(ROWS), rep = args.Hq / args.H, row_tiles = (args.N * rep + ROWS - 1) / ROWS;
+  KiviTreeArgs a = args;
+  a.rep = int_div(rep);
+  a.row_tiles = int_div(row_tiles);
+  a.segs = int_div(a.H * row_tiles);
+  a.blocks = int_div(G);
+  a.ring = int_div(a.residual);
   kernel<<<G, threads, smem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_merge<ROWS>(a, G, st);

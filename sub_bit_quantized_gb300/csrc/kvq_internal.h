@@ -211,6 +211,9 @@ int kivi_attn_max_tok_per_split(int residual);
 cudaError_t launch_kivi_attn(const KiviAttnArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- tree attention
+struct IntDiv {                    // a divisor of the launch: n / d for 0 <= n < 2^31 by one high product and one step
+  int d; uint32_t inv;             // inv = (2^32 - 1) / d
+};
 struct KiviTreeArgs {
   const uint8_t* k_codes; const uint16_t* k_scale; const uint16_t* k_zero;
   const uint8_t* v_codes; const uint16_t* v_scale; const uint16_t* v_zero;
@@ -224,6 +227,8 @@ struct KiviTreeArgs {
   float* part;                     // workspace: what blocks share, partial softmaxes of those segments
   int* err;
   int B, N, H, Hq, k_bits, v_bits, max_tokens, residual;
+  // set by the launch: query heads of a KV head, row tiles of a KV head, segments of a request, blocks, ring rows
+  IntDiv rep, row_tiles, segs, blocks, ring;
 };
 // bytes of partials a launch of this shape may write
 size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits);
