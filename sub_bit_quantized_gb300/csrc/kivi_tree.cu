@@ -174,12 +174,10 @@ __device__ __forceinline__ int ring_place(int p, int i, int R) {
 __device__ __forceinline__ uint4 row8(const uint16_t* p, int c) {
   return p ? __ldg(reinterpret_cast<const uint4*>(p + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
 }
-// true where a half of w is infinite or NaN; those become 0
-__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
-  bool any = false;
-  if ((w & 0x7C00u) == 0x7C00u) { w &= 0xFFFF0000u; any = true; }
-  if ((w & 0x7C000000u) == 0x7C000000u) { w &= 0xFFFFu; any = true; }
-  return any;
+// halves of w that are infinite or NaN become 0
+__device__ __forceinline__ void drop_nonfinite(uint32_t& w) {
+  if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
+  if ((w & 0x7C000000u) == 0x7C000000u) w &= 0xFFFFu;
 }
 
 // Channel order of the staged keys and queries. The contraction runs over all 128 channels, so any order serves
@@ -235,6 +233,17 @@ __device__ __forceinline__ __half2 code_h2(const CodeScale& cs, uint32_t w, int 
 }
 // s c - s z, one rounding of s z and one of the result
 __device__ __forceinline__ uint32_t dequant_h2(__half2 c, __half2 s, __half2 nsz) { return as_u(__hfma2(c, s, nsz)); }
+// the values of eight codes (VB == 2: the low half of w), natural order
+template <int VB>
+__device__ __forceinline__ uint4 dequant8(const CodeScale& cs, uint32_t w, uint32_t s, uint32_t z) {
+  if constexpr (VB == 2) w = __byte_perm(w, 0, 0x4140);  // codes 0 .. 3 and 4 .. 7 in the two halves
+  const __half2 s2 = as_h2(s * 0x10001u), nsz = __hneg2(__hmul2(s2, as_h2(z * 0x10001u)));
+  uint32_t x[4];  // codes j, j + 4
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = dequant_h2(code_h2<VB>(cs, w, j), s2, nsz);
+  return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                    __byte_perm(x[2], x[3], 0x7632));
+}
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -333,17 +342,6 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
   return real;
 }
 
-// eight codes of a word as fp16 values s (c - z), natural order
-template <int BITS>
-__device__ __forceinline__ uint4 scalar_dequant8(uint32_t w, float s, float z) {
-  uint32_t o[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    o[e] = pack_h2(s * ((float)((w >> (BITS * 2 * e)) & ((1 << BITS) - 1)) - z),
-                   s * ((float)((w >> (BITS * (2 * e + 1))) & ((1 << BITS) - 1)) - z));
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // ======================================================================================
 // Up to 32 rows: warp-wide products
 // ======================================================================================
@@ -390,12 +388,12 @@ struct MmaLayout {
   using S = StageLayout<KB, VB, kGroupT>;
   static constexpr int kRows = 8 * NT;
   // resident blocks the registers (32 NT sums a thread) and the shared memory leave room for
-  static constexpr int kBlocks = (NT == 1) ? 4 : (NT == 2) ? 3 : 2;
+  static constexpr int kBlocks = (NT == 1) ? 4 : 3;
   static constexpr int kStages = 2;            // of a warp's ring, one key group each
   static constexpr int kOffQ = kMmaWarps * kStages * S::kBytes;     // uint4 [4][NT][32 lanes]: B fragments of two k-steps
   static constexpr int kOffO = kOffQ + 4 * NT * 32 * 16;            // float [2][kRows][128]: sums on their way to a warp
-  static constexpr int kOffMl = kOffO + 2 * kRows * kD * 4;         // float2 [4 warps][kRows]: m, l
-  static constexpr int kOffMask = kOffMl + kMmaWarps * kRows * 8;   // uint64 [kRows]
+  static constexpr int kOffMl = kOffO + 2 * kRows * kD * 4;         // float2 [4 warps][kRows]: m, l; [kRows]: the block's
+  static constexpr int kOffMask = kOffMl + (kMmaWarps + 1) * kRows * 8;  // uint64 [kRows]
   static constexpr int kOffC = kOffMask + kRows * 8;                // float [kRows]: log2 units per score unit
   static constexpr int kOffAhead = kOffC + kRows * 4;               // Walk [4 warps]: the warp's next copy; Walk: the block's
   static constexpr int kOffFlag = kOffAhead + (kMmaWarps + 1) * 48;
@@ -428,6 +426,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
   uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ);
   float* osum = reinterpret_cast<float*>(sm + L::kOffO);
   float2* ml = reinterpret_cast<float2*>(sm + L::kOffMl);
+  float2* row_ml = ml + kMmaWarps * kRows;
   uint64_t* mask = reinterpret_cast<uint64_t*>(sm + L::kOffMask);
   float* rowc = reinterpret_cast<float*>(sm + L::kOffC);
   int* nonfinite = reinterpret_cast<int*>(sm + L::kOffFlag);
@@ -683,15 +682,19 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
             for (int e = 0; e < 4; ++e) over = over || s[nt][t][e] - m[nt][e & 1] > kRaise + kSlack;
         if (!plain) {  // drafted tokens among the 32
           over = true;
+          const uint64_t there = w.len.nd >= 64 ? ~0ull : (1ull << w.len.nd) - 1;
+          const int dj = tok8 - to_n;  // the drafted token of the lane's first one (-31 .. : cached below 0)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t mk = mask[8 * nt + 2 * q4 + e] & there;
+              // bit 8 oct: the row sees the lane's token of that octet
+              const uint32_t sees = dj >= 64 ? 0u : dj >= 0 ? (uint32_t)(mk >> dj) : ((uint32_t)(mk << -dj) | ((1u << -dj) - 1u));
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int dj = 8 * (2 * t + (e >> 1)) + tok8 - to_n;
-                if (dj >= 0 && (dj >= w.len.nd || !((mask[8 * nt + 2 * q4 + (e & 1)] >> dj) & 1ull))) s[nt][t][e] = -INFINITY;
-              }
+              for (int oct = 0; oct < 4; ++oct)
+                if (!((sees >> (8 * oct)) & 1u)) s[nt][oct >> 1][e + 2 * (oct & 1)] = -INFINITY;
+            }
         }
         if (__builtin_expect(__any_sync(0xFFFFFFFFu, over), 0)) {
           // raise the maxima of the rows with a score past them
@@ -793,8 +796,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
                 if (tt < to_v) {
                   const uint32_t cwd = *reinterpret_cast<const uint32_t*>(stage + S::kVc + tt * S::kVRow + n8 * (2 * VB) + (VB == 4 ? 4 * hw : 0)) >> (VB == 2 ? 16 * hw : 0);
                   const int at = tt * 4 + (n8 >> 1);
-                  const uint4 v = scalar_dequant8<VB>(cwd, th2f(reinterpret_cast<const uint16_t*>(stage + S::kVs)[at]),
-                                                      th2f(reinterpret_cast<const uint16_t*>(stage + S::kVz)[at]));
+                  const uint4 v = dequant8<VB>(cs0, cwd, reinterpret_cast<const uint16_t*>(stage + S::kVs)[at],
+                                               reinterpret_cast<const uint16_t*>(stage + S::kVz)[at]);
                   x[y][0] = v.x;
                   x[y][1] = v.y;
                   x[y][2] = v.z;
@@ -806,14 +809,23 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by
               // every row's weight, 0 for the others: one that is not finite is taken as 0 and added at the
               // end to the rows that see it.
+              const __half2 nil = __float2half2_rn(0.f);
+              __half2 z = nil;  // 0 times a number that is not finite is not 0
 #pragma unroll
               for (int y = 0; y < 8; ++y)
                 if (8 * (y >> 1) + ((y & 1) ? cb : ca) >= to_n) {
-                  bool any = false;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) any |= drop_nonfinite(x[y][e]);
-                  if (any) *nonfinite = 1;
+                  for (int e = 0; e < 4; ++e) z = __hfma2(as_h2(x[y][e]), nil, z);
                 }
+              if (__builtin_expect(!__hbeq2(z, nil), 0)) {
+                *nonfinite = 1;
+#pragma unroll
+                for (int y = 0; y < 8; ++y)
+                  if (8 * (y >> 1) + ((y & 1) ? cb : ca) >= to_n) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) drop_nonfinite(x[y][e]);
+                  }
+              }
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c)  // channels 2 c, 2 c + 1 of the eight
@@ -850,114 +862,100 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
         if (n8 == 0) ml[warp * kRows + 8 * nt + 2 * q4 + e] = make_float2(m[nt][e], l[nt][e]);
       }
     __syncthreads();
-    // every warp's sums against the block's maximum; warps 2, 3 hand theirs to 0, 1, then 1 to 0
-    float ms[NT][2], lt[NT][2];
+    // every warp's sums against the block's maximum; warps 2, 3 hand theirs to 0, 1, which leave two for all to add
+    auto top = [&](int r) {
+      float x = ml[r].x;
+#pragma unroll
+      for (int k = 1; k < kMmaWarps; ++k) x = fmaxf(x, ml[k * kRows + r].x);
+      return x;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 8 * nt + 2 * q4 + e;
-        float2 v[kMmaWarps];
-#pragma unroll
-        for (int k = 0; k < kMmaWarps; ++k) v[k] = ml[k * kRows + r];
-        ms[nt][e] = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-        lt[nt][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMmaWarps; ++k)
-          if (v[k].y != 0.f) lt[nt][e] += v[k].y * exp2_approx(v[k].x - ms[nt][e]);  // 0: the row saw nothing there
-        const float f = l[nt][e] == 0.f ? 0.f : exp2_approx(m[nt][e] - ms[nt][e]);
+        const float f = l[nt][e] == 0.f ? 0.f : exp2_approx(m[nt][e] - top(8 * nt + 2 * q4 + e));
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
           o[nt][t][e] = f == 0.f ? 0.f : o[nt][t][e] * f;
           o[nt][t][2 + e] = f == 0.f ? 0.f : o[nt][t][2 + e] * f;
         }
       }
+    if (tid < kRows) {
+      const float mr = top(tid);
+      float lr = 0.f;
 #pragma unroll
-    for (int half = 2; half >= 1; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
-        float* dst = osum + (warp - half) * kRows * kD + lane;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[((nt * 8 + t) * 4 + e) * 32] = o[nt][t][e];
+      for (int k = 0; k < kMmaWarps; ++k) {
+        const float2 v = ml[k * kRows + tid];
+        if (v.y != 0.f) lr += v.y * exp2_approx(v.x - mr);  // 0: the row saw nothing there
       }
-      __syncthreads();
-      if (warp < half) {
-        const float* src = osum + warp * kRows * kD + lane;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][t][e] += src[((nt * 8 + t) * 4 + e) * 32];
-      }
-      __syncthreads();
+      row_ml[tid] = make_float2(mr, lr);
     }
-    if (warp == 0) {  // rows 8 nt + 2 q + e, channels 16 n + 0 .. 15: o[nt][c / 2][e + 2 (c % 2)]
-      if (earlier) sh.first = last ? 2 : 1;
-      else if (!last) {
-        sh.open = w.b * seg_per_b + w.seg;
-        sh.nd = w.len.nd;
-      }
-      float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<kRows>();
-      const bool fix = *nonfinite != 0;
+    float* mine = osum + (warp & 1) * kRows * kD + lane;
+    auto element = [](int nt, int t, int e) { return ((nt * 8 + t) * 4 + e) * 32; };
+    if (warp >= 2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * nt + 2 * q4 + e, di = div_by(r, a.rep);
-          if (r >= rows_all || di >= w.len.nd) continue;  // padding
-          float v[16];
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] = o[nt][c >> 1][e + 2 * (c & 1)];
-          if (fix) {  // of the drafted tokens in this block's tiles
-            const int j1 = min(w.len.nd, t_end * kTile - w.len.n);
+          for (int e = 0; e < 4; ++e) mine[element(nt, t, e)] = o[nt][t][e];
+    }
+    __syncthreads();
+    if (warp < 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mine[element(nt, t, e)] += o[nt][t][e];
+    }
+    __syncthreads();
+    if (earlier) sh.first = last ? 2 : 1;
+    else if (!last) {
+      sh.open = w.b * seg_per_b + w.seg;
+      sh.nd = w.len.nd;
+    }
+    float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<kRows>();
+    const bool fix = *nonfinite != 0;
 #pragma unroll 1
-            for (int j = max(0, tile_first * kTile - w.len.n); j < j1; ++j) {
-              if (!((mask[r] >> j) & 1ull)) continue;
-              const uint16_t* d = a.v_draft + (((size_t)w.b * a.N + j) * a.H + h) * kD + 16 * n8;
+    for (int x = 0; x < 2 * NT; ++x) {  // row 8 nt + 2 q + e, channels 16 n + 4 warp .. + 3: o[nt][2 warp + c / 2][e + 2 (c % 2)]
+      const int nt = x >> 1, e = x & 1, r = 8 * nt + 2 * q4 + e, di = div_by(r, a.rep), ch = 16 * n8 + 4 * warp;
+      if (r >= rows_all || di >= w.len.nd) continue;  // padding
+      const float* s0 = osum + element(nt, 2 * warp, e) + lane;
+      float v[4];
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if ((d[c] & 0x7C00u) == 0x7C00u) v[c] += th2f(d[c]);
-            }
-          }
-          const float ls = lt[nt][e];
-          if (whole) {
-            const bool some = ls > 0.f || ls != ls;
+      for (int c = 0; c < 4; ++c) v[c] = s0[64 * c] + s0[kRows * kD + 64 * c];
+      if (fix) {  // of the drafted tokens in this block's tiles
+        const int j1 = min(w.len.nd, t_end * kTile - w.len.n);
+#pragma unroll 1
+        for (int j = max(0, tile_first * kTile - w.len.n); j < j1; ++j) {
+          if (!((mask[r] >> j) & 1ull)) continue;
+          const uint16_t* d = a.v_draft + (((size_t)w.b * a.N + j) * a.H + h) * kD + ch;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = some ? v[c] / ls : 0.f;
-            const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r - di * rep) * kD + 16 * n8;
-            if (a.out_fp32) {
-              float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) p[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            } else {
-              uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t u[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) u[k] = f32_to_bf16(v[8 * c + 2 * k]) | ((uint32_t)f32_to_bf16(v[8 * c + 2 * k + 1]) << 16);
-                p[c] = make_uint4(u[0], u[1], u[2], u[3]);
-              }
-            }
-          } else {
-            float4* p = reinterpret_cast<float4*>(slot + (size_t)r * kD + 16 * n8);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) p[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            if (n8 == 0) {
-              slot[(size_t)kRows * kD + r] = ms[nt][e];
-              slot[(size_t)kRows * kD + kRows + r] = ls;
-            }
-          }
+          for (int c = 0; c < 4; ++c)
+            if ((d[c] & 0x7C00u) == 0x7C00u) v[c] += th2f(d[c]);
         }
-      __syncwarp();
-      if (lane == 0) *nonfinite = 0;
+      }
+      const float2 t = row_ml[r];
+      float* to = slot + (size_t)r * kD + ch;
+      if (whole) {
+        const float inv = (t.y > 0.f || t.y != t.y) ? 1.f / t.y : 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = inv == 0.f ? 0.f : v[c] * inv;
+        const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r - di * rep) * kD + ch;
+        to = reinterpret_cast<float*>(a.out) + at;
+        if (!a.out_fp32)
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+              make_uint2(f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16));
+      } else if (n8 == 0 && warp == 0) {
+        slot[(size_t)kRows * kD + r] = t.x;
+        slot[(size_t)kRows * kD + kRows + r] = t.y;
+      }
+      if (!whole || a.out_fp32) *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
     }
     __syncthreads();  // the queries, the row state and the place are read before the next segment's
     if (tid == 0) {
+      *nonfinite = 0;
       w.tile = t_end - 1;
       w.next(a, seg_per_b, i < n);
     }
