@@ -20,7 +20,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 64;
 
 __device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 __device__ __forceinline__ float2 hf2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
@@ -45,11 +45,19 @@ __device__ __forceinline__ void load8(const void* base, int64_t elem, float (&v)
   }
 }
 
+// kStream: the first to leave L2 again
+template <bool kStream>
+__device__ __forceinline__ void put16(void* p, uint4 u) {
+  if constexpr (kStream) __stcs(static_cast<uint4*>(p), u);
+  else *static_cast<uint4*>(p) = u;
+}
+template <bool kStream>
 __device__ __forceinline__ void store8(void* base, int64_t elem, int dt, const float (&v)[8]) {
   if (dt == KVQ_DT_FP32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + elem);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    float* p = static_cast<float*>(base) + elem;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      put16<kStream>(p + i, make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])));
     return;
   }
   uint32_t w[4];
@@ -63,7 +71,7 @@ __device__ __forceinline__ void store8(void* base, int64_t elem, int dt, const f
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + elem) = make_uint4(w[0], w[1], w[2], w[3]);
+  put16<kStream>(static_cast<uint16_t*>(base) + elem, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // sum over the eight lanes of a row
@@ -78,12 +86,12 @@ template <int DT>
 struct Raw8 {
   uint4 u[DT == KVQ_DT_FP32 ? 2 : 1];
 };
-template <int DT>
+template <int DT, bool kStream>
 __device__ __forceinline__ Raw8<DT> load_raw8(const void* base, int64_t elem) {
   Raw8<DT> r;
   const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + elem * (DT == KVQ_DT_FP32 ? 4 : 2));
-  r.u[0] = p[0];
-  if constexpr (DT == KVQ_DT_FP32) r.u[1] = p[1];
+  r.u[0] = kStream ? __ldcs(p) : p[0];
+  if constexpr (DT == KVQ_DT_FP32) r.u[1] = kStream ? __ldcs(p + 1) : p[1];
   return r;
 }
 template <int DT>
@@ -130,8 +138,8 @@ __global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a
     const QkRows& t = h < a.q.heads ? a.q : h < a.q.heads + a.k.heads ? a.k : a.v;
     if (h >= a.q.heads) h -= h < a.q.heads + a.k.heads ? a.q.heads : a.q.heads + a.k.heads;
     const int64_t e = (int64_t)b * t.sb + (int64_t)j * t.st + (int64_t)h * t.sh + 8 * l8;
-    rl[p] = load_raw8<DT>(t.in, e);
-    rh[p] = load_raw8<DT>(t.in, e + 64);
+    rl[p] = load_raw8<DT, (kPer > 1)>(t.in, e);
+    rh[p] = load_raw8<DT, (kPer > 1)>(t.in, e + 64);
   }
   float c[8] = {}, s[8] = {};
   if (a.cos) {
@@ -187,8 +195,8 @@ __global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a
       }
     }
     const int64_t o = (int64_t)b * t.ob + (int64_t)j * t.ot + (int64_t)h * t.oh + 8 * l8;
-    store8(t.out, o, t.out_dt, lo);
-    store8(t.out, o + 64, t.out_dt, hi);
+    store8<(kPer > 1)>(t.out, o, t.out_dt, lo);
+    store8<(kPer > 1)>(t.out, o + 64, t.out_dt, hi);
   }
 }
 
@@ -203,8 +211,9 @@ cudaError_t launch_rows(const QkRowsArgs& a, int quads, cudaStream_t s) {
 template <int DT>
 cudaError_t launch_rows_of(const QkRowsArgs& a, cudaStream_t s) {
   const int quads = (a.q.heads + a.k.heads + a.v.heads + 3) / 4;
-  // two quads a warp once that still leaves every SM two rounds of warps, so that few tokens use every SM
-  if ((int64_t)a.B * a.N * quads >= 2 * 2 * 64 * 152) return launch_rows<DT, 2>(a, quads, s);
+  // Three quads a warp, read and written past the table's rows in L2, once that leaves every SM two rounds of warps;
+  // one quad a warp below, so that few tokens use every SM and what they write stays in L2 for its reader.
+  if ((int64_t)a.B * a.N * quads >= 3 * 2 * 64 * 152) return launch_rows<DT, 3>(a, quads, s);
   return launch_rows<DT, 1>(a, quads, s);
 }
 
