@@ -111,6 +111,39 @@ def test_rows_of_extreme_magnitude(scale):
     check_rows(x[:, 2:], w, 1e-6, None, None, None, o[:, 2:])
 
 
+@pytest.mark.parametrize("dt,N,Hq,H", [(torch.bfloat16, 30011, 5, 1), (torch.float32, 5003, 32, 8), (torch.float16, 9001, 20, 4)])
+def test_rows_of_a_large_call_equal_those_of_small_ones(dt, N, Hq, H):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    qkv = torch.randn((1, N, Hq + 2 * H, D), generator=g, device="cuda").to(dt)
+    wq, wk = (torch.randn(D, generator=g, device="cuda").to(dt) for _ in range(2))
+    cos, sin = rope_table(512)
+    pos = torch.randint(-1, 512, (1, N), generator=g, device="cuda").int()
+
+    def outs():
+        return (torch.full((1, N, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda"),
+                torch.full((1, H, N, D), 7.0, dtype=torch.float16, device="cuda").transpose(1, 2),
+                torch.full((1, N, H, D), 7.0, device="cuda"))
+    whole, parts = outs(), outs()
+    kvq.kvq_qk_norm_rope(*qkv.split([Hq, H, H], dim=2), wq, wk, 1e-6, cos, sin, pos, *whole)
+    for t in range(0, N, 997):
+        u = slice(t, min(t + 997, N))
+        kvq.kvq_qk_norm_rope(*qkv[:, u].split([Hq, H, H], dim=2), wq, wk, 1e-6, cos, sin, pos[:, u].clone(),
+                             *(x[:, u] for x in parts))
+    torch.cuda.synchronize()
+    assert kvq.device_error() == 0
+    for x, y in zip(whole, parts):
+        assert torch.equal(x, y)
+    assert (whole[0][0, pos[0] < 0] == 7).all()
+    mine = qkv.clone()  # in place
+    q, k, v = mine.split([Hq, H, H], dim=2)
+    kvq.kvq_qk_norm_rope(q, k, v, wq, wk, 1e-6, cos, sin, pos, q, k, v)
+    live = pos[0] >= 0
+    if dt == torch.float32:  # rounded afterwards instead
+        assert torch.equal(mine[0, :, :Hq][live].bfloat16(), whole[0][0][live])
+        assert torch.equal(mine[0, :, Hq:Hq + H][live].half(), whole[1][0][live])
+    assert torch.equal(mine[0, :, Hq + H:], qkv[0, :, Hq + H:]) and torch.equal(mine[0][~live], qkv[0][~live])
+
+
 # ------------------------------------------------------------------------------------ read
 
 def read_bound(ref, dtype):
@@ -316,6 +349,70 @@ def test_tree_masks():
     got = T.run_tree(case)
     T.check_rows(got, ref, bound, 7.0)
     assert not got[0, 1].any()  # attends nothing: 0
+
+
+@pytest.mark.parametrize("rep", [1, 6, 16])
+def test_tree_many_requests(rep):
+    # more requests than a warp has lanes, some with nothing cached, nothing drafted or neither
+    B, N = 70, 2
+    nq, nr = [32 * (b % 5) for b in range(B)], [(b * 7) % 100 if b % 3 else 0 for b in range(B)]
+    nd = [0 if b % 11 == 4 or 30 <= b < 40 else 1 + b % 2 for b in range(B)]
+    case = T.make_tree_case(2460, B=B, H=1, N=N, n_quant=nq, n_resid=nr, n_draft=nd, rep=rep, residual=128)
+    ref, bound = T.reference(case)
+    T.check_rows(T.run_tree(case), ref, bound, 7.0)
+
+
+@pytest.mark.parametrize("rep", [1, 2, 4, 9])
+def test_tree_maxima_that_move_late(rep):
+    # drafted keys of large scores (exact in fp16): the maxima of a long context's parts move in the last tile only
+    case = T.make_tree_case(2470, B=2, H=2, N=8, n_quant=[32 * 70, 128], n_resid=[100, 40], rep=rep, k_bits=4, q_scale=0.3)
+    case.kd *= np.float16(8)
+    ref, bound = T.reference(case)
+    T.check_rows(T.run_tree(case), ref, bound, 7.0)
+
+
+@pytest.mark.parametrize("rep", [1, 2, 4, 9])
+def test_tree_scores_that_are_not_numbers(rep):
+    # a drafted key and a query row of NaN in a context that several blocks share
+    N = 8
+    case = T.make_tree_case(2480, B=1, H=2, N=N, n_quant=[32 * 90], n_resid=[61], rep=rep, q_scale=0.3)
+    fine = T.TreeCase(case.base, case.q.copy(), case.kd.copy(), case.vd, case.mask, case.n_draft)
+    case.kd[0, 3, 1], case.q[0, 5, 0] = np.nan, np.nan
+    bad = np.zeros(case.q.shape[:3], bool)
+    bad[0, :, rep:] = np.array([int(x) >> 3 & 1 for x in case.mask[0]], bool)[:, None]
+    bad[0, 5, 0] = True
+    ref, bound = T.reference(fine)
+    got = T.run_tree(case)
+    assert np.isnan(got[bad]).all()
+    T.check_rows(got[~bad], ref[~bad], bound[~bad], 7.0)
+
+
+@pytest.mark.parametrize("rep", [1, 5])
+def test_tree_calls_at_once_and_workspaces_as_they_come(rep):
+    cases = [T.make_tree_case(2490 + i, B=3, H=4, N=7, n_quant=[32 * 80, 96 * i, 640], n_resid=[50, 9, 128], rep=rep, q_scale=0.5)
+             for i in range(2)]
+    caches = [C.fill_kivi_cache(c.base) for c in cases]
+    args = [T.tensors(c) for c in cases]
+    want, wss, outs = [], [], []
+    for c, cache, (q, kd, vd, mask, nd) in zip(cases, caches, args):
+        ref, bound = T.reference(c)
+        got = T.run_tree(c, cache)
+        T.check_rows(got, ref, bound, 7.0)
+        want.append(got)
+        ws = kvq.make_tree_workspace(c.base.cfg, 3, 7)
+        ws.fill_(255)  # needs no initialisation
+        wss.append(ws)
+        outs.append(torch.empty(q.shape, device="cuda"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for c, cache, (q, kd, vd, mask, nd), ws, out, st in zip(cases, caches, args, wss, outs, streams):
+            with torch.cuda.stream(st):
+                kvq.kvq_kivi_tree_attn(c.base.cfg, cache, q, kd, vd, mask, out, n_draft=nd, ws=ws)
+    torch.cuda.synchronize()
+    assert kvq.device_error() == 0
+    for out, w in zip(outs, want):
+        assert np.array_equal(out.double().cpu().numpy(), w)
 
 
 def test_tree_no_residual():
