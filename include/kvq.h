@@ -394,9 +394,12 @@ kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_ro
  * NaN among them; a row that attends nothing (no cached token, empty mask) is 0.
  * The cache is read, not changed; kvq_kivi_commit appends the accepted tokens afterwards.
  * out: [B][N][n_q_heads][D], KVQ_OUT_BF16 or KVQ_OUT_FP32.
- * Arithmetic: softmax statistics and all sums in fp32; q (scaled by a power of two for each row),
- * the dequantized keys and values and the softmax weights enter the tensor cores as fp16, one
- * rounding each (relative 2^-11); a dequantized value beyond 65504 overflows.
+ * Arithmetic: softmax statistics and all sums in fp32. The tensor cores take fp16 operands, each
+ * rounded once (half a step: relative 2^-11, absolute 2^-25 below 2^-14): the queries (scaled by a
+ * power of two for each row), the softmax weights, the dequantized values (one beyond 65504
+ * overflows) and keys. With up to 16 rows, N * n_q_heads / n_heads, the key codes enter exactly
+ * and in place of queries and keys the products of query elements, in units of the row's largest
+ * (below 1, and up to 2^-4 times that), and key scales are rounded.
  * ws: device workspace of at least kvq_kivi_tree_workspace_size() bytes, needing no
  * initialisation. Two calls that run at the same time need two workspaces.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_CAPACITY (B > max_batch), KVQ_ERR_WORKSPACE,

@@ -8,18 +8,26 @@
 //
 // Tokens (cached, then drafted) form tiles of 128, and a persistent grid takes equal contiguous
 // shares of all tiles (segment by segment, a segment being a request, KV head and row tile).
-// Keys and values are dequantized to fp16 operands, one rounding each; the sums, the running
-// maxima and the normalisers are fp32. The running maximum of a row moves only when a score
-// passes it by 2^kSlack. Segments that blocks share leave partial softmaxes in the workspace,
-// which a second small kernel joins in block order.
+// Operands enter the tensor cores as fp16, one rounding each; the sums, the running maxima and
+// the normalisers are fp32. The running maximum of a row moves only when a score passes it by
+// 2^kSlack. Segments that blocks share leave partial softmaxes in the workspace, which a second
+// small kernel joins in block order, so the result does not depend on timing.
 //
-// Two kernels by the number of rows R of a KV head (tree_rows):
-//  * R <= 32: warp-wide products. A warp takes a 32-token key group, unpacks the codes straight
-//    into the B fragments of m16n8k16 products and keeps scores and sums in registers; nothing
-//    goes through shared memory but the stored tile, and warps meet only at the segment's end.
-//  * more rows: tcgen05 on tiles of 64 rows. S^T [128 tokens x rows] = K . q^T and
+// Two kernels by the number of rows R of a KV head (tree_rows, where both sides are measured):
+//  * R <= 16: warp-wide products. A warp takes a 32-token key group and unpacks the codes straight
+//    into the A fragments of m16n8k16 products (tokens and channels are the 16 rows, query rows the
+//    8 columns); scores and sums stay in registers, nothing goes through shared memory but the
+//    stored tile, and warps meet only at the segment's end.
+//  * more rows: tcgen05 on tiles of 32 or 64 rows. S^T [128 tokens x rows] = K . q^T and
 //    O^T [128 channels x rows] += V^T . P^T keep all 128 lanes of every product busy; the unpacked
-//    operands go through shared memory once for 64 rows.
+//    operands go through shared memory once for a tile's rows.
+// HBM traffic is the codes and scales once per row tile; both kernels are bound on chip (below).
+//
+// What a block runs once or once per segment (its share, the queries, the last tile's drafts, the
+// segment's end) is written for few instructions rather than few steps: rolled loops, divisions by
+// the launch's constants as one product. Unrolled, that code was fetched cold in every block and
+// took longer than the work in it (two requests, 1K context, 64 rows: 22.8 -> 20.2 us; 16 rows, 4K:
+// 142 -> 123).
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -65,7 +73,8 @@ __device__ __forceinline__ int div_by(int n, const IntDiv& v) {
 
 // The work of a call, the same for every block: segment (b, h, row tile) has T_b tiles (its cached
 // and drafted tokens), all segments in the order b, h, row tile form one list of P tile positions,
-// and block k of G takes positions [k P / G, (k + 1) P / G).
+// and block k of G takes positions [k P / G, (k + 1) P / G); of fewer than G positions the first blocks take one each,
+// so that the blocks of a segment are neighbours (two requests, 1K context, 64 rows: 20.2 -> 16.6 us).
 struct TreeLens {
   int nqk, nqv, n, nd;  // quantized keys, quantized values, cached tokens, drafted tokens
   int tiles;
@@ -79,8 +88,9 @@ __device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
   L.tiles = L.nd > 0 ? (int)((uint32_t)(L.n + L.nd + kTile - 1) / kTile) : 0;
   return L;
 }
-// k P / G without leaving 32 bits (k <= G, G far below 2^15)
+// where the share of block k of G begins, without leaving 32 bits (k <= G, G far below 2^15)
 __device__ __forceinline__ int share_begin(int P, int k, const IntDiv& G) {
+  if (P <= G.d) return min(k, P);
   const int q = div_by(P, G);
   return k * q + div_by(k * (P - q * G.d), G);
 }
@@ -343,7 +353,7 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
 }
 
 // ======================================================================================
-// Up to 32 rows: warp-wide products
+// Up to 16 rows: warp-wide products
 // ======================================================================================
 //
 // Tokens (scores) and channels (values) are the 16 rows of an m16n8k16 product, the query rows its 8 columns:
@@ -364,6 +374,10 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
 //    (q' = fp16(q s 2^-k), one rounding, in both sums), and the second sum is a product with the zero-points as A.
 // Bound: instruction issue. A group of 32 tokens costs a warp about 170 instructions for the keys (1 per code pair),
 // 50 for the softmax of 8 rows and 270 for the values (3 per code pair), and 40 products per 8 rows.
+// Measured (16 requests, 32 KV heads, 4K context, 2 bits): 78 us for 8 rows (208 MB, 2.7 TB/s, 39 % of the copy rate),
+// 123 us for 16. Per-warp rings of two groups by cp.async (each lane copies what its warp reads, so no block barrier
+// in the loop); four blocks of four warps an SM for 8 rows, three for 16, as the registers of the sums allow. Five
+// blocks of 96 registers spilled in the loop: 105 us against 88 then.
 constexpr int kMmaThreads = 128;
 constexpr int kMmaWarps = kMmaThreads / 32;
 
@@ -965,13 +979,24 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 }
 
 // ======================================================================================
-// More rows: tcgen05 on tiles of 64 rows
+// More rows: tcgen05 on tiles of 32 or 64 rows
 // ======================================================================================
 //
 //   S^T [128 tokens x rows] = K [128 x 128] . q^T      K dequantized to fp16 in shared memory
 //   P^T = exp2(S^T c - m)                               a thread owns a token and half the rows
 //   O^T [128 channels x rows] += V^T [128 x 128] . P^T  V^T dequantized to fp16 in shared memory
 // The sums l stay per thread until the segment ends; whether a running maximum has to move is a block-wide vote.
+//
+// Two blocks an SM, so that one's products, copies and barriers run beside the other's unpacking and softmax. The next
+// tile's stored keys and values are on their way (bulk copies) from the moment this tile's are unpacked, and its keys
+// are unpacked into registers while this tile's value product still reads the weights, which lie where the keys were.
+//
+// Bound: no single unit (16 requests, 8 KV heads, 192 rows, 4K context, 4 bits: 177 us; issue 45 % of the cycles, ALU
+// 30 %, tensor 15 %, DRAM 7 %), but the chain of a tile: 8000 cycles with two blocks an SM, of which unpacking 2300, the
+// softmax with what raises maxima 2300, barriers 1200, the rest issuing the two products and waiting for them. Measured and not kept: four more
+// warps a block (64 registers, 234 us against 191 then), copies and products issued by warps of their own with the
+// registers that costs (238; four roles with code of their own 463), the softmax in pieces of 16 rows with the scores
+// read twice (212), weights before the vote (194).
 constexpr int kTreeThreads = 256;
 
 // V^T is staged in 8 channel x 8 token core matrices: the 16 of a row group (8 channels) are contiguous, row
@@ -1683,8 +1708,12 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
   }
 }
 
-// Rows of a tile, which also choose the kernel: up to 32 rows the warp-wide products (8, 16 or 32 rows), else tcgen05
-// on tiles of 64.
+// Rows of a tile, which also choose the kernel: the warp-wide products for 8 or 16 rows, tcgen05 with 32 or 64. Of
+// a tile's cost most is the same for any number of rows (the codes are unpacked once), so the smallest tile that holds
+// all rows wins, and 64 above that. Measured with one kernel and the other (16 requests, 32 KV heads, 4K context, 2
+// bits): 8 rows on the tile of 8 / 16 / 32: 78 / 120 / 166 us; 16 rows on 16 / 32: 123 / 168;
+// 32 rows on 32 / 64: 173 / 201 (warp-wide on 32: 334 when 16 took 145); 64 rows on 32 / 64: 328 / 213. A tile of 96
+// does not fit two blocks an SM with the sums of a row in registers.
 int tree_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 int sm_count_tree() {
   static int cached[64] = {};

@@ -192,13 +192,22 @@ class _Call:
     or else on the stream that is current when it is called."""
 
     def __init__(self, name: str, stream, device, keep):
-        self._name, self._f = name, getattr(lib(), name)
+        self._name = name
         self._stream = None if stream is None else _stream(stream)
         self._device, self._keep = device.index, (stream, keep)
 
+    def _bind(self, *args):
+        """All arguments but the stream, converted to their C types once: the call itself then goes through a
+        prototype without conversions (2.2 -> 1.2 us of host time for 17 arguments)."""
+        f = getattr(lib(), self._name)
+        self._args = [x if x is None or hasattr(x, "_obj") else t(x) for x, t in zip(args, f.argtypes)]
+        self._f = lib()[self._name]
+
     def __call__(self):
         s = self._stream
-        st = self._f(*self._args, torch._C._cuda_getCurrentRawStream(self._device) if s is None else s)
+        if s is None:
+            s = torch._C._cuda_getCurrentRawStream(self._device)
+        st = self._f(*self._args, ctypes.c_void_p(s))
         if st != KVQ_OK:
             _check(st, self._name)
 
@@ -455,8 +464,8 @@ class KiviCommitCall(_Call):
         _operand("n_accept", n_accept, (torch.int32,), (n_seq,))
         c, kc = cfg.to_c(), cache.c_struct()
         super().__init__("kvq_kivi_commit", stream, path.device, (c, kc, cache, k_draft, v_draft, path, n_accept))
-        self._args = (ctypes.byref(c), ctypes.byref(kc), _ptr(k_draft), _ptr(v_draft), _ptr(path), _ptr(n_accept),
-                      n_seq, N)
+        self._bind(ctypes.byref(c), ctypes.byref(kc), _ptr(k_draft), _ptr(v_draft), _ptr(path), _ptr(n_accept),
+                   n_seq, N)
 
 
 def kvq_kivi_commit(cfg: KiviConfig, cache: KiviCache, k_draft, v_draft, path, n_accept, stream=None):
@@ -484,8 +493,8 @@ class KiviReadCall(_Call):
             _operand("tok_begin", tok_begin, (torch.int32,), (B,))
         c, kc = cfg.to_c(), cache.c_struct()
         super().__init__("kvq_kivi_read", stream, x.device, (c, kc, cache, k_out, v_out, tok_begin))
-        self._args = (ctypes.byref(c), ctypes.byref(kc), _ptr(tok_begin), b0, B, n, _ptr(k_out), _ptr(v_out),
-                      _DT[x.dtype], _step(x, 0), _step(x, 1))
+        self._bind(ctypes.byref(c), ctypes.byref(kc), _ptr(tok_begin), b0, B, n, _ptr(k_out), _ptr(v_out),
+                   _DT[x.dtype], _step(x, 0), _step(x, 1))
 
 
 def kvq_kivi_read(cfg: KiviConfig, cache: KiviCache, k_out, v_out, tok_begin=None, b0: int = 0, stream=None):
@@ -539,9 +548,9 @@ class QkNormRopeCall(_Call):
         super().__init__("kvq_qk_norm_rope", stream, x.device,
                          (rows, q, k, v, w_q, w_k, rope_cos, rope_sin, pos, q_out, k_out, v_out))
         ref = [None if r is None else ctypes.byref(r) for r in rows]
-        self._args = (D, B, N, *ref[:3], _ptr(w_q) if q is not None else None, _ptr(w_k) if k is not None else None,
-                      float(eps), _ptr(rope_cos), _ptr(rope_sin), 0 if rope_cos is None else rope_cos.shape[0],
-                      _ptr(pos), *ref[3:])
+        self._bind(D, B, N, *ref[:3], _ptr(w_q) if q is not None else None, _ptr(w_k) if k is not None else None,
+                   float(eps), _ptr(rope_cos), _ptr(rope_sin), 0 if rope_cos is None else rope_cos.shape[0],
+                   _ptr(pos), *ref[3:])
 
 
 def kvq_qk_norm_rope(q, k, v, w_q, w_k, eps, rope_cos, rope_sin, pos, q_out, k_out, v_out, stream=None):
@@ -582,9 +591,9 @@ class TreeAttnCall(_Call):
         c, kc = cfg.to_c(), cache.c_struct()
         super().__init__("kvq_kivi_tree_attn", stream, q.device,
                          (c, kc, cache, q, k_draft, v_draft, mask, out, n_draft, ws))
-        self._args = (ctypes.byref(c), ctypes.byref(kc), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
-                      _ptr(n_draft), B, N, _ptr(out), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16,
-                      _ptr(ws), ws.numel() * ws.element_size())
+        self._bind(ctypes.byref(c), ctypes.byref(kc), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
+                   _ptr(n_draft), B, N, _ptr(out), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16,
+                   _ptr(ws), ws.numel() * ws.element_size())
 
 
 def kvq_kivi_tree_attn(cfg: KiviConfig, cache: KiviCache, q, k_draft, v_draft, mask, out, n_draft=None, ws=None,

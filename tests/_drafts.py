@@ -67,7 +67,9 @@ def reference(case: TreeCase):
     """(out, bound), both [B][N][Hq][D] fp64; rows of padding tokens are NaN in out.
 
     The bound follows the roundings. A dequantized element X = s q - s z enters as fp16: at most
-    2^-11 |X| for the result and 2^-11 |s z| for the constant. A score is off by
+    2^-11 |X| for the result and 2^-11 |s z| for the constant. (With few rows the keys enter as
+    exact codes and q_d s as fp16, in the codes' sum and the zero-points': 2^-11 |q_d X|, less.) A
+    score is off by
       e_t = (sum_d |q_d| dK_td + 2^-16 sum_d |q_d K_td|) / sqrt(D)
     (q is exact in fp16 after its power-of-two scaling up to 2^-24 of its largest element, fp32
     accumulation of 128 products stays under 2^-17 of the absolute sum: 2^-16 covers both and the
