@@ -397,8 +397,8 @@ PROFILED_TRAFFIC = {
         245771008 + 3553280),
     "kivi_b16_4k:kivi_attn_kernel": (
         "sub_bit_quantized_gb300/csrc/kivi.cu",
-        "d9212bd30963454ad0bd578eb125492d04f4c19620162fddb05c762924a4ffbd",
-        228793344 + 3551488),
+        "da3cc058cbd7d45dbced17726abc10689e0ad0fe5630f391ede9b2f132f2c922",
+        228830208 + 3591936),
     "encode_32k:encode_tc_kernel": (
         "sub_bit_quantized_gb300/csrc/vq_encode_tc.cu",
         "8f4d7c4d56f8e4813997994084beadad628c36cd5447f2bd11be519377daa3e4",
@@ -406,12 +406,12 @@ PROFILED_TRAFFIC = {
     # both quantize launches (keys per channel, values per token) of one step
     "kivi_quant_32k:kivi_quant_kernel": (
         "sub_bit_quantized_gb300/csrc/kivi.cu",
-        "d9212bd30963454ad0bd578eb125492d04f4c19620162fddb05c762924a4ffbd",
-        134273792 + 9351936 + 134293760 + 6658560),
+        "da3cc058cbd7d45dbced17726abc10689e0ad0fe5630f391ede9b2f132f2c922",
+        134280448 + 9078272 + 134321408 + 6676736),
     "kivi4_gqa_b16_4k:kivi_attn_kernel": (
         "sub_bit_quantized_gb300/csrc/kivi.cu",
-        "d9212bd30963454ad0bd578eb125492d04f4c19620162fddb05c762924a4ffbd",
-        89870592 + 2173440),
+        "da3cc058cbd7d45dbced17726abc10689e0ad0fe5630f391ede9b2f132f2c922",
+        89868800 + 2138880),
 }
 
 
