@@ -204,6 +204,8 @@ class _Call:
         self._f = lib()[self._name]
 
     def __call__(self):
+        if torch._C._cuda_getDevice() != self._device:
+            raise ValueError(f"{self._name}: its tensors are on device {self._device}, not on the current one")
         s = self._stream
         if s is None:
             s = torch._C._cuda_getCurrentRawStream(self._device)

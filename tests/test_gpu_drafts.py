@@ -560,3 +560,13 @@ def test_a_speculative_step_equals_decoding():
     graph.replay()
     torch.cuda.synchronize()
     assert cache.n_tok.tolist() == [158, 154, 150] and kvq.device_error() == 0
+
+
+def test_a_call_refuses_to_run_on_another_device(monkeypatch):
+    x = torch.zeros((1, 2, 4, D), device="cuda").half()
+    call = kvq.QkNormRopeCall(x, None, None, torch.ones(D, device="cuda").half(), None, 1e-6, None, None, None, x, None, None)
+    call()
+    other = torch.cuda.current_device() + 1  # as if it were the current one
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: other)
+    with pytest.raises(ValueError, match="device"):
+        call()
