@@ -241,14 +241,13 @@ __device__ __forceinline__ void read_rows(const KiviReadArgs& a, int b, int h, i
 template <int OUT>
 __global__ void __launch_bounds__(kReadThreads) kivi_read_kernel(const KiviReadArgs a) {
   const int lane = threadIdx.x & 31;
-  const int chunks = a.n_tok_out / kGroup + 2, both = (a.k_out ? 1 : 0) + (a.v_out ? 1 : 0);
-  const long long unit = (long long)blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
-  if (unit >= (long long)a.B * a.H * chunks * both) return;
-  const long long row = unit / chunks;  // (b, h, keys or values)
-  const int u = (int)(unit - row * chunks);
-  const bool keys = a.k_out && (both == 1 || (row & 1) == 0);
-  const long long bh = row / both;
-  const int b = a.b0 + (int)(bh / a.H), h = (int)(bh % a.H);
+  const int two = a.k_out && a.v_out;
+  const unsigned unit = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= (unsigned)(a.B * a.H * a.chunks.d) << two) return;  // below 2^31 (checked by the host)
+  const int row = div_by((int)unit, a.chunks), u = (int)unit - row * a.chunks.d;  // row: (b, h, keys or values)
+  const bool keys = a.k_out && !(two && (row & 1));
+  const int bh = row >> two, x = div_by(bh, a.heads);
+  const int b = a.b0 + x, h = bh - x * a.H;
   if (keys) {
     if (a.k_bits == 2) read_rows<2, true, OUT>(a, b, h, u, lane);
     else read_rows<4, true, OUT>(a, b, h, u, lane);
@@ -260,11 +259,12 @@ __global__ void __launch_bounds__(kReadThreads) kivi_read_kernel(const KiviReadA
 
 }  // namespace
 
-cudaError_t launch_kivi_read(const KiviReadArgs& a, int out_dt, cudaStream_t s) {
-  const long long chunks = a.n_tok_out / kGroup + 2;  // the asked tokens may begin and end inside a group
-  const long long units = (long long)a.B * a.H * chunks * ((a.k_out ? 1 : 0) + (a.v_out ? 1 : 0));
-  const long long blocks = (units + kReadThreads / 32 - 1) / (kReadThreads / 32);
-  const unsigned g = (unsigned)blocks;  // below 2^31 (checked by the host)
+cudaError_t launch_kivi_read(const KiviReadArgs& args, int out_dt, cudaStream_t s) {
+  KiviReadArgs a = args;
+  a.chunks = int_div(a.n_tok_out / kGroup + 2);  // the asked tokens may begin and end inside a group
+  a.heads = int_div(a.H);
+  const unsigned units = (unsigned)(a.B * a.H * a.chunks.d) << (a.k_out && a.v_out);  // below 2^31 (checked by the host)
+  const unsigned g = (units + kReadThreads / 32 - 1) / (kReadThreads / 32);
   if (out_dt == KVQ_DT_FP32) kivi_read_kernel<KVQ_DT_FP32><<<g, kReadThreads, 0, s>>>(a);
   else if (out_dt == KVQ_DT_FP16) kivi_read_kernel<KVQ_DT_FP16><<<g, kReadThreads, 0, s>>>(a);
   else kivi_read_kernel<KVQ_DT_BF16><<<g, kReadThreads, 0, s>>>(a);

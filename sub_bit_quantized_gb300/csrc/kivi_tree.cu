@@ -64,13 +64,6 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// n / d: the high product is at most one too small, n (1 + 1 / d) / 2^32 < 1
-__device__ __forceinline__ int div_by(int n, const IntDiv& v) {
-  int q = (int)__umulhi((uint32_t)n, v.inv);
-  if (n - q * v.d >= v.d) ++q;
-  return q;
-}
-
 // The work of a call, the same for every block: segment (b, h, row tile) has T_b tiles (its cached
 // and drafted tokens), all segments in the order b, h, row tile form one list of P tile positions,
 // and block k of G takes positions [k P / G, (k + 1) P / G); of fewer than G positions the first blocks take one each,
@@ -1726,8 +1719,6 @@ int sm_count_tree() {
 int tree_blocks(int r) {
   return sm_count_tree() * (r == 8 ? 4 : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
 }
-
-IntDiv int_div(int d) { return {d, d > 0 ? 0xFFFFFFFFu / (uint32_t)d : 0u}; }
 
 template <int ROWS>
 cudaError_t launch_merge(const KiviTreeArgs& a, int G, cudaStream_t st) {

@@ -524,7 +524,7 @@ KVQ_API kvq_status kvq_kivi_read(const kvq_kivi_cfg* c, const kvq_kivi_cache* k,
   if (b0 < 0 || B < 0 || n_tok < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: negative size", __func__);
   if ((long long)b0 + B > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: b0 + B > max_batch", __func__);
   if (B == 0 || n_tok == 0) return KVQ_OK;
-  if ((double)B * c->n_heads * (n_tok / 32 + 2) >= 2147483648.0)
+  if ((double)B * c->n_heads * (n_tok / 32 + 2) * (k_out && v_out ? 2 : 1) >= 2147483648.0)
     return fail(KVQ_ERR_UNSUPPORTED, "%s: too many rows for one call", __func__);
   kvq::KiviReadArgs a{};
   a.k_codes = k->k_codes; a.k_scale = k->k_scale; a.k_zero = k->k_zero;

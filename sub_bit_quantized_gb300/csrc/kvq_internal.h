@@ -137,6 +137,17 @@ cudaError_t launch_vq_roll_tc(const VqEncodeArgs& a, cudaStream_t s);
 cudaError_t launch_split_codebooks(const float* cb, uint8_t* cbp, long long n, int Tc, int G, cudaStream_t s);
 size_t split_codebook_bytes(int G);
 
+struct IntDiv {                    // a divisor of the launch: n / d for 0 <= n < 2^31 by one high product and one step
+  int d; uint32_t inv;             // inv = (2^32 - 1) / d
+};
+inline IntDiv int_div(int d) { return {d, d > 0 ? 0xFFFFFFFFu / (uint32_t)d : 0u}; }
+// n / d: the high product is at most one too small, n (1 + 1 / d) / 2^32 < 1
+__device__ __forceinline__ int div_by(int n, const IntDiv& v) {
+  int q = (int)__umulhi((uint32_t)n, v.inv);
+  if (n - q * v.d >= v.d) ++q;
+  return q;
+}
+
 // ---------------------------------------------------------------- KIVI
 struct KiviQuantArgs {
   const uint16_t* x;               // fp16 (b, h, j, ch)
@@ -189,6 +200,7 @@ struct KiviReadArgs {
   void* k_out; void* v_out;        // element (i, h, j, ch) at i*sb + h*sh + j*D + ch; one may be null
   int64_t sb, sh;
   int b0, B, H, k_bits, v_bits, residual, max_tokens, n_tok_out;
+  IntDiv chunks, heads;            // set by the launch: 32-token groups a row of out may touch, KV heads
 };
 cudaError_t launch_kivi_read(const KiviReadArgs& a, int out_dt, cudaStream_t s);
 
@@ -211,9 +223,6 @@ int kivi_attn_max_tok_per_split(int residual);
 cudaError_t launch_kivi_attn(const KiviAttnArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- tree attention
-struct IntDiv {                    // a divisor of the launch: n / d for 0 <= n < 2^31 by one high product and one step
-  int d; uint32_t inv;             // inv = (2^32 - 1) / d
-};
 struct KiviTreeArgs {
   const uint8_t* k_codes; const uint16_t* k_scale; const uint16_t* k_zero;
   const uint8_t* v_codes; const uint16_t* v_scale; const uint16_t* v_zero;
@@ -250,6 +259,7 @@ struct QkRowsArgs {
   int* err;
   float eps;
   int B, N, max_ctx;
+  IntDiv parts, tokens;            // set by the launch: warps a token, tokens a request
 };
 cudaError_t launch_qk_rows(const QkRowsArgs& a, int in_dt, cudaStream_t s);
 

@@ -120,13 +120,13 @@ __device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8]) {
 // A warp takes kPer row quads of one token (the first quads of the query, key and value rows, in that order, are
 // part 0), all their loads in flight before the first is used; the token's cos and sin serve them all.
 template <int DT, int kPer>
-__global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a, const unsigned parts) {
+__global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a, const unsigned units) {
   const int lane = threadIdx.x & 31, l8 = lane & 7;
   const int rows = a.q.heads + a.k.heads + a.v.heads;
   const unsigned unit = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const unsigned token = unit / parts, part = unit - token * parts;
-  if (token >= (unsigned)a.B * (unsigned)a.N) return;  // warp-uniform
-  const int b = (int)(token / (unsigned)a.N), j = (int)(token - (unsigned)b * (unsigned)a.N);
+  if (unit >= units) return;  // warp-uniform
+  const int token = div_by((int)unit, a.parts), part = (int)unit - token * a.parts.d;
+  const int b = div_by(token, a.tokens), j = token - b * a.N;
   const int pos = a.pos ? a.pos[token] : 0;
   if (pos < 0) return;  // padding: neither read nor written
   if (a.cos && pos >= a.max_ctx) {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a
   Raw8<DT> rl[kPer], rh[kPer];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    int h = ((int)part * kPer + p) * 4 + (lane >> 3);
+    int h = (part * kPer + p) * 4 + (lane >> 3);
     if (h >= rows) {
       rl[p] = rh[p] = {};
       continue;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a
   }
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    int h = ((int)part * kPer + p) * 4 + (lane >> 3);
+    int h = (part * kPer + p) * 4 + (lane >> 3);
     const bool there = h < rows;
     const bool is_q = h < a.q.heads, is_v = h >= a.q.heads + a.k.heads;
     if (!is_q) h -= is_v ? a.q.heads + a.k.heads : a.q.heads;
@@ -207,11 +207,12 @@ __global__ void __launch_bounds__(kRowThreads) qk_rows_kernel(const QkRowsArgs a
 }
 
 template <int DT, int kPer>
-cudaError_t launch_rows(const QkRowsArgs& a, int quads, cudaStream_t s) {
-  const unsigned parts = (unsigned)((quads + kPer - 1) / kPer);
-  const int64_t units = (int64_t)a.B * a.N * parts;
-  // below 2^31 (checked by the host)
-  qk_rows_kernel<DT, kPer><<<(unsigned)((units + kRowThreads / 32 - 1) / (kRowThreads / 32)), kRowThreads, 0, s>>>(a, parts);
+cudaError_t launch_rows(const QkRowsArgs& args, int quads, cudaStream_t s) {
+  QkRowsArgs a = args;
+  a.parts = int_div((quads + kPer - 1) / kPer);
+  a.tokens = int_div(a.N);
+  const unsigned units = (unsigned)(a.B * a.N * a.parts.d);  // below 2^31 (checked by the host)
+  qk_rows_kernel<DT, kPer><<<(units + kRowThreads / 32 - 1) / (kRowThreads / 32), kRowThreads, 0, s>>>(a, units);
   return cudaGetLastError();
 }
 template <int DT>
