@@ -362,6 +362,22 @@ def test_tree_many_requests(rep):
     T.check_rows(T.run_tree(case), ref, bound, 7.0)
 
 
+@pytest.mark.parametrize("max_tokens", [32, 96, 160])
+@pytest.mark.parametrize("rep,kb,vb", [(1, 2, 4), (2, 4, 2), (6, 2, 2), (20, 4, 4)])
+def test_tree_caches_filled_to_the_end(max_tokens, rep, kb, vb):
+    # quantized tokens up to the last place of the arrays, values up to it and short of it
+    case = T.make_tree_case(2465, B=3, H=2, N=5, n_quant=[max_tokens] * 3, n_resid=[0, 32, 9], rep=rep, k_bits=kb, v_bits=vb,
+                            residual=32, max_tokens=max_tokens, n_quant_v=[max_tokens, max_tokens, max_tokens - 23], q_scale=0.5)
+    ref, bound = T.reference(case)
+    T.check_rows(T.run_tree(case), ref, bound, 7.0)
+
+
+def test_tree_many_query_heads():
+    case = T.make_tree_case(2467, B=1, H=1, N=64, n_quant=[64], n_resid=[21], rep=33, n_draft=[61], q_scale=0.5)
+    ref, bound = T.reference(case)
+    T.check_rows(T.run_tree(case), ref, bound, 7.0)
+
+
 @pytest.mark.parametrize("rep", [1, 2, 4, 9])
 def test_tree_maxima_that_move_late(rep):
     # drafted keys of large scores (exact in fp16): the maxima of a long context's parts move in the last tile only
