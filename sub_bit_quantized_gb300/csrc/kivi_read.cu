@@ -8,10 +8,9 @@
 // Sixteen lanes share a token, so a warp stores two whole rows at a time; a warp takes the 32
 // tokens of a key group of one head, keys or values, eight of a lane's loads in flight at once.
 // Measured: 16 requests, 32 heads, 4K tokens at 2 bits into fp16 (1.14 GB) 183 us, 6.25 TB/s, 92 %
-// of the copy rate; 3 requests, 8 heads, 20011 tokens at 4 bits into fp32 (498 MB) 91 us, 5.5 TB/s,
-// 81 %. The first form, without the loads in flight together, took 265 and 102 us. Blocks of 64
-// threads take 3 us off the second and put 4 on the short windows of a batch; stores that are the
-// first to leave L2 change nothing.
+// of the copy rate; 3 requests, 8 heads, 20011 tokens at 4 bits into fp32 (498 MB) 88 us, 5.7 TB/s,
+// 84 %. The first form, without the loads in flight together, took 265 and 102 us. Stores that are
+// the first to leave L2 change nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -22,7 +21,10 @@
 namespace kvq {
 namespace {
 
-constexpr int kReadThreads = 256;
+// Threads of a block: small blocks leave their places sooner, which pays when a warp writes 16 KB (fp32: 3 requests, 8
+// heads, 20011 tokens, 4 bits 87.7 us with 64, 90.1 with 256; 64 requests, 32 heads, 160 tokens 77.5 and 82.6) and does
+// not when it writes 8 (fp16: 54.2 and 53.7; 53.1 and 51.6).
+constexpr int read_threads(int out) { return out == KVQ_DT_FP32 ? 64 : 256; }
 constexpr int kGroup = 32;     // tokens per key group, channels per value group; tokens of a warp
 
 // A lane's eight channels of a token are two quads: channels 8c .. 8c+7 for 16-bit outputs, so that a lane stores
@@ -239,10 +241,10 @@ __device__ __forceinline__ void read_rows(const KiviReadArgs& a, int b, int h, i
 }
 
 template <int OUT>
-__global__ void __launch_bounds__(kReadThreads) kivi_read_kernel(const KiviReadArgs a) {
+__global__ void __launch_bounds__(read_threads(OUT)) kivi_read_kernel(const KiviReadArgs a) {
   const int lane = threadIdx.x & 31;
   const int two = a.k_out && a.v_out;
-  const unsigned unit = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
+  const unsigned unit = blockIdx.x * (read_threads(OUT) / 32) + (threadIdx.x >> 5);
   if (unit >= (unsigned)(a.B * a.H * a.chunks.d) << two) return;  // below 2^31 (checked by the host)
   const int row = div_by((int)unit, a.chunks), u = (int)unit - row * a.chunks.d;  // row: (b, h, keys or values)
   const bool keys = a.k_out && !(two && (row & 1));
@@ -257,6 +259,12 @@ __global__ void __launch_bounds__(kReadThreads) kivi_read_kernel(const KiviReadA
   }
 }
 
+template <int OUT>
+void launch(const KiviReadArgs& a, unsigned units, cudaStream_t s) {
+  constexpr int kThreads = read_threads(OUT);
+  kivi_read_kernel<OUT><<<(units + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, s>>>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_kivi_read(const KiviReadArgs& args, int out_dt, cudaStream_t s) {
@@ -264,10 +272,9 @@ cudaError_t launch_kivi_read(const KiviReadArgs& args, int out_dt, cudaStream_t 
   a.chunks = int_div(a.n_tok_out / kGroup + 2);  // the asked tokens may begin and end inside a group
   a.heads = int_div(a.H);
   const unsigned units = (unsigned)(a.B * a.H * a.chunks.d) << (a.k_out && a.v_out);  // below 2^31 (checked by the host)
-  const unsigned g = (units + kReadThreads / 32 - 1) / (kReadThreads / 32);
-  if (out_dt == KVQ_DT_FP32) kivi_read_kernel<KVQ_DT_FP32><<<g, kReadThreads, 0, s>>>(a);
-  else if (out_dt == KVQ_DT_FP16) kivi_read_kernel<KVQ_DT_FP16><<<g, kReadThreads, 0, s>>>(a);
-  else kivi_read_kernel<KVQ_DT_BF16><<<g, kReadThreads, 0, s>>>(a);
+  if (out_dt == KVQ_DT_FP32) launch<KVQ_DT_FP32>(a, units, s);
+  else if (out_dt == KVQ_DT_FP16) launch<KVQ_DT_FP16>(a, units, s);
+  else launch<KVQ_DT_BF16>(a, units, s);
   return cudaGetLastError();
 }
 
