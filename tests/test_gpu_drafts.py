@@ -125,8 +125,8 @@ def test_rows_of_a_large_call_equal_those_of_small_ones(dt, N, Hq, H):
                 torch.full((1, N, H, D), 7.0, device="cuda"))
     whole, parts = outs(), outs()
     kvq.kvq_qk_norm_rope(*qkv.split([Hq, H, H], dim=2), wq, wk, 1e-6, cos, sin, pos, *whole)
-    for t in range(0, N, 997):
-        u = slice(t, min(t + 997, N))
+    for t in range(0, N, 211):
+        u = slice(t, min(t + 211, N))
         kvq.kvq_qk_norm_rope(*qkv[:, u].split([Hq, H, H], dim=2), wq, wk, 1e-6, cos, sin, pos[:, u].clone(),
                              *(x[:, u] for x in parts))
     torch.cuda.synchronize()
