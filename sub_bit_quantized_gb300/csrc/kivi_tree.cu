@@ -364,11 +364,13 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
 //  * P^T turns from accumulator into B fragment by the 8 x 8 transposition of packed halves.
 //  * Keys are not dequantized: sum_c q_c s_c (code_c - z_c) = sum_c (q_c s_c) code_c - sum_c (q_c s_c) z_c. A masked
 //    half of a code word is the fp16 subnormal code 2^(k - 24), exact; the scales of the group go into the queries
-//    (q' = fp16(q s 2^-k), one rounding, in both sums), and the second sum is a product with the zero-points as A.
+//    (q' = fp16(q s 2^-k), one rounding, in both sums), and the second sum is a product with the zero-points as A. A
+//    group whose scales are all below 2^-6 has them times 2^10 (3 % of the time), or q' would lose bits as a subnormal:
+//    at 4 bits and scales near 2^-16 results were off by 4e-2 instead of 4e-4.
 // Bound: instruction issue. A group of 32 tokens costs a warp about 170 instructions for the keys (1 per code pair),
 // 50 for the softmax of 8 rows and 270 for the values (3 per code pair), and 40 products per 8 rows.
-// Measured (16 requests, 32 KV heads, 4K context, 2 bits): 78 us for 8 rows (208 MB, 2.7 TB/s, 39 % of the copy rate),
-// 123 us for 16. Per-warp rings of two groups by cp.async (each lane copies what its warp reads, so no block barrier
+// Measured (16 requests, 32 KV heads, 4K context, 2 bits): 80 us for 8 rows (208 MB, 2.6 TB/s, 38 % of the copy rate),
+// 126 us for 16. Per-warp rings of two groups by cp.async (each lane copies what its warp reads, so no block barrier
 // in the loop); four blocks of four warps an SM for 8 rows, three for 16, as the registers of the sums allow. Five
 // blocks of 96 registers spilled in the loop: 105 us against 88 then.
 constexpr int kMmaThreads = 128;
@@ -591,11 +593,23 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               u[t][3] = v.w;
             }
           }
+          float down = 1.f;
           {  // the group's scales and zero-points in pair order, in place: a lane takes 16 channels of one of them
             uint4* blk = reinterpret_cast<uint4*>(const_cast<unsigned char*>(stage) + S::kKs) + 2 * (lane & 15);
             uint4 x0, x1;
             pair_order<KB>(blk[0], blk[1], x0, x1);
-            __syncwarp();
+            // scales all below 2^-6 (lanes 0 .. 7) are taken times 2^10, exactly: q' keeps its bits
+            const __half2 top = __hmax2(__hmax2(__hmax2(__habs2(as_h2(x0.x)), __habs2(as_h2(x0.y))), __hmax2(__habs2(as_h2(x0.z)), __habs2(as_h2(x0.w)))),
+                                        __hmax2(__hmax2(__habs2(as_h2(x1.x)), __habs2(as_h2(x1.y))), __hmax2(__habs2(as_h2(x1.z)), __habs2(as_h2(x1.w)))));
+            const bool high = lane < 8 && __hbgt2(__hmax2(top, __lowhigh2highlow(top)), __float2half2_rn(0.01562f));
+            if (!__any_sync(0xFFFFFFFFu, high)) {
+              down = 1.f / 1024.f;
+              if (lane < 8) {
+                uint32_t* w[8] = {&x0.x, &x0.y, &x0.z, &x0.w, &x1.x, &x1.y, &x1.z, &x1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *w[i] = as_u(__hmul2(as_h2(*w[i]), __float2half2_rn(1024.f)));
+              }
+            }
             if (lane < 16) {
               blk[0] = x0;
               blk[1] = x1;
@@ -641,8 +655,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                s[nt][t][e] = fmaf(s[nt][t][e], cs[nt][e & 1] * 16777216.f, -zs[nt][e & 1] * cs[nt][e & 1]);
+              for (int e = 0; e < 4; ++e) {
+                const float c = cs[nt][e & 1] * down;
+                s[nt][t][e] = fmaf(s[nt][t][e], c * 16777216.f, -zs[nt][e & 1] * c);
+              }
         } else {  // fp16 rows: residual, drafted, or none
           const uint16_t* row[4];
 #pragma unroll
@@ -1704,7 +1720,8 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
 // Rows of a tile, which also choose the kernel: the warp-wide products for 8 or 16 rows, tcgen05 with 32 or 64. Of
 // a tile's cost most is the same for any number of rows (the codes are unpacked once), so the smallest tile that holds
 // all rows wins, and 64 above that. Measured with one kernel and the other (16 requests, 32 KV heads, 4K context, 2
-// bits): 8 rows on the tile of 8 / 16 / 32: 78 / 120 / 166 us; 16 rows on 16 / 32: 123 / 168;
+// bits): 8 rows on the tile of 8 / 16 / 32: 78 / 120 / 166 us; 16 rows on 16 / 32: 123 / 168 (before the 3 % for
+// small scales);
 // 32 rows on 32 / 64: 173 / 201 (warp-wide on 32: 334 when 16 took 145); 64 rows on 32 / 64: 328 / 213. A tile of 96
 // does not fit two blocks an SM with the sums of a row in registers.
 int tree_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }

@@ -372,6 +372,20 @@ def test_tree_caches_filled_to_the_end(max_tokens, rep, kb, vb):
     T.check_rows(T.run_tree(case), ref, bound, 7.0)
 
 
+@pytest.mark.parametrize("rep,kb", [(1, 2), (1, 4), (2, 2), (6, 4)])
+@pytest.mark.parametrize("down", [5, 9, 12, 14])
+def test_tree_small_keys_and_large_queries(rep, kb, down):
+    # keys times 2^-down, queries times 2^down: the same scores
+    case = T.make_tree_case(2469, B=2, H=2, N=6, n_quant=[256, 32], n_resid=[40, 3], rep=rep, k_bits=kb, q_scale=0.5)
+    f = np.float16(2.0 ** -down)
+    case.base.k_scale[:] *= f
+    case.base.k_res[:] *= f
+    case.kd *= f
+    case.q *= 2.0 ** down
+    ref, bound = T.reference(case)
+    T.check_rows(T.run_tree(case), ref, bound, 7.0)
+
+
 def test_tree_many_query_heads():
     case = T.make_tree_case(2467, B=1, H=1, N=64, n_quant=[64], n_resid=[21], rep=33, n_draft=[61], q_scale=0.5)
     ref, bound = T.reference(case)
