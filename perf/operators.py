@@ -116,8 +116,7 @@ def _quantize(x, dim, bits):
     """Codes, fp16 scale and fp16 zero-point of groups along ``dim``; every step one fp32 rounding."""
     x = x.float()
     lo, hi = x.amin(dim, keepdim=True), x.amax(dim, keepdim=True)
-    # a tensor as the divisor: torch multiplies by the reciprocal of a plain number, which rounds differently
-    s = ((hi - lo) / torch.full_like(lo, float(2 ** bits - 1))).half()
+    s = ((hi - lo) / float(2 ** bits - 1)).half()
     s = torch.where(s == 0, torch.ones_like(s), s)
     z = (-lo / s.float()).half()
     q = (x / s.float() + z.float()).round().clamp(0, 2 ** bits - 1)
