@@ -400,7 +400,9 @@ kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_ro
  * overflows) and keys. With up to 16 rows, N * n_q_heads / n_heads, the key codes enter exactly
  * and in place of queries and keys the products of query elements, in units of the row's largest
  * (below 1, and up to 2^-4 times that), and key scales (times 2^10 where a 32-token group has
- * none of 2^-6) are rounded.
+ * none of 2^-6), as two fp16 parts; a quantized value enters as s (c - c0), c0 the middle code,
+ * rounded once, beside the exact constants of its group, and the weights' sum is that of the
+ * rounded ones.
  * ws: device workspace of at least kvq_kivi_tree_workspace_size() bytes, needing no
  * initialisation. Two calls that run at the same time need two workspaces.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_CAPACITY (B > max_batch), KVQ_ERR_WORKSPACE,

@@ -223,7 +223,8 @@ struct CodeScale {
 };
 // Code j of both halves of w as fp16 (exact): masked in place under the exponent of 2^10, where it stands for
 // 1024 + c 2^(b j), and scaled back by one FMA. Codes above the ten mantissa bits come from w shifted right.
-template <int BITS>
+// CENTRE: what is taken off the code.
+template <int BITS, int CENTRE = 0>
 __device__ __forceinline__ __half2 code_h2(const CodeScale& cs, uint32_t w, int j) {
   constexpr int kIn = (BITS == 2) ? 5 : 2;  // codes that fit in place
   const int jj = j < kIn ? j : j - kIn, k = BITS * jj / 2;
@@ -231,19 +232,23 @@ __device__ __forceinline__ __half2 code_h2(const CodeScale& cs, uint32_t w, int 
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
       : "=r"(m)
       : "r"(j < kIn ? w : w >> (BITS * kIn)), "r"((((1u << BITS) - 1u) << (BITS * jj)) * 0x10001u), "r"(cs.magic));
-  if (k == 0) return __hadd2(as_h2(m), __float2half2_rn(-1024.f));
-  return __hfma2(as_h2(m), as_h2(cs.p[k - 1]), __float2half2_rn(-1024.f / (float)(1 << (2 * k))));
+  if (k == 0) return __hadd2(as_h2(m), __float2half2_rn(-1024.f - CENTRE));
+  return __hfma2(as_h2(m), as_h2(cs.p[k - 1]), __float2half2_rn(-1024.f / (float)(1 << (2 * k)) - CENTRE));
 }
+// What a stored element is made of: X = s (c - z) = s (c - c0) - (s z - c0 s). With the middle code c0 the first part
+// is small and one fp16 (exact with 2 bits; with 4 off by 2^-11 of at most 8 s), however far the group lies from zero;
+// the second is one number per group and is never added to it in fp16.
+template <int BITS>
+constexpr int kCentre = BITS == 2 ? 1 : 8;
 // s c - s z, one rounding of s z and one of the result
 __device__ __forceinline__ uint32_t dequant_h2(__half2 c, __half2 s, __half2 nsz) { return as_u(__hfma2(c, s, nsz)); }
-// the values of eight codes (VB == 2: the low half of w), natural order
+// s (c - c0) of eight codes (VB == 2: the low half of w), natural order
 template <int VB>
-__device__ __forceinline__ uint4 dequant8(const CodeScale& cs, uint32_t w, uint32_t s, uint32_t z) {
+__device__ __forceinline__ uint4 centred8(const CodeScale& cs, uint32_t w, __half2 s) {
   if constexpr (VB == 2) w = __byte_perm(w, 0, 0x4140);  // codes 0 .. 3 and 4 .. 7 in the two halves
-  const __half2 s2 = as_h2(s * 0x10001u), nsz = __hneg2(__hmul2(s2, as_h2(z * 0x10001u)));
   uint32_t x[4];  // codes j, j + 4
 #pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = dequant_h2(code_h2<VB>(cs, w, j), s2, nsz);
+  for (int j = 0; j < 4; ++j) x[j] = as_u(__hmul2(code_h2<VB, kCentre<VB>>(cs, w, j), s));
   return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
                     __byte_perm(x[2], x[3], 0x7632));
 }
@@ -363,16 +368,23 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
 //    channels 16 n + 2 t and + 1.
 //  * P^T turns from accumulator into B fragment by the 8 x 8 transposition of packed halves.
 //  * Keys are not dequantized: sum_c q_c s_c (code_c - z_c) = sum_c (q_c s_c) code_c - sum_c (q_c s_c) z_c. A masked
-//    half of a code word is the fp16 subnormal code 2^(k - 24), exact; the scales of the group go into the queries
-//    (q' = fp16(q s 2^-k), one rounding, in both sums), and the second sum is a product with the zero-points as A. A
-//    group whose scales are all below 2^-6 has them times 2^10 (3 % of the time), or q' would lose bits as a subnormal:
-//    at 4 bits and scales near 2^-16 results were off by 4e-2 instead of 4e-4.
-// Bound: instruction issue. A group of 32 tokens costs a warp about 170 instructions for the keys (1 per code pair),
-// 50 for the softmax of 8 rows and 270 for the values (3 per code pair), and 40 products per 8 rows.
-// Measured (16 requests, 32 KV heads, 4K context, 2 bits): 80 us for 8 rows (208 MB, 2.6 TB/s, 38 % of the copy rate),
-// 126 us for 16. Per-warp rings of two groups by cp.async (each lane copies what its warp reads, so no block barrier
-// in the loop); four blocks of four warps an SM for 8 rows, three for 16, as the registers of the sums allow. Five
-// blocks of 96 registers spilled in the loop: 105 us against 88 then.
+//    half of a code word is the fp16 subnormal code 2^(k - 24), exact; the scales of the group go into the queries,
+//    q s 2^-k = q' + q'' with q' its fp16 and q'' the exact rest as fp16, in both sums (with q' alone the output was off
+//    by up to 7e-3, three times the bound of attention), and the second sum is a product with the zero-points as A.
+//    A group whose scales are all below 2^-6 has them times 2^10, or q' would lose bits as a subnormal: at 4 bits and
+//    scales near 2^-16 results were off by 4e-2 instead of 4e-4.
+//  * Values: s (c - z) = s (c - c0) - (s z - c0 s) with the middle code c0: the first part is one fp16 (exact at 2 bits,
+//    one rounding of at most 8 s at 4), the second one number per token and channel group. A product of its own has
+//    the constants as its rows: s z as fp16, the exact rest of it, c0 s, and ones, whose sums are those of the rounded
+//    weights, so that a weight's rounding leaves a row's weights a convex combination. Values are halved on the way in:
+//    8 s passes the fp16 range for values near its end.
+// Bound: instruction issue. A group of 32 tokens costs a warp about 210 instructions for the keys (1 per code pair),
+// 50 for the softmax of 8 rows and 280 for the values (3 per code pair), and 66 products per 8 rows.
+// Measured (16 requests, 32 KV heads, 4K context, 2 bits): 102 us for 8 rows (208 MB, 2.0 TB/s, 30 % of the copy rate),
+// 166 us for 16; the second parts q'' and the constants' products are 22 and 40 of it (max-abs error of the parity cases 7e-3
+// without, 1e-3 with them). Per-warp rings of two groups by cp.async (each lane copies what its warp reads, so no block barrier
+// in the loop); four blocks of four warps an SM for 8 rows, two for 16, as the registers of the sums allow (three, with
+// spills in the loop: 173 us). Five blocks of 96 registers for 8 rows spilled in the loop: 105 us against 88 then.
 constexpr int kMmaThreads = 128;
 constexpr int kMmaWarps = kMmaThreads / 32;
 
@@ -396,8 +408,8 @@ template <int KB, int VB, int NT>  // NT: row tiles of 8
 struct MmaLayout {
   using S = StageLayout<KB, VB, kGroupT>;
   static constexpr int kRows = 8 * NT;
-  // resident blocks the registers (32 NT sums a thread) and the shared memory leave room for
-  static constexpr int kBlocks = (NT == 1) ? 4 : 3;
+  // resident blocks the registers (36 NT sums a thread) and the shared memory leave room for
+  static constexpr int kBlocks = (NT == 1) ? 4 : 2;
   static constexpr int kStages = 2;            // of a warp's ring, one key group each
   static constexpr int kOffQ = kMmaWarps * kStages * S::kBytes;     // uint4 [4][NT][32 lanes]: B fragments of two k-steps
   static constexpr int kOffO = kOffQ + 4 * NT * 32 * 16;            // float [2][kRows][128]: sums on their way to a warp
@@ -413,7 +425,7 @@ struct MmaLayout {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -423,6 +435,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// what the rounding of p = fp16(x y) left, exactly
+__device__ __forceinline__ uint32_t product_rest(uint32_t x, uint32_t y, uint32_t p) {
+  return as_u(__hfma2(as_h2(x), as_h2(y), __hneg2(as_h2(p))));
+}
+__device__ __forceinline__ uint32_t halved(uint32_t x) { return as_u(__hmul2(as_h2(x), __float2half2_rn(0.5f))); }
+// A fragments of the constants' product from a token pair's scales and zero-points of the lane's channel group: rows n
+// (az) s z / 2 in an even lane row and what its rounding left in an odd one, rows n + 8 (ac) c0 s / 2 or 1. Returns s / 2.
+template <int VB>
+__device__ __forceinline__ __half2 constants(uint32_t s, uint32_t z, bool odd, uint32_t& az, uint32_t& ac) {
+  const uint32_t s2 = halved(s), p = as_u(__hmul2(as_h2(s2), as_h2(z)));
+  az = odd ? product_rest(s2, z, p) : p;
+  ac = odd ? 0x3C003C00u : as_u(__hmul2(as_h2(s2), __float2half2_rn(kCentre<VB>)));
+  return as_h2(s2);
 }
 
 template <int KB, int VB, int NT>
@@ -542,15 +569,15 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       }
     }
     __syncthreads();  // queries staged
-    float m[NT][2], l[NT][2], cs[NT][2];  // of rows 8 nt + 2 q, + 1: maximum - kRaise, sum, scale
-    float o[NT][8][4];
+    float m[NT][2], cs[NT][2];  // of rows 8 nt + 2 q, + 1: maximum - kRaise, scale
+    float o[NT][8][4], w0[NT][4];  // sums of s (c - c0), and of the constants and weights (below)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[nt][e] = -FLT_MAX;
-        l[nt][e] = 0.f;
         cs[nt][e] = rowc[8 * nt + 2 * q4 + e];
+        w0[nt][e] = w0[nt][2 + e] = 0.f;
       }
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -626,14 +653,20 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
             const int j0 = 4 * (k2 & 1), hw = k2 >> 1;
             const uint4 sc = *reinterpret_cast<const uint4*>(stage + S::kKs + (32 * q4 + 8 * k2) * 2);
             const uint4 zp = *reinterpret_cast<const uint4*>(stage + S::kKz + (32 * q4 + 8 * k2) * 2);
-            uint4 bq[NT];
+            uint4 bq[NT][2];  // q s 2^-k and what its rounding left
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint4 x = qf[(k2 * NT + nt) * 32 + lane];
-              bq[nt] = make_uint4(as_u(__hmul2(as_h2(x.x), as_h2(sc.x))), as_u(__hmul2(as_h2(x.y), as_h2(sc.y))),
-                                  as_u(__hmul2(as_h2(x.z), as_h2(sc.z))), as_u(__hmul2(as_h2(x.w), as_h2(sc.w))));
-              mma_f16(zs[nt], zp.x, zp.x, zp.y, zp.y, pos_scale<KB, 1>(bq[nt].x, j0), pos_scale<KB, 1>(bq[nt].y, j0 + 1));
-              mma_f16(zs[nt], zp.z, zp.z, zp.w, zp.w, pos_scale<KB, 1>(bq[nt].z, j0 + 2), pos_scale<KB, 1>(bq[nt].w, j0 + 3));
+              bq[nt][0] = make_uint4(as_u(__hmul2(as_h2(x.x), as_h2(sc.x))), as_u(__hmul2(as_h2(x.y), as_h2(sc.y))),
+                                     as_u(__hmul2(as_h2(x.z), as_h2(sc.z))), as_u(__hmul2(as_h2(x.w), as_h2(sc.w))));
+              bq[nt][1] = make_uint4(product_rest(x.x, sc.x, bq[nt][0].x), product_rest(x.y, sc.y, bq[nt][0].y),
+                                     product_rest(x.z, sc.z, bq[nt][0].z), product_rest(x.w, sc.w, bq[nt][0].w));
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const uint4 y = bq[nt][p];
+                mma_f16(zs[nt], zp.x, zp.x, zp.y, zp.y, pos_scale<KB, 1>(y.x, j0), pos_scale<KB, 1>(y.y, j0 + 1));
+                mma_f16(zs[nt], zp.z, zp.z, zp.w, zp.w, pos_scale<KB, 1>(y.z, j0 + 2), pos_scale<KB, 1>(y.w, j0 + 3));
+              }
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -645,11 +678,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
                 const uint32_t a2 = pair_codes<KB>(ua, j0 + 2 * kk + 1), a3 = pair_codes<KB>(ub, j0 + 2 * kk + 1);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(s[nt][t], a0, a1, a2, a3, kk ? bq[nt].z : bq[nt].x, kk ? bq[nt].w : bq[nt].y);
+#pragma unroll
+                  for (int p = 0; p < 2; ++p)
+                    mma_f16(s[nt][t], a0, a1, a2, a3, kk ? bq[nt][p].z : bq[nt][p].x, kk ? bq[nt][p].w : bq[nt][p].y);
               }
             }
           }
-          // codes are 2^-24 of themselves in the products
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -657,7 +691,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float c = cs[nt][e & 1] * down;
-                s[nt][t][e] = fmaf(s[nt][t][e], c * 16777216.f, -zs[nt][e & 1] * c);
+                s[nt][t][e] = fmaf(s[nt][t][e], c * 16777216.f, -zs[nt][e & 1] * c);  // codes are 2^-24 of themselves in the products
               }
         } else {  // fp16 rows: residual, drafted, or none
           const uint16_t* row[4];
@@ -731,7 +765,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               if (mx - m[nt][e] > kRaise + kSlack) {
                 const float f = exp2_approx(m[nt][e] - (mx - kRaise));
                 m[nt][e] = mx - kRaise;
-                l[nt][e] *= f;
+                w0[nt][e] *= f;
+                w0[nt][2 + e] *= f;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                   o[nt][t][e] *= f;
@@ -748,8 +783,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
             for (int oc = 0; oc < 2; ++oc) {
               const float p0 = exp2_approx(s[nt][t][2 * oc] - m[nt][0]), p1 = exp2_approx(s[nt][t][2 * oc + 1] - m[nt][1]);
-              l[nt][0] += p0;
-              l[nt][1] += p1;
               pf[nt][2 * t + oc] = transpose8(pack_h2(p0, p1));
             }
         // ---- values: token pairs at places 2 q, 2 q + 1 of the four octets ----
@@ -757,7 +790,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           const uint16_t* sp = reinterpret_cast<const uint16_t*>(stage + S::kVs) + (n8 >> 1);
           const uint16_t* zp = reinterpret_cast<const uint16_t*>(stage + S::kVz) + (n8 >> 1);
           const unsigned char* cw = stage + S::kVc + n8 * (2 * VB);
-          uint32_t sv[4], nz[4];
+          __half2 sv[4];
+          uint32_t az[4], ac[4];
           uint32_t wa[4][VB / 2], wb[4][VB / 2];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
@@ -772,9 +806,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               wb[t][0] = vb.x;
               wb[t][1] = vb.y;
             }
-            sv[t] = sp[ta * 4] | ((uint32_t)sp[tb * 4] << 16);
-            nz[t] = as_u(__hmul2(__hneg2(as_h2(sv[t])), as_h2(zp[ta * 4] | ((uint32_t)zp[tb * 4] << 16))));
+            sv[t] = constants<VB>(sp[ta * 4] | ((uint32_t)sp[tb * 4] << 16), zp[ta * 4] | ((uint32_t)zp[tb * 4] << 16), n8 & 1, az[t], ac[t]);
           }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(w0[nt], az[2 * k], ac[2 * k], az[2 * k + 1], ac[2 * k + 1], pf[nt][2 * k], pf[nt][2 * k + 1]);
           constexpr int kCodes = 16 / VB;  // channels of a half word
 #pragma unroll
           for (int hw = 0; hw < VB; ++hw) {  // half words of the lane's 16 channels
@@ -790,7 +827,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
                 for (int oc = 0; oc < 2; ++oc)
 #pragma unroll
                   for (int f = 0; f < 2; ++f)
-                    af[2 * oc + f] = dequant_h2(code_h2<VB>(cs0, x[2 * k + oc], c + f), as_h2(sv[2 * k + oc]), as_h2(nz[2 * k + oc]));
+                    af[2 * oc + f] = as_u(__hmul2(code_h2<VB, kCentre<VB>>(cs0, x[2 * k + oc], c + f), sv[2 * k + oc]));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma_f16(o[nt][(hw * kCodes + c) / 2], af[0], af[1], af[2], af[3], pf[nt][2 * k], pf[nt][2 * k + 1]);
@@ -798,6 +835,26 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           }
         } else {  // fp16 rows, and the group in which the quantized values end
           const int place = a.residual > 0 ? tw - div_by(tw, a.ring) * a.residual : 0;
+          {  // the stored tokens' constants; of the others none but the weights
+            uint32_t az[4], ac[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              uint32_t s2 = 0, z2 = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int tt = 8 * t + (e ? cb : ca), at = tt * 4 + (n8 >> 1);
+                if (tt < to_v) {
+                  s2 |= (uint32_t)reinterpret_cast<const uint16_t*>(stage + S::kVs)[at] << (16 * e);
+                  z2 |= (uint32_t)reinterpret_cast<const uint16_t*>(stage + S::kVz)[at] << (16 * e);
+                }
+              }
+              constants<VB>(s2, z2, n8 & 1, az[t], ac[t]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(w0[nt], az[2 * k], ac[2 * k], az[2 * k + 1], ac[2 * k + 1], pf[nt][2 * k], pf[nt][2 * k + 1]);
+          }
 #pragma unroll 1
           for (int hw = 0; hw < 2; ++hw) {  // channels 16 n8 + 8 hw .. + 7
             uint32_t x[8][4];  // octet y / 2, place 2 q + y % 2
@@ -807,10 +864,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               const uint4 v = tt < to_v
                                   ? make_uint4(0u, 0u, 0u, 0u)
                                   : row8(fp16_value(a, w.len, w.b, h, tw + tt, ring_place(place, tt, a.residual)), 2 * n8 + hw);
-              x[y][0] = v.x;
-              x[y][1] = v.y;
-              x[y][2] = v.z;
-              x[y][3] = v.w;
+              x[y][0] = halved(v.x);
+              x[y][1] = halved(v.y);
+              x[y][2] = halved(v.z);
+              x[y][3] = halved(v.w);
             }
             if (to_v > 0) {
 #pragma unroll
@@ -819,8 +876,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
                 if (tt < to_v) {
                   const uint32_t cwd = *reinterpret_cast<const uint32_t*>(stage + S::kVc + tt * S::kVRow + n8 * (2 * VB) + (VB == 4 ? 4 * hw : 0)) >> (VB == 2 ? 16 * hw : 0);
                   const int at = tt * 4 + (n8 >> 1);
-                  const uint4 v = dequant8<VB>(cs0, cwd, reinterpret_cast<const uint16_t*>(stage + S::kVs)[at],
-                                               reinterpret_cast<const uint16_t*>(stage + S::kVz)[at]);
+                  const uint4 v = centred8<VB>(cs0, cwd, as_h2(halved(reinterpret_cast<const uint16_t*>(stage + S::kVs)[at] * 0x10001u)));
                   x[y][0] = v.x;
                   x[y][1] = v.y;
                   x[y][2] = v.z;
@@ -876,12 +932,16 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     const int tile_first = w.tile, t_end = tile_first + i - i_first;  // tiles of the segment that are done
     const bool last = t_end == w.len.tiles, earlier = tile_first > 0 && i_first == 0;
     const bool whole = last && !earlier;
+    // the sum of weights, and the constants' part of the sums: lanes n and n ^ 1 hold them for their channel group
+    float l[NT][2], wc[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int off = 4; off <= 16; off <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], off);
+        const float z = w0[nt][e] + __shfl_xor_sync(0xFFFFFFFFu, w0[nt][e], 4);
+        const float y = __shfl_xor_sync(0xFFFFFFFFu, w0[nt][2 + e], 4);
+        l[nt][e] = (n8 & 1) ? w0[nt][2 + e] : y;
+        wc[nt][e] = ((n8 & 1) ? y : w0[nt][2 + e]) - z;
         if (n8 == 0) ml[warp * kRows + 8 * nt + 2 * q4 + e] = make_float2(m[nt][e], l[nt][e]);
       }
     __syncthreads();
@@ -896,11 +956,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float f = l[nt][e] == 0.f ? 0.f : exp2_approx(m[nt][e] - top(8 * nt + 2 * q4 + e));
+        // values were halved
+        const float f = l[nt][e] == 0.f ? 0.f : 2.f * exp2_approx(m[nt][e] - top(8 * nt + 2 * q4 + e));
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-          o[nt][t][e] = f == 0.f ? 0.f : o[nt][t][e] * f;
-          o[nt][t][2 + e] = f == 0.f ? 0.f : o[nt][t][2 + e] * f;
+          o[nt][t][e] = f == 0.f ? 0.f : (o[nt][t][e] + wc[nt][e]) * f;
+          o[nt][t][2 + e] = f == 0.f ? 0.f : (o[nt][t][2 + e] + wc[nt][e]) * f;
         }
       }
     if (tid < kRows) {
