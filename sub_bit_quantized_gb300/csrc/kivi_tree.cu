@@ -8,8 +8,8 @@
 //
 // Tokens (cached, then drafted) form tiles of 128, and a persistent grid takes equal contiguous
 // shares of all tiles (segment by segment, a segment being a request, KV head and row tile).
-// Operands enter the tensor cores as fp16, one rounding each; the sums, the running maxima and
-// the normalisers are fp32. The running maximum of a row moves only when a score passes it by
+// Operands enter the tensor cores as fp16, in two parts where one would cost more than the bound of
+// attention allows; the sums, the running maxima and the normalisers are fp32. The running maximum of a row moves only when a score passes it by
 // 2^kSlack. Segments that blocks share leave partial softmaxes in the workspace, which a second
 // small kernel joins in block order, so the result does not depend on timing.
 //
@@ -240,8 +240,11 @@ __device__ __forceinline__ __half2 code_h2(const CodeScale& cs, uint32_t w, int 
 // the second is one number per group and is never added to it in fp16.
 template <int BITS>
 constexpr int kCentre = BITS == 2 ? 1 : 8;
-// s c - s z, one rounding of s z and one of the result
-__device__ __forceinline__ uint32_t dequant_h2(__half2 c, __half2 s, __half2 nsz) { return as_u(__hfma2(c, s, nsz)); }
+// what the rounding of p = fp16(x y) left, exactly
+__device__ __forceinline__ uint32_t product_rest(uint32_t x, uint32_t y, uint32_t p) {
+  return as_u(__hfma2(as_h2(x), as_h2(y), __hneg2(as_h2(p))));
+}
+__device__ __forceinline__ uint32_t halved(uint32_t x) { return as_u(__hmul2(as_h2(x), __float2half2_rn(0.5f))); }
 // s (c - c0) of eight codes (VB == 2: the low half of w), natural order
 template <int VB>
 __device__ __forceinline__ uint4 centred8(const CodeScale& cs, uint32_t w, __half2 s) {
@@ -437,11 +440,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// what the rounding of p = fp16(x y) left, exactly
-__device__ __forceinline__ uint32_t product_rest(uint32_t x, uint32_t y, uint32_t p) {
-  return as_u(__hfma2(as_h2(x), as_h2(y), __hneg2(as_h2(p))));
-}
-__device__ __forceinline__ uint32_t halved(uint32_t x) { return as_u(__hmul2(as_h2(x), __float2half2_rn(0.5f))); }
 // A fragments of the constants' product from a token pair's scales and zero-points of the lane's channel group: rows n
 // (az) s z / 2 in an even lane row and what its rounding left in an odd one, rows n + 8 (ac) c0 s / 2 or 1. Returns s / 2.
 template <int VB>
@@ -1052,26 +1050,35 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 // More rows: tcgen05 on tiles of 32 or 64 rows
 // ======================================================================================
 //
-//   S^T [128 tokens x rows] = K [128 x 128] . q^T      K dequantized to fp16 in shared memory
+//   S^T [128 tokens x rows] = K [128 x 128] . q^T      K = s (c - c0) as fp16 in shared memory (4 bits: in two parts)
 //   P^T = exp2(S^T c - m)                               a thread owns a token and half the rows
-//   O^T [128 channels x rows] += V^T [128 x 128] . P^T  V^T dequantized to fp16 in shared memory
-// The sums l stay per thread until the segment ends; whether a running maximum has to move is a block-wide vote.
+//   O^T [128 channels x rows] += V^T [128 x 128] . P^T  V^T = s (c - c0) as fp16 in shared memory
+// The constants s (z - c0) of a key group's channels, of a token's channel groups, and the sum of a row's weights come
+// from products of their own (kConst below). Whether a running maximum has to move is a block-wide vote.
 //
 // Two blocks an SM, so that one's products, copies and barriers run beside the other's unpacking and softmax. The next
 // tile's stored keys and values are on their way (bulk copies) from the moment this tile's are unpacked, and its keys
 // are unpacked into registers while this tile's value product still reads the weights, which lie where the keys were.
 //
-// Bound: no single unit (16 requests, 8 KV heads, 192 rows, 4K context, 4 bits: 177 us; issue 45 % of the cycles, ALU
-// 30 %, tensor 15 %, DRAM 7 %), but the chain of a tile: 8000 cycles with two blocks an SM, of which unpacking 2300, the
-// softmax with what raises maxima 2300, barriers 1200, the rest issuing the two products and waiting for them. Measured and not kept: four more
-// warps a block (64 registers, 234 us against 191 then), copies and products issued by warps of their own with the
-// registers that costs (238; four roles with code of their own 463), the softmax in pieces of 16 rows with the scores
-// read twice (212), weights before the vote (194).
+// Bound: no single unit (16 requests, 8 KV heads, 192 rows, 4K context, 4 bits: 247 us), but the chain of a tile:
+// unpacking, the products, the softmax with what raises maxima, barriers. 175 us of it are the same kernel with keys and
+// values dequantized to one fp16, which leaves the bound of attention (errors up to 3.7e-2 on the parity cases, now 1.2e-3): the
+// constants' products cost 24, reading the keys' ones back 10, the keys' second parts and the constants themselves 38.
+// Measured with the one-fp16 form and not kept: four more warps a block (64 registers, 234 us against 191 then), copies and
+// products issued by warps of their own with the registers that costs (238; four roles with code of their own 463),
+// the softmax in pieces of 16 rows with the scores read twice (212), weights before the vote (194).
 constexpr int kTreeThreads = 256;
 
 // V^T is staged in 8 channel x 8 token core matrices: the 16 of a row group (8 channels) are contiguous, row
 // groups 2064 bytes apart, so that eight threads with eight row groups store to different banks
 constexpr int kVRowGrp = (kTile / 8) * 128 + 16;
+
+// The constants of a tile's keys (s z - c0 s of each channel) and values (of each token) as rows of a product of their
+// own: 16 rows of 8 elements for each 8 channels or tokens, kConst bytes apart. Row 4 g + i is constant i of group g; with
+// 16 bytes from row group to row group of the 128 the tensor core takes, lane 32 g + i of the result is that row, for
+// i < 8, so that a group's constants come out beside its tokens or channels. The other lanes' sums are not used.
+constexpr int kConst = 16 * 16 + 16;            // (+ 16: neighbours in different banks)
+constexpr int kConstBytes = 16 * kConst + 128;  // with what the last row groups reach past them
 
 struct Place : Walk {
   int h, row0;  // KV head, first row
@@ -1082,17 +1089,21 @@ struct TreeLayout {
   static constexpr int kOffQ = 0;                                  // fp16 [ROWS x 128], K-major
   static constexpr int kOffK = kOffQ + ROWS * kD * 2;              // fp16 [128 tokens x 128], K-major; then P
   static constexpr int kOffV = kOffK + kTile * kD * 2;             // fp16 [128 channels x 128 tokens], K-major
-  static constexpr int kOffStage = (kOffV + (kD / 8) * kVRowGrp + 127) / 128 * 128;
+  static constexpr int kOffZ = (kOffV + (kD / 8) * kVRowGrp + 127) / 128 * 128;  // constants of the keys
+  static constexpr int kOffW = kOffZ + kConstBytes;                // and of the values
+  static constexpr int kOffStage = kOffW + kConstBytes;
   static constexpr int kOffMask = kOffStage + StageLayout<KB, VB, kTile>::kBytes;  // uint64 [ROWS]
   static constexpr int kOffC = kOffMask + ROWS * 8;                // float [ROWS]: log2 units per score unit
   static constexpr int kOffM = kOffC + ROWS * 4;                   // float [ROWS]: kRaise - running maximum (log2)
   static constexpr int kOffF = kOffM + ROWS * 4;                   // float [ROWS]: rescale factor
-  static constexpr int kOffRed = kOffF + ROWS * 4;                 // float [4][ROWS]: per lane quadrant
-  static constexpr int kOffWalk = kOffRed + 4 * ROWS * 4;          // Place [2]: this position's and the next one's
+  static constexpr int kOffRed = kOffF + ROWS * 4;                 // float [2][4][ROWS]: per lane quadrant
+  static constexpr int kOffUnit = kOffRed + 8 * ROWS * 4;          // float [2][4]: what a key group's sums count
+  static constexpr int kOffWalk = kOffUnit + 32;                   // Place [2]: this position's and the next one's
   static constexpr int kOffBar = kOffWalk + 96;                    // mbarriers, TMEM address, flags
   static constexpr int kSmem = kOffBar + 64;
-  static constexpr uint32_t kCols = 2 * ROWS < 32 ? 32 : 2 * ROWS;  // TMEM: S^T, O^T
+  static constexpr uint32_t kCols = 4 * ROWS;  // TMEM: S^T, O^T, and the sums of the keys' and values' constants
   static_assert(ROWS * 256 <= kTile * kD * 2, "P fits in the key tile");
+  static_assert((kD / 8) * kVRowGrp >= kTile * kD * 2, "the keys' second parts fit in the value tile");
   static_assert(kSmem <= 232448 / 2 - 1024, "two blocks per SM");
 };
 
@@ -1163,55 +1174,80 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
   return r;
 }
-// Reduces N (a power of two, up to 32) values over a warp's lanes: v[0] of lane i < N is value i's.
-template <int N, typename F>
-__device__ __forceinline__ void lanes_reduce(float (&v)[N], int lane, F f) {
-#pragma unroll
-  for (int off = 16; off >= N; off >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = f(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], off));
-#pragma unroll
-  for (int w = N / 2; w >= 1; w >>= 1) {
-    const bool up = (lane & w) != 0;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
-      v[i] = f(keep, __shfl_xor_sync(0xFFFFFFFFu, send, w));
-    }
-  }
-}
-
 // ---- keys of a tile. A lane takes token lane % 8 of an octet and a code word (2 bits: 16 channels, 4 bits: 8);
 //      a warp one key group and half of the words, so a lane unpacks four tokens per scale. Groups behind the
 //      quantized keys are fp16 rows.
+//      A stored key enters as s (c - c0), exact in one fp16 at 2 bits and in two at 4 (`rest`), the scales times a power
+//      of two that puts the group's largest in [2^11, 2^12); its constants s (z - c0), times one of their own, as two
+//      rows of `consts`. unit: what their sums count.
 //      free() waits until the tile may be written: the codes are unpacked into registers before. ----
 template <int KB, typename F>
 __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
                                             const unsigned char* codes, const unsigned char* scale,
-                                            const unsigned char* zero, unsigned char* dst0, int warp, int lane, F free) {
+                                            const unsigned char* zero, unsigned char* dst0, unsigned char* rest0,
+                                            unsigned char* consts, float* unit, int warp, int lane, F free) {
   constexpr int kRow = kD * KB / 8;
   const int g = warp & 3, tok = 32 * g + (lane & 7);
   if (t0 + 32 * g < len.nqk) {
     constexpr int kBlocks = (KB == 2) ? 1 : 2;   // of four words
     constexpr int kPairs = (KB == 2) ? 8 : 4;    // channel pairs of a word
     const int w0 = (warp >> 2) * 4 * kBlocks + (lane >> 3);
-    uint32_t o[kBlocks][4][kPairs];
+    scale += g * kD * 2;
+    zero += g * kD * 2;
+    const uint2 four = *reinterpret_cast<const uint2*>(scale + 8 * lane);
+    const __half2 t = __hmax2(__habs2(as_h2(four.x)), __habs2(as_h2(four.y)));
+    const int e = 26 - (int)(__reduce_max_sync(0xFFFFFFFFu, max(as_u(t) & 0xFFFFu, as_u(t) >> 16)) >> 10);  // -5 .. 26
+    if (warp < 4) {
+      // the lane's pairs j, j + 1 of 16 channels, j = 2 (lane % 4), in pair order
+      const int j = lane & 3, ch = 16 * (lane >> 2) + (KB == 2 ? 2 * j : 8 * (j >> 1) + 2 * (j & 1));
+      constexpr int kTo = KB == 2 ? 8 : 4;  // channels of a pair are kTo apart
+      float2 y[2];
+      float most = 0.f;
+      {
+        const float2 sa = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(scale + 2 * ch)));
+        const float2 sb = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(scale + 2 * (ch + kTo))));
+        const float2 za = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(zero + 2 * ch)));
+        const float2 zb = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(zero + 2 * (ch + kTo))));
+        constexpr float c0 = kCentre<KB>;
+        y[0] = make_float2(sa.x * (za.x - c0), sb.x * (zb.x - c0));
+        y[1] = make_float2(sa.y * (za.y - c0), sb.y * (zb.y - c0));
+      }
+      most = fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fabsf(y[1].x), fabsf(y[1].y)));
+      // the largest in [2^13, 2^14)
+      const int top = (int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)) >> 23), sh = min(140 - top, 64);
+      const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        y[i] = __fmul2_rn(y[i], make_float2(f, f));
+        hi[i] = pack_h2(y[i].x, y[i].y);
+        const float2 back = __half22float2(as_h2(hi[i]));
+        lo[i] = pack_h2(y[i].x - back.x, y[i].y - back.y);
+      }
+      unsigned char* at = consts + (2 * (lane >> 2) + (j >> 1)) * kConst + 4 * g * 16 + (j & 1) * 8;
+      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(at + 16) = make_uint2(lo[0], lo[1]);
+      if (lane == 0) {
+        unit[g] = __uint_as_float((uint32_t)(127 - e) << 23);
+        unit[4 + g] = __uint_as_float((uint32_t)(127 - sh) << 23);
+      }
+    }
+    uint32_t o[kBlocks][4][kPairs], r[KB == 4 ? kBlocks : 1][4][kPairs];
+    const __half2 f0 = as_h2((uint32_t)(min(e, 15) + 15) * 0x4000400u), f1 = as_h2((uint32_t)(max(e, 15)) * 0x4000400u);
 #pragma unroll
     for (int blk = 0; blk < kBlocks; ++blk) {
       const int w = w0 + 4 * blk;
-      __half2 s[kPairs], nsz[kPairs];
-      const uint4* sp = reinterpret_cast<const uint4*>(scale + (g * kD + 2 * kPairs * w) * 2);
-      const uint4* zp = reinterpret_cast<const uint4*>(zero + (g * kD + 2 * kPairs * w) * 2);
+      __half2 s[kPairs];
+      const uint4* sp = reinterpret_cast<const uint4*>(scale + 2 * kPairs * w * 2);
       {
-        uint4 s0, s1, z0, z1;
+        uint4 s0, s1;
         pair_order<KB>(sp[0], sp[KB == 2 ? 1 : 0], s0, s1);
-        pair_order<KB>(zp[0], zp[KB == 2 ? 1 : 0], z0, z1);
         const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-        const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          s[j] = as_h2(sw[j]);
-          nsz[j] = __hneg2(__hmul2(s[j], as_h2(zw[j])));
+        for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(as_h2(sw[j]), f0);
+        if (e > 15) {  // the rest of a power past the largest fp16 one
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(s[j], f1);
         }
       }
       uint32_t u[4];
@@ -1220,18 +1256,26 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) o[blk][i][j] = dequant_h2(code_h2<KB>(cs0, u[i], j), s[j], nsz[j]);
+        for (int j = 0; j < kPairs; ++j) {
+          const __half2 c = code_h2<KB, kCentre<KB>>(cs0, u[i], j);
+          o[blk][i][j] = as_u(__hmul2(c, s[j]));
+          if constexpr (KB == 4) r[blk][i][j] = product_rest(as_u(c), as_u(s[j]), o[blk][i][j]);
+        }
     }
     free();
 #pragma unroll
     for (int blk = 0; blk < kBlocks; ++blk)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = tok + 8 * i;
+        const int t = tok + 8 * i, at = (t >> 3) * 2048 + (w0 + 4 * blk) * (kPairs * 32) + (t & 7) * 16;
         const uint32_t(&x)[kPairs] = o[blk][i];
-        unsigned char* dst = dst0 + (t >> 3) * 2048 + (w0 + 4 * blk) * (kPairs * 32) + (t & 7) * 16;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
-        if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + 128) = make_uint4(x[4], x[5], x[6], x[7]);
+        *reinterpret_cast<uint4*>(dst0 + at) = make_uint4(x[0], x[1], x[2], x[3]);
+        if constexpr (KB == 2) {
+          *reinterpret_cast<uint4*>(dst0 + at + 128) = make_uint4(x[4], x[5], x[6], x[7]);
+        } else {
+          const uint32_t(&y)[kPairs] = r[blk][i];
+          *reinterpret_cast<uint4*>(rest0 + at) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
       }
   } else {
     const int c = (warp >> 2) * 4 + (lane >> 3);  // 16 channels c
@@ -1245,40 +1289,59 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
     free();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = tok + 8 * i;
+      const int t = tok + 8 * i, at = (t >> 3) * 2048 + c * 256 + (t & 7) * 16;
       uint4 x0, x1;
       pair_order<KB>(x[i][0], x[i][1], x0, x1);
-      unsigned char* dst = dst0 + (t >> 3) * 2048 + c * 256 + (t & 7) * 16;
-      *reinterpret_cast<uint4*>(dst) = x0;
-      *reinterpret_cast<uint4*>(dst + 128) = x1;
+      *reinterpret_cast<uint4*>(dst0 + at) = x0;
+      *reinterpret_cast<uint4*>(dst0 + at + 128) = x1;
+      if constexpr (KB == 4) {
+        *reinterpret_cast<uint4*>(rest0 + at) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(rest0 + at + 128) = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
   }
 }
 
 // ---- values of a tile, transposed. A thread takes a token octet and eight channels; octets with tokens behind
-//      the quantized values mix stored tokens and fp16 rows ----
-template <int VB>
+//      the quantized values mix stored tokens and fp16 rows. Stored values enter as s (c - c0), their constants as rows
+//      of `consts` (of four threads with one channel group each writes one: s z, the rest of it, c0 s, and ones, which
+//      stay), all of them halved: 8 s passes the fp16 range for values near its end.
+//      free() waits until the tile may be written. ----
+template <int VB, typename F>
 __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int b, int h, int t0,
                                               const unsigned char* codes, const unsigned char* scale,
-                                              const unsigned char* zero, unsigned char* dst0, int* nonfinite, int warp,
-                                              int lane) {
+                                              const unsigned char* zero, unsigned char* dst0, unsigned char* consts,
+                                              int* nonfinite, int warp, int lane, F free) {
   constexpr int kRow = kD * VB / 8;
   const int c = lane & 15, oct = 2 * warp + (lane >> 4), flip = oct & 1;
   unsigned char* dst = dst0 + c * kVRowGrp + oct * 128;
   const unsigned char* cw = codes + 8 * oct * kRow + ((VB == 2) ? (c >> 1) : c) * 4;
   const uint16_t* sp = reinterpret_cast<const uint16_t*>(scale) + 8 * oct * 4 + (c >> 2);
   const uint16_t* zp = reinterpret_cast<const uint16_t*>(zero) + 8 * oct * 4 + (c >> 2);
-  if (t0 + 8 * oct < len.nqv) {
-    uint32_t w[8];  // place i of the octet: token i ^ flip
-    __half2 s[4], nsz[4];
+  const int n = len.nqv - t0 - 8 * oct;  // stored tokens from the octet's first
+  uint32_t w[8], s2[4], y[4];  // place i of the octet: token i ^ flip
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(cw + (i ^ flip) * kRow);
+  for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(cw + (i ^ flip) * kRow);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ta = ((2 * i) ^ flip) * 4, tb = ((2 * i + 1) ^ flip) * 4;
-      s[i] = as_h2(sp[ta] | ((uint32_t)sp[tb] << 16));
-      nsz[i] = __hneg2(__hmul2(s[i], as_h2(zp[ta] | ((uint32_t)zp[tb] << 16))));
+  for (int i = 0; i < 4; ++i) {
+    const int ta = (2 * i) ^ flip, tb = (2 * i + 1) ^ flip;
+    uint32_t z2;
+    s2[i] = z2 = 0;  // of tokens behind the stored ones
+    if (ta < n) {
+      s2[i] = sp[4 * ta];
+      z2 = zp[4 * ta];
     }
+    if (tb < n) {
+      s2[i] |= (uint32_t)sp[4 * tb] << 16;
+      z2 |= (uint32_t)zp[4 * tb] << 16;
+    }
+    s2[i] = halved(s2[i]);
+    const uint32_t p = as_u(__hmul2(as_h2(s2[i]), as_h2(z2)));
+    y[i] = (c & 3) == 0 ? p : (c & 3) == 1 ? product_rest(s2[i], z2, p) : as_u(__hmul2(as_h2(s2[i]), __float2half2_rn(kCentre<VB>)));
+  }
+  free();
+  if ((c & 3) < 3) *reinterpret_cast<uint4*>(consts + oct * kConst + c * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+  if (n > 0) {
     if constexpr (VB == 2) {
       const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
       uint32_t x[4];
@@ -1288,7 +1351,7 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
       for (int e = 0; e < 8; ++e) {
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<2>(cs0, x[i], e), s[i], nsz[i]);
+        for (int i = 0; i < 4; ++i) o[i] = as_u(__hmul2(code_h2<2, kCentre<2>>(cs0, x[i], e), as_h2(s2[i])));
         *reinterpret_cast<uint4*>(dst + e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     } else {
@@ -1301,7 +1364,7 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
         for (int e = 0; e < 4; ++e) {
           uint32_t o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = dequant_h2(code_h2<4>(cs0, x[i], e), s[i], nsz[i]);
+          for (int i = 0; i < 4; ++i) o[i] = as_u(__hmul2(code_h2<4, kCentre<4>>(cs0, x[i], e), as_h2(s2[i])));
           *reinterpret_cast<uint4*>(dst + (4 * hw + e) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
@@ -1322,7 +1385,7 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
       for (int e = 0; e < 4; ++e) {
         const int t = t8 + i + e;
         if (t < len.nqv) continue;
-        uint32_t x[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+        uint32_t x[4] = {halved(u[e].x), halved(u[e].y), halved(u[e].z), halved(u[e].w)};
         // A drafted value is seen only by the rows whose mask has it, but the product multiplies it by every row's
         // weight, 0 for the others: one that is not finite is staged as 0 and added at the end to the rows that see it.
         if (t >= len.n) {
@@ -1355,6 +1418,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   float* rowm = reinterpret_cast<float*>(sm + L::kOffM);
   float* rowf = reinterpret_cast<float*>(sm + L::kOffF);
   float* red = reinterpret_cast<float*>(sm + L::kOffRed);
+  float* unit = reinterpret_cast<float*>(sm + L::kOffUnit);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // scores done
   uint64_t* bar_o = bar_s + 1;                                      // value product done
   uint64_t* bar_k = bar_s + 2;                                      // the tile's stored keys landed
@@ -1414,6 +1478,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     *nonfinite = 0;
     fence_mbar_init();
   }
+  // the rows of ones among the values' constants: their sums are those of the weights
+  if (tid < 64) *reinterpret_cast<uint4*>(sm + L::kOffW + (tid & 15) * kConst + (4 * (tid >> 4) + 3) * 16) = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);
   tmem_before();
   __syncthreads();
   tmem_after();
@@ -1425,11 +1491,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   constexpr int kHR = ROWS / 2;                            // rows a thread works on
   const int r0 = half * kHR;
   uint32_t phase = 0;    // of the barriers: one completion each per tile
-  // the operands' descriptors; a k-step further on is 256 bytes (16 units) further on in each
+  // the operands' descriptors; a k-step further on is 256 bytes (16 units) further on, 2 kConst in the constants
   const uint64_t desc_k = tree_desc(smem_u32(sm + L::kOffK), 128, 2048), desc_q = tree_desc(smem_u32(sm + L::kOffQ), 128, 2048);
   const uint64_t desc_v = tree_desc(smem_u32(sm + L::kOffV), 128, kVRowGrp), desc_p = desc_k;  // P lies where K was
+  const uint64_t desc_kr = tree_desc(smem_u32(sm + L::kOffV), 128, 2048);  // the keys' second parts, before the values
+  const uint64_t desc_z = tree_desc(smem_u32(sm + L::kOffZ), kConst, 16), desc_w = tree_desc(smem_u32(sm + L::kOffW), kConst, 16);
   const CodeScale cs0;
-  float2 l[kHR / 2];
   bool first = true;    // of the segment's tiles in this block
   int tile_first = 0;   // that tile
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -1452,8 +1519,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     }
     if (first) {
       // ---- the segment's query rows, masks and running state (8 lanes a row) ----
-#pragma unroll
-      for (int i = 0; i < kHR / 2; ++i) l[i] = make_float2(0.f, 0.f);
 #pragma unroll 1  // run once per segment: fewer instructions to fetch
       for (int i = tid; i < ROWS * 8; i += kTreeThreads) {
         const int r = i >> 3, c = i & 7;
@@ -1476,7 +1541,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       tile_first = tile;
     }
     wait(bar_k, phase);
-    unpack_keys<KB>(cs0, a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, warp, lane, [&]() {
+    unpack_keys<KB>(cs0, a, len, b, h, t0, stage, stage + S::kKs, stage + S::kKz, sm + L::kOffK, sm + L::kOffV, sm + L::kOffZ, unit, warp, lane, [&]() {
       if (p > p0) wait(bar_o, phase ^ 1);  // the value product before has read its weights
       tmem_after();
     });
@@ -1487,27 +1552,57 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       tmem_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k) umma_f16(tmem, desc_k + 16 * k, desc_q + 16 * k, tree_idesc(ROWS, false), k > 0);
+      if constexpr (KB == 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) umma_f16(tmem, desc_kr + 16 * k, desc_q + 16 * k, tree_idesc(ROWS, false), 1);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_f16(tmem + 2 * ROWS, desc_z + k * (2 * kConst / 16), desc_q + 16 * k, tree_idesc(ROWS, false), k > 0);
       tree_commit(bar_s);
     }
     if (tid == 96 && more) keys_of(nw);  // every thread has read this tile's
     wait(bar_v, phase);
-    unpack_values<VB>(cs0, a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, nonfinite, warp, lane);
+    unpack_values<VB>(cs0, a, len, b, h, t0, stage + S::kVc, stage + S::kVs, stage + S::kVz, sm + L::kOffV, sm + L::kOffW, nonfinite, warp, lane, [&]() {
+      if constexpr (KB == 4) wait(bar_s, phase);  // the score product has read the keys' second parts
+    });
     wait(bar_s, phase);
     tmem_after();
-    // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1, two rows an operation. x = s c is rounded
+    // ---- the constants' part of the scores of the warp's key group, negative: lanes 0 and 1 hold its two sums ----
+    float* nz = red + quad * ROWS + r0;
+    const bool stored = t0 + 32 * quad < len.nqk;
+    if (stored) {
+      uint32_t zr[kHR];
+#pragma unroll
+      for (int i = 0; i < kHR; i += 8) tmem_ld8(t_lane + 2 * ROWS + r0 + i, zr + i);
+      tmem_wait_ld();
+      if (lane < 2) {
+#pragma unroll
+        for (int i = 0; i < kHR; i += 4)
+          *reinterpret_cast<uint4*>(nz + 4 * ROWS * lane + i) = make_uint4(zr[i], zr[i + 1], zr[i + 2], zr[i + 3]);
+      }
+      __syncwarp();
+      if (lane < kHR) nz[lane] = -(nz[lane] + nz[4 * ROWS + lane]) * unit[4 + quad];
+    } else if (lane < kHR) {
+      nz[lane] = 0.f;
+    }
+    __syncwarp();
+    // ---- weights: this thread's token against rows r0 .. r0 + kHR - 1, two rows an operation. x is rounded
     //      before the maximum is taken from it, so that the largest score's weight is exact however large it is ----
     const int tt = 32 * quad + lane;
     float2 x[kHR / 2];
     {
+      const float un = stored ? unit[quad] : 1.f;
       uint32_t xr[kHR];
 #pragma unroll
       for (int i = 0; i < kHR; i += 8) tmem_ld8(t_lane + r0 + i, xr + i);
       tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < kHR; i += 4) {
-        const float4 c4 = *reinterpret_cast<const float4*>(rowc + r0 + i);
-        x[i / 2] = __fmul2_rn(make_float2(__uint_as_float(xr[i]), __uint_as_float(xr[i + 1])), make_float2(c4.x, c4.y));
-        x[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(xr[i + 2]), __uint_as_float(xr[i + 3])), make_float2(c4.z, c4.w));
+        const float4 c4 = *reinterpret_cast<const float4*>(rowc + r0 + i), z4 = *reinterpret_cast<const float4*>(nz + i);
+        const float2 u2 = make_float2(un, un);
+        x[i / 2] = __fmul2_rn(__ffma2_rn(make_float2(__uint_as_float(xr[i]), __uint_as_float(xr[i + 1])), u2, make_float2(z4.x, z4.y)), make_float2(c4.x, c4.y));
+        x[i / 2 + 1] = __fmul2_rn(__ffma2_rn(make_float2(__uint_as_float(xr[i + 2]), __uint_as_float(xr[i + 3])), u2, make_float2(z4.z, z4.w)), make_float2(c4.z, c4.w));
       }
     }
     if (t0 + kTile > len.n) {  // drafted tokens in the tile, or none at all behind the last one
@@ -1553,20 +1648,20 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         if (up) rowm[r] = kRaise - mt;
       }
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kHR / 2; ++i) l[i] = __fmul2_rn(l[i], *reinterpret_cast<const float2*>(rowf + r0 + 2 * i));
-      if (!first) {  // O^T: the value product of the tile before is done (waited for below)
+      if (!first) {  // the sums: the value product of the tile before is done (waited for above)
         tmem_after();
 #pragma unroll
-        for (int i = 0; i < kHR; i += 8) {
-          uint32_t u[8];
-          float o[8];
-          tmem_ld8(t_lane + ROWS + r0 + i, u);
-          tmem_wait_ld();
+        for (int y = ROWS; y < 4 * ROWS; y += 2 * ROWS)  // O^T, and the constants' and weights'
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(u[e]) * rowf[r0 + i + e];
-          tmem_st8(t_lane + ROWS + r0 + i, o);
-        }
+          for (int i = 0; i < kHR; i += 8) {
+            uint32_t u[8];
+            float o[8];
+            tmem_ld8(t_lane + y + r0 + i, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(u[e]) * rowf[r0 + i + e];
+            tmem_st8(t_lane + y + r0 + i, o);
+          }
         tmem_wait_st();
       }
     }
@@ -1580,8 +1675,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         float2 d0 = __fadd2_rn(x[y], make_float2(m4.x, m4.y)), d1 = __fadd2_rn(x[y + 1], make_float2(m4.z, m4.w));
         d0 = make_float2(exp2_approx(d0.x), exp2_approx(d0.y));
         d1 = make_float2(exp2_approx(d1.x), exp2_approx(d1.y));
-        l[y] = __fadd2_rn(l[y], d0);
-        l[y + 1] = __fadd2_rn(l[y + 1], d1);
         o[e / 2] = pack_h2(d0.x, d0.y);
         o[e / 2 + 1] = pack_h2(d1.x, d1.y);
       }
@@ -1594,20 +1687,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       tmem_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k) umma_f16(tmem + ROWS, desc_v + 16 * k, desc_p + 16 * k, tree_idesc(ROWS, true), !first || k > 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_f16(tmem + 3 * ROWS, desc_w + k * (2 * kConst / 16), desc_p + 16 * k, tree_idesc(ROWS, true), !first || k > 0);
       tree_commit(bar_o);
     }
     first = false;
 
     // ---- the segment ends here (or the share does): hand its sums on ----
     if (last || p + 1 == p1) {
-      {  // l: over the tokens (lanes and quadrants)
-        float v[kHR];
-#pragma unroll
-        for (int i = 0; i < kHR; ++i) v[i] = (i & 1) ? l[i >> 1].y : l[i >> 1].x;
-        lanes_reduce<kHR>(v, lane, [](float p, float q) { return p + q; });
-        if (lane < kHR) red[quad * ROWS + r0 + lane] = v[0];
-      }
-      __syncthreads();
       const bool earlier = p - tile < p0;  // the segment began in an earlier block
       const bool whole = last && !earlier;
       if (earlier) sh.first = last ? 2 : 1;
@@ -1616,21 +1704,41 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         sh.nd = len.nd;
       }
       float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<ROWS>();
+      wait(bar_o, phase);
+      tmem_after();
+      // the sums of the constants of the warp's channel group and of the weights, lanes 0 .. 3, where the weights lay
+      float* wc = reinterpret_cast<float*>(sm + L::kOffK) + 4 * ROWS * quad;
+      {
+        uint32_t u[kHR];
+#pragma unroll
+        for (int i = 0; i < kHR; i += 8) tmem_ld8(t_lane + 3 * ROWS + r0 + i, u + i);
+        tmem_wait_ld();
+        if (lane < 4) {
+#pragma unroll
+          for (int i = 0; i < kHR; i += 4)
+            *reinterpret_cast<uint4*>(wc + ROWS * lane + r0 + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+        }
+        __syncwarp();
+        if (lane < kHR) {
+          const int r = r0 + lane;
+          wc[r] = wc[2 * ROWS + r] - (wc[r] + wc[ROWS + r]);
+          if (quad == 0) red[r] = wc[3 * ROWS + r];
+        }
+      }
+      __syncthreads();
       // each row's place in the output or the slot (-1: padding) and factor, once for all channels
       int* at_row = reinterpret_cast<int*>(rowc);
       if (tid < ROWS) {
         const int r = tid, row = row0 + r, di = div_by(row, a.rep);
-        const float lt = red[r] + red[ROWS + r] + red[2 * ROWS + r] + red[3 * ROWS + r];
+        const float lt = red[r];
         const bool real = row < rows_all && di < len.nd;
         if (real && !whole) {
           slot[(size_t)ROWS * kD + r] = -rowm[r];
           slot[(size_t)ROWS * kD + ROWS + r] = lt;
         }
         at_row[r] = !real ? -1 : whole ? di * a.Hq + h * rep + row - di * rep : r;
-        rowf[r] = !whole ? 1.f : (lt > 0.f || lt != lt) ? 1.f / lt : 0.f;
+        rowf[r] = !whole ? 2.f : (lt > 0.f || lt != lt) ? 2.f / lt : 0.f;  // values were halved
       }
-      wait(bar_o, phase);
-      tmem_after();
       __syncthreads();
       const int ch = 32 * quad + lane;
       if (*nonfinite != 0) {  // of the drafted tokens in this block's tiles
@@ -1657,14 +1765,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       for (int i = r0; i < r0 + kHR; i += 4) {
         uint32_t u[4];
         tmem_ld4(t_lane + ROWS + i, u);
-        const float4 f4 = *reinterpret_cast<const float4*>(rowf + i);
+        const float4 f4 = *reinterpret_cast<const float4*>(rowf + i), w4 = *reinterpret_cast<const float4*>(wc + i);
         const int4 at4 = *reinterpret_cast<const int4*>(at_row + i);
-        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+        const float f[4] = {f4.x, f4.y, f4.z, f4.w}, y[4] = {w4.x, w4.y, w4.z, w4.w};
         const int at[4] = {at4.x, at4.y, at4.z, at4.w};
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float o = f[e] == 0.f ? 0.f : __uint_as_float(u[e]) * f[e];
+          const float o = f[e] == 0.f ? 0.f : (__uint_as_float(u[e]) + y[e]) * f[e];
           if (at[e] < 0) continue;
           if (f32) to32[(size_t)at[e] * kD] = o;
           else to16[(size_t)at[e] * kD] = f32_to_bf16(o);
@@ -1781,10 +1889,8 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
 // Rows of a tile, which also choose the kernel: the warp-wide products for 8 or 16 rows, tcgen05 with 32 or 64. Of
 // a tile's cost most is the same for any number of rows (the codes are unpacked once), so the smallest tile that holds
 // all rows wins, and 64 above that. Measured with one kernel and the other (16 requests, 32 KV heads, 4K context, 2
-// bits): 8 rows on the tile of 8 / 16 / 32: 78 / 120 / 166 us; 16 rows on 16 / 32: 123 / 168 (before the 3 % for
-// small scales);
-// 32 rows on 32 / 64: 173 / 201 (warp-wide on 32: 334 when 16 took 145); 64 rows on 32 / 64: 328 / 213. A tile of 96
-// does not fit two blocks an SM with the sums of a row in registers.
+// bits): 8 rows on the tile of 8 / 16 / 32: 102 / 159 / 221 us; 16 rows on 16 / 32: 166 / 223; 32 rows on 32 / 64:
+// 228 / 274; 64 rows on 32 / 64: 448 / 288. A tile of 96 does not fit two blocks an SM with the sums of a row in registers.
 int tree_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 int sm_count_tree() {
   static int cached[64] = {};

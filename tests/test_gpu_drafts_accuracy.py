@@ -39,7 +39,7 @@ def check_attention_bound(case, cache=None):
         C.check_close(got[b][real[b]], ref[b][real[b]])
 
 
-SMALL = [(1, 1), (1, 8), (2, 7), (4, 4)]
+SMALL, LARGE = [(1, 1), (1, 8), (2, 7), (4, 4)], [(4, 5), (3, 16), (7, 33), (2, 64)]
 BITS = [(2, 2), (4, 4), (2, 4), (4, 2)]
 
 
@@ -52,6 +52,12 @@ def ragged_case(rep, N, kb, vb):
 @pytest.mark.parametrize("kb,vb", BITS)
 @pytest.mark.parametrize("rep,N", SMALL)
 def test_up_to_16_rows_within_the_attention_bound(rep, N, kb, vb):
+    check_attention_bound(ragged_case(rep, N, kb, vb))
+
+
+@pytest.mark.parametrize("kb,vb", BITS)
+@pytest.mark.parametrize("rep,N", LARGE)
+def test_more_rows_within_the_attention_bound(rep, N, kb, vb):
     check_attention_bound(ragged_case(rep, N, kb, vb))
 
 
@@ -85,3 +91,9 @@ def prefilled_case(seed, n, rep, N, kb, vb, offset=0.0):
 @pytest.mark.parametrize("rep,N", [(1, 8), (2, 8)])
 def test_up_to_16_rows_over_a_prefilled_cache(rep, N, kb, vb):
     check_attention_bound(*prefilled_case(4100, 3000, rep, N, kb, vb))
+
+
+@pytest.mark.parametrize("kb,vb", BITS)
+@pytest.mark.parametrize("rep,N", [(4, 8), (4, 48)])
+def test_more_rows_over_a_prefilled_cache(rep, N, kb, vb):
+    check_attention_bound(*prefilled_case(4200, 3000, rep, N, kb, vb))
