@@ -397,11 +397,12 @@ kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_ro
  * Arithmetic: softmax statistics and all sums in fp32; for values of a few units the fp32 output is
  * within max-abs 2e-3 and rel-L2 1e-3 of fp64. The tensor cores take fp16 operands: queries, scaled
  * by a power of two for each row; what is made of key codes, scales and zero-points exactly or in
- * two parts (relative 2^-21; with up to 16 rows, N * n_q_heads / n_heads, scales are taken times
- * 2^10 where a 32-token group has none of 2^-6); a quantized value s (q - z) as s (q - c0), c0 the
- * middle code, exact with 2 bits and rounded once with 4, and its group's constants exactly, all
- * halved (absolute 2^-25 below 2^-13); the softmax weights rounded once (relative 2^-11), their
- * sum being that of the rounded ones.
+ * two parts (a query element is off by at most 2^-27 of its row's largest, its product with a key
+ * scale by 2^-21 of itself or 2^-34 of the largest such product of the row and the 32-token
+ * group); a quantized value s (q - z) as s (q - c0), c0 the middle code, exact with 2 bits and
+ * rounded once with 4, and its group's constants exactly, all halved (absolute 2^-25 below
+ * 2^-13); the softmax weights rounded once (relative 2^-11), their sum being that of the rounded
+ * ones.
  * ws: device workspace of at least kvq_kivi_tree_workspace_size() bytes, needing no
  * initialisation. Two calls that run at the same time need two workspaces.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_CAPACITY (B > max_batch), KVQ_ERR_WORKSPACE,

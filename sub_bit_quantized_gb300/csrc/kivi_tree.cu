@@ -374,8 +374,9 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
 //    half of a code word is the fp16 subnormal code 2^(k - 24), exact; the scales of the group go into the queries,
 //    q s 2^-k = q' + q'' with q' its fp16 and q'' the exact rest as fp16, in both sums (with q' alone the output was off
 //    by up to 7e-3, three times the bound of attention), and the second sum is a product with the zero-points as A.
-//    A group whose scales are all below 2^-6 has them times 2^10, or q' would lose bits as a subnormal: at 4 bits and
-//    scales near 2^-16 results were off by 4e-2 instead of 4e-4.
+//    The group's scales are taken times a power of two that puts the largest in [2^6, 2^7), the queries' rows likewise:
+//    products reach 2^14, and scales down to 2^-20 of the largest keep their bits beside it (a dead channel has scale
+//    1; times a fixed 2^10 for all groups of small scales, one such channel left errors of 0.17 at scales near 2^-16).
 //  * Values: s (c - z) = s (c - c0) - (s z - c0 s) with the middle code c0: the first part is one fp16 (exact at 2 bits,
 //    one rounding of at most 8 s at 4), the second one number per token and channel group. A product of its own has
 //    the constants as its rows: s z as fp16, the exact rest of it, c0 s, and ones, whose sums are those of the rounded
@@ -384,7 +385,7 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
 // Bound: instruction issue. A group of 32 tokens costs a warp about 210 instructions for the keys (1 per code pair),
 // 50 for the softmax of 8 rows and 280 for the values (3 per code pair), and 66 products per 8 rows.
 // Measured (16 requests, 32 KV heads, 4K context, 2 bits): 102 us for 8 rows (208 MB, 2.0 TB/s, 30 % of the copy rate),
-// 166 us for 16; the second parts q'' and the constants' products are 22 and 40 of it (max-abs error of the parity cases 7e-3
+// 164 us for 16; the second parts q'' and the constants' products are 22 and 38 of it (max-abs error of the parity cases 7e-3
 // without, 1e-3 with them). Per-warp rings of two groups by cp.async (each lane copies what its warp reads, so no block barrier
 // in the loop); four blocks of four warps an SM for 8 rows, two for 16, as the registers of the sums allow (three, with
 // spills in the loop: 173 us). Five blocks of 96 registers for 8 rows spilled in the loop: 105 us against 88 then.
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       const int r = x >> 3, c = x & 7;
       uint32_t u[8], o[8];
       const bool real = load_query(a, w.len, w.b, h, r, c, u);
-      const float back = query_fp16<-1>(u, o, scale_log2);
+      const float back = query_fp16<6>(u, o, scale_log2);
       uint4 x0, x1;
       pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
       x0 = make_uint4(pos_scale<KB, -1>(x0.x, 0), pos_scale<KB, -1>(x0.y, 1), pos_scale<KB, -1>(x0.z, 2), pos_scale<KB, -1>(x0.w, 3));
@@ -618,23 +619,30 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
               u[t][3] = v.w;
             }
           }
-          float down = 1.f;
+          float code_unit, zero_unit;  // what a sum of code products and one with the zero-points count
           {  // the group's scales and zero-points in pair order, in place: a lane takes 16 channels of one of them
             uint4* blk = reinterpret_cast<uint4*>(const_cast<unsigned char*>(stage) + S::kKs) + 2 * (lane & 15);
             uint4 x0, x1;
             pair_order<KB>(blk[0], blk[1], x0, x1);
-            // scales all below 2^-6 (lanes 0 .. 7) are taken times 2^10, exactly: q' keeps its bits
-            const __half2 top = __hmax2(__hmax2(__hmax2(__habs2(as_h2(x0.x)), __habs2(as_h2(x0.y))), __hmax2(__habs2(as_h2(x0.z)), __habs2(as_h2(x0.w)))),
-                                        __hmax2(__hmax2(__habs2(as_h2(x1.x)), __habs2(as_h2(x1.y))), __hmax2(__habs2(as_h2(x1.z)), __habs2(as_h2(x1.w)))));
-            const bool high = lane < 8 && __hbgt2(__hmax2(top, __lowhigh2highlow(top)), __float2half2_rn(0.01562f));
-            if (!__any_sync(0xFFFFFFFFu, high)) {
-              down = 1.f / 1024.f;
-              if (lane < 8) {
-                uint32_t* w[8] = {&x0.x, &x0.y, &x0.z, &x0.w, &x1.x, &x1.y, &x1.z, &x1.w};
+            // The scales (lanes 0 .. 7) are taken times the power of two that puts the group's largest in [2^6, 2^7):
+            // however small, and beside whatever larger ones, the others keep their bits in q' then.
+            const __half2 t = __hmax2(__hmax2(__hmax2(__habs2(as_h2(x0.x)), __habs2(as_h2(x0.y))), __hmax2(__habs2(as_h2(x0.z)), __habs2(as_h2(x0.w)))),
+                                      __hmax2(__hmax2(__habs2(as_h2(x1.x)), __habs2(as_h2(x1.y))), __hmax2(__habs2(as_h2(x1.z)), __habs2(as_h2(x1.w)))));
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, lane < 8 ? max(as_u(t) & 0xFFFFu, as_u(t) >> 16) : 0u);
+            const int e = 21 - (int)(top >> 10);  // -10 .. 21
+            if (lane < 8) {
+              uint32_t* x[8] = {&x0.x, &x0.y, &x0.z, &x0.w, &x1.x, &x1.y, &x1.z, &x1.w};
+              const __half2 f = as_h2((uint32_t)(min(e, 15) + 15) * 0x4000400u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) *w[i] = as_u(__hmul2(as_h2(*w[i]), __float2half2_rn(1024.f)));
+              for (int i = 0; i < 8; ++i) *x[i] = as_u(__hmul2(as_h2(*x[i]), f));
+              if (e > 15) {  // the rest of a power past the largest fp16 one
+                const __half2 f1 = as_h2((uint32_t)e * 0x4000400u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *x[i] = as_u(__hmul2(as_h2(*x[i]), f1));
               }
             }
+            code_unit = __uint_as_float((uint32_t)(127 + 24 - e) << 23);  // codes are 2^-24 of themselves in the products
+            zero_unit = __uint_as_float((uint32_t)(127 - e) << 23);
             if (lane < 16) {
               blk[0] = x0;
               blk[1] = x1;
@@ -688,8 +696,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float c = cs[nt][e & 1] * down;
-                s[nt][t][e] = fmaf(s[nt][t][e], c * 16777216.f, -zs[nt][e & 1] * c);  // codes are 2^-24 of themselves in the products
+                const float c = cs[nt][e & 1];
+                s[nt][t][e] = fmaf(s[nt][t][e], c * code_unit, -zs[nt][e & 1] * (c * zero_unit));
               }
         } else {  // fp16 rows: residual, drafted, or none
           const uint16_t* row[4];

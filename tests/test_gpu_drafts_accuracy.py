@@ -1,5 +1,6 @@
 """How near the attention of drafted tokens comes to fp64: the library's bound for attention (max-abs
-2e-3, rel-L2 1e-3 of the fp32 output, as the decode's tests hold it) on queries as they come."""
+2e-3, rel-L2 1e-3 of the fp32 output, as the decode's tests hold it) on queries as they come, and keys
+and queries of unequal magnitudes within one group."""
 import numpy as np
 import pytest
 import torch
@@ -97,3 +98,27 @@ def test_up_to_16_rows_over_a_prefilled_cache(rep, N, kb, vb):
 @pytest.mark.parametrize("rep,N", [(4, 8), (4, 48)])
 def test_more_rows_over_a_prefilled_cache(rep, N, kb, vb):
     check_attention_bound(*prefilled_case(4200, 3000, rep, N, kb, vb))
+
+
+@pytest.mark.parametrize("what", ["dead", "outlier"])
+@pytest.mark.parametrize("rep,kb", [(1, 2), (1, 4), (2, 2), (2, 4), (6, 2), (6, 4)])
+@pytest.mark.parametrize("down", [9, 12, 14, 16])
+def test_small_key_scales_beside_a_large_one(rep, kb, down, what):
+    # keys times 2^-down and queries times 2^down, the same scores, with one channel whose scale is 1 in every group: a
+    # dead channel as the quantizer stores it (scale 1, codes and zero-point 0), or keys 2^down times as large as the
+    # others under queries 2^down times as small
+    case = T.make_tree_case(4300, B=2, H=2, N=6, n_quant=[256, 32], n_resid=[40, 3], rep=rep, k_bits=kb, q_scale=0.5)
+    base, f = case.base, np.float16(2.0 ** -down)
+    for x in (base.k_scale, base.k_res, case.kd):
+        x *= f
+    case.q *= 2.0 ** down
+    for x in (base.k_scale, base.k_res, case.kd):
+        x[..., 77] = 1 if what == "outlier" else 0
+    if what == "outlier":
+        base.k_res[..., 77] = base.k_res[..., 76] / f  # neighbours' values in the outlier's range
+        case.kd[..., 77] = case.kd[..., 76] / f
+        case.q[..., 77] *= 2.0 ** -down
+    else:
+        base.k_scale[..., 77], base.k_zero[..., 77], base.k_codes[..., 77] = 1, 0, 0
+    ref, bound = T.reference(case)
+    T.check_rows(T.run_tree(case), ref, bound, 7.0)
