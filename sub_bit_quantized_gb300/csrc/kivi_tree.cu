@@ -695,10 +695,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float c = cs[nt][e & 1];
-                s[nt][t][e] = fmaf(s[nt][t][e], c * code_unit, -zs[nt][e & 1] * (c * zero_unit));
-              }
+              for (int e = 0; e < 4; ++e)  // the row's own factor last: with the units it may pass the fp32 range
+                s[nt][t][e] = fmaf(s[nt][t][e], code_unit, -zs[nt][e & 1] * zero_unit) * cs[nt][e & 1];
         } else {  // fp16 rows: residual, drafted, or none
           const uint16_t* row[4];
 #pragma unroll

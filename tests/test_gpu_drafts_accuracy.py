@@ -122,3 +122,27 @@ def test_small_key_scales_beside_a_large_one(rep, kb, down, what):
         base.k_scale[..., 77], base.k_zero[..., 77], base.k_codes[..., 77] = 1, 0, 0
     ref, bound = T.reference(case)
     T.check_rows(T.run_tree(case), ref, bound, 7.0)
+
+
+@pytest.mark.parametrize("rep", [1, 2, 4, 9])
+@pytest.mark.parametrize("power", [60, 104, 118])
+def test_queries_whose_scores_still_fit_fp32(rep, power):
+    # elements up to 2^120: one token takes all the weight, so rows whose largest score stands out by more than the
+    # scores' own rounding (2^-12 of the absolute sums: fp32 sums of fp16 products, far below) equal its value
+    case = T.make_tree_case(4400, B=1, H=1, N=4, n_quant=[64], n_resid=[30], rep=rep)
+    case.q *= 2.0 ** power
+    got = T.run_tree(case)
+    assert np.isfinite(got).all()
+    K, V, _, _ = T.context(case.base, 0, 0)
+    keys, vals = (np.concatenate([x, y[0, :, 0].astype(np.float64)]) for x, y in ((K, case.kd), (V, case.vd)))
+    clear = []
+    for i in range(4):
+        seen = np.array([True] * len(K) + [bool(int(case.mask[0, i]) >> j & 1) for j in range(4)])
+        for r in range(rep):
+            q = case.q[0, i, r]
+            s, a = keys[seen] @ q, np.abs(keys[seen]) @ np.abs(q)
+            top = np.argsort(s)[-2:]
+            clear.append(s[top[1]] - s[top[0]] > 2.0 ** -12 * a.max())
+            if clear[-1]:
+                C.check_close(got[0, i, r], vals[seen][top[1]])
+    assert np.mean(clear) > 0.5
