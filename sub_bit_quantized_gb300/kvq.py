@@ -5,6 +5,7 @@ there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -142,6 +143,17 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _on(stream, device):
+    """Context in which PyTorch allocates and fills on ``stream`` (None: the current one). A block that it frees again
+    then waits for what is queued there, and one that it gives out has nothing pending elsewhere."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        h = _stream(stream)
+        stream = torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _check(st: int, where: str):
@@ -588,20 +600,31 @@ class TreeAttnCall(_Call):
         _operand("mask", mask, (torch.int64, torch.uint64), (B, N))
         if n_draft is not None:
             _operand("n_draft", n_draft, (torch.int32,), (B,))
-        if ws is None:
-            ws = make_tree_workspace(cfg, B, N, q.device)
         c, kc = cfg.to_c(), cache.c_struct()
-        super().__init__("kvq_kivi_tree_attn", stream, q.device,
-                         (c, kc, cache, q, k_draft, v_draft, mask, out, n_draft, ws))
-        self._bind(ctypes.byref(c), ctypes.byref(kc), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
-                   _ptr(n_draft), B, N, _ptr(out), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16,
-                   _ptr(ws), ws.numel() * ws.element_size())
+        super().__init__("kvq_kivi_tree_attn", stream, q.device, (c, kc, cache, q, k_draft, v_draft, mask, out, n_draft, ws))
+        args = (ctypes.byref(c), ctypes.byref(kc), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
+                _ptr(n_draft), B, N, _ptr(out), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16)
+        self._own = None  # the stream that a workspace of the call's own was allocated on
+        if ws is None:
+            with _on(stream, q.device):
+                ws = self._ws = make_tree_workspace(cfg, B, N, q.device)
+            self._own = _stream(stream)
+            self._again = lambda: make_tree_workspace(cfg, B, N, q.device)
+        self._bind(*args, _ptr(ws), ws.numel() * ws.element_size())
+
+    def __call__(self):
+        if self._own is not None and self._stream is None:
+            s = torch._C._cuda_getCurrentRawStream(self._device)
+            if s != self._own:  # called on another stream than before: a workspace that belongs there
+                self._own, self._ws = s, self._again()
+                self._args[-2] = ctypes.c_void_p(_ptr(self._ws))
+        super().__call__()
 
 
 def kvq_kivi_tree_attn(cfg: KiviConfig, cache: KiviCache, q, k_draft, v_draft, mask, out, n_draft=None, ws=None,
                        stream=None):
     """Attention of a tree of drafted tokens over the cache and one another. Without a workspace one is allocated
-    for this call (through PyTorch)."""
+    for this call (through PyTorch, on the stream it runs on)."""
     TreeAttnCall(cfg, cache, q, k_draft, v_draft, mask, out, n_draft, ws, stream)()
 
 
