@@ -84,6 +84,16 @@ def test_tree_call_kept_for_several_streams(monkeypatch):
     assert s.used == [("alloc", 5), ("run", 5), ("run", 5)]
 
 
+@pytest.mark.parametrize("stream", [7, types.SimpleNamespace(cuda_stream=9), None])
+def test_decode_workspace_comes_from_the_stream_of_the_call(monkeypatch, stream):
+    s = Streams(monkeypatch)
+    cfg, cache = tree_args()[:2]
+    q = torch.zeros((1, 2, D), dtype=torch.bfloat16)
+    kvq.kvq_decode_attn(cfg, cache, 0, 1, q, q.float(), stream=stream)
+    h = stream if isinstance(stream, int) else stream.cuda_stream if stream else 1
+    assert s.used == [("alloc", h), ("run", h)]
+
+
 @pytest.mark.gpu
 def test_tree_calls_on_a_side_stream_without_a_workspace():
     from tests import _cases as C
@@ -111,3 +121,25 @@ def test_tree_calls_on_a_side_stream_without_a_workspace():
             call()
         torch.cuda.synchronize()
         assert np.array_equal(out.double().cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+def test_decode_on_a_side_stream_without_a_workspace():
+    from tests import _cases as C
+    case = C.make_kivi_case(4600, B=1, H=2, n_quant=[32 * 200], n_resid=[60], Hq=8)
+    cache = C.fill_kivi_cache(case)
+    q = C.bf16_tensor(case.q)
+    out, want = torch.empty(q.shape, device="cuda"), torch.empty(q.shape, device="cuda")
+    kvq.kvq_decode_attn(case.cfg, cache, 0, 1, q, want)
+    size = kvq.kvq_decode_workspace_size(case.cfg, 1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for k in range(20):
+        out.zero_()
+        torch.cuda.synchronize()
+        kvq.kvq_decode_attn(case.cfg, cache, 0, 1, q, out, stream=side if k % 2 else side.cuda_stream)
+        for _ in range(4):
+            torch.full((max(size, 1),), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert (out - want).abs().max() <= 2.0 ** -20 * want.abs().max()  # fp32 sums, in any order
+    assert kvq.device_error() == 0
