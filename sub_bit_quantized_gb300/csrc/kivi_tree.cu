@@ -75,8 +75,9 @@ struct TreeLens {
 __device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
   TreeLens L;
   L.nqk = min(max(a.n_quant_k[b], 0), a.max_tokens) & -kGroupT;
-  L.nqv = (a.residual > 0) ? min(max(a.n_quant_v[b], 0), L.nqk) : L.nqk;
   L.n = L.nqk + max(0, min(a.n_tok[b] - L.nqk, a.residual));
+  // at least n - residual, as in every valid state: the ring holds no more values
+  L.nqv = (a.residual > 0) ? min(max(a.n_quant_v[b], max(L.n - a.residual, 0)), L.nqk) : L.nqk;
   L.nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
   L.tiles = L.nd > 0 ? (int)((uint32_t)(L.n + L.nd + kTile - 1) / kTile) : 0;
   return L;

@@ -146,3 +146,14 @@ def test_queries_whose_scores_still_fit_fp32(rep, power):
             if clear[-1]:
                 C.check_close(got[0, i, r], vals[seen][top[1]])
     assert np.mean(clear) > 0.5
+
+
+@pytest.mark.parametrize("rep", [1, 2, 5])
+def test_a_state_with_too_few_quantized_values_stays_in_the_buffers(rep):
+    # n_quant_v below n_tok - residual is no valid state: it counts as n_tok - residual
+    case = T.make_tree_case(4700, B=2, H=2, N=6, n_quant=[32 * 40, 256], n_resid=[90, 128], rep=rep,
+                            n_quant_v=[32 * 40 + 90 - 128, 256])
+    cache = C.fill_kivi_cache(case.base)
+    want = T.run_tree(case, cache)
+    cache.n_quant_v.copy_(torch.tensor([0, -5], dtype=torch.int32))
+    assert np.array_equal(T.run_tree(case, cache), want)
