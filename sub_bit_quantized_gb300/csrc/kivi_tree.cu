@@ -32,6 +32,7 @@
 
 #include <cfloat>
 
+#include "kivi_tree_join.h"
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
 #include "../../include/kvq.h"
@@ -108,9 +109,8 @@ struct Walk {
 // partial softmax of a segment: rows of o[128], then m, l per row
 template <int ROWS>
 __host__ __device__ constexpr size_t slot_floats() { return (size_t)ROWS * (kD + 2); }
-// What block k did with the segments it shares, for the merge. first: 0 its first segment begins there, 1 it goes
-// on past the block, 2 it ends there, 3 the block had no work. open: the segment that begins in the block and goes
-// on (b * segments per request + seg), or -1; nd: that request's drafted tokens.
+// What block k did with the segments it shares, for the merge. first: its first segment (kSeg...). open: the segment
+// that begins in the block and goes on (b * segments per request + seg), or -1; nd: that request's drafted tokens.
 struct TreeShared {
   int first, open, nd, pad;
 };
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     if (tid == 0) w = x;
     if (lane == 0) ahead = x;
   }
-  TreeShared sh = {n > 0 ? 0 : 3, -1, 0, 0};
+  TreeShared sh = {n > 0 ? kSegBegins : kSegNoWork, -1, 0, 0};
   if (n == 0) {
     if (tid == 0) shared[blockIdx.x] = sh;
     return;
@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
           for (int e = 0; e < 4; ++e) mine[element(nt, t, e)] += o[nt][t][e];
     }
     __syncthreads();
-    if (earlier) sh.first = last ? 2 : 1;
+    if (earlier) sh.first = last ? kSegEnds : kSegGoesOn;
     else if (!last) {
       sh.open = w.b * seg_per_b + w.seg;
       sh.nd = w.len.nd;
@@ -1454,7 +1454,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     if (tid == 0) place[p0 & 1] = place_of(x);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's blocks take places that become free
-  TreeShared sh = {p0 < p1 ? 0 : 3, -1, 0, 0};
+  TreeShared sh = {p0 < p1 ? kSegBegins : kSegNoWork, -1, 0, 0};
   if (p0 >= p1) {
     if (tid == 0) shared[blockIdx.x] = sh;
     return;
@@ -1705,7 +1705,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     if (last || p + 1 == p1) {
       const bool earlier = p - tile < p0;  // the segment began in an earlier block
       const bool whole = last && !earlier;
-      if (earlier) sh.first = last ? 2 : 1;
+      if (earlier) sh.first = last ? kSegEnds : kSegGoesOn;
       else if (!last) {
         sh.open = b * seg_per_b + w.seg;
         sh.nd = len.nd;
@@ -1816,7 +1816,7 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
   const TreeShared* shared = reinterpret_cast<const TreeShared*>(a.part);
   const float* slots = reinterpret_cast<const float*>(shared + G);
   const int seg_all = shared[k].open;
-  int f = k + 1 + lane < G ? shared[k + 1 + lane].first : 2;
+  int f = k + 1 + lane < G ? shared[k + 1 + lane].first : kSegNoWork;
   if (seg_all < 0) return;
   const int rep = a.rep.d, rows_all = a.N * rep;
   const int b = div_by(seg_all, a.segs), seg = seg_all - b * a.segs.d, h = div_by(seg, a.row_tiles);
@@ -1830,9 +1830,9 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
   // the blocks behind k that hold a part, 32 at a time: slot 0 of those, up to the one it ends in
   constexpr int kBatch = ROWS <= 16 ? 8 : 4;  // parts whose sums are on their way at once
   for (int base = k + 1;; base += 32) {
-    const uint32_t end = __ballot_sync(0xFFFFFFFFu, f == 2);
-    const uint32_t upto = end ? (end & -end) * 2 - 1 : 0xFFFFFFFFu;
-    uint32_t parts = __ballot_sync(0xFFFFFFFFu, f == 1 || f == 2) & upto;
+    const JoinParts join = join_parts(__ballot_sync(0xFFFFFFFFu, f == kSegGoesOn), __ballot_sync(0xFFFFFFFFu, f == kSegEnds));
+    if (join.state == 2) return;  // a block's wait ran out (reported): the row is left as it was
+    uint32_t parts = join.parts;
     const float* s = slots + (size_t)(base + lane) * 2 * slot_floats<ROWS>();
     const bool has = (parts >> lane) & 1u;
     float m = has ? s[mo] : -FLT_MAX, l = has ? s[lo] : 0.f;
@@ -1875,8 +1875,8 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
       if (!parts) break;
       load();
     }
-    if (end) break;
-    f = base + 32 + lane < G ? shared[base + 32 + lane].first : 2;
+    if (join.state == 1) break;
+    f = base + 32 + lane < G ? shared[base + 32 + lane].first : kSegNoWork;
   }
   const bool none = !(lt > 0.f || lt != lt);
   const size_t at = (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row - di * rep) * kD + 4 * lane;
