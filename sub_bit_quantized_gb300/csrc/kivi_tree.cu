@@ -1793,9 +1793,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
   }
   if (tid == 0) {
     shared[blockIdx.x] = sh;
-    if (*failed) {  // a wait that ran out leaves the loop at the next barrier: let this block's copies land first
+    if (*failed) {  // a wait that ran out leaves the loop at the next barrier: let this block's copies and products end first
       mbar_wait_bounded(bar_k, phase, 10000000ull);
       mbar_wait_bounded(bar_v, phase, 10000000ull);
+      mbar_wait_bounded(bar_o, phase ^ 1, 10000000ull);  // and its last value product, which the others came before
     }
   }
   tmem_before();
