@@ -325,7 +325,8 @@ kvq_status kvq_kivi_append(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
  * n_accept = 0 is left as it is. So is one that cannot be committed whole, and kvq_device_error()
  * then reports KVQ_ERR_INVALID_ARG (n_accept outside [0, N], an index outside [0, N)) or
  * KVQ_ERR_CAPACITY (n_accept > residual, an invalid state, or a key flush past max_tokens).
- * Commits and appends to one cache must not run at the same time.
+ * Commits and appends to one cache must not run at the same time. n_seq = 0 or N = 0 is a no-op
+ * (the arrays may be NULL then).
  * Errors: KVQ_ERR_INVALID_ARG (residual not a positive multiple of group, n_seq or N < 0),
  * KVQ_ERR_CAPACITY (n_seq > max_batch). */
 kvq_status kvq_kivi_commit(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
@@ -337,7 +338,8 @@ kvq_status kvq_kivi_commit(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
  * fp16 row, rounded once to out_dtype (KVQ_DT_*; fp16 overflows to infinity past 65504). Rows
  * whose t lies outside [0, n_tok of the request) are left as they are.
  * k_out, v_out: element (i, h, j, ch) at x[i*x_stride_b + h*x_stride_h + j*D + ch], as
- * kvq_kivi_prefill reads them; one of the two may be NULL (not read back).
+ * kvq_kivi_prefill reads them; one of the two may be NULL (not read back). B = 0 or n_tok = 0 is a
+ * no-op (both may be NULL then).
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_CAPACITY (b0 + B > max_batch), KVQ_ERR_UNSUPPORTED (a
  * call of more than 2^31 blocks). */
 kvq_status kvq_kivi_read(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
@@ -371,6 +373,7 @@ typedef struct {
  * padding: its rows are neither read nor written. One with rotation and a position >= max_ctx is
  * left as it is and raises KVQ_ERR_CAPACITY through kvq_device_error().
  * An output may be its own input (same pointer, strides and type); other overlaps are not allowed.
+ * B = 0 or N = 0 is a no-op (the rows' pointers and pos may be NULL then).
  * Errors: KVQ_ERR_INVALID_ARG (pointers, strides, types, head counts; eps outside [1e-30, 1]),
  * KVQ_ERR_UNSUPPORTED (D other than 128, more than 2^31 blocks). */
 kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_rows* k,

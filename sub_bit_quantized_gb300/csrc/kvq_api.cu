@@ -489,14 +489,14 @@ KVQ_API kvq_status kvq_kivi_commit(const kvq_kivi_cfg* c, const kvq_kivi_cache* 
   kvq_status st = check_kivi_cfg(c, __func__);
   if (st != KVQ_OK) return st;
   if ((st = check_kivi_cache(k, __func__)) != KVQ_OK) return st;
+  if (c->residual <= 0) return fail(KVQ_ERR_INVALID_ARG, "%s: the streaming cache needs residual > 0", __func__);
+  if (n_seq < 0 || N < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: n_seq or N < 0", __func__);
+  if (n_seq > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: n_seq > max_batch", __func__);
+  if (n_seq == 0 || N == 0) return KVQ_OK;  // empty arrays may have no address
   CHECK_PTR(k_draft);
   CHECK_PTR(v_draft);
   CHECK_PTR(path);
   CHECK_PTR(n_accept);
-  if (c->residual <= 0) return fail(KVQ_ERR_INVALID_ARG, "%s: the streaming cache needs residual > 0", __func__);
-  if (n_seq < 0 || N < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: n_seq or N < 0", __func__);
-  if (n_seq > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: n_seq > max_batch", __func__);
-  if (n_seq == 0 || N == 0) return KVQ_OK;
   kvq::KiviCommitArgs a{};
   a.k_draft = k_draft; a.v_draft = v_draft; a.path = path; a.n_accept = n_accept;
   a.k_codes = k->k_codes; a.k_scale = k->k_scale; a.k_zero = k->k_zero;
@@ -516,14 +516,14 @@ KVQ_API kvq_status kvq_kivi_read(const kvq_kivi_cfg* c, const kvq_kivi_cache* k,
   if (st != KVQ_OK) return st;
   if ((st = check_kivi_cache(k, __func__)) != KVQ_OK) return st;
   if ((st = check_x_strides(__func__, 0, st_b, st_h)) != KVQ_OK) return st;
+  if (!known_dtype(out_dtype)) return fail(KVQ_ERR_INVALID_ARG, "%s: out_dtype must be a KVQ_DT_ value", __func__);
+  if (b0 < 0 || B < 0 || n_tok < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: negative size", __func__);
+  if ((long long)b0 + B > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: b0 + B > max_batch", __func__);
+  if (B == 0 || n_tok == 0) return KVQ_OK;  // empty arrays may have no address
   if (tok_begin) CHECK_PTR(tok_begin);
   if (!k_out && !v_out) return fail(KVQ_ERR_INVALID_ARG, "%s: neither k_out nor v_out is given", __func__);
   if (k_out) CHECK_PTR(k_out);
   if (v_out) CHECK_PTR(v_out);
-  if (!known_dtype(out_dtype)) return fail(KVQ_ERR_INVALID_ARG, "%s: out_dtype must be a KVQ_DT_ value", __func__);
-  if (b0 < 0 || B < 0 || n_tok < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: negative size", __func__);
-  if ((long long)b0 + B > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: b0 + B > max_batch", __func__);
-  if (B == 0 || n_tok == 0) return KVQ_OK;
   if ((double)B * c->n_heads * (n_tok / 32 + 2) * (k_out && v_out ? 2 : 1) >= 2147483648.0)
     return fail(KVQ_ERR_UNSUPPORTED, "%s: too many rows for one call", __func__);
   kvq::KiviReadArgs a{};
@@ -539,11 +539,11 @@ KVQ_API kvq_status kvq_kivi_read(const kvq_kivi_cfg* c, const kvq_kivi_cache* k,
 
 // one kind of rows of kvq_qk_norm_rope: input and output of the same heads
 static kvq_status check_rows(const char* fn, const char* kind, const kvq_rows* in, const kvq_rows* out, int in_dt,
-                             kvq::QkRows* r) {
+                             bool empty, kvq::QkRows* r) {
   *r = kvq::QkRows{};
   if (!in != !out) return fail(KVQ_ERR_INVALID_ARG, "%s: %s rows need both an input and an output", fn, kind);
   if (!in) return KVQ_OK;
-  if (!aligned16(in->p) || !aligned16(out->p))
+  if (!empty && (!aligned16(in->p) || !aligned16(out->p)))  // empty arrays may have no address
     return fail(KVQ_ERR_INVALID_ARG, "%s: a pointer of the %s rows is null or not 16-byte aligned", fn, kind);
   kvq_status st = check_x_strides(fn, in->stride_t, in->stride_b, in->stride_h);
   if (st != KVQ_OK) return st;
@@ -569,10 +569,11 @@ KVQ_API kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, cons
   if (!(eps >= 1e-30f && eps <= 1.f)) return fail(KVQ_ERR_INVALID_ARG, "%s: eps outside [1e-30, 1]", __func__);
   kvq::QkRowsArgs a{};
   const int dt = q ? q->dtype : k ? k->dtype : v->dtype;
+  const bool empty = B == 0 || N == 0;
   kvq_status st;
-  if ((st = check_rows(__func__, "query", q, q_out, dt, &a.q)) != KVQ_OK) return st;
-  if ((st = check_rows(__func__, "key", k, k_out, dt, &a.k)) != KVQ_OK) return st;
-  if ((st = check_rows(__func__, "value", v, v_out, dt, &a.v)) != KVQ_OK) return st;
+  if ((st = check_rows(__func__, "query", q, q_out, dt, empty, &a.q)) != KVQ_OK) return st;
+  if ((st = check_rows(__func__, "key", k, k_out, dt, empty, &a.k)) != KVQ_OK) return st;
+  if ((st = check_rows(__func__, "value", v, v_out, dt, empty, &a.v)) != KVQ_OK) return st;
   if (q) CHECK_PTR(w_q);
   if (k) CHECK_PTR(w_k);
   if (!rope_cos != !rope_sin) return fail(KVQ_ERR_INVALID_ARG, "%s: rope_cos and rope_sin go together", __func__);
@@ -580,10 +581,10 @@ KVQ_API kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, cons
     CHECK_PTR(rope_cos);
     CHECK_PTR(rope_sin);
     if (max_ctx <= 0) return fail(KVQ_ERR_INVALID_ARG, "%s: max_ctx <= 0", __func__);
-    if (!pos) return fail(KVQ_ERR_INVALID_ARG, "%s: rotation needs positions", __func__);
+    if (!pos && !empty) return fail(KVQ_ERR_INVALID_ARG, "%s: rotation needs positions", __func__);
   }
+  if (empty) return KVQ_OK;
   if (pos) CHECK_PTR(pos);
-  if (B == 0 || N == 0) return KVQ_OK;
   const int rows = a.q.heads + a.k.heads + a.v.heads;
   if ((double)B * N * ((rows + 3) / 4) >= 2147483648.0)
     return fail(KVQ_ERR_UNSUPPORTED, "%s: too many rows for one call", __func__);
