@@ -1900,16 +1900,9 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
 // bits): 8 rows on the tile of 8 / 16 / 32: 102 / 159 / 221 us; 16 rows on 16 / 32: 166 / 223; 32 rows on 32 / 64:
 // 228 / 274; 64 rows on 32 / 64: 448 / 288. A tile of 96 does not fit two blocks an SM with the sums of a row in registers.
 int tree_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-int sm_count_tree() {
-  static int cached[64] = {};
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms;
-  if (cached[dev] == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) cached[dev] = sms;
-  return cached[dev] ? cached[dev] : sms;
-}
 // resident blocks
 int tree_blocks(int r) {
-  return sm_count_tree() * (r == 8 ? 4 : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
+  return device_sms() * (r == 8 ? 4 : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
 }
 
 template <int ROWS>
@@ -1950,6 +1943,14 @@ cudaError_t launch_tree_rows(const KiviTreeArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+int device_sms() {
+  static int cached[64] = {};
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms;
+  if (cached[dev] == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) cached[dev] = sms;
+  return cached[dev] ? cached[dev] : sms;
+}
 
 size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits) {
   const int r = tree_rows(N * (Hq / H));

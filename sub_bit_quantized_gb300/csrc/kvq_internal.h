@@ -137,6 +137,8 @@ cudaError_t launch_vq_roll_tc(const VqEncodeArgs& a, cudaStream_t s);
 cudaError_t launch_split_codebooks(const float* cb, uint8_t* cbp, long long n, int Tc, int G, cudaStream_t s);
 size_t split_codebook_bytes(int G);
 
+int device_sms();                  // SMs of the current device
+
 struct IntDiv {                    // a divisor of the launch: n / d for 0 <= n < 2^31 by one high product and one step
   int d; uint32_t inv;             // inv = (2^32 - 1) / d
 };

@@ -221,7 +221,7 @@ cudaError_t launch_rows_of(const QkRowsArgs& a, cudaStream_t s) {
   // Three quads a warp, read and written past the table's rows in L2, once every SM has thirty; one quad below, where
   // more warps shorten the chain. 48 heads, bf16, three / one: 64 tokens 3.2 / 2.5 us, 272 3.4 / 3.1, 500 4.0 / 4.5,
   // 1000 5.9 / 6.5, 4000 17.9 / 22.4, 16381 68 / 92.
-  if ((int64_t)a.B * a.N * quads >= 30 * 152) return launch_rows<DT, 3>(a, quads, s);
+  if ((int64_t)a.B * a.N * quads >= 30 * device_sms()) return launch_rows<DT, 3>(a, quads, s);
   return launch_rows<DT, 1>(a, quads, s);
 }
 
