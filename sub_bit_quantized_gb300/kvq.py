@@ -610,6 +610,8 @@ class TreeAttnCall(_Call):
                 ws = self._ws = make_tree_workspace(cfg, B, N, q.device)
             self._own = _stream(stream)
             self._again = lambda: make_tree_workspace(cfg, B, N, q.device)
+        else:  # its bytes are what it says: contiguous, on the device
+            _operand("ws", ws, (ws.dtype,), tuple(ws.shape))
         self._bind(*args, _ptr(ws), ws.numel() * ws.element_size())
 
     def __call__(self):

@@ -84,6 +84,47 @@ def test_tree_call_kept_for_several_streams(monkeypatch):
     assert s.used == [("alloc", 5), ("run", 5), ("run", 5)]
 
 
+@pytest.mark.gpu
+def test_tree_workspace_is_what_it_says():
+    cfg, cache, q, kd, vd, mask, out = [x.cuda() if isinstance(x, torch.Tensor) else x for x in tree_args()]
+    size = kvq.kvq_kivi_tree_workspace_size(cfg, 1, 3)
+    byte = torch.empty(1, dtype=torch.uint8, device="cuda")
+    for ws in (byte.expand(size), torch.empty((size, 2), dtype=torch.uint8, device="cuda")[:, 0],
+               torch.empty(size, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="ws"):
+            kvq.TreeAttnCall(cfg, cache, q, kd, vd, mask, out, ws=ws)
+    kvq.TreeAttnCall(cfg, cache, q, kd, vd, mask, out, ws=torch.empty(size, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_tree_without_a_workspace_captured():
+    from tests import _cases as C
+    from tests import _drafts as T
+    case = T.make_tree_case(4550, B=2, H=4, N=7, n_quant=[32 * 90, 640], n_resid=[50, 128], rep=5, q_scale=0.5)
+    cache = C.fill_kivi_cache(case.base)
+    want = T.run_tree(case, cache)
+    q, kd, vd, mask, nd = T.tensors(case)
+    outs = [torch.zeros(q.shape, device="cuda") for _ in range(3)]
+    call = kvq.TreeAttnCall(case.base.cfg, cache, q, kd, vd, mask, outs[2], n_draft=nd)
+    call()  # the kernels are loaded
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for out in outs[:2]:
+            kvq.kvq_kivi_tree_attn(case.base.cfg, cache, q, kd, vd, mask, out, n_draft=nd)
+        call()
+    for _ in range(3):
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert np.array_equal(out.double().cpu().numpy(), want)
+    call()  # and eagerly again
+    torch.cuda.synchronize()
+    assert kvq.device_error() == 0 and np.array_equal(outs[2].double().cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("stream", [7, types.SimpleNamespace(cuda_stream=9), None])
 def test_decode_workspace_comes_from_the_stream_of_the_call(monkeypatch, stream):
     s = Streams(monkeypatch)
