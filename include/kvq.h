@@ -247,11 +247,11 @@ typedef struct {
  *     of group), the rest are in k_resid
  * n_quant_v int32 [max_batch]: values of tokens [0, n_quant_v) are quantized, the rest
  *     are in v_resid
- * sync      int32 [max_batch]: scratch of kvq_kivi_append (its blocks count their arrivals
- *     per request there); zero before the first call, every call leaves it zero
+ * sync      int32 [max_batch]: scratch of kvq_kivi_append and kvq_kivi_commit (their blocks count
+ *     their arrivals per request there); zero before the first call, every call leaves it zero
  * A valid state has n_quant_v <= n_quant_k <= n_tok, n_tok - n_quant_v <= residual and
- * n_quant_k <= max_tokens; kvq_kivi_prefill and kvq_kivi_append keep it valid. Attention
- * over an invalid state stays inside the buffers but its result is undefined.
+ * n_quant_k <= max_tokens; kvq_kivi_prefill, kvq_kivi_append and kvq_kivi_commit keep it valid.
+ * Attention over an invalid state stays inside the buffers but its result is undefined.
  */
 typedef struct {
   uint8_t* k_codes;
@@ -396,7 +396,7 @@ kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_ro
  * whatever its mask says. Keys and values a row does not attend cannot change it, infinities and
  * NaN among them; a row that attends nothing (no cached token, empty mask) is 0.
  * The cache is read, not changed; kvq_kivi_commit appends the accepted tokens afterwards.
- * out: [B][N][n_q_heads][D], KVQ_OUT_BF16 or KVQ_OUT_FP32.
+ * out: [B][N][n_q_heads][D], KVQ_OUT_BF16 or KVQ_OUT_FP32; it overlaps no input.
  * Arithmetic: softmax statistics and all sums in fp32; for values of a few units the fp32 output is
  * within max-abs 2e-3 and rel-L2 1e-3 of fp64. The tensor cores take fp16 operands: queries, scaled
  * by a power of two for each row; what is made of key codes, scales and zero-points exactly or in
