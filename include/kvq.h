@@ -401,9 +401,9 @@ kvq_status kvq_qk_norm_rope(int D, int B, int N, const kvq_rows* q, const kvq_ro
  * within max-abs 2e-3 and rel-L2 1e-3 of fp64. The tensor cores take fp16 operands: queries, scaled
  * by a power of two for each row; what is made of key codes, scales and zero-points exactly or in
  * two parts (a query element is off by at most 2^-27 of its row's largest, its product with a key
- * scale by 2^-21 of itself or 2^-34 of the largest such product of the row and the 32-token
- * group); a quantized value s (q - z) as s (q - c0), c0 the middle code, exact with 2 bits and
- * rounded once with 4, and its group's constants exactly, all halved (absolute 2^-25 below
+ * scale by 2^-21 of itself or 2^-33 of the row's largest element times the 32-token group's
+ * largest scale); a quantized value s (q - z) as s (q - c0), c0 the middle code, exact with 2 bits
+ * and rounded once with 4, and its group's constants exactly, all halved (absolute 2^-24 below
  * 2^-13); the softmax weights rounded once (relative 2^-11), their sum being that of the rounded
  * ones.
  * ws: device workspace of at least kvq_kivi_tree_workspace_size() bytes, needing no

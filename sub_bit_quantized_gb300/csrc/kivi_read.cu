@@ -7,9 +7,9 @@
 // Bound: HBM, mostly the writes (a 2-bit token and head reads 96 bytes and writes 512 in fp16).
 // Sixteen lanes share a token, so a warp stores two whole rows at a time; a warp takes the 32
 // tokens of a key group of one head, keys or values, eight of a lane's loads in flight at once.
-// Measured: 16 requests, 32 heads, 4K tokens at 2 bits into fp16 (1.14 GB) 175 us, 6.5 TB/s, 96 %
-// of the copy rate; 3 requests, 8 heads, 20011 tokens at 4 bits into fp32 (498 MB) 86 us, 5.8 TB/s,
-// 86 %. The first form, without the loads in flight together, took 265 and 102 us. Stores that are
+// Measured (calls back to back): 16 requests, 32 heads, 4K tokens at 2 bits into fp16 (1.14 GB) 174 to 180 us, 6.4 TB/s,
+// 95 % of the copy rate; 3 requests, 8 heads, 20011 tokens at 4 bits into fp32 (498 MB) 86 to 90 us, 5.7 TB/s,
+// 84 %. The first form, without the loads in flight together, took 265 and 102 us. Stores that are
 // the first to leave L2 change nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

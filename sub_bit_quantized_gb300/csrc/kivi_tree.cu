@@ -27,7 +27,7 @@
 // segment's end) is written for few instructions rather than few steps: rolled loops, divisions by
 // the launch's constants as one product. Unrolled, that code was fetched cold in every block and
 // took longer than the work in it (two requests, 1K context, 64 rows: 22.8 -> 20.2 us; 16 rows, 4K:
-// 142 -> 123).
+// 142 -> 123 in the form of then).
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -383,13 +383,14 @@ __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens
 //    the constants as its rows: s z as fp16, the exact rest of it, c0 s, and ones, whose sums are those of the rounded
 //    weights, so that a weight's rounding leaves a row's weights a convex combination. Values are halved on the way in:
 //    8 s passes the fp16 range for values near its end.
-// Bound: instruction issue. A group of 32 tokens costs a warp about 210 instructions for the keys (1 per code pair),
-// 50 for the softmax of 8 rows and 280 for the values (3 per code pair), and 66 products per 8 rows.
+// Bound: instruction issue (53 % of the cycles) and fixed latencies. A group of 32 tokens costs a warp 940 instructions at
+// 8 rows (counted over a launch, segment ends included): one a code pair for the keys, three for the values, 66 products.
 // Measured (16 requests, 32 KV heads, 4K context, 2 bits): 102 us for 8 rows (208 MB, 2.0 TB/s, 30 % of the copy rate),
-// 164 us for 16; the second parts q'' and the constants' products are 22 and 38 of it (max-abs error of the parity cases 7e-3
-// without, 1e-3 with them). Per-warp rings of two groups by cp.async (each lane copies what its warp reads, so no block barrier
-// in the loop); four blocks of four warps an SM for 8 rows, two for 16, as the registers of the sums allow (three, with
-// spills in the loop: 173 us). Five blocks of 96 registers for 8 rows spilled in the loop: 105 us against 88 then.
+// 164 us for 16. Without q'' and with values dequantized to one fp16 it took 80 and 126 us, outside the bound of
+// attention (max-abs 2e-3): worst error of random cases 7e-3, now 1.7e-3. Per-warp rings of two groups by cp.async
+// (each lane copies what its warp reads, so no block barrier in the loop); four blocks of four warps an SM for 8 rows, two
+// for 16, as the registers of the sums allow (three, with spills in the loop: 173 us). Five blocks of 96 registers for 8
+// rows spilled in the loop: 105 us against 88 then.
 constexpr int kMmaThreads = 128;
 constexpr int kMmaWarps = kMmaThreads / 32;
 
@@ -1067,10 +1068,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 // tile's stored keys and values are on their way (bulk copies) from the moment this tile's are unpacked, and its keys
 // are unpacked into registers while this tile's value product still reads the weights, which lie where the keys were.
 //
-// Bound: no single unit (16 requests, 8 KV heads, 192 rows, 4K context, 4 bits: 247 us), but the chain of a tile:
-// unpacking, the products, the softmax with what raises maxima, barriers. 175 us of it are the same kernel with keys and
-// values dequantized to one fp16, which leaves the bound of attention (errors up to 3.7e-2 on the parity cases, now 1.2e-3): the
-// constants' products cost 24, reading the keys' ones back 10, the keys' second parts and the constants themselves 38.
+// Bound: no single unit (16 requests, 8 KV heads, 192 rows, 4K context, 4 bits: 247 us; issue 41 % of the cycles, ALU
+// 28 %, tensor 22 %, shared-memory wavefronts 58 %, DRAM 6 %), but the chain of a tile: unpacking, the
+// products, the softmax with what raises maxima, barriers. 175 us of it are the same kernel with keys and values dequantized
+// to one fp16, outside the bound of attention (max-abs 2e-3): worst error of random cases 3.7e-2, now 1.2e-3. Of the rest
+// the constants' products cost 24, reading the keys' ones back 10, the keys' second parts and the constants themselves 38.
 // Measured with the one-fp16 form and not kept: four more warps a block (64 registers, 234 us against 191 then), copies and
 // products issued by warps of their own with the registers that costs (238; four roles with code of their own 463),
 // the softmax in pieces of 16 rows with the scores read twice (212), weights before the vote (194).
@@ -1897,8 +1899,9 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
 // Rows of a tile, which also choose the kernel: the warp-wide products for 8 or 16 rows, tcgen05 with 32 or 64. Of
 // a tile's cost most is the same for any number of rows (the codes are unpacked once), so the smallest tile that holds
 // all rows wins, and 64 above that. Measured with one kernel and the other (16 requests, 32 KV heads, 4K context, 2
-// bits): 8 rows on the tile of 8 / 16 / 32: 102 / 159 / 221 us; 16 rows on 16 / 32: 166 / 223; 32 rows on 32 / 64:
-// 228 / 274; 64 rows on 32 / 64: 448 / 288. A tile of 96 does not fit two blocks an SM with the sums of a row in registers.
+// bits): 8 rows on the tile of 8 / 16 / 32: 102 / 159 / 221 us; 16 rows on 16 / 32: 164 / 223; 32 rows on 32 / 64:
+// 228 / 274; 64 rows on 32 / 64: 448 / 288. A tile of 96 does not fit two blocks an SM: a thread's 48 scores would not
+// stay in its registers.
 int tree_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // resident blocks
 int tree_blocks(int r) {

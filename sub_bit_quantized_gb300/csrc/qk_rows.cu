@@ -10,12 +10,13 @@
 // lanes share a row, lane l holding channels 8l .. 8l+7 and their partners 64 + 8l .., so both
 // halves of every pair are in one lane, the loads and stores are 16 bytes and the mean takes
 // three shuffles; a warp works on four rows of one token at a time, three such quads at once in
-// large calls. Measured: 16381 tokens of 32 + 8 + 8 heads, bf16 in and out (411 MB): 70.5 us,
-// 5.8 TB/s, 86 % of the copy rate (a plain copy of the same bytes takes 68). Without the rotation
-// 64 us: what is left is the table's rows, which come from DRAM once and then from L2. On the way:
-// the first form 91 us, two quads with their loads in flight together 79, two with rows that are the first to leave L2 72; three are 70.5,
-// four 74; blocks of 256 threads cost 3 us more than blocks of 64, which leave their places
-// sooner. One token of 48 rows takes 5.2 us, the launch.
+// large calls. Measured (launches back to back in a graph, cos and sin in L2 from the one before): 16381 tokens of
+// 32 + 8 + 8 heads, bf16 in, bf16 and fp16 out (411 MB): 67.8 us, 6.1 TB/s, 90 % of the copy rate (a plain copy of as
+// many bytes takes 61.3); without the rotation 62.6: what is left is the table's rows, which come from L2. As calls of
+// their own with the table from DRAM 70 to 74. One token of 48 rows 2.3 us, all latency. On the way, as
+// calls of their own: the first form 91 us, two quads with their loads in flight together 79, two with rows that are
+// the first to leave L2 72, three 70.5, four 74; blocks of 256 threads cost 3 us more than blocks of 64, which leave
+// their places sooner.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -219,8 +220,8 @@ template <int DT>
 cudaError_t launch_rows_of(const QkRowsArgs& a, cudaStream_t s) {
   const int quads = (a.q.heads + a.k.heads + a.v.heads + 3) / 4;
   // Three quads a warp, read and written past the table's rows in L2, once every SM has thirty; one quad below, where
-  // more warps shorten the chain. 48 heads, bf16, three / one: 64 tokens 3.2 / 2.5 us, 272 3.4 / 3.1, 500 4.0 / 4.5,
-  // 1000 5.9 / 6.5, 4000 17.9 / 22.4, 16381 68 / 92.
+  // more warps shorten the chain. 48 heads, bf16, back to back in a graph, three / one: 1 token 2.9 / 2.3 us, 64 tokens
+  // 3.1 / 2.6, 272 3.6 / 3.2, 500 4.2 / 4.4, 1000 5.9 / 6.5, 4000 18.2 / 22.2, 16381 67.8 / 93.2.
   if ((int64_t)a.B * a.N * quads >= 30 * device_sms()) return launch_rows<DT, 3>(a, quads, s);
   return launch_rows<DT, 1>(a, quads, s);
 }
