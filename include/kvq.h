@@ -420,6 +420,106 @@ kvq_status kvq_kivi_tree_attn(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cac
 size_t kvq_kivi_tree_workspace_size(const kvq_kivi_cfg* cfg, int B, int N);
 
 /* ---------------------------------------------------------------------------------- */
+/* Attention of a batch that shares a prefix                                           */
+/* ---------------------------------------------------------------------------------- */
+
+/* Requests b < B of a cache continue one prefix that is cached once, in slot `slot` of `prefix` (a
+ * KIVI cache of the same heads; bit widths, residual and capacities of its own; it may be the same
+ * cache). Request b has N <= 64 rows a query head. Row i attends every token of the prefix, every
+ * cached token of its request and, with a mask, the request's drafted tokens j whose bit j is set in
+ * mask[b][i]: one softmax over all of them, scale 1/sqrt(D). The prefix is read once for all
+ * requests. Keys are rotated: those of a request at the positions that follow the prefix.
+ * q, k_draft, v_draft, mask, n_draft, out, out_dtype: as in kvq_kivi_tree_attn. k_draft, v_draft and
+ * mask may all be NULL: rows attend no drafted tokens (decoding after kvq_kivi_append). A row that
+ * attends nothing is 0; rows i >= n_draft[b] are padding and stay as they are. An empty prefix or
+ * cache counts no tokens. Neither cache is changed. Arithmetic and bounds: those of
+ * kvq_kivi_tree_attn, the two parts joined in fp32.
+ * ws: device workspace of at least kvq_kivi_prefix_workspace_size() bytes, needing no
+ * initialisation. Two calls that run at the same time need two workspaces.
+ * Errors: KVQ_ERR_INVALID_ARG (heads that differ, slot < 0, drafts without a mask), KVQ_ERR_CAPACITY
+ * (B > max_batch, slot >= max_batch of the prefix), KVQ_ERR_WORKSPACE, KVQ_ERR_UNSUPPORTED (N > 64,
+ * more than 2^31 rows or blocks). */
+kvq_status kvq_kivi_prefix_attn(const kvq_kivi_cfg* cfg, const kvq_kivi_cache* cache,
+                                const kvq_kivi_cfg* prefix_cfg, const kvq_kivi_cache* prefix, int slot,
+                                const uint16_t* q, const uint16_t* k_draft, const uint16_t* v_draft,
+                                const uint64_t* mask, const int32_t* n_draft, int B, int N, void* out,
+                                int out_dtype, void* ws, size_t ws_bytes, kvq_stream stream);
+
+/* Workspace bytes kvq_kivi_prefix_attn needs for these arguments on the current device (0 for ones that it refuses). */
+size_t kvq_kivi_prefix_workspace_size(const kvq_kivi_cfg* cfg, const kvq_kivi_cfg* prefix_cfg, int B, int N);
+
+/* ---------------------------------------------------------------------------------- */
+/* Slots of a cache (both formats)                                                     */
+/* ---------------------------------------------------------------------------------- */
+
+/* What source[i] says of a slot besides the number of the slot that it continues. */
+enum { KVQ_SLOT_KEEP = -1, KVQ_SLOT_FREE = -2 };
+
+/* Forking, reordering, compacting and freeing slots (requests): for i < n slot b0 + i of `cache`
+ * becomes what slot source[i] of `from` was before the call, every slot at once, so that any map is
+ * allowed (several slots may continue one, slots may change places). KVQ_SLOT_KEEP leaves a slot as
+ * it is, KVQ_SLOT_FREE empties it (its lengths become 0). What a slot holds moves (pages, groups,
+ * fp16 or bf16 tokens, lengths); bytes behind that stay as they are.
+ * format, cfg, cache: as in kvq_decode_attn. from_cfg and from may be NULL, or the cache itself:
+ * slots of one cache. Another cache overlaps none of `cache`'s buffers and has the same shape but
+ * for max_batch and its capacity (KIVI: max_tokens; n_q_heads does not matter; LoopVQ: max_pages and
+ * max_ctx; the codebooks are not moved and are to be the same).
+ * source: device int32 [n]. A slot whose source lies outside [0, max_batch of from) and is neither of
+ * the two values, or whose source has lengths that no call leaves, stays as it is, and
+ * kvq_device_error() then reports KVQ_ERR_INVALID_ARG; one that does not fit reports
+ * KVQ_ERR_CAPACITY. Calls that change either cache must not run at the same time. n = 0 is a no-op
+ * (source may be NULL then).
+ * Errors: KVQ_ERR_INVALID_ARG (pointers, negative sizes, shapes that differ), KVQ_ERR_CAPACITY (b0 +
+ * n > max_batch), KVQ_ERR_UNSUPPORTED (n > KVQ_FORK_MAX, or more than 2^31 blocks). */
+#define KVQ_FORK_MAX 256
+kvq_status kvq_cache_fork(int format, const void* cfg, const void* cache, const void* from_cfg,
+                          const void* from, const int32_t* source, int b0, int n, kvq_stream stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* Verification of drafted tokens                                                      */
+/* ---------------------------------------------------------------------------------- */
+
+/* Rows of a distribution over the vocabulary: entry (b, i, v) at p[b*stride_b + i*stride_t + v]. */
+typedef struct {
+  const void* p;
+  int64_t stride_b, stride_t;
+  int dtype; /* KVQ_DT_* */
+} kvq_dist;
+
+/* Verification of drafted tokens (speculative sampling, and its recursive form over a tree): from
+ * node 0, request b's newest token, the walk goes on to the first child of its node that is
+ * accepted, children in the order of their numbers, until none is; the accepted path goes to
+ * kvq_kivi_commit. Node i < n_draft[b] (NULL: N for every one; values outside [0, N] count as the
+ * nearest) is token[b][i], a child of node parent[b][i] < i (parent[b][0] is not read).
+ * target: P_i, the target's distribution behind node i. draft: Q_i, the one that node i's children
+ * were drawn from, independently; NULL: every child is a point mass of its own.
+ * u: random numbers in [0, 1), u[b][i] for the test of node i, u[b][0] for the next token. At a node
+ * with distribution P, a child of token x is accepted if
+ *   u Z Q(x) < w(x),  w = max(0, P - a Q),  a = 0 and Z = 1 at first; a rejection adds Z to a, then
+ *   Z = sum of w,
+ * which is the test u < R(x) / Q(x) against the residual R = w / Z, and leaves the residual
+ * max(0, R - Q), normalised. Point masses: u Z < w(x), w = P without the tokens rejected at the
+ * node; a rejection takes w(x) off Z. The next token is drawn from w at the path's end: the lowest v
+ * with w(0) + .. + w(v) > u[b][0] sum of w (w = P if the residual has no mass). Sums are exact to
+ * 2^-44 of themselves and more, so they do not depend on how the work is split.
+ * u NULL: no sampling. A child is accepted if its token is the lowest index of the largest entry of
+ * the target's row (probabilities or logits; NaN counts as the lowest value), and the next token is that
+ * entry's index at the path's end; draft is NULL then.
+ * Entries are finite and, with u, not negative; of others the walk and tokens are undefined, but in
+ * range. Outputs: n_accept[b], the length of the path (0 with n_draft[b] = 0), path[b][0 ..
+ * n_accept[b] - 1], its nodes from 0 on (the rest stays as it is), next[b], the next token (left as
+ * it is with n_draft[b] = 0). A request with a parent outside [0, i) or a token outside [0, V) gets
+ * n_accept = 0, its path and next stay, and kvq_device_error() reports KVQ_ERR_INVALID_ARG.
+ * token, parent, path: int32 [B][N]; u: fp32 [B][N]; n_draft, n_accept, next: int32 [B]; all on the
+ * device. target and draft: 16-byte aligned, any strides >= 0, of one type.
+ * B = 0 or N = 0 is a no-op (the arrays may be NULL then).
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (N > 64, B > 65535). */
+kvq_status kvq_verify_draft(int B, int N, int V, const kvq_dist* target, const kvq_dist* draft,
+                            const int32_t* token, const int32_t* parent, const int32_t* n_draft,
+                            const float* u, int32_t* path, int32_t* n_accept, int32_t* next,
+                            kvq_stream stream);
+
+/* ---------------------------------------------------------------------------------- */
 /* Decode attention (both formats)                                                     */
 /* ---------------------------------------------------------------------------------- */
 

@@ -70,8 +70,8 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 // and block k of G takes positions [k P / G, (k + 1) P / G); of fewer than G positions the first blocks take one each,
 // so that the blocks of a segment are neighbours (two requests, 1K context, 64 rows: 20.2 -> 16.6 us).
 struct TreeLens {
-  int nqk, nqv, n, nd;  // quantized keys, quantized values, cached tokens, drafted tokens
-  int tiles;
+  int nqk, nqv, n, nd;  // quantized keys, quantized values, cached tokens, drafted tokens that rows may attend
+  int tiles, nr;        // tiles; tokens whose rows attend (nd, or without drafts the queries')
 };
 __device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
   TreeLens L;
@@ -79,8 +79,9 @@ __device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
   L.n = L.nqk + max(0, min(a.n_tok[b] - L.nqk, a.residual));
   // at least n - residual, as in every valid state: the ring holds no more values
   L.nqv = (a.residual > 0) ? min(max(a.n_quant_v[b], max(L.n - a.residual, 0)), L.nqk) : L.nqk;
-  L.nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
-  L.tiles = L.nd > 0 ? (int)((uint32_t)(L.n + L.nd + kTile - 1) / kTile) : 0;
+  L.nr = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
+  L.nd = a.mask ? L.nr : 0;
+  L.tiles = L.nr > 0 ? max((int)((uint32_t)(L.n + L.nd + kTile - 1) / kTile), 1) : 0;
   return L;
 }
 // where the share of block k of G begins, without leaving 32 bits (k <= G, G far below 2^15)
@@ -110,9 +111,9 @@ struct Walk {
 template <int ROWS>
 __host__ __device__ constexpr size_t slot_floats() { return (size_t)ROWS * (kD + 2); }
 // What block k did with the segments it shares, for the merge. first: its first segment (kSeg...). open: the segment
-// that begins in the block and goes on (b * segments per request + seg), or -1; nd: that request's drafted tokens.
+// that begins in the block and goes on (b * segments per request + seg), or -1; nr: that request's tokens with rows.
 struct TreeShared {
-  int first, open, nd, pad;
+  int first, open, nr, pad;
 };
 
 // The place in all positions where the block's share begins, and the share [p0, p1): each warp on its own, its lanes
@@ -341,7 +342,7 @@ __device__ __forceinline__ float query_fp16(const uint32_t (&w)[8], uint32_t (&o
 __device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int row, int c,
                                            uint32_t (&w)[8]) {
   const int di = div_by(row, a.rep);
-  const bool real = row < a.N * a.rep.d && di < len.nd;
+  const bool real = row < a.N * a.rep.d && di < len.nr;
   uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
   if (real) {
     const uint4* src = reinterpret_cast<const uint4*>(
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
       dst[NT * 32] = x1;
       if (c == 0) {
         rowc[r] = back;
-        mask[r] = real ? a.mask[(size_t)w.b * a.N + div_by(r, a.rep)] : 0ull;
+        mask[r] = real && w.len.nd > 0 ? a.mask[(size_t)w.b * a.N + div_by(r, a.rep)] : 0ull;
       }
     }
     __syncthreads();  // queries staged
@@ -1003,14 +1004,14 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     if (earlier) sh.first = last ? kSegEnds : kSegGoesOn;
     else if (!last) {
       sh.open = w.b * seg_per_b + w.seg;
-      sh.nd = w.len.nd;
+      sh.nr = w.len.nr;
     }
     float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<kRows>();
     const bool fix = *nonfinite != 0;
 #pragma unroll 1
     for (int x = 0; x < 2 * NT; ++x) {  // row 8 nt + 2 q + e, channels 16 n + 4 warp .. + 3: o[nt][2 warp + c / 2][e + 2 (c % 2)]
       const int nt = x >> 1, e = x & 1, r = 8 * nt + 2 * q4 + e, di = div_by(r, a.rep), ch = 16 * n8 + 4 * warp;
-      if (r >= rows_all || di >= w.len.nd) continue;  // padding
+      if (r >= rows_all || di >= w.len.nr) continue;  // padding
       const float* s0 = osum + element(nt, 2 * warp, e) + lane;
       float v[4];
 #pragma unroll
@@ -1034,6 +1035,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
         for (int c = 0; c < 4; ++c) v[c] = inv == 0.f ? 0.f : v[c] * inv;
         const size_t at = (((size_t)w.b * a.N + di) * a.Hq + (size_t)h * rep + r - di * rep) * kD + ch;
         to = reinterpret_cast<float*>(a.out) + at;
+        if (a.lse && n8 == 0 && warp == 0) a.lse[at / kD] = t.x + __log2f(t.y);
         if (!a.out_fp32)
           *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
               make_uint2(f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16));
@@ -1533,7 +1535,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
         const int r = i >> 3, c = i & 7;
         uint32_t u[8], o[8];
         const bool real = load_query(a, len, b, h, row0 + r, c, u);
-        const uint64_t sees = real ? a.mask[(size_t)b * a.N + div_by(row0 + r, a.rep)] : 0ull;
+        const uint64_t sees = real && len.nd > 0 ? a.mask[(size_t)b * a.N + div_by(row0 + r, a.rep)] : 0ull;
         const float back = query_fp16<14>(u, o, scale_log2);
         uint4 x0, x1;
         pair_order<KB>(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), x0, x1);
@@ -1710,7 +1712,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       if (earlier) sh.first = last ? kSegEnds : kSegGoesOn;
       else if (!last) {
         sh.open = b * seg_per_b + w.seg;
-        sh.nd = len.nd;
+        sh.nr = len.nr;
       }
       float* slot = slots + ((size_t)blockIdx.x * 2 + (earlier ? 0 : 1)) * slot_floats<ROWS>();
       wait(bar_o, phase);
@@ -1740,12 +1742,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
       if (tid < ROWS) {
         const int r = tid, row = row0 + r, di = div_by(row, a.rep);
         const float lt = red[r];
-        const bool real = row < rows_all && di < len.nd;
+        const bool real = row < rows_all && di < len.nr;
         if (real && !whole) {
           slot[(size_t)ROWS * kD + r] = -rowm[r];
           slot[(size_t)ROWS * kD + ROWS + r] = lt;
         }
         at_row[r] = !real ? -1 : whole ? di * a.Hq + h * rep + row - di * rep : r;
+        if (a.lse && real && whole) a.lse[(size_t)b * a.N * a.Hq + at_row[r]] = __log2f(lt) - rowm[r];
         rowf[r] = !whole ? 2.f : (lt > 0.f || lt != lt) ? 2.f / lt : 0.f;  // values were halved
       }
       __syncthreads();
@@ -1824,7 +1827,7 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
   const int rep = a.rep.d, rows_all = a.N * rep;
   const int b = div_by(seg_all, a.segs), seg = seg_all - b * a.segs.d, h = div_by(seg, a.row_tiles);
   const int row = (seg - h * a.row_tiles.d) * ROWS + r, di = div_by(row, a.rep);
-  if (row >= rows_all || di >= shared[k].nd) return;
+  if (row >= rows_all || di >= shared[k].nr) return;
   const size_t mo = (size_t)ROWS * kD + r, lo = mo + ROWS;
   const float* own = slots + ((size_t)k * 2 + 1) * slot_floats<ROWS>();
   float M = own[mo], lt = own[lo];
@@ -1883,6 +1886,7 @@ __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_m
   }
   const bool none = !(lt > 0.f || lt != lt);
   const size_t at = (((size_t)b * a.N + di) * a.Hq + (size_t)h * rep + row - di * rep) * kD + 4 * lane;
+  if (a.lse && lane == 0) a.lse[at / kD] = M + __log2f(lt);
   float val[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) val[e] = none ? 0.f : val[e] / lt;

@@ -633,6 +633,237 @@ KVQ_API kvq_status kvq_kivi_tree_attn(const kvq_kivi_cfg* c, const kvq_kivi_cach
   return cuda_status(kvq::launch_kivi_tree(a, (cudaStream_t)stream), __func__);
 }
 
+static kvq::ForkArray fork_array(const void* src, void* dst, int kind, int outer, int heads, long long row,
+                                 long long src_rows, long long src_slots, long long dst_rows, long long dst_slots) {
+  kvq::ForkArray x{};
+  x.src = static_cast<const unsigned char*>(src); x.dst = static_cast<unsigned char*>(dst);
+  x.outer = outer; x.row = (int)row; x.kind = kind;
+  x.src_head = src_rows * row; x.src_slot = x.src_head * heads; x.src_outer = x.src_slot * src_slots;
+  x.dst_head = dst_rows * row; x.dst_slot = x.dst_head * heads; x.dst_outer = x.dst_slot * dst_slots;
+  return x;
+}
+
+KVQ_API kvq_status kvq_cache_fork(int format, const void* cfg, const void* cache, const void* from_cfg,
+                                  const void* from, const int32_t* source, int b0, int n, kvq_stream stream) {
+  if (format != KVQ_FMT_LOOPVQ && format != KVQ_FMT_KIVI)
+    return fail(KVQ_ERR_INVALID_ARG, "%s: format must be KVQ_FMT_LOOPVQ or KVQ_FMT_KIVI", __func__);
+  if (!from_cfg != !from) return fail(KVQ_ERR_INVALID_ARG, "%s: from_cfg and from go together", __func__);
+  if (!from) {
+    from_cfg = cfg;
+    from = cache;
+  }
+  kvq::CacheForkArgs a{};
+  kvq_status st;
+  int max_batch;
+  if (format == KVQ_FMT_KIVI) {
+    const kvq_kivi_cfg *c = static_cast<const kvq_kivi_cfg*>(cfg), *fc = static_cast<const kvq_kivi_cfg*>(from_cfg);
+    const kvq_kivi_cache *k = static_cast<const kvq_kivi_cache*>(cache), *f = static_cast<const kvq_kivi_cache*>(from);
+    if ((st = check_kivi_cfg(c, __func__)) != KVQ_OK || (st = check_kivi_cfg(fc, __func__)) != KVQ_OK) return st;
+    if ((st = check_kivi_cache(k, __func__)) != KVQ_OK || (st = check_kivi_cache(f, __func__)) != KVQ_OK) return st;
+    if (fc->n_heads != c->n_heads || fc->k_bits != c->k_bits || fc->v_bits != c->v_bits || fc->residual != c->residual)
+      return fail(KVQ_ERR_INVALID_ARG, "%s: the caches differ in heads, bits or residual", __func__);
+    a.same = k->n_tok == f->n_tok;
+    if (a.same && (fc->max_batch != c->max_batch || fc->max_tokens != c->max_tokens))
+      return fail(KVQ_ERR_INVALID_ARG, "%s: one cache with two shapes", __func__);
+    const int H = c->n_heads, D = c->D, R = c->residual;
+    const long long T = c->max_tokens, F = fc->max_tokens, B = c->max_batch, E = fc->max_batch;
+    auto add = [&](const void* src, void* dst, int kind, long long row, long long to, long long fro) {
+      a.array[a.n_arrays++] = fork_array(src, dst, kind, 1, H, row, fro, E, to, B);
+    };
+    add(f->k_codes, k->k_codes, kvq::kForkA, D * c->k_bits / 8, T, F);
+    add(f->v_codes, k->v_codes, kvq::kForkB, D * c->v_bits / 8, T, F);
+    add(f->k_scale, k->k_scale, kvq::kForkGroups, D * 2, T / c->group, F / c->group);
+    add(f->k_zero, k->k_zero, kvq::kForkGroups, D * 2, T / c->group, F / c->group);
+    add(f->v_scale, k->v_scale, kvq::kForkB, D / c->group * 2, T, F);
+    add(f->v_zero, k->v_zero, kvq::kForkB, D / c->group * 2, T, F);
+    if (R > 0) {
+      add(f->k_resid, k->k_resid, kvq::kForkTail, D * 2, R, R);
+      add(f->v_resid, k->v_resid, kvq::kForkRing, D * 2, R, R);
+    }
+    int32_t* to[3] = {k->n_tok, k->n_quant_k, k->n_quant_v};
+    const int32_t* fr[3] = {f->n_tok, f->n_quant_k, f->n_quant_v};
+    for (int i = 0; i < 3; ++i) a.len[i] = to[i], a.from_len[i] = fr[i];
+    a.heads = H; a.room = c->max_tokens; a.from_room = fc->max_tokens; a.residual = R; a.ring = R;
+    a.from_batch = fc->max_batch;
+    max_batch = c->max_batch;
+  } else {
+    const kvq_vq_cfg *c = static_cast<const kvq_vq_cfg*>(cfg), *fc = static_cast<const kvq_vq_cfg*>(from_cfg);
+    const kvq_vq_cache *k = static_cast<const kvq_vq_cache*>(cache), *f = static_cast<const kvq_vq_cache*>(from);
+    if ((st = check_vq_cfg(c, __func__)) != KVQ_OK || (st = check_vq_cfg(fc, __func__)) != KVQ_OK) return st;
+    for (const kvq_vq_cache* x : {k, f}) {
+      if (!x) return fail(KVQ_ERR_INVALID_ARG, "%s: cache is null", __func__);
+      const void* ptrs[] = {x->idx_k, x->idx_v, x->win_k, x->win_v, x->seq_len, x->n_pages};
+      for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(KVQ_ERR_INVALID_ARG, "%s: a cache pointer is null or misaligned", __func__);
+    }
+    if (fc->T != c->T || fc->Tc != c->Tc || fc->G != c->G || fc->n_layers != c->n_layers || fc->n_heads != c->n_heads ||
+        fc->sink != c->sink || fc->recent != c->recent)
+      return fail(KVQ_ERR_INVALID_ARG, "%s: the caches differ in loop steps, coupling, layers, heads or windows", __func__);
+    a.same = k->seq_len == f->seq_len;
+    if (a.same && (fc->max_batch != c->max_batch || fc->max_pages != c->max_pages))
+      return fail(KVQ_ERR_INVALID_ARG, "%s: one cache with two shapes", __func__);
+    const int H = c->n_heads, NB = c->T / c->Tc, NG = c->D / (c->G / c->Tc), slots = win_slots(c);
+    const long long B = c->max_batch, E = fc->max_batch;
+    if ((double)c->n_layers * c->T * H >= 2147483648.0)
+      return fail(KVQ_ERR_UNSUPPORTED, "%s: too many layers, loop steps and heads for one call", __func__);
+    auto add = [&](const void* src, void* dst, int kind, int outer, long long row, long long to, long long fro) {
+      a.array[a.n_arrays++] = fork_array(src, dst, kind, outer, H, row, fro, E, to, B);
+    };
+    add(f->idx_k, k->idx_k, kvq::kForkA, c->n_layers * NB, kvq::kPage * NG, c->max_pages, fc->max_pages);
+    add(f->idx_v, k->idx_v, kvq::kForkA, c->n_layers * NB, kvq::kPage * NG, c->max_pages, fc->max_pages);
+    add(f->win_k, k->win_k, kvq::kForkWindow, c->n_layers * c->T, c->D * 2, slots, slots);
+    add(f->win_v, k->win_v, kvq::kForkWindow, c->n_layers * c->T, c->D * 2, slots, slots);
+    a.len[0] = k->seq_len; a.len[1] = k->n_pages;
+    a.from_len[0] = f->seq_len; a.from_len[1] = f->n_pages;
+    a.heads = H; a.room = c->max_pages; a.from_room = fc->max_pages; a.ring = c->recent + kvq::kPage; a.sink = c->sink;
+    a.max_ctx = c->max_ctx;
+    a.from_batch = fc->max_batch;
+    max_batch = c->max_batch;
+  }
+  if (b0 < 0 || n < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: b0 or n < 0", __func__);
+  if ((long long)b0 + n > max_batch) return fail(KVQ_ERR_CAPACITY, "%s: b0 + n > max_batch", __func__);
+  if (n > KVQ_FORK_MAX) return fail(KVQ_ERR_UNSUPPORTED, "%s: n=%d (at most %d slots a call)", __func__, n, KVQ_FORK_MAX);
+  if (n == 0) return KVQ_OK;  // an empty array may have no address
+  CHECK_PTR(source);
+  long long pieces = 0;  // of 2 KB, of the longest slots there can be
+  for (int i = 0; i < a.n_arrays; ++i)
+    pieces += (std::min(a.array[i].src_head, a.array[i].dst_head) + 2047) / 2048 * a.array[i].outer * a.heads;
+  a.format = format; a.source = source; a.b0 = b0; a.n = n; a.err = device_error_ptr();
+  return cuda_status(kvq::launch_cache_fork(a, pieces, (cudaStream_t)stream), __func__);
+}
+
+KVQ_API kvq_status kvq_verify_draft(int B, int N, int V, const kvq_dist* target, const kvq_dist* draft,
+                                    const int32_t* token, const int32_t* parent, const int32_t* n_draft,
+                                    const float* u, int32_t* path, int32_t* n_accept, int32_t* next,
+                                    kvq_stream stream) {
+  if (B < 0 || N < 0 || V < 1) return fail(KVQ_ERR_INVALID_ARG, "%s: B or N < 0, or V < 1", __func__);
+  if (N > 64) return fail(KVQ_ERR_UNSUPPORTED, "%s: N=%d (a tree has at most 64 drafted tokens)", __func__, N);
+  if (B > 65535) return fail(KVQ_ERR_UNSUPPORTED, "%s: B=%d (at most 65535 requests a call)", __func__, B);
+  if (V > (1 << 30)) return fail(KVQ_ERR_UNSUPPORTED, "%s: V=%d (at most 2^30 entries)", __func__, V);
+  if (!target) return fail(KVQ_ERR_INVALID_ARG, "%s: target is null", __func__);
+  if (!u && draft) return fail(KVQ_ERR_INVALID_ARG, "%s: without random numbers there is no draft distribution", __func__);
+  for (const kvq_dist* x : {target, draft})
+    if (x && (x->stride_b < 0 || x->stride_t < 0 || x->dtype != target->dtype || !known_dtype(x->dtype)))
+      return fail(KVQ_ERR_INVALID_ARG, "%s: strides are not negative, types are one KVQ_DT_ type", __func__);
+  if (B == 0 || N == 0) return KVQ_OK;  // empty arrays may have no address
+  CHECK_PTR(target->p);
+  if (draft) CHECK_PTR(draft->p);
+  CHECK_PTR(token);
+  CHECK_PTR(parent);
+  if (n_draft) CHECK_PTR(n_draft);
+  if (u) CHECK_PTR(u);
+  CHECK_PTR(path);
+  CHECK_PTR(n_accept);
+  CHECK_PTR(next);
+  kvq::VerifyArgs a{};
+  a.p = target->p; a.p_sb = target->stride_b; a.p_st = target->stride_t;
+  if (draft) {
+    a.q = draft->p; a.q_sb = draft->stride_b; a.q_st = draft->stride_t;
+  }
+  a.token = token; a.parent = parent; a.n_draft = n_draft; a.u = u;
+  a.path = path; a.n_accept = n_accept; a.next = next; a.err = device_error_ptr();
+  a.B = B; a.N = N; a.V = V;
+  return cuda_status(kvq::launch_verify(a, target->dtype, (cudaStream_t)stream), __func__);
+}
+
+// Parts of the workspace of kvq_kivi_prefix_attn: what the two passes need, their outputs and sums
+struct PrefixPlan {
+  size_t prefix, own, out, lse, total;  // bytes; of out and lse each of the two
+};
+static PrefixPlan plan_prefix(const kvq_kivi_cfg* c, const kvq_kivi_cfg* pc, int B, int N) {
+  PrefixPlan p;
+  const size_t rows = (size_t)B * N * c->n_q_heads;
+  p.prefix = align256(kvq::kivi_tree_ws_bytes(1, B * N, c->n_heads, c->n_q_heads, pc->k_bits, pc->v_bits));
+  p.own = align256(kvq::kivi_tree_ws_bytes(B, N, c->n_heads, c->n_q_heads, c->k_bits, c->v_bits));
+  p.out = align256(rows * kvq::kD * sizeof(float));
+  p.lse = align256(rows * sizeof(float));
+  p.total = p.prefix + p.own + 2 * (p.out + p.lse);
+  return p;
+}
+// the two caches of one call
+static kvq_status check_prefix_cfgs(const kvq_kivi_cfg* c, const kvq_kivi_cfg* pc, int B, int N, const char* fn) {
+  kvq_status st = check_kivi_cfg(c, fn);
+  if (st != KVQ_OK) return st;
+  if ((st = check_kivi_cfg(pc, fn)) != KVQ_OK) return st;
+  if (pc->n_heads != c->n_heads || pc->n_q_heads != c->n_q_heads)
+    return fail(KVQ_ERR_INVALID_ARG, "%s: the prefix has %d KV and %d query heads, the cache %d and %d", fn, pc->n_heads,
+                pc->n_q_heads, c->n_heads, c->n_q_heads);
+  if (B < 1 || N < 1) return fail(KVQ_ERR_INVALID_ARG, "%s: B or N < 1", fn);
+  if (B > c->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: B > max_batch", fn);
+  if (N > 64) return fail(KVQ_ERR_UNSUPPORTED, "%s: N=%d (a request has at most 64 rows a head)", fn, N);
+  if ((long long)B * N * c->n_q_heads >= (1ll << 31) ||
+      kvq::kivi_tree_positions(B, N, c->n_heads, c->n_q_heads, c->max_tokens, c->residual) >= (1ll << 31) ||
+      kvq::kivi_tree_positions(1, B * N, c->n_heads, c->n_q_heads, pc->max_tokens, pc->residual) >= (1ll << 31))
+    return fail(KVQ_ERR_UNSUPPORTED, "%s: too many tokens and query rows for one call", fn);
+  return KVQ_OK;
+}
+static void set_tree_cache(kvq::KiviTreeArgs& a, const kvq_kivi_cfg* c, const kvq_kivi_cache* k, int slot) {
+  const size_t bh = (size_t)slot * c->n_heads, rows = bh * c->max_tokens, D = c->D;
+  a.k_codes = k->k_codes + rows * (D * c->k_bits / 8);
+  a.k_scale = k->k_scale + rows / c->group * D;
+  a.k_zero = k->k_zero + rows / c->group * D;
+  a.v_codes = k->v_codes + rows * (D * c->v_bits / 8);
+  a.v_scale = k->v_scale + rows * (D / c->group);
+  a.v_zero = k->v_zero + rows * (D / c->group);
+  a.k_resid = k->k_resid + bh * c->residual * D;
+  a.v_resid = k->v_resid + bh * c->residual * D;
+  a.n_tok = k->n_tok + slot; a.n_quant_k = k->n_quant_k + slot; a.n_quant_v = k->n_quant_v + slot;
+  a.H = c->n_heads; a.Hq = c->n_q_heads; a.k_bits = c->k_bits; a.v_bits = c->v_bits;
+  a.max_tokens = c->max_tokens; a.residual = c->residual;
+}
+
+KVQ_API size_t kvq_kivi_prefix_workspace_size(const kvq_kivi_cfg* c, const kvq_kivi_cfg* pc, int B, int N) {
+  if (check_prefix_cfgs(c, pc, B, N, __func__) != KVQ_OK) return 0;
+  return plan_prefix(c, pc, B, N).total;
+}
+
+KVQ_API kvq_status kvq_kivi_prefix_attn(const kvq_kivi_cfg* c, const kvq_kivi_cache* k, const kvq_kivi_cfg* pc,
+                                        const kvq_kivi_cache* pk, int slot, const uint16_t* q, const uint16_t* k_draft,
+                                        const uint16_t* v_draft, const uint64_t* mask, const int32_t* n_draft, int B,
+                                        int N, void* out, int out_dtype, void* ws, size_t ws_bytes, kvq_stream stream) {
+  kvq_status st = check_prefix_cfgs(c, pc, B, N, __func__);
+  if (st != KVQ_OK) return st;
+  if ((st = check_kivi_cache(k, __func__)) != KVQ_OK) return st;
+  if ((st = check_kivi_cache(pk, __func__)) != KVQ_OK) return st;
+  if (slot < 0) return fail(KVQ_ERR_INVALID_ARG, "%s: slot < 0", __func__);
+  if (slot >= pc->max_batch) return fail(KVQ_ERR_CAPACITY, "%s: slot >= max_batch of the prefix", __func__);
+  CHECK_PTR(q);
+  if (mask) {
+    CHECK_PTR(k_draft);
+    CHECK_PTR(v_draft);
+    CHECK_PTR(mask);
+  } else if (k_draft || v_draft) {
+    return fail(KVQ_ERR_INVALID_ARG, "%s: drafted keys and values go with a mask", __func__);
+  }
+  if (n_draft) CHECK_PTR(n_draft);
+  CHECK_PTR(out);
+  if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_FP32)
+    return fail(KVQ_ERR_INVALID_ARG, "%s: out_dtype must be KVQ_OUT_BF16 or KVQ_OUT_FP32", __func__);
+  const PrefixPlan plan = plan_prefix(c, pc, B, N);
+  if (!ws || ws_bytes < plan.total || !aligned16(ws))
+    return fail(KVQ_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu)", __func__, plan.total, ws_bytes);
+  kvq::KiviPrefixArgs a{};
+  set_tree_cache(a.own, c, k, 0);
+  set_tree_cache(a.prefix, pc, pk, slot);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  for (kvq::KiviTreeArgs* t : {&a.prefix, &a.own}) {
+    t->part = reinterpret_cast<float*>(w);
+    w += t == &a.own ? plan.own : plan.prefix;
+    t->out = w;
+    w += plan.out;
+    t->lse = reinterpret_cast<float*>(w);
+    w += plan.lse;
+    t->out_fp32 = 1;
+    t->q = q;
+    t->err = device_error_ptr();
+  }
+  a.own.k_draft = k_draft; a.own.v_draft = v_draft; a.own.mask = mask; a.own.n_draft = n_draft;
+  a.own.B = B; a.own.N = N;
+  a.prefix.B = 1; a.prefix.N = B * N;  // rows of padding among them: nobody reads theirs
+  a.out = out; a.out_fp32 = (out_dtype == KVQ_OUT_FP32);
+  return cuda_status(kvq::launch_kivi_prefix(a, (cudaStream_t)stream), __func__);
+}
+
 KVQ_API size_t kvq_decode_workspace_size(int format, const void* cfg, int B, int n_splits) {
   if (B <= 0 || !cfg) return 0;
   if (format == KVQ_FMT_LOOPVQ) {

@@ -232,9 +232,10 @@ struct KiviTreeArgs {
   const int32_t* n_tok; const int32_t* n_quant_k; const int32_t* n_quant_v;
   const uint16_t* q;               // bf16 [B][N][Hq][D]
   const uint16_t* k_draft; const uint16_t* v_draft;  // fp16 [B][N][H][D]
-  const uint64_t* mask;            // [B][N]
+  const uint64_t* mask;            // [B][N]; null: the rows attend no drafted token
   const int32_t* n_draft;          // [B], null: N
   void* out; int out_fp32;         // [B][N][Hq][D]
+  float* lse;                      // [B][N][Hq], or null: log2 of a row's sum of 2^score (scores in log2 units)
   float* part;                     // workspace: what blocks share, partial softmaxes of those segments
   int* err;
   int B, N, H, Hq, k_bits, v_bits, max_tokens, residual;
@@ -246,6 +247,50 @@ size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits);
 // tile positions of a launch whose requests are full (below 2^31: checked by the host)
 long long kivi_tree_positions(int B, int N, int H, int Hq, int max_tokens, int residual);
 cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- attention under a shared prefix
+struct KiviPrefixArgs {
+  KiviTreeArgs prefix;             // one request of all the call's rows, over the prefix's slot
+  KiviTreeArgs own;                // the requests over their own caches and drafts; both write fp32 and lse
+  void* out; int out_fp32;         // [B][N][Hq][D]
+  IntDiv heads, tokens;            // set by the launch: query heads, tokens a request
+};
+cudaError_t launch_kivi_prefix(const KiviPrefixArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- slots of a cache
+// What of an array a slot holds, by its lengths (n, a, b): KIVI tokens, quantized keys, quantized values; LoopVQ
+// tokens, index pages, none.
+enum { kForkA, kForkGroups, kForkB, kForkTail, kForkRing, kForkWindow };  // rows a, a / 32, b, n - a, the ring's, the window's
+constexpr int kForkArrays = 8;
+struct ForkArray {                 // [outer][slot][head][rows of `row` bytes], strides in bytes
+  const unsigned char* src; unsigned char* dst;
+  long long src_outer, src_slot, src_head, dst_outer, dst_slot, dst_head;
+  int outer, row, kind;
+};
+struct CacheForkArgs {
+  ForkArray array[kForkArrays];
+  int32_t* len[3]; const int32_t* from_len[3];  // n, a, b of every slot (b may be null)
+  const int32_t* source;           // [n]
+  int* err;
+  int format, n_arrays, b0, n, heads, from_batch;
+  int same;                        // both caches are one
+  int room, from_room;             // most quantized tokens, or pages
+  int residual, ring, sink, max_ctx;  // ring: rows of the value ring, or of the window's behind the sink
+};
+cudaError_t launch_cache_fork(const CacheForkArgs& a, long long most_pieces, cudaStream_t s);
+
+// ---------------------------------------------------------------- verification of drafted tokens
+struct VerifyArgs {
+  const void* p; const void* q;    // entry (b, i, v) at b*sb + i*st + v; q may be null
+  int64_t p_sb, p_st, q_sb, q_st;
+  const int32_t* token; const int32_t* parent; const int32_t* n_draft;  // [B][N], [B][N], [B] or null
+  const float* u;                  // [B][N] or null
+  int32_t* path; int32_t* n_accept; int32_t* next;
+  int* err;
+  int B, N, V;
+  int slice, chunk;                // set by the launch: entries a block takes, entries a sum is kept of
+};
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
 
 // ---------------------------------------------------------------- norm and rotation of rows
 struct QkRows {                    // rows of one kind: heads == 0 when absent

@@ -26,6 +26,8 @@ FMT_LOOPVQ, FMT_KIVI = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 PER_CHANNEL, PER_TOKEN = 0, 1
 DT_BF16, DT_FP32, DT_FP16 = 0, 1, 2
+SLOT_KEEP, SLOT_FREE = -1, -2
+FORK_MAX = 256
 PAGE = 8
 
 
@@ -71,6 +73,11 @@ class Rows(ctypes.Structure):
                 ("stride_h", ctypes.c_int64), ("heads", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class Dist(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -97,6 +104,10 @@ _SIGS = {
     "kvq_qk_norm_rope": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _F, _P, _P, _I, _P, _P, _P, _P, _P]),
     "kvq_kivi_tree_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _SZ, _P]),
     "kvq_kivi_tree_workspace_size": (_SZ, [_P, _I, _I]),
+    "kvq_kivi_prefix_attn": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _SZ, _P]),
+    "kvq_kivi_prefix_workspace_size": (_SZ, [_P, _P, _I, _I]),
+    "kvq_cache_fork": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "kvq_verify_draft": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "kvq_decode_attn": (_I, [_I, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _SZ, _P]),
     "kvq_decode_attn_noalloc": (_I, [_I, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P]),
     "kvq_decode_workspace_size": (_SZ, [_I, _P, _I, _I]),
@@ -586,7 +597,32 @@ def make_tree_workspace(cfg: KiviConfig, B: int, N: int, device="cuda") -> torch
     return torch.empty(max(16, kvq_kivi_tree_workspace_size(cfg, B, N)), dtype=torch.uint8, device=device)
 
 
-class TreeAttnCall(_Call):
+class _WorkspaceCall(_Call):
+    """A call with a workspace, its last arguments but the stream. One that the caller does not give belongs to the
+    stream of the call, and is made anew when the call runs on another one."""
+
+    def _bind_ws(self, ws, make, device, *args):
+        self._own = None  # the stream that a workspace of the call's own was allocated on
+        if ws is None:
+            with _on(self._keep[0], device):
+                ws = self._ws = make()
+            self._own = _stream(self._keep[0])
+            self._again = make
+        else:  # its bytes are what it says: contiguous, on the device
+            _operand("ws", ws, (ws.dtype,), tuple(ws.shape))
+            self._ws = ws
+        self._bind(*args, _ptr(ws), ws.numel() * ws.element_size())
+
+    def __call__(self):
+        if self._own is not None and self._stream is None:
+            s = torch._C._cuda_getCurrentRawStream(self._device)
+            if s != self._own:  # called on another stream than before: a workspace that belongs there
+                self._own, self._ws = s, self._again()
+                self._args[-2] = ctypes.c_void_p(_ptr(self._ws))
+        super().__call__()
+
+
+class TreeAttnCall(_WorkspaceCall):
     """kvq_kivi_tree_attn: q bf16 [B][N][Hq][D], k_draft and v_draft fp16 [B][N][H][D], mask int64 (or uint64)
     [B][N] (bit j: drafted token j is seen), out bf16 or fp32 [B][N][Hq][D], n_draft int32 [B] or None (all N)."""
 
@@ -604,23 +640,7 @@ class TreeAttnCall(_Call):
         super().__init__("kvq_kivi_tree_attn", stream, q.device, (c, kc, cache, q, k_draft, v_draft, mask, out, n_draft, ws))
         args = (ctypes.byref(c), ctypes.byref(kc), _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(mask),
                 _ptr(n_draft), B, N, _ptr(out), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16)
-        self._own = None  # the stream that a workspace of the call's own was allocated on
-        if ws is None:
-            with _on(stream, q.device):
-                ws = self._ws = make_tree_workspace(cfg, B, N, q.device)
-            self._own = _stream(stream)
-            self._again = lambda: make_tree_workspace(cfg, B, N, q.device)
-        else:  # its bytes are what it says: contiguous, on the device
-            _operand("ws", ws, (ws.dtype,), tuple(ws.shape))
-        self._bind(*args, _ptr(ws), ws.numel() * ws.element_size())
-
-    def __call__(self):
-        if self._own is not None and self._stream is None:
-            s = torch._C._cuda_getCurrentRawStream(self._device)
-            if s != self._own:  # called on another stream than before: a workspace that belongs there
-                self._own, self._ws = s, self._again()
-                self._args[-2] = ctypes.c_void_p(_ptr(self._ws))
-        super().__call__()
+        self._bind_ws(ws, lambda: make_tree_workspace(cfg, B, N, q.device), q.device, *args)
 
 
 def kvq_kivi_tree_attn(cfg: KiviConfig, cache: KiviCache, q, k_draft, v_draft, mask, out, n_draft=None, ws=None,
@@ -628,6 +648,126 @@ def kvq_kivi_tree_attn(cfg: KiviConfig, cache: KiviCache, q, k_draft, v_draft, m
     """Attention of a tree of drafted tokens over the cache and one another. Without a workspace one is allocated
     for this call (through PyTorch, on the stream it runs on)."""
     TreeAttnCall(cfg, cache, q, k_draft, v_draft, mask, out, n_draft, ws, stream)()
+
+
+# ------------------------------------------------------------------------------------------
+# Attention under a shared prefix
+# ------------------------------------------------------------------------------------------
+
+def kvq_kivi_prefix_workspace_size(cfg: KiviConfig, prefix_cfg: KiviConfig, B: int, N: int) -> int:
+    c, pc = cfg.to_c(), prefix_cfg.to_c()
+    return lib().kvq_kivi_prefix_workspace_size(ctypes.byref(c), ctypes.byref(pc), B, N)
+
+
+def make_prefix_workspace(cfg: KiviConfig, prefix_cfg: KiviConfig, B: int, N: int, device="cuda") -> torch.Tensor:
+    """A workspace for kvq_kivi_prefix_attn (needs no initialisation; one for each call that runs at a time)."""
+    return torch.empty(max(16, kvq_kivi_prefix_workspace_size(cfg, prefix_cfg, B, N)), dtype=torch.uint8, device=device)
+
+
+class PrefixAttnCall(_WorkspaceCall):
+    """kvq_kivi_prefix_attn: q bf16 [B][N][Hq][D], out bf16 or fp32 of that shape; ``prefix`` a KiviCache whose slot
+    ``slot`` holds the tokens that every request of ``cache`` continues. k_draft and v_draft fp16 [B][N][H][D] and mask
+    int64 (or uint64) [B][N] as in TreeAttnCall, or all None: no drafted tokens. n_draft int32 [B] or None (all N)."""
+
+    def __init__(self, cfg: KiviConfig, cache: KiviCache, prefix_cfg: KiviConfig, prefix: KiviCache, slot: int, q, out,
+                 k_draft=None, v_draft=None, mask=None, n_draft=None, ws=None, stream=None):
+        if q.dim() != 4:
+            raise ValueError(f"q: expected the shape (B, N, Hq, D), got {tuple(q.shape)}")
+        B, N = q.shape[:2]
+        _operand("q", q, (torch.bfloat16,), (B, N, cfg.q_heads, cfg.D))
+        _operand("out", out, (torch.bfloat16, torch.float32), tuple(q.shape))
+        if (k_draft is None) != (mask is None) or (v_draft is None) != (mask is None):
+            raise ValueError("k_draft, v_draft and mask go together")
+        if mask is not None:
+            for name, x in (("k_draft", k_draft), ("v_draft", v_draft)):
+                _operand(name, x, (torch.float16,), (B, N, cfg.n_heads, cfg.D))
+            _operand("mask", mask, (torch.int64, torch.uint64), (B, N))
+        if n_draft is not None:
+            _operand("n_draft", n_draft, (torch.int32,), (B,))
+        c, kc, pc, pk = cfg.to_c(), cache.c_struct(), prefix_cfg.to_c(), prefix.c_struct()
+        super().__init__("kvq_kivi_prefix_attn", stream, q.device,
+                         (c, kc, pc, pk, cache, prefix, q, k_draft, v_draft, mask, out, n_draft, ws))
+        self._bind_ws(ws, lambda: make_prefix_workspace(cfg, prefix_cfg, B, N, q.device), q.device, ctypes.byref(c),
+                      ctypes.byref(kc), ctypes.byref(pc), ctypes.byref(pk), slot, _ptr(q), _ptr(k_draft), _ptr(v_draft),
+                      _ptr(mask), _ptr(n_draft), B, N, _ptr(out), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16)
+
+
+def kvq_kivi_prefix_attn(cfg: KiviConfig, cache: KiviCache, prefix_cfg: KiviConfig, prefix: KiviCache, slot: int, q, out,
+                         k_draft=None, v_draft=None, mask=None, n_draft=None, ws=None, stream=None):
+    """Attention of requests that continue one cached prefix: over the prefix, their own caches and their drafts.
+    Without a workspace one is allocated for this call (through PyTorch, on the stream it runs on)."""
+    PrefixAttnCall(cfg, cache, prefix_cfg, prefix, slot, q, out, k_draft, v_draft, mask, n_draft, ws, stream)()
+
+
+# ------------------------------------------------------------------------------------------
+# Slots of a cache
+# ------------------------------------------------------------------------------------------
+
+class CacheForkCall(_Call):
+    """kvq_cache_fork: slot b0 + i of ``cache`` (VqCache or KiviCache) becomes what slot source[i] (int32 [n]) of
+    ``from_cache`` was, or of ``cache`` itself without one; SLOT_KEEP and SLOT_FREE leave and empty a slot."""
+
+    def __init__(self, cfg, cache, source, from_cfg=None, from_cache=None, b0: int = 0, stream=None):
+        fmt, c = _fmt_cfg(cfg)
+        if (from_cfg is None) != (from_cache is None):
+            raise ValueError("from_cfg and from_cache go together")
+        if from_cfg is not None and type(from_cfg) is not type(cfg):
+            raise TypeError("caches of two formats")
+        _operand("source", source, (torch.int32,), (None,))
+        fc = None if from_cfg is None else _fmt_cfg(from_cfg)[1]
+        kc, fk = cache.c_struct(), None if from_cache is None else from_cache.c_struct()
+        super().__init__("kvq_cache_fork", stream, source.device, (c, kc, fc, fk, cache, from_cache, source))
+        self._bind(fmt, ctypes.byref(c), ctypes.byref(kc), None if fc is None else ctypes.byref(fc),
+                   None if fk is None else ctypes.byref(fk), _ptr(source), b0, source.shape[0])
+
+
+def kvq_cache_fork(cfg, cache, source, from_cfg=None, from_cache=None, b0: int = 0, stream=None):
+    """Slots of a cache continue other slots (fork, reorder, compact), or are freed."""
+    CacheForkCall(cfg, cache, source, from_cfg, from_cache, b0, stream)()
+
+
+# ------------------------------------------------------------------------------------------
+# Verification of drafted tokens
+# ------------------------------------------------------------------------------------------
+
+def _dist(t: torch.Tensor | None):
+    return None if t is None else Dist(t.data_ptr(), _step(t, 0), _step(t, 1), _DT[t.dtype])
+
+
+class VerifyDraftCall(_Call):
+    """kvq_verify_draft: target [B][N][V] (fp32, bf16 or fp16; any strides with contiguous entries), the target's
+    probabilities behind every node, draft of that type and shape or None (point masses), token and parent int32 [B][N],
+    u fp32 [B][N] or None (no sampling); path int32 [B][N], n_accept and next_token int32 [B] are written. n_draft int32
+    [B] or None (all N)."""
+
+    def __init__(self, target, draft, token, parent, u, path, n_accept, next_token, n_draft=None, stream=None):
+        if target.dtype not in _DT:
+            raise TypeError(f"target: expected one of {tuple(_DT)}, got {target.dtype}")
+        if target.dim() != 3:
+            raise ValueError(f"target: expected the shape (B, N, V), got {tuple(target.shape)}")
+        B, N, V = target.shape
+        for name, x in (("target", target), ("draft", draft)):
+            if x is not None:
+                _operand(name, x, (target.dtype,), (B, N, V), contiguous=False)
+                if x.shape[2] > 1 and x.stride(2) != 1:
+                    raise ValueError(f"{name}: the entries of a row need to be contiguous")
+        for name, x in (("token", token), ("parent", parent), ("path", path)):
+            _operand(name, x, (torch.int32,), (B, N))
+        for name, x in (("n_accept", n_accept), ("next_token", next_token), ("n_draft", n_draft)):
+            if x is not None or name != "n_draft":
+                _operand(name, x, (torch.int32,), (B,))
+        if u is not None:
+            _operand("u", u, (torch.float32,), (B, N))
+        p, q = _dist(target), _dist(draft)
+        super().__init__("kvq_verify_draft", stream, target.device,
+                         (p, q, target, draft, token, parent, u, path, n_accept, next_token, n_draft))
+        self._bind(B, N, V, ctypes.byref(p), None if q is None else ctypes.byref(q), _ptr(token), _ptr(parent),
+                   _ptr(n_draft), _ptr(u), _ptr(path), _ptr(n_accept), _ptr(next_token))
+
+
+def kvq_verify_draft(target, draft, token, parent, u, path, n_accept, next_token, n_draft=None, stream=None):
+    """Walk each request's tree of drafted tokens along the accepted ones and draw the token behind them."""
+    VerifyDraftCall(target, draft, token, parent, u, path, n_accept, next_token, n_draft, stream)()
 
 
 # ------------------------------------------------------------------------------------------
