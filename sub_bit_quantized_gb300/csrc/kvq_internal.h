@@ -288,7 +288,7 @@ struct VerifyArgs {
   int32_t* path; int32_t* n_accept; int32_t* next;
   int* err;
   int B, N, V;
-  int slice, chunk;                // set by the launch: entries a block takes, entries a sum is kept of
+  int blocks, slice, chunk;        // set by the launch: blocks a request, entries a block takes and a sum is kept of
 };
 cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
 

@@ -35,39 +35,46 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
-// a sum in two floats: hi + lo, lo what hi's roundings left
+__device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
+__device__ __forceinline__ float2 sub2(float2 x, float2 y) { return __fadd2_rn(x, neg2(y)); }
+
+// Two sums, each in two floats: hi + lo, lo what hi's roundings left
 struct Sum2 {
-  float hi, lo;
-  __device__ __forceinline__ void add(float x, float y) {  // x + y, |y| small beside x
-    const float h = __fadd_rn(hi, x), b = __fsub_rn(h, hi);
-    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(h, b)), __fsub_rn(x, b)), y));
+  float2 hi, lo;
+  __device__ __forceinline__ void add(float2 x) {
+    const float2 h = __fadd2_rn(hi, x), b = sub2(h, hi);
+    lo = __fadd2_rn(lo, __fadd2_rn(sub2(hi, sub2(h, b)), sub2(x, b)));
     hi = h;
   }
-  __device__ __forceinline__ void shuffle_add(int off) {
-    const float x = __shfl_xor_sync(0xFFFFFFFFu, hi, off), y = __shfl_xor_sync(0xFFFFFFFFu, lo, off);
-    add(x, y);
+  // of the warp's lanes: the sum of both, in fp32 pairs, since fp64 adds take the unit 16 cycles a warp
+  __device__ __forceinline__ double total() {
+    float h = hi.x, l = __fadd_rn(lo.x, lo.y);
+    auto plus = [&](float x, float y) {
+      const float s = __fadd_rn(h, x), b = __fsub_rn(s, h);
+      l = __fadd_rn(l, __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(x, b)), y));
+      h = s;
+    };
+    plus(hi.y, 0.f);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) plus(__shfl_xor_sync(0xFFFFFFFFu, h, off), __shfl_xor_sync(0xFFFFFFFFu, l, off));
+    return (double)h + (double)l;
   }
-  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
 };
 
-// a, in two floats
-struct Two {
-  float hi, lo;
+// w = max(0, p - a q) in two floats (hi, lo), of two entries; a in two floats
+struct Weight2 {
+  float2 hi, lo;
 };
-__device__ __forceinline__ Two split(double x) {
-  Two t;
-  t.hi = (float)x;
-  t.lo = (float)(x - (double)t.hi);
-  return t;
-}
-// w = max(0, p - a q) in two floats
-__device__ __forceinline__ Two weight(float p, float q, Two a) {
-  const float h = __fmul_rn(a.hi, q), l = __fmaf_rn(a.lo, q, __fmaf_rn(a.hi, q, -h));  // a q = h + l
-  const float d = __fsub_rn(p, h), b = __fsub_rn(d, p);
-  const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(h, b)), l);  // what d's rounding left, and l
-  const float s = __fadd_rn(d, e);
-  if (!(s > 0.f)) return {0.f, 0.f};
-  return {s, __fsub_rn(e, __fsub_rn(s, d))};
+__device__ __forceinline__ Weight2 weight(float2 p, float2 q, float a_hi, float a_lo) {
+  const float2 h = __fmul2_rn(f2(a_hi), q), l = __ffma2_rn(f2(a_lo), q, __ffma2_rn(f2(a_hi), q, neg2(h)));  // a q = h + l
+  const float2 d = sub2(p, h), b = sub2(d, p);
+  const float2 e = sub2(sub2(sub2(p, sub2(d, b)), __fadd2_rn(h, b)), l);  // what d's rounding left, and l
+  const float2 s = __fadd2_rn(d, e), r = sub2(e, sub2(s, d));
+  Weight2 w;
+  w.hi = make_float2(s.x > 0.f ? s.x : 0.f, s.y > 0.f ? s.y : 0.f);
+  w.lo = make_float2(s.x > 0.f ? r.x : 0.f, s.y > 0.f ? r.y : 0.f);
+  return w;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -87,340 +94,429 @@ __device__ __forceinline__ void store_remote(void* p, uint32_t rank, uint64_t v)
       : "memory");
 }
 
-// Entries v .. v + 3 of a row, 0 from `end` on. wide: the row's address and v allow one load.
+// 16 entries of a row for a lane, 0 from `end` on. kWide (the row's address allows it): piece k, entries 4 k + e, is at
+// v + 128 k + 4 lane + e, in loads of four entries; else entry j at v + 32 j + lane, one by one, so that a warp's loads
+// stay contiguous at any alignment.
 template <typename T>
-__device__ __forceinline__ void load4(const T* row, int v, int end, bool wide, float (&x)[4]) {
-  if (wide && v + 4 <= end) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(row + v));
-      x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-    } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + v));
-      T t[4];
-      *reinterpret_cast<uint2*>(t) = u;
+__device__ __forceinline__ void load16(const T* row, int v, int end, int lane, bool wide, float2 (&x)[8]) {
+  float y[16];
+  if (wide) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = to_f(t[i]);
+    for (int k = 0; k < 4; ++k) {
+      const int at = v + 128 * k + 4 * lane;
+      if (at + 4 <= end) {
+        if constexpr (sizeof(T) == 4) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(row + at));
+          y[4 * k] = f.x; y[4 * k + 1] = f.y; y[4 * k + 2] = f.z; y[4 * k + 3] = f.w;
+        } else {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + at));
+          const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[4 * k + e] = to_f(t[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[4 * k + e] = at + e < end ? to_f(row[at + e]) : 0.f;
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = v + i < end ? to_f(row[v + i]) : 0.f;
+    for (int j = 0; j < 16; ++j) {
+      const int at = v + 32 * j + lane;
+      y[j] = at < end ? to_f(row[at]) : 0.f;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
+}
+// which entry that is
+__device__ __forceinline__ int entry16(int v, int j, int lane, bool wide) {
+  return wide ? v + 128 * (j >> 2) + 4 * lane + (j & 3) : v + 32 * j + lane;
 }
 
 struct Shared {
   double chunk[kMaxChunks];
   uint64_t total[2][kMaxCluster];  // of the cluster's blocks, by turns
-  double part[kWarps];
-  float pz[kMaxNodes], qz[kMaxNodes], u[kMaxNodes];
-  int token[kMaxNodes], parent[kMaxNodes], path[kMaxNodes], gone[kMaxNodes];
-  int bad, node, count, n_gone, at, pass, found;
-  double a, z, target;
   uint64_t best[kWarps];
+  int path[kMaxNodes], gone[kMaxNodes];
+  int bad, node, n_gone, done;
+  float a_hi, a_lo;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
-  __shared__ Shared s;
-  const int C = gridDim.x / a.B;
-  const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = C > 1 ? cluster_rank() : 0;
-  const int nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
-  if (nd == 0) {  // the whole cluster
-    if (rank == 0 && tid == 0) a.n_accept[b] = 0;
-    return;
+// The nodes of a request: lane l of every warp holds nodes l and l + 32
+struct Nodes {
+  int token[2], parent[2];
+  // bit i: node i >= from is a child of `node` (and its token is x)
+  __device__ __forceinline__ uint64_t children(int node, int from) const {
+    const uint64_t m = (uint64_t)__ballot_sync(0xFFFFFFFFu, parent[0] == node) |
+                       (uint64_t)__ballot_sync(0xFFFFFFFFu, parent[1] == node) << 32;
+    return from >= 64 ? 0ull : m >> from << from;
   }
+  __device__ __forceinline__ uint64_t say(int x) const {
+    return (uint64_t)__ballot_sync(0xFFFFFFFFu, token[0] == x) | (uint64_t)__ballot_sync(0xFFFFFFFFu, token[1] == x) << 32;
+  }
+};
+template <typename V>
+__device__ __forceinline__ V of_node(const V (&x)[2], int i) {
+  const V lo = __shfl_sync(0xFFFFFFFFu, x[0], i & 31), hi = __shfl_sync(0xFFFFFFFFu, x[1], i & 31);
+  return i < 32 ? lo : hi;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
+  __shared__ Shared s;
+  const int C = a.blocks, b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = C > 1 ? cluster_rank() : 0;
   const T* P = static_cast<const T*>(a.p) + b * a.p_sb;
   const T* Q = a.q ? static_cast<const T*>(a.q) + b * a.q_sb : nullptr;
-  if (tid == 0) s.bad = 0;
-  __syncthreads();
-  if (tid < nd) {
-    const int i = tid, x = a.token[(size_t)b * a.N + i], par = i ? a.parent[(size_t)b * a.N + i] : 0;
-    const bool ok = x >= 0 && x < a.V && par >= 0 && (i == 0 || par < i);
-    if (!ok) s.bad = 1;
-    s.token[i] = x;
-    s.parent[i] = i ? par : -1;
-    s.u[i] = a.u ? a.u[(size_t)b * a.N + i] : 0.f;
-    if (ok && i && a.u) {
-      s.pz[i] = to_f(P[par * a.p_st + x]);
-      s.qz[i] = Q ? to_f(Q[par * a.q_st + x]) : 1.f;
+  const int nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
+  // ---- the nodes; of those that count a parent before them and a token of the vocabulary (every warp sees the same) ----
+  Nodes nodes;
+  bool ok = true;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h;
+    nodes.token[h] = nodes.parent[h] = -1;
+    if (i < a.N) {
+      nodes.token[h] = a.token[(size_t)b * a.N + i];
+      nodes.parent[h] = a.parent[(size_t)b * a.N + i];
     }
+    if (i >= nd) nodes.token[h] = nodes.parent[h] = -1;
+    else ok = ok && nodes.token[h] >= 0 && nodes.token[h] < a.V && (i == 0 || (nodes.parent[h] >= 0 && nodes.parent[h] < i));
+    if (i == 0) nodes.parent[h] = -1;
   }
-  __syncthreads();
-  if (s.bad) {
+  if (nd == 0 || !__all_sync(0xFFFFFFFFu, ok)) {  // the whole cluster
     if (rank == 0 && tid == 0) {
       a.n_accept[b] = 0;
-      set_error(a.err, KVQ_ERR_INVALID_ARG);
+      if (nd > 0) set_error(a.err, KVQ_ERR_INVALID_ARG);
     }
     return;
   }
-  if (C > 1) cluster_sync();  // every block's shared memory is there
   const int v0 = min(a.V, (int)rank * a.slice), v1 = min(a.V, v0 + a.slice);
-  const int n_chunks = (v1 - v0 + a.chunk - 1) / a.chunk;
   int turn = 0;
-  auto share = [&](uint64_t mine) {  // this block's value to every block; all values in s.total[turn]
-    if (C > 1) {
-      if (tid < C) store_remote(&s.total[turn][rank], tid, mine);
-      cluster_sync();
-    } else {
-      if (tid == 0) s.total[turn][0] = mine;
-      __syncthreads();
-    }
+  auto cluster_wait = [&]() {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
   };
 
   if (!a.u) {
     // ---- no sampling: the arg max of each node of the path ----
+    if (C > 1) cluster_sync();  // every block's shared memory is there
     int node = 0, count = 1, best = 0;
     if (tid == 0) s.path[0] = 0;
     for (;;) {
       const T* row = P + node * a.p_st;
-      const bool wide = (reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) == 0;  // v0 is a multiple of 4
+      constexpr int kLoad = sizeof(T) == 4 ? 4 : 8;  // entries of a 16-byte load
+      const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;  // v0 is a multiple of 512
       float top = -INFINITY;
       int at = 0x7FFFFFFF;
+      auto look = [&](float x, int i) {
+        if (x > top) {
+          top = x;
+          at = i;
+        }
+      };
       constexpr int kAhead = 4;
-      for (int v = v0 + 4 * tid; v < v1; v += 4 * kThreads * kAhead) {
-        float x[kAhead][4];
+      int v = v0;
+      if (wide) {
+        constexpr int kStep = kLoad * kThreads;
+        for (; v + kStep <= v1; v += kAhead * kStep) {
+          uint4 u[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) load4(row, v + 4 * kThreads * k, v1, wide, x[k]);
+          for (int k = 0; k < kAhead; ++k)
+            if (v + (k + 1) * kStep <= v1) u[k] = __ldg(reinterpret_cast<const uint4*>(row + v + k * kStep) + tid);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
+          for (int k = 0; k < kAhead; ++k)
+            if (v + (k + 1) * kStep <= v1) {
+              const T* t = reinterpret_cast<const T*>(&u[k]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = v + 4 * kThreads * k + e;
-            if (i < v1 && x[k][e] > top) {
-              top = x[k][e];
-              at = i;
+              for (int e = 0; e < kLoad; ++e) look(to_f(t[e]), v + k * kStep + kLoad * tid + e);
             }
-          }
+        }
+        v = v0 + (v1 - v0) / kStep * kStep;
+      }
+      for (; v < v1; v += kAhead * kThreads) {
+        float x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = v + k * kThreads + tid < v1 ? to_f(row[v + k * kThreads + tid]) : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) look(x[k], v + k * kThreads + tid);
       }
       // one number that is larger for larger values and, of equal ones, lower indices
-      const uint32_t f = __float_as_uint(top + 0.f);  // -0 counts as 0
-      uint64_t key = ((uint64_t)((f & 0x80000000u) ? ~f : f | 0x80000000u) << 32) | (0x7FFFFFFFu - (uint32_t)at);
+      auto key_of = [](float x, int i) {
+        const uint32_t f = __float_as_uint(x + 0.f);  // -0 counts as 0
+        return ((uint64_t)((f & 0x80000000u) ? ~f : f | 0x80000000u) << 32) | (0x7FFFFFFFu - (uint32_t)i);
+      };
+      uint64_t key = key_of(top, at);
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
       if (lane == 0) s.best[warp] = key;
       __syncthreads();
-      for (int w = 0; w < kWarps; ++w) key = max(key, s.best[w]);
-      share(key);
-      key = s.total[turn][0];
-      for (int r = 1; r < C; ++r) key = max(key, s.total[turn][r]);
+      if (warp == 0) {
+        key = s.best[lane & (kWarps - 1)];
+#pragma unroll
+        for (int off = kWarps / 2; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+        if (lane < C) store_remote(&s.total[turn][rank], lane, key);
+      }
+      cluster_wait();
+      key = lane < C ? s.total[turn][lane] : 0;
+#pragma unroll
+      for (int off = kMaxCluster / 2; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+      key = __shfl_sync(0xFFFFFFFFu, key, 0);
       turn ^= 1;
       best = (int)(0x7FFFFFFFu - (uint32_t)key);
       if (best == 0x7FFFFFFF) best = 0;  // nothing above the lowest value
-      int next = 0;
-      for (int i = node + 1; i < nd && !next; ++i)
-        if (s.parent[i] == node && s.token[i] == best) next = i;
+      const uint64_t next = nodes.children(node, node + 1) & nodes.say(best);
       if (!next) break;
-      node = next;
-      if (tid == 0) s.path[count] = next;
+      node = __ffsll(next) - 1;
+      if (tid == 0) s.path[count] = node;
       ++count;
     }
-    if (rank == 0) {
-      __syncthreads();
-      if (tid < count) a.path[(size_t)b * a.N + tid] = s.path[tid];
-      if (tid == 0) {
+    if (rank == 0 && warp == 0) {
+      __syncwarp();
+      for (int i = lane; i < count; i += 32) a.path[(size_t)b * a.N + i] = s.path[i];
+      if (lane == 0) {
         a.n_accept[b] = count;
         a.next[b] = best;
       }
     }
-    if (C > 1) cluster_sync();  // nobody leaves while its shared memory is written
-    return;
+    return;  // the last writes into this block's memory were those that the last barrier waited for
   }
 
-  // ---- sampling ----
-  if (tid == 0) {
-    s.path[0] = 0;
-    s.node = 0;
-    s.count = 1;
-    s.n_gone = 0;
-    s.at = 1;
-    s.a = 0.0;
-    s.z = 1.0;
+  // ---- sampling: warp 0 walks, all warps add ----
+  float pz[2] = {0.f, 0.f}, qz[2] = {1.f, 1.f}, u[2] = {0.f, 0.f};
+  if (warp == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      if (i < nd) u[h] = a.u[(size_t)b * a.N + i];
+      if (i < nd && i > 0) {
+        pz[h] = to_f(P[nodes.parent[h] * a.p_st + nodes.token[h]]);
+        if (Q) qz[h] = to_f(Q[nodes.parent[h] * a.q_st + nodes.token[h]]);
+      }
+    }
   }
-  int fallback = 0;
+  if (C > 1) cluster_sync();  // every block's shared memory is there
+  const int n_chunks = (v1 - v0 + a.chunk - 1) / a.chunk;
+  int node = 0, at = 1, count = 1;   // warp 0's
+  uint64_t gone = 0;                 // children of the node that were rejected (point masses)
+  double wa = 0.0, wz = 1.0;
+  bool fallback = false;
+  if (tid == 0) s.path[0] = 0;
   for (;;) {
-    __syncthreads();
-    if (tid == 0) {  // on until a pass is needed: after a rejection against Q, or at the end
-      s.pass = 0;
-      for (; s.at < nd; ++s.at) {
-        const int i = s.at;
-        if (s.parent[i] != s.node) continue;
-        const float q = s.qz[i];
-        bool gone = false;
-        for (int k = 0; k < s.n_gone; ++k) gone = gone || s.gone[k] == s.token[i];
-        double w = (double)s.pz[i];
-        if (Q) w = fmax(w - s.a * (double)q, 0.0);
-        else if (gone) w = 0.0;
-        if ((double)s.u[i] * s.z * (double)q < w) {
-          s.path[s.count++] = i;
-          s.node = i;
-          s.a = 0.0;
-          s.z = 1.0;
-          s.n_gone = 0;
+    bool rejected = false;
+    if (warp == 0) {  // on until a pass is needed: after a rejection against Q, or at the end
+      for (;;) {
+        const uint64_t m = nodes.children(node, at);
+        if (!m || fallback) break;
+        const int i = __ffsll(m) - 1;
+        at = i + 1;
+        const float q = of_node(qz, i), p = of_node(pz, i), ui = of_node(u, i);
+        double w = (double)p;
+        if (Q) w = fmax(w - wa * (double)q, 0.0);
+        else if (gone) w = (gone & nodes.say(of_node(nodes.token, i))) ? 0.0 : w;
+        if ((double)ui * wz * (double)q < w) {
+          if (lane == 0) s.path[count] = i;
+          ++count;
+          node = i;
+          wa = 0.0;
+          wz = 1.0;
+          gone = 0;
         } else if (Q) {
-          s.a += s.z;
-          s.pass = 1;
-          ++s.at;
+          wa += wz;
+          rejected = true;
           break;
         } else {
-          s.z -= w;
-          s.gone[s.n_gone++] = s.token[i];
+          wz -= w;
+          gone |= 1ull << i;
         }
       }
-      if (fallback) {
-        s.a = 0.0;
-        s.n_gone = 0;
+      const int n_lo = __popc((uint32_t)gone);
+      if ((gone >> lane) & 1) s.gone[__popc((uint32_t)gone & ((1u << lane) - 1))] = nodes.token[0];
+      if ((gone >> (lane + 32)) & 1) s.gone[n_lo + __popc((uint32_t)(gone >> 32) & ((1u << lane) - 1))] = nodes.token[1];
+      if (lane == 0) {
+        s.node = node;
+        s.n_gone = __popcll(gone);
+        s.a_hi = (float)wa;
+        s.a_lo = (float)(wa - (double)s.a_hi);
+        s.done = 0;
       }
     }
     __syncthreads();
-    const bool rejected = s.pass;  // else this pass is the draw's
     const T* row = P + s.node * a.p_st;
-    const T* qrow = Q && s.a > 0.0 ? Q + s.node * a.q_st : nullptr;
+    const float a_hi = s.a_hi, a_lo = s.a_lo;
+    const T* qrow = Q && a_hi > 0.f ? Q + s.node * a.q_st : nullptr;
     const bool wide = (reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) == 0 &&
                       (!qrow || (reinterpret_cast<uintptr_t>(qrow) & (4 * sizeof(T) - 1)) == 0);
-    const Two f = split(s.a);
     const int n_gone = s.n_gone;
-    auto is_gone = [&](int v) {
-      for (int k = 0; k < n_gone; ++k)
-        if (s.gone[k] == v) return true;
-      return false;
+    // P without what was rejected
+    auto drop_gone = [&](float2 (&x)[8], int v, int end) {
+      for (int k = 0; k < n_gone; ++k) {
+        const int g = s.gone[k];
+        if (g < v || g >= end) continue;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (entry16(v, j, lane, wide) == g) (j & 1 ? x[j >> 1].y : x[j >> 1].x) = 0.f;
+      }
     };
     // ---- sums of w over the block's chunks ----
     for (int c = warp; c < n_chunks; c += kWarps) {
       const int c0 = v0 + c * a.chunk, c1 = min(v1, c0 + a.chunk);
-      bool some_gone = false;
-      for (int k = lane; k < n_gone; k += 32) some_gone = some_gone || (s.gone[k] >= c0 && s.gone[k] < c1);
-      some_gone = __any_sync(0xFFFFFFFFu, some_gone);
-      Sum2 sum = {0.f, 0.f};
-      for (int v = c0 + 4 * lane; v < c1; v += 512) {
-        float p[4][4], q[4][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) load4(row, v + 128 * k, c1, wide, p[k]);
+      Sum2 sum = {f2(0.f), f2(0.f)};
+      for (int v = c0; v < c1; v += 512) {
+        float2 p[8], q[8];
+        load16(row, v, c1, lane, wide, p);
         if (qrow) {
+          load16(qrow, v, c1, lane, wide, q);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) load4(qrow, v + 128 * k, c1, wide, q[k]);
-        }
-        if (some_gone) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (is_gone(v + 128 * k + e)) p[k][e] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (qrow) {
-              const Two w = weight(p[k][e], q[k][e], f);
-              sum.add(w.hi, w.lo);
-            } else {
-              sum.add(p[k][e], 0.f);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const Weight2 w = weight(p[i], q[i], a_hi, a_lo);
+            sum.add(w.hi);
+            sum.lo = __fadd2_rn(sum.lo, w.lo);
           }
-      }
+        } else {
+          if (n_gone) drop_gone(p, v, min(c1, v + 512));
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) sum.shuffle_add(off);
-      if (lane == 0) s.chunk[c] = sum.value();
+          for (int i = 0; i < 8; ++i) sum.add(p[i]);
+        }
+      }
+      const double t = sum.total();
+      if (lane == 0) s.chunk[c] = t;
     }
     __syncthreads();
-    double mine = 0.0;
-    for (int c = tid; c < n_chunks; c += kThreads) mine += s.chunk[c];
+    // ---- warp 0: runs of chunks a lane, the block's total to every block ----
+    const int run = (n_chunks + 31) / 32;
+    double upto = 0.0;  // the block's sum up to the end of the lane's run
+    if (warp == 0) {
+      for (int c = lane * run; c < min(n_chunks, (lane + 1) * run); ++c) upto += s.chunk[c];
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, off);
-    if (lane == 0) s.part[warp] = mine;
-    __syncthreads();
-    mine = 0.0;
-    for (int w = 0; w < kWarps; ++w) mine += s.part[w];
-    share(__double_as_longlong(mine));
-    double total = 0.0, before = 0.0;
-    for (int r = 0; r < C; ++r) {
-      if (r == (int)rank) before = total;
-      total += __longlong_as_double(s.total[turn][r]);
+      for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+        if (lane >= off) upto += y;
+      }
+      const double mine = __shfl_sync(0xFFFFFFFFu, upto, 31);
+      if (lane < C) store_remote(&s.total[turn][rank], lane, __double_as_longlong(mine));
+    }
+    cluster_wait();
+    if (warp == 0) {
+      double end = lane < C ? __longlong_as_double(s.total[turn][lane]) : 0.0;  // the sum up to the end of block `lane`
+#pragma unroll
+      for (int off = 1; off < kMaxCluster; off <<= 1) {
+        const double y = __shfl_up_sync(0xFFFFFFFFu, end, off);
+        if (lane >= off) end += y;
+      }
+      const double total = __shfl_sync(0xFFFFFFFFu, end, C - 1);
+      // a rejection with a later child left to test: on; else these are the draw's sums. A residual without mass: P's
+      const bool more = rejected && nodes.children(node, at), empty = !more && !fallback && !(total > 0.0);
+      if (more) {
+        wz = total;
+      } else if (empty) {
+        fallback = true;
+        wa = 0.0;
+        gone = 0;
+      } else {
+        // ---- the draw: the block, the chunk, the entry in which the sums pass u total ----
+        const double target = (double)__shfl_sync(0xFFFFFFFFu, u[0], 0) * total;
+        // each block's end is the next one's beginning, so exactly one holds the target; without mass any token does
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, lane < C && end > target);
+        const double before = __shfl_sync(0xFFFFFFFFu, end, rank > 0 ? (int)rank - 1 : 0);
+        if (rank == 0) {
+          for (int i = lane; i < count; i += 32) a.path[(size_t)b * a.N + i] = s.path[i];
+          if (lane == 0) {
+            a.n_accept[b] = count;
+            if (!past) a.next[b] = 0;
+          }
+        }
+        if (past && __ffs(past) - 1 == (int)rank) {
+          double base = rank > 0 ? before : 0.0;
+          const unsigned in = __ballot_sync(0xFFFFFFFFu, base + upto > target);
+          const int last_run = (n_chunks - 1) / run, hold = in ? min(__ffs(in) - 1, last_run) : last_run;
+          const double y = __shfl_sync(0xFFFFFFFFu, upto, hold > 0 ? hold - 1 : 0);
+          if (hold > 0) base += y;
+          int c = hold * run;
+          for (; c + 1 < min(n_chunks, (hold + 1) * run); ++c) {
+            const double e = base + s.chunk[c];
+            if (e > target) break;
+            base = e;
+          }
+          const int c0 = v0 + c * a.chunk, c1 = min(v1, c0 + a.chunk);
+          int last = c0, found = -1;  // last: the last entry with a weight, should roundings leave none past the target
+          for (int v = c0; v < c1 && found < 0; v += 512) {
+            // 16 entries a lane, in order: v + 16 lane ..
+            float2 p[8], q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int x = v + 16 * lane + 2 * i;
+              p[i] = make_float2(x < c1 ? to_f(row[x]) : 0.f, x + 1 < c1 ? to_f(row[x + 1]) : 0.f);
+              q[i] = f2(0.f);
+              if (qrow) q[i] = make_float2(x < c1 ? to_f(qrow[x]) : 0.f, x + 1 < c1 ? to_f(qrow[x + 1]) : 0.f);
+            }
+            for (int k = 0; k < n_gone; ++k) {
+              const int g = s.gone[k] - v - 16 * lane;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (j == g) (j & 1 ? p[j >> 1].y : p[j >> 1].x) = 0.f;
+            }
+            float hi[16], lo[16];
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              Weight2 w = {p[i], f2(0.f)};
+              if (qrow) w = weight(p[i], q[i], a_hi, a_lo);
+              hi[2 * i] = w.hi.x; hi[2 * i + 1] = w.hi.y;
+              lo[2 * i] = w.lo.x; lo[2 * i + 1] = w.lo.y;
+            }
+            Sum2 t = {f2(0.f), f2(0.f)};
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              t.add(make_float2(hi[j], hi[j + 1]));
+              t.lo = __fadd2_rn(t.lo, make_float2(lo[j], lo[j + 1]));
+              if (hi[j] > 0.f) last = v + 16 * lane + j;
+              if (hi[j + 1] > 0.f) last = v + 16 * lane + j + 1;
+            }
+            sum = ((double)t.hi.x + (double)t.hi.y) + ((double)t.lo.x + (double)t.lo.y);
+            double end16 = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+              const double z = __shfl_up_sync(0xFFFFFFFFu, end16, off);
+              if (lane >= off) end16 += z;
+            }
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, base + end16 > target);
+            if (hit) {  // that lane's entries, one a lane
+              const int src = __ffs(hit) - 1;
+              float h = 0.f, l = 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float x = __shfl_sync(0xFFFFFFFFu, hi[j], src), z = __shfl_sync(0xFFFFFFFFu, lo[j], src);
+                if (lane == j) {
+                  h = x;
+                  l = z;
+                }
+              }
+              double e = (double)h + (double)l;
+#pragma unroll
+              for (int off = 1; off < 16; off <<= 1) {
+                const double z = __shfl_up_sync(0xFFFFFFFFu, e, off);
+                if (lane >= off) e += z;
+              }
+              const double at16 = src > 0 ? __shfl_sync(0xFFFFFFFFu, end16, src - 1) : 0.0;
+              const unsigned one = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f && base + at16 + e > target);
+              const unsigned some = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f);
+              found = v + 16 * src + (one ? __ffs(one) - 1 : some ? 31 - __clz(some) : 0);
+            }
+            base += __shfl_sync(0xFFFFFFFFu, end16, 31);
+          }
+#pragma unroll
+          for (int off = 16; off >= 1; off >>= 1) last = max(last, __shfl_xor_sync(0xFFFFFFFFu, last, off));
+          if (lane == 0) a.next[b] = found >= 0 ? found : last;
+        }
+        if (lane == 0) s.done = 1;
+      }
     }
     turn ^= 1;
-    if (rejected) {
-      // the walk goes on if a later child of this node is left to test; else these are the draw's sums
-      bool more = false;
-      for (int i = s.at; i < nd; ++i) more = more || s.parent[i] == s.node;
-      if (more) {
-        __syncthreads();
-        if (tid == 0) s.z = total;
-        continue;
-      }
-    }
-    if (!(total > 0.0) && !fallback) {
-      fallback = 1;
-      continue;
-    }
-    // ---- the draw: the block, the chunk, the entry in which the sums pass u total ----
-    const double target = (double)s.u[0] * total;
-    // each block's end is the next one's beginning, so exactly one holds the target
-    if (rank == 0 && tid < s.count) a.path[(size_t)b * a.N + tid] = s.path[tid];
-    if (rank == 0 && tid == 0) a.n_accept[b] = s.count;
-    const bool none = !(total > 0.0);  // of a row without mass any token does
-    if (none && rank == 0 && tid == 0) a.next[b] = 0;
-    double end = 0.0;
-    bool earlier = false;
-    for (int r = 0; r <= (int)rank; ++r) {
-      end += __longlong_as_double(s.total[turn ^ 1][r]);
-      if (r < (int)rank) earlier = earlier || end > target;
-    }
-    if (!none && !earlier && end > target && warp == 0) {
-      int c = 0;
-      double base = before;
-      for (; c + 1 < n_chunks; ++c) {
-        const double e = base + s.chunk[c];
-        if (e > target) break;
-        base = e;
-      }
-      const int c0 = v0 + c * a.chunk, c1 = min(v1, c0 + a.chunk);
-      int last = c0;  // the last entry with a weight, should roundings leave none past the target
-      int found = -1;
-      for (int v = c0 + 4 * lane; v - 4 * lane < c1 && found < 0; v += 128) {
-        float p[4], q[4];
-        load4(row, v, c1, wide, p);
-        if (qrow) load4(qrow, v, c1, wide, q);
-        double w[4], run = 0.0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (n_gone && is_gone(v + e)) p[e] = 0.f;
-          Two t = {p[e], 0.f};
-          if (qrow) t = weight(p[e], q[e], f);
-          w[e] = (double)t.hi + (double)t.lo;
-          run += w[e];
-          if (w[e] > 0.0) last = max(last, v + e);
-        }
-        double upto = run;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const double y = __shfl_up_sync(0xFFFFFFFFu, upto, off);
-          if (lane >= off) upto += y;
-        }
-        const unsigned past = __ballot_sync(0xFFFFFFFFu, base + upto > target);
-        if (past) {
-          const int src = __ffs(past) - 1;
-          double at = base + (upto - run);
-          int hit = v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (w[e] > 0.0) hit = v + e;
-#pragma unroll
-          for (int e = 3; e >= 0; --e) {
-            double x = at;
-            for (int k = 0; k <= e; ++k) x += w[k];
-            if (x > target) hit = v + e;
-          }
-          found = __shfl_sync(0xFFFFFFFFu, hit, src);
-        }
-        base += __shfl_sync(0xFFFFFFFFu, upto, 31);
-      }
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) last = max(last, __shfl_xor_sync(0xFFFFFFFFu, last, off));
-      if (lane == 0) a.next[b] = found >= 0 ? found : last;
-    }
-    break;
+    __syncthreads();
+    if (s.done) return;  // the last writes into this block's memory were those that the last barrier waited for
   }
-  if (C > 1) cluster_sync();  // nobody leaves while its shared memory is written
 }
 
 template <typename T>
@@ -428,6 +524,7 @@ cudaError_t launch_typed(const VerifyArgs& args, cudaStream_t st) {
   VerifyArgs a = args;
   int C = 1;
   while (C < kMaxCluster && a.B * C * 2 <= 2 * device_sms() && a.V / (2 * C) >= 2048) C *= 2;
+  a.blocks = C;
   a.slice = ((a.V + C - 1) / C + 511) / 512 * 512;
   a.chunk = 512;
   while ((a.slice + a.chunk - 1) / a.chunk > kMaxChunks) a.chunk *= 2;
