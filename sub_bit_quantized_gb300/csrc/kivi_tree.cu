@@ -32,6 +32,7 @@
 
 #include <cfloat>
 
+#include "kivi_tc.cuh"
 #include "kivi_tree_join.h"
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
@@ -41,12 +42,6 @@ namespace kvq {
 namespace {
 
 constexpr int kTile = 128;    // tokens per tile
-constexpr int kGroupT = 32;   // tokens per key group, channels per value group
-// A row's weights are exp2(x - m + kRaise), m its running maximum, which moves when a score passes it by kSlack (log2):
-// weights stay below 2^15 and are held as fp16, where one below 2^-30 of the maximum's is lost (2^-25 without kRaise).
-// Raising costs a pass over the sums; at a slack of 7 the peaked scores of outlier channels raise some row of a tile
-// of 64 in most of a segment's first tiles.
-constexpr float kSlack = 10.f, kRaise = 5.f;
 
 // TOK stored tokens (a key group or a tile): key codes, scales and zeros [groups][128], value codes, scales and
 // zeros [tokens][4]
@@ -59,37 +54,10 @@ struct StageLayout {
   static constexpr int kBytes = kVz + TOK * (kD / kGroupT) * 2;
 };
 
-__device__ __forceinline__ float th2f(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // The work of a call, the same for every block: segment (b, h, row tile) has T_b tiles (its cached
 // and drafted tokens), all segments in the order b, h, row tile form one list of P tile positions,
 // and block k of G takes positions [k P / G, (k + 1) P / G); of fewer than G positions the first blocks take one each,
 // so that the blocks of a segment are neighbours (two requests, 1K context, 64 rows: 20.2 -> 16.6 us).
-struct TreeLens {
-  int nqk, nqv, n, nd;  // quantized keys, quantized values, cached tokens, drafted tokens that rows may attend
-  int tiles, nr;        // tiles; tokens whose rows attend (nd, or without drafts the queries')
-};
-__device__ __forceinline__ TreeLens tree_lens(const KiviTreeArgs& a, int b) {
-  TreeLens L;
-  L.nqk = min(max(a.n_quant_k[b], 0), a.max_tokens) & -kGroupT;
-  L.n = L.nqk + max(0, min(a.n_tok[b] - L.nqk, a.residual));
-  // at least n - residual, as in every valid state: the ring holds no more values
-  L.nqv = (a.residual > 0) ? min(max(a.n_quant_v[b], max(L.n - a.residual, 0)), L.nqk) : L.nqk;
-  L.nr = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
-  L.nd = a.mask ? L.nr : 0;
-  L.tiles = L.nr > 0 ? max((int)((uint32_t)(L.n + L.nd + kTile - 1) / kTile), 1) : 0;
-  return L;
-}
-// where the share of block k of G begins, without leaving 32 bits (k <= G, G far below 2^15)
-__device__ __forceinline__ int share_begin(int P, int k, const IntDiv& G) {
-  if (P <= G.d) return min(k, P);
-  const int q = div_by(P, G);
-  return k * q + div_by(k * (P - q * G.d), G);
-}
 
 // A role's place in the block's share
 struct Walk {
@@ -102,7 +70,7 @@ struct Walk {
     tile = 0;
     if (++seg < seg_per_b) return;
     seg = 0;
-    do len = tree_lens(a, ++b);
+    do len = tree_lens(a, ++b, kTile);
     while (len.tiles == 0);  // a position is left, so such a request exists
   }
 };
@@ -124,7 +92,7 @@ __device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b,
   int upto = 0;  // tiles of this lane's requests, then of all up to it
 #pragma unroll 1
   for (int b = b1 - 1; b >= b0; --b) {  // L: of the first one
-    L = tree_lens(a, b);
+    L = tree_lens(a, b, kTile);
     upto += L.tiles;
   }
   const int mine = upto;
@@ -143,7 +111,7 @@ __device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b,
       w.b = b0;
       while (p0 >= (before + L.tiles) * seg_per_b) {  // ends inside the run
         before += L.tiles;
-        L = tree_lens(a, ++w.b);
+        L = tree_lens(a, ++w.b, kTile);
       }
       const int off = p0 - before * seg_per_b;
       w.len = L;
@@ -157,111 +125,15 @@ __device__ __forceinline__ int2 find_share(const KiviTreeArgs& a, int seg_per_b,
   return make_int2(p0, p1);
 }
 
-// The row of a token behind the quantized ones (token t, value: of the ring): residual, drafted, or none
-__device__ __forceinline__ const uint16_t* fp16_key(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t) {
-  if (t < L.n) return a.k_resid + (((size_t)b * a.H + h) * a.residual + (t - L.nqk)) * kD;
-  if (t < L.n + L.nd) return a.k_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
-  return nullptr;
-}
-// place: t % residual for a token that is cached
-__device__ __forceinline__ const uint16_t* fp16_value(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int place) {
-  if (t < L.n) return a.v_resid + (((size_t)b * a.H + h) * a.residual + place) * kD;
-  if (t < L.n + L.nd) return a.v_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
-  return nullptr;
-}
-// place of token t0 + i (i < 32) when t0's is p: the ring holds at least 32 rows, or none (no token is there then)
-__device__ __forceinline__ int ring_place(int p, int i, int R) {
-  p += i;
-  if (p >= R) p -= R;
-  return p;
-}
-// channels 8c .. 8c+7 of a row, zero without one
-__device__ __forceinline__ uint4 row8(const uint16_t* p, int c) {
-  return p ? __ldg(reinterpret_cast<const uint4*>(p + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
-}
 // halves of w that are infinite or NaN become 0
 __device__ __forceinline__ void drop_nonfinite(uint32_t& w) {
   if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
   if ((w & 0x7C000000u) == 0x7C000000u) w &= 0xFFFFu;
 }
 
-// Channel order of the staged keys and queries. The contraction runs over all 128 channels, so any order serves
-// that both share; this one is the order in which a code word's halves unpack: pairs (c, c + 8) of 16 channels
-// (2 bits), (c, c + 4) of 8 (4 bits). lo, hi: channels 16 w .. + 7, 16 w + 8 .. + 15, natural order; out: the two
-// 16-byte chunks of the block.
-template <int KB>
-__device__ __forceinline__ void pair_order(const uint4 lo, const uint4 hi, uint4& out0, uint4& out1) {
-  if constexpr (KB == 2) {
-    out0 = make_uint4(__byte_perm(lo.x, hi.x, 0x5410), __byte_perm(lo.x, hi.x, 0x7632), __byte_perm(lo.y, hi.y, 0x5410),
-                      __byte_perm(lo.y, hi.y, 0x7632));
-    out1 = make_uint4(__byte_perm(lo.z, hi.z, 0x5410), __byte_perm(lo.z, hi.z, 0x7632), __byte_perm(lo.w, hi.w, 0x5410),
-                      __byte_perm(lo.w, hi.w, 0x7632));
-  } else {
-    out0 = make_uint4(__byte_perm(lo.x, lo.z, 0x5410), __byte_perm(lo.x, lo.z, 0x7632), __byte_perm(lo.y, lo.w, 0x5410),
-                      __byte_perm(lo.y, lo.w, 0x7632));
-    out1 = make_uint4(__byte_perm(hi.x, hi.z, 0x5410), __byte_perm(hi.x, hi.z, 0x7632), __byte_perm(hi.y, hi.w, 0x5410),
-                      __byte_perm(hi.y, hi.w, 0x7632));
-  }
-}
 // Token order of the staged values and weights: in odd octets neighbours change places, so that the two octets a
 // warp reads at a time come from different banks.
 __device__ __forceinline__ int token_place(int t) { return t ^ ((t >> 3) & 1); }
-
-__device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
-__device__ __forceinline__ uint32_t as_u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-// Constants of the unpacking, held in registers, since an instruction has room for one immediate: the exponent of
-// 2^10 in both halves (mask and insert are then one instruction), and the powers of two that bring codes unpacked in
-// place back to their value.
-struct CodeScale {
-  uint32_t magic;
-  uint32_t p[4];  // 2^-2, 2^-4, 2^-6, 2^-8 as packed halves
-  __device__ __forceinline__ CodeScale() {
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-    asm volatile("mov.b32 %0, 0x34003400;" : "=r"(p[0]));
-    asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(p[1]));
-    asm volatile("mov.b32 %0, 0x24002400;" : "=r"(p[2]));
-    asm volatile("mov.b32 %0, 0x1C001C00;" : "=r"(p[3]));
-  }
-};
-// Code j of both halves of w as fp16 (exact): masked in place under the exponent of 2^10, where it stands for
-// 1024 + c 2^(b j), and scaled back by one FMA. Codes above the ten mantissa bits come from w shifted right.
-// CENTRE: what is taken off the code.
-template <int BITS, int CENTRE = 0>
-__device__ __forceinline__ __half2 code_h2(const CodeScale& cs, uint32_t w, int j) {
-  constexpr int kIn = (BITS == 2) ? 5 : 2;  // codes that fit in place
-  const int jj = j < kIn ? j : j - kIn, k = BITS * jj / 2;
-  uint32_t m;  // (w & mask) | magic
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-      : "=r"(m)
-      : "r"(j < kIn ? w : w >> (BITS * kIn)), "r"((((1u << BITS) - 1u) << (BITS * jj)) * 0x10001u), "r"(cs.magic));
-  if (k == 0) return __hadd2(as_h2(m), __float2half2_rn(-1024.f - CENTRE));
-  return __hfma2(as_h2(m), as_h2(cs.p[k - 1]), __float2half2_rn(-1024.f / (float)(1 << (2 * k)) - CENTRE));
-}
-// What a stored element is made of: X = s (c - z) = s (c - c0) - (s z - c0 s). With the middle code c0 the first part
-// is small and one fp16 (exact with 2 bits; with 4 off by 2^-11 of at most 8 s), however far the group lies from zero;
-// the second is one number per group and is never added to it in fp16.
-template <int BITS>
-constexpr int kCentre = BITS == 2 ? 1 : 8;
-// what the rounding of p = fp16(x y) left, exactly
-__device__ __forceinline__ uint32_t product_rest(uint32_t x, uint32_t y, uint32_t p) {
-  return as_u(__hfma2(as_h2(x), as_h2(y), __hneg2(as_h2(p))));
-}
-__device__ __forceinline__ uint32_t halved(uint32_t x) { return as_u(__hmul2(as_h2(x), __float2half2_rn(0.5f))); }
-// s (c - c0) of eight codes (VB == 2: the low half of w), natural order
-template <int VB>
-__device__ __forceinline__ uint4 centred8(const CodeScale& cs, uint32_t w, __half2 s) {
-  if constexpr (VB == 2) w = __byte_perm(w, 0, 0x4140);  // codes 0 .. 3 and 4 .. 7 in the two halves
-  uint32_t x[4];  // codes j, j + 4
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = as_u(__hmul2(code_h2<VB, kCentre<VB>>(cs, w, j), s));
-  return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
-                    __byte_perm(x[2], x[3], 0x7632));
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void cp_async16(unsigned char* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -316,43 +188,6 @@ __device__ __forceinline__ void prefetch_fp16(const KiviTreeArgs& a, const TreeL
     bulk_prefetch_l2(a.v_resid + (bh * R + r) * kD, first * kD * 2);
     if (first < t1 - tv) bulk_prefetch_l2(a.v_resid + bh * R * kD, (t1 - tv - first) * kD * 2);
   }
-}
-
-// A query row as fp16 times a power of two that puts its largest magnitude in [2^TOP, 2^(TOP + 1)): eight lanes, 16
-// channels each (w: bf16 pairs; o: fp16 pairs). Returns what a score has to be multiplied with (scale: log2 units).
-template <int TOP>
-__device__ __forceinline__ float query_fp16(const uint32_t (&w)[8], uint32_t (&o)[8], float scale) {
-  float mx = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-#pragma unroll
-  for (int off = 4; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-  const int ex = (int)(__float_as_uint(mx) >> 23);  // biased exponent; 0: zero or subnormal, 255: not finite
-  // times 2^(TOP - (ex - 127)) in two factors, since the power may pass the fp32 range
-  const int sh = (ex == 0 || ex == 255) ? 0 : TOP + 127 - ex;
-  const float f1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 y = __fmul2_rn(__fmul2_rn(make_float2(bf16_lo(w[e]), bf16_hi(w[e])), make_float2(f1, f1)), make_float2(f2, f2));
-    o[e] = pack_h2(y.x, y.y);
-  }
-  return scale / f1 / f2;
-}
-// 16 channels 16c .. of query row `row` of (b, KV head h), zero for padding
-__device__ __forceinline__ bool load_query(const KiviTreeArgs& a, const TreeLens& len, int b, int h, int row, int c,
-                                           uint32_t (&w)[8]) {
-  const int di = div_by(row, a.rep);
-  const bool real = row < a.N * a.rep.d && di < len.nr;
-  uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (real) {
-    const uint4* src = reinterpret_cast<const uint4*>(
-        a.q + (((size_t)b * a.N + di) * a.Hq + (size_t)h * a.rep.d + row - di * a.rep.d) * kD + 16 * c);
-    u[0] = __ldg(src);
-    u[1] = __ldg(src + 1);
-  }
-  w[0] = u[0].x; w[1] = u[0].y; w[2] = u[0].z; w[3] = u[0].w;
-  w[4] = u[1].x; w[5] = u[1].y; w[6] = u[1].z; w[7] = u[1].w;
-  return real;
 }
 
 // ======================================================================================
@@ -1118,73 +953,6 @@ struct TreeLayout {
   static_assert(kSmem <= 232448 / 2 - 1024, "two blocks per SM");
 };
 
-// shared-memory matrix descriptor, no swizzle. K-major: lbo steps 8 elements along K, sbo 8 rows;
-// MN-major: lbo steps 8 along K, sbo 8 along N
-__device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
-}
-// instruction descriptor, kind::f16: fp32 D, fp16 A (K-major) and B, M = 128
-__host__ __device__ constexpr uint32_t tree_idesc(int n, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tree_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// eight consecutive fp32 columns of this thread's TMEM lane (valid after tmem_wait_ld)
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr)
-               : "memory");
-}
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
-  tmem_wait_ld();
-  return __uint_as_float(r);
-}
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-               : "memory");
-}
-
-// the largest of the lanes' values that are numbers
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
-  return r;
-}
 // ---- keys of a tile. A lane takes token lane % 8 of an octet and a code word (2 bits: 16 channels, 4 bits: 8);
 //      a warp one key group and half of the words, so a lane unpacks four tokens per scale. Groups behind the
 //      quantized keys are fp16 rows.

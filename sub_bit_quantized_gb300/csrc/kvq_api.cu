@@ -773,7 +773,7 @@ struct PrefixPlan {
 static PrefixPlan plan_prefix(const kvq_kivi_cfg* c, const kvq_kivi_cfg* pc, int B, int N) {
   PrefixPlan p;
   const size_t rows = (size_t)B * N * c->n_q_heads;
-  p.prefix = align256(kvq::kivi_tree_ws_bytes(1, B * N, c->n_heads, c->n_q_heads, pc->k_bits, pc->v_bits));
+  p.prefix = align256(kvq::kivi_prefix_ws_bytes(B * N, c->n_heads, c->n_q_heads, pc->k_bits, pc->v_bits));
   p.own = align256(kvq::kivi_tree_ws_bytes(B, N, c->n_heads, c->n_q_heads, c->k_bits, c->v_bits));
   p.out = align256(rows * kvq::kD * sizeof(float));
   p.lse = align256(rows * sizeof(float));
@@ -793,7 +793,7 @@ static kvq_status check_prefix_cfgs(const kvq_kivi_cfg* c, const kvq_kivi_cfg* p
   if (N > 64) return fail(KVQ_ERR_UNSUPPORTED, "%s: N=%d (a request has at most 64 rows a head)", fn, N);
   if ((long long)B * N * c->n_q_heads >= (1ll << 31) ||
       kvq::kivi_tree_positions(B, N, c->n_heads, c->n_q_heads, c->max_tokens, c->residual) >= (1ll << 31) ||
-      kvq::kivi_tree_positions(1, B * N, c->n_heads, c->n_q_heads, pc->max_tokens, pc->residual) >= (1ll << 31))
+      kvq::kivi_prefix_positions(B * N, c->n_heads, c->n_q_heads, pc->max_tokens, pc->residual) >= (1ll << 31))
     return fail(KVQ_ERR_UNSUPPORTED, "%s: too many tokens and query rows for one call", fn);
   return KVQ_OK;
 }

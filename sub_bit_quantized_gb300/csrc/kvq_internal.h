@@ -255,6 +255,10 @@ struct KiviPrefixArgs {
   void* out; int out_fp32;         // [B][N][Hq][D]
   IntDiv heads, tokens;            // set by the launch: query heads, tokens a request
 };
+// workspace bytes, and tile positions (below 2^31: checked by the host), of the pass over the prefix with `rows` rows a
+// query head
+size_t kivi_prefix_ws_bytes(int rows, int H, int Hq, int k_bits, int v_bits);
+long long kivi_prefix_positions(int rows, int H, int Hq, int max_tokens, int residual);
 cudaError_t launch_kivi_prefix(const KiviPrefixArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- slots of a cache
