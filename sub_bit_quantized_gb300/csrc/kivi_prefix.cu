@@ -27,12 +27,12 @@ namespace {
 // The constants enter as further tokens and channels of the same two products, so what a group lies off
 // from zero is never rounded to fp16 (as in the tree kernels). 96 tokens: 2 (112 + 144) fp32 columns are
 // the 512 of TMEM.
-// Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 11 unpack codes into two stages of
-// shared memory, warp 12 issues the products. A row's maximum moves only when a score passes it by
+// Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 11 unpack keys and 12 - 14 values into
+// two stages of shared memory, warp 15 issues the products. A row's maximum moves only when a score passes it by
 // 2^kSlack, so rescaling O is rare and left to the softmax warps.
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;
 constexpr uint32_t kColS = 112, kColO = 144;     // TMEM columns of S and of O
 constexpr int kVSbo = kTok * 16 + 16;            // V': from eight channels to the next (+ 16: other banks)
 
@@ -64,15 +64,15 @@ __device__ __forceinline__ PrefixPlace prefix_place(const KiviTreeArgs& a, const
   return x;
 }
 
-// ---- keys of a tile, by four warps: warp w takes channels 32 w .. + 31 of every token. A lane takes token lane % 8
-//      of an octet and a code word (2 bits: 16 channels, two octets; 4 bits: 8 channels, four octets). ----
+// ---- keys of a 32-token group, by four warps: warp w takes channels 32 w .. + 31 of every token. A lane takes token
+//      lane % 8 of an octet and a code word (2 bits: 16 channels, two octets; 4 bits: 8 channels, four octets). ----
 template <int KB>
 struct KeyRegs {
   static constexpr int kOct = KB == 2 ? 2 : 4;
-  uint32_t code[kGroups][kOct];
-  uint4 scale[kGroups][KB == 2 ? 2 : 1];  // of the lane's word
-  uint2 four[kGroups];                    // of channels 4 lane .., for the group's largest
-  uint32_t cs[2], cz[2];                  // scales and zeros of the constants the lane makes (group w)
+  uint32_t code[kOct];
+  uint4 scale[KB == 2 ? 2 : 1];           // of the lane's word
+  uint2 four;                             // of channels 4 lane .., for the group's largest
+  uint32_t cs[2], cz[2];                  // scales and zeros of the constants the lane makes (one warp of the four)
 };
 template <int KB>
 struct KeyLane {
@@ -88,178 +88,159 @@ struct KeyLane {
     return 16 * (lane >> 2) + (KB == 2 ? 2 * j : 8 * (j >> 1) + 2 * (j & 1));
   }
 };
+// t: the group's first token; g: its place in the tile
 template <int KB>
-__device__ __forceinline__ void load_keys(const KiviTreeArgs& a, const TreeLens& len, int h, int t0, const KeyLane<KB>& l,
+__device__ __forceinline__ void load_keys(const KiviTreeArgs& a, const TreeLens& len, int h, int t, int g, const KeyLane<KB>& l,
                                           KeyRegs<KB>& r) {
+  if (t >= len.nqk) return;
   constexpr int kRow = kD * KB / 8;
-  const size_t tok = (size_t)h * a.max_tokens + t0;
-  const uint8_t* codes = a.k_codes + tok * kRow + 4 * l.word;
-  const uint16_t* scale = a.k_scale + tok / kGroupT * kD;
+  const size_t tok = (size_t)h * a.max_tokens + t, grp = tok / kGroupT * kD;
+  const uint8_t* codes = a.k_codes + (tok + 8 * l.oct + (l.lane & 7)) * kRow + 4 * l.word;
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    if (t0 + 32 * g >= len.nqk) continue;
-#pragma unroll
-    for (int i = 0; i < KeyRegs<KB>::kOct; ++i)
-      r.code[g][i] = __ldg(reinterpret_cast<const uint32_t*>(codes + (size_t)(32 * g + 8 * (l.oct + i) + (l.lane & 7)) * kRow));
-    const uint4* sp = reinterpret_cast<const uint4*>(scale + g * kD + (KB == 2 ? 16 : 8) * l.word);
-    r.scale[g][0] = __ldg(sp);
-    if constexpr (KB == 2) r.scale[g][1] = __ldg(sp + 1);
-    r.four[g] = __ldg(reinterpret_cast<const uint2*>(scale + g * kD) + l.lane);
-  }
-  if (l.w < kGroups && t0 + 32 * l.w < len.nqk) {
-    const size_t at = (tok / kGroupT + l.w) * kD + l.ch();
+  for (int i = 0; i < KeyRegs<KB>::kOct; ++i) r.code[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + 8 * i * kRow));
+  const uint4* sp = reinterpret_cast<const uint4*>(a.k_scale + grp + (KB == 2 ? 16 : 8) * l.word);
+  r.scale[0] = __ldg(sp);
+  if constexpr (KB == 2) r.scale[1] = __ldg(sp + 1);
+  r.four = __ldg(reinterpret_cast<const uint2*>(a.k_scale + grp) + l.lane);
+  if (l.w == g) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      r.cs[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scale + at + i * l.kTo));
-      r.cz[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_zero + at + i * l.kTo));
+      r.cs[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scale + grp + l.ch() + i * l.kTo));
+      r.cz[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_zero + grp + l.ch() + i * l.kTo));
     }
   }
 }
 template <int KB>
-__device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t0,
+__device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int g,
                                            const KeyLane<KB>& l, const KeyRegs<KB>& r, unsigned char* dst,
                                            unsigned char* rest, float* unit) {
   constexpr int kPairs = KB == 2 ? 8 : 4;
-  const int at0 = l.word * (kPairs * 32) + (l.lane & 7) * 16;
+  const int at0 = (4 * g + l.oct) * 2048 + l.word * (kPairs * 32) + (l.lane & 7) * 16;
+  unsigned char* cdst = dst + kTok * kD * 2 + 2 * (l.lane >> 2) * 128 + ((l.lane & 3) >> 1) * 128 + 2 * g * 16 + (l.lane & 1) * 8;
+  if (t < len.nqk) {
+    const __half2 most2 = __hmax2(__habs2(as_h2(r.four.x)), __habs2(as_h2(r.four.y)));
+    const int e = 26 - (int)(__reduce_max_sync(0xFFFFFFFFu, max(as_u(most2) & 0xFFFFu, as_u(most2) >> 16)) >> 10);  // -5 .. 26
+    if (l.w == g) {
+      float2 y[2];
+      const float2 sa = __half22float2(as_h2(r.cs[0])), sb = __half22float2(as_h2(r.cs[1]));
+      const float2 za = __half22float2(as_h2(r.cz[0])), zb = __half22float2(as_h2(r.cz[1]));
+      constexpr float c0 = kCentre<KB>;
+      y[0] = make_float2(sa.x * (za.x - c0), sb.x * (zb.x - c0));
+      y[1] = make_float2(sa.y * (za.y - c0), sb.y * (zb.y - c0));
+      const float most = fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fabsf(y[1].x), fabsf(y[1].y)));
+      // the largest in [2^13, 2^14)
+      const int top = (int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)) >> 23), sh = min(140 - top, 64);
+      const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+      uint32_t hi[2], lo[2];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    unsigned char* cdst = dst + kTok * kD * 2 + 2 * (l.lane >> 2) * 128 + ((l.lane & 3) >> 1) * 128 + 2 * g * 16 + (l.lane & 1) * 8;
-    if (t0 + 32 * g < len.nqk) {
-      const __half2 t = __hmax2(__habs2(as_h2(r.four[g].x)), __habs2(as_h2(r.four[g].y)));
-      const int e = 26 - (int)(__reduce_max_sync(0xFFFFFFFFu, max(as_u(t) & 0xFFFFu, as_u(t) >> 16)) >> 10);  // -5 .. 26
-      if (l.w == g) {
-        float2 y[2];
-        const float2 sa = __half22float2(as_h2(r.cs[0])), sb = __half22float2(as_h2(r.cs[1]));
-        const float2 za = __half22float2(as_h2(r.cz[0])), zb = __half22float2(as_h2(r.cz[1]));
-        constexpr float c0 = kCentre<KB>;
-        y[0] = make_float2(sa.x * (za.x - c0), sb.x * (zb.x - c0));
-        y[1] = make_float2(sa.y * (za.y - c0), sb.y * (zb.y - c0));
-        const float most = fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fabsf(y[1].x), fabsf(y[1].y)));
-        // the largest in [2^13, 2^14)
-        const int top = (int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)) >> 23), sh = min(140 - top, 64);
-        const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          y[i] = __fmul2_rn(y[i], make_float2(f, f));
-          hi[i] = pack_h2(y[i].x, y[i].y);
-          const float2 back = __half22float2(as_h2(hi[i]));
-          lo[i] = pack_h2(y[i].x - back.x, y[i].y - back.y);
-        }
-        *reinterpret_cast<uint2*>(cdst) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(cdst + 16) = make_uint2(lo[0], lo[1]);
-        if (l.lane == 0) {
-          unit[g] = __uint_as_float((uint32_t)(127 - e) << 23);
-          unit[4 + g] = __uint_as_float((uint32_t)(127 - sh) << 23);
-        }
+      for (int i = 0; i < 2; ++i) {
+        y[i] = __fmul2_rn(y[i], make_float2(f, f));
+        hi[i] = pack_h2(y[i].x, y[i].y);
+        const float2 back = __half22float2(as_h2(hi[i]));
+        lo[i] = pack_h2(y[i].x - back.x, y[i].y - back.y);
       }
-      // the scales times the power of two that puts the group's largest in [2^11, 2^12)
-      const __half2 f0 = as_h2((uint32_t)(min(e, 15) + 15) * 0x4000400u), f1 = as_h2((uint32_t)(max(e, 15)) * 0x4000400u);
-      __half2 s[kPairs];
-      uint4 s0, s1;
-      pair_order<KB>(r.scale[g][0], r.scale[g][KB == 2 ? 1 : 0], s0, s1);
-      const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(as_h2(sw[j]), f0);
-      if (e > 15) {  // the rest of a power past the largest fp16 one
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(s[j], f1);
+      *reinterpret_cast<uint2*>(cdst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(cdst + 16) = make_uint2(lo[0], lo[1]);
+      if (l.lane == 0) {
+        unit[g] = __uint_as_float((uint32_t)(127 - e) << 23);
+        unit[4 + g] = __uint_as_float((uint32_t)(127 - sh) << 23);
       }
+    }
+    // the scales times the power of two that puts the group's largest in [2^11, 2^12)
+    const __half2 f0 = as_h2((uint32_t)(min(e, 15) + 15) * 0x4000400u), f1 = as_h2((uint32_t)(max(e, 15)) * 0x4000400u);
+    __half2 s[kPairs];
+    uint4 s0, s1;
+    pair_order<KB>(r.scale[0], r.scale[KB == 2 ? 1 : 0], s0, s1);
+    const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-      for (int i = 0; i < KeyRegs<KB>::kOct; ++i) {
-        uint32_t x[kPairs], y[kPairs];
+    for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(as_h2(sw[j]), f0);
+    if (e > 15) {  // the rest of a power past the largest fp16 one
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          const __half2 c = code_h2<KB, kCentre<KB>>(cs0, r.code[g][i], j);
-          x[j] = as_u(__hmul2(c, s[j]));
-          if constexpr (KB == 4) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
-        }
-        const int at = (4 * g + l.oct + i) * 2048 + at0;
-        *reinterpret_cast<uint4*>(dst + at) = make_uint4(x[0], x[1], x[2], x[3]);
-        if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + at + 128) = make_uint4(x[4], x[5], x[6], x[7]);
-        else *reinterpret_cast<uint4*>(rest + at) = make_uint4(y[0], y[1], y[2], y[3]);
-      }
-    } else {  // fp16 rows, or none
-      if (l.w == g) {
-        *reinterpret_cast<uint2*>(cdst) = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(cdst + 16) = make_uint2(0u, 0u);
-        if (l.lane == 0) unit[g] = unit[4 + g] = 1.f;
-      }
+      for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(s[j], f1);
+    }
 #pragma unroll
-      for (int i = 0; i < KeyRegs<KB>::kOct; ++i) {
-        const uint16_t* row = fp16_key(a, len, 0, h, t0 + 32 * g + 8 * (l.oct + i) + (l.lane & 7));
-        const int at = (4 * g + l.oct + i) * 2048 + at0;
-        uint4 x0, x1;
-        if constexpr (KB == 2) {
-          pair_order<2>(row8(row, 2 * l.word), row8(row, 2 * l.word + 1), x0, x1);
-          *reinterpret_cast<uint4*>(dst + at + 128) = x1;
-        } else {
-          const uint4 v = row8(row, l.word);
-          pair_order<4>(v, v, x0, x1);
-          *reinterpret_cast<uint4*>(rest + at) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        *reinterpret_cast<uint4*>(dst + at) = x0;
+    for (int i = 0; i < KeyRegs<KB>::kOct; ++i) {
+      uint32_t x[kPairs], y[kPairs];
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const __half2 c = code_h2<KB, kCentre<KB>>(cs0, r.code[i], j);
+        x[j] = as_u(__hmul2(c, s[j]));
+        if constexpr (KB == 4) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
       }
+      *reinterpret_cast<uint4*>(dst + at0 + 2048 * i) = make_uint4(x[0], x[1], x[2], x[3]);
+      if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + at0 + 2048 * i + 128) = make_uint4(x[4], x[5], x[6], x[7]);
+      else *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  } else {  // fp16 rows, or none
+    if (l.w == g) {
+      *reinterpret_cast<uint2*>(cdst) = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(cdst + 16) = make_uint2(0u, 0u);
+      if (l.lane == 0) unit[g] = unit[4 + g] = 1.f;
+    }
+#pragma unroll 1
+    for (int i = 0; i < KeyRegs<KB>::kOct; ++i) {
+      const uint16_t* row = fp16_key(a, len, 0, h, t + 8 * (l.oct + i) + (l.lane & 7));
+      uint4 x0, x1;
+      if constexpr (KB == 2) {
+        pair_order<2>(row8(row, 2 * l.word), row8(row, 2 * l.word + 1), x0, x1);
+        *reinterpret_cast<uint4*>(dst + at0 + 2048 * i + 128) = x1;
+      } else {
+        const uint4 v = row8(row, l.word);
+        pair_order<4>(v, v, x0, x1);
+        *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      *reinterpret_cast<uint4*>(dst + at0 + 2048 * i) = x0;
     }
   }
 }
 
-// ---- values of a tile, by four warps: warp w takes value group w (32 channels) of every token, a lane a token ----
+// ---- values of 32 tokens and a value group w (32 channels), by one warp: a lane a token ----
 template <int VB>
 struct ValueRegs {
-  uint32_t code[kGroups][VB];
-  uint16_t s[kGroups], z[kGroups];
+  uint32_t code[VB];
+  uint16_t s, z;
 };
 template <int VB>
-__device__ __forceinline__ void load_values(const KiviTreeArgs& a, const TreeLens& len, int h, int t0, int w, int lane,
-                                            ValueRegs<VB>& r) {
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const int t = t0 + 32 * g + lane;
-    if (t >= len.nqv) continue;
-    const size_t tok = (size_t)h * a.max_tokens + t;
-    const uint8_t* src = a.v_codes + tok * (kD * VB / 8) + 4 * VB * w;
-    if constexpr (VB == 2) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-      r.code[g][0] = u.x; r.code[g][1] = u.y;
-    } else {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
-      r.code[g][0] = u.x; r.code[g][1] = u.y; r.code[g][2] = u.z; r.code[g][3] = u.w;
-    }
-    r.s[g] = __ldg(a.v_scale + tok * (kD / kGroupT) + w);
-    r.z[g] = __ldg(a.v_zero + tok * (kD / kGroupT) + w);
+__device__ __forceinline__ void load_values(const KiviTreeArgs& a, const TreeLens& len, int h, int t, int w, ValueRegs<VB>& r) {
+  if (t >= len.nqv) return;
+  const size_t tok = (size_t)h * a.max_tokens + t;
+  const uint8_t* src = a.v_codes + tok * (kD * VB / 8) + 4 * VB * w;
+  if constexpr (VB == 2) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+    r.code[0] = u.x; r.code[1] = u.y;
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+    r.code[0] = u.x; r.code[1] = u.y; r.code[2] = u.z; r.code[3] = u.w;
   }
+  r.s = __ldg(a.v_scale + tok * (kD / kGroupT) + w);
+  r.z = __ldg(a.v_zero + tok * (kD / kGroupT) + w);
 }
+// t: the lane's token; dst: its place in V'
 template <int VB>
-__device__ __forceinline__ void store_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t0,
-                                             int w, int lane, const ValueRegs<VB>& r, unsigned char* dst0) {
+__device__ __forceinline__ void store_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int w,
+                                             const ValueRegs<VB>& r, unsigned char* dst) {
+  // columns of the constants: s z, what its rounding left, c0 s (all halved as the values), 1
+  uint2 c = make_uint2(0u, 0x3C000000u);
+  if (t < len.nqv) {
+    const __half2 s2 = as_h2(halved(r.s * 0x10001u));
+    const uint32_t p = as_u(__hmul2(s2, as_h2(r.z * 0x10001u))), left = product_rest(as_u(s2), r.z * 0x10001u, p);
+    c.x = (p & 0xFFFFu) | (left << 16);
+    c.y |= as_u(__hmul2(s2, __float2half2_rn(kCentre<VB>))) & 0xFFFFu;
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const int t = t0 + 32 * g + lane;
-    unsigned char* dst = dst0 + (32 * g + lane) * 16;
-    // columns of the constants: s z, what its rounding left, c0 s (all halved as the values), 1
-    uint2 c = make_uint2(0u, 0x3C000000u);
-    if (t < len.nqv) {
-      const __half2 s2 = as_h2(halved(r.s[g] * 0x10001u));
-      const uint32_t p = as_u(__hmul2(s2, as_h2(r.z[g] * 0x10001u))), left = product_rest(as_u(s2), r.z[g] * 0x10001u, p);
-      c.x = (p & 0xFFFFu) | (left << 16);
-      c.y |= as_u(__hmul2(s2, __float2half2_rn(kCentre<VB>))) & 0xFFFFu;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t word = VB == 4 ? r.code[g][i & (VB - 1)] : r.code[g][i >> 1] >> (16 * (i & 1));
-        *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = centred8<VB>(cs0, word, s2);
-      }
-    } else {
-      const uint16_t* row = nullptr;
-      if (t < len.n) row = fp16_value(a, len, 0, h, t, t - div_by(t, a.ring) * a.residual);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = row8(row, 4 * w + i);
-        *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = make_uint4(halved(v.x), halved(v.y), halved(v.z), halved(v.w));
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t word = VB == 4 ? r.code[i & (VB - 1)] : r.code[i >> 1] >> (16 * (i & 1));
+      *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = centred8<VB>(cs0, word, s2);
     }
-    *reinterpret_cast<uint2*>(dst + (16 + (w >> 1)) * kVSbo + (w & 1) * 8) = c;
+  } else {
+    const uint16_t* row = nullptr;
+    if (t < len.n) row = fp16_value(a, len, 0, h, t, t - div_by(t, a.ring) * a.residual);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = row8(row, 4 * w + i);
+      *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = make_uint4(halved(v.x), halved(v.y), halved(v.z), halved(v.w));
+    }
   }
+  *reinterpret_cast<uint2*>(dst + (16 + (w >> 1)) * kVSbo + (w & 1) * 8) = c;
 }
 
 // the stored part of a tile into L2, by one thread
@@ -300,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   const PrefixPlace at = prefix_place(a, len, blockIdx.x);
   if (at.p0 >= at.p1) return;
   const int rows_all = a.N * a.rep.d;
-  if (warp == 12) {
+  if (warp == 15) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -313,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       mbar_init(bar_o + i, 1);
       mbar_init(k_full + i, 128);
       mbar_init(k_empty + i, 1);
-      mbar_init(v_full + i, 128);
+      mbar_init(v_full + i, 32 * kGroups);
       mbar_init(v_empty + i, 1);
     }
     *failed = 0;
@@ -325,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   const uint32_t tmem = *tmem_slot;
   // a wait that runs out ends its role, and with it the waits of the others
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_wait_bounded(bar, parity & 1)) return true;
+    if (mbar_wait_bounded_sleep(bar, parity & 1)) return true;
     *failed = 1;
     set_error(a.err, KVQ_ERR_TIMEOUT);
     return false;
@@ -395,9 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
             if (2 * i + 1 >= there) x[i].y = -INFINITY;
           }
         }
-        float mx = -INFINITY;
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kTok / 2; ++i) mx = fmaxf(mx, fmaxf(x[i].x, x[i].y));
+        for (int i = 0; i < kTok / 2; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(x[i].x, x[i].y));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const bool up = mx + nm > kSlack + kRaise;
         if (__any_sync(0xFFFFFFFFu, up)) {
           const float f = up ? exp2_approx((kRaise - mx) - nm) : 1.f;
@@ -479,42 +461,71 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       }
     }
   } else if (warp < 12) {
-    // ================= unpacking =================
-    const int w = warp - 8;
+    // ================= keys: four warps, the next group on its way meanwhile =================
     const CodeScale cs0;
-    const KeyLane<KB> kl(w, lane);
-    KeyRegs<KB> kr;
-    ValueRegs<VB> vr;
+    const KeyLane<KB> kl(warp & 3, lane);
+    KeyRegs<KB> now, next;
     int h = div_by(seg, a.row_tiles);
-    load_keys<KB>(a, len, h, tile * kTok, kl, kr);
-    load_values<VB>(a, len, h, tile * kTok, w, lane, vr);
     // the place kAhead tiles on, whose stored part is fetched into L2
     constexpr int kAhead = 4;
-    for (int p = at.p0; p < at.p1; ++p) {
-      const int it = p - at.p0, st = it & 1;
-      if (w == 0 && lane == 0 && p + kAhead < at.p1) {
-        const int far = p + kAhead, fseg = far / at.T;
-        prefetch_tile<KB, VB>(a, len, div_by(fseg, a.row_tiles), (far - fseg * at.T) * kTok);
+    auto fetch = [&](int p) {
+      if (p >= at.p1) return;
+      const int fseg = p / at.T;
+      prefetch_tile<KB, VB>(a, len, div_by(fseg, a.row_tiles), (p - fseg * at.T) * kTok);
+    };
+    load_keys<KB>(a, len, h, tile * kTok, 0, kl, now);
+    int g = 0, p = at.p0;
+#pragma unroll 1
+    while (p < at.p1) {
+      const int it = p - at.p0, st = it & 1, t = tile * kTok + g * kGroupT, h0 = h, g0 = g;
+      if (g == 0) {
+        if (warp == 8 && lane == 0) fetch(p + kAhead);
+        if (it >= 2 && !wait_warp(k_empty + st, (it >> 1) + 1)) break;
       }
-      int nseg = seg, ntile = tile + 1;
-      if (ntile == at.T) {
-        ntile = 0;
-        ++nseg;
+      if (++g == kGroups) {
+        g = 0;
+        ++p;
+        if (++tile == at.T) {
+          tile = 0;
+          h = div_by(++seg, a.row_tiles);
+        }
       }
-      const int nh = div_by(nseg, a.row_tiles);
-      if (it >= 2 && !wait_warp(k_empty + st, (it >> 1) + 1)) break;
-      store_keys<KB>(cs0, a, len, h, tile * kTok, kl, kr, sm + L::kOffK + st * L::kK, sm + L::kOffKr + st * L::kKr, unit + (p & 3) * 8);
-      fence_proxy_async_smem();
-      mbar_arrive(k_full + st);
-      if (p + 1 < at.p1) load_keys<KB>(a, len, nh, ntile * kTok, kl, kr);
-      if (it >= 2 && !wait_warp(v_empty + st, (it >> 1) + 1)) break;
-      store_values<VB>(cs0, a, len, h, tile * kTok, w, lane, vr, sm + L::kOffV + st * L::kV);
-      fence_proxy_async_smem();
-      mbar_arrive(v_full + st);
-      if (p + 1 < at.p1) load_values<VB>(a, len, nh, ntile * kTok, w, lane, vr);
-      seg = nseg;
-      tile = ntile;
-      h = nh;
+      if (p < at.p1) load_keys<KB>(a, len, h, tile * kTok + g * kGroupT, g, kl, next);
+      store_keys<KB>(cs0, a, len, h0, t, g0, kl, now, sm + L::kOffK + st * L::kK, sm + L::kOffKr + st * L::kKr,
+                     unit + ((at.p0 + it) & 3) * 8);
+      if (g == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive(k_full + st);
+      }
+      now = next;
+    }
+  } else if (warp < 12 + kGroups) {
+    // ================= values: a warp a 32-token group, one value group after the other =================
+    const CodeScale cs0;
+    ValueRegs<VB> now, next;
+    int h = div_by(seg, a.row_tiles);
+    const int lt = 32 * (warp - 12) + lane;  // the lane's token of the tile
+    load_values<VB>(a, len, h, tile * kTok + lt, 0, now);
+    int w = 0, p = at.p0;
+#pragma unroll 1
+    while (p < at.p1) {
+      const int it = p - at.p0, st = it & 1, t = tile * kTok + lt, h0 = h, w0 = w;
+      if (w == 0 && it >= 2 && !wait_warp(v_empty + st, (it >> 1) + 1)) break;
+      if (++w == 4) {
+        w = 0;
+        ++p;
+        if (++tile == at.T) {
+          tile = 0;
+          h = div_by(++seg, a.row_tiles);
+        }
+      }
+      if (p < at.p1) load_values<VB>(a, len, h, tile * kTok + lt, w, next);
+      store_values<VB>(cs0, a, len, h0, t, w0, now, sm + L::kOffV + st * L::kV + lt * 16);
+      if (w == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive(v_full + st);
+      }
+      now = next;
     }
   } else if (lane == 0) {
     // ================= products =================
@@ -583,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   __syncwarp();
   tmem_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 15) {
     tmem_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
