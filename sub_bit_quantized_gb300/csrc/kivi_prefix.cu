@@ -34,18 +34,25 @@ constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
 constexpr int kThreads = 512;
 constexpr uint32_t kColS = 112, kColO = 144;     // TMEM columns of S and of O
-constexpr int kVSbo = kTok * 16 + 16;            // V': from eight channels to the next (+ 16: other banks)
+constexpr int kVSbo = kGroupT * 16 + 16;         // V' of a group: from eight channels to the next (+ 16: other banks)
+constexpr int kVRing = 4, kStages = 3;           // groups: unpacked values; stored keys, and values, on their way
 
-template <int KB>
+template <int KB, int VB>
 struct PrefixLayout {
-  static constexpr int kK = (kTok + 16) * kD * 2, kKr = KB == 4 ? kTok * kD * 2 : 0, kV = (18 * kVSbo + 127) / 128 * 128;
+  // a group's stored keys or values: codes, scales, zero-points
+  static constexpr int kKCode = kGroupT * kD * KB / 8, kVCode = kGroupT * kD * VB / 8, kPart = kD * 2;
+  static constexpr int kKStage = kKCode + 2 * kPart, kVStage = kVCode + 2 * kPart;
+  static constexpr int kK = (kTok + 16) * kD * 2, kKr = KB == 4 ? kTok * kD * 2 : 0, kV = 18 * kVSbo;
   static constexpr int kOffQ = 0;                          // fp16 [2][128 x 128], K-major
-  static constexpr int kOffK = kOffQ + 2 * 128 * kD * 2;   // [2 stages] K' (112 rows), K-major
-  static constexpr int kOffKr = kOffK + 2 * kK;            // [2 stages] second parts of the keys (4 bits)
-  static constexpr int kOffV = kOffKr + 2 * kKr;           // [2 stages] V', tokens within eight channels
-  static constexpr int kOffUnit = kOffV + 2 * kV;          // float [4][8]: what a group's sums count, constants' from 4
+  static constexpr int kOffK = kOffQ + 2 * 128 * kD * 2;   // [2] K' of a tile (112 rows), K-major
+  static constexpr int kOffKr = kOffK + 2 * kK;            // [2] second parts of the keys (4 bits)
+  static constexpr int kOffV = kOffKr + 2 * kKr;           // [kVRing] V' of a group, tokens within eight channels
+  static constexpr int kOffKs = kOffV + kVRing * kV;       // [kStages] stored keys of a group
+  static constexpr int kOffVs = kOffKs + kStages * kKStage;
+  static constexpr int kOffUnit = kOffVs + kStages * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
   static constexpr int kOffBar = kOffUnit + 4 * 8 * 4;
-  static constexpr int kSmem = kOffBar + 160;
+  static constexpr int kBars = 8 + 4 + 2 * kVRing + 4 * kStages;
+  static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
@@ -66,64 +73,30 @@ __device__ __forceinline__ PrefixPlace prefix_place(const KiviTreeArgs& a, const
 
 // ---- keys of a 32-token group, by four warps: warp w takes channels 32 w .. + 31 of every token. A lane takes token
 //      lane % 8 of an octet and a code word (2 bits: 16 channels, two octets; 4 bits: 8 channels, four octets). ----
+// t: the group's first token; g: its place in the tile; stage: what is stored of it
 template <int KB>
-struct KeyRegs {
-  static constexpr int kOct = KB == 2 ? 2 : 4;
-  uint32_t code[kOct];
-  uint4 scale[KB == 2 ? 2 : 1];           // of the lane's word
-  uint2 four;                             // of channels 4 lane .., for the group's largest
-  uint32_t cs[2], cz[2];                  // scales and zeros of the constants the lane makes (one warp of the four)
-};
-template <int KB>
-struct KeyLane {
-  int w, lane, word, oct;
-  __device__ __forceinline__ KeyLane(int w_, int lane_) : w(w_), lane(lane_) {
-    word = KB == 2 ? 2 * w + ((lane >> 3) & 1) : 4 * w + (lane >> 3);
-    oct = KB == 2 ? 2 * (lane >> 4) : 0;
-  }
-  // constants: the lane's pairs j, j + 1 of 16 channels, j = 2 (lane % 4), in pair order: channels ch, ch + 1, and kTo on
-  static constexpr int kTo = KB == 2 ? 8 : 4;
-  __device__ __forceinline__ int ch() const {
-    const int j = lane & 3;
-    return 16 * (lane >> 2) + (KB == 2 ? 2 * j : 8 * (j >> 1) + 2 * (j & 1));
-  }
-};
-// t: the group's first token; g: its place in the tile
-template <int KB>
-__device__ __forceinline__ void load_keys(const KiviTreeArgs& a, const TreeLens& len, int h, int t, int g, const KeyLane<KB>& l,
-                                          KeyRegs<KB>& r) {
-  if (t >= len.nqk) return;
-  constexpr int kRow = kD * KB / 8;
-  const size_t tok = (size_t)h * a.max_tokens + t, grp = tok / kGroupT * kD;
-  const uint8_t* codes = a.k_codes + (tok + 8 * l.oct + (l.lane & 7)) * kRow + 4 * l.word;
-#pragma unroll
-  for (int i = 0; i < KeyRegs<KB>::kOct; ++i) r.code[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + 8 * i * kRow));
-  const uint4* sp = reinterpret_cast<const uint4*>(a.k_scale + grp + (KB == 2 ? 16 : 8) * l.word);
-  r.scale[0] = __ldg(sp);
-  if constexpr (KB == 2) r.scale[1] = __ldg(sp + 1);
-  r.four = __ldg(reinterpret_cast<const uint2*>(a.k_scale + grp) + l.lane);
-  if (l.w == g) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      r.cs[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_scale + grp + l.ch() + i * l.kTo));
-      r.cz[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_zero + grp + l.ch() + i * l.kTo));
-    }
-  }
-}
-template <int KB>
-__device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int g,
-                                           const KeyLane<KB>& l, const KeyRegs<KB>& r, unsigned char* dst,
-                                           unsigned char* rest, float* unit) {
-  constexpr int kPairs = KB == 2 ? 8 : 4;
-  const int at0 = (4 * g + l.oct) * 2048 + l.word * (kPairs * 32) + (l.lane & 7) * 16;
-  unsigned char* cdst = dst + kTok * kD * 2 + 2 * (l.lane >> 2) * 128 + ((l.lane & 3) >> 1) * 128 + 2 * g * 16 + (l.lane & 1) * 8;
+__device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int g,
+                                            int w, int lane, const unsigned char* stage, unsigned char* dst, unsigned char* rest,
+                                            float* unit) {
+  constexpr int kPairs = KB == 2 ? 8 : 4, kOct = KB == 2 ? 2 : 4, kRow = kD * KB / 8;
+  const int word = KB == 2 ? 2 * w + ((lane >> 3) & 1) : 4 * w + (lane >> 3), oct = KB == 2 ? 2 * (lane >> 4) : 0;
+  const int at0 = (4 * g + oct) * 2048 + word * (kPairs * 32) + (lane & 7) * 16;
+  unsigned char* cdst = dst + kTok * kD * 2 + 2 * (lane >> 2) * 128 + ((lane & 3) >> 1) * 128 + 2 * g * 16 + (lane & 1) * 8;
   if (t < len.nqk) {
-    const __half2 most2 = __hmax2(__habs2(as_h2(r.four.x)), __habs2(as_h2(r.four.y)));
+    const unsigned char* scale = stage + kGroupT * kRow;
+    const uint2 four = *reinterpret_cast<const uint2*>(scale + 8 * lane);
+    const __half2 most2 = __hmax2(__habs2(as_h2(four.x)), __habs2(as_h2(four.y)));
     const int e = 26 - (int)(__reduce_max_sync(0xFFFFFFFFu, max(as_u(most2) & 0xFFFFu, as_u(most2) >> 16)) >> 10);  // -5 .. 26
-    if (l.w == g) {
+    if (w == g) {
+      // constants: the lane's pairs j, j + 1 of 16 channels, j = 2 (lane % 4), in pair order
+      const int j = lane & 3, ch = 16 * (lane >> 2) + (KB == 2 ? 2 * j : 8 * (j >> 1) + 2 * (j & 1));
+      constexpr int kTo = KB == 2 ? 8 : 4;  // channels of a pair are kTo apart
+      const unsigned char* zero = scale + kD * 2;
       float2 y[2];
-      const float2 sa = __half22float2(as_h2(r.cs[0])), sb = __half22float2(as_h2(r.cs[1]));
-      const float2 za = __half22float2(as_h2(r.cz[0])), zb = __half22float2(as_h2(r.cz[1]));
+      const float2 sa = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(scale + 2 * ch)));
+      const float2 sb = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(scale + 2 * (ch + kTo))));
+      const float2 za = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(zero + 2 * ch)));
+      const float2 zb = __half22float2(as_h2(*reinterpret_cast<const uint32_t*>(zero + 2 * (ch + kTo))));
       constexpr float c0 = kCentre<KB>;
       y[0] = make_float2(sa.x * (za.x - c0), sb.x * (zb.x - c0));
       y[1] = make_float2(sa.y * (za.y - c0), sb.y * (zb.y - c0));
@@ -141,7 +114,7 @@ __device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeA
       }
       *reinterpret_cast<uint2*>(cdst) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(cdst + 16) = make_uint2(lo[0], lo[1]);
-      if (l.lane == 0) {
+      if (lane == 0) {
         unit[g] = __uint_as_float((uint32_t)(127 - e) << 23);
         unit[4 + g] = __uint_as_float((uint32_t)(127 - sh) << 23);
       }
@@ -150,7 +123,8 @@ __device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeA
     const __half2 f0 = as_h2((uint32_t)(min(e, 15) + 15) * 0x4000400u), f1 = as_h2((uint32_t)(max(e, 15)) * 0x4000400u);
     __half2 s[kPairs];
     uint4 s0, s1;
-    pair_order<KB>(r.scale[0], r.scale[KB == 2 ? 1 : 0], s0, s1);
+    const uint4* sp = reinterpret_cast<const uint4*>(scale + 4 * kPairs * word);
+    pair_order<KB>(sp[0], sp[KB == 2 ? 1 : 0], s0, s1);
     const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(as_h2(sw[j]), f0);
@@ -158,12 +132,15 @@ __device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeA
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(s[j], f1);
     }
+    uint32_t code[kOct];
 #pragma unroll
-    for (int i = 0; i < KeyRegs<KB>::kOct; ++i) {
+    for (int i = 0; i < kOct; ++i) code[i] = *reinterpret_cast<const uint32_t*>(stage + (8 * (oct + i) + (lane & 7)) * kRow + 4 * word);
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
       uint32_t x[kPairs], y[kPairs];
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        const __half2 c = code_h2<KB, kCentre<KB>>(cs0, r.code[i], j);
+        const __half2 c = code_h2<KB, kCentre<KB>>(cs0, code[i], j);
         x[j] = as_u(__hmul2(c, s[j]));
         if constexpr (KB == 4) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
       }
@@ -172,20 +149,20 @@ __device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeA
       else *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   } else {  // fp16 rows, or none
-    if (l.w == g) {
+    if (w == g) {
       *reinterpret_cast<uint2*>(cdst) = make_uint2(0u, 0u);
       *reinterpret_cast<uint2*>(cdst + 16) = make_uint2(0u, 0u);
-      if (l.lane == 0) unit[g] = unit[4 + g] = 1.f;
+      if (lane == 0) unit[g] = unit[4 + g] = 1.f;
     }
 #pragma unroll 1
-    for (int i = 0; i < KeyRegs<KB>::kOct; ++i) {
-      const uint16_t* row = fp16_key(a, len, 0, h, t + 8 * (l.oct + i) + (l.lane & 7));
+    for (int i = 0; i < kOct; ++i) {
+      const uint16_t* row = fp16_key(a, len, 0, h, t + 8 * (oct + i) + (lane & 7));
       uint4 x0, x1;
       if constexpr (KB == 2) {
-        pair_order<2>(row8(row, 2 * l.word), row8(row, 2 * l.word + 1), x0, x1);
+        pair_order<2>(row8(row, 2 * word), row8(row, 2 * word + 1), x0, x1);
         *reinterpret_cast<uint4*>(dst + at0 + 2048 * i + 128) = x1;
       } else {
-        const uint4 v = row8(row, l.word);
+        const uint4 v = row8(row, word);
         pair_order<4>(v, v, x0, x1);
         *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -194,86 +171,114 @@ __device__ __forceinline__ void store_keys(const CodeScale& cs0, const KiviTreeA
   }
 }
 
-// ---- values of 32 tokens and a value group w (32 channels), by one warp: a lane a token ----
+// ---- values of a 32-token group, by one warp: a lane a token, one value group (32 channels) after the other ----
+// t: the group's first token; dst: its V'
 template <int VB>
-struct ValueRegs {
-  uint32_t code[VB];
-  uint16_t s, z;
-};
-template <int VB>
-__device__ __forceinline__ void load_values(const KiviTreeArgs& a, const TreeLens& len, int h, int t, int w, ValueRegs<VB>& r) {
-  if (t >= len.nqv) return;
-  const size_t tok = (size_t)h * a.max_tokens + t;
-  const uint8_t* src = a.v_codes + tok * (kD * VB / 8) + 4 * VB * w;
-  if constexpr (VB == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-    r.code[0] = u.x; r.code[1] = u.y;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
-    r.code[0] = u.x; r.code[1] = u.y; r.code[2] = u.z; r.code[3] = u.w;
-  }
-  r.s = __ldg(a.v_scale + tok * (kD / kGroupT) + w);
-  r.z = __ldg(a.v_zero + tok * (kD / kGroupT) + w);
-}
-// t: the lane's token; dst: its place in V'
-template <int VB>
-__device__ __forceinline__ void store_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int w,
-                                             const ValueRegs<VB>& r, unsigned char* dst) {
-  // columns of the constants: s z, what its rounding left, c0 s (all halved as the values), 1
-  uint2 c = make_uint2(0u, 0x3C000000u);
-  if (t < len.nqv) {
-    const __half2 s2 = as_h2(halved(r.s * 0x10001u));
-    const uint32_t p = as_u(__hmul2(s2, as_h2(r.z * 0x10001u))), left = product_rest(as_u(s2), r.z * 0x10001u, p);
-    c.x = (p & 0xFFFFu) | (left << 16);
-    c.y |= as_u(__hmul2(s2, __float2half2_rn(kCentre<VB>))) & 0xFFFFu;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t word = VB == 4 ? r.code[i & (VB - 1)] : r.code[i >> 1] >> (16 * (i & 1));
-      *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = centred8<VB>(cs0, word, s2);
-    }
-  } else {
-    const uint16_t* row = nullptr;
-    if (t < len.n) row = fp16_value(a, len, 0, h, t, t - div_by(t, a.ring) * a.residual);
+__device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int lane,
+                                              const unsigned char* stage, unsigned char* dst) {
+  constexpr int kRow = kD * VB / 8;
+  t += lane;
+  dst += lane * 16;
+  const bool stored = t < len.nqv;
+  const unsigned char* codes = stage + lane * kRow;
+  const uint16_t* scale = reinterpret_cast<const uint16_t*>(stage + kGroupT * kRow) + 4 * lane;
+  const uint16_t* row = nullptr;
+  if (!stored && t < len.n) row = fp16_value(a, len, 0, h, t, t - div_by(t, a.ring) * a.residual);
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = row8(row, 4 * w + i);
-      *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = make_uint4(halved(v.x), halved(v.y), halved(v.z), halved(v.w));
+  for (int w = 0; w < 4; ++w) {
+    // columns of the constants: s z, what its rounding left, c0 s (all halved as the values), 1
+    uint2 c = make_uint2(0u, 0x3C000000u);
+    if (stored) {
+      uint32_t word[4];
+      if constexpr (VB == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(codes + 8 * w);
+        word[0] = u.x; word[1] = u.x >> 16; word[2] = u.y; word[3] = u.y >> 16;
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(codes + 16 * w);
+        word[0] = u.x; word[1] = u.y; word[2] = u.z; word[3] = u.w;
+      }
+      const uint32_t z = scale[w + kGroupT * 4] * 0x10001u;
+      const __half2 s2 = as_h2(halved(scale[w] * 0x10001u));
+      const uint32_t p = as_u(__hmul2(s2, as_h2(z))), left = product_rest(as_u(s2), z, p);
+      c.x = (p & 0xFFFFu) | (left << 16);
+      c.y |= as_u(__hmul2(s2, __float2half2_rn(kCentre<VB>))) & 0xFFFFu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = centred8<VB>(cs0, word[i], s2);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = row8(row, 4 * w + i);
+        *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = make_uint4(halved(v.x), halved(v.y), halved(v.z), halved(v.w));
+      }
     }
+    *reinterpret_cast<uint2*>(dst + (16 + (w >> 1)) * kVSbo + (w & 1) * 8) = c;
   }
-  *reinterpret_cast<uint2*>(dst + (16 + (w >> 1)) * kVSbo + (w & 1) * 8) = c;
 }
 
-// the stored part of a tile into L2, by one thread
+// What is stored of a group into a stage, by one thread; with nothing to copy the barrier completes at once.
 template <int KB, int VB>
-__device__ __forceinline__ void prefetch_tile(const KiviTreeArgs& a, const TreeLens& len, int h, int t0) {
-  const size_t tok = (size_t)h * a.max_tokens + t0, g = tok / kGroupT * kD;
-  const int nk = min(kTok, len.nqk - t0), nv = (min(kTok, len.nqv - t0) + 1) & ~1;  // whole 16-byte pieces
-  if (nk > 0) {
-    bulk_prefetch_l2(a.k_codes + tok * (kD * KB / 8), nk * (kD * KB / 8));
-    bulk_prefetch_l2(a.k_scale + g, nk / kGroupT * kD * 2);
-    bulk_prefetch_l2(a.k_zero + g, nk / kGroupT * kD * 2);
+__device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens& len, int h, int t, unsigned char* stage, uint64_t* full) {
+  using L = PrefixLayout<KB, VB>;
+  if (t >= len.nqk) {
+    mbar_arrive(full);
+    return;
   }
-  if (nv > 0) {
-    bulk_prefetch_l2(a.v_codes + tok * (kD * VB / 8), nv * (kD * VB / 8));
-    bulk_prefetch_l2(a.v_scale + tok * (kD / kGroupT), nv * 8);
-    bulk_prefetch_l2(a.v_zero + tok * (kD / kGroupT), nv * 8);
-  }
+  const size_t tok = (size_t)h * a.max_tokens + t, g = tok / kGroupT * kD;
+  mbar_arrive_expect_tx(full, L::kKStage);
+  bulk_g2s(stage, a.k_codes + tok * (kD * KB / 8), L::kKCode, full);
+  bulk_g2s(stage + L::kKCode, a.k_scale + g, L::kPart, full);
+  bulk_g2s(stage + L::kKCode + L::kPart, a.k_zero + g, L::kPart, full);
 }
+template <int KB, int VB>
+__device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLens& len, int h, int t, unsigned char* stage, uint64_t* full) {
+  using L = PrefixLayout<KB, VB>;
+  if (t >= len.nqv) {
+    mbar_arrive(full);
+    return;
+  }
+  const size_t tok = (size_t)h * a.max_tokens + t;  // the rows behind n_quant_v are there, but not used
+  mbar_arrive_expect_tx(full, L::kVStage);
+  bulk_g2s(stage, a.v_codes + tok * (kD * VB / 8), L::kVCode, full);
+  bulk_g2s(stage + L::kVCode, a.v_scale + tok * (kD / kGroupT), L::kPart, full);
+  bulk_g2s(stage + L::kVCode + L::kPart, a.v_zero + tok * (kD / kGroupT), L::kPart, full);
+}
+
+// The groups of the block's share in order: group i of them, the g-th of tile p
+struct Groups {
+  int i, p, seg, tile, h, t, g;  // t: the group's first token
+  __device__ __forceinline__ Groups(const KiviTreeArgs& a, const PrefixPlace& at, int seg_, int tile_)
+      : i(0), p(at.p0), seg(seg_), tile(tile_), h(div_by(seg_, a.row_tiles)), t(tile_ * kTok), g(0) {}
+  __device__ __forceinline__ void next(const KiviTreeArgs& a, const PrefixPlace& at) {
+    ++i;
+    t += kGroupT;
+    if (++g < kGroups) return;
+    g = 0;
+    ++p;
+    if (++tile == at.T) {
+      tile = t = 0;
+      h = div_by(++seg, a.row_tiles);
+    }
+  }
+};
 
 template <int KB, int VB>
 __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTreeArgs a, const float scale_log2) {
-  using L = PrefixLayout<KB>;
+  using L = PrefixLayout<KB, VB>;
   extern __shared__ __align__(128) unsigned char sm[];
   float* unit = reinterpret_cast<float*>(sm + L::kOffUnit);
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [2] a row tile's queries are there
   uint64_t* bar_s = bar_q + 2;                                      // [2] its scores
   uint64_t* bar_p = bar_q + 4;                                      // [2] its weights
   uint64_t* bar_o = bar_q + 6;                                      // [2] its value product is done
-  uint64_t* k_full = bar_q + 8;                                     // [2] a stage's keys are unpacked
+  uint64_t* k_full = bar_q + 8;                                     // [2] a tile's keys are unpacked
   uint64_t* k_empty = bar_q + 10;                                   // [2] and read
-  uint64_t* v_full = bar_q + 12;
-  uint64_t* v_empty = bar_q + 14;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q + 16);
+  uint64_t* v_full = bar_q + 12;                                    // [kVRing] a group's values are unpacked
+  uint64_t* v_empty = v_full + kVRing;                              // [kVRing] and read
+  uint64_t* ks_full = v_empty + kVRing;                             // [kStages] a group's stored keys landed
+  uint64_t* ks_empty = ks_full + kStages;                           // [kStages] and are unpacked
+  uint64_t* vs_full = ks_empty + kStages;
+  uint64_t* vs_empty = vs_full + kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q + L::kBars);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -288,14 +293,22 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_q + i, 128);
+      mbar_init(bar_q + i, 4);
       mbar_init(bar_s + i, 1);
-      mbar_init(bar_p + i, 128);
+      mbar_init(bar_p + i, 4);
       mbar_init(bar_o + i, 1);
-      mbar_init(k_full + i, 128);
+      mbar_init(k_full + i, 4);
       mbar_init(k_empty + i, 1);
-      mbar_init(v_full + i, 32 * kGroups);
+    }
+    for (int i = 0; i < kVRing; ++i) {
+      mbar_init(v_full + i, 1);
       mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(ks_full + i, 1);
+      mbar_init(ks_empty + i, 4);
+      mbar_init(vs_full + i, 1);
+      mbar_init(vs_empty + i, 1);
     }
     *failed = 0;
     fence_mbar_init();
@@ -312,6 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
     return false;
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+  // of a warp: one arrival
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
   int seg = at.p0 / at.T, tile = at.p0 - seg * at.T;
   // row tiles of the segment: the second one may hold no row
   auto second = [&](int sg) { return rows_all - (sg - div_by(sg, a.row_tiles) * a.row_tiles.d) * kRows > 128; };
@@ -346,12 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
           }
           nm = FLT_MAX;
           fence_proxy_async_smem();
-          mbar_arrive(bar_q + r);
+          arrive(bar_q + r);
         }
         if (!wait_warp(bar_s + r, n)) break;
         tmem_after();
-        // ---- scores in log2 units; they are rounded before the maximum is taken from them, so that the largest one's
-        //      weight is exact however large it is ----
+        // ---- scores, in units of 1 / rowc log2 ----
         float2 x[kTok / 2];
         {
           const float* un = unit + (p & 3) * 8;
@@ -364,8 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
           for (int g = 0; g < kGroups; ++g) {
             const float z = -(__uint_as_float(cr[2 * g]) + __uint_as_float(cr[2 * g + 1])) * un[4 + g], f = un[g];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              x[16 * g + i] = __fmul2_rn(__ffma2_rn(x[16 * g + i], make_float2(f, f), make_float2(z, z)), make_float2(rowc, rowc));
+            for (int i = 0; i < 16; ++i) x[16 * g + i] = __ffma2_rn(x[16 * g + i], make_float2(f, f), make_float2(z, z));
           }
         }
         if (last && len.n - tile * kTok < kTok) {  // none behind the last token
@@ -379,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < kTok / 2; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(x[i].x, x[i].y));
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowc;
         const bool up = mx + nm > kSlack + kRaise;
         if (__any_sync(0xFFFFFFFFu, up)) {
           const float f = up ? exp2_approx((kRaise - mx) - nm) : 1.f;
@@ -399,20 +415,28 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
             }
           }
         }
-        // ---- weights, into the scores' columns ----
+        // ---- weights, into the scores' columns. A weight is exp2(x rowc + nm) by one FMA: what the rounding of the maximum
+        //      leaves in nm is common to the row. Scores so large that this is no longer small are rounded first, so that
+        //      the largest one's weight is exact. ----
+        float rc = rowc;
+        if (__any_sync(0xFFFFFFFFu, !(fabsf(mx) < 1048576.f) || (nm != FLT_MAX && !(fabsf(nm) < 1048576.f)))) {
+#pragma unroll
+          for (int i = 0; i < kTok / 2; ++i) x[i] = __fmul2_rn(x[i], make_float2(rowc, rowc));
+          rc = 1.f;
+        }
 #pragma unroll
         for (int c = 0; c < kTok / 32; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 d = __fadd2_rn(x[16 * c + i], make_float2(nm, nm));
+            const float2 d = __ffma2_rn(x[16 * c + i], make_float2(rc, rc), make_float2(nm, nm));
             w[i] = pack_h2(exp2_approx(d.x), exp2_approx(d.y));
           }
           tmem_st16(t_s + 16 * c, w);
         }
         tmem_wait_st();
         tmem_before();
-        mbar_arrive(bar_p + r);
+        arrive(bar_p + r);
         first = false;
         if (last || p + 1 == at.p1) {
           // ---- the segment ends here (or the share does): hand its sums on ----
@@ -461,122 +485,124 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       }
     }
   } else if (warp < 12) {
-    // ================= keys: four warps, the next group on its way meanwhile =================
+    // ================= keys: four warps a group; its stored part comes by bulk copies two groups ahead =================
     const CodeScale cs0;
-    const KeyLane<KB> kl(warp & 3, lane);
-    KeyRegs<KB> now, next;
-    int h = div_by(seg, a.row_tiles);
-    // the place kAhead tiles on, whose stored part is fetched into L2
-    constexpr int kAhead = 4;
-    auto fetch = [&](int p) {
-      if (p >= at.p1) return;
-      const int fseg = p / at.T;
-      prefetch_tile<KB, VB>(a, len, div_by(fseg, a.row_tiles), (p - fseg * at.T) * kTok);
+    Groups x(a, at, seg, tile), ahead = x;
+    const int n = (at.p1 - at.p0) * kGroups;
+    auto copy = [&]() {  // by the first warp: the next group's, into the stage of group i - kStages
+      const int st = ahead.i % kStages;
+      if (ahead.i >= kStages && !wait_warp(ks_empty + st, ahead.i / kStages + 1)) return false;
+      if (lane == 0) copy_keys<KB, VB>(a, len, ahead.h, ahead.t, sm + L::kOffKs + st * L::kKStage, ks_full + st);
+      ahead.next(a, at);
+      return true;
     };
-    load_keys<KB>(a, len, h, tile * kTok, 0, kl, now);
-    int g = 0, p = at.p0;
+    for (int i = 0; i < kStages - 1 && warp == 8; ++i) copy();  // a tile has kStages groups: these are there
 #pragma unroll 1
-    while (p < at.p1) {
-      const int it = p - at.p0, st = it & 1, t = tile * kTok + g * kGroupT, h0 = h, g0 = g;
-      if (g == 0) {
-        if (warp == 8 && lane == 0) fetch(p + kAhead);
-        if (it >= 2 && !wait_warp(k_empty + st, (it >> 1) + 1)) break;
-      }
-      if (++g == kGroups) {
-        g = 0;
-        ++p;
-        if (++tile == at.T) {
-          tile = 0;
-          h = div_by(++seg, a.row_tiles);
-        }
-      }
-      if (p < at.p1) load_keys<KB>(a, len, h, tile * kTok + g * kGroupT, g, kl, next);
-      store_keys<KB>(cs0, a, len, h0, t, g0, kl, now, sm + L::kOffK + st * L::kK, sm + L::kOffKr + st * L::kKr,
-                     unit + ((at.p0 + it) & 3) * 8);
-      if (g == 0) {
+    while (x.i < n) {
+      const int it = x.p - at.p0, st = it & 1, sg = x.i % kStages;
+      if (warp == 8 && ahead.i < n && !copy()) break;
+      if (x.g == 0 && it >= 2 && !wait_warp(k_empty + st, (it >> 1) + 1)) break;
+      if (!wait_warp(ks_full + sg, x.i / kStages)) break;
+      unpack_keys<KB>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage, sm + L::kOffK + st * L::kK,
+                      sm + L::kOffKr + st * L::kKr, unit + (x.p & 3) * 8);
+      arrive(ks_empty + sg);
+      if (x.g == kGroups - 1) {
         fence_proxy_async_smem();
-        mbar_arrive(k_full + st);
+        arrive(k_full + st);
       }
-      now = next;
+      x.next(a, at);
     }
   } else if (warp < 12 + kGroups) {
-    // ================= values: a warp a 32-token group, one value group after the other =================
+    // ================= values: a warp every third group, whose stored part it copies a tile ahead =================
     const CodeScale cs0;
-    ValueRegs<VB> now, next;
-    int h = div_by(seg, a.row_tiles);
-    const int lt = 32 * (warp - 12) + lane;  // the lane's token of the tile
-    load_values<VB>(a, len, h, tile * kTok + lt, 0, now);
-    int w = 0, p = at.p0;
+    const int g = warp - 12;
+    Groups x(a, at, seg, tile);
+    const int n = (at.p1 - at.p0) * kGroups;
+    for (int i = 0; i < g; ++i) x.next(a, at);
+    Groups ahead = x;
+    static_assert(kStages == kGroups, "a stage a warp");
+    unsigned char* stage = sm + L::kOffVs + g * L::kVStage;
+    auto copy = [&]() {
+      if (lane == 0) copy_values<KB, VB>(a, len, ahead.h, ahead.t, stage, vs_full + g);
+      for (int i = 0; i < kGroups; ++i) ahead.next(a, at);
+    };
+    copy();
 #pragma unroll 1
-    while (p < at.p1) {
-      const int it = p - at.p0, st = it & 1, t = tile * kTok + lt, h0 = h, w0 = w;
-      if (w == 0 && it >= 2 && !wait_warp(v_empty + st, (it >> 1) + 1)) break;
-      if (++w == 4) {
-        w = 0;
-        ++p;
-        if (++tile == at.T) {
-          tile = 0;
-          h = div_by(++seg, a.row_tiles);
-        }
-      }
-      if (p < at.p1) load_values<VB>(a, len, h, tile * kTok + lt, w, next);
-      store_values<VB>(cs0, a, len, h0, t, w0, now, sm + L::kOffV + st * L::kV + lt * 16);
-      if (w == 0) {
-        fence_proxy_async_smem();
-        mbar_arrive(v_full + st);
-      }
-      now = next;
+    while (x.i < n) {
+      const int it = x.p - at.p0, sv = x.i % kVRing;
+      if (x.i >= kVRing && !wait_warp(v_empty + sv, x.i / kVRing + 1)) break;
+      if (!wait_warp(vs_full + g, it)) break;
+      unpack_values<VB>(cs0, a, len, x.h, x.t, lane, stage, sm + L::kOffV + sv * L::kV);
+      fence_proxy_async_smem();
+      arrive(v_full + sv);
+      if (ahead.i < n) copy();  // every lane has read the stage
+      for (int i = 0; i < kGroups; ++i) x.next(a, at);
     }
-  } else if (lane == 0) {
-    // ================= products =================
-    const uint64_t desc_q = tree_desc(smem_u32(sm + L::kOffQ), 128, 2048);
-    const uint64_t desc_k = tree_desc(smem_u32(sm + L::kOffK), 128, 2048);
-    const uint64_t desc_kr = tree_desc(smem_u32(sm + L::kOffKr), 128, 2048);
-    const uint64_t desc_v = tree_desc(smem_u32(sm + L::kOffV), 128, kVSbo);
+  } else {
+    // ================= products: the warp walks together, one lane issues =================
+    const uint32_t leader = elect_one();
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t q0 = desc_lo(sm + L::kOffQ, 128), k0 = desc_lo(sm + L::kOffK, 128), kr0 = desc_lo(sm + L::kOffKr, 128);
+    const uint32_t v0 = desc_lo(sm + L::kOffV, 128);
+    constexpr uint32_t kHi = desc_hi(2048), kHiV = desc_hi(kVSbo);
     uint32_t n[2] = {0, 0}, parts[2] = {0, 0};  // tiles, and parts of segments, of each row tile
     // the scores of row tile r for the tile in stage st; starts: the part's first
     auto scores = [&](int r, int st, bool starts) {
-      if (starts && !wait(bar_q + r, parts[r]++)) return false;
+      if (starts && !wait_warp(bar_q + r, parts[r]++)) return false;
       tmem_after();
-      const uint64_t q = desc_q + r * (128 * kD * 2 / 16), k = desc_k + st * (L::kK / 16);
+      const uint32_t q = q0 + r * (128 * kD * 2 / 16), k = k0 + st * (L::kK / 16), d = tm + r * kColS;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) umma_f16(tmem + r * kColS, q + 16 * i, k + 16 * i, tree_idesc(kColS, false), i > 0);
+      for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kColS, false)>(leader, d, q + 16 * i, k + 16 * i, i > 0);
       if constexpr (KB == 4) {
-        const uint64_t kk = desc_kr + st * (L::kKr / 16);
+        const uint32_t kk = kr0 + st * (L::kKr / 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) umma_f16(tmem + r * kColS, q + 16 * i, kk + 16 * i, tree_idesc(kTok, false), 1);
+        for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kTok, false)>(leader, d, q + 16 * i, kk + 16 * i, 1);
       }
-      tree_commit(bar_s + r);
+      commit_if(leader, bar_s + r);
       return true;
     };
     bool ok = true, starts = true;
-    int last_r = second(seg) ? 1 : 0;
-    ok = wait(k_full, 0);
+    int last_r = second(seg) ? 1 : 0, sv = 0, sv_round = 0;  // the next group's place in the ring of values, and times around
+    ok = wait_warp(k_full, 0);
     for (int r = 0; ok && r <= last_r; ++r) ok = scores(r, 0, true);
-    if (ok) tree_commit(k_empty);
+    if (ok) commit_if(leader, k_empty);
+#pragma unroll 1
     for (int p = at.p0; ok && p < at.p1; ++p) {
       const int it = p - at.p0, st = it & 1;
       const bool ends = tile + 1 == at.T, more = p + 1 < at.p1;
-      const int nseg = ends ? seg + 1 : seg, next_r = !more ? -1 : second(nseg) ? 1 : 0;
-      if (more) ok = wait(k_full + (st ^ 1), (it + 1) >> 1);
-      if (ok) ok = wait(v_full + st, it >> 1);
-      for (int r = 0; ok && r < 2; ++r) {
-        if (r <= last_r) {
-          if (!(ok = wait(bar_p + r, n[r]))) break;
-          tmem_after();
-          const uint64_t v = desc_v + st * (L::kV / 16);
+      const int nseg = ends ? seg + 1 : seg, next_r = !more ? -1 : ends ? (second(nseg) ? 1 : 0) : last_r;
+      int slot[kGroups];
 #pragma unroll
-          for (int i = 0; i < kTok / 16; ++i)
-            umma_f16_ta(tmem + 2 * kColS + r * kColO, tmem + r * kColS + 8 * i, v + 16 * i, tree_idesc(kColO, true), !starts || i > 0);
-          tree_commit(bar_o + r);
-          if (r == last_r) tree_commit(v_empty + st);
+      for (int g = 0; g < kGroups; ++g) {
+        slot[g] = sv;
+        if (ok) ok = wait_warp(v_full + sv, sv_round);
+        if (++sv == kVRing) {
+          sv = 0;
+          ++sv_round;
+        }
+      }
+      if (more && ok) ok = wait_warp(k_full + (st ^ 1), (it + 1) >> 1);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (ok && r <= last_r) {
+          if (!(ok = wait_warp(bar_p + r, n[r]))) break;
+          tmem_after();
+#pragma unroll
+          for (int i = 0; i < 2 * kGroups; ++i)
+            umma_lo_ta<kHiV, tree_idesc(kColO, true)>(leader, tm + 2 * kColS + r * kColO, tm + r * kColS + 8 * i,
+                                                      v0 + slot[i / 2] * (L::kV / 16) + 16 * (i & 1), i > 0 || !starts);
+          commit_if(leader, bar_o + r);
+          if (r == last_r) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) commit_if(leader, v_empty + slot[g]);
+          }
           // the scores of the next tile take the columns that this product reads
-          if (!(ok = wait(bar_o + r, n[r]))) break;
+          if (r <= next_r && !(ok = wait_warp(bar_o + r, n[r]))) break;
           ++n[r];
         }
-        if (r <= next_r) {
+        if (ok && r <= next_r) {
           if (!(ok = scores(r, st ^ 1, ends))) break;
-          if (r == next_r) tree_commit(k_empty + (st ^ 1));
+          if (r == next_r) commit_if(leader, k_empty + (st ^ 1));
         }
       }
       starts = ends;
@@ -584,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       seg = nseg;
       tile = ends ? 0 : tile + 1;
     }
-    if (!ok) {  // let what was issued end before the memory goes
+    if (!ok && leader) {  // let what was issued end before the memory goes
       mbar_wait_bounded(bar_s, n[0] & 1, 10000000ull);
       mbar_wait_bounded(bar_s + 1, n[1] & 1, 10000000ull);
       mbar_wait_bounded(bar_o, n[0] & 1, 10000000ull);
@@ -675,9 +701,9 @@ __global__ void __launch_bounds__(kJoinThreads) kivi_prefix_join_kernel(const Ki
 template <int KB, int VB>
 cudaError_t launch_prefix_rows(const KiviTreeArgs& a, cudaStream_t st) {
   auto kernel = kivi_prefix_kernel<KB, VB>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixLayout<KB>::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixLayout<KB, VB>::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<a.blocks.d, kThreads, PrefixLayout<KB>::kSmem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
+  kernel<<<a.blocks.d, kThreads, PrefixLayout<KB, VB>::kSmem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
   return cudaGetLastError();
 }
 

@@ -258,16 +258,54 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// D += A B with A in TMEM: a lane a row, a column two elements of K
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Products of a warp that walks together, of which one lane issues: operands stay in uniform registers. Descriptors in
+// two words, the upper one a constant.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t desc_lo(const void* p, uint32_t lbo) {
+  return __shfl_sync(0xFFFFFFFFu, ((smem_u32(p) & 0x3FFFFu) >> 4) | (lbo >> 4) << 16, 0);
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | 1u << 14; }
+template <uint32_t AHI, uint32_t BHI, uint32_t IDESC>
+__device__ __forceinline__ void umma_lo(uint32_t leader, uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\t"
+      "mov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %7, p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(accumulate), "r"(leader), "n"(AHI), "n"(BHI), "n"(IDESC)
       : "memory");
 }
+// A in TMEM: a lane a row, a column two elements of K
+template <uint32_t BHI, uint32_t IDESC>
+__device__ __forceinline__ void umma_lo_ta(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %6, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(accumulate), "r"(leader), "n"(BHI), "n"(IDESC)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
 // the largest of the lanes' values that are numbers
 __device__ __forceinline__ float warp_max(float x) {
   float r;
