@@ -20,41 +20,51 @@ namespace {
 // ======================================================================================
 //
 //   S [128 rows x 112] = q [128 x 128] . K'^T      K' = 96 tokens s (c - c0), exact in one fp16 at 2 bits and in
-//                                                  two at 4, and rows of the groups' constants s (z - c0)
+//                                                  two at 4 (below), and rows of the groups' constants s (z - c0)
 //   P = exp2(S c - m)                              a thread owns a row; P takes the columns of S
 //   O [128 rows x 144] += P [128 x 96] . V'        V' = 128 channels s (c - c0), and columns of the tokens'
 //                                                  constants s z, c0 s and of ones, whose sums are the weights'
 // The constants enter as further tokens and channels of the same two products, so what a group lies off
 // from zero is never rounded to fp16 (as in the tree kernels). 96 tokens: 2 (112 + 144) fp32 columns are
 // the 512 of TMEM.
-// Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 11 unpack keys and 12 - 14 values into
-// two stages of shared memory, warp 15 issues the products. A row's maximum moves only when a score passes it by
+// Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 15 unpack keys and 16 - 18 values into
+// shared memory, warp 19 issues the products. A row's maximum moves only when a score passes it by
 // 2^kSlack, so rescaling O is rare and left to the softmax warps.
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr uint32_t kColS = 112, kColO = 144;     // TMEM columns of S and of O
 constexpr int kVSbo = kGroupT * 16 + 16;         // V' of a group: from eight channels to the next (+ 16: other banks)
-constexpr int kVRing = 4, kStages = 3;           // groups: unpacked values; stored keys, and values, on their way
+constexpr int kKStages = 5;                      // groups whose stored keys are on their way
 
-template <int KB, int VB>
+// REST: the keys' second parts
+template <int KB, int VB, bool REST>
 struct PrefixLayout {
+  static constexpr int kVRing = REST ? 4 : 6;              // groups of unpacked values
   // a group's stored keys or values: codes, scales, zero-points
   static constexpr int kKCode = kGroupT * kD * KB / 8, kVCode = kGroupT * kD * VB / 8, kPart = kD * 2;
   static constexpr int kKStage = kKCode + 2 * kPart, kVStage = kVCode + 2 * kPart;
-  static constexpr int kK = (kTok + 16) * kD * 2, kKr = KB == 4 ? kTok * kD * 2 : 0, kV = 18 * kVSbo;
+  static constexpr int kK = (kTok + 16) * kD * 2, kKr = REST ? kTok * kD * 2 : 0, kV = 18 * kVSbo;
   static constexpr int kOffQ = 0;                          // fp16 [2][128 x 128], K-major
   static constexpr int kOffK = kOffQ + 2 * 128 * kD * 2;   // [2] K' of a tile (112 rows), K-major
-  static constexpr int kOffKr = kOffK + 2 * kK;            // [2] second parts of the keys (4 bits)
+  static constexpr int kOffKr = kOffK + 2 * kK;            // [2] second parts of the keys
   static constexpr int kOffV = kOffKr + 2 * kKr;           // [kVRing] V' of a group, tokens within eight channels
-  static constexpr int kOffKs = kOffV + kVRing * kV;       // [kStages] stored keys of a group
-  static constexpr int kOffVs = kOffKs + kStages * kKStage;
-  static constexpr int kOffUnit = kOffVs + kStages * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
+  static constexpr int kOffKs = kOffV + kVRing * kV;       // [kKStages] stored keys of a group
+  static constexpr int kOffVs = kOffKs + kKStages * kKStage;
+  static constexpr int kOffUnit = kOffVs + kGroups * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
   static constexpr int kOffBar = kOffUnit + 4 * 8 * 4;
-  static constexpr int kBars = 8 + 4 + 2 * kVRing + 4 * kStages;
+  static constexpr int kBars = 8 + 4 + 2 * kVRing + 2 * kKStages + kGroups;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory of a block");
 };
+
+// Registers: 96 a thread at launch, of which the softmax warps, with 96 scores each, take from the others.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
+static_assert(256 * kRegsSoftmax + 384 * kRegsOther <= kThreads * kRegsLaunch, "registers of a block");
+template <int N>
+__device__ __forceinline__ void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // partial softmax of a segment: o [32 chunks of four channels][kRows][4], then m, l of each row
 constexpr size_t kSlotFloats = (size_t)kRows * (kD + 2);
@@ -74,7 +84,7 @@ __device__ __forceinline__ PrefixPlace prefix_place(const KiviTreeArgs& a, const
 // ---- keys of a 32-token group, by four warps: warp w takes channels 32 w .. + 31 of every token. A lane takes token
 //      lane % 8 of an octet and a code word (2 bits: 16 channels, two octets; 4 bits: 8 channels, four octets). ----
 // t: the group's first token; g: its place in the tile; stage: what is stored of it
-template <int KB>
+template <int KB, bool REST>
 __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int g,
                                             int w, int lane, const unsigned char* stage, unsigned char* dst, unsigned char* rest,
                                             float* unit) {
@@ -142,11 +152,11 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
       for (int j = 0; j < kPairs; ++j) {
         const __half2 c = code_h2<KB, kCentre<KB>>(cs0, code[i], j);
         x[j] = as_u(__hmul2(c, s[j]));
-        if constexpr (KB == 4) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
+        if constexpr (REST) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
       }
       *reinterpret_cast<uint4*>(dst + at0 + 2048 * i) = make_uint4(x[0], x[1], x[2], x[3]);
       if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + at0 + 2048 * i + 128) = make_uint4(x[4], x[5], x[6], x[7]);
-      else *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+      if constexpr (REST) *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   } else {  // fp16 rows, or none
     if (w == g) {
@@ -164,7 +174,7 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
       } else {
         const uint4 v = row8(row, word);
         pair_order<4>(v, v, x0, x1);
-        *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (REST) *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(0u, 0u, 0u, 0u);
       }
       *reinterpret_cast<uint4*>(dst + at0 + 2048 * i) = x0;
     }
@@ -216,9 +226,9 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
 }
 
 // What is stored of a group into a stage, by one thread; with nothing to copy the barrier completes at once.
-template <int KB, int VB>
+template <int KB, int VB, bool REST>
 __device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens& len, int h, int t, unsigned char* stage, uint64_t* full) {
-  using L = PrefixLayout<KB, VB>;
+  using L = PrefixLayout<KB, VB, REST>;
   if (t >= len.nqk) {
     mbar_arrive(full);
     return;
@@ -229,9 +239,9 @@ __device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens&
   bulk_g2s(stage + L::kKCode, a.k_scale + g, L::kPart, full);
   bulk_g2s(stage + L::kKCode + L::kPart, a.k_zero + g, L::kPart, full);
 }
-template <int KB, int VB>
+template <int KB, int VB, bool REST>
 __device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLens& len, int h, int t, unsigned char* stage, uint64_t* full) {
-  using L = PrefixLayout<KB, VB>;
+  using L = PrefixLayout<KB, VB, REST>;
   if (t >= len.nqv) {
     mbar_arrive(full);
     return;
@@ -261,9 +271,10 @@ struct Groups {
   }
 };
 
-template <int KB, int VB>
+template <int KB, int VB, bool REST>
 __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTreeArgs a, const float scale_log2) {
-  using L = PrefixLayout<KB, VB>;
+  using L = PrefixLayout<KB, VB, REST>;
+  constexpr int kVRing = L::kVRing;
   extern __shared__ __align__(128) unsigned char sm[];
   float* unit = reinterpret_cast<float*>(sm + L::kOffUnit);
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [2] a row tile's queries are there
@@ -274,10 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   uint64_t* k_empty = bar_q + 10;                                   // [2] and read
   uint64_t* v_full = bar_q + 12;                                    // [kVRing] a group's values are unpacked
   uint64_t* v_empty = v_full + kVRing;                              // [kVRing] and read
-  uint64_t* ks_full = v_empty + kVRing;                             // [kStages] a group's stored keys landed
-  uint64_t* ks_empty = ks_full + kStages;                           // [kStages] and are unpacked
-  uint64_t* vs_full = ks_empty + kStages;
-  uint64_t* vs_empty = vs_full + kStages;
+  uint64_t* ks_full = v_empty + kVRing;                             // [kKStages] a group's stored keys landed
+  uint64_t* ks_empty = ks_full + kKStages;                          // [kKStages] and are unpacked
+  uint64_t* vs_full = ks_empty + kKStages;                          // [kGroups] a tile's group's stored values landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q + L::kBars);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   const PrefixPlace at = prefix_place(a, len, blockIdx.x);
   if (at.p0 >= at.p1) return;
   const int rows_all = a.N * a.rep.d;
-  if (warp == 15) {
+  if (warp == 19) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -297,19 +307,18 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       mbar_init(bar_s + i, 1);
       mbar_init(bar_p + i, 4);
       mbar_init(bar_o + i, 1);
-      mbar_init(k_full + i, 4);
+      mbar_init(k_full + i, 4 * kGroups);
       mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < kVRing; ++i) {
       mbar_init(v_full + i, 1);
       mbar_init(v_empty + i, 1);
     }
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kKStages; ++i) {
       mbar_init(ks_full + i, 1);
       mbar_init(ks_empty + i, 4);
-      mbar_init(vs_full + i, 1);
-      mbar_init(vs_empty + i, 1);
     }
+    for (int i = 0; i < kGroups; ++i) mbar_init(vs_full + i, 1);
     *failed = 0;
     fence_mbar_init();
   }
@@ -336,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
 
   if (warp < 8) {
     // ================= softmax: row tile r, a thread a row =================
+    set_regs_up<kRegsSoftmax>();
     const int r = warp >> 2, row_t = tid & 127;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_s = t_lane + r * kColS, t_o = t_lane + 2 * kColS + r * kColO;
@@ -484,143 +494,150 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         ++tile;
       }
     }
-  } else if (warp < 12) {
-    // ================= keys: four warps a group; its stored part comes by bulk copies two groups ahead =================
-    const CodeScale cs0;
-    Groups x(a, at, seg, tile), ahead = x;
-    const int n = (at.p1 - at.p0) * kGroups;
-    auto copy = [&]() {  // by the first warp: the next group's, into the stage of group i - kStages
-      const int st = ahead.i % kStages;
-      if (ahead.i >= kStages && !wait_warp(ks_empty + st, ahead.i / kStages + 1)) return false;
-      if (lane == 0) copy_keys<KB, VB>(a, len, ahead.h, ahead.t, sm + L::kOffKs + st * L::kKStage, ks_full + st);
-      ahead.next(a, at);
-      return true;
-    };
-    for (int i = 0; i < kStages - 1 && warp == 8; ++i) copy();  // a tile has kStages groups: these are there
-#pragma unroll 1
-    while (x.i < n) {
-      const int it = x.p - at.p0, st = it & 1, sg = x.i % kStages;
-      if (warp == 8 && ahead.i < n && !copy()) break;
-      if (x.g == 0 && it >= 2 && !wait_warp(k_empty + st, (it >> 1) + 1)) break;
-      if (!wait_warp(ks_full + sg, x.i / kStages)) break;
-      unpack_keys<KB>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage, sm + L::kOffK + st * L::kK,
-                      sm + L::kOffKr + st * L::kKr, unit + (x.p & 3) * 8);
-      arrive(ks_empty + sg);
-      if (x.g == kGroups - 1) {
-        fence_proxy_async_smem();
-        arrive(k_full + st);
-      }
-      x.next(a, at);
-    }
-  } else if (warp < 12 + kGroups) {
-    // ================= values: a warp every third group, whose stored part it copies a tile ahead =================
-    const CodeScale cs0;
-    const int g = warp - 12;
-    Groups x(a, at, seg, tile);
-    const int n = (at.p1 - at.p0) * kGroups;
-    for (int i = 0; i < g; ++i) x.next(a, at);
-    Groups ahead = x;
-    static_assert(kStages == kGroups, "a stage a warp");
-    unsigned char* stage = sm + L::kOffVs + g * L::kVStage;
-    auto copy = [&]() {
-      if (lane == 0) copy_values<KB, VB>(a, len, ahead.h, ahead.t, stage, vs_full + g);
-      for (int i = 0; i < kGroups; ++i) ahead.next(a, at);
-    };
-    copy();
-#pragma unroll 1
-    while (x.i < n) {
-      const int it = x.p - at.p0, sv = x.i % kVRing;
-      if (x.i >= kVRing && !wait_warp(v_empty + sv, x.i / kVRing + 1)) break;
-      if (!wait_warp(vs_full + g, it)) break;
-      unpack_values<VB>(cs0, a, len, x.h, x.t, lane, stage, sm + L::kOffV + sv * L::kV);
-      fence_proxy_async_smem();
-      arrive(v_full + sv);
-      if (ahead.i < n) copy();  // every lane has read the stage
-      for (int i = 0; i < kGroups; ++i) x.next(a, at);
-    }
   } else {
-    // ================= products: the warp walks together, one lane issues =================
-    const uint32_t leader = elect_one();
-    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    const uint32_t q0 = desc_lo(sm + L::kOffQ, 128), k0 = desc_lo(sm + L::kOffK, 128), kr0 = desc_lo(sm + L::kOffKr, 128);
-    const uint32_t v0 = desc_lo(sm + L::kOffV, 128);
-    constexpr uint32_t kHi = desc_hi(2048), kHiV = desc_hi(kVSbo);
-    uint32_t n[2] = {0, 0}, parts[2] = {0, 0};  // tiles, and parts of segments, of each row tile
-    // the scores of row tile r for the tile in stage st; starts: the part's first
-    auto scores = [&](int r, int st, bool starts) {
-      if (starts && !wait_warp(bar_q + r, parts[r]++)) return false;
-      tmem_after();
-      const uint32_t q = q0 + r * (128 * kD * 2 / 16), k = k0 + st * (L::kK / 16), d = tm + r * kColS;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kColS, false)>(leader, d, q + 16 * i, k + 16 * i, i > 0);
-      if constexpr (KB == 4) {
-        const uint32_t kk = kr0 + st * (L::kKr / 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kTok, false)>(leader, d, q + 16 * i, kk + 16 * i, 1);
-      }
-      commit_if(leader, bar_s + r);
-      return true;
-    };
-    bool ok = true, starts = true;
-    int last_r = second(seg) ? 1 : 0, sv = 0, sv_round = 0;  // the next group's place in the ring of values, and times around
-    ok = wait_warp(k_full, 0);
-    for (int r = 0; ok && r <= last_r; ++r) ok = scores(r, 0, true);
-    if (ok) commit_if(leader, k_empty);
+    set_regs_down<kRegsOther>();
+    if (warp < 16) {
+      // ================= keys: four warps a group, two such sets in turn; stored parts come by bulk copies =================
+      const CodeScale cs0;
+      const int set = (warp - 8) >> 2;
+      Groups x(a, at, seg, tile), ahead = x;
+      const int n = (at.p1 - at.p0) * kGroups;
+      auto copy = [&](int upto) {  // by the first warp: stored parts of groups below `upto`, each into the stage of group i - kKStages
+        for (; ahead.i < min(upto, n); ahead.next(a, at)) {
+          const int sg = ahead.i % kKStages;
+          if (ahead.i >= kKStages && !wait_warp(ks_empty + sg, ahead.i / kKStages + 1)) return false;
+          if (lane == 0) copy_keys<KB, VB, REST>(a, len, ahead.h, ahead.t, sm + L::kOffKs + sg * L::kKStage, ks_full + sg);
+        }
+        return true;
+      };
+      if (set) x.next(a, at);
+      int seen = 1;  // tiles whose stage was found empty (the first two are)
 #pragma unroll 1
-    for (int p = at.p0; ok && p < at.p1; ++p) {
-      const int it = p - at.p0, st = it & 1;
-      const bool ends = tile + 1 == at.T, more = p + 1 < at.p1;
-      const int nseg = ends ? seg + 1 : seg, next_r = !more ? -1 : ends ? (second(nseg) ? 1 : 0) : last_r;
-      int slot[kGroups];
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        slot[g] = sv;
-        if (ok) ok = wait_warp(v_full + sv, sv_round);
-        if (++sv == kVRing) {
-          sv = 0;
-          ++sv_round;
+      while (x.i < n) {
+        const int it = x.p - at.p0, st = it & 1, sg = x.i % kKStages;
+        if (warp == 8 && !copy(x.i + kKStages - 1)) break;
+        if (it > seen) {
+          if (!wait_warp(k_empty + st, (it >> 1) + 1)) break;
+          seen = it;
         }
+        if (!wait_warp(ks_full + sg, x.i / kKStages)) break;
+        unpack_keys<KB, REST>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage, sm + L::kOffK + st * L::kK,
+                        sm + L::kOffKr + st * L::kKr, unit + (x.p & 3) * 8);
+        fence_proxy_async_smem();
+        arrive(ks_empty + sg);
+        if (lane == 0) mbar_arrive(k_full + st);
+        x.next(a, at);
+        x.next(a, at);
       }
-      if (more && ok) ok = wait_warp(k_full + (st ^ 1), (it + 1) >> 1);
+    } else if (warp < 16 + kGroups) {
+      // ================= values: a warp every third group, whose stored part it copies a tile ahead =================
+      const CodeScale cs0;
+      const int g = warp - 16;
+      Groups x(a, at, seg, tile);
+      const int n = (at.p1 - at.p0) * kGroups;
+      for (int i = 0; i < g; ++i) x.next(a, at);
+      Groups ahead = x;
+      unsigned char* stage = sm + L::kOffVs + g * L::kVStage;
+      auto copy = [&]() {
+        if (lane == 0) copy_values<KB, VB, REST>(a, len, ahead.h, ahead.t, stage, vs_full + g);
+        for (int i = 0; i < kGroups; ++i) ahead.next(a, at);
+      };
+      copy();
+#pragma unroll 1
+      while (x.i < n) {
+        const int it = x.p - at.p0, sv = x.i % kVRing;
+        if (x.i >= kVRing && !wait_warp(v_empty + sv, x.i / kVRing + 1)) break;
+        if (!wait_warp(vs_full + g, it)) break;
+        unpack_values<VB>(cs0, a, len, x.h, x.t, lane, stage, sm + L::kOffV + sv * L::kV);
+        fence_proxy_async_smem();
+        arrive(v_full + sv);
+        if (ahead.i < n) copy();  // every lane has read the stage
+        for (int i = 0; i < kGroups; ++i) x.next(a, at);
+      }
+    } else {
+      // ================= products: the warp walks together, one lane issues =================
+      const uint32_t leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint32_t q0 = desc_lo(sm + L::kOffQ, 128), k0 = desc_lo(sm + L::kOffK, 128), kr0 = desc_lo(sm + L::kOffKr, 128);
+      const uint32_t v0 = desc_lo(sm + L::kOffV, 128);
+      constexpr uint32_t kHi = desc_hi(2048), kHiV = desc_hi(kVSbo);
+      uint32_t n[2] = {0, 0}, parts[2] = {0, 0};  // tiles, and parts of segments, of each row tile
+      // the scores of row tile r for the tile in stage st; starts: the part's first
+      auto scores = [&](int r, int st, bool starts) {
+        if (starts && !wait_warp(bar_q + r, parts[r]++)) return false;
+        tmem_after();
+        const uint32_t q = q0 + r * (128 * kD * 2 / 16), k = k0 + st * (L::kK / 16), d = tm + r * kColS;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (ok && r <= last_r) {
-          if (!(ok = wait_warp(bar_p + r, n[r]))) break;
-          tmem_after();
+        for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kColS, false)>(leader, d, q + 16 * i, k + 16 * i, i > 0);
+        if constexpr (REST) {
+          const uint32_t kk = kr0 + st * (L::kKr / 16);
 #pragma unroll
-          for (int i = 0; i < 2 * kGroups; ++i)
-            umma_lo_ta<kHiV, tree_idesc(kColO, true)>(leader, tm + 2 * kColS + r * kColO, tm + r * kColS + 8 * i,
-                                                      v0 + slot[i / 2] * (L::kV / 16) + 16 * (i & 1), i > 0 || !starts);
-          commit_if(leader, bar_o + r);
-          if (r == last_r) {
+          for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kTok, false)>(leader, d, q + 16 * i, kk + 16 * i, 1);
+        }
+        commit_if(leader, bar_s + r);
+        return true;
+      };
+      bool ok = true, starts = true;
+      int last_r = second(seg) ? 1 : 0, sv = 0, sv_round = 0;  // the next group's place in the ring of values, and times around
+      ok = wait_warp(k_full, 0);
+      for (int r = 0; ok && r <= last_r; ++r) ok = scores(r, 0, true);
+      if (ok) commit_if(leader, k_empty);
+#pragma unroll 1
+      for (int p = at.p0; ok && p < at.p1; ++p) {
+        const int it = p - at.p0, st = it & 1;
+        const bool ends = tile + 1 == at.T, more = p + 1 < at.p1;
+        const int nseg = ends ? seg + 1 : seg, next_r = !more ? -1 : ends ? (second(nseg) ? 1 : 0) : last_r;
+        int slot[kGroups];
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) commit_if(leader, v_empty + slot[g]);
+        for (int g = 0; g < kGroups; ++g) {
+          slot[g] = sv;
+          if (ok) ok = wait_warp(v_full + sv, sv_round);
+          if (++sv == kVRing) {
+            sv = 0;
+            ++sv_round;
           }
-          // the scores of the next tile take the columns that this product reads
-          if (r <= next_r && !(ok = wait_warp(bar_o + r, n[r]))) break;
-          ++n[r];
         }
-        if (ok && r <= next_r) {
-          if (!(ok = scores(r, st ^ 1, ends))) break;
-          if (r == next_r) commit_if(leader, k_empty + (st ^ 1));
+        if (more && ok) ok = wait_warp(k_full + (st ^ 1), (it + 1) >> 1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (ok && r <= last_r) {
+            if (!(ok = wait_warp(bar_p + r, n[r]))) break;
+            tmem_after();
+#pragma unroll
+            for (int i = 0; i < 2 * kGroups; ++i)
+              umma_lo_ta<kHiV, tree_idesc(kColO, true)>(leader, tm + 2 * kColS + r * kColO, tm + r * kColS + 8 * i,
+                                                        v0 + slot[i / 2] * (L::kV / 16) + 16 * (i & 1), i > 0 || !starts);
+            commit_if(leader, bar_o + r);
+            if (r == last_r) {
+#pragma unroll
+              for (int g = 0; g < kGroups; ++g) commit_if(leader, v_empty + slot[g]);
+            }
+            // the scores of the next tile take the columns that this product reads
+            if (r <= next_r && !(ok = wait_warp(bar_o + r, n[r]))) break;
+            ++n[r];
+          }
+          if (ok && r <= next_r) {
+            if (!(ok = scores(r, st ^ 1, ends))) break;
+            if (r == next_r) commit_if(leader, k_empty + (st ^ 1));
+          }
         }
+        starts = ends;
+        last_r = next_r;
+        seg = nseg;
+        tile = ends ? 0 : tile + 1;
       }
-      starts = ends;
-      last_r = next_r;
-      seg = nseg;
-      tile = ends ? 0 : tile + 1;
-    }
-    if (!ok && leader) {  // let what was issued end before the memory goes
-      mbar_wait_bounded(bar_s, n[0] & 1, 10000000ull);
-      mbar_wait_bounded(bar_s + 1, n[1] & 1, 10000000ull);
-      mbar_wait_bounded(bar_o, n[0] & 1, 10000000ull);
-      mbar_wait_bounded(bar_o + 1, n[1] & 1, 10000000ull);
+      if (!ok && leader) {  // let what was issued end before the memory goes
+        mbar_wait_bounded(bar_s, n[0] & 1, 10000000ull);
+        mbar_wait_bounded(bar_s + 1, n[1] & 1, 10000000ull);
+        mbar_wait_bounded(bar_o, n[0] & 1, 10000000ull);
+        mbar_wait_bounded(bar_o + 1, n[1] & 1, 10000000ull);
+      }
     }
   }
   __syncwarp();
   tmem_before();
   __syncthreads();
-  if (warp == 15) {
+  if (warp == 19) {
     tmem_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
@@ -698,13 +715,19 @@ __global__ void __launch_bounds__(kJoinThreads) kivi_prefix_join_kernel(const Ki
               *reinterpret_cast<const float4*>(static_cast<const float*>(a.own.out) + at));
 }
 
-template <int KB, int VB>
+template <int KB, int VB, bool REST>
 cudaError_t launch_prefix_rows(const KiviTreeArgs& a, cudaStream_t st) {
-  auto kernel = kivi_prefix_kernel<KB, VB>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixLayout<KB, VB>::kSmem);
+  auto kernel = kivi_prefix_kernel<KB, VB, REST>;
+  constexpr int kSmem = PrefixLayout<KB, VB, REST>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<a.blocks.d, kThreads, PrefixLayout<KB, VB>::kSmem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
+  kernel<<<a.blocks.d, kThreads, kSmem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
   return cudaGetLastError();
+}
+template <int VB>
+cudaError_t launch_prefix_keys(const KiviTreeArgs& a, bool fp32, cudaStream_t st) {
+  if (a.k_bits == 2) return launch_prefix_rows<2, VB, false>(a, st);
+  return fp32 ? launch_prefix_rows<4, VB, true>(a, st) : launch_prefix_rows<4, VB, false>(a, st);
 }
 
 // Rows of a KV head from which on the kernel of this file takes the prefix
@@ -738,8 +761,7 @@ cudaError_t launch_kivi_prefix(const KiviPrefixArgs& args, cudaStream_t st) {
     t.segs = int_div(t.H * t.row_tiles.d);
     t.blocks = int_div(device_sms());
     t.ring = int_div(t.residual);
-    e = t.k_bits == 2 ? (t.v_bits == 2 ? launch_prefix_rows<2, 2>(t, st) : launch_prefix_rows<2, 4>(t, st))
-                      : (t.v_bits == 2 ? launch_prefix_rows<4, 2>(t, st) : launch_prefix_rows<4, 4>(t, st));
+    e = t.v_bits == 2 ? launch_prefix_keys<2>(t, a.out_fp32, st) : launch_prefix_keys<4>(t, a.out_fp32, st);
   } else {
     e = launch_kivi_tree(t, st);
   }
