@@ -27,20 +27,19 @@ namespace {
 // The constants enter as further tokens and channels of the same two products, so what a group lies off
 // from zero is never rounded to fp16 (as in the tree kernels). 96 tokens: 2 (112 + 144) fp32 columns are
 // the 512 of TMEM.
-// Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 15 unpack keys and 16 - 18 values into
-// shared memory, warp 19 issues the products. A row's maximum moves only when a score passes it by
+// Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 15 unpack keys and 16 - 21 values into
+// shared memory, warp 22 issues the products (and one is idle: registers are split by four warps). A row's maximum moves only when a score passes it by
 // 2^kSlack, so rescaling O is rare and left to the softmax warps.
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr uint32_t kColS = 112, kColO = 144;     // TMEM columns of S and of O
 constexpr int kVSbo = kGroupT * 16 + 16;         // V' of a group: from eight channels to the next (+ 16: other banks)
-constexpr int kKStages = 5;                      // groups whose stored keys are on their way
-
 // REST: the keys' second parts
 template <int KB, int VB, bool REST>
 struct PrefixLayout {
   static constexpr int kVRing = REST ? 4 : 6;              // groups of unpacked values
+  static constexpr int kKStages = REST ? 5 : 9, kVStages = REST ? 1 : 2;  // groups whose stored keys are on their way; a warp's values
   // a group's stored keys or values: codes, scales, zero-points
   static constexpr int kKCode = kGroupT * kD * KB / 8, kVCode = kGroupT * kD * VB / 8, kPart = kD * 2;
   static constexpr int kKStage = kKCode + 2 * kPart, kVStage = kVCode + 2 * kPart;
@@ -51,16 +50,16 @@ struct PrefixLayout {
   static constexpr int kOffV = kOffKr + 2 * kKr;           // [kVRing] V' of a group, tokens within eight channels
   static constexpr int kOffKs = kOffV + kVRing * kV;       // [kKStages] stored keys of a group
   static constexpr int kOffVs = kOffKs + kKStages * kKStage;
-  static constexpr int kOffUnit = kOffVs + kGroups * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
+  static constexpr int kOffUnit = kOffVs + kGroups * kVStages * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
   static constexpr int kOffBar = kOffUnit + 4 * 8 * 4;
-  static constexpr int kBars = 8 + 4 + 2 * kVRing + 2 * kKStages + kGroups;
+  static constexpr int kBars = 8 + 4 + 2 * kVRing + 2 * kKStages + 2 * kGroups * kVStages;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
-// Registers: 96 a thread at launch, of which the softmax warps, with 96 scores each, take from the others.
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
-static_assert(256 * kRegsSoftmax + 384 * kRegsOther <= kThreads * kRegsLaunch, "registers of a block");
+// Registers: 80 a thread at launch, of which the softmax warps, with 96 scores each, take from the others.
+constexpr int kRegsLaunch = 80, kRegsSoftmax = 128, kRegsOther = 56;
+static_assert(256 * kRegsSoftmax + 512 * kRegsOther <= kThreads * kRegsLaunch, "registers of a block");
 template <int N>
 __device__ __forceinline__ void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -181,11 +180,11 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
   }
 }
 
-// ---- values of a 32-token group, by one warp: a lane a token, one value group (32 channels) after the other ----
-// t: the group's first token; dst: its V'
+// ---- values of a 32-token group, by two warps: a lane a token, two value groups (32 channels each) a warp ----
+// t: the group's first token; w0: the warp's first value group; dst: V' of the group
 template <int VB>
-__device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int lane,
-                                              const unsigned char* stage, unsigned char* dst) {
+__device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int w0,
+                                              int lane, const unsigned char* stage, unsigned char* dst) {
   constexpr int kRow = kD * VB / 8;
   t += lane;
   dst += lane * 16;
@@ -195,7 +194,7 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
   const uint16_t* row = nullptr;
   if (!stored && t < len.n) row = fp16_value(a, len, 0, h, t, t - div_by(t, a.ring) * a.residual);
 #pragma unroll 1
-  for (int w = 0; w < 4; ++w) {
+  for (int w = w0; w < w0 + 2; ++w) {
     // columns of the constants: s z, what its rounding left, c0 s (all halved as the values), 1
     uint2 c = make_uint2(0u, 0x3C000000u);
     if (stored) {
@@ -258,14 +257,16 @@ struct Groups {
   int i, p, seg, tile, h, t, g;  // t: the group's first token
   __device__ __forceinline__ Groups(const KiviTreeArgs& a, const PrefixPlace& at, int seg_, int tile_)
       : i(0), p(at.p0), seg(seg_), tile(tile_), h(div_by(seg_, a.row_tiles)), t(tile_ * kTok), g(0) {}
-  __device__ __forceinline__ void next(const KiviTreeArgs& a, const PrefixPlace& at) {
-    ++i;
-    t += kGroupT;
-    if (++g < kGroups) return;
-    g = 0;
+  // d < kGroups groups on
+  __device__ __forceinline__ void next(const KiviTreeArgs& a, const PrefixPlace& at, int d) {
+    i += d;
+    t += d * kGroupT;
+    if ((g += d) < kGroups) return;
+    g -= kGroups;
     ++p;
     if (++tile == at.T) {
-      tile = t = 0;
+      tile = 0;
+      t = g * kGroupT;
       h = div_by(++seg, a.row_tiles);
     }
   }
@@ -274,7 +275,7 @@ struct Groups {
 template <int KB, int VB, bool REST>
 __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTreeArgs a, const float scale_log2) {
   using L = PrefixLayout<KB, VB, REST>;
-  constexpr int kVRing = L::kVRing;
+  constexpr int kVRing = L::kVRing, kKStages = L::kKStages, kVStages = L::kVStages;
   extern __shared__ __align__(128) unsigned char sm[];
   float* unit = reinterpret_cast<float*>(sm + L::kOffUnit);
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [2] a row tile's queries are there
@@ -287,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   uint64_t* v_empty = v_full + kVRing;                              // [kVRing] and read
   uint64_t* ks_full = v_empty + kVRing;                             // [kKStages] a group's stored keys landed
   uint64_t* ks_empty = ks_full + kKStages;                          // [kKStages] and are unpacked
-  uint64_t* vs_full = ks_empty + kKStages;                          // [kGroups] a tile's group's stored values landed
+  uint64_t* vs_full = ks_empty + kKStages;                          // [kGroups][kVStages] a tile's group's stored values landed
+  uint64_t* vs_empty = vs_full + kGroups * kVStages;                // and are unpacked
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q + L::kBars);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   const PrefixPlace at = prefix_place(a, len, blockIdx.x);
   if (at.p0 >= at.p1) return;
   const int rows_all = a.N * a.rep.d;
-  if (warp == 19) {
+  if (warp == 16 + 2 * kGroups) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -311,14 +313,17 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < kVRing; ++i) {
-      mbar_init(v_full + i, 1);
+      mbar_init(v_full + i, 2);
       mbar_init(v_empty + i, 1);
     }
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(ks_full + i, 1);
       mbar_init(ks_empty + i, 4);
     }
-    for (int i = 0; i < kGroups; ++i) mbar_init(vs_full + i, 1);
+    for (int i = 0; i < kGroups * kVStages; ++i) {
+      mbar_init(vs_full + i, 1);
+      mbar_init(vs_empty + i, 2);
+    }
     *failed = 0;
     fence_mbar_init();
   }
@@ -414,14 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
             if (!wait_warp(bar_o + r, n - 1)) break;
             tmem_after();
 #pragma unroll 1
-            for (int i = 0; i < (int)kColO; i += 8) {
-              uint32_t u[8];
-              float o[8];
+            for (int i = 0; i < (int)kColO; i += 16) {
+              uint32_t u[16];
               tmem_ld8(t_o + i, u);
+              tmem_ld8(t_o + i + 8, u + 8);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(u[e]) * f;
-              tmem_st8(t_o + i, o);
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+              tmem_st16(t_o + i, u);
             }
           }
         }
@@ -503,14 +508,14 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       Groups x(a, at, seg, tile), ahead = x;
       const int n = (at.p1 - at.p0) * kGroups;
       auto copy = [&](int upto) {  // by the first warp: stored parts of groups below `upto`, each into the stage of group i - kKStages
-        for (; ahead.i < min(upto, n); ahead.next(a, at)) {
+        for (; ahead.i < min(upto, n); ahead.next(a, at, 1)) {
           const int sg = ahead.i % kKStages;
           if (ahead.i >= kKStages && !wait_warp(ks_empty + sg, ahead.i / kKStages + 1)) return false;
           if (lane == 0) copy_keys<KB, VB, REST>(a, len, ahead.h, ahead.t, sm + L::kOffKs + sg * L::kKStage, ks_full + sg);
         }
         return true;
       };
-      if (set) x.next(a, at);
+      if (set) x.next(a, at, 1);
       int seen = 1;  // tiles whose stage was found empty (the first two are)
 #pragma unroll 1
       while (x.i < n) {
@@ -526,35 +531,54 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         fence_proxy_async_smem();
         arrive(ks_empty + sg);
         if (lane == 0) mbar_arrive(k_full + st);
-        x.next(a, at);
-        x.next(a, at);
+        x.next(a, at, 2);
       }
-    } else if (warp < 16 + kGroups) {
-      // ================= values: a warp every third group, whose stored part it copies a tile ahead =================
+    } else if (warp < 16 + 2 * kGroups) {
+      // ================= values: two warps every third group, whose stored part the first copies tiles ahead =================
       const CodeScale cs0;
-      const int g = warp - 16;
-      Groups x(a, at, seg, tile);
-      const int n = (at.p1 - at.p0) * kGroups;
-      for (int i = 0; i < g; ++i) x.next(a, at);
-      Groups ahead = x;
-      unsigned char* stage = sm + L::kOffVs + g * L::kVStage;
+      const int g = (warp - 16) >> 1, n = at.p1 - at.p0;
+      int h = div_by(seg, a.row_tiles), t = tile * kTok;         // the tile's
+      int c_it = 0, c_seg = seg, c_tile = tile;                  // the next one to copy
+      unsigned char* stages = sm + L::kOffVs + g * kVStages * L::kVStage;
+      uint64_t *landed = vs_full + g * kVStages, *taken = vs_empty + g * kVStages;
       auto copy = [&]() {
-        if (lane == 0) copy_values<KB, VB, REST>(a, len, ahead.h, ahead.t, stage, vs_full + g);
-        for (int i = 0; i < kGroups; ++i) ahead.next(a, at);
+        if (c_it >= n) return true;
+        const int sg = c_it % kVStages;
+        if (c_it >= kVStages && !wait_warp(taken + sg, c_it / kVStages + 1)) return false;
+        if (lane == 0)
+          copy_values<KB, VB, REST>(a, len, div_by(c_seg, a.row_tiles), c_tile * kTok + g * kGroupT, stages + sg * L::kVStage, landed + sg);
+        ++c_it;
+        if (++c_tile == at.T) {
+          c_tile = 0;
+          ++c_seg;
+        }
+        return true;
       };
-      copy();
+      if (!(warp & 1))
+        for (int i = 0; i < kVStages; ++i) copy();
+      int sv = g, round = 0;  // the group's place in the ring, times around
 #pragma unroll 1
-      while (x.i < n) {
-        const int it = x.p - at.p0, sv = x.i % kVRing;
-        if (x.i >= kVRing && !wait_warp(v_empty + sv, x.i / kVRing + 1)) break;
-        if (!wait_warp(vs_full + g, it)) break;
-        unpack_values<VB>(cs0, a, len, x.h, x.t, lane, stage, sm + L::kOffV + sv * L::kV);
+      for (int it = 0; it < n; ++it) {
+        const int sg = it % kVStages;
+        if (round > 0 && !wait_warp(v_empty + sv, round + 1)) break;
+        if (!wait_warp(landed + sg, it / kVStages)) break;
+        unpack_values<VB>(cs0, a, len, h, t + g * kGroupT, 2 * (warp & 1), lane, stages + sg * L::kVStage, sm + L::kOffV + sv * L::kV);
         fence_proxy_async_smem();
-        arrive(v_full + sv);
-        if (ahead.i < n) copy();  // every lane has read the stage
-        for (int i = 0; i < kGroups; ++i) x.next(a, at);
+        arrive(taken + sg);
+        if (lane == 0) mbar_arrive(v_full + sv);
+        if (!(warp & 1) && !copy()) break;
+        sv += kGroups;
+        if (sv >= kVRing) {
+          sv -= kVRing;
+          ++round;
+        }
+        t += kTok;
+        if (++tile == at.T) {
+          tile = t = 0;
+          h = div_by(++seg, a.row_tiles);
+        }
       }
-    } else {
+    } else if (warp == 16 + 2 * kGroups) {
       // ================= products: the warp walks together, one lane issues =================
       const uint32_t leader = elect_one();
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
@@ -637,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   __syncwarp();
   tmem_before();
   __syncthreads();
-  if (warp == 19) {
+  if (warp == 16 + 2 * kGroups) {
     tmem_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
