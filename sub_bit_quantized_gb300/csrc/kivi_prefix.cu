@@ -141,15 +141,17 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) s[j] = __hmul2(s[j], f1);
     }
-    uint32_t code[kOct];
-#pragma unroll
-    for (int i = 0; i < kOct; ++i) code[i] = *reinterpret_cast<const uint32_t*>(stage + (8 * (oct + i) + (lane & 7)) * kRow + 4 * word);
-#pragma unroll
+    const unsigned char* src = stage + (8 * oct + (lane & 7)) * kRow + 4 * word;
+    uint32_t next = *reinterpret_cast<const uint32_t*>(src);
+#pragma unroll 1  // short loops: the roles' unrolled code does not stay in the instruction cache
     for (int i = 0; i < kOct; ++i) {
+      const uint32_t code = next;
+      src += 8 * kRow;
+      if (i + 1 < kOct) next = *reinterpret_cast<const uint32_t*>(src);
       uint32_t x[kPairs], y[kPairs];
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        const __half2 c = code_h2<KB, kCentre<KB>>(cs0, code[i], j);
+        const __half2 c = code_h2<KB, kCentre<KB>>(cs0, code, j);
         x[j] = as_u(__hmul2(c, s[j]));
         if constexpr (REST) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
       }
@@ -198,21 +200,23 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
     // columns of the constants: s z, what its rounding left, c0 s (all halved as the values), 1
     uint2 c = make_uint2(0u, 0x3C000000u);
     if (stored) {
-      uint32_t word[4];
-      if constexpr (VB == 2) {
-        const uint2 u = *reinterpret_cast<const uint2*>(codes + 8 * w);
-        word[0] = u.x; word[1] = u.x >> 16; word[2] = u.y; word[3] = u.y >> 16;
-      } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(codes + 16 * w);
-        word[0] = u.x; word[1] = u.y; word[2] = u.z; word[3] = u.w;
-      }
       const uint32_t z = scale[w + kGroupT * 4] * 0x10001u;
       const __half2 s2 = as_h2(halved(scale[w] * 0x10001u));
+      const unsigned char* src = codes + 4 * VB * w;
+      unsigned char* to = dst + 4 * w * kVSbo;
+      auto eight = [&](int i) -> uint32_t {  // codes of channels 8 i .. + 7
+        return VB == 2 ? (uint32_t)*reinterpret_cast<const uint16_t*>(src + 2 * i) : *reinterpret_cast<const uint32_t*>(src + 4 * i);
+      };
+      uint32_t next = eight(0);
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i, to += kVSbo) {
+        const uint32_t word = next;
+        if (i < 3) next = eight(i + 1);
+        *reinterpret_cast<uint4*>(to) = centred8<VB>(cs0, word, s2);
+      }
       const uint32_t p = as_u(__hmul2(s2, as_h2(z))), left = product_rest(as_u(s2), z, p);
       c.x = (p & 0xFFFFu) | (left << 16);
       c.y |= as_u(__hmul2(s2, __float2half2_rn(kCentre<VB>))) & 0xFFFFu;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + (4 * w + i) * kVSbo) = centred8<VB>(cs0, word[i], s2);
     } else {
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
@@ -721,16 +725,34 @@ __global__ void __launch_bounds__(kJoinThreads) kivi_prefix_join_kernel(const Ki
     int k = P <= t.blocks.d ? begin : (int)((long long)begin * t.blocks.d / P);
     while (k > 0 && share_begin(P, k, t.blocks) > begin) --k;
     while (share_begin(P, k + 1, t.blocks) <= begin) ++k;
-    for (; k < t.blocks.d && share_begin(P, k, t.blocks) < end; ++k) {
-      const float* slot = t.part + (size_t)(k + seg) * kSlotFloats;
-      const float m = slot[(size_t)kRows * kD + r], lp = slot[(size_t)kRows * (kD + 1) + r];
-      const float4 v = reinterpret_cast<const float4*>(slot)[c * kRows + r];
-      if (lp == 0.f) continue;  // the row saw nothing there
-      const float up = fmaxf(top, m), f = l == 0.f ? 0.f : exp2_approx(top - up), w = lp != lp ? 1.f : exp2_approx(m - up);
+    int last = P <= t.blocks.d ? end - 1 : (int)((long long)(end - 1) * t.blocks.d / P);
+    while (last > 0 && share_begin(P, last, t.blocks) >= end) --last;
+    while (last + 1 < t.blocks.d && share_begin(P, last + 1, t.blocks) < end) ++last;
+    constexpr int kBatch = 8;  // parts on their way at once
+    for (; k <= last; k += kBatch) {
+      float m[kBatch], lp[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const float* slot = t.part + (size_t)(min(k + e, last) + seg) * kSlotFloats;
+        m[e] = slot[(size_t)kRows * kD + r];
+        lp[e] = k + e <= last ? slot[(size_t)kRows * (kD + 1) + r] : 0.f;
+        v[e] = reinterpret_cast<const float4*>(slot)[c * kRows + r];
+      }
+      float up = top;
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) up = lp[e] == 0.f ? up : fmaxf(up, m[e]);  // 0: the row saw nothing there
+      const float f = l == 0.f ? 0.f : exp2_approx(top - up);
       top = up;
-      l = (f == 0.f ? 0.f : l * f) + (w == 0.f ? 0.f : lp * w);
-      auto add = [&](float x, float y) { return (f == 0.f ? 0.f : x * f) + (w == 0.f ? 0.f : y * w); };
-      o = make_float4(add(o.x, v.x), add(o.y, v.y), add(o.z, v.z), add(o.w, v.w));
+      l = f == 0.f ? 0.f : l * f;
+      o = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const float w = lp[e] == 0.f ? 0.f : lp[e] != lp[e] ? 1.f : exp2_approx(m[e] - up);
+        if (w == 0.f) continue;
+        l = fmaf(lp[e], w, l);
+        o = make_float4(fmaf(v[e].x, w, o.x), fmaf(v[e].y, w, o.y), fmaf(v[e].z, w, o.z), fmaf(v[e].w, w, o.w));
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
