@@ -29,16 +29,20 @@ namespace {
 // the 512 of TMEM.
 // Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 15 unpack keys and 16 - 21 values into
 // shared memory, warp 22 issues the products (and one is idle: registers are split by four warps). A row's maximum moves only when a score passes it by
-// 2^kSlack, so rescaling O is rare and left to the softmax warps.
+// 2^kRoom, so rescaling O is rare and left to the softmax warps.
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
 constexpr int kThreads = 768;
 constexpr uint32_t kColS = 112, kColO = 144;     // TMEM columns of S and of O
-constexpr int kVSbo = kGroupT * 16 + 16;         // V' of a group: from eight channels to the next (+ 16: other banks)
+constexpr int kVSbo = kTok * 16 + 16;            // V': from eight channels to the next (+ 16: other banks)
+// A row's weights are exp2(x - m + kUp), m its running maximum, which moves when a score passes it by kRoom (log2): one
+// beyond fp16's subnormals, 2^-26 of the maximum's, is lost. With the 5 and 10 of the tree kernels some row of 128 passes
+// its maximum in a third of the first tiles (keys with outlier channels), and each time the products wait.
+constexpr float kRoom = 14.f, kUp = 1.f;
 // REST: the keys' second parts
 template <int KB, int VB, bool REST>
 struct PrefixLayout {
-  static constexpr int kVRing = REST ? 4 : 6;              // groups of unpacked values
+  static constexpr int kVTiles = REST ? 1 : 2;             // tiles of unpacked values
   static constexpr int kKStages = REST ? 5 : 9, kVStages = REST ? 1 : 2;  // groups whose stored keys are on their way; a warp's values
   // a group's stored keys or values: codes, scales, zero-points
   static constexpr int kKCode = kGroupT * kD * KB / 8, kVCode = kGroupT * kD * VB / 8, kPart = kD * 2;
@@ -47,12 +51,12 @@ struct PrefixLayout {
   static constexpr int kOffQ = 0;                          // fp16 [2][128 x 128], K-major
   static constexpr int kOffK = kOffQ + 2 * 128 * kD * 2;   // [2] K' of a tile (112 rows), K-major
   static constexpr int kOffKr = kOffK + 2 * kK;            // [2] second parts of the keys
-  static constexpr int kOffV = kOffKr + 2 * kKr;           // [kVRing] V' of a group, tokens within eight channels
-  static constexpr int kOffKs = kOffV + kVRing * kV;       // [kKStages] stored keys of a group
+  static constexpr int kOffV = kOffKr + 2 * kKr;           // [kVTiles] V' of a tile, tokens within eight channels
+  static constexpr int kOffKs = kOffV + kVTiles * kV;       // [kKStages] stored keys of a group
   static constexpr int kOffVs = kOffKs + kKStages * kKStage;
   static constexpr int kOffUnit = kOffVs + kGroups * kVStages * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
   static constexpr int kOffBar = kOffUnit + 4 * 8 * 4;
-  static constexpr int kBars = 8 + 4 + 2 * kVRing + 2 * kKStages + 2 * kGroups * kVStages;
+  static constexpr int kBars = 8 + 4 + 2 * kVTiles + 2 * kKStages + 2 * kGroups * kVStages;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory of a block");
 };
@@ -279,7 +283,7 @@ struct Groups {
 template <int KB, int VB, bool REST>
 __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTreeArgs a, const float scale_log2) {
   using L = PrefixLayout<KB, VB, REST>;
-  constexpr int kVRing = L::kVRing, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr int kVTiles = L::kVTiles, kKStages = L::kKStages, kVStages = L::kVStages;
   extern __shared__ __align__(128) unsigned char sm[];
   float* unit = reinterpret_cast<float*>(sm + L::kOffUnit);
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [2] a row tile's queries are there
@@ -288,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   uint64_t* bar_o = bar_q + 6;                                      // [2] its value product is done
   uint64_t* k_full = bar_q + 8;                                     // [2] a tile's keys are unpacked
   uint64_t* k_empty = bar_q + 10;                                   // [2] and read
-  uint64_t* v_full = bar_q + 12;                                    // [kVRing] a group's values are unpacked
-  uint64_t* v_empty = v_full + kVRing;                              // [kVRing] and read
-  uint64_t* ks_full = v_empty + kVRing;                             // [kKStages] a group's stored keys landed
+  uint64_t* v_full = bar_q + 12;                                    // [kVTiles] a tile's values are unpacked
+  uint64_t* v_empty = v_full + kVTiles;                             // [kVTiles] and read
+  uint64_t* ks_full = v_empty + kVTiles;                            // [kKStages] a group's stored keys landed
   uint64_t* ks_empty = ks_full + kKStages;                          // [kKStages] and are unpacked
   uint64_t* vs_full = ks_empty + kKStages;                          // [kGroups][kVStages] a tile's group's stored values landed
   uint64_t* vs_empty = vs_full + kGroups * kVStages;                // and are unpacked
@@ -316,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       mbar_init(k_full + i, 4 * kGroups);
       mbar_init(k_empty + i, 1);
     }
-    for (int i = 0; i < kVRing; ++i) {
-      mbar_init(v_full + i, 2);
+    for (int i = 0; i < kVTiles; ++i) {
+      mbar_init(v_full + i, 2 * kGroups);
       mbar_init(v_empty + i, 1);
     }
     for (int i = 0; i < kKStages; ++i) {
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
     const uint32_t t_s = t_lane + r * kColS, t_o = t_lane + 2 * kColS + r * kColO;
     uint32_t n = 0;                 // tiles done
     bool first = true;
-    float rowc = 0.f, nm = FLT_MAX;  // log2 units per score unit; kRaise - running maximum
+    float rowc = 0.f, nm = FLT_MAX;  // log2 units per score unit; kUp - running maximum
     for (int p = at.p0; p < at.p1; ++p) {
       const bool last = tile + 1 == at.T;
       if (r == 0 || second(seg)) {
@@ -415,10 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
 #pragma unroll
         for (int i = 0; i < kTok / 2; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(x[i].x, x[i].y));
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowc;
-        const bool up = mx + nm > kSlack + kRaise;
+        const bool up = mx + nm > kRoom + kUp;
         if (__any_sync(0xFFFFFFFFu, up)) {
-          const float f = up ? exp2_approx((kRaise - mx) - nm) : 1.f;
-          if (up) nm = kRaise - mx;
+          const float f = up ? exp2_approx((kUp - mx) - nm) : 1.f;
+          if (up) nm = kUp - mx;
           if (!first) {  // the sums, once the value product of the tile before is done
             if (!wait_warp(bar_o + r, n - 1)) break;
             tmem_after();
@@ -560,22 +564,18 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       };
       if (!(warp & 1))
         for (int i = 0; i < kVStages; ++i) copy();
-      int sv = g, round = 0;  // the group's place in the ring, times around
 #pragma unroll 1
       for (int it = 0; it < n; ++it) {
         const int sg = it % kVStages;
-        if (round > 0 && !wait_warp(v_empty + sv, round + 1)) break;
+        const int sv = it % kVTiles;
+        if (it >= kVTiles && !wait_warp(v_empty + sv, it / kVTiles + 1)) break;
         if (!wait_warp(landed + sg, it / kVStages)) break;
-        unpack_values<VB>(cs0, a, len, h, t + g * kGroupT, 2 * (warp & 1), lane, stages + sg * L::kVStage, sm + L::kOffV + sv * L::kV);
+        unpack_values<VB>(cs0, a, len, h, t + g * kGroupT, 2 * (warp & 1), lane, stages + sg * L::kVStage,
+                          sm + L::kOffV + sv * L::kV + g * kGroupT * 16);
         fence_proxy_async_smem();
         arrive(taken + sg);
         if (lane == 0) mbar_arrive(v_full + sv);
         if (!(warp & 1) && !copy()) break;
-        sv += kGroups;
-        if (sv >= kVRing) {
-          sv -= kVRing;
-          ++round;
-        }
         t += kTok;
         if (++tile == at.T) {
           tile = t = 0;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         return true;
       };
       bool ok = true, starts = true;
-      int last_r = second(seg) ? 1 : 0, sv = 0, sv_round = 0;  // the next group's place in the ring of values, and times around
+      int last_r = second(seg) ? 1 : 0;
       ok = wait_warp(k_full, 0);
       for (int r = 0; ok && r <= last_r; ++r) ok = scores(r, 0, true);
       if (ok) commit_if(leader, k_empty);
@@ -615,17 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         const int it = p - at.p0, st = it & 1;
         const bool ends = tile + 1 == at.T, more = p + 1 < at.p1;
         const int nseg = ends ? seg + 1 : seg, next_r = !more ? -1 : ends ? (second(nseg) ? 1 : 0) : last_r;
-        int slot[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          slot[g] = sv;
-          if (ok) ok = wait_warp(v_full + sv, sv_round);
-          if (++sv == kVRing) {
-            sv = 0;
-            ++sv_round;
-          }
-        }
-        if (more && ok) ok = wait_warp(k_full + (st ^ 1), (it + 1) >> 1);
+        const int sv = it % kVTiles;
+        ok = wait_warp(v_full + sv, it / kVTiles);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if (ok && r <= last_r) {
@@ -634,17 +625,15 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
 #pragma unroll
             for (int i = 0; i < 2 * kGroups; ++i)
               umma_lo_ta<kHiV, tree_idesc(kColO, true)>(leader, tm + 2 * kColS + r * kColO, tm + r * kColS + 8 * i,
-                                                        v0 + slot[i / 2] * (L::kV / 16) + 16 * (i & 1), i > 0 || !starts);
+                                                        v0 + sv * (L::kV / 16) + 16 * i, i > 0 || !starts);
             commit_if(leader, bar_o + r);
-            if (r == last_r) {
-#pragma unroll
-              for (int g = 0; g < kGroups; ++g) commit_if(leader, v_empty + slot[g]);
-            }
+            if (r == last_r) commit_if(leader, v_empty + sv);
             // the scores of the next tile take the columns that this product reads
             if (r <= next_r && !(ok = wait_warp(bar_o + r, n[r]))) break;
             ++n[r];
           }
           if (ok && r <= next_r) {
+            if (r == 0 && !(ok = wait_warp(k_full + (st ^ 1), (it + 1) >> 1))) break;
             if (!(ok = scores(r, st ^ 1, ends))) break;
             if (r == next_r) commit_if(leader, k_empty + (st ^ 1));
           }
@@ -654,6 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         seg = nseg;
         tile = ends ? 0 : tile + 1;
       }
+      const int done = at.p1 - at.p0 - 1;  // the last arrival there is
+      if (ok) wait_warp(v_empty + done % kVTiles, done / kVTiles);
       if (!ok && leader) {  // let what was issued end before the memory goes
         mbar_wait_bounded(bar_s, n[0] & 1, 10000000ull);
         mbar_wait_bounded(bar_s + 1, n[1] & 1, 10000000ull);
