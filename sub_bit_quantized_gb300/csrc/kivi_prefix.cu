@@ -28,7 +28,7 @@ namespace {
 // from zero is never rounded to fp16 (as in the tree kernels). 96 tokens: 2 (112 + 144) fp32 columns are
 // the 512 of TMEM.
 // Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 15 unpack keys and 16 - 21 values into
-// shared memory, warp 22 issues the products (and one is idle: registers are split by four warps). A row's maximum moves only when a score passes it by
+// shared memory, warp 22 issues the products and warp 23 the copies of what is stored. A row's maximum moves only when a score passes it by
 // 2^kRoom, so rescaling O is rare and left to the softmax warps.
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
@@ -510,25 +510,16 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   } else {
     set_regs_down<kRegsOther>();
     if (warp < 16) {
-      // ================= keys: four warps a group, two such sets in turn; stored parts come by bulk copies =================
+      // ================= keys: four warps a group, two such sets in turn =================
       const CodeScale cs0;
       const int set = (warp - 8) >> 2;
-      Groups x(a, at, seg, tile), ahead = x;
+      Groups x(a, at, seg, tile);
       const int n = (at.p1 - at.p0) * kGroups;
-      auto copy = [&](int upto) {  // by the first warp: stored parts of groups below `upto`, each into the stage of group i - kKStages
-        for (; ahead.i < min(upto, n); ahead.next(a, at, 1)) {
-          const int sg = ahead.i % kKStages;
-          if (ahead.i >= kKStages && !wait_warp(ks_empty + sg, ahead.i / kKStages + 1)) return false;
-          if (lane == 0) copy_keys<KB, VB, REST>(a, len, ahead.h, ahead.t, sm + L::kOffKs + sg * L::kKStage, ks_full + sg);
-        }
-        return true;
-      };
       if (set) x.next(a, at, 1);
       int seen = 1;  // tiles whose stage was found empty (the first two are)
 #pragma unroll 1
       while (x.i < n) {
         const int it = x.p - at.p0, st = it & 1, sg = x.i % kKStages;
-        if (warp == 8 && !copy(x.i + kKStages - 1)) break;
         if (it > seen) {
           if (!wait_warp(k_empty + st, (it >> 1) + 1)) break;
           seen = it;
@@ -542,28 +533,12 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         x.next(a, at, 2);
       }
     } else if (warp < 16 + 2 * kGroups) {
-      // ================= values: two warps every third group, whose stored part the first copies tiles ahead =================
+      // ================= values: two warps every third group =================
       const CodeScale cs0;
       const int g = (warp - 16) >> 1, n = at.p1 - at.p0;
       int h = div_by(seg, a.row_tiles), t = tile * kTok;         // the tile's
-      int c_it = 0, c_seg = seg, c_tile = tile;                  // the next one to copy
-      unsigned char* stages = sm + L::kOffVs + g * kVStages * L::kVStage;
+      const unsigned char* stages = sm + L::kOffVs + g * kVStages * L::kVStage;
       uint64_t *landed = vs_full + g * kVStages, *taken = vs_empty + g * kVStages;
-      auto copy = [&]() {
-        if (c_it >= n) return true;
-        const int sg = c_it % kVStages;
-        if (c_it >= kVStages && !wait_warp(taken + sg, c_it / kVStages + 1)) return false;
-        if (lane == 0)
-          copy_values<KB, VB, REST>(a, len, div_by(c_seg, a.row_tiles), c_tile * kTok + g * kGroupT, stages + sg * L::kVStage, landed + sg);
-        ++c_it;
-        if (++c_tile == at.T) {
-          c_tile = 0;
-          ++c_seg;
-        }
-        return true;
-      };
-      if (!(warp & 1))
-        for (int i = 0; i < kVStages; ++i) copy();
 #pragma unroll 1
       for (int it = 0; it < n; ++it) {
         const int sg = it % kVStages;
@@ -575,12 +550,23 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         fence_proxy_async_smem();
         arrive(taken + sg);
         if (lane == 0) mbar_arrive(v_full + sv);
-        if (!(warp & 1) && !copy()) break;
         t += kTok;
         if (++tile == at.T) {
           tile = t = 0;
           h = div_by(++seg, a.row_tiles);
         }
+      }
+    } else if (warp == 17 + 2 * kGroups) {
+      // ================= copies: the stored keys and values of each group in turn, as stages become free =================
+      Groups x(a, at, seg, tile);
+      const int n = (at.p1 - at.p0) * kGroups;
+#pragma unroll 1
+      for (; x.i < n; x.next(a, at, 1)) {
+        const int it = x.p - at.p0, sg = x.i % kKStages, sv = x.g * kVStages + it % kVStages;
+        if (x.i >= kKStages && !wait_warp(ks_empty + sg, x.i / kKStages + 1)) break;
+        if (lane == 0) copy_keys<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffKs + sg * L::kKStage, ks_full + sg);
+        if (it >= kVStages && !wait_warp(vs_empty + sv, it / kVStages + 1)) break;
+        if (lane == 0) copy_values<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffVs + sv * L::kVStage, vs_full + sv);
       }
     } else if (warp == 16 + 2 * kGroups) {
       // ================= products: the warp walks together, one lane issues =================
