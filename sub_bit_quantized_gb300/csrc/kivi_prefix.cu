@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const TreeLens len = tree_lens(a, 0, kTok);
   const PrefixPlace at = prefix_place(a, len, blockIdx.x);
+  launch_dependents();
   if (at.p0 >= at.p1) return;
   const int rows_all = a.N * a.rep.d;
   if (warp == 16 + 2 * kGroups) {
@@ -671,6 +672,7 @@ __device__ __forceinline__ void combine_row(const KiviPrefixArgs& a, size_t at, 
         make_uint2(f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16));
 }
 __global__ void __launch_bounds__(kCombineThreads) kivi_prefix_combine_kernel(const KiviPrefixArgs a, const int rows) {
+  wait_behind();
   const int row = blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= rows) return;
   const int tok = div_by(row, a.heads), b = div_by(tok, a.tokens);
@@ -684,6 +686,7 @@ __global__ void __launch_bounds__(kCombineThreads) kivi_prefix_combine_kernel(co
 // it. A block takes eight rows of a KV head, a thread four channels of one of them.
 constexpr int kJoinThreads = 256, kJoinRows = 8;
 __global__ void __launch_bounds__(kJoinThreads) kivi_prefix_join_kernel(const KiviPrefixArgs a) {
+  wait_behind();
   const KiviTreeArgs& t = a.prefix;
   const int lane = threadIdx.x & 31, c = 4 * (threadIdx.x >> 5) + (lane >> 3), h = blockIdx.y;
   const int row = blockIdx.x * kJoinRows + (lane & 7);  // of the KV head
@@ -786,17 +789,18 @@ cudaError_t launch_kivi_prefix(const KiviPrefixArgs& args, cudaStream_t st) {
     t.ring = int_div(t.residual);
     e = t.v_bits == 2 ? launch_prefix_keys<2>(t, a.out_fp32, st) : launch_prefix_keys<4>(t, a.out_fp32, st);
   } else {
-    e = launch_kivi_tree(t, st);
+    t.chained = kChainedFirst;
+    e = launch_kivi_tree(t, st, kTreeAttend);
   }
+  // every further launch is early: the blocks of both passes share the GPU, and what joins them is there when they end
+  a.own.chained = kChainedBehind;
+  if (e == cudaSuccess) e = launch_kivi_tree(a.own, st, kTreeAttend);
+  if (e == cudaSuccess && !many) e = launch_kivi_tree(t, st, kTreeMerge);
+  if (e == cudaSuccess) e = launch_kivi_tree(a.own, st, kTreeMerge);
   if (e != cudaSuccess) return e;
-  if ((e = launch_kivi_tree(a.own, st)) != cudaSuccess) return e;
-  if (many) {
-    kivi_prefix_join_kernel<<<dim3((rows + kJoinRows - 1) / kJoinRows, t.H), kJoinThreads, 0, st>>>(a);
-  } else {
-    const int all = a.own.B * a.own.N * a.own.Hq, per = kCombineThreads / 32;
-    kivi_prefix_combine_kernel<<<(all + per - 1) / per, kCombineThreads, 0, st>>>(a, all);
-  }
-  return cudaGetLastError();
+  if (many) return launch_early(true, kivi_prefix_join_kernel, dim3((rows + kJoinRows - 1) / kJoinRows, t.H), kJoinThreads, 0, st, a);
+  const int all = a.own.B * a.own.N * a.own.Hq, per = kCombineThreads / 32;
+  return launch_early(true, kivi_prefix_combine_kernel, dim3((all + per - 1) / per), kCombineThreads, 0, st, a, all);
 }
 
 }  // namespace kvq

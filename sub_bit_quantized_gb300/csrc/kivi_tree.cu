@@ -319,9 +319,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     if (tid == 0) w = x;
     if (lane == 0) ahead = x;
   }
+  if (a.chained) launch_dependents();
   TreeShared sh = {n > 0 ? kSegBegins : kSegNoWork, -1, 0, 0};
   if (n == 0) {
     if (tid == 0) shared[blockIdx.x] = sh;
+    end_behind(a);
     return;
   }
   // The warp's ring: its key group of tile i is in stage i % kSt, copied kSt - 1 tiles ahead by its own lanes.
@@ -889,6 +891,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
     __syncthreads();
   }
   if (tid == 0) shared[blockIdx.x] = sh;
+  end_behind(a);
 }
 
 // ======================================================================================
@@ -1225,10 +1228,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     p1 = share.y;
     if (tid == 0) place[p0 & 1] = place_of(x);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge's blocks take places that become free
+  launch_dependents();  // the merge's blocks take places that become free
   TreeShared sh = {p0 < p1 ? kSegBegins : kSegNoWork, -1, 0, 0};
   if (p0 >= p1) {
     if (tid == 0) shared[blockIdx.x] = sh;
+    end_behind(a);
     return;
   }
 
@@ -1578,6 +1582,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
     tmem_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
   }
+  end_behind(a);
 }
 
 // Joins the partials of a segment that several blocks shared, in block order. Block (k, rows): the segment that
@@ -1585,7 +1590,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) kivi_tree_kernel(const KiviTr
 constexpr int kMergeThreads = 128;
 template <int ROWS>
 __global__ void __launch_bounds__(kMergeThreads, ROWS <= 16 ? 6 : 9) kivi_tree_merge_kernel(const KiviTreeArgs a, const int G) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead of the attention's end
+  launch_dependents();
+  wait_behind();  // launched ahead of the attention's end
   const int lane = threadIdx.x & 31, k = blockIdx.x, r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
   const TreeShared* shared = reinterpret_cast<const TreeShared*>(a.part);
   const float* slots = reinterpret_cast<const float*>(shared + G);
@@ -1680,21 +1686,8 @@ int tree_blocks(int r) {
   return device_sms() * (r == 8 ? 4 : r == 16 ? MmaLayout<2, 2, 2>::kBlocks : 2);
 }
 
-template <int ROWS>
-cudaError_t launch_merge(const KiviTreeArgs& a, int G, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(G, ROWS / (kMergeThreads / 32));
-  cfg.blockDim = kMergeThreads;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kivi_tree_merge_kernel<ROWS>, a, G);
-}
 template <int ROWS, typename K>
-cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& args, cudaStream_t st) {
+cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& args, int parts, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int G = tree_blocks(ROWS), rep = args.Hq / args.H, row_tiles = (args.N * rep + ROWS - 1) / ROWS;
@@ -1704,17 +1697,19 @@ cudaError_t launch_with(K kernel, int threads, int smem, const KiviTreeArgs& arg
   a.segs = int_div(a.H * row_tiles);
   a.blocks = int_div(G);
   a.ring = int_div(a.residual);
-  kernel<<<G, threads, smem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_merge<ROWS>(a, G, st);
+  if (parts & kTreeAttend)
+    e = launch_early(a.chained == kChainedBehind, kernel, dim3(G), threads, smem, st, a, 1.4426950408889634f / sqrtf((float)kD));
+  if (e == cudaSuccess && (parts & kTreeMerge))
+    e = launch_early(true, kivi_tree_merge_kernel<ROWS>, dim3(G, ROWS / (kMergeThreads / 32)), kMergeThreads, 0, st, a, G);
+  return e;
 }
 template <int KB, int VB>
-cudaError_t launch_tree_rows(const KiviTreeArgs& a, cudaStream_t st) {
+cudaError_t launch_tree_rows(const KiviTreeArgs& a, int parts, cudaStream_t st) {
   const int r = tree_rows(a.N * (a.Hq / a.H));
-  if (r == 8) return launch_with<8>(kivi_tree_mma_kernel<KB, VB, 1>, kMmaThreads, MmaLayout<KB, VB, 1>::kSmem, a, st);
-  if (r == 16) return launch_with<16>(kivi_tree_mma_kernel<KB, VB, 2>, kMmaThreads, MmaLayout<KB, VB, 2>::kSmem, a, st);
-  if (r == 32) return launch_with<32>(kivi_tree_kernel<KB, VB, 32>, kTreeThreads, TreeLayout<KB, VB, 32>::kSmem, a, st);
-  return launch_with<64>(kivi_tree_kernel<KB, VB, 64>, kTreeThreads, TreeLayout<KB, VB, 64>::kSmem, a, st);
+  if (r == 8) return launch_with<8>(kivi_tree_mma_kernel<KB, VB, 1>, kMmaThreads, MmaLayout<KB, VB, 1>::kSmem, a, parts, st);
+  if (r == 16) return launch_with<16>(kivi_tree_mma_kernel<KB, VB, 2>, kMmaThreads, MmaLayout<KB, VB, 2>::kSmem, a, parts, st);
+  if (r == 32) return launch_with<32>(kivi_tree_kernel<KB, VB, 32>, kTreeThreads, TreeLayout<KB, VB, 32>::kSmem, a, parts, st);
+  return launch_with<64>(kivi_tree_kernel<KB, VB, 64>, kTreeThreads, TreeLayout<KB, VB, 64>::kSmem, a, parts, st);
 }
 
 }  // namespace
@@ -1736,11 +1731,11 @@ long long kivi_tree_positions(int B, int N, int H, int Hq, int max_tokens, int r
   return (long long)B * H * ((rows + r - 1) / r) * (((long long)max_tokens + residual + N + kTile - 1) / kTile);
 }
 
-cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t st) {
-  if (a.k_bits == 2 && a.v_bits == 2) return launch_tree_rows<2, 2>(a, st);
-  if (a.k_bits == 2) return launch_tree_rows<2, 4>(a, st);
-  if (a.v_bits == 2) return launch_tree_rows<4, 2>(a, st);
-  return launch_tree_rows<4, 4>(a, st);
+cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t st, int parts) {
+  if (a.k_bits == 2 && a.v_bits == 2) return launch_tree_rows<2, 2>(a, parts, st);
+  if (a.k_bits == 2) return launch_tree_rows<2, 4>(a, parts, st);
+  if (a.v_bits == 2) return launch_tree_rows<4, 2>(a, parts, st);
+  return launch_tree_rows<4, 4>(a, parts, st);
 }
 
 }  // namespace kvq

@@ -239,6 +239,7 @@ struct KiviTreeArgs {
   float* part;                     // workspace: what blocks share, partial softmaxes of those segments
   int* err;
   int B, N, H, Hq, k_bits, v_bits, max_tokens, residual;
+  int chained;                     // one of several passes of a call (kChained...), or 0
   // set by the launch: query heads of a KV head, row tiles of a KV head, segments of a request, blocks, ring rows
   IntDiv rep, row_tiles, segs, blocks, ring;
 };
@@ -246,7 +247,9 @@ struct KiviTreeArgs {
 size_t kivi_tree_ws_bytes(int B, int N, int H, int Hq, int k_bits, int v_bits);
 // tile positions of a launch whose requests are full (below 2^31: checked by the host)
 long long kivi_tree_positions(int B, int N, int H, int Hq, int max_tokens, int residual);
-cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t s);
+enum { kChainedFirst = 1, kChainedBehind = 2 };  // the pass before is none; one that this does not depend on
+enum { kTreeAttend = 1, kTreeMerge = 2 };
+cudaError_t launch_kivi_tree(const KiviTreeArgs& a, cudaStream_t s, int parts = kTreeAttend | kTreeMerge);
 
 // ---------------------------------------------------------------- attention under a shared prefix
 struct KiviPrefixArgs {
