@@ -18,9 +18,9 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStage = 16;     // hazards that a full-width unit row stages (32 KB)
+constexpr int kStage = 8;      // hazards that a full-width row of units stages (16 KB)
 constexpr int kBatch = 8;      // moves whose loads are in flight together
-constexpr int kBlocks = 5;     // an SM, as the staging leaves room for
+constexpr int kBlocks = 7;     // an SM, as the staging leaves room for
 
 // What a slot holds. KIVI: tokens, quantized keys, quantized values; LoopVQ: tokens, index pages.
 struct Lens {
@@ -52,138 +52,161 @@ __device__ __forceinline__ int judge(const CacheForkArgs& a, int i, Move& m) {
   return L.a > a.room || L.n > a.max_ctx ? KVQ_ERR_CAPACITY : 0;
 }
 
-// Bytes of a line up to the last one that a slot of these lengths may hold
-__device__ __forceinline__ long long line_bytes(const CacheForkArgs& a, const ForkArray& x, const Lens& L) {
+// Eighths of a line's bytes up to the last one that a slot of these lengths may hold (rows are multiples of 8 bytes)
+__device__ __forceinline__ int line_eighths(const CacheForkArgs& a, const ForkArray& x, const Lens& L) {
+  const int row = x.row / 8;
   switch (x.kind) {
-    case kForkA: return (long long)L.a * x.row;
-    case kForkGroups: return (long long)(L.a / 32) * x.row;
-    case kForkB: return (long long)L.b * x.row;
-    case kForkTail: return (long long)(L.n - L.a) * x.row;
-    case kForkRing: return L.n > L.b ? (long long)a.ring * x.row : 0;
-    default: return (long long)(a.sink + a.ring) * x.row;  // window
+    case kForkA: return L.a * row;
+    case kForkGroups: return L.a / 32 * row;
+    case kForkB: return L.b * row;
+    case kForkTail: return (L.n - L.a) * row;
+    case kForkRing: return L.n > L.b ? a.ring * row : 0;
+    default: return (a.sink + a.ring) * row;  // window
   }
 }
-// Bytes (16, 8 or 0) of the unit at `off` of a line that a slot of these lengths holds
-__device__ __forceinline__ int unit_bytes(const CacheForkArgs& a, const ForkArray& x, const Lens& L, long long off, long long end) {
-  if (off >= end) return 0;
-  if (x.kind < kForkRing) return end - off >= 16 ? 16 : 8;  // rows are multiples of 8 bytes
-  int r = (int)off / x.row;  // a few rows
-  if (x.kind == kForkWindow) {
-    if (r < a.sink) return r < L.n ? 16 : 0;
-    r -= a.sink;
+// Rows of a ring (of the window's: behind the sink): `held` of them from `first` on, around its end
+struct Ring {
+  int first, held;
+};
+__device__ __forceinline__ Ring ring_of(const CacheForkArgs& a, const Lens& L) {
+  if (a.ring == 0) return {0, 0};
+  if (a.format == KVQ_FMT_KIVI) return {L.b % a.ring, L.n - L.b};
+  return {kPage * L.a % a.ring, L.n - a.sink - kPage * L.a};
+}
+__device__ __forceinline__ bool in_ring(const CacheForkArgs& a, int kind, int row, int n, const Ring& g) {
+  if (kind == kForkWindow) {
+    if (row < a.sink) return row < n;
+    row -= a.sink;
   }
-  // tokens t0 .. n - 1 in rows t % ring (window: (t - sink) % ring)
-  const int t0 = x.kind == kForkRing ? L.b : kPage * L.a, held = x.kind == kForkRing ? L.n - L.b : L.n - a.sink - t0;
-  int d = r - t0 % a.ring;
+  int d = row - g.first;
   if (d < 0) d += a.ring;
-  return d < held ? 16 : 0;
+  return d < g.held;
 }
 
 __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const CacheForkArgs a) {
   __shared__ __align__(16) uint4 stage[kStage * kThreads];
   __shared__ Move moves[KVQ_FORK_MAX];
-  __shared__ unsigned char is_move[KVQ_FORK_MAX], is_hazard[KVQ_FORK_MAX];
-  __shared__ long long longest[kForkArrays], upto[kForkArrays + 1];
+  __shared__ Ring rings[KVQ_FORK_MAX];
+  __shared__ int ends[kForkArrays][KVQ_FORK_MAX];  // eighths of a line that a move has
+  __shared__ unsigned char is_move[KVQ_FORK_MAX];
+  __shared__ int longest[kForkArrays], upto[kForkArrays + 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, n = a.n;
-  Move mine[KVQ_FORK_MAX / kThreads];
+  constexpr int kMine = KVQ_FORK_MAX / kThreads, kWords = KVQ_FORK_MAX / 32;
+  Move mine[kMine];
 #pragma unroll
-  for (int k = 0; k < KVQ_FORK_MAX / kThreads; ++k) {
+  for (int k = 0; k < kMine; ++k) {
     const int i = tid + k * kThreads;
-    if (i < n) is_move[i] = judge(a, i, mine[k]) == 0;
+    is_move[i] = i < n && judge(a, i, mine[k]) == 0;
   }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < KVQ_FORK_MAX / kThreads; ++k) {
-    const int i = tid + k * kThreads, s = i < n && is_move[i] ? mine[k].src - a.b0 : -1;
-    if (i < n) is_hazard[i] = a.same && s >= 0 && s < n && is_move[s];
-  }
+  if (tid < kForkArrays) longest[tid] = 0;
   __syncthreads();
   // the list of moves, hazards first
+  uint32_t moved[kWords], hazard[kWords];
   int hazards = 0, total = 0;
-  for (int base = 0; base < n; base += 32) {
-    const bool in = base + lane < n;
-    const unsigned h = __ballot_sync(0xFFFFFFFFu, in && is_hazard[base + lane]);
-    const unsigned m = __ballot_sync(0xFFFFFFFFu, in && is_move[base + lane]);
-    hazards += __popc(h);
-    total += __popc(m);
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    moved[w] = hazard[w] = 0;
+    if (32 * w < n) {
+      const int i = 32 * w + lane, s = is_move[i] ? a.source[i] - a.b0 : -1;
+      moved[w] = __ballot_sync(0xFFFFFFFFu, is_move[i]);
+      hazard[w] = __ballot_sync(0xFFFFFFFFu, a.same && s >= 0 && s < n && is_move[s]);
+      hazards += __popc(hazard[w]);
+      total += __popc(moved[w]);
+    }
   }
   if (total == 0) return;
 #pragma unroll
-  for (int k = 0; k < KVQ_FORK_MAX / kThreads; ++k) {
+  for (int k = 0; k < kMine; ++k) {
     const int i = tid + k * kThreads;
-    if (i >= n || !is_move[i]) continue;
-    int at = is_hazard[i] ? 0 : hazards;
-    for (int j = 0; j < i; ++j) at += is_move[j] && is_hazard[j] == is_hazard[i];
+    if (!is_move[i]) continue;
+    int before_h = 0, before_o = 0;
+    bool h = false;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const uint32_t below = w < i >> 5 ? ~0u : w == i >> 5 ? (1u << (i & 31)) - 1 : 0u;
+      before_h += __popc(hazard[w] & below);
+      before_o += __popc(moved[w] & ~hazard[w] & below);
+      if (w == i >> 5) h = (hazard[w] >> (i & 31)) & 1;
+    }
+    const int at = h ? before_h : hazards + before_o;
     moves[at] = mine[k];
+    rings[at] = ring_of(a, mine[k].len);
+    for (int x = 0; x < a.n_arrays; ++x) {
+      const int e = line_eighths(a, a.array[x], mine[k].len);
+      ends[x][at] = e;
+      atomicMax(&longest[x], e);
+    }
   }
-  __syncthreads();
   // units across: as many as the hazards of each leave room for; the rest of the threads takes other moves of theirs
   int width = kThreads;
   while (hazards * width > kStage * kThreads) width >>= 1;
   const int unit = tid & (width - 1), group = tid / width, groups = kThreads / width;
-  for (int x = tid >> 5; x < a.n_arrays; x += kThreads / 32) {
-    long long most = 0;
-    for (int i = lane; i < total; i += 32) most = max(most, line_bytes(a, a.array[x], moves[i].len));
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, off));
-    if (lane == 0) longest[x] = most;
-  }
   __syncthreads();
   if (tid == 0) {
     upto[0] = 0;
     for (int x = 0; x < a.n_arrays; ++x)
-      upto[x + 1] = upto[x] + (longest[x] + width * 16 - 1) / (width * 16) * a.array[x].outer * a.heads;
+      upto[x + 1] = upto[x] + (longest[x] + 2 * width - 1) / (2 * width) * a.array[x].outer * a.heads;
   }
   __syncthreads();
-  const long long pieces = upto[a.n_arrays];
-  for (long long p = blockIdx.x; p < pieces; p += gridDim.x) {
+  // without hazards any moves of a piece may go to any block: kBatch of them each
+  const int runs = hazards ? 1 : (total + kBatch - 1) / kBatch;
+  const long long tasks = (long long)upto[a.n_arrays] * runs;
+  for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int p = hazards ? (int)task : (int)(task / runs), run = hazards ? 0 : (int)(task - (long long)p * runs);
     int xi = 0;
     while (p >= upto[xi + 1]) ++xi;
     const ForkArray& x = a.array[xi];
-    const int lines = x.outer * a.heads;
-    const long long rel = p - upto[xi], piece = rel / lines;
-    const int line = (int)(rel - piece * lines), o = line / a.heads, h = line - o * a.heads;
-    const long long off = (piece * width + unit) * 16;
-    const unsigned char* src = x.src + o * x.src_outer + h * x.src_head + off;
-    unsigned char* dst = x.dst + o * x.dst_outer + h * x.dst_head + off;
-    auto bytes = [&](const Move& m) { return unit_bytes(a, x, m.len, off, line_bytes(a, x, m.len)); };
-    auto load = [&](const Move& m, int k) {
-      const unsigned char* at = src + m.src * x.src_slot;
-      if (k == 16) return *reinterpret_cast<const uint4*>(at);
-      const uint2 u = *reinterpret_cast<const uint2*>(at);
-      return make_uint4(u.x, u.y, 0u, 0u);
+    const int kind = x.kind, lines = x.outer * a.heads, rel = p - upto[xi], piece = rel / lines;
+    const int line = rel - piece * lines, o = line / a.heads, h = line - o * a.heads;
+    const int mine_at = 2 * (piece * width + unit);  // the thread's unit of the line, in eighths
+    const unsigned char* src = x.src + o * x.src_outer + h * x.src_head + mine_at * 8ll;
+    unsigned char* dst = x.dst + o * x.dst_outer + h * x.dst_head + mine_at * 8ll;
+    const int ring_row = kind >= kForkRing ? mine_at / (x.row / 8) : 0;
+    // what move i has of the unit: 16 bytes (2), 8 (1) or none
+    auto has = [&](int i) {
+      const int left = ends[xi][i] - mine_at;
+      if (left <= 0) return 0;
+      if (kind >= kForkRing) return in_ring(a, kind, ring_row, moves[i].len.n, rings[i]) ? 2 : 0;
+      return left >= 2 ? 2 : 1;
     };
-    auto store = [&](const Move& m, int k, const uint4& v) {
-      unsigned char* at = dst + m.dst * x.dst_slot;
-      if (k == 16) *reinterpret_cast<uint4*>(at) = v;
+    auto load = [&](int i, int k) {
+      const unsigned char* at = src + moves[i].src * x.src_slot;
+      if (k == 2) return *reinterpret_cast<const uint4*>(at);
+      const uint2 v = *reinterpret_cast<const uint2*>(at);
+      return make_uint4(v.x, v.y, 0u, 0u);
+    };
+    auto store = [&](int i, int k, const uint4& v) {
+      unsigned char* at = dst + moves[i].dst * x.dst_slot;
+      if (k == 2) *reinterpret_cast<uint4*>(at) = v;
       else *reinterpret_cast<uint2*>(at) = make_uint2(v.x, v.y);
     };
     if (hazards > 0) {
       int st = tid;
       for (int i = group; i < hazards; i += groups, st += kThreads) {
-        const int k = bytes(moves[i]);
-        if (k) stage[st] = load(moves[i], k);
+        const int k = has(i);
+        if (k) stage[st] = load(i, k);
       }
       if (groups > 1) __syncthreads();  // other threads write what these have read
     }
-    for (int i0 = hazards + group; i0 < total; i0 += kBatch * groups) {
+    for (int i0 = hazards + run * kBatch + group; i0 < total; i0 += kBatch * groups) {
       uint4 v[kBatch];
       int k[kBatch];
 #pragma unroll
       for (int e = 0; e < kBatch; ++e) {
         const int i = i0 + e * groups;
-        k[e] = i < total ? bytes(moves[i]) : 0;
-        if (k[e]) v[e] = load(moves[i], k[e]);
+        k[e] = i < total ? has(i) : 0;
+        if (k[e]) v[e] = load(i, k[e]);
       }
 #pragma unroll
       for (int e = 0; e < kBatch; ++e)
-        if (k[e]) store(moves[i0 + e * groups], k[e], v[e]);
+        if (k[e]) store(i0 + e * groups, k[e], v[e]);
+      if (hazards == 0) break;  // the next ones are another task's
     }
     int st = tid;
     for (int i = group; i < hazards; i += groups, st += kThreads) {
-      const int k = bytes(moves[i]);
-      if (k) store(moves[i], k, stage[st]);
+      const int k = has(i);
+      if (k) store(i, k, stage[st]);
     }
   }
 }

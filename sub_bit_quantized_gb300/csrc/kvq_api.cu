@@ -728,6 +728,8 @@ KVQ_API kvq_status kvq_cache_fork(int format, const void* cfg, const void* cache
   long long pieces = 0;  // of 2 KB, of the longest slots there can be
   for (int i = 0; i < a.n_arrays; ++i)
     pieces += (std::min(a.array[i].src_head, a.array[i].dst_head) + 2047) / 2048 * a.array[i].outer * a.heads;
+  if (pieces >= (1ll << 27) || (long long)a.room * 64 >= (1ll << 31) || (long long)a.from_room * 64 >= (1ll << 31))
+    return fail(KVQ_ERR_UNSUPPORTED, "%s: slots too large for one call", __func__);
   a.format = format; a.source = source; a.b0 = b0; a.n = n; a.err = device_error_ptr();
   return cuda_status(kvq::launch_cache_fork(a, pieces, (cudaStream_t)stream), __func__);
 }
