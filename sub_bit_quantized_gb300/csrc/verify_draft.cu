@@ -35,6 +35,40 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
+// A number in two floats, lo what hi's rounding left: sums and products are off by 2^-45 of themselves at most. (fp64
+// operations run at 1/64 of the rate here and take a warp some hundred cycles each in a row.)
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two norm(float h, float l) {  // |l| <= |h|
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Two plus(Two x, Two y) {
+  const float h = __fadd_rn(x.hi, y.hi), b = __fsub_rn(h, x.hi);
+  const float e = __fadd_rn(__fsub_rn(x.hi, __fsub_rn(h, b)), __fsub_rn(y.hi, b));
+  return norm(h, __fadd_rn(e, __fadd_rn(x.lo, y.lo)));
+}
+__device__ __forceinline__ Two minus(Two x, Two y) { return plus(x, {-y.hi, -y.lo}); }
+__device__ __forceinline__ Two times(Two x, Two y) {
+  const float h = __fmul_rn(x.hi, y.hi);
+  return norm(h, __fadd_rn(__fmaf_rn(x.hi, y.hi, -h), __fmaf_rn(x.hi, y.lo, __fmul_rn(x.lo, y.hi))));
+}
+__device__ __forceinline__ bool less(Two x, Two y) { return x.hi < y.hi || (x.hi == y.hi && x.lo < y.lo); }
+__device__ __forceinline__ Two shfl(Two x, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
+}
+// the sums of lanes 0 .. lane, of `lanes` lanes
+__device__ __forceinline__ Two scan(Two x, int lane, int lanes) {
+  for (int off = 1; off < lanes; off <<= 1) {
+    const Two y = {__shfl_up_sync(0xFFFFFFFFu, x.hi, off), __shfl_up_sync(0xFFFFFFFFu, x.lo, off)};
+    if (lane >= off) x = plus(y, x);
+  }
+  return x;
+}
+__device__ __forceinline__ uint64_t bits(Two x) { return (uint64_t)__float_as_uint(x.hi) << 32 | __float_as_uint(x.lo); }
+__device__ __forceinline__ Two two(uint64_t b) { return {__uint_as_float((uint32_t)(b >> 32)), __uint_as_float((uint32_t)b)}; }
+
 __device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
 __device__ __forceinline__ float2 sub2(float2 x, float2 y) { return __fadd2_rn(x, neg2(y)); }
@@ -47,20 +81,13 @@ struct Sum2 {
     lo = __fadd2_rn(lo, __fadd2_rn(sub2(hi, sub2(h, b)), sub2(x, b)));
     hi = h;
   }
-  // of the warp's lanes: the sum of both, in fp32 pairs, since fp64 adds take the unit 16 cycles a warp
-  __device__ __forceinline__ double total() {
-    float h = hi.x, l = __fadd_rn(lo.x, lo.y);
-    auto plus = [&](float x, float y) {
-      const float s = __fadd_rn(h, x), b = __fsub_rn(s, h);
-      l = __fadd_rn(l, __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(x, b)), y));
-      h = s;
-    };
-    plus(hi.y, 0.f);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) plus(__shfl_xor_sync(0xFFFFFFFFu, h, off), __shfl_xor_sync(0xFFFFFFFFu, l, off));
-    return (double)h + (double)l;
-  }
+  __device__ __forceinline__ Two total() const { return plus(norm(hi.x, lo.x), norm(hi.y, lo.y)); }
 };
+__device__ __forceinline__ Two warp_sum(Two x) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x = plus(x, {__shfl_xor_sync(0xFFFFFFFFu, x.hi, off), __shfl_xor_sync(0xFFFFFFFFu, x.lo, off)});
+  return x;
+}
 
 // w = max(0, p - a q) in two floats (hi, lo), of two entries; a in two floats
 struct Weight2 {
@@ -135,7 +162,7 @@ __device__ __forceinline__ int entry16(int v, int j, int lane, bool wide) {
 }
 
 struct Shared {
-  double chunk[kMaxChunks];
+  Two chunk[kMaxChunks];
   uint64_t total[2][kMaxCluster];  // of the cluster's blocks, by turns
   uint64_t best[kWarps];
   int path[kMaxNodes], gone[kMaxNodes];
@@ -208,6 +235,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       const T* row = P + node * a.p_st;
       constexpr int kLoad = sizeof(T) == 4 ? 4 : 8;  // entries of a 16-byte load
       const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;  // v0 is a multiple of 512
+      // most likely the first child is accepted: this block's slice of its row on its way meanwhile
+      const uint64_t first = nodes.children(node, node + 1);
+      if (first && tid == 0) {
+        const T* to = P + (__ffsll(first) - 1) * a.p_st + v0;
+        const uint32_t n = min(v1 - v0, 1 << 24) * (uint32_t)sizeof(T) & ~15u;
+        if ((reinterpret_cast<uintptr_t>(to) & 15) == 0 && n) bulk_prefetch_l2(to, n);
+      }
       float top = -INFINITY;
       int at = 0x7FFFFFFF;
       auto look = [&](float x, int i) {
@@ -300,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
   const int n_chunks = (v1 - v0 + a.chunk - 1) / a.chunk;
   int node = 0, at = 1, count = 1;   // warp 0's
   uint64_t gone = 0;                 // children of the node that were rejected (point masses)
-  double wa = 0.0, wz = 1.0;
+  Two wa = {0.f, 0.f}, wz = {1.f, 0.f};
   bool fallback = false;
   if (tid == 0) s.path[0] = 0;
   for (;;) {
@@ -312,22 +346,26 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         const int i = __ffsll(m) - 1;
         at = i + 1;
         const float q = of_node(qz, i), p = of_node(pz, i), ui = of_node(u, i);
-        double w = (double)p;
-        if (Q) w = fmax(w - wa * (double)q, 0.0);
-        else if (gone) w = (gone & nodes.say(of_node(nodes.token, i))) ? 0.0 : w;
-        if ((double)ui * wz * (double)q < w) {
+        Two w = {p, 0.f};
+        if (Q) {
+          const Weight2 y = weight(f2(p), f2(q), wa.hi, wa.lo);
+          w = {y.hi.x, y.lo.x};
+        } else if (gone && (gone & nodes.say(of_node(nodes.token, i)))) {
+          w.hi = 0.f;
+        }
+        if (less(times(times({ui, 0.f}, {q, 0.f}), wz), w)) {
           if (lane == 0) s.path[count] = i;
           ++count;
           node = i;
-          wa = 0.0;
-          wz = 1.0;
+          wa = {0.f, 0.f};
+          wz = {1.f, 0.f};
           gone = 0;
         } else if (Q) {
-          wa += wz;
+          wa = plus(wa, wz);
           rejected = true;
           break;
         } else {
-          wz -= w;
+          wz = minus(wz, w);
           gone |= 1ull << i;
         }
       }
@@ -337,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       if (lane == 0) {
         s.node = node;
         s.n_gone = __popcll(gone);
-        s.a_hi = (float)wa;
-        s.a_lo = (float)(wa - (double)s.a_hi);
+        s.a_hi = wa.hi;
+        s.a_lo = wa.lo;
         s.done = 0;
       }
     }
@@ -380,46 +418,39 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
           for (int i = 0; i < 8; ++i) sum.add(p[i]);
         }
       }
-      const double t = sum.total();
+      const Two t = warp_sum(sum.total());
       if (lane == 0) s.chunk[c] = t;
     }
     __syncthreads();
     // ---- warp 0: runs of chunks a lane, the block's total to every block ----
     const int run = (n_chunks + 31) / 32;
-    double upto = 0.0;  // the block's sum up to the end of the lane's run
+    Two upto = {0.f, 0.f};  // the block's sum up to the end of the lane's run
     if (warp == 0) {
-      for (int c = lane * run; c < min(n_chunks, (lane + 1) * run); ++c) upto += s.chunk[c];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xFFFFFFFFu, upto, off);
-        if (lane >= off) upto += y;
-      }
-      const double mine = __shfl_sync(0xFFFFFFFFu, upto, 31);
-      if (lane < C) store_remote(&s.total[turn][rank], lane, __double_as_longlong(mine));
+      for (int c = lane * run; c < min(n_chunks, (lane + 1) * run); ++c) upto = plus(upto, s.chunk[c]);
+      upto = scan(upto, lane, 32);
+      const Two mine = shfl(upto, 31);
+      if (lane < C) store_remote(&s.total[turn][rank], lane, bits(mine));
     }
     cluster_wait();
     if (warp == 0) {
-      double end = lane < C ? __longlong_as_double(s.total[turn][lane]) : 0.0;  // the sum up to the end of block `lane`
-#pragma unroll
-      for (int off = 1; off < kMaxCluster; off <<= 1) {
-        const double y = __shfl_up_sync(0xFFFFFFFFu, end, off);
-        if (lane >= off) end += y;
-      }
-      const double total = __shfl_sync(0xFFFFFFFFu, end, C - 1);
+      Two end = {0.f, 0.f};  // the sum up to the end of block `lane`
+      if (lane < C) end = two(s.total[turn][lane]);
+      end = scan(end, lane, C);
+      const Two total = shfl(end, C - 1);
       // a rejection with a later child left to test: on; else these are the draw's sums. A residual without mass: P's
-      const bool more = rejected && nodes.children(node, at), empty = !more && !fallback && !(total > 0.0);
+      const bool more = rejected && nodes.children(node, at), empty = !more && !fallback && !(total.hi > 0.f);
       if (more) {
         wz = total;
       } else if (empty) {
         fallback = true;
-        wa = 0.0;
+        wa = {0.f, 0.f};
         gone = 0;
       } else {
         // ---- the draw: the block, the chunk, the entry in which the sums pass u total ----
-        const double target = (double)__shfl_sync(0xFFFFFFFFu, u[0], 0) * total;
+        const Two target = times({__shfl_sync(0xFFFFFFFFu, u[0], 0), 0.f}, total);
         // each block's end is the next one's beginning, so exactly one holds the target; without mass any token does
-        const unsigned past = __ballot_sync(0xFFFFFFFFu, lane < C && end > target);
-        const double before = __shfl_sync(0xFFFFFFFFu, end, rank > 0 ? (int)rank - 1 : 0);
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, lane < C && less(target, end));
+        const Two before = shfl(end, rank > 0 ? (int)rank - 1 : 0);
         if (rank == 0) {
           for (int i = lane; i < count; i += 32) a.path[(size_t)b * a.N + i] = s.path[i];
           if (lane == 0) {
@@ -428,15 +459,15 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
           }
         }
         if (past && __ffs(past) - 1 == (int)rank) {
-          double base = rank > 0 ? before : 0.0;
-          const unsigned in = __ballot_sync(0xFFFFFFFFu, base + upto > target);
+          Two base = rank > 0 ? before : Two{0.f, 0.f};
+          const unsigned in = __ballot_sync(0xFFFFFFFFu, less(target, plus(base, upto)));
           const int last_run = (n_chunks - 1) / run, hold = in ? min(__ffs(in) - 1, last_run) : last_run;
-          const double y = __shfl_sync(0xFFFFFFFFu, upto, hold > 0 ? hold - 1 : 0);
-          if (hold > 0) base += y;
+          const Two y = shfl(upto, hold > 0 ? hold - 1 : 0);
+          if (hold > 0) base = plus(base, y);
           int c = hold * run;
           for (; c + 1 < min(n_chunks, (hold + 1) * run); ++c) {
-            const double e = base + s.chunk[c];
-            if (e > target) break;
+            const Two e = plus(base, s.chunk[c]);
+            if (less(target, e)) break;
             base = e;
           }
           const int c0 = v0 + c * a.chunk, c1 = min(v1, c0 + a.chunk);
@@ -458,7 +489,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
                 if (j == g) (j & 1 ? p[j >> 1].y : p[j >> 1].x) = 0.f;
             }
             float hi[16], lo[16];
-            double sum = 0.0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               Weight2 w = {p[i], f2(0.f)};
@@ -474,14 +504,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
               if (hi[j] > 0.f) last = v + 16 * lane + j;
               if (hi[j + 1] > 0.f) last = v + 16 * lane + j + 1;
             }
-            sum = ((double)t.hi.x + (double)t.hi.y) + ((double)t.lo.x + (double)t.lo.y);
-            double end16 = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-              const double z = __shfl_up_sync(0xFFFFFFFFu, end16, off);
-              if (lane >= off) end16 += z;
-            }
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, base + end16 > target);
+            const Two end16 = scan(t.total(), lane, 32);
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, less(target, plus(base, end16)));
             if (hit) {  // that lane's entries, one a lane
               const int src = __ffs(hit) - 1;
               float h = 0.f, l = 0.f;
@@ -493,18 +517,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
                   l = z;
                 }
               }
-              double e = (double)h + (double)l;
-#pragma unroll
-              for (int off = 1; off < 16; off <<= 1) {
-                const double z = __shfl_up_sync(0xFFFFFFFFu, e, off);
-                if (lane >= off) e += z;
-              }
-              const double at16 = src > 0 ? __shfl_sync(0xFFFFFFFFu, end16, src - 1) : 0.0;
-              const unsigned one = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f && base + at16 + e > target);
+              const Two e = scan({h, l}, lane, 16);
+              const Two at16 = shfl(end16, src > 0 ? src - 1 : 0), from = src > 0 ? plus(base, at16) : base;
+              const unsigned one = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f && less(target, plus(from, e)));
               const unsigned some = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f);
               found = v + 16 * src + (one ? __ffs(one) - 1 : some ? 31 - __clz(some) : 0);
             }
-            base += __shfl_sync(0xFFFFFFFFu, end16, 31);
+            base = plus(base, shfl(end16, 31));
           }
 #pragma unroll
           for (int off = 16; off >= 1; off >>= 1) last = max(last, __shfl_xor_sync(0xFFFFFFFFu, last, off));
