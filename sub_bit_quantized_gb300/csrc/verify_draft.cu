@@ -26,7 +26,6 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxNodes = 64;
 constexpr int kMaxChunks = 1024;   // of a block
 constexpr int kMaxCluster = 8;
@@ -112,6 +111,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// the same in two steps: every block's shared memory is there behind the second
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_began() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void store_remote(void* p, uint32_t rank, uint64_t v) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
@@ -161,18 +163,31 @@ __device__ __forceinline__ int entry16(int v, int j, int lane, bool wide) {
   return wide ? v + 128 * (j >> 2) + 4 * lane + (j & 3) : v + 32 * j + lane;
 }
 
-struct Shared {
-  Two chunk[kMaxChunks];
-  uint64_t total[2][kMaxCluster];  // of the cluster's blocks, by turns
-  uint64_t best[kWarps];
-  int path[kMaxNodes], gone[kMaxNodes];
-  int bad, node, n_gone, done;
-  float a_hi, a_lo;
+// Of the cluster's blocks, by turns: what each found
+struct Exchange {
+  uint64_t total[2][kMaxCluster];
 };
-
 // The nodes of a request: lane l of every warp holds nodes l and l + 32
 struct Nodes {
   int token[2], parent[2];
+  // Of nd nodes; those that count have a parent before them and a token of the vocabulary. false: some has not (every
+  // warp of every block sees the same).
+  __device__ __forceinline__ bool load(const VerifyArgs& a, int b, int nd, int lane) {
+    bool ok = true;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      token[h] = parent[h] = -1;
+      if (i < a.N) {
+        token[h] = a.token[(size_t)b * a.N + i];
+        parent[h] = a.parent[(size_t)b * a.N + i];
+      }
+      if (i >= nd) token[h] = parent[h] = -1;
+      else ok = ok && token[h] >= 0 && token[h] < a.V && (i == 0 || (parent[h] >= 0 && parent[h] < i));
+      if (i == 0) parent[h] = -1;
+    }
+    return __all_sync(0xFFFFFFFFu, ok) != 0;
+  }
   // bit i: node i >= from is a child of `node` (and its token is x)
   __device__ __forceinline__ uint64_t children(int node, int from) const {
     const uint64_t m = (uint64_t)__ballot_sync(0xFFFFFFFFu, parent[0] == node) |
@@ -189,135 +204,172 @@ __device__ __forceinline__ V of_node(const V (&x)[2], int i) {
   return i < 32 ? lo : hi;
 }
 
+// A request of a kernel's cluster and the block's slice of the vocabulary
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
-  __shared__ Shared s;
-  const int C = a.blocks, b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = C > 1 ? cluster_rank() : 0;
-  const T* P = static_cast<const T*>(a.p) + b * a.p_sb;
-  const T* Q = a.q ? static_cast<const T*>(a.q) + b * a.q_sb : nullptr;
-  const int nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
-  // ---- the nodes; of those that count a parent before them and a token of the vocabulary (every warp sees the same) ----
-  Nodes nodes;
-  bool ok = true;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = lane + 32 * h;
-    nodes.token[h] = nodes.parent[h] = -1;
-    if (i < a.N) {
-      nodes.token[h] = a.token[(size_t)b * a.N + i];
-      nodes.parent[h] = a.parent[(size_t)b * a.N + i];
-    }
-    if (i >= nd) nodes.token[h] = nodes.parent[h] = -1;
-    else ok = ok && nodes.token[h] >= 0 && nodes.token[h] < a.V && (i == 0 || (nodes.parent[h] >= 0 && nodes.parent[h] < i));
-    if (i == 0) nodes.parent[h] = -1;
+struct Part {
+  int C, b, v0, v1, turn;
+  uint32_t rank;
+  bool began;
+  const T* P;
+  __device__ __forceinline__ explicit Part(const VerifyArgs& a) {
+    C = a.blocks;
+    b = blockIdx.x / C;
+    rank = C > 1 ? cluster_rank() : 0;
+    if (C > 1) cluster_begin();
+    began = C == 1;
+    P = static_cast<const T*>(a.p) + b * a.p_sb;
+    v0 = min(a.V, (int)rank * a.slice);
+    v1 = min(a.V, v0 + a.slice);
+    turn = 0;
   }
-  if (nd == 0 || !__all_sync(0xFFFFFFFFu, ok)) {  // the whole cluster
-    if (rank == 0 && tid == 0) {
+  __device__ __forceinline__ void begin() {  // before this block's first access to the others' memory
+    if (!began) cluster_began();
+    began = true;
+  }
+  __device__ __forceinline__ void wait() {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+  }
+  // a request without nodes, or with bad ones: the whole cluster leaves
+  __device__ __forceinline__ void leave(const VerifyArgs& a, int nd) {
+    begin();
+    if (rank == 0 && threadIdx.x == 0) {
       a.n_accept[b] = 0;
       if (nd > 0) set_error(a.err, KVQ_ERR_INVALID_ARG);
     }
-    return;
   }
-  const int v0 = min(a.V, (int)rank * a.slice), v1 = min(a.V, v0 + a.slice);
-  int turn = 0;
-  auto cluster_wait = [&]() {
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-  };
+};
 
-  if (!a.u) {
-    // ---- no sampling: the arg max of each node of the path ----
-    if (C > 1) cluster_sync();  // every block's shared memory is there
-    int node = 0, count = 1, best = 0;
-    if (tid == 0) s.path[0] = 0;
-    for (;;) {
-      const T* row = P + node * a.p_st;
-      constexpr int kLoad = sizeof(T) == 4 ? 4 : 8;  // entries of a 16-byte load
-      const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;  // v0 is a multiple of 512
-      // most likely the first child is accepted: this block's slice of its row on its way meanwhile
-      const uint64_t first = nodes.children(node, node + 1);
-      if (first && tid == 0) {
-        const T* to = P + (__ffsll(first) - 1) * a.p_st + v0;
-        const uint32_t n = min(v1 - v0, 1 << 24) * (uint32_t)sizeof(T) & ~15u;
-        if ((reinterpret_cast<uintptr_t>(to) & 15) == 0 && n) bulk_prefetch_l2(to, n);
-      }
-      float top = -INFINITY;
-      int at = 0x7FFFFFFF;
-      auto look = [&](float x, int i) {
-        if (x > top) {
-          top = x;
-          at = i;
-        }
-      };
-      constexpr int kAhead = 4;
-      int v = v0;
-      if (wide) {
-        constexpr int kStep = kLoad * kThreads;
-        for (; v + kStep <= v1; v += kAhead * kStep) {
-          uint4 u[kAhead];
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k)
-            if (v + (k + 1) * kStep <= v1) u[k] = __ldg(reinterpret_cast<const uint4*>(row + v + k * kStep) + tid);
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k)
-            if (v + (k + 1) * kStep <= v1) {
-              const T* t = reinterpret_cast<const T*>(&u[k]);
-#pragma unroll
-              for (int e = 0; e < kLoad; ++e) look(to_f(t[e]), v + k * kStep + kLoad * tid + e);
-            }
-        }
-        v = v0 + (v1 - v0) / kStep * kStep;
-      }
-      for (; v < v1; v += kAhead * kThreads) {
-        float x[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) x[k] = v + k * kThreads + tid < v1 ? to_f(row[v + k * kThreads + tid]) : -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) look(x[k], v + k * kThreads + tid);
-      }
-      // one number that is larger for larger values and, of equal ones, lower indices
-      auto key_of = [](float x, int i) {
-        const uint32_t f = __float_as_uint(x + 0.f);  // -0 counts as 0
-        return ((uint64_t)((f & 0x80000000u) ? ~f : f | 0x80000000u) << 32) | (0x7FFFFFFFu - (uint32_t)i);
-      };
-      uint64_t key = key_of(top, at);
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
-      if (lane == 0) s.best[warp] = key;
-      __syncthreads();
-      if (warp == 0) {
-        key = s.best[lane & (kWarps - 1)];
-#pragma unroll
-        for (int off = kWarps / 2; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
-        if (lane < C) store_remote(&s.total[turn][rank], lane, key);
-      }
-      cluster_wait();
-      key = lane < C ? s.total[turn][lane] : 0;
-#pragma unroll
-      for (int off = kMaxCluster / 2; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
-      key = __shfl_sync(0xFFFFFFFFu, key, 0);
-      turn ^= 1;
-      best = (int)(0x7FFFFFFFu - (uint32_t)key);
-      if (best == 0x7FFFFFFF) best = 0;  // nothing above the lowest value
-      const uint64_t next = nodes.children(node, node + 1) & nodes.say(best);
-      if (!next) break;
-      node = __ffsll(next) - 1;
-      if (tid == 0) s.path[count] = node;
-      ++count;
+// ---- no sampling: the arg max of each node of the path ----
+constexpr int kGreedyThreads = 512;
+template <typename T>
+__global__ void __launch_bounds__(kGreedyThreads, 2) verify_greedy_kernel(const VerifyArgs a) {
+  constexpr int kThreads = kGreedyThreads, kWarps = kThreads / 32;
+  __shared__ Exchange x;
+  __shared__ uint64_t best_of[kWarps];
+  __shared__ int path[kMaxNodes];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Part<T> part(a);
+  const int b = part.b, C = part.C, v0 = part.v0, v1 = part.v1;
+  const T* P = part.P;
+  const int nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
+  Nodes nodes;
+  const bool ok = nodes.load(a, b, nd, lane);
+  if (nd == 0 || !ok) return part.leave(a, nd);
+  int node = 0, count = 1, best = 0;
+  if (tid == 0) path[0] = 0;
+  for (;;) {
+    const T* row = P + node * a.p_st;
+    constexpr int kLoad = sizeof(T) == 4 ? 4 : 8;  // entries of a 16-byte load
+    const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;  // v0 is a multiple of 512
+    // most likely the first child is accepted: this block's slice of its row on its way meanwhile
+    const uint64_t first = nodes.children(node, node + 1);
+    if (first && tid == 0) {
+      const T* to = P + (__ffsll(first) - 1) * a.p_st + v0;
+      const uint32_t n = min(v1 - v0, 1 << 24) * (uint32_t)sizeof(T) & ~15u;
+      if ((reinterpret_cast<uintptr_t>(to) & 15) == 0 && n) bulk_prefetch_l2(to, n);
     }
-    if (rank == 0 && warp == 0) {
-      __syncwarp();
-      for (int i = lane; i < count; i += 32) a.path[(size_t)b * a.N + i] = s.path[i];
-      if (lane == 0) {
-        a.n_accept[b] = count;
-        a.next[b] = best;
+    float top = -INFINITY;
+    int at = 0x7FFFFFFF;
+    auto look = [&](float x, int i) {
+      if (x > top) {
+        top = x;
+        at = i;
       }
+    };
+    constexpr int kAhead = 4;
+    int v = v0;
+    if (wide) {
+      constexpr int kStep = kLoad * kThreads;
+      for (; v + kStep <= v1; v += kAhead * kStep) {
+        uint4 u[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (v + (k + 1) * kStep <= v1) u[k] = __ldg(reinterpret_cast<const uint4*>(row + v + k * kStep) + tid);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (v + (k + 1) * kStep <= v1) {
+            const T* t = reinterpret_cast<const T*>(&u[k]);
+#pragma unroll
+            for (int e = 0; e < kLoad; ++e) look(to_f(t[e]), v + k * kStep + kLoad * tid + e);
+          }
+      }
+      v = v0 + (v1 - v0) / kStep * kStep;
     }
-    return;  // the last writes into this block's memory were those that the last barrier waited for
+    for (; v < v1; v += kAhead * kThreads) {
+      float x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) x[k] = v + k * kThreads + tid < v1 ? to_f(row[v + k * kThreads + tid]) : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) look(x[k], v + k * kThreads + tid);
+    }
+    // one number that is larger for larger values and, of equal ones, lower indices
+    auto key_of = [](float x, int i) {
+      const uint32_t f = __float_as_uint(x + 0.f);  // -0 counts as 0
+      return ((uint64_t)((f & 0x80000000u) ? ~f : f | 0x80000000u) << 32) | (0x7FFFFFFFu - (uint32_t)i);
+    };
+    uint64_t key = key_of(top, at);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+    if (lane == 0) best_of[warp] = key;
+    part.begin();
+    __syncthreads();
+    if (warp == 0) {
+      key = best_of[lane & (kWarps - 1)];
+#pragma unroll
+      for (int off = kWarps / 2; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+      if (lane < C) store_remote(&x.total[part.turn][part.rank], lane, key);
+    }
+    part.wait();
+    key = lane < C ? x.total[part.turn][lane] : 0;
+#pragma unroll
+    for (int off = kMaxCluster / 2; off >= 1; off >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, off));
+    key = __shfl_sync(0xFFFFFFFFu, key, 0);
+    part.turn ^= 1;
+    best = (int)(0x7FFFFFFFu - (uint32_t)key);
+    if (best == 0x7FFFFFFF) best = 0;  // nothing above the lowest value
+    const uint64_t next = nodes.children(node, node + 1) & nodes.say(best);
+    if (!next) break;
+    node = __ffsll(next) - 1;
+    if (tid == 0) path[count] = node;
+    ++count;
   }
+  if (part.rank == 0 && warp == 0) {
+    __syncwarp();
+    for (int i = lane; i < count; i += 32) a.path[(size_t)b * a.N + i] = path[i];
+    if (lane == 0) {
+      a.n_accept[b] = count;
+      a.next[b] = best;
+    }
+  }
+  // the last writes into this block's memory were those that the last barrier waited for
+}
 
-  // ---- sampling: warp 0 walks, all warps add ----
+// ---- sampling: warp 0 walks, all warps add ----
+// THREADS a block: 512 where every block has an SM of its own, else 256 with twice the registers (128 of a thread either
+// way: with 64 the pass's loads spill). 64 chains of 131072 entries: 33 us with 256, 39 with 512; 16 trees of 50021: 29
+// and 27; trees of points: 18 and 17.
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const VerifyArgs a) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ struct {
+    Two chunk[kMaxChunks];
+    Exchange x;
+    float w[2][512 + 32];            // the drawn entries' weights in order, in two floats each (16 a lane, padded)
+    int path[kMaxNodes], gone[kMaxNodes];
+    int node, n_gone, done;
+    float a_hi, a_lo;
+  } s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Part<T> part(a);
+  const int b = part.b, C = part.C, v0 = part.v0, v1 = part.v1;
+  const uint32_t rank = part.rank;
+  const T* P = part.P;
+  const T* Q = a.q ? static_cast<const T*>(a.q) + b * a.q_sb : nullptr;
+  const int nd = a.n_draft ? min(max(a.n_draft[b], 0), a.N) : a.N;
+  Nodes nodes;
+  const bool ok = nodes.load(a, b, nd, lane);
+  if (nd == 0 || !ok) return part.leave(a, nd);
   float pz[2] = {0.f, 0.f}, qz[2] = {1.f, 1.f}, u[2] = {0.f, 0.f};
   if (warp == 0) {
 #pragma unroll
@@ -330,7 +382,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       }
     }
   }
-  if (C > 1) cluster_sync();  // every block's shared memory is there
+  // the test of a child that is its node's first: u Q(x) < P(x)
+  uint64_t at_once = 0;
+  if (warp == 0) {
+    bool yes[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) yes[h] = less(times({u[h], 0.f}, {qz[h], 0.f}), {pz[h], 0.f});
+    at_once = (uint64_t)__ballot_sync(0xFFFFFFFFu, yes[0]) | (uint64_t)__ballot_sync(0xFFFFFFFFu, yes[1]) << 32;
+  }
   const int n_chunks = (v1 - v0 + a.chunk - 1) / a.chunk;
   int node = 0, at = 1, count = 1;   // warp 0's
   uint64_t gone = 0;                 // children of the node that were rejected (point masses)
@@ -345,6 +404,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         if (!m || fallback) break;
         const int i = __ffsll(m) - 1;
         at = i + 1;
+        if (wa.hi == 0.f && !gone && (at_once >> i & 1)) {
+          if (lane == 0) s.path[count] = i;
+          ++count;
+          node = i;
+          continue;
+        }
         const float q = of_node(qz, i), p = of_node(pz, i), ui = of_node(u, i);
         Two w = {p, 0.f};
         if (Q) {
@@ -422,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       if (lane == 0) s.chunk[c] = t;
     }
     __syncthreads();
+    part.begin();
     // ---- warp 0: runs of chunks a lane, the block's total to every block ----
     const int run = (n_chunks + 31) / 32;
     Two upto = {0.f, 0.f};  // the block's sum up to the end of the lane's run
@@ -429,12 +495,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       for (int c = lane * run; c < min(n_chunks, (lane + 1) * run); ++c) upto = plus(upto, s.chunk[c]);
       upto = scan(upto, lane, 32);
       const Two mine = shfl(upto, 31);
-      if (lane < C) store_remote(&s.total[turn][rank], lane, bits(mine));
+      if (lane < C) store_remote(&s.x.total[part.turn][rank], lane, bits(mine));
     }
-    cluster_wait();
+    part.wait();
     if (warp == 0) {
       Two end = {0.f, 0.f};  // the sum up to the end of block `lane`
-      if (lane < C) end = two(s.total[turn][lane]);
+      if (lane < C) end = two(s.x.total[part.turn][lane]);
       end = scan(end, lane, C);
       const Two total = shfl(end, C - 1);
       // a rejection with a later child left to test: on; else these are the draw's sums. A residual without mass: P's
@@ -473,50 +539,38 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
           const int c0 = v0 + c * a.chunk, c1 = min(v1, c0 + a.chunk);
           int last = c0, found = -1;  // last: the last entry with a weight, should roundings leave none past the target
           for (int v = c0; v < c1 && found < 0; v += 512) {
-            // 16 entries a lane, in order: v + 16 lane ..
             float2 p[8], q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int x = v + 16 * lane + 2 * i;
-              p[i] = make_float2(x < c1 ? to_f(row[x]) : 0.f, x + 1 < c1 ? to_f(row[x + 1]) : 0.f);
-              q[i] = f2(0.f);
-              if (qrow) q[i] = make_float2(x < c1 ? to_f(qrow[x]) : 0.f, x + 1 < c1 ? to_f(qrow[x + 1]) : 0.f);
-            }
-            for (int k = 0; k < n_gone; ++k) {
-              const int g = s.gone[k] - v - 16 * lane;
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j == g) (j & 1 ? p[j >> 1].y : p[j >> 1].x) = 0.f;
-            }
-            float hi[16], lo[16];
+            load16(row, v, c1, lane, wide, p);
+            if (qrow) load16(qrow, v, c1, lane, wide, q);
+            if (n_gone) drop_gone(p, v, min(c1, v + 512));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               Weight2 w = {p[i], f2(0.f)};
               if (qrow) w = weight(p[i], q[i], a_hi, a_lo);
-              hi[2 * i] = w.hi.x; hi[2 * i + 1] = w.hi.y;
-              lo[2 * i] = w.lo.x; lo[2 * i + 1] = w.lo.y;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int x = entry16(v, 2 * i + e, lane, wide) - v, at = x + (x >> 4);
+                s.w[0][at] = e ? w.hi.y : w.hi.x;
+                s.w[1][at] = e ? w.lo.y : w.lo.x;
+              }
             }
+            __syncwarp();
+            // 16 entries a lane, in order: v + 16 lane ..
+            const float *hi = s.w[0] + 17 * lane, *lo = s.w[1] + 17 * lane;
             Sum2 t = {f2(0.f), f2(0.f)};
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              t.add(make_float2(hi[j], hi[j + 1]));
+              const float2 x = make_float2(hi[j], hi[j + 1]);
+              t.add(x);
               t.lo = __fadd2_rn(t.lo, make_float2(lo[j], lo[j + 1]));
-              if (hi[j] > 0.f) last = v + 16 * lane + j;
-              if (hi[j + 1] > 0.f) last = v + 16 * lane + j + 1;
+              if (x.x > 0.f) last = v + 16 * lane + j;
+              if (x.y > 0.f) last = v + 16 * lane + j + 1;
             }
             const Two end16 = scan(t.total(), lane, 32);
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, less(target, plus(base, end16)));
             if (hit) {  // that lane's entries, one a lane
               const int src = __ffs(hit) - 1;
-              float h = 0.f, l = 0.f;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float x = __shfl_sync(0xFFFFFFFFu, hi[j], src), z = __shfl_sync(0xFFFFFFFFu, lo[j], src);
-                if (lane == j) {
-                  h = x;
-                  l = z;
-                }
-              }
+              const float h = lane < 16 ? s.w[0][17 * src + lane] : 0.f, l = lane < 16 ? s.w[1][17 * src + lane] : 0.f;
               const Two e = scan({h, l}, lane, 16);
               const Two at16 = shfl(end16, src > 0 ? src - 1 : 0), from = src > 0 ? plus(base, at16) : base;
               const unsigned one = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f && less(target, plus(from, e)));
@@ -524,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
               found = v + 16 * src + (one ? __ffs(one) - 1 : some ? 31 - __clz(some) : 0);
             }
             base = plus(base, shfl(end16, 31));
+            __syncwarp();  // the weights are read
           }
 #pragma unroll
           for (int off = 16; off >= 1; off >>= 1) last = max(last, __shfl_xor_sync(0xFFFFFFFFu, last, off));
@@ -532,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         if (lane == 0) s.done = 1;
       }
     }
-    turn ^= 1;
+    part.turn ^= 1;
     __syncthreads();
     if (s.done) return;  // the last writes into this block's memory were those that the last barrier waited for
   }
@@ -541,15 +596,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 template <typename T>
 cudaError_t launch_typed(const VerifyArgs& args, cudaStream_t st) {
   VerifyArgs a = args;
-  int C = 1;
+  int C = 1;  // two blocks an SM at most; a slice of 2048 entries at least
   while (C < kMaxCluster && a.B * C * 2 <= 2 * device_sms() && a.V / (2 * C) >= 2048) C *= 2;
   a.blocks = C;
   a.slice = ((a.V + C - 1) / C + 511) / 512 * 512;
   a.chunk = 512;
   while ((a.slice + a.chunk - 1) / a.chunk > kMaxChunks) a.chunk *= 2;
+  const bool few = a.B * C <= device_sms();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = (unsigned)(a.B * C);
-  cfg.blockDim = kThreads;
+  cfg.blockDim = !a.u ? kGreedyThreads : few ? 512 : 256;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -557,7 +613,8 @@ cudaError_t launch_typed(const VerifyArgs& args, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
+  if (!a.u) return cudaLaunchKernelEx(&cfg, verify_greedy_kernel<T>, a);
+  return few ? cudaLaunchKernelEx(&cfg, verify_kernel<T, 512>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<T, 256>, a);
 }
 
 }  // namespace
