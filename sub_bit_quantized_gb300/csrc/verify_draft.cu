@@ -88,18 +88,17 @@ __device__ __forceinline__ Two warp_sum(Two x) {
   return x;
 }
 
-// w = max(0, p - a q) in two floats (hi, lo), of two entries; a in two floats
+// w = max(0, p - a q) of two entries, not normalised: hi + lo. a q = h + l; where p - h is not negative, or small beside
+// them, what its rounding left is (p - d) - h.
 struct Weight2 {
   float2 hi, lo;
 };
 __device__ __forceinline__ Weight2 weight(float2 p, float2 q, float a_hi, float a_lo) {
-  const float2 h = __fmul2_rn(f2(a_hi), q), l = __ffma2_rn(f2(a_lo), q, __ffma2_rn(f2(a_hi), q, neg2(h)));  // a q = h + l
-  const float2 d = sub2(p, h), b = sub2(d, p);
-  const float2 e = sub2(sub2(sub2(p, sub2(d, b)), __fadd2_rn(h, b)), l);  // what d's rounding left, and l
-  const float2 s = __fadd2_rn(d, e), r = sub2(e, sub2(s, d));
+  const float2 h = __fmul2_rn(f2(a_hi), q), l = __ffma2_rn(f2(a_lo), q, __ffma2_rn(f2(a_hi), q, neg2(h)));
+  const float2 d = sub2(p, h), e = sub2(sub2(sub2(p, d), h), l), s = __fadd2_rn(d, e);
   Weight2 w;
-  w.hi = make_float2(s.x > 0.f ? s.x : 0.f, s.y > 0.f ? s.y : 0.f);
-  w.lo = make_float2(s.x > 0.f ? r.x : 0.f, s.y > 0.f ? r.y : 0.f);
+  w.hi = make_float2(s.x > 0.f ? d.x : 0.f, s.y > 0.f ? d.y : 0.f);
+  w.lo = make_float2(s.x > 0.f ? e.x : 0.f, s.y > 0.f ? e.y : 0.f);
   return w;
 }
 
@@ -123,15 +122,16 @@ __device__ __forceinline__ void store_remote(void* p, uint32_t rank, uint64_t v)
       : "memory");
 }
 
-// 16 entries of a row for a lane, 0 from `end` on. kWide (the row's address allows it): piece k, entries 4 k + e, is at
-// v + 128 k + 4 lane + e, in loads of four entries; else entry j at v + 32 j + lane, one by one, so that a warp's loads
-// stay contiguous at any alignment.
+// Eight entries of a row for a lane, 0 from `end` on. wide (the row's address allows it): entries 4 k + e are at v + 128 k +
+// 4 lane + e, in loads of four; else entry j is at v + 32 j + lane, one by one, so that a warp's loads stay contiguous at
+// any alignment.
+constexpr int kStep = 256;  // entries of a warp's step
 template <typename T>
-__device__ __forceinline__ void load16(const T* row, int v, int end, int lane, bool wide, float2 (&x)[8]) {
-  float y[16];
+__device__ __forceinline__ void load8(const T* row, int v, int end, int lane, bool wide, float2 (&x)[4]) {
+  float y[8];
   if (wide) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const int at = v + 128 * k + 4 * lane;
       if (at + 4 <= end) {
         if constexpr (sizeof(T) == 4) {
@@ -150,17 +150,24 @@ __device__ __forceinline__ void load16(const T* row, int v, int end, int lane, b
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const int at = v + 32 * j + lane;
       y[j] = at < end ? to_f(row[at]) : 0.f;
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
 }
 // which entry that is
-__device__ __forceinline__ int entry16(int v, int j, int lane, bool wide) {
+__device__ __forceinline__ int entry8(int v, int j, int lane, bool wide) {
   return wide ? v + 128 * (j >> 2) + 4 * lane + (j & 3) : v + 32 * j + lane;
+}
+
+// A row's entries v0 .. v1 - 1 on their way to L2, whole 16-byte pieces of them
+template <typename T>
+__device__ __forceinline__ void fetch_row(const T* row, int v0, int v1) {
+  const uintptr_t from = (reinterpret_cast<uintptr_t>(row + v0) + 15) & ~(uintptr_t)15, to = reinterpret_cast<uintptr_t>(row + v1) & ~(uintptr_t)15;
+  if (from < to) bulk_prefetch_l2(reinterpret_cast<const void*>(from), (uint32_t)min((unsigned long long)(to - from), 1ull << 28));
 }
 
 // Of the cluster's blocks, by turns: what each found
@@ -264,11 +271,7 @@ __global__ void __launch_bounds__(kGreedyThreads, 2) verify_greedy_kernel(const 
     const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0;  // v0 is a multiple of 512
     // most likely the first child is accepted: this block's slice of its row on its way meanwhile
     const uint64_t first = nodes.children(node, node + 1);
-    if (first && tid == 0) {
-      const T* to = P + (__ffsll(first) - 1) * a.p_st + v0;
-      const uint32_t n = min(v1 - v0, 1 << 24) * (uint32_t)sizeof(T) & ~15u;
-      if ((reinterpret_cast<uintptr_t>(to) & 15) == 0 && n) bulk_prefetch_l2(to, n);
-    }
+    if (first && tid == 0) fetch_row(P + (__ffsll(first) - 1) * a.p_st, v0, v1);
     float top = -INFINITY;
     int at = 0x7FFFFFFF;
     auto look = [&](float x, int i) {
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
     Exchange x;
     float w[2][512 + 32];            // the drawn entries' weights in order, in two floats each (16 a lane, padded)
     int path[kMaxNodes], gone[kMaxNodes];
-    int node, n_gone, done;
+    int node, n_gone, done, c0, found;  // done: 1 the request is, 2 but for the draw from the chunk at c0
     float a_hi, a_lo;
   } s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
         Two w = {p, 0.f};
         if (Q) {
           const Weight2 y = weight(f2(p), f2(q), wa.hi, wa.lo);
-          w = {y.hi.x, y.lo.x};
+          w = plus({y.hi.x, 0.f}, {y.lo.x, 0.f});
         } else if (gone && (gone & nodes.say(of_node(nodes.token, i)))) {
           w.hi = 0.f;
         }
@@ -452,39 +455,55 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
     const bool wide = (reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) == 0 &&
                       (!qrow || (reinterpret_cast<uintptr_t>(qrow) & (4 * sizeof(T) - 1)) == 0);
     const int n_gone = s.n_gone;
-    // P without what was rejected
-    auto drop_gone = [&](float2 (&x)[8], int v, int end) {
-      for (int k = 0; k < n_gone; ++k) {
-        const int g = s.gone[k];
-        if (g < v || g >= end) continue;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (entry16(v, j, lane, wide) == g) (j & 1 ? x[j >> 1].y : x[j >> 1].x) = 0.f;
-      }
+    auto is_gone = [&](int v) {
+      bool g = false;
+      for (int k = 0; k < n_gone; ++k) g = g || s.gone[k] == v;
+      return g;
     };
-    // ---- sums of w over the block's chunks ----
-    for (int c = warp; c < n_chunks; c += kWarps) {
-      const int c0 = v0 + c * a.chunk, c1 = min(v1, c0 + a.chunk);
-      Sum2 sum = {f2(0.f), f2(0.f)};
-      for (int v = c0; v < c1; v += 512) {
-        float2 p[8], q[8];
-        load16(row, v, c1, lane, wide, p);
+    // ---- sums of w over the block's chunks; a step's entries are on their way while the one before is added ----
+    const int per = a.chunk / kStep, steps = warp < n_chunks ? ((n_chunks - 1 - warp) / kWarps + 1) * per : 0;
+    float2 p[4], q[4], pn[4], qn[4];
+    Sum2 sum = {f2(0.f), f2(0.f)};
+    int at_v = 0, at_end = 0;  // the step that is added
+#pragma unroll 1
+    for (int k = 0; k <= steps; ++k) {
+      const int c = warp + k / per * kWarps, c0 = v0 + c * a.chunk, v = c0 + k % per * kStep, end = min(v1, c0 + a.chunk);
+      if (k < steps) {
+        load8(row, v, end, lane, wide, pn);
+        if (qrow) load8(qrow, v, end, lane, wide, qn);
+      }
+      if (k > 0) {
         if (qrow) {
-          load16(qrow, v, c1, lane, wide, q);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             const Weight2 w = weight(p[i], q[i], a_hi, a_lo);
             sum.add(w.hi);
             sum.lo = __fadd2_rn(sum.lo, w.lo);
           }
         } else {
-          if (n_gone) drop_gone(p, v, min(c1, v + 512));
+          for (int g = 0; g < n_gone; ++g) {
+            const int x = s.gone[g];
+            if (x < at_v || x >= min(at_end, at_v + kStep)) continue;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum.add(p[i]);
+            for (int j = 0; j < 8; ++j)
+              if (entry8(at_v, j, lane, wide) == x) (j & 1 ? p[j >> 1].y : p[j >> 1].x) = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum.add(p[i]);
+        }
+        if (k % per == 0) {
+          const Two t = warp_sum(sum.total());
+          if (lane == 0) s.chunk[warp + (k - 1) / per * kWarps] = t;
+          sum = {f2(0.f), f2(0.f)};
         }
       }
-      const Two t = warp_sum(sum.total());
-      if (lane == 0) s.chunk[c] = t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = pn[i];
+        q[i] = qn[i];
+      }
+      at_v = v;
+      at_end = end;
     }
     __syncthreads();
     part.begin();
@@ -498,6 +517,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
       if (lane < C) store_remote(&s.x.total[part.turn][rank], lane, bits(mine));
     }
     part.wait();
+    Two target = {0.f, 0.f}, base = {0.f, 0.f};
     if (warp == 0) {
       Two end = {0.f, 0.f};  // the sum up to the end of block `lane`
       if (lane < C) end = two(s.x.total[part.turn][lane]);
@@ -513,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
         gone = 0;
       } else {
         // ---- the draw: the block, the chunk, the entry in which the sums pass u total ----
-        const Two target = times({__shfl_sync(0xFFFFFFFFu, u[0], 0), 0.f}, total);
+        target = times({__shfl_sync(0xFFFFFFFFu, u[0], 0), 0.f}, total);
         // each block's end is the next one's beginning, so exactly one holds the target; without mass any token does
         const unsigned past = __ballot_sync(0xFFFFFFFFu, lane < C && less(target, end));
         const Two before = shfl(end, rank > 0 ? (int)rank - 1 : 0);
@@ -525,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
           }
         }
         if (past && __ffs(past) - 1 == (int)rank) {
-          Two base = rank > 0 ? before : Two{0.f, 0.f};
+          if (rank > 0) base = before;
           const unsigned in = __ballot_sync(0xFFFFFFFFu, less(target, plus(base, upto)));
           const int last_run = (n_chunks - 1) / run, hold = in ? min(__ffs(in) - 1, last_run) : last_run;
           const Two y = shfl(upto, hold > 0 ? hold - 1 : 0);
@@ -536,60 +556,66 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
             if (less(target, e)) break;
             base = e;
           }
-          const int c0 = v0 + c * a.chunk, c1 = min(v1, c0 + a.chunk);
-          int last = c0, found = -1;  // last: the last entry with a weight, should roundings leave none past the target
-          for (int v = c0; v < c1 && found < 0; v += 512) {
-            float2 p[8], q[8];
-            load16(row, v, c1, lane, wide, p);
-            if (qrow) load16(qrow, v, c1, lane, wide, q);
-            if (n_gone) drop_gone(p, v, min(c1, v + 512));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              Weight2 w = {p[i], f2(0.f)};
-              if (qrow) w = weight(p[i], q[i], a_hi, a_lo);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int x = entry16(v, 2 * i + e, lane, wide) - v, at = x + (x >> 4);
-                s.w[0][at] = e ? w.hi.y : w.hi.x;
-                s.w[1][at] = e ? w.lo.y : w.lo.x;
-              }
-            }
-            __syncwarp();
-            // 16 entries a lane, in order: v + 16 lane ..
-            const float *hi = s.w[0] + 17 * lane, *lo = s.w[1] + 17 * lane;
-            Sum2 t = {f2(0.f), f2(0.f)};
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float2 x = make_float2(hi[j], hi[j + 1]);
-              t.add(x);
-              t.lo = __fadd2_rn(t.lo, make_float2(lo[j], lo[j + 1]));
-              if (x.x > 0.f) last = v + 16 * lane + j;
-              if (x.y > 0.f) last = v + 16 * lane + j + 1;
-            }
-            const Two end16 = scan(t.total(), lane, 32);
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, less(target, plus(base, end16)));
-            if (hit) {  // that lane's entries, one a lane
-              const int src = __ffs(hit) - 1;
-              const float h = lane < 16 ? s.w[0][17 * src + lane] : 0.f, l = lane < 16 ? s.w[1][17 * src + lane] : 0.f;
-              const Two e = scan({h, l}, lane, 16);
-              const Two at16 = shfl(end16, src > 0 ? src - 1 : 0), from = src > 0 ? plus(base, at16) : base;
-              const unsigned one = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f && less(target, plus(from, e)));
-              const unsigned some = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f);
-              found = v + 16 * src + (one ? __ffs(one) - 1 : some ? 31 - __clz(some) : 0);
-            }
-            base = plus(base, shfl(end16, 31));
-            __syncwarp();  // the weights are read
+          if (lane == 0) {
+            s.c0 = v0 + c * a.chunk;
+            s.found = -1;
+            s.done = 2;
           }
-#pragma unroll
-          for (int off = 16; off >= 1; off >>= 1) last = max(last, __shfl_xor_sync(0xFFFFFFFFu, last, off));
-          if (lane == 0) a.next[b] = found >= 0 ? found : last;
+        } else if (lane == 0) {
+          s.done = 1;
         }
-        if (lane == 0) s.done = 1;
       }
     }
     part.turn ^= 1;
     __syncthreads();
-    if (s.done) return;  // the last writes into this block's memory were those that the last barrier waited for
+    if (s.done == 1) return;  // the last writes into this block's memory were those that the last barrier waited for
+    if (s.done == 2) {
+      // ---- the chunk that holds the target, 512 entries at a time: an entry a thread, then 16 a lane of warp 0 ----
+      const int c1 = min(v1, s.c0 + a.chunk);
+      int last = s.c0;  // the last entry with a weight, should roundings leave none past the target
+      for (int v = s.c0; v < c1; v += 512) {
+        for (int i = tid; i < 512; i += THREADS) {
+          const int x = v + i;
+          float p = x < c1 ? to_f(row[x]) : 0.f;
+          const float q = qrow && x < c1 ? to_f(qrow[x]) : 0.f;
+          if (n_gone && is_gone(x)) p = 0.f;
+          const Weight2 w = weight(f2(p), f2(q), a_hi, a_lo);  // p without a row of Q
+          const Two y = plus({w.hi.x, 0.f}, {w.lo.x, 0.f});
+          s.w[0][i + (i >> 4)] = y.hi;
+          s.w[1][i + (i >> 4)] = y.lo;
+        }
+        __syncthreads();
+        if (warp == 0) {
+          const float *hi = s.w[0] + 17 * lane, *lo = s.w[1] + 17 * lane;
+          Two t = {0.f, 0.f};
+#pragma unroll 4
+          for (int j = 0; j < 16; ++j) {
+            t = plus(t, {hi[j], lo[j]});
+            if (hi[j] > 0.f) last = v + 16 * lane + j;
+          }
+          const Two upto16 = scan(t, lane, 32);
+          const unsigned hit = __ballot_sync(0xFFFFFFFFu, less(target, plus(base, upto16)));
+          if (hit) {  // that lane's entries, one a lane
+            const int src = __ffs(hit) - 1;
+            const float h = lane < 16 ? s.w[0][17 * src + lane] : 0.f, l = lane < 16 ? s.w[1][17 * src + lane] : 0.f;
+            const Two e = scan({h, l}, lane, 16);
+            const Two at16 = shfl(upto16, src > 0 ? src - 1 : 0), from = src > 0 ? plus(base, at16) : base;
+            const unsigned some = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f);
+            const unsigned one = __ballot_sync(0xFFFFFFFFu, lane < 16 && h > 0.f && less(target, plus(from, e)));
+            if (lane == 0) s.found = v + 16 * src + (one ? __ffs(one) - 1 : some ? 31 - __clz(some) : 0);
+          }
+          base = plus(base, shfl(upto16, 31));
+        }
+        __syncthreads();
+        if (s.found >= 0) break;
+      }
+      if (warp == 0) {
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) last = max(last, __shfl_xor_sync(0xFFFFFFFFu, last, off));
+        if (lane == 0) a.next[b] = s.found >= 0 ? s.found : last;
+      }
+      return;
+    }
   }
 }
 
