@@ -6,7 +6,7 @@
 //   o = (2^(L0 - M) o0 + 2^(L1 - M) o1) / (2^(L0 - M) + 2^(L1 - M)),  M = max(L0, L1).
 // Over the prefix the rows of all requests are rows of one matrix per KV head; over its own tokens a
 // request is a tree without the prefix (kivi_tree.cu), which writes fp32 outputs and L into the
-// workspace. Up to 64 rows a KV head the prefix, too, is one request of the tree kernels; more rows take
+// workspace. Up to 32 rows a KV head the prefix, too, is one request of the tree kernels; more rows take
 // the kernel below, which unpacks a tile of the prefix once for 256 of them.
 #include <cfloat>
 
@@ -16,20 +16,36 @@ namespace kvq {
 namespace {
 
 // ======================================================================================
-// More than 64 rows: tcgen05 on tiles of 96 tokens and 2 x 128 rows
+// More than 32 rows: tcgen05 on tiles of 96 tokens and 2 x 128 rows
 // ======================================================================================
 //
-//   S [128 rows x 112] = q [128 x 128] . K'^T      K' = 96 tokens s (c - c0), exact in one fp16 at 2 bits and in
-//                                                  two at 4 (below), and rows of the groups' constants s (z - c0)
+//   S [128 rows x 112] = q [128 x 128] . K'^T      K' = 96 tokens s (c - c0) and rows of the groups' constants
+//                                                  s (z - c0)
 //   P = exp2(S c - m)                              a thread owns a row; P takes the columns of S
 //   O [128 rows x 144] += P [128 x 96] . V'        V' = 128 channels s (c - c0), and columns of the tokens'
 //                                                  constants s z, c0 s and of ones, whose sums are the weights'
 // The constants enter as further tokens and channels of the same two products, so what a group lies off
 // from zero is never rounded to fp16 (as in the tree kernels). 96 tokens: 2 (112 + 144) fp32 columns are
 // the 512 of TMEM.
-// Roles: warps 0 - 7 softmax (two row tiles, a thread a row), 8 - 15 unpack keys and 16 - 21 values into
-// shared memory, warp 22 issues the products and warp 23 the copies of what is stored. A row's maximum moves only when a score passes it by
-// 2^kRoom, so rescaling O is rare and left to the softmax warps.
+// s (c - c0) is exact in one fp16 at 2 bits. At 4 bits it takes two for fp32 outputs (REST: a second product with what
+// the rounding left); for bf16 outputs it is rounded once, by 2^-11 of itself, which moves a score by at most
+// 2^-11 sum |q s (c - c0)| / sqrt(D) and adds little to the output's own rounding (relative error against fp64 1.8e-3, of
+// the rounding alone 1.7e-3). 512 rows over 32768 tokens: 142 us rounded, 198 in two parts.
+//
+// Roles: warps 0 - 7 softmax (two row tiles, a thread a row); 8 - 15 unpack keys, four warps a 32-token group; 16 - 21
+// unpack values, two warps a group; 22 issues the products; 23 copies what is stored of the groups ahead. Products and
+// softmax of the two row tiles alternate: a tile's scores take the columns of its weights, so the score product waits for
+// the value product. A row's maximum moves only when a score passes it by 2^kRoom, so rescaling O is rare and left to the
+// softmax warps.
+//
+// Bound: the chain of a row tile (16 requests x 8 drafts x 4 heads, 32768 tokens, 4 and 2 bits: 36 tiles a block, 4600
+// cycles each): score product 500 cycles, softmax 1700 - 2300, value product 450, and the barriers between them 900; issue
+// 45 % of the cycles. What it took (the same case, whole call): the tree kernels, four row tiles of 64 that unpack the
+// prefix each, 360 us; unpacking by four warps in unrolled code 220 (as many stalls on instruction fetch as issues);
+// rolled loops by group 187; products issued by a warp that walks together 193 -> 182 with one part of the keys; two
+// warps a group of values 179; loops of four code words 170; kRoom 14 for 10 163; copies by a warp of their own 157;
+// passes launched early 144. Tried and dropped: the softmax in pieces with the scores read twice (204 against 187), loads
+// of codes two groups ahead into registers (192: their moves wait for them), spinning on barriers (266).
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
 constexpr int kThreads = 768;
@@ -371,7 +387,15 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       if (r == 0 || second(seg)) {
         const int h = div_by(seg, a.row_tiles), rt = seg - h * a.row_tiles.d, row0 = rt * kRows + 128 * r;
         if (first) {
-          // the tile's queries: 8 lanes a row, four rows a warp at a time
+          // the tile's queries, every row on its way before the first is waited for: 8 lanes a row, four rows a warp at a time
+          {
+            const int row = row0 + row_t, di = div_by(row, a.rep);
+            if (row < rows_all) {
+              const uint16_t* src = a.q + ((size_t)di * a.Hq + (size_t)h * a.rep.d + row - di * a.rep.d) * kD;
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+            }
+          }
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             const int rr = 32 * (warp & 3) + 4 * i + (lane >> 3), c = lane & 7;
@@ -526,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
           seen = it;
         }
         if (!wait_warp(ks_full + sg, x.i / kKStages)) break;
-        unpack_keys<KB, REST>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage, sm + L::kOffK + st * L::kK,
-                        sm + L::kOffKr + st * L::kKr, unit + (x.p & 3) * 8);
+        unpack_keys<KB, REST>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage,
+                              sm + L::kOffK + st * L::kK, sm + L::kOffKr + st * L::kKr, unit + (x.p & 3) * 8);
         fence_proxy_async_smem();
         arrive(ks_empty + sg);
         if (lane == 0) mbar_arrive(k_full + st);
@@ -561,14 +585,20 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       // ================= copies: the stored keys and values of each group in turn, as stages become free =================
       Groups x(a, at, seg, tile);
       const int n = (at.p1 - at.p0) * kGroups;
+      int copied = 0;
 #pragma unroll 1
       for (; x.i < n; x.next(a, at, 1)) {
         const int it = x.p - at.p0, sg = x.i % kKStages, sv = x.g * kVStages + it % kVStages;
         if (x.i >= kKStages && !wait_warp(ks_empty + sg, x.i / kKStages + 1)) break;
         if (lane == 0) copy_keys<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffKs + sg * L::kKStage, ks_full + sg);
+        copied = x.i + 1;  // of its values at most
         if (it >= kVStages && !wait_warp(vs_empty + sv, it / kVStages + 1)) break;
         if (lane == 0) copy_values<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffVs + sv * L::kVStage, vs_full + sv);
       }
+      // nothing is in flight when the block ends, also where a wait ran out: the last copy into every stage
+      for (int i = max(0, copied - kKStages); i < copied; ++i) mbar_wait_bounded(ks_full + i % kKStages, (i / kKStages) & 1, 10000000ull);
+      for (int i = max(0, copied - kGroups * kVStages); i < copied; ++i)
+        mbar_wait_bounded(vs_full + i % kGroups * kVStages + i / kGroups % kVStages, (i / kGroups / kVStages) & 1, 10000000ull);
     } else if (warp == 16 + 2 * kGroups) {
       // ================= products: the warp walks together, one lane issues =================
       const uint32_t leader = elect_one();
@@ -756,8 +786,10 @@ cudaError_t launch_prefix_keys(const KiviTreeArgs& a, bool fp32, cudaStream_t st
   return fp32 ? launch_prefix_rows<4, VB, true>(a, st) : launch_prefix_rows<4, VB, false>(a, st);
 }
 
-// Rows of a KV head from which on the kernel of this file takes the prefix
-bool many_rows(int rows) { return rows > 64; }
+// Rows of a KV head from which on the kernel above takes the prefix. Measured with it and with the tree kernels (8 KV heads,
+// 4 bits, whole call): 32 rows over 8192 tokens 46 / 44 us, 64 rows 46 / 49, 128 rows 46 / 55; 64 rows over 1024 tokens 28 /
+// 33; 32 KV heads, 2 bits, 4096 tokens: 32 rows 71 / 63, 128 rows 138 / 155.
+bool many_rows(int rows) { return rows > 32; }
 int row_tiles(int rows) { return (rows + kRows - 1) / kRows; }
 
 }  // namespace

@@ -20,8 +20,9 @@ def prefix_reference(case: T.TreeCase, prefix: C.KiviCase, slot: int, drafts: bo
     (with ``drafts``) the drafted tokens of their mask; rows of padding tokens are NaN in out.
 
     The roundings are those that tests/_drafts.py counts, over both contexts: elements of stored keys and values by
-    2^-11 of themselves and of |s z|, scores by 2^-16 of their absolute sum, weights by 2^-11, weights below 2^-30 of
-    the largest lost. Joining the two parts adds a few fp32 steps to each (log2 of a sum: 2^-21 of the weight, two
+    2^-11 of themselves and of |s z|, scores by 2^-16 of their absolute sum, weights by 2^-11, weights below 2^-26 of
+    the largest lost (the kernel for many rows takes weights up to 2^15 and lets the largest start at 2^1; half a step of
+    an fp16 subnormal is 2^-25: each of n weights is off by at most 2^-26 of the largest). Joining the two parts adds a few fp32 steps to each (log2 of a sum: 2^-21 of the weight, two
     products, a sum, a reciprocal: under 2^-19 of sum p |v|), which 2^-16 of it covers together with the rest."""
     base = case.base
     B, N, Hq, _ = case.q.shape
@@ -50,7 +51,7 @@ def prefix_reference(case: T.TreeCase, prefix: C.KiviCase, slot: int, drafts: bo
                     f = np.expm1(((dk + 2.0 ** -16 * keys)[seen] @ np.abs(q)) / np.sqrt(D)) + T.U16
                     ps, av = p[seen], vals[seen]
                     bound[b, i, hq] = 1.1 * ((ps * (f + ps @ f)) @ av + ps @ dv[seen] +
-                                             seen.sum() * 2.0 ** -30 * ps.max() * av.max() + 2.0 ** -16 * (ps @ av))
+                                             seen.sum() * 2.0 ** -26 * ps.max() * av.max() + 2.0 ** -16 * (ps @ av))
     return out, bound
 
 

@@ -42,6 +42,61 @@ def test_prefix_rows_and_bits(B, H, rep, N, kb, vb):
     T.check_rows(K.run_prefix(case, prefix), ref, bound, 7.0)
 
 
+@pytest.mark.parametrize("kb,vb", [(4, 4), (4, 2), (2, 2)])
+@pytest.mark.parametrize("B,H,rep,N", [(11, 2, 3, 1), (33, 1, 4, 1), (13, 1, 4, 5)])
+def test_prefix_bf16_outputs_of_many_rows(B, H, rep, N, kb, vb):
+    # 4-bit keys enter rounded to one fp16: 2^-11 of themselves, which the bound counts; then half a step of bf16
+    case, prefix = prefix_case(B * 10 + N, B, H, rep, N, (32, 9), (288, 50), kb, vb)
+    ref, bound = K.prefix_reference(case, prefix, 0)
+    got = K.run_prefix(case, prefix, dtype=torch.bfloat16)
+    T.check_rows(got, ref, bound + 2.0 ** -8 * (np.abs(np.nan_to_num(ref)) + bound), 7.0)
+
+
+@pytest.mark.parametrize("B,rep", [(3, 2), (40, 2)])
+def test_prefix_without_residuals_and_padding_without_drafts(B, rep):
+    # attention-only caches (residual 0) hold quantized tokens alone; rows behind n_draft are padding without drafts too
+    case, prefix = prefix_case(31, B, 2, rep, 3, (64, 0), (224, 0), 4, 2, residual=0, presid=0, n_draft=[b % 4 for b in range(B)])
+    ref, bound = K.prefix_reference(case, prefix, 0, drafts=False)
+    T.check_rows(K.run_prefix(case, prefix, drafts=False), ref, bound, 7.0)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -30, 2.0 ** 12, 2.0 ** 60])
+@pytest.mark.parametrize("B", [3, 40])
+def test_prefix_queries_of_any_magnitude(B, scale):
+    # tiny ones average the values, huge ones pick the largest score's
+    case, prefix = prefix_case(32, B, 1, 2, 1, (32, 5), (160, 40), 2, 2)
+    case.q = case.q * scale
+    case.q = np.asarray(case.q, np.float32).astype(np.float64)
+    got = K.run_prefix(case, prefix)
+    ref, bound = K.prefix_reference(case, prefix, 0)
+    assert np.isfinite(got).all()
+    if scale < 1:
+        T.check_rows(got, ref, bound, 7.0)
+    else:  # a row whose two best scores lie further apart than their errors is the best token's value
+        for b in range(B):
+            K0, V0, _, _ = T.context(prefix, 0, 0)
+            K1, V1, _, _ = T.context(case.base, b, 0)
+            k = np.concatenate([K0, K1, case.kd[b, :, 0]]).astype(np.float64)
+            v = np.concatenate([V0, V1, case.vd[b, :, 0]]).astype(np.float64)
+            for r in range(2):
+                s = np.sort(k @ case.q[b, 0, r])
+                if (s[-1] - s[-2]) / np.sqrt(D) > 60 + 2.0 ** -9 * np.abs(s).max() / np.sqrt(D):
+                    best = v[np.argmax(k @ case.q[b, 0, r])]
+                    assert np.abs(got[b, 0, r] - best).max() <= 2.0 ** -9 * (np.abs(best).max() + 8), (b, r)
+
+
+def test_prefix_workspace_of_the_calls_own_on_other_streams():
+    make, out, ref, bound, _ = prepared(33, 40, 2, (96, 10))
+    call = make(None)
+    for s in (None, torch.cuda.Stream(), torch.cuda.Stream()):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s) if s is not None else torch.cuda.stream(torch.cuda.current_stream()):
+            call()
+        torch.cuda.synchronize()
+        T.check_rows(out.double().cpu().numpy(), ref, bound, 7.0)
+
+
 @pytest.mark.parametrize("n,nqk,nqv", [(1, 0, 0), (31, 0, 0), (127, 32, 10), (128, 64, 64), (129, 96, 33), (160, 160, 160),
                                        (300, 192, 175), (515, 512, 401)])
 @pytest.mark.parametrize("B,rep", [(3, 1), (9, 4), (40, 4)])
