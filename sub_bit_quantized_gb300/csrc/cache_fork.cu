@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const Cac
   __shared__ int ends[kForkArrays][KVQ_FORK_MAX];  // eighths of a line that a move has
   __shared__ unsigned char is_move[KVQ_FORK_MAX];
   __shared__ int longest[kForkArrays], upto[kForkArrays + 1];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, n = a.n;
   constexpr int kMine = KVQ_FORK_MAX / kThreads, kWords = KVQ_FORK_MAX / 32;
   Move mine[kMine];
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const Cac
 
 // The lengths, once every block above has read them.
 __global__ void __launch_bounds__(KVQ_FORK_MAX) cache_fork_lens_kernel(const CacheForkArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_behind();
   const int i = threadIdx.x;
   Move m = {};
   const int st = i < a.n ? judge(a, i, m) : -1;
@@ -235,16 +235,7 @@ cudaError_t launch_cache_fork(const CacheForkArgs& a, long long most_pieces, cud
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = 1;
-  cfg.blockDim = KVQ_FORK_MAX;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = grid > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, cache_fork_lens_kernel, a);
+  return launch_early(grid > 0, cache_fork_lens_kernel, dim3(1), KVQ_FORK_MAX, 0, st, a);
 }
 
 }  // namespace kvq

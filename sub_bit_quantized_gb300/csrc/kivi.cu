@@ -932,6 +932,7 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
   const size_t bq0 = (size_t)b * a.Hq + (size_t)hk * rep + sub * RH;  // first query row
   const int NQK = min(max(a.n_quant_k[b], 0), a.max_tokens) / kGroup * kGroup;
   const int NQV = (R > 0) ? min(max(a.n_quant_v[b], 0), NQK) : NQK;
+  if (a.lse) launch_dependents();
   for (int i = tid; i < RH * kD; i += kAThreads) qs[i] = bf16_to_f32(a.q[bq0 * kD + i]);
   if (tid == 0) {
     for (int s = 0; s < L::kAStages; ++s) {
@@ -1365,7 +1366,10 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
       redm[warp * RH + r] = M[r];
     }
   __syncthreads();
-  if (*failed) return;  // uniform after the barrier
+  auto end_behind = [&]() {  // as in kivi_tc.cuh
+    if (a.lse && split == 0 && sub == 0 && b == 0 && hk == 0) wait_behind();
+  };
+  if (*failed) return end_behind();  // uniform after the barrier
 
   constexpr int kIt = (RH * kD + kAThreads - 1) / kAThreads;  // outputs per thread
   float ov[kIt], Ls[kIt], Mv[kIt];
@@ -1396,9 +1400,11 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
       const int i = it * kAThreads + tid;
-      if (i < RH * kD) write_out(i, (Ls[it] > 0.f) ? ov[it] / Ls[it] : 0.f);
+      if (i >= RH * kD) continue;
+      write_out(i, (Ls[it] > 0.f) ? ov[it] / Ls[it] : 0.f);
+      if (a.lse && i % kD == 0) a.lse[bq0 + i / kD] = Mv[it] + log2f(Ls[it]);  // -infinity: nothing attended
     }
-    return;
+    return end_behind();
   }
 #pragma unroll
   for (int it = 0; it < kIt; ++it) {
@@ -1454,8 +1460,7 @@ cudaError_t launch_attn(const KiviAttnArgs& a, cudaStream_t st) {
   const int n_sub = (a.Hq / a.H) / RH;
   // token splits per head subgroup; the last split also attends the fp16 residual
   dim3 grid(a.n_split * n_sub, a.B, a.H);
-  kivi_attn_kernel<KB, VB, RH><<<grid, kAThreads, smem, st>>>(a, scale_log2);
-  return cudaGetLastError();
+  return launch_early(a.lse != nullptr, kivi_attn_kernel<KB, VB, RH>, grid, kAThreads, (int)smem, st, a, scale_log2);
 }
 
 template <int KB, int VB>

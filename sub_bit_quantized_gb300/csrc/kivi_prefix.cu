@@ -6,8 +6,9 @@
 //   o = (2^(L0 - M) o0 + 2^(L1 - M) o1) / (2^(L0 - M) + 2^(L1 - M)),  M = max(L0, L1).
 // Over the prefix the rows of all requests are rows of one matrix per KV head; over its own tokens a
 // request is a tree without the prefix (kivi_tree.cu), which writes fp32 outputs and L into the
-// workspace. Up to 32 rows a KV head the prefix, too, is one request of the tree kernels; more rows take
-// the kernel below, which unpacks a tile of the prefix once for 256 of them.
+// workspace; with one row a KV head and many requests it is the decode's (kivi.cu). Up to 32 rows a KV
+// head the prefix, too, is one request of the tree kernels; more rows take the kernel below, which unpacks
+// a tile of the prefix once for 256 of them.
 #include <cfloat>
 
 #include "kivi_tc.cuh"
@@ -683,24 +684,45 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
 // Joining the two sides
 // ======================================================================================
 
-// A warp a row, a lane four channels.
-constexpr int kCombineThreads = 128;
-__device__ __forceinline__ void combine_row(const KiviPrefixArgs& a, size_t at, float l0, float4 x, float l1, float4 y) {
+// One side of a row: its four channels o, L the log2 of its sum of 2^score
+struct Side {
+  float l;
+  float4 o;
+};
+__device__ __forceinline__ Side side(const KiviTreeArgs& t, size_t row, size_t at) {
+  return {t.lse[row], *reinterpret_cast<const float4*>(static_cast<const float*>(t.out) + at)};
+}
+// The drafted token of a request with one row (`apart`): its value, and the score q k / sqrt(D) of the four channels at c
+// (log2 units). -infinity: the row does not see it.
+__device__ __forceinline__ bool sees_draft(const KiviPrefixArgs& a, int b) { return a.apart && a.own.mask && (a.own.mask[b] & 1ull); }
+__device__ __forceinline__ Side draft(const KiviPrefixArgs& a, size_t row, int b, int h, int c) {
+  const size_t at = ((size_t)b * a.own.H + h) * kD + 4 * c;
+  const uint2 q = *reinterpret_cast<const uint2*>(a.own.q + row * kD + 4 * c);
+  const uint2 k = *reinterpret_cast<const uint2*>(a.own.k_draft + at), v = *reinterpret_cast<const uint2*>(a.own.v_draft + at);
+  const float2 k0 = __half22float2(as_h2(k.x)), k1 = __half22float2(as_h2(k.y)), v0 = __half22float2(as_h2(v.x)), v1 = __half22float2(as_h2(v.y));
+  const float s = fmaf(bf16_hi(q.y), k1.y, fmaf(bf16_lo(q.y), k1.x, fmaf(bf16_hi(q.x), k0.y, bf16_lo(q.x) * k0.x)));
+  return {s * (1.4426950408889634f * 0.08838834764831845f), make_float4(v0.x, v0.y, v1.x, v1.y)};
+}
+__device__ __forceinline__ void combine_row(const KiviPrefixArgs& a, size_t at, const Side& x, const Side& y, const Side& z) {
   // a side that saw nothing stays out, whatever its row holds; one that is not a number says so in the result
-  const float top = fmaxf(fmaxf(l0, l1), -FLT_MAX);
-  float w0 = l0 != l0 ? l0 : exp2f(l0 - top), w1 = l1 != l1 ? l1 : exp2f(l1 - top);
-  const float sum = w0 + w1;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float top = fmaxf(fmaxf(fmaxf(x.l, y.l), z.l), -FLT_MAX);
+  auto weight = [&](float l) { return l != l ? l : exp2f(l - top); };
+  float w0 = weight(x.l), w1 = weight(y.l), w2 = weight(z.l);
+  const float sum = w0 + w1 + w2, inv = sum == 0.f ? 0.f : 1.f / sum;
   w0 *= inv;
   w1 *= inv;
-  auto mix = [&](float p, float q) { return (w0 == 0.f ? 0.f : w0 * p) + (w1 == 0.f ? 0.f : w1 * q); };
-  const float v[4] = {mix(x.x, y.x), mix(x.y, y.y), mix(x.z, y.z), mix(x.w, y.w)};
+  w2 *= inv;
+  auto mix = [&](float p, float q, float r) { return (w0 == 0.f ? 0.f : w0 * p) + (w1 == 0.f ? 0.f : w1 * q) + (w2 == 0.f ? 0.f : w2 * r); };
+  const float v[4] = {mix(x.o.x, y.o.x, z.o.x), mix(x.o.y, y.o.y, z.o.y), mix(x.o.z, y.o.z, z.o.z), mix(x.o.w, y.o.w, z.o.w)};
   if (a.out_fp32)
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
         make_uint2(f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16));
 }
+
+// A warp a row, a lane four channels.
+constexpr int kCombineThreads = 128;
 __global__ void __launch_bounds__(kCombineThreads) kivi_prefix_combine_kernel(const KiviPrefixArgs a, const int rows) {
   wait_behind();
   const int row = blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -708,8 +730,13 @@ __global__ void __launch_bounds__(kCombineThreads) kivi_prefix_combine_kernel(co
   const int tok = div_by(row, a.heads), b = div_by(tok, a.tokens);
   if (a.own.n_draft && tok - b * a.own.N >= a.own.n_draft[b]) return;  // padding
   const size_t at = (size_t)row * kD + 4 * lane;
-  combine_row(a, at, a.prefix.lse[row], *reinterpret_cast<const float4*>(static_cast<const float*>(a.prefix.out) + at), a.own.lse[row],
-              *reinterpret_cast<const float4*>(static_cast<const float*>(a.own.out) + at));
+  Side z = {-INFINITY, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (sees_draft(a, b)) {
+    z = draft(a, row, b, div_by(row - tok * a.own.Hq, a.prefix.rep), lane);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) z.l += __shfl_xor_sync(0xFFFFFFFFu, z.l, off);
+  }
+  combine_row(a, at, side(a.prefix, row, at), side(a.own, row, at), z);
 }
 
 // The same behind the kernel above: the parts of a segment lie in the slots block + segment of the blocks that shared
@@ -719,11 +746,30 @@ __global__ void __launch_bounds__(kJoinThreads) kivi_prefix_join_kernel(const Ki
   wait_behind();
   const KiviTreeArgs& t = a.prefix;
   const int lane = threadIdx.x & 31, c = 4 * (threadIdx.x >> 5) + (lane >> 3), h = blockIdx.y;
-  const int row = blockIdx.x * kJoinRows + (lane & 7);  // of the KV head
-  if (row >= t.N * t.rep.d) return;
+  const int row = min(blockIdx.x * kJoinRows + (lane & 7), t.N * t.rep.d - 1);  // of the KV head; of the last block the last ones again
   const int tok = div_by(row, t.rep), b = div_by(tok, a.tokens);
-  if (a.own.n_draft && tok - b * a.own.N >= a.own.n_draft[b]) return;  // padding
+  const bool real = !a.own.n_draft || tok - b * a.own.N < a.own.n_draft[b];  // no padding
   const size_t out_row = (size_t)tok * t.Hq + h * t.rep.d + row - tok * t.rep.d;
+  Side z = {-INFINITY, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (a.apart) {  // each warp has four of a row's 32 pieces
+    __shared__ float score[kJoinThreads / 32][kJoinRows];
+    const bool sees = real && sees_draft(a, b);
+    float s = 0.f;
+    if (sees) {
+      z = draft(a, out_row, b, h, c);
+      s = z.l;
+    }
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+    if (lane < kJoinRows) score[threadIdx.x >> 5][lane] = s;
+    __syncthreads();
+    if (sees) {
+      z.l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinThreads / 32; ++w) z.l += score[w][lane & 7];
+    }
+  }
+  if (!real) return;
   const TreeLens len = tree_lens(t, 0, kTok);
   const int T = (int)((uint32_t)(len.n + kTok - 1) / kTok), P = T * t.segs.d;
   const int seg = h * t.row_tiles.d + row / kRows, r = row & (kRows - 1);
@@ -767,8 +813,7 @@ __global__ void __launch_bounds__(kJoinThreads) kivi_prefix_join_kernel(const Ki
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const size_t at = out_row * kD + 4 * c;
-  combine_row(a, at, l == 0.f ? -INFINITY : top + __log2f(l), make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), a.own.lse[out_row],
-              *reinterpret_cast<const float4*>(static_cast<const float*>(a.own.out) + at));
+  combine_row(a, at, {l == 0.f ? -INFINITY : top + __log2f(l), make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv)}, side(a.own, out_row, at), z);
 }
 
 template <int KB, int VB, bool REST>
@@ -790,6 +835,11 @@ cudaError_t launch_prefix_keys(const KiviTreeArgs& a, bool fp32, cudaStream_t st
 // 4 bits, whole call): 32 rows over 8192 tokens 46 / 44 us, 64 rows 46 / 49, 128 rows 46 / 55; 64 rows over 1024 tokens 28 /
 // 33; 32 KV heads, 2 bits, 4096 tokens: 32 rows 71 / 63, 128 rows 138 / 155.
 bool many_rows(int rows) { return rows > 32; }
+// Requests with one row a KV head attend their own caches as the decode does, unsplit, if that makes two blocks an SM (a
+// drafted token is joined apart): it spends a third of the tree kernel's instructions on one row. Measured with it and
+// without (whole call, 32 KV heads, 2 bits): 16 requests of 512 tokens 54 / 67 us, 64 requests of 40 tokens 71 / 95, 128
+// 99 / 138. Four query heads a KV head, 64 requests of 640 tokens, 4 bits: 93 / 86, so not there.
+bool alone(int B, int N, int H, int rep) { return N == 1 && rep == 1 && (long long)B * H >= 2ll * device_sms(); }
 int row_tiles(int rows) { return (rows + kRows - 1) / kRows; }
 
 }  // namespace
@@ -825,10 +875,27 @@ cudaError_t launch_kivi_prefix(const KiviPrefixArgs& args, cudaStream_t st) {
     e = launch_kivi_tree(t, st, kTreeAttend);
   }
   // every further launch is early: the blocks of both passes share the GPU, and what joins them is there when they end
-  a.own.chained = kChainedBehind;
-  if (e == cudaSuccess) e = launch_kivi_tree(a.own, st, kTreeAttend);
+  KiviTreeArgs& o = a.own;
+  a.apart = alone(o.B, o.N, o.H, rep);
+  o.chained = kChainedBehind;
+  t.rep = int_div(rep);
+  if (e == cudaSuccess && a.apart) {
+    KiviAttnArgs d{};
+    d.k_codes = o.k_codes; d.k_scale = o.k_scale; d.k_zero = o.k_zero;
+    d.v_codes = o.v_codes; d.v_scale = o.v_scale; d.v_zero = o.v_zero;
+    d.k_resid = o.k_resid; d.v_resid = o.v_resid;
+    d.n_tok = o.n_tok; d.n_quant_k = o.n_quant_k; d.n_quant_v = o.n_quant_v;
+    d.q = o.q; d.out = o.out; d.out_fp32 = 1; d.lse = o.lse; d.err = o.err;
+    d.B = o.B; d.H = o.H; d.Hq = o.Hq; d.k_bits = o.k_bits; d.v_bits = o.v_bits;
+    d.max_tokens = o.max_tokens; d.residual = o.residual; d.group = kGroupT;
+    d.n_split = 1;
+    d.tok_per_split = max(o.max_tokens, kGroupT);
+    e = launch_kivi_attn(d, st);
+  } else if (e == cudaSuccess) {
+    e = launch_kivi_tree(o, st, kTreeAttend);
+  }
   if (e == cudaSuccess && !many) e = launch_kivi_tree(t, st, kTreeMerge);
-  if (e == cudaSuccess) e = launch_kivi_tree(a.own, st, kTreeMerge);
+  if (e == cudaSuccess && !a.apart) e = launch_kivi_tree(o, st, kTreeMerge);
   if (e != cudaSuccess) return e;
   if (many) return launch_early(true, kivi_prefix_join_kernel, dim3((rows + kJoinRows - 1) / kJoinRows, t.H), kJoinThreads, 0, st, a);
   const int all = a.own.B * a.own.N * a.own.Hq, per = kCombineThreads / 32;

@@ -9,27 +9,10 @@
 
 namespace kvq {
 
-// ---- launches ahead of the end of the kernel before (programmatic dependent launch) ----
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_behind() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The end of a kernel that was launched early behind one that it does not depend on: what comes next waits for this
 // kernel alone, so it does not end before the other. (All blocks of that one run: otherwise this would not have begun.)
 __device__ __forceinline__ void end_behind(const KiviTreeArgs& a) {
   if (a.chained == kChainedBehind && blockIdx.x == 0) wait_behind();
-}
-template <typename... P, typename... A>
-cudaError_t launch_early(bool early, void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = (unsigned)threads;
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 constexpr int kGroupT = 32;   // tokens per key group, channels per value group

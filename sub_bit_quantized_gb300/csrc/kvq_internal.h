@@ -214,6 +214,8 @@ struct KiviAttnArgs {
   const uint16_t* q;               // bf16 [B][Hq][D]
   void* out; int out_fp32;
   float* part; int* counters; int* err;
+  float* lse;                      // [B][Hq], or null: log2 of a row's sum of 2^score, of an unsplit call that is launched
+                                   // early behind a kernel it does not depend on, and does not end before that one
   int B, H, Hq, k_bits, v_bits, max_tokens, residual, group;
   int n_split, tok_per_split;
 };
@@ -256,7 +258,9 @@ struct KiviPrefixArgs {
   KiviTreeArgs prefix;             // one request of all the call's rows, over the prefix's slot
   KiviTreeArgs own;                // the requests over their own caches and drafts; both write fp32 and lse
   void* out; int out_fp32;         // [B][N][Hq][D]
-  IntDiv heads, tokens;            // set by the launch: query heads, tokens a request
+  // set by the launch: query heads, tokens a request; 1: `own` holds the cached tokens alone, a draft is joined apart
+  IntDiv heads, tokens;
+  int apart;
 };
 // workspace bytes, and tile positions (below 2^31: checked by the host), of the pass over the prefix with `rows` rows a
 // query head

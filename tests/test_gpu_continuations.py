@@ -60,6 +60,28 @@ def test_prefix_without_residuals_and_padding_without_drafts(B, rep):
     T.check_rows(K.run_prefix(case, prefix, drafts=False), ref, bound, 7.0)
 
 
+@pytest.mark.parametrize("kb,vb", [(2, 2), (4, 4), (2, 4), (4, 2)])
+@pytest.mark.parametrize("B,H,rep", [(10, 32, 1), (39, 8, 1), (77, 4, 2), (155, 2, 4), (310, 1, 4), (103, 1, 3)])
+def test_prefix_one_row_a_request_and_many_of_them(B, H, rep, kb, vb):
+    # from two blocks an SM on a request's own tokens are attended as the decode does, its drafted token apart; some
+    # requests hold nothing, some are padding, some do not see their drafted token
+    own = [(0, 0) if b % 7 == 0 else (32 * (b % 3), 1 + b % 30) for b in range(B)]
+    case, prefix = prefix_case(B + H, B, H, rep, 1, own, (96, 20), kb, vb, residual=32 * (1 + B % 3),
+                               n_draft=[0 if b % 11 == 3 else 1 for b in range(B)])
+    case.mask[::5] = 0
+    ref, bound = K.prefix_reference(case, prefix, 0)
+    T.check_rows(K.run_prefix(case, prefix), ref, bound, 7.0)
+    got = K.run_prefix(case, prefix, dtype=torch.bfloat16)
+    T.check_rows(got, ref, bound + 2.0 ** -8 * (np.abs(np.nan_to_num(ref)) + bound), 7.0)
+    ref, bound = K.prefix_reference(case, prefix, 0, drafts=False)
+    T.check_rows(K.run_prefix(case, prefix, drafts=False), ref, bound, 7.0)
+    case.vd[::5] = np.nan  # unseen
+    ref, bound = K.prefix_reference(case, prefix, 0, drafts=False)
+    got = K.run_prefix(case, prefix)
+    rows = [b for b in range(0, B, 5) if case.n_draft[b]]
+    T.check_rows(got[rows], ref[rows], bound[rows], 7.0)
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -30, 2.0 ** 12, 2.0 ** 60])
 @pytest.mark.parametrize("B", [3, 40])
 def test_prefix_queries_of_any_magnitude(B, scale):
