@@ -85,11 +85,12 @@ __device__ __forceinline__ bool in_ring(const CacheForkArgs& a, int kind, int ro
 
 __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const CacheForkArgs a) {
   __shared__ __align__(16) uint4 stage[kStage * kThreads];
-  __shared__ Move moves[KVQ_FORK_MAX];
+  __shared__ int2 moves[KVQ_FORK_MAX];             // from, to
+  __shared__ int tokens[KVQ_FORK_MAX];
   __shared__ Ring rings[KVQ_FORK_MAX];
   __shared__ int ends[kForkArrays][KVQ_FORK_MAX];  // eighths of a line that a move has
   __shared__ unsigned char is_move[KVQ_FORK_MAX];
-  __shared__ int longest[kForkArrays], upto[kForkArrays + 1];
+  __shared__ int longest[kForkArrays], shortest[kForkArrays], upto[kForkArrays + 1];
   launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, n = a.n;
   constexpr int kMine = KVQ_FORK_MAX / kThreads, kWords = KVQ_FORK_MAX / 32;
@@ -99,7 +100,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const Cac
     const int i = tid + k * kThreads;
     is_move[i] = i < n && judge(a, i, mine[k]) == 0;
   }
-  if (tid < kForkArrays) longest[tid] = 0;
+  if (tid < kForkArrays) {
+    longest[tid] = 0;
+    shortest[tid] = 0x7FFFFFFF;
+  }
   __syncthreads();
   // the list of moves, hazards first
   uint32_t moved[kWords], hazard[kWords];
@@ -130,12 +134,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const Cac
       if (w == i >> 5) h = (hazard[w] >> (i & 31)) & 1;
     }
     const int at = h ? before_h : hazards + before_o;
-    moves[at] = mine[k];
+    moves[at] = make_int2(mine[k].src, mine[k].dst);
+    tokens[at] = mine[k].len.n;
     rings[at] = ring_of(a, mine[k].len);
     for (int x = 0; x < a.n_arrays; ++x) {
       const int e = line_eighths(a, a.array[x], mine[k].len);
       ends[x][at] = e;
       atomicMax(&longest[x], e);
+      atomicMin(&shortest[x], e);
     }
   }
   // units across: as many as the hazards of each leave room for; the rest of the threads takes other moves of theirs
@@ -150,34 +156,60 @@ __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const Cac
   }
   __syncthreads();
   // without hazards any moves of a piece may go to any block: kBatch of them each
-  const int runs = hazards ? 1 : (total + kBatch - 1) / kBatch;
-  const long long tasks = (long long)upto[a.n_arrays] * runs;
-  for (long long task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int p = hazards ? (int)task : (int)(task / runs), run = hazards ? 0 : (int)(task - (long long)p * runs);
+  const int all_runs = (total + kBatch - 1) / kBatch, pieces = upto[a.n_arrays];
+  const bool spread = hazards == 0 && (long long)pieces * all_runs < (1ll << 31);
+  const IntDiv runs = {spread ? all_runs : 1, 0xFFFFFFFFu / (uint32_t)(spread ? all_runs : 1)};
+  for (long long task = blockIdx.x, tasks = (long long)pieces * runs.d; task < tasks; task += gridDim.x) {
+    const int p = div_by((int)task, runs), run = (int)task - p * runs.d;
     int xi = 0;
     while (p >= upto[xi + 1]) ++xi;
     const ForkArray& x = a.array[xi];
-    const int kind = x.kind, lines = x.outer * a.heads, rel = p - upto[xi], piece = rel / lines;
-    const int line = rel - piece * lines, o = line / a.heads, h = line - o * a.heads;
+    const int kind = x.kind, rel = p - upto[xi], piece = div_by(rel, x.lines);
+    const int line = rel - piece * x.lines.d, o = div_by(line, a.per_outer), h = line - o * a.heads;
     const int mine_at = 2 * (piece * width + unit);  // the thread's unit of the line, in eighths
     const unsigned char* src = x.src + o * x.src_outer + h * x.src_head + mine_at * 8ll;
     unsigned char* dst = x.dst + o * x.dst_outer + h * x.dst_head + mine_at * 8ll;
     const int ring_row = kind >= kForkRing ? mine_at / (x.row / 8) : 0;
+    if (spread && kind < kForkRing && 2 * (piece + 1) * width <= shortest[xi] && (run + 1) * kBatch <= total) {
+      // every move has the whole piece: no questions asked, a source that they share (a forked prompt) read once
+      const uint32_t from = (uint32_t)(x.src_slot >> 4), to = (uint32_t)(x.dst_slot >> 4);
+      int2 m[kBatch];
+      bool one = true;
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        m[e] = moves[run * kBatch + e];
+        one = one && m[e].x == m[0].x;
+      }
+      uint4 v[kBatch];
+      const uint4* src16 = reinterpret_cast<const uint4*>(src);
+      uint4* dst16 = reinterpret_cast<uint4*>(dst);
+      if (one) {
+        v[0] = src16[(uint64_t)(uint32_t)m[0].x * from];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) dst16[(uint64_t)(uint32_t)m[e].y * to] = v[0];
+      } else {
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) v[e] = src16[(uint64_t)(uint32_t)m[e].x * from];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) dst16[(uint64_t)(uint32_t)m[e].y * to] = v[e];
+      }
+      continue;
+    }
     // what move i has of the unit: 16 bytes (2), 8 (1) or none
     auto has = [&](int i) {
       const int left = ends[xi][i] - mine_at;
       if (left <= 0) return 0;
-      if (kind >= kForkRing) return in_ring(a, kind, ring_row, moves[i].len.n, rings[i]) ? 2 : 0;
+      if (kind >= kForkRing) return in_ring(a, kind, ring_row, tokens[i], rings[i]) ? 2 : 0;
       return left >= 2 ? 2 : 1;
     };
     auto load = [&](int i, int k) {
-      const unsigned char* at = src + moves[i].src * x.src_slot;
+      const unsigned char* at = src + moves[i].x * x.src_slot;
       if (k == 2) return *reinterpret_cast<const uint4*>(at);
       const uint2 v = *reinterpret_cast<const uint2*>(at);
       return make_uint4(v.x, v.y, 0u, 0u);
     };
     auto store = [&](int i, int k, const uint4& v) {
-      unsigned char* at = dst + moves[i].dst * x.dst_slot;
+      unsigned char* at = dst + moves[i].y * x.dst_slot;
       if (k == 2) *reinterpret_cast<uint4*>(at) = v;
       else *reinterpret_cast<uint2*>(at) = make_uint2(v.x, v.y);
     };
@@ -201,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const Cac
 #pragma unroll
       for (int e = 0; e < kBatch; ++e)
         if (k[e]) store(i0 + e * groups, k[e], v[e]);
-      if (hazards == 0) break;  // the next ones are another task's
+      if (spread) break;  // the next ones are another task's
     }
     int st = tid;
     for (int i = group; i < hazards; i += groups, st += kThreads) {

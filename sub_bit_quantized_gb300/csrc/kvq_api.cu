@@ -639,6 +639,7 @@ static kvq::ForkArray fork_array(const void* src, void* dst, int kind, int outer
   x.src = static_cast<const unsigned char*>(src); x.dst = static_cast<unsigned char*>(dst);
   x.outer = outer; x.row = (int)row; x.kind = kind;
   x.src_head = src_rows * row; x.src_slot = x.src_head * heads; x.src_outer = x.src_slot * src_slots;
+  x.lines = kvq::int_div(outer * heads);
   x.dst_head = dst_rows * row; x.dst_slot = x.dst_head * heads; x.dst_outer = x.dst_slot * dst_slots;
   return x;
 }
@@ -730,6 +731,10 @@ KVQ_API kvq_status kvq_cache_fork(int format, const void* cfg, const void* cache
     pieces += (std::min(a.array[i].src_head, a.array[i].dst_head) + 2047) / 2048 * a.array[i].outer * a.heads;
   if (pieces >= (1ll << 27) || (long long)a.room * 64 >= (1ll << 31) || (long long)a.from_room * 64 >= (1ll << 31))
     return fail(KVQ_ERR_UNSUPPORTED, "%s: slots too large for one call", __func__);
+  a.per_outer = kvq::int_div(a.heads);
+  for (int i = 0; i < a.n_arrays; ++i)
+    if ((a.array[i].src_slot >> 4) >= (1ll << 32) || (a.array[i].dst_slot >> 4) >= (1ll << 32))
+      return fail(KVQ_ERR_UNSUPPORTED, "%s: slots too large for one call", __func__);
   a.format = format; a.source = source; a.b0 = b0; a.n = n; a.err = device_error_ptr();
   return cuda_status(kvq::launch_cache_fork(a, pieces, (cudaStream_t)stream), __func__);
 }

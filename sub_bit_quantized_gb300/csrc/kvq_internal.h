@@ -277,6 +277,7 @@ struct ForkArray {                 // [outer][slot][head][rows of `row` bytes], 
   const unsigned char* src; unsigned char* dst;
   long long src_outer, src_slot, src_head, dst_outer, dst_slot, dst_head;
   int outer, row, kind;
+  IntDiv lines;                    // outer * heads
 };
 struct CacheForkArgs {
   ForkArray array[kForkArrays];
@@ -286,6 +287,7 @@ struct CacheForkArgs {
   int format, n_arrays, b0, n, heads, from_batch;
   int same;                        // both caches are one
   int room, from_room;             // most quantized tokens, or pages
+  IntDiv per_outer;                // heads
   int residual, ring, sink, max_ctx;  // ring: rows of the value ring, or of the window's behind the sink
 };
 cudaError_t launch_cache_fork(const CacheForkArgs& a, long long most_pieces, cudaStream_t s);
