@@ -508,6 +508,31 @@ def test_verify_greedy_ties_infinities_and_nan(V):
         assert check_verify(P.to(dt), None, token, parent, None) == 24
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [1, 9, 517, 5003, 50021])
+def test_verify_greedy_paths_of_every_length(V, dt):
+    # chains accepted up to node k, and the same behind a rejected first child of every node
+    g = torch.Generator().manual_seed(V)
+    N = 9
+    P = torch.randint(-50, 50, (2 * N, N, V), generator=g).to(dt)
+    best = torch.from_numpy(P.float().numpy().argmax(-1).astype(np.int32))
+    parent = torch.zeros((2 * N, N), dtype=torch.int32)
+    token = torch.zeros((2 * N, N), dtype=torch.int32)
+    for k in range(N):
+        parent[k, 1:] = torch.arange(N - 1)
+        token[k, 1:] = best[k, :-1]
+        if k + 1 < N:
+            token[k, k + 1] = (best[k, k] + 1) % V
+        # nodes 1, 3, 5, 7 rejected where there is another token, 2, 4, 6, 8 go on up to the k-th
+        b = N + k
+        for i in range(1, N):
+            parent[b, i] = 2 * ((i - 1) // 2)
+            token[b, i] = best[b, parent[b, i]] if i % 2 == 0 and i <= k else (best[b, parent[b, i]] + 1) % V
+    accepted = check_verify(P, None, token, parent, None)
+    if V > 1:
+        assert accepted == sum(range(1, N + 1)) + sum(1 + k // 2 for k in range(N))
+
+
 def test_verify_strides_and_alignment():
     g = torch.Generator().manual_seed(9)
     P, Q = K.dists(g, 3, 5, 1003, torch.float32)
