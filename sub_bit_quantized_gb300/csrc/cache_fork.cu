@@ -8,7 +8,11 @@
 // chains) has to wait in shared memory; those of forks and of beams that replace dropped ones stream
 // through registers. The blocks take equal shares of the units up to the longest slot that moves.
 //
-// Bound: HBM, each moved byte read once per distinct source and written once per slot.
+// Bound: HBM, each moved byte read once per distinct source and written once per slot, behind a chain of dependent loads
+// (sources, lengths, table, first units: about 5 us). A prompt of 4096 tokens to 16 slots (32 heads, 2 bits, 243 MB): 52 us,
+// 4.7 TB/s, 69 % of the copy rate; 64 beams of 1531 tokens in place, about half of which move: 30; eight slots of 701 tokens in
+// index pages: 17. The first form took 64, 39 and 20. Blocks of 256 threads, batches of 4 and 16
+// moves, streaming stores and loads past L1 were not better.
 #include <algorithm>
 
 #include "kvq_common.cuh"
