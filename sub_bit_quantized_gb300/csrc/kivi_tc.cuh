@@ -50,17 +50,21 @@ __device__ __forceinline__ int share_begin(int P, int k, const IntDiv& G) {
   return k * q + div_by(k * (P - q * G.d), G);
 }
 
-// The row of a token behind the quantized ones (token t, value: of the ring): residual, drafted, or none
+// The row of a token behind the quantized ones (token t, value: of the ring): residual, drafted, or none. By selection: where
+// many are loaded in a row, a branch between two of them would keep the second from starting before the first arrives.
+__device__ __forceinline__ const uint16_t* fp16_row(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int place,
+                                                    const uint16_t* resid, const uint16_t* draft) {
+  const size_t r = ((size_t)b * a.H + h) * a.residual + place, d = ((size_t)b * a.N + (t - L.n)) * a.H + h;
+  const uint16_t* from = t < L.n ? resid : draft;
+  const size_t at = t < L.n ? r : d;
+  return t < L.n + L.nd ? from + at * kD : nullptr;
+}
 __device__ __forceinline__ const uint16_t* fp16_key(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t) {
-  if (t < L.n) return a.k_resid + (((size_t)b * a.H + h) * a.residual + (t - L.nqk)) * kD;
-  if (t < L.n + L.nd) return a.k_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
-  return nullptr;
+  return fp16_row(a, L, b, h, t, t - L.nqk, a.k_resid, a.k_draft);
 }
 // place: t % residual for a token that is cached
 __device__ __forceinline__ const uint16_t* fp16_value(const KiviTreeArgs& a, const TreeLens& L, int b, int h, int t, int place) {
-  if (t < L.n) return a.v_resid + (((size_t)b * a.H + h) * a.residual + place) * kD;
-  if (t < L.n + L.nd) return a.v_draft + (((size_t)b * a.N + (t - L.n)) * a.H + h) * kD;
-  return nullptr;
+  return fp16_row(a, L, b, h, t, place, a.v_resid, a.v_draft);
 }
 // place of token t0 + i (i < 32) when t0's is p: the ring holds at least 32 rows, or none (no token is there then)
 __device__ __forceinline__ int ring_place(int p, int i, int R) {
@@ -68,9 +72,18 @@ __device__ __forceinline__ int ring_place(int p, int i, int R) {
   if (p >= R) p -= R;
   return p;
 }
-// channels 8c .. 8c+7 of a row, zero without one
+// channels 8c .. 8c+7 of a row, zero without one: a load under a predicate, as branches around several of them would keep
+// each from starting before the one ahead has arrived
 __device__ __forceinline__ uint4 row8(const uint16_t* p, int c) {
-  return p ? __ldg(reinterpret_cast<const uint4*>(p + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+  const uint64_t at = p ? reinterpret_cast<uint64_t>(p + 8 * c) : 0;
+  uint4 v;
+  asm("{\n\t.reg .pred there;\n\t"
+      "setp.ne.u64 there, %4, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@there ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(at));
+  return v;
 }
 // Channel order of the staged keys and queries. The contraction runs over all 128 channels, so any order serves
 // that both share; this one is the order in which a code word's halves unpack: pairs (c, c + 8) of 16 channels

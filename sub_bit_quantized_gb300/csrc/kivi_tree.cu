@@ -705,14 +705,17 @@ __global__ void __launch_bounds__(kMmaThreads, MmaLayout<KB, VB, NT>::kBlocks)
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const int tt = 8 * (y >> 1) + ((y & 1) ? cb : ca);
-              const uint4 v = tt < to_v
-                                  ? make_uint4(0u, 0u, 0u, 0u)
-                                  : row8(fp16_value(a, w.len, w.b, h, tw + tt, ring_place(place, tt, a.residual)), 2 * n8 + hw);
-              x[y][0] = halved(v.x);
-              x[y][1] = halved(v.y);
-              x[y][2] = halved(v.z);
-              x[y][3] = halved(v.w);
+              const uint16_t* row = fp16_value(a, w.len, w.b, h, tw + tt, ring_place(place, tt, a.residual));
+              const uint4 v = row8(tt < to_v ? nullptr : row, 2 * n8 + hw);
+              x[y][0] = v.x;
+              x[y][1] = v.y;
+              x[y][2] = v.z;
+              x[y][3] = v.w;
             }
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[y][e] = halved(x[y][e]);
             if (to_v > 0) {
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
@@ -1160,8 +1163,8 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
       uint4 u[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        u[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (t8 + i + e >= len.nqv) u[e] = row8(fp16_value(a, len, b, h, t8 + i + e, ring_place(place, i + e, a.residual)), c);
+        const uint16_t* row = fp16_value(a, len, b, h, t8 + i + e, ring_place(place, i + e, a.residual));
+        u[e] = row8(t8 + i + e < len.nqv ? nullptr : row, c);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
