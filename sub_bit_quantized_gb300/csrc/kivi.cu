@@ -723,6 +723,11 @@ struct AttnLayout {
   static constexpr int kTPW = (RH == 1) ? 32 : 16;
   static constexpr int kWPC = kAChunk / kTPW;             // warps per chunk
   static constexpr int kNPar = kAThreads / 32 / kWPC;     // chunk parities
+  // Barriers of landed chunks, in turn: a warp tells only a barrier's last phase from the one before, so it has to see every
+  // phase of those it waits on. With two parities and an odd ring the warps of both take a stage by turns; a barrier of its own
+  // for every second turn keeps each one with one parity (a warp three chunks ahead of another of its parity took the chunk
+  // before for its own otherwise).
+  static constexpr int kBars = (kAStages % kNPar == 0) ? kAStages : kAStages * kNPar;
   static constexpr int kKRow = kD * KB / 8;               // key code bytes per token
   static constexpr int kVRow = kD * VB / 8;               // value code bytes per token
   static constexpr int kCKc = 0;                          // stage layout (bytes)
@@ -751,6 +756,7 @@ struct AttnLayout {
   static_assert(KB == 2 || KB == 4, "2- or 4-bit keys");
   static constexpr int kWPS = 16 * KB / 32;               // code words per 16-channel k-step
   static constexpr bool kMma = RH > 1;
+  static_assert(kBars * 8 + 4 <= 64, "barriers and the flag");
   static constexpr int kOffS = kOffBar + 64;
   static constexpr int kSmem = kOffS + (kMma ? kAWarps * 16 * RH * 4 : 0);
   // value phase: a lane takes kLW code words of one token, all in one value group (with one
@@ -921,7 +927,7 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
   int* released = flag + 1;                                  // warps done with a stage's chunk
   int* issued = released + L::kAStages;                      // chunks whose copies were issued
   uint64_t* full = reinterpret_cast<uint64_t*>(sma + L::kOffBar);
-  volatile int* failed = reinterpret_cast<volatile int*>(sma + L::kOffBar + L::kAStages * 8);
+  volatile int* failed = reinterpret_cast<volatile int*>(sma + L::kOffBar + L::kBars * 8);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rep = a.Hq / a.H, n_sub = rep / RH;
   const int split = blockIdx.x / n_sub, sub = blockIdx.x % n_sub, b = blockIdx.y, hk = blockIdx.z;
@@ -935,10 +941,8 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
   if (a.lse) launch_dependents();
   for (int i = tid; i < RH * kD; i += kAThreads) qs[i] = bf16_to_f32(a.q[bq0 * kD + i]);
   if (tid == 0) {
-    for (int s = 0; s < L::kAStages; ++s) {
-      mbar_init(&full[s], 1);
-      released[s] = 0;
-    }
+    for (int s = 0; s < L::kBars; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < L::kAStages; ++s) released[s] = 0;
     *issued = 0;
     *failed = 0;
     fence_mbar_init();
@@ -1008,16 +1012,17 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
     const size_t grp0 = bh * (a.max_tokens / kGroup);   // key group row base of (b, hk)
     auto produce = [&](int c) {                         // thread 0
       const int st = c % L::kAStages;
+      uint64_t* bar = &full[c % L::kBars];
       unsigned char* dst = sma + st * L::kStage;
       const int t = t0 + c * kAChunk;
       const int n = min(kAChunk, t1 - t), ng = n / kGroup;
-      mbar_arrive_expect_tx(&full[st], (uint32_t)(n * (L::kKRow + L::kVRow) + ng * kD * 2 * 2 + n * 8 * 2));
-      bulk_g2s(dst + L::kCKc, a.k_codes + (tok0 + t) * L::kKRow, n * L::kKRow, &full[st]);
-      bulk_g2s(dst + L::kCVc, a.v_codes + (tok0 + t) * L::kVRow, n * L::kVRow, &full[st]);
-      bulk_g2s(dst + L::kCKs, a.k_scale + (grp0 + t / kGroup) * kD, ng * kD * 2, &full[st]);
-      bulk_g2s(dst + L::kCKz, a.k_zero + (grp0 + t / kGroup) * kD, ng * kD * 2, &full[st]);
-      bulk_g2s(dst + L::kCVs, a.v_scale + (tok0 + t) * 4, n * 8, &full[st]);
-      bulk_g2s(dst + L::kCVz, a.v_zero + (tok0 + t) * 4, n * 8, &full[st]);
+      mbar_arrive_expect_tx(bar, (uint32_t)(n * (L::kKRow + L::kVRow) + ng * kD * 2 * 2 + n * 8 * 2));
+      bulk_g2s(dst + L::kCKc, a.k_codes + (tok0 + t) * L::kKRow, n * L::kKRow, bar);
+      bulk_g2s(dst + L::kCVc, a.v_codes + (tok0 + t) * L::kVRow, n * L::kVRow, bar);
+      bulk_g2s(dst + L::kCKs, a.k_scale + (grp0 + t / kGroup) * kD, ng * kD * 2, bar);
+      bulk_g2s(dst + L::kCKz, a.k_zero + (grp0 + t / kGroup) * kD, ng * kD * 2, bar);
+      bulk_g2s(dst + L::kCVs, a.v_scale + (tok0 + t) * 4, n * 8, bar);
+      bulk_g2s(dst + L::kCVz, a.v_zero + (tok0 + t) * 4, n * 8, bar);
     };
     if (tid == 0) {
       for (int c = 0; c < min(L::kAStages, n_chunks); ++c) produce(c);
@@ -1034,7 +1039,7 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
     const int tb = L::kTPW * wc, g = (RH == 1) ? wc : warp >> 1, hf = warp & 1;
     for (int c = warp / L::kWPC; c < n_chunks; c += L::kNPar) {
       const int st = c % L::kAStages;
-      kivi_wait(&full[st], (c / L::kAStages) & 1, failed, a.err);  // a timeout leaves stale data: harmless, reported
+      kivi_wait(&full[c % L::kBars], (c / L::kBars) & 1, failed, a.err);  // a timeout leaves stale data: harmless, reported
       const unsigned char* stage = sma + st * L::kStage;
       const int tc0 = t0 + c * kAChunk;  // token of chunk row 0
       const int n = min(kAChunk, t1 - tc0);  // a multiple of 32: a key group's warps have all its tokens or none
@@ -1273,7 +1278,7 @@ __global__ void __launch_bounds__(kAThreads, AttnLayout<KB, VB, RH>::kMinBlocks)
     // after a timed-out wait, let this block's copies still in flight land first
     if (tid == 0 && *failed)
       for (int c = max(0, *issued - L::kAStages); c < *issued; ++c)
-        mbar_wait_bounded(&full[c % L::kAStages], (c / L::kAStages) & 1);
+        mbar_wait_bounded(&full[c % L::kBars], (c / L::kBars) & 1);
   }
   if (has_resid) {
     // ============ fp16 residual (keys and values), after the last split's quantized keys ============
