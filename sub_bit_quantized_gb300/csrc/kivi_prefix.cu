@@ -73,7 +73,10 @@ struct PrefixLayout {
   static constexpr int kOffVs = kOffKs + kKStages * kKStage;
   static constexpr int kOffUnit = kOffVs + kGroups * kVStages * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
   static constexpr int kOffBar = kOffUnit + 4 * 8 * 4;
-  static constexpr int kBars = 8 + 4 + 2 * kVTiles + 2 * kKStages + 2 * kGroups * kVStages;
+  // Landed groups have two barriers a stage, by turns: with an odd number of stages the two sets of warps that unpack keys
+  // take a stage by turns, and a warp has to see every phase of a barrier that it waits on.
+  static constexpr int kKBars = 2 * kKStages;
+  static constexpr int kBars = 8 + 4 + 2 * kVTiles + kKBars + kKStages + 2 * kGroups * kVStages;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory of a block");
 };
@@ -300,7 +303,7 @@ struct Groups {
 template <int KB, int VB, bool REST>
 __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTreeArgs a, const float scale_log2) {
   using L = PrefixLayout<KB, VB, REST>;
-  constexpr int kVTiles = L::kVTiles, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr int kVTiles = L::kVTiles, kKStages = L::kKStages, kKBars = L::kKBars, kVStages = L::kVStages;
   extern __shared__ __align__(128) unsigned char sm[];
   float* unit = reinterpret_cast<float*>(sm + L::kOffUnit);
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [2] a row tile's queries are there
@@ -311,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   uint64_t* k_empty = bar_q + 10;                                   // [2] and read
   uint64_t* v_full = bar_q + 12;                                    // [kVTiles] a tile's values are unpacked
   uint64_t* v_empty = v_full + kVTiles;                             // [kVTiles] and read
-  uint64_t* ks_full = v_empty + kVTiles;                            // [kKStages] a group's stored keys landed
-  uint64_t* ks_empty = ks_full + kKStages;                          // [kKStages] and are unpacked
+  uint64_t* ks_full = v_empty + kVTiles;                            // [kKBars] a group's stored keys landed
+  uint64_t* ks_empty = ks_full + kKBars;                            // [kKStages] and are unpacked
   uint64_t* vs_full = ks_empty + kKStages;                          // [kGroups][kVStages] a tile's group's stored values landed
   uint64_t* vs_empty = vs_full + kGroups * kVStages;                // and are unpacked
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q + L::kBars);
@@ -342,10 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       mbar_init(v_full + i, 2 * kGroups);
       mbar_init(v_empty + i, 1);
     }
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(ks_full + i, 1);
-      mbar_init(ks_empty + i, 4);
-    }
+    for (int i = 0; i < kKBars; ++i) mbar_init(ks_full + i, 1);
+    for (int i = 0; i < kKStages; ++i) mbar_init(ks_empty + i, 4);
     for (int i = 0; i < kGroups * kVStages; ++i) {
       mbar_init(vs_full + i, 1);
       mbar_init(vs_empty + i, 2);
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
           if (!wait_warp(k_empty + st, (it >> 1) + 1)) break;
           seen = it;
         }
-        if (!wait_warp(ks_full + sg, x.i / kKStages)) break;
+        if (!wait_warp(ks_full + x.i % kKBars, x.i / kKBars)) break;
         unpack_keys<KB, REST>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage,
                               sm + L::kOffK + st * L::kK, sm + L::kOffKr + st * L::kKr, unit + (x.p & 3) * 8);
         fence_proxy_async_smem();
@@ -591,13 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       for (; x.i < n; x.next(a, at, 1)) {
         const int it = x.p - at.p0, sg = x.i % kKStages, sv = x.g * kVStages + it % kVStages;
         if (x.i >= kKStages && !wait_warp(ks_empty + sg, x.i / kKStages + 1)) break;
-        if (lane == 0) copy_keys<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffKs + sg * L::kKStage, ks_full + sg);
+        if (lane == 0) copy_keys<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffKs + sg * L::kKStage, ks_full + x.i % kKBars);
         copied = x.i + 1;  // of its values at most
         if (it >= kVStages && !wait_warp(vs_empty + sv, it / kVStages + 1)) break;
         if (lane == 0) copy_values<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffVs + sv * L::kVStage, vs_full + sv);
       }
       // nothing is in flight when the block ends, also where a wait ran out: the last copy into every stage
-      for (int i = max(0, copied - kKStages); i < copied; ++i) mbar_wait_bounded(ks_full + i % kKStages, (i / kKStages) & 1, 10000000ull);
+      for (int i = max(0, copied - kKStages); i < copied; ++i) mbar_wait_bounded(ks_full + i % kKBars, (i / kKBars) & 1, 10000000ull);
       for (int i = max(0, copied - kGroups * kVStages); i < copied; ++i)
         mbar_wait_bounded(vs_full + i % kGroups * kVStages + i / kGroups % kVStages, (i / kGroups / kVStages) & 1, 10000000ull);
     } else if (warp == 16 + 2 * kGroups) {
