@@ -73,9 +73,11 @@ struct PrefixLayout {
   static constexpr int kOffVs = kOffKs + kKStages * kKStage;
   static constexpr int kOffUnit = kOffVs + kGroups * kVStages * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
   static constexpr int kOffBar = kOffUnit + 4 * 8 * 4;
-  // Landed groups have two barriers a stage, by turns: with an odd number of stages the two sets of warps that unpack keys
-  // take a stage by turns, and a warp has to see every phase of a barrier that it waits on.
-  static constexpr int kKBars = 2 * kKStages;
+  // Barriers of landed groups. With an odd number of stages the two sets of warps that unpack keys take a stage by turns, and a
+  // warp that waits for group i must not meet the phase of group i - kKStages, the other set's, unfinished. Its tile of K' is
+  // free, so all groups of the tile before the last one are unpacked, those up to i - 6 (kGroups = 3): enough for more stages
+  // than that; fewer have two barriers a stage, by turns, so that each is one set's.
+  static constexpr int kKBars = kKStages >= 2 * kGroups ? kKStages : 2 * kKStages;
   static constexpr int kBars = 8 + 4 + 2 * kVTiles + kKBars + kKStages + 2 * kGroups * kVStages;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory of a block");
@@ -834,13 +836,13 @@ cudaError_t launch_prefix_keys(const KiviTreeArgs& a, bool fp32, cudaStream_t st
 }
 
 // Rows of a KV head from which on the kernel above takes the prefix. Measured with it and with the tree kernels (8 KV heads,
-// 4 bits, whole call): 32 rows over 8192 tokens 46 / 44 us, 64 rows 46 / 49, 128 rows 46 / 55; 64 rows over 1024 tokens 28 /
-// 33; 32 KV heads, 2 bits, 4096 tokens: 32 rows 71 / 63, 128 rows 138 / 155.
+// 4 bits, whole call): 32 rows over 8192 tokens 40 / 39 us, 64 rows 40 / 45, 128 rows 42 / 51; 64 rows over 1024 tokens 24 /
+// 30; 32 KV heads, 2 bits, 4096 tokens: 32 rows 52 / 50, 128 rows 95 / 110.
 bool many_rows(int rows) { return rows > 32; }
 // Requests with one row a KV head attend their own caches as the decode does, unsplit, if that makes two blocks an SM (a
 // drafted token is joined apart): it spends a third of the tree kernel's instructions on one row. Measured with it and
-// without (whole call, 32 KV heads, 2 bits): 16 requests of 512 tokens 54 / 67 us, 64 requests of 40 tokens 71 / 95, 128
-// 99 / 138. Four query heads a KV head, 64 requests of 640 tokens, 4 bits: 93 / 86, so not there.
+// without (whole call, 32 KV heads, 2 bits): 16 requests of 512 tokens 54 / 60 us, 64 requests of 40 tokens 66 / 79, 128
+// 95 / 114. Four query heads a KV head, 64 requests of 640 tokens, 4 bits: 89 / 75, so not there.
 bool alone(int B, int N, int H, int rep) { return N == 1 && rep == 1 && (long long)B * H >= 2ll * device_sms(); }
 int row_tiles(int rows) { return (rows + kRows - 1) / kRows; }
 
