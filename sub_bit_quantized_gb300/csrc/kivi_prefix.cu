@@ -45,7 +45,7 @@ namespace {
 // prefix each, 360 us; unpacking by four warps in unrolled code 220 (as many stalls on instruction fetch as issues);
 // rolled loops by group 187; products issued by a warp that walks together 193 -> 182 with one part of the keys; two
 // warps a group of values 179; loops of four code words 170; kRoom 14 for 10 163; copies by a warp of their own 157;
-// passes launched early 144. Tried and dropped: the softmax in pieces with the scores read twice (204 against 187), loads
+// passes launched early 144; the join 140. Tried and dropped: the softmax in pieces with the scores read twice (204 against 187), loads
 // of codes two groups ahead into registers (192: their moves wait for them), spinning on barriers (266).
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
