@@ -36,7 +36,7 @@ struct Move {
 };
 
 // 0: a move; else the error of a slot that cannot be one (-1: nothing to do, -2: to be freed)
-__device__ __forceinline__ int judge(const CacheForkArgs& a, int i, Move& m) {
+__device__ __forceinline__ int check_move(const CacheForkArgs& a, int i, Move& m) {
   const int s = a.source[i];
   m.dst = a.b0 + i;
   m.src = s;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) cache_fork_kernel(const Cac
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
     const int i = tid + k * kThreads;
-    is_move[i] = i < n && judge(a, i, mine[k]) == 0;
+    is_move[i] = i < n && check_move(a, i, mine[k]) == 0;
   }
   if (tid < kForkArrays) {
     longest[tid] = 0;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(KVQ_FORK_MAX) cache_fork_lens_kernel(const Cac
   wait_behind();
   const int i = threadIdx.x;
   Move m = {};
-  const int st = i < a.n ? judge(a, i, m) : -1;
+  const int st = i < a.n ? check_move(a, i, m) : -1;
   if (st > 0) set_error(a.err, st);
   __syncthreads();
   if (st != 0 && st != -2) return;
