@@ -36,7 +36,7 @@ namespace {
 // Roles: warps 0 - 7 softmax (two row tiles, a thread a row); 8 - 15 unpack keys, four warps a 32-token group; 16 - 21
 // unpack values, two warps a group; 22 issues the products; 23 copies what is stored of the groups ahead. Products and
 // softmax of the two row tiles alternate: a tile's scores take the columns of its weights, so the score product waits for
-// the value product. A row's maximum moves only when a score passes it by 2^kRoom, so rescaling O is rare and left to the
+// the value product. A row's maximum moves only when a score passes it by 2^kSlack, so rescaling O is rare and left to the
 // softmax warps.
 //
 // Bound: the chain of a row tile (16 requests x 8 drafts x 4 heads, 32768 tokens, 4 and 2 bits: 36 tiles a block, 4600
@@ -44,18 +44,16 @@ namespace {
 // 45 % of the cycles. What it took (the same case, whole call): the tree kernels, four row tiles of 64 that unpack the
 // prefix each, 360 us; unpacking by four warps in unrolled code 220 (as many stalls on instruction fetch as issues);
 // rolled loops by group 187; products issued by a warp that walks together 193 -> 182 with one part of the keys; two
-// warps a group of values 179; loops of four code words 170; kRoom 14 for 10 163; copies by a warp of their own 157;
-// passes launched early 144; the join 140. Tried and dropped: the softmax in pieces with the scores read twice (204 against 187), loads
+// warps a group of values 179; loops of four code words 170; a room of 14 for kSlack's 10, with 1
+// for kRaise, 163; copies by a warp of their own 157; passes launched early 144; the join 140 (142 as measured since); kSlack
+// and kRaise again 146, as 14 and 1 lose what lies below 2^-26 of a row's largest weight, 2^-30 elsewhere, and thousands of
+// such tokens add up beside one large score. Tried and dropped: the softmax in pieces with the scores read twice (204 against 187), loads
 // of codes two groups ahead into registers (192: their moves wait for them), spinning on barriers (266).
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
 constexpr int kThreads = 768;
 constexpr uint32_t kColS = 112, kColO = 144;     // TMEM columns of S and of O
 constexpr int kVSbo = kTok * 16 + 16;            // V': from eight channels to the next (+ 16: other banks)
-// A row's weights are exp2(x - m + kUp), m its running maximum, which moves when a score passes it by kRoom (log2): one
-// beyond fp16's subnormals, 2^-26 of the maximum's, is lost. With the 5 and 10 of the tree kernels some row of 128 passes
-// its maximum in a third of the first tiles (keys with outlier channels), and each time the products wait.
-constexpr float kRoom = 14.f, kUp = 1.f;
 // REST: the keys' second parts
 template <int KB, int VB, bool REST>
 struct PrefixLayout {
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
     const uint32_t t_s = t_lane + r * kColS, t_o = t_lane + 2 * kColS + r * kColO;
     uint32_t n = 0;                 // tiles done
     bool first = true;
-    float rowc = 0.f, nm = FLT_MAX;  // log2 units per score unit; kUp - running maximum
+    float rowc = 0.f, nm = FLT_MAX;  // log2 units per score unit; kRaise - running maximum
     for (int p = at.p0; p < at.p1; ++p) {
       const bool last = tile + 1 == at.T;
       if (r == 0 || second(seg)) {
@@ -448,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
 #pragma unroll
         for (int i = 0; i < kTok / 2; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(x[i].x, x[i].y));
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowc;
-        const bool up = mx + nm > kRoom + kUp;
+        const bool up = mx + nm > kSlack + kRaise;
         if (__any_sync(0xFFFFFFFFu, up)) {
-          const float f = up ? exp2_approx((kUp - mx) - nm) : 1.f;
-          if (up) nm = kUp - mx;
+          const float f = up ? exp2_approx((kRaise - mx) - nm) : 1.f;
+          if (up) nm = kRaise - mx;
           if (!first) {  // the sums, once the value product of the tile before is done
             if (!wait_warp(bar_o + r, n - 1)) break;
             tmem_after();
