@@ -433,9 +433,8 @@ size_t kvq_kivi_tree_workspace_size(const kvq_kivi_cfg* cfg, int B, int N);
  * mask may all be NULL: rows attend no drafted tokens (decoding after kvq_kivi_append). A row that
  * attends nothing is 0; rows i >= n_draft[b] are padding and stay as they are. An empty prefix or
  * cache counts no tokens. Neither cache is changed. Arithmetic and bounds: those of
- * kvq_kivi_tree_attn, the two parts joined in fp32; but with 4-bit keys, bf16 output and more than 32
- * rows of the call a KV head, s (code - c0) of the prefix's keys (c0 the middle code) is rounded once to
- * fp16, which moves a score by at most 2^-11 sum |q s (code - c0)| / sqrt(D).
+ * kvq_kivi_tree_attn, the two parts joined in fp32, however many rows share the prefix; a bf16 output
+ * is the fp32 one rounded.
  * ws: device workspace of at least kvq_kivi_prefix_workspace_size() bytes, needing no
  * initialisation. Two calls that run at the same time need two workspaces.
  * Errors: KVQ_ERR_INVALID_ARG (heads that differ, slot < 0, drafts without a mask), KVQ_ERR_CAPACITY

@@ -28,10 +28,11 @@ namespace {
 // The constants enter as further tokens and channels of the same two products, so what a group lies off
 // from zero is never rounded to fp16 (as in the tree kernels). 96 tokens: 2 (112 + 144) fp32 columns are
 // the 512 of TMEM.
-// s (c - c0) is exact in one fp16 at 2 bits. At 4 bits it takes two for fp32 outputs (REST: a second product with what
-// the rounding left); for bf16 outputs it is rounded once, by 2^-11 of itself, which moves a score by at most
-// 2^-11 sum |q s (c - c0)| / sqrt(D) and adds little to the output's own rounding (relative error against fp64 1.8e-3, of
-// the rounding alone 1.7e-3). 512 rows over 32768 tokens: 142 us rounded, 198 in two parts.
+// s (c - c0) is exact in one fp16 at 2 bits. At 4 bits it takes two (kRest: a second product with what the rounding left),
+// as in the tree kernels, so that a row's precision does not depend on how many others share the prefix. Rounded once it is
+// off by 2^-11, which moves outputs by up to 6e-3 (queries as they come; by 4.6e-2 with eight times larger ones) against a
+// bf16 rounding of 3e-2 at most. 512 rows over 32768 tokens: 142 us rounded, 159 in two parts; 256 rows over 8191 tokens 75
+// and 81.
 //
 // Roles: warps 0 - 7 softmax (two row tiles, a thread a row); 8 - 15 unpack keys, four warps a 32-token group; 16 - 21
 // unpack values, two warps a group; 22 issues the products; 23 copies what is stored of the groups ahead. Products and
@@ -54,15 +55,17 @@ constexpr int kRows = 256;                       // of a segment: two row tiles
 constexpr int kThreads = 768;
 constexpr uint32_t kColS = 112, kColO = 144;     // TMEM columns of S and of O
 constexpr int kVSbo = kTok * 16 + 16;            // V': from eight channels to the next (+ 16: other banks)
-// REST: the keys' second parts
-template <int KB, int VB, bool REST>
+template <int KB, int VB>
 struct PrefixLayout {
-  static constexpr int kVTiles = REST ? 1 : 2;             // tiles of unpacked values
-  static constexpr int kKStages = REST ? 5 : 9, kVStages = REST ? 1 : 2;  // groups whose stored keys are on their way; a warp's values
+  static constexpr bool kRest = KB == 4;                   // the keys have second parts
+  static constexpr int kVTiles = kRest ? 1 : 2;            // tiles of unpacked values
+  // Groups whose stored keys are on their way; a warp's values. What is left of shared memory beside the second parts goes
+  // to two stages of values first: 512 rows over 32768 tokens 159 us with (6, 2) to (8, 2), 196 with (9, 1), 200 with (5, 1).
+  static constexpr int kKStages = kRest ? 6 : 9, kVStages = 2;
   // a group's stored keys or values: codes, scales, zero-points
   static constexpr int kKCode = kGroupT * kD * KB / 8, kVCode = kGroupT * kD * VB / 8, kPart = kD * 2;
   static constexpr int kKStage = kKCode + 2 * kPart, kVStage = kVCode + 2 * kPart;
-  static constexpr int kK = (kTok + 16) * kD * 2, kKr = REST ? kTok * kD * 2 : 0, kV = 18 * kVSbo;
+  static constexpr int kK = (kTok + 16) * kD * 2, kKr = kRest ? kTok * kD * 2 : 0, kV = 18 * kVSbo;
   static constexpr int kOffQ = 0;                          // fp16 [2][128 x 128], K-major
   static constexpr int kOffK = kOffQ + 2 * 128 * kD * 2;   // [2] K' of a tile (112 rows), K-major
   static constexpr int kOffKr = kOffK + 2 * kK;            // [2] second parts of the keys
@@ -71,12 +74,12 @@ struct PrefixLayout {
   static constexpr int kOffVs = kOffKs + kKStages * kKStage;
   static constexpr int kOffUnit = kOffVs + kGroups * kVStages * kVStage;  // float [4][8]: what a group's sums count, constants' from 4
   static constexpr int kOffBar = kOffUnit + 4 * 8 * 4;
-  // Barriers of landed groups. With an odd number of stages the two sets of warps that unpack keys take a stage by turns, and a
-  // warp that waits for group i must not meet the phase of group i - kKStages, the other set's, unfinished. Its tile of K' is
-  // free, so all groups of the tile before the last one are unpacked, those up to i - 6 (kGroups = 3): enough for more stages
-  // than that; fewer have two barriers a stage, by turns, so that each is one set's.
-  static constexpr int kKBars = kKStages >= 2 * kGroups ? kKStages : 2 * kKStages;
-  static constexpr int kBars = 8 + 4 + 2 * kVTiles + kKBars + kKStages + 2 * kGroups * kVStages;
+  // A barrier of landed groups is waited on by the set of warps that unpacks the group. With an even number of stages a stage is
+  // one set's. With an odd one the two sets take it by turns, and a warp that waits for group i must not meet the phase of group
+  // i - kKStages, the other set's, unfinished: its tile of K' is free, so all groups of the tile before the last one are
+  // unpacked, those up to i - 6 (kGroups = 3).
+  static_assert(kKStages % 2 == 0 || kKStages >= 2 * kGroups, "phases that a set of warps does not see");
+  static constexpr int kBars = 8 + 4 + 2 * kVTiles + 2 * kKStages + 2 * kGroups * kVStages;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory of a block");
 };
@@ -107,10 +110,11 @@ __device__ __forceinline__ PrefixPlace prefix_place(const KiviTreeArgs& a, const
 // ---- keys of a 32-token group, by four warps: warp w takes channels 32 w .. + 31 of every token. A lane takes token
 //      lane % 8 of an octet and a code word (2 bits: 16 channels, two octets; 4 bits: 8 channels, four octets). ----
 // t: the group's first token; g: its place in the tile; stage: what is stored of it
-template <int KB, bool REST>
+template <int KB>
 __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTreeArgs& a, const TreeLens& len, int h, int t, int g,
                                             int w, int lane, const unsigned char* stage, unsigned char* dst, unsigned char* rest,
                                             float* unit) {
+  constexpr bool kRest = KB == 4;
   constexpr int kPairs = KB == 2 ? 8 : 4, kOct = KB == 2 ? 2 : 4, kRow = kD * KB / 8;
   const int word = KB == 2 ? 2 * w + ((lane >> 3) & 1) : 4 * w + (lane >> 3), oct = KB == 2 ? 2 * (lane >> 4) : 0;
   const int at0 = (4 * g + oct) * 2048 + word * (kPairs * 32) + (lane & 7) * 16;
@@ -177,11 +181,11 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
       for (int j = 0; j < kPairs; ++j) {
         const __half2 c = code_h2<KB, kCentre<KB>>(cs0, code, j);
         x[j] = as_u(__hmul2(c, s[j]));
-        if constexpr (REST) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
+        if constexpr (kRest) y[j] = product_rest(as_u(c), as_u(s[j]), x[j]);
       }
       *reinterpret_cast<uint4*>(dst + at0 + 2048 * i) = make_uint4(x[0], x[1], x[2], x[3]);
       if constexpr (KB == 2) *reinterpret_cast<uint4*>(dst + at0 + 2048 * i + 128) = make_uint4(x[4], x[5], x[6], x[7]);
-      if constexpr (REST) *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+      if constexpr (kRest) *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   } else {  // fp16 rows, or none
     if (w == g) {
@@ -199,7 +203,7 @@ __device__ __forceinline__ void unpack_keys(const CodeScale& cs0, const KiviTree
       } else {
         const uint4 v = row8(row, word);
         pair_order<4>(v, v, x0, x1);
-        if constexpr (REST) *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(rest + at0 + 2048 * i) = make_uint4(0u, 0u, 0u, 0u);
       }
       *reinterpret_cast<uint4*>(dst + at0 + 2048 * i) = x0;
     }
@@ -253,9 +257,9 @@ __device__ __forceinline__ void unpack_values(const CodeScale& cs0, const KiviTr
 }
 
 // What is stored of a group into a stage, by one thread; with nothing to copy the barrier completes at once.
-template <int KB, int VB, bool REST>
+template <int KB, int VB>
 __device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens& len, int h, int t, unsigned char* stage, uint64_t* full) {
-  using L = PrefixLayout<KB, VB, REST>;
+  using L = PrefixLayout<KB, VB>;
   if (t >= len.nqk) {
     mbar_arrive(full);
     return;
@@ -266,9 +270,9 @@ __device__ __forceinline__ void copy_keys(const KiviTreeArgs& a, const TreeLens&
   bulk_g2s(stage + L::kKCode, a.k_scale + g, L::kPart, full);
   bulk_g2s(stage + L::kKCode + L::kPart, a.k_zero + g, L::kPart, full);
 }
-template <int KB, int VB, bool REST>
+template <int KB, int VB>
 __device__ __forceinline__ void copy_values(const KiviTreeArgs& a, const TreeLens& len, int h, int t, unsigned char* stage, uint64_t* full) {
-  using L = PrefixLayout<KB, VB, REST>;
+  using L = PrefixLayout<KB, VB>;
   if (t >= len.nqv) {
     mbar_arrive(full);
     return;
@@ -300,10 +304,10 @@ struct Groups {
   }
 };
 
-template <int KB, int VB, bool REST>
+template <int KB, int VB>
 __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTreeArgs a, const float scale_log2) {
-  using L = PrefixLayout<KB, VB, REST>;
-  constexpr int kVTiles = L::kVTiles, kKStages = L::kKStages, kKBars = L::kKBars, kVStages = L::kVStages;
+  using L = PrefixLayout<KB, VB>;
+  constexpr int kVTiles = L::kVTiles, kKStages = L::kKStages, kVStages = L::kVStages;
   extern __shared__ __align__(128) unsigned char sm[];
   float* unit = reinterpret_cast<float*>(sm + L::kOffUnit);
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(sm + L::kOffBar);  // [2] a row tile's queries are there
@@ -314,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   uint64_t* k_empty = bar_q + 10;                                   // [2] and read
   uint64_t* v_full = bar_q + 12;                                    // [kVTiles] a tile's values are unpacked
   uint64_t* v_empty = v_full + kVTiles;                             // [kVTiles] and read
-  uint64_t* ks_full = v_empty + kVTiles;                            // [kKBars] a group's stored keys landed
-  uint64_t* ks_empty = ks_full + kKBars;                            // [kKStages] and are unpacked
+  uint64_t* ks_full = v_empty + kVTiles;                            // [kKStages] a group's stored keys landed
+  uint64_t* ks_empty = ks_full + kKStages;                          // [kKStages] and are unpacked
   uint64_t* vs_full = ks_empty + kKStages;                          // [kGroups][kVStages] a tile's group's stored values landed
   uint64_t* vs_empty = vs_full + kGroups * kVStages;                // and are unpacked
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q + L::kBars);
@@ -345,8 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       mbar_init(v_full + i, 2 * kGroups);
       mbar_init(v_empty + i, 1);
     }
-    for (int i = 0; i < kKBars; ++i) mbar_init(ks_full + i, 1);
-    for (int i = 0; i < kKStages; ++i) mbar_init(ks_empty + i, 4);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(ks_full + i, 1);
+      mbar_init(ks_empty + i, 4);
+    }
     for (int i = 0; i < kGroups * kVStages; ++i) {
       mbar_init(vs_full + i, 1);
       mbar_init(vs_empty + i, 2);
@@ -551,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
           if (!wait_warp(k_empty + st, (it >> 1) + 1)) break;
           seen = it;
         }
-        if (!wait_warp(ks_full + x.i % kKBars, x.i / kKBars)) break;
-        unpack_keys<KB, REST>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage,
+        if (!wait_warp(ks_full + sg, x.i / kKStages)) break;
+        unpack_keys<KB>(cs0, a, len, x.h, x.t, x.g, warp & 3, lane, sm + L::kOffKs + sg * L::kKStage,
                               sm + L::kOffK + st * L::kK, sm + L::kOffKr + st * L::kKr, unit + (x.p & 3) * 8);
         fence_proxy_async_smem();
         arrive(ks_empty + sg);
@@ -592,13 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       for (; x.i < n; x.next(a, at, 1)) {
         const int it = x.p - at.p0, sg = x.i % kKStages, sv = x.g * kVStages + it % kVStages;
         if (x.i >= kKStages && !wait_warp(ks_empty + sg, x.i / kKStages + 1)) break;
-        if (lane == 0) copy_keys<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffKs + sg * L::kKStage, ks_full + x.i % kKBars);
+        if (lane == 0) copy_keys<KB, VB>(a, len, x.h, x.t, sm + L::kOffKs + sg * L::kKStage, ks_full + sg);
         copied = x.i + 1;  // of its values at most
         if (it >= kVStages && !wait_warp(vs_empty + sv, it / kVStages + 1)) break;
-        if (lane == 0) copy_values<KB, VB, REST>(a, len, x.h, x.t, sm + L::kOffVs + sv * L::kVStage, vs_full + sv);
+        if (lane == 0) copy_values<KB, VB>(a, len, x.h, x.t, sm + L::kOffVs + sv * L::kVStage, vs_full + sv);
       }
       // nothing is in flight when the block ends, also where a wait ran out: the last copy into every stage
-      for (int i = max(0, copied - kKStages); i < copied; ++i) mbar_wait_bounded(ks_full + i % kKBars, (i / kKBars) & 1, 10000000ull);
+      for (int i = max(0, copied - kKStages); i < copied; ++i) mbar_wait_bounded(ks_full + i % kKStages, (i / kKStages) & 1, 10000000ull);
       for (int i = max(0, copied - kGroups * kVStages); i < copied; ++i)
         mbar_wait_bounded(vs_full + i % kGroups * kVStages + i / kGroups % kVStages, (i / kGroups / kVStages) & 1, 10000000ull);
     } else if (warp == 16 + 2 * kGroups) {
@@ -616,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
         const uint32_t q = q0 + r * (128 * kD * 2 / 16), k = k0 + st * (L::kK / 16), d = tm + r * kColS;
 #pragma unroll
         for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kColS, false)>(leader, d, q + 16 * i, k + 16 * i, i > 0);
-        if constexpr (REST) {
+        if constexpr (L::kRest) {
           const uint32_t kk = kr0 + st * (L::kKr / 16);
 #pragma unroll
           for (int i = 0; i < 8; ++i) umma_lo<kHi, kHi, tree_idesc(kTok, false)>(leader, d, q + 16 * i, kk + 16 * i, 1);
@@ -818,19 +824,18 @@ __global__ void __launch_bounds__(kJoinThreads) kivi_prefix_join_kernel(const Ki
   combine_row(a, at, {l == 0.f ? -INFINITY : top + __log2f(l), make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv)}, own, z);
 }
 
-template <int KB, int VB, bool REST>
+template <int KB, int VB>
 cudaError_t launch_prefix_rows(const KiviTreeArgs& a, cudaStream_t st) {
-  auto kernel = kivi_prefix_kernel<KB, VB, REST>;
-  constexpr int kSmem = PrefixLayout<KB, VB, REST>::kSmem;
+  auto kernel = kivi_prefix_kernel<KB, VB>;
+  constexpr int kSmem = PrefixLayout<KB, VB>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<a.blocks.d, kThreads, kSmem, st>>>(a, 1.4426950408889634f / sqrtf((float)kD));
   return cudaGetLastError();
 }
-template <int VB>
-cudaError_t launch_prefix_keys(const KiviTreeArgs& a, bool fp32, cudaStream_t st) {
-  if (a.k_bits == 2) return launch_prefix_rows<2, VB, false>(a, st);
-  return fp32 ? launch_prefix_rows<4, VB, true>(a, st) : launch_prefix_rows<4, VB, false>(a, st);
+cudaError_t launch_prefix_bits(const KiviTreeArgs& a, cudaStream_t st) {
+  if (a.k_bits == 2) return a.v_bits == 2 ? launch_prefix_rows<2, 2>(a, st) : launch_prefix_rows<2, 4>(a, st);
+  return a.v_bits == 2 ? launch_prefix_rows<4, 2>(a, st) : launch_prefix_rows<4, 4>(a, st);
 }
 
 // Rows of a KV head from which on the kernel above takes the prefix. Measured with it and with the tree kernels (8 KV heads,
@@ -871,7 +876,7 @@ cudaError_t launch_kivi_prefix(const KiviPrefixArgs& args, cudaStream_t st) {
     t.segs = int_div(t.H * t.row_tiles.d);
     t.blocks = int_div(device_sms());
     t.ring = int_div(t.residual);
-    e = t.v_bits == 2 ? launch_prefix_keys<2>(t, a.out_fp32, st) : launch_prefix_keys<4>(t, a.out_fp32, st);
+    e = launch_prefix_bits(t, st);
   } else {
     t.chained = kChainedFirst;
     e = launch_kivi_tree(t, st, kTreeAttend);
