@@ -846,7 +846,14 @@ bool many_rows(int rows) { return rows > 32; }
 // drafted token is joined apart): it spends a third of the tree kernel's instructions on one row. Measured with it and
 // without (whole call, 32 KV heads, 2 bits): 16 requests of 512 tokens 54 / 60 us, 64 requests of 40 tokens 66 / 79, 128
 // 95 / 114. Four query heads a KV head, 64 requests of 640 tokens, 4 bits: 89 / 75, so not there.
-bool alone(int B, int N, int H, int rep) { return N == 1 && rep == 1 && (long long)B * H >= 2ll * device_sms(); }
+// One block walks a (request, head) to its end, so a long request holds up a call of short ones, which the tree kernels split.
+// The host knows the caches' capacity alone: up to 2048 tokens of it (16 requests, 32 heads over 1024 tokens: all of 2048 75 /
+// 85, one of 2048 among 64s 48 / 46; beyond, all of 4096 112 / 122 and of 8192 187 / 198, but one of 4096 69 / 54, of 16384
+// 183 / 98; 64 requests, 8 heads, one of 16384: 138 / 54).
+constexpr int kAloneTokens = 2048;
+bool alone(const KiviTreeArgs& a, int rep) {
+  return a.N == 1 && rep == 1 && a.max_tokens <= kAloneTokens && (long long)a.B * a.H >= 2ll * device_sms();
+}
 int row_tiles(int rows) { return (rows + kRows - 1) / kRows; }
 
 }  // namespace
@@ -883,7 +890,7 @@ cudaError_t launch_kivi_prefix(const KiviPrefixArgs& args, cudaStream_t st) {
   }
   // every further launch is early: the blocks of both passes share the GPU, and what joins them is there when they end
   KiviTreeArgs& o = a.own;
-  a.apart = alone(o.B, o.N, o.H, rep);
+  a.apart = alone(o, rep);
   o.chained = kChainedBehind;
   t.rep = int_div(rep);
   if (e == cudaSuccess && a.apart) {
