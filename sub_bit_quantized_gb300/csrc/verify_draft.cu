@@ -167,13 +167,6 @@ __device__ __forceinline__ int entry8(int v, int j, int lane, bool wide) {
   return wide ? v + 128 * (j >> 2) + 4 * lane + (j & 3) : v + 32 * j + lane;
 }
 
-// A row's entries v0 .. v1 - 1 on their way to L2, whole 16-byte pieces of them
-template <typename T>
-__device__ __forceinline__ void fetch_row(const T* row, int v0, int v1) {
-  const uintptr_t from = (reinterpret_cast<uintptr_t>(row + v0) + 15) & ~(uintptr_t)15, to = reinterpret_cast<uintptr_t>(row + v1) & ~(uintptr_t)15;
-  if (from < to) bulk_prefetch_l2(reinterpret_cast<const void*>(from), (uint32_t)min((unsigned long long)(to - from), 1ull << 28));
-}
-
 // Of the cluster's blocks, by turns: what each found
 struct Exchange {
   uint64_t total[2][kMaxCluster];
