@@ -434,7 +434,9 @@ size_t kvq_kivi_tree_workspace_size(const kvq_kivi_cfg* cfg, int B, int N);
  * attends nothing is 0; rows i >= n_draft[b] are padding and stay as they are. An empty prefix or
  * cache counts no tokens. Neither cache is changed. Arithmetic and bounds: those of
  * kvq_kivi_tree_attn, the two parts joined in fp32, however many rows share the prefix; a bf16 output
- * is the fp32 one rounded.
+ * is the fp32 one rounded. With one row a KV head, two (request, KV head) pairs an SM and caches of up to
+ * 2048 tokens' capacity the requests' own tokens are attended as kvq_decode_attn does, with one query head:
+ * a weight times its value scale rounded to fp16 once (relative 2^-11, absolute 2^-25).
  * ws: device workspace of at least kvq_kivi_prefix_workspace_size() bytes, needing no
  * initialisation. Two calls that run at the same time need two workspaces.
  * Errors: KVQ_ERR_INVALID_ARG (heads that differ, slot < 0, drafts without a mask), KVQ_ERR_CAPACITY
@@ -471,7 +473,9 @@ enum { KVQ_SLOT_KEEP = -1, KVQ_SLOT_FREE = -2 };
  * KVQ_ERR_CAPACITY. Calls that change either cache must not run at the same time. n = 0 is a no-op
  * (source may be NULL then).
  * Errors: KVQ_ERR_INVALID_ARG (pointers, negative sizes, shapes that differ), KVQ_ERR_CAPACITY (b0 +
- * n > max_batch), KVQ_ERR_UNSUPPORTED (n > KVQ_FORK_MAX, or more than 2^31 blocks). */
+ * n > max_batch), KVQ_ERR_UNSUPPORTED (n > KVQ_FORK_MAX; max_tokens, or max_pages, of 2^25 and more;
+ * 2^31 layers x loop steps x heads and more; an array with 2^36 bytes a slot and layer, or arrays with 2^38 a
+ * slot, and more). */
 #define KVQ_FORK_MAX 256
 kvq_status kvq_cache_fork(int format, const void* cfg, const void* cache, const void* from_cfg,
                           const void* from, const int32_t* source, int b0, int n, kvq_stream stream);
@@ -502,7 +506,7 @@ typedef struct {
  * max(0, R - Q), normalised. Point masses: u Z < w(x), w = P without the tokens rejected at the
  * node; a rejection takes w(x) off Z. The next token is drawn from w at the path's end: the lowest v
  * with w(0) + .. + w(v) > u[b][0] sum of w (w = P if the residual has no mass). Sums are exact to
- * 2^-44 of themselves and more, so they do not depend on how the work is split.
+ * 2^-44 of the sum of P and a Q (V up to 2^24; 2^-36 at 2^30), so they do not depend on how the work is split.
  * u NULL: no sampling. A child is accepted if its token is the lowest index of the largest entry of
  * the target's row (probabilities or logits; NaN counts as the lowest value), and the next token is that
  * entry's index at the path's end; draft is NULL then.
@@ -514,7 +518,7 @@ typedef struct {
  * token, parent, path: int32 [B][N]; u: fp32 [B][N]; n_draft, n_accept, next: int32 [B]; all on the
  * device. target and draft: 16-byte aligned, any strides >= 0, of one type.
  * B = 0 or N = 0 is a no-op (the arrays may be NULL then).
- * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (N > 64, B > 65535). */
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (N > 64, B > 65535, V > 2^30). */
 kvq_status kvq_verify_draft(int B, int N, int V, const kvq_dist* target, const kvq_dist* draft,
                             const int32_t* token, const int32_t* parent, const int32_t* n_draft,
                             const float* u, int32_t* path, int32_t* n_accept, int32_t* next,
@@ -536,7 +540,7 @@ kvq_status kvq_verify_draft(int B, int N, int V, const kvq_dist* target, const k
  * weight rounded to the nearest unit once, an absolute error of at most 2^-21), then
  * multiplied by the fp16 value codebook in fp32. KIVI, when a block serves one query head
  * (n_q_heads / n_heads odd), rounds each token's weight to fp16 once in an fp16 x fp16 + fp32
- * FMA (relative error 2^-12); otherwise fp32 throughout.
+ * FMA (relative error 2^-11); otherwise fp32 throughout.
  *
  * format KVQ_FMT_LOOPVQ: cfg is kvq_vq_cfg*, cache kvq_vq_cache*; layer and loop_step
  *   select the cache slice. The query sits at position seq_len[b] - 1; every key and the
