@@ -126,41 +126,61 @@ __device__ __forceinline__ void store_remote(void* p, uint32_t rank, uint64_t v)
       : "memory");
 }
 
-// Eight entries of a row for a lane, 0 from `end` on. wide (the row's address allows it): entries 4 k + e are at v + 128 k +
-// 4 lane + e, in loads of four; else entry j is at v + 32 j + lane, one by one, so that a warp's loads stay contiguous at
-// any alignment.
+// Eight entries of a row for a lane, 0 from `end` on, as they lie in memory: converted where they are used, or the conversion
+// would wait for the loads that are to be on their way meanwhile (64 chains of 131072 bf16 entries 51 us). wide (the row's
+// address allows it): entries 4 k + e are at v + 128 k + 4 lane + e, in loads of four, 16-bit ones two a word; else entry j is
+// at v + 32 j + lane, one by one, so that a warp's loads stay contiguous at any alignment.
 constexpr int kStep = 256;  // entries of a warp's step
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int v, int end, int lane, bool wide, float2 (&x)[4]) {
-  float y[8];
+__device__ __forceinline__ uint32_t raw(T x) {
+  if constexpr (sizeof(T) == 4) return __float_as_uint(x);
+  else return *reinterpret_cast<const uint16_t*>(&x);
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int v, int end, int lane, bool wide, uint32_t (&w)[8]) {
   if (wide) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int at = v + 128 * k + 4 * lane;
       if (at + 4 <= end) {
         if constexpr (sizeof(T) == 4) {
-          const float4 f = __ldg(reinterpret_cast<const float4*>(row + at));
-          y[4 * k] = f.x; y[4 * k + 1] = f.y; y[4 * k + 2] = f.z; y[4 * k + 3] = f.w;
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + at));
+          w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
         } else {
           const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + at));
-          const T* t = reinterpret_cast<const T*>(&u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[4 * k + e] = to_f(t[e]);
+          w[2 * k] = u.x; w[2 * k + 1] = u.y;
         }
       } else {
+        uint32_t y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[4 * k + e] = at + e < end ? to_f(row[at + e]) : 0.f;
+        for (int e = 0; e < 4; ++e) y[e] = at + e < end ? raw(row[at + e]) : 0u;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[4 * k + e] = y[e];
+        } else {
+          w[2 * k] = y[0] | y[1] << 16;
+          w[2 * k + 1] = y[2] | y[3] << 16;
+        }
       }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int at = v + 32 * j + lane;
-      y[j] = at < end ? to_f(row[at]) : 0.f;
+      w[j] = at < end ? raw(row[at]) : 0u;
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
+}
+// entries 2 i, 2 i + 1 of them
+template <typename T>
+__device__ __forceinline__ float2 pair_of(const uint32_t (&w)[8], int i, bool wide) {
+  if constexpr (sizeof(T) == 4) {
+    return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  } else {
+    const uint32_t u = wide ? w[i] : __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
 }
 // which entry that is
 __device__ __forceinline__ int entry8(int v, int j, int lane, bool wide) {
@@ -503,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
     };
     // ---- sums of w over the block's chunks; a step's entries are on their way while the one before is added ----
     const int per = a.chunk / kStep, steps = warp < n_chunks ? ((n_chunks - 1 - warp) / kWarps + 1) * per : 0;
-    float2 p[4], q[4], pn[4], qn[4];
+    uint32_t p[8], q[8], pn[8], qn[8];
     Sum2 sum = {f2(0.f), f2(0.f)};
     int at_v = 0, at_end = 0;  // the step that is added
 #pragma unroll 1
@@ -517,20 +537,23 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
         if (qrow) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const Weight2 w = weight(p[i], q[i], a_hi, a_lo);
+            const Weight2 w = weight(pair_of<T>(p, i, wide), pair_of<T>(q, i, wide), a_hi, a_lo);
             sum.add(w.hi);
             sum.lo = __fadd2_rn(sum.lo, w.lo);
           }
         } else {
+          float2 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = pair_of<T>(p, i, wide);
           for (int g = 0; g < n_gone; ++g) {
-            const int x = s.gone[g];
-            if (x < at_v || x >= min(at_end, at_v + kStep)) continue;
+            const int t = s.gone[g];
+            if (t < at_v || t >= min(at_end, at_v + kStep)) continue;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (entry8(at_v, j, lane, wide) == x) (j & 1 ? p[j >> 1].y : p[j >> 1].x) = 0.f;
+              if (entry8(at_v, j, lane, wide) == t) (j & 1 ? x[j >> 1].y : x[j >> 1].x) = 0.f;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum.add(p[i]);
+          for (int i = 0; i < 4; ++i) sum.add(x[i]);
         }
         if (k % per == 0) {
           const Two t = warp_sum(sum.total());
@@ -539,7 +562,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) verify_kernel(const Ve
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         p[i] = pn[i];
         q[i] = qn[i];
       }
