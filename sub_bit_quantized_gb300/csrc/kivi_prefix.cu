@@ -323,7 +323,6 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   uint64_t* vs_full = ks_empty + kKStages;                          // [kGroups][kVStages] a tile's group's stored values landed
   uint64_t* vs_empty = vs_full + kGroups * kVStages;                // and are unpacked
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q + L::kBars);
-  volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const TreeLens len = tree_lens(a, 0, kTok);
@@ -357,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
       mbar_init(vs_full + i, 1);
       mbar_init(vs_empty + i, 2);
     }
-    *failed = 0;
     fence_mbar_init();
   }
   tmem_before();
@@ -367,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1) kivi_prefix_kernel(const KiviTree
   // a wait that runs out ends its role, and with it the waits of the others
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait_bounded_sleep(bar, parity & 1)) return true;
-    *failed = 1;
     set_error(a.err, KVQ_ERR_TIMEOUT);
     return false;
   };
