@@ -10,9 +10,11 @@
 //
 // Bound: HBM, each moved byte read once per distinct source and written once per slot, behind a chain of dependent loads
 // (sources, lengths, table, first units: about 5 us). A prompt of 4096 tokens to 16 slots (32 heads, 2 bits, 243 MB): 52 us,
-// 4.7 TB/s, 69 % of the copy rate; 64 beams of 1531 tokens in place, about half of which move: 30; eight slots of 701 tokens in
-// index pages: 17. The first form took 64, 39 and 20. Blocks of 256 threads, batches of 4 and 16
-// moves, streaming stores and loads past L1 were not better.
+// 4.7 TB/s, 69 % of the copy rate; 64 beams of 1531 tokens in place, about half of which move: 31; eight slots of 701 tokens in
+// index pages: 16 - 18. The first form took 64, 39 and 20. Blocks of 256 threads, batches of 4 and 16
+// moves, streaming stores and loads past L1 were not better. Moves with hazards, every unit by way of shared memory: 64 slots of
+// 1531 tokens (8 heads, 4 bits) compacted to 43 57 us (floor 29), in another order 98 (42); 16 slots of 4096 (32 heads, 2 bits)
+// in a ring 124 (67).
 #include <algorithm>
 
 #include "kvq_common.cuh"

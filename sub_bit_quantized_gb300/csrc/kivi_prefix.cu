@@ -40,16 +40,18 @@ namespace {
 // the value product. A row's maximum moves only when a score passes it by 2^kSlack, so rescaling O is rare and left to the
 // softmax warps.
 //
-// Bound: the chain of a row tile (16 requests x 8 drafts x 4 heads, 32768 tokens, 4 and 2 bits: 36 tiles a block, 4600
-// cycles each): score product 500 cycles, softmax 1700 - 2300, value product 450, and the barriers between them 900; issue
-// 45 % of the cycles. What it took (the same case, whole call): the tree kernels, four row tiles of 64 that unpack the
-// prefix each, 360 us; unpacking by four warps in unrolled code 220 (as many stalls on instruction fetch as issues);
-// rolled loops by group 187; products issued by a warp that walks together 193 -> 182 with one part of the keys; two
-// warps a group of values 179; loops of four code words 170; a room of 14 for kSlack's 10, with 1
-// for kRaise, 163; copies by a warp of their own 157; passes launched early 144; the join 140 (142 as measured since); kSlack
-// and kRaise again 146, as 14 and 1 lose what lies below 2^-26 of a row's largest weight, 2^-30 elsewhere, and thousands of
-// such tokens add up beside one large score. Tried and dropped: the softmax in pieces with the scores read twice (204 against 187), loads
-// of codes two groups ahead into registers (192: their moves wait for them), spinning on barriers (266).
+// Bound: the chain of a row tile (16 requests x 8 drafts x 4 heads, 32768 tokens, 4 and 2 bits, 126 us of the call's 158): 36
+// tiles a block, 5700 cycles each with the begins and ends of segments (SMs are active 205 k cycles; the launch's 250 k under
+// the profiler have its own begin and end): score product 500 cycles a part, softmax 1700 - 2300, value product 450, the
+// barriers between them 900. Of the active cycles the tensor pipe has 44 %, issue 47 %, ALU 30 %, FMA 27 %. What it took (the
+// same case, whole call with L2 flushed before it): the tree kernels, four row tiles of 64 that unpack the prefix each, 360 us;
+// unpacking by four warps in unrolled code 220 (as many stalls on instruction fetch as issues); rolled loops by group 187;
+// products issued by a warp that walks together 193 -> 182 with one part of the keys; two warps a group of values 179; loops of
+// four code words 170; a room of 14 for kSlack's 10, with 1 for kRaise, 163; copies by a warp of their own 157; passes launched
+// early 144; the join 140 (142 as measured since); kSlack and kRaise again 146, as 14 and 1 lose what lies below 2^-26 of a
+// row's largest weight, 2^-30 elsewhere, and thousands of such tokens add up beside one large score; two parts of the keys 159.
+// Tried and dropped: the softmax in pieces with the scores read twice (204 against 187), loads of codes two groups ahead into
+// registers (192: their moves wait for them), spinning on barriers (266).
 constexpr int kTok = 96, kGroups = kTok / kGroupT;
 constexpr int kRows = 256;                       // of a segment: two row tiles
 constexpr int kThreads = 768;
@@ -835,9 +837,11 @@ cudaError_t launch_prefix_bits(const KiviTreeArgs& a, cudaStream_t st) {
   return a.v_bits == 2 ? launch_prefix_rows<4, 2>(a, st) : launch_prefix_rows<4, 4>(a, st);
 }
 
-// Rows of a KV head from which on the kernel above takes the prefix. Measured with it and with the tree kernels (8 KV heads,
-// 4 bits, whole call): 32 rows over 8192 tokens 40 / 39 us, 64 rows 40 / 45, 128 rows 42 / 51; 64 rows over 1024 tokens 24 /
-// 30; 32 KV heads, 2 bits, 4096 tokens: 32 rows 52 / 50, 128 rows 95 / 110.
+// Rows of a KV head from which on the kernel above takes the prefix. Measured with it and with the tree kernels (whole call, 4
+// bits): 8 KV heads, 36 rows over 1024, 4096 and 8192 tokens 26 / 28 us, 36 / 33, 40 / 43; 64 rows 24 / 29, 36 / 40, 40 / 44; 128
+// rows 26 / 31, 38 / 42, 41 / 51; 32 KV heads, 33 rows 45 / 44, 58 / 58, 79 / 75; 64 rows 58 / 60, 74 / 75, 93 / 93; 128 rows
+// 95 / 95, 112 / 122, 130 / 159. 2 bits alike. Up to 32 rows the tree kernels have a tile for all of them: 32 rows over 8192
+// tokens, 8 KV heads, 40 / 39.
 bool many_rows(int rows) { return rows > 32; }
 // Requests with one row a KV head attend their own caches as the decode does, unsplit, if that makes two blocks an SM (a
 // drafted token is joined apart): it spends a third of the tree kernel's instructions on one row. Measured with it and

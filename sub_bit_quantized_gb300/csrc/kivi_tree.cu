@@ -221,8 +221,8 @@ __device__ __forceinline__ void prefetch_fp16(const KiviTreeArgs& a, const TreeL
 //    8 s passes the fp16 range for values near its end.
 // Bound: instruction issue (53 % of the cycles) and fixed latencies. A group of 32 tokens costs a warp 940 instructions at
 // 8 rows (counted over a launch, segment ends included): one a code pair for the keys, three for the values, 66 products.
-// Measured (16 requests, 32 KV heads, 4K context, 2 bits): 98 us for 8 rows (208 MB, 2.1 TB/s, 31 % of the copy rate; 102
-// before the fp16 rows' loads started together), 164 us for 16 then. Without q'' and with values dequantized to one fp16 it took 80 and 126 us, outside the bound of
+// Measured (16 requests, 32 KV heads, 4K context, 2 bits): 98 us for 8 rows (208 MB, 2.1 TB/s, 31 % of the copy rate),
+// 144 us for 16 (102 and 164 before the fp16 rows' loads started together). Without q'' and with values dequantized to one fp16 it took 80 and 126 us, outside the bound of
 // attention (max-abs 2e-3): worst error of random cases 7e-3, now 1.7e-3. Per-warp rings of two groups by cp.async
 // (each lane copies what its warp reads, so no block barrier in the loop); four blocks of four warps an SM for 8 rows, two
 // for 16, as the registers of the sums allow (three, with spills in the loop: 173 us). Five blocks of 96 registers for 8
